@@ -49,7 +49,8 @@ typedef enum sage_status {
   SAGE_ERR_CUDA = 4,        /* a CUDA runtime or launch error (message kept) */
   SAGE_ERR_NO_MEMORY = 5,   /* workspace allocation failed */
   SAGE_ERR_TIMEOUT = 6,     /* a device wait gave up (reported by sage_sync_status) */
-  SAGE_ERR_WORKSPACE = 7    /* caller workspace smaller than sage_workspace_bytes() */
+  SAGE_ERR_WORKSPACE = 7,   /* caller workspace smaller than the call's *_workspace_bytes() */
+  SAGE_ERR_BAD_PAGE = 8     /* a page table led out of the cache (reported by sage_sync_status) */
 } sage_status;
 
 /* Head dimension, Q/K quantisation block and tile sizes of this library. */
@@ -317,12 +318,136 @@ sage_status sage_debug_qk_int32(const int8_t* q_i8, const float* q_scale, const 
 sage_status sage_debug_staging_codes(const void* q, const void* k, int B, int S, int H, int D, void* q16,
                                      float* q_scale, void* k16, float* k_scale, void* stream);
 
+/*
+ * A paged quantised KV cache.  No counterpart on the pages, whose kernel
+ * quantises whole sequences; the code types are theirs (INT8 K, FP8 V), with
+ * one scale per token and head, since a cache grows token by token.
+ *
+ *   k_codes  int8   [num_pages, H, page_size, 128]
+ *   k_scale  fp32   [num_pages, H, page_size]      K = k_codes * k_scale
+ *   v_codes  E4M3FN [num_pages, H, page_size, 128]
+ *   v_scale  fp32   [num_pages, H, page_size]      V = v_codes * v_scale
+ *
+ * All four are device memory that the caller owns, 16-byte aligned.  H is the
+ * number of key/value heads; page_size is 16, 32, 64, 128 or 256 tokens.
+ * Position i of sequence b is token i % page_size of page
+ * block_table[b * table_stride + i / page_size]; a table has table_width
+ * entries a row, of which a call reads those that its positions need.
+ * Sequences may share pages; a page that a call writes has one owner and one
+ * place in its table (else those positions' contents are unspecified).
+ * Lengths, starts and counts are device arrays, so that a recorded graph
+ * follows them; a sequence has at most 2^30 positions.
+ * A table entry outside [0, num_pages), or a position that the table does not
+ * reach, is an error that the device finds: the position is not written, or
+ * reads as zeros (sage_kv_cache_read), or makes its sequence's attention
+ * unspecified; nothing out of bounds is touched, other sequences are not
+ * affected and sage_sync_status() reports SAGE_ERR_BAD_PAGE.
+ */
+typedef struct sage_kv_cache {
+  int8_t* k_codes;
+  float* k_scale;
+  uint8_t* v_codes;
+  float* v_scale;
+  int32_t num_pages;
+  int32_t H;
+  int32_t page_size;
+} sage_kv_cache;
+
+/*
+ * sage_kv_cache_write -- quantise new tokens and put them into the cache.
+ *
+ *   k, v       in : bf16 [B, S, H, D]; the heads of a token are dense, tokens
+ *                   are k_stride_s and batches k_stride_b elements apart
+ *                   (v: v_stride_*), multiples of 8, so that slices of one
+ *                   projection's output can be given
+ *   start      in : int32 [B]; token i of sequence b goes to position
+ *                   start[b] + i
+ *   count      in : int32 [B] or NULL: only tokens i < count[b] are written
+ *                   (NULL: all S)
+ * Per token and head: k_scale = amax / 127, code = clamp(rint(k / k_scale),
+ * -127, 127); v_scale = amax / 448, code = e4m3_rn_satfinite(v / v_scale)
+ * (fp32 divisions to nearest even; 0 and codes 0 for a row of zeros).  A row
+ * with an infinity or a NaN has a NaN scale and codes 0: it reads back as NaN.
+ * One launch.  B * S * H <= 2^31 - 1.
+ * Errors: INVALID_ARG, UNSUPPORTED (D, page_size), MISALIGNED, CUDA.
+ */
+sage_status sage_kv_cache_write(const sage_kv_cache* cache, const void* k, const void* v, int64_t k_stride_b,
+                                int64_t k_stride_s, int64_t v_stride_b, int64_t v_stride_s, int B, int S, int D,
+                                const int32_t* block_table, int table_width, int64_t table_stride,
+                                const int32_t* start, const int32_t* count, void* stream);
+
+/*
+ * sage_kv_cache_read -- read sequences back as bf16, for attention in other
+ * precisions or layouts (sage_attn_fwd_cross takes the result).
+ *
+ *   lens       in : int32 [B]
+ *   k, v       out: bf16 [B, S, H, D], 16-byte aligned; position i of sequence
+ *                   b is bf16(fp32(code * scale)) for i < lens[b], zero from there
+ * One launch.  B * S * H <= 2^31 - 1.  Errors as sage_kv_cache_write.
+ */
+sage_status sage_kv_cache_read(const sage_kv_cache* cache, const int32_t* block_table, int table_width,
+                               int64_t table_stride, const int32_t* lens, void* k, void* v, int B, int S, int D,
+                               void* stream);
+
+/*
+ * sage_attn_fwd_cache -- the Sq newest tokens of each sequence attend to the
+ * whole sequence in the cache (their own keys and values written already).
+ *
+ *   q          in : bf16 [B, Sq, Hq, D], heads dense, tokens q_stride_s and
+ *                   batches q_stride_b elements apart (multiples of 8); Hq is a
+ *                   multiple of the cache's H, and query head h reads
+ *                   key/value head h / (Hq / H)
+ *   lens       in : int32 [B], positions of each sequence in the cache
+ *   causal     in : non-zero: query i of sequence b sees positions <= lens[b] -
+ *                   Sq + i; zero: it sees all lens[b]
+ *   out        out: bf16 [B, Sq, Hq, D], 32-byte aligned: softmax(q K^T *
+ *                   softmax_scale) V with K and V as the cache's codes and
+ *                   scales say, FP32 scores, weights and sums; zeros for a
+ *                   query that sees nothing
+ *   lse        out: fp32 [B, Hq, Sq] or NULL: log sum exp of the scores (-inf
+ *                   for a query that sees nothing)
+ *   workspace  caller-owned, 256-byte aligned, of at least
+ *              sage_attn_fwd_cache_workspace_bytes(...) bytes, or NULL with
+ *              workspace_bytes 0: taken from the library's pool in stream order.
+ *              Calls that share a workspace must not overlap on the GPU.
+ * Sq = 1 is the generation step, Sq > 1 a chunk of a prompt or drafted tokens.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, NO_MEMORY, CUDA.
+ */
+sage_status sage_attn_fwd_cache(const void* q, int64_t q_stride_b, int64_t q_stride_s, const sage_kv_cache* cache,
+                                const int32_t* block_table, int table_width, int64_t table_stride,
+                                const int32_t* lens, void* out, float* lse, int B, int Sq, int Hq, int D,
+                                float softmax_scale, int causal, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/*
+ * sage_attn_fwd_cache_prefix -- sage_attn_fwd_cache for sequences that all
+ * begin with the same prefix_len cached positions, pages prefix_table[0 ..
+ * ceil(prefix_len / page_size) - 1] (device int32).  Sequence b is the prefix
+ * followed by the lens[b] positions of its row of block_table, and the result
+ * is that of sage_attn_fwd_cache on the sequences put together (up to the
+ * order of the sums); the prefix is read and multiplied once for the queries of
+ * all sequences.  prefix_len >= 1 is a host value of at most 2^30, and need
+ * not fill its last page.  With causal, query i of sequence b sees the
+ * positions <= prefix_len + lens[b] - Sq + i of the whole.
+ * Other arguments and errors as sage_attn_fwd_cache.
+ */
+sage_status sage_attn_fwd_cache_prefix(const void* q, int64_t q_stride_b, int64_t q_stride_s,
+                                       const sage_kv_cache* cache, const int32_t* prefix_table, int prefix_len,
+                                       const int32_t* block_table, int table_width, int64_t table_stride,
+                                       const int32_t* lens, void* out, float* lse, int B, int Sq, int Hq, int D,
+                                       float softmax_scale, int causal, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
+/* Bytes of device workspace sage_attn_fwd_cache (prefix_len 0) or
+ * sage_attn_fwd_cache_prefix need, H key/value heads (0 for invalid sizes). */
+size_t sage_attn_fwd_cache_workspace_bytes(int B, int Sq, int Hq, int H, int prefix_len);
+
 /* Fault sites of sage_debug_inject_fault. */
 enum {
   SAGE_FAULT_NONE = 0,          /* disarm */
   SAGE_FAULT_POOL_ALLOC = 1,    /* a workspace / scratch allocation (the library's pool, or a plan's workspace) */
-  SAGE_FAULT_QUANT_LAUNCH = 2,  /* the Q/K quantisation launch of the attention entry points */
-  SAGE_FAULT_ATTN_LAUNCH = 3    /* the attention kernel launch */
+  SAGE_FAULT_QUANT_LAUNCH = 2,  /* the Q/K quantisation launch of the attention entry points; a cache write or read */
+  SAGE_FAULT_ATTN_LAUNCH = 3    /* the attention kernel launch (over a cache: the first) */
 };
 
 /*
@@ -357,8 +482,8 @@ sage_status sage_debug_pool_state(int* created, uint64_t* used_bytes);
 sage_status sage_debug_wait_timeout(uint64_t timeout_ns, void* stream);
 
 /* Synchronise `stream`, then report (and clear) the device error word of the
- * current device: SAGE_OK, SAGE_ERR_TIMEOUT, or SAGE_ERR_CUDA if the stream
- * itself failed. */
+ * current device: SAGE_OK, SAGE_ERR_TIMEOUT, SAGE_ERR_BAD_PAGE, or
+ * SAGE_ERR_CUDA if the stream itself failed. */
 sage_status sage_sync_status(void* stream);
 
 /* Limit, in nanoseconds, of every device-side wait in later launches from

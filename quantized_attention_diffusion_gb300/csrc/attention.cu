@@ -754,6 +754,10 @@ cudaError_t read_and_clear_device_error(int* code, cudaStream_t stream) {
   return e;
 }
 
+cudaError_t device_error_word(int** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_sage_error);
+}
+
 cudaError_t launch_wait_timeout_probe(uint64_t timeout_ns, cudaStream_t stream) {
   wait_timeout_probe_kernel<<<1, 32, 0, stream>>>(timeout_ns);
   return cudaGetLastError();

@@ -1,0 +1,929 @@
+// cache_attention.cu -- attention of a sequence's newest tokens over the
+// paged quantised cache, and over a prefix that all sequences share (sm_103a).
+//
+// Per query row i (one query head of one new token), over the cached keys j it
+// sees, with kc, vc the codes and sk, sv the scales of key j's row:
+//
+//   x_j = (q_i . kc_j) * softmax_scale * log2 e * sk_j
+//   m   = max x_j,   L = sum 2^(x_j - m),   lse = ln 2 * (m + log2 L)
+//   out = sum 2^(x_j - m) sv_j vc_j / L      (0, and lse = -inf, if no key is seen)
+//
+// The query heads that share a key/value head are rows of one tile, so the
+// cache is read once for all of them.  A row's weights of V are kept apart
+// from its sum: with w_j = x_j + log2 sv_j and M = max w_j the products are
+// formed from 2^(w_j - M), at most 1 whatever the scales of V are, in fp16 (a
+// relative rounding of 2^-11 or less for every weight above 2^-14 of the
+// largest, and 2^-25 of the largest below), and out = 2^(M - m) / L * sum.
+// Q enters as fp16 times a power of two that puts the row's largest magnitude
+// in [2^14, 2^15), and K's integer codes are exact in fp16, so that the
+// products of Q and K are exact but for values 2^-28 below the row's largest.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cuda_runtime.h>
+
+#include "sage_internal.cuh"
+#include "sm103_ptx.cuh"
+
+namespace sage {
+
+namespace {
+
+constexpr int kTok = 64;                                  // keys per tile
+constexpr int kConsumers = 4;                             // warps that compute, 16 keys of a tile each
+constexpr int kThreads = (kConsumers + 1) * 32;           // and one that copies
+constexpr int kStages = 4;
+constexpr uint32_t kOffV = kTok * kHeadDim;
+constexpr uint32_t kOffKs = 2 * kTok * kHeadDim;
+constexpr uint32_t kOffVs = kOffKs + kTok * 4;
+constexpr uint32_t kStageBytes = kOffVs + kTok * 4;
+constexpr uint32_t kMergeBytes = kConsumers * 16 * kHeadDim * 4;
+constexpr uint32_t kSmemBytes = kStages * kStageBytes + kMergeBytes;
+constexpr int kMaxCtas = 2 * 152;                         // two CTAs on each SM
+constexpr int kMaxBatch = 512;                            // sequences of one launch
+constexpr float kLog2e = 1.44269502162933349609375f;      // fp32(log2 e)
+constexpr float kLn2 = 0.693147182464599609375f;          // fp32(ln 2)
+
+struct Params {
+  CacheView cache;
+  PageTable table;           // of the sequences, or of the prefix (one row)
+  const int32_t* lens;       // [B] of this launch
+  const uint16_t* q;
+  int64_t q_sb, q_ss;
+  uint16_t* out;
+  float* lse;
+  int B, Sq, G, Hq;          // G query heads share a key/value head
+  int causal, prefix_len;
+  int room;                  // longest sequence the sequences' table can hold
+  int rows, row_tiles;       // query rows of one unit's key/value head, and tiles of them
+  float c_scale;             // softmax_scale * log2 e
+  int keep;                  // 1: every result goes to the workspace (merged with another launch's)
+  float* part_o;             // [slot][R][128]: sums relative to M
+  float4* part_ml;           // [slot][R]: m, L, M
+  int4* desc;                // [CTA]: the unit that begins in this CTA and ends in a later one
+  int2* info;                // [unit], with keep: first CTA and CTAs of the unit (0: its own slot)
+  uint64_t timeout_ns;
+  int* err;
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Four INT8 codes (one word) -> two pairs of fp16: code + 128 is put into the
+// low bits of 1024 and 1152 taken off again, both exact.
+__device__ __forceinline__ void k_codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  lo = sub_f16x2(__byte_perm(u, 0x64646464u, 0x4140), 0x64806480u);
+  hi = sub_f16x2(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u);
+}
+
+// Two E4M3 codes in the low or high half of a word -> a pair of fp16.
+__device__ __forceinline__ uint32_t v_codes_f16_lo(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t v_codes_f16_hi(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+
+// Untiled copy global -> shared, completion counted on `bar` in bytes.  Both
+// addresses and the size are multiples of 16.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory"); }
+
+// 2^(a - b) for a <= b, 0 where both are -inf.
+__device__ __forceinline__ float ratio(float a, float b) { return b == -INFINITY ? 0.0f : ex2_approx(a - b); }
+
+// x * 2^e for a finite e, without an intermediate overflow or underflow.
+__device__ __forceinline__ float scale2(float e) { return ex2_approx(0.5f * e); }
+
+// A launch's work is a row of key tiles: for each sequence, each tile of query
+// rows and each key/value head (a unit) its tiles of 64 keys in order.  CTA c
+// takes tiles [c * per, (c + 1) * per), whatever units they belong to, so that
+// unequal lengths leave no SM idle.  The part of a unit that a CTA has is a
+// segment: a unit of one segment is written out at once, segments of a unit
+// that CTAs share go to the workspace (slot 2c + 1 for the unit that begins
+// in CTA c and ends later, slot 2c for one that began earlier) and the merge
+// kernel joins them in the order of the CTAs.
+struct Place {
+  int b, rt, h, tile, n;     // n: tiles of the unit
+};
+
+template <int R, bool kPrefix>
+struct Walk {
+  const Params& p;
+  const int* s_len;
+  const long long* s_off;
+
+  // Keys that query row rr of sequence b may see, in this launch's keys.
+  __device__ int limit(int b, int rr) const {
+    if constexpr (kPrefix) {
+      if (!p.causal) return p.prefix_len;
+      const int per_seq = p.Sq * p.G, seq = rr / per_seq, t = rr % per_seq / p.G;
+      return max(0, min(p.prefix_len, p.prefix_len + s_len[seq] - p.Sq + t + 1));
+    } else {
+      const int len = s_len[b];
+      return p.causal ? max(0, min(len, len - p.Sq + rr / p.G + 1)) : len;
+    }
+  }
+  // Keys that some row of the unit may see.
+  __device__ int keys(int b, int rt) const {
+    if constexpr (kPrefix) return p.prefix_len;
+    return limit(b, min(p.rows, (rt + 1) * R) - 1);
+  }
+  __device__ int tiles(int b, int rt) const { return max(1, (keys(b, rt) + kTok - 1) / kTok); }
+  __device__ int seqs() const { return kPrefix ? 1 : p.B; }
+
+  __device__ Place locate(long long f) const {
+    Place x;
+    int lo = 0, hi = seqs();
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_off[mid] * p.cache.H <= f)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    long long rem = f - s_off[lo] * p.cache.H;
+    x.b = lo;
+    x.rt = 0;
+    x.n = tiles(lo, 0);
+    while (rem >= static_cast<long long>(x.n) * p.cache.H) {
+      rem -= static_cast<long long>(x.n) * p.cache.H;
+      x.n = tiles(lo, ++x.rt);
+    }
+    x.h = static_cast<int>(rem / x.n);
+    x.tile = static_cast<int>(rem % x.n);
+    return x;
+  }
+  __device__ void next(Place& x) const {
+    x.tile = 0;
+    if (++x.h < p.cache.H) return;
+    x.h = 0;
+    if (++x.rt == p.row_tiles) {
+      x.rt = 0;
+      ++x.b;
+    }
+    if (x.b < seqs()) x.n = tiles(x.b, x.rt);
+  }
+  __device__ int unit(const Place& x) const { return (x.b * p.row_tiles + x.rt) * p.cache.H + x.h; }
+};
+
+template <int RT, bool kPrefix>
+__global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) cache_attn_kernel(const Params p) {
+  constexpr int R = 16 * RT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full[kStages], empty[kStages];
+  __shared__ int abort_flag;
+  __shared__ int s_len[kMaxBatch];
+  __shared__ long long s_off[kPrefix ? 2 : kMaxBatch + 1];
+  __shared__ float s_m[kConsumers][16], s_w[kConsumers][16], s_l[kConsumers][16];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_v = &abort_flag;
+  // The merge kernel (or the other part's launch) may be scheduled as soon as
+  // there is room; it waits for this grid before it reads anything from it.
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  const Walk<R, kPrefix> walk{p, s_len, s_off};
+  for (int i = threadIdx.x; i < p.B; i += kThreads) s_len[i] = max(0, min(p.room, __ldg(p.lens + i)));
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kConsumers);
+    }
+    abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  __syncthreads();
+  if (warp == 0) {   // s_off[b]: tiles of the sequences before b, for one key/value head
+    long long base = 0;
+    for (int b0 = 0; b0 < walk.seqs(); b0 += 32) {
+      long long n = 0;
+      if (b0 + lane < walk.seqs())
+        for (int rt = 0; rt < p.row_tiles; ++rt) n += walk.tiles(b0 + lane, rt);
+      long long sum = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long up = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+        if (lane >= d) sum += up;
+      }
+      if (b0 + lane < walk.seqs()) s_off[b0 + lane] = base + sum - n;
+      base += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    }
+    if (lane == 0) s_off[walk.seqs()] = base;
+  }
+  __syncthreads();
+
+  const long long total = s_off[walk.seqs()] * p.cache.H;
+  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long f0 = blockIdx.x * per, f1 = min(total, f0 + per);
+  if (!p.keep && threadIdx.x == 0) p.desc[blockIdx.x].w = 0;
+  if (f0 < f1) {
+    Place x = walk.locate(f0);
+    const uint32_t smem0 = smem_addr(smem);
+    if (warp == kConsumers) {
+      // ------------------------------------------------------------ copies --
+      // A tile is 1, 2 or 4 runs of keys that lie together in a page; lane
+      // 4i + k copies part k (K, V, their scales) of run i.  Every lane holds a
+      // page number of the unit's table, reloaded for the next 32 pages.
+      const int ps = p.cache.page_shift;
+      const int run = min(kTok, 1 << ps), runs = kTok / run;
+      const int my_run = lane >> 2, part = lane & 3;
+      int it = 0;
+      bool bad = false, ok = true;
+      for (long long f = f0; f < f1 && ok;) {
+        const int hi = walk.keys(x.b, x.rt);
+        const int32_t* row = p.table.pages + (kPrefix ? 0 : x.b * p.table.stride);
+        const int last = static_cast<int>(min(static_cast<long long>(x.n), x.tile + (f1 - f)));
+        int base = (x.tile * kTok) >> ps;
+        int cur = base + lane < p.table.width ? __ldg(row + base + lane) : -1;
+        int nxt = base + 32 + lane < p.table.width ? __ldg(row + base + 32 + lane) : -1;
+        for (int t = x.tile; t < last; ++t, ++it) {
+          const int t0 = t * kTok + my_run * run;
+          if (((t * kTok) >> ps) - base >= 32) {
+            base += 32;
+            cur = nxt;
+            nxt = base + 32 + lane < p.table.width ? __ldg(row + base + 32 + lane) : -1;
+          }
+          // The tile's pages are base .. base + 31: run <= page and a tile
+          // begins at a multiple of 64 keys.
+          int page = __shfl_sync(0xFFFFFFFFu, cur, ((t0 >> ps) - base) & 31);
+          const bool live = my_run < runs && t0 < hi;
+          if (live && (page < 0 || page >= p.cache.num_pages)) {
+            bad = true;
+            page = 0;        // a page that exists: the result is void, the read is not out of bounds
+          }
+          const int s = it % kStages, round = it / kStages;
+          if (round > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[s], (round - 1) & 1, abort_v, p.err, p.timeout_ns))) {
+            ok = false;
+            break;
+          }
+          const int n_live = (min(kTok, hi - t * kTok) + run - 1) / run;   // <= 0 for a unit without keys
+          if (lane == 0) mbar_arrive_expect_tx(&full[s], max(0, n_live) * run * (2 * kHeadDim + 8));
+          __syncwarp();
+          if (live) {
+            const int64_t r = ((static_cast<int64_t>(page) * p.cache.H + x.h) << ps) + (t0 & ((1 << ps) - 1));
+            const uint32_t bar = smem_addr(&full[s]), st = smem0 + s * kStageBytes;
+            const int o = my_run * run;
+            if (part == 0)
+              bulk_load(st + o * kHeadDim, p.cache.k_codes + r * kHeadDim, run * kHeadDim, bar);
+            else if (part == 1)
+              bulk_load(st + kOffV + o * kHeadDim, p.cache.v_codes + r * kHeadDim, run * kHeadDim, bar);
+            else if (part == 2)
+              bulk_load(st + kOffKs + o * 4, p.cache.k_scale + r, run * 4, bar);
+            else
+              bulk_load(st + kOffVs + o * 4, p.cache.v_scale + r, run * 4, bar);
+          }
+        }
+        f += last - x.tile;
+        walk.next(x);
+      }
+      if (bad) atomicExch(p.err, SAGE_DEVERR_BAD_PAGE);
+      if (!ok) {   // let the copies in flight land before the CTA can exit
+        for (int j = max(0, it - kStages); j < it; ++j) {
+          int local_abort = 0;
+          (void)mbar_wait(&full[j % kStages], (j / kStages) & 1, &local_abort, p.err, p.timeout_ns);
+        }
+      }
+    } else {
+      // ----------------------------------------------------------- compute --
+      // Lane (r, c) = (lane / 4, lane % 4) of the m16n8k16 products: rows r and
+      // r + 8 of A and of the accumulator, column r of B, and k indices 2c,
+      // 2c + 1, 2c + 8, 2c + 9.  The order of the summed index is free as long
+      // as A and B agree, so for Q K^T those are channels 32c + 4i .. + 3 in
+      // product i, which makes a lane's share of a key 32 bytes that lie
+      // together; for P V the output columns are free, and column r of product
+      // j is channel 16r + j, which makes a lane's share of a key 16 bytes.
+      const int r = lane >> 2, c = lane & 3;
+      float* merge = reinterpret_cast<float*>(smem + kStages * kStageBytes);
+      int it = 0;
+      bool ok = true;
+      for (long long f = f0; f < f1;) {
+        const int hi = walk.keys(x.b, x.rt);
+        const int last = static_cast<int>(min(static_cast<long long>(x.n), x.tile + (f1 - f)));
+        uint32_t q[RT][8][4];
+        float crow[RT][2];
+        int lim[RT][2];
+        int lo = INT_MAX;            // keys that every row sees
+#pragma unroll
+        for (int a = 0; a < RT; ++a) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int rr = x.rt * R + a * 16 + e * 8 + r;
+            uint4 w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
+            lim[a][e] = hi;
+            if (rr < p.rows) {
+              lim[a][e] = min(hi, walk.limit(x.b, rr));
+              const int per_seq = p.Sq * p.G;
+              const int seq = kPrefix ? rr / per_seq : x.b, in = kPrefix ? rr % per_seq : rr;
+              const uint16_t* src = p.q + seq * p.q_sb + (in / p.G) * p.q_ss + (x.h * p.G + in % p.G) * kHeadDim + c * 32;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+            }
+            lo = min(lo, lim[a][e]);
+            const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+            uint32_t top = 0u;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = max(top, max(u[i] & 0x7FFFu, (u[i] >> 16) & 0x7FFFu));
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            // 2^(141 - exponent of the row's maximum), at most 2^113
+            const uint32_t ex = min(240u, 268u - (top >> 7));
+            const float up = __uint_as_float(ex << 23);
+            crow[a][e] = p.c_scale * __uint_as_float((254u - ex) << 23);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                const uint32_t v = u[2 * i + g];
+                q[a][i][2 * g + e] = pack_f16(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xFFFF0000u) * up);
+              }
+            }
+          }
+        }
+        lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+
+        float o[RT][16][4];
+        float m[RT][2], mw[RT][2], l[RT][2];
+#pragma unroll
+        for (int a = 0; a < RT; ++a) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[a][j][e] = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            m[a][e] = mw[a][e] = -INFINITY;
+            l[a][e] = 0.0f;
+          }
+        }
+
+        for (int t = x.tile; t < last; ++t, ++it) {
+          const int s = it % kStages;
+          ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&full[s], (it / kStages) & 1, abort_v, p.err, p.timeout_ns));
+          const int t0 = t * kTok + warp * 16;      // this warp's first key
+          if (ok && t0 < hi) {
+            const uint8_t* st = smem + s * kStageBytes;
+            const uint8_t* kp = st + (warp * 16 + r) * kHeadDim + c * 32;
+            const uint8_t* vp = st + kOffV + (warp * 16 + 2 * c) * kHeadDim + r * 16;
+            float sc[RT][2][4];
+#pragma unroll
+            for (int a = 0; a < RT; ++a)
+#pragma unroll
+              for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[a][n][e] = 0.0f;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint4 kw[2];
+#pragma unroll
+              for (int n = 0; n < 2; ++n) kw[n] = *reinterpret_cast<const uint4*>(kp + n * 8 * kHeadDim + half * 16);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                  uint32_t b0, b1;
+                  k_codes_f16(reinterpret_cast<const uint32_t*>(&kw[n])[i], b0, b1);
+#pragma unroll
+                  for (int a = 0; a < RT; ++a) mma_f16(sc[a][n], q[a][half * 4 + i], b0, b1);
+                }
+              }
+            }
+            // Scores of rows r (e 0, 1) and r + 8 (e 2, 3) for keys
+            // 8n + 2c, 8n + 2c + 1.
+            float ks[2][2], lv[2][2];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const float2 k2 = *reinterpret_cast<const float2*>(st + kOffKs + (warp * 16 + n * 8 + 2 * c) * 4);
+              const float2 v2 = *reinterpret_cast<const float2*>(st + kOffVs + (warp * 16 + n * 8 + 2 * c) * 4);
+              ks[n][0] = k2.x;
+              ks[n][1] = k2.y;
+              lv[n][0] = lg2_approx(v2.x);
+              lv[n][1] = lg2_approx(v2.y);
+            }
+            const bool cut = t0 + 16 > lo;          // some row does not see all of these keys
+            uint32_t pa[RT][4];
+#pragma unroll
+            for (int a = 0; a < RT; ++a) {
+              float w[2][4];
+              float mx[2] = {m[a][0], m[a][1]}, mwx[2] = {mw[a][0], mw[a][1]};
+#pragma unroll
+              for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  float v = (sc[a][n][e] * crow[a][e >> 1]) * ks[n][e & 1];
+                  float vw = v + lv[n][e & 1];
+                  if (cut && t0 + n * 8 + 2 * c + (e & 1) >= lim[a][e >> 1]) v = vw = -INFINITY;
+                  sc[a][n][e] = v;
+                  w[n][e] = vw;
+                  mx[e >> 1] = fmaxf(mx[e >> 1], v);
+                  mwx[e >> 1] = fmaxf(mwx[e >> 1], vw);
+                }
+              bool moved = false;
+              float alpha[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 1));
+                mwx[e] = fmaxf(mwx[e], __shfl_xor_sync(0xFFFFFFFFu, mwx[e], 1));
+                mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 2));
+                mwx[e] = fmaxf(mwx[e], __shfl_xor_sync(0xFFFFFFFFu, mwx[e], 2));
+                l[a][e] *= ratio(m[a][e], mx[e]);
+                alpha[e] = ratio(mw[a][e], mwx[e]);
+                moved |= mwx[e] != mw[a][e];
+                m[a][e] = mx[e];
+                mw[a][e] = mwx[e];
+                if (mx[e] == -INFINITY) mx[e] = 0.0f;        // 2^(-inf - 0) = 0
+                if (mwx[e] == -INFINITY) mwx[e] = 0.0f;
+              }
+#pragma unroll
+              for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  l[a][e >> 1] += ex2_approx(sc[a][n][e] - mx[e >> 1]);
+                  w[n][e] = ex2_approx(w[n][e] - mwx[e >> 1]);
+                }
+                pa[a][2 * n] = pack_f16(w[n][0], w[n][1]);
+                pa[a][2 * n + 1] = pack_f16(w[n][2], w[n][3]);
+              }
+              if (__any_sync(0xFFFFFFFFu, moved)) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  o[a][j][0] *= alpha[0];
+                  o[a][j][1] *= alpha[0];
+                  o[a][j][2] *= alpha[1];
+                  o[a][j][3] *= alpha[1];
+                }
+              }
+            }
+            uint4 vw[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int tok = (k >> 1) * 8 + (k & 1);        // this lane's key 2c + tok
+              vw[k] = *reinterpret_cast<const uint4*>(vp + tok * kHeadDim);
+              // Codes behind the last key may be anything, NaN too.
+              if (t0 + 16 > hi && t0 + 2 * c + tok >= hi) vw[k] = make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t w0 = reinterpret_cast<const uint32_t*>(&vw[0])[i], w1 = reinterpret_cast<const uint32_t*>(&vw[1])[i];
+              const uint32_t w2 = reinterpret_cast<const uint32_t*>(&vw[2])[i], w3 = reinterpret_cast<const uint32_t*>(&vw[3])[i];
+              const uint32_t a01 = __byte_perm(w0, w1, 0x5140), b01 = __byte_perm(w0, w1, 0x7362);
+              const uint32_t a23 = __byte_perm(w2, w3, 0x5140), b23 = __byte_perm(w2, w3, 0x7362);
+#pragma unroll
+              for (int a = 0; a < RT; ++a) {
+                mma_f16(o[a][4 * i], pa[a], v_codes_f16_lo(a01), v_codes_f16_lo(a23));
+                mma_f16(o[a][4 * i + 1], pa[a], v_codes_f16_hi(a01), v_codes_f16_hi(a23));
+                mma_f16(o[a][4 * i + 2], pa[a], v_codes_f16_lo(b01), v_codes_f16_lo(b23));
+                mma_f16(o[a][4 * i + 3], pa[a], v_codes_f16_hi(b01), v_codes_f16_hi(b23));
+              }
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty[s]);
+        }
+
+        // The four warps' parts of the segment, 16 rows at a time.  A warp
+        // whose wait gave up takes part in the barriers and writes nothing.
+        const bool whole = x.tile == 0 && last == x.n;
+        const int slot = !whole ? (x.tile > 0 ? 2 * blockIdx.x : 2 * blockIdx.x + 1)
+                                : 2 * static_cast<int>(gridDim.x) + walk.unit(x);
+#pragma unroll
+        for (int a = 0; a < RT; ++a) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            l[a][e] += __shfl_xor_sync(0xFFFFFFFFu, l[a][e], 1);
+            l[a][e] += __shfl_xor_sync(0xFFFFFFFFu, l[a][e], 2);
+            if (c == 0) {
+              s_m[warp][e * 8 + r] = m[a][e];
+              s_w[warp][e * 8 + r] = mw[a][e];
+              s_l[warp][e * 8 + r] = l[a][e];
+            }
+          }
+          consumer_sync();
+          const int row = threadIdx.x >> 3, g8 = threadIdx.x & 7;   // 16 channels of a row a thread
+          float wrow[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = s_w[0][e * 8 + r];
+#pragma unroll
+            for (int k = 1; k < kConsumers; ++k) top = fmaxf(top, s_w[k][e * 8 + r]);
+            wrow[e] = ratio(mw[a][e], top);
+          }
+          float M = s_w[0][row], mm = s_m[0][row], L = 0.0f;
+#pragma unroll
+          for (int k = 1; k < kConsumers; ++k) {
+            M = fmaxf(M, s_w[k][row]);
+            mm = fmaxf(mm, s_m[k][row]);
+          }
+#pragma unroll
+          for (int k = 0; k < kConsumers; ++k) L += s_l[k][row] * ratio(s_m[k][row], mm);
+          // float4 i of channels 32c .. 32c + 31 stands at i ^ (lane % 8): the
+          // eight lanes of a store fall into distinct banks.
+          float4* buf = reinterpret_cast<float4*>(merge) + warp * 16 * 32;
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int j = (i & 3) * 4, k = 2 * e + (i >> 2);
+              buf[(e * 8 + r) * 32 + c * 8 + (i ^ (lane & 7))] =
+                  make_float4(o[a][j][k] * wrow[e], o[a][j + 1][k] * wrow[e], o[a][j + 2][k] * wrow[e], o[a][j + 3][k] * wrow[e]);
+            }
+          consumer_sync();
+          const int rr = x.rt * R + a * 16 + row;
+          if (rr < p.rows && !abort_flag) {
+            float4 sum[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int at = g8 * 4 + e, cc = at >> 3;
+              const int idx = row * 32 + cc * 8 + ((at & 7) ^ (((row & 1) << 2) | cc));
+              sum[e] = reinterpret_cast<const float4*>(merge)[idx];
+#pragma unroll
+              for (int k = 1; k < kConsumers; ++k) {
+                const float4 y = reinterpret_cast<const float4*>(merge)[k * 16 * 32 + idx];
+                sum[e].x += y.x;
+                sum[e].y += y.y;
+                sum[e].z += y.z;
+                sum[e].w += y.w;
+              }
+            }
+            if (whole && !p.keep) {
+              const int t = rr / p.G, hq = x.h * p.G + rr % p.G;
+              const float half = L == 0.0f ? 0.0f : scale2(M - mm);
+              const float inv = L == 0.0f ? 0.0f : half / L;
+              uint32_t w[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                w[2 * e] = pack_bf16(sum[e].x * half * inv, sum[e].y * half * inv);
+                w[2 * e + 1] = pack_bf16(sum[e].z * half * inv, sum[e].w * half * inv);
+              }
+              uint4* dst = reinterpret_cast<uint4*>(
+                  p.out + ((static_cast<int64_t>(x.b) * p.Sq + t) * p.Hq + hq) * kHeadDim + g8 * 16);
+              dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+              if (p.lse != nullptr && g8 == 0)
+                p.lse[(static_cast<int64_t>(x.b) * p.Hq + hq) * p.Sq + t] = L == 0.0f ? -INFINITY : (mm + log2f(L)) * kLn2;
+            } else {
+              const int64_t at = static_cast<int64_t>(slot) * R + a * 16 + row;
+              float4* dst = reinterpret_cast<float4*>(p.part_o + at * kHeadDim) + g8 * 4;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) dst[e] = sum[e];
+              if (g8 == 0) p.part_ml[at] = make_float4(mm, L, M, 0.0f);
+            }
+          }
+        }
+        if (threadIdx.x == 0 && x.tile == 0) {   // the unit begins here: how many CTAs have a part of it
+          const int ctas = static_cast<int>((f + x.n - 1) / per) - static_cast<int>(blockIdx.x) + 1;
+          if (p.keep)
+            p.info[walk.unit(x)] = make_int2(blockIdx.x, whole ? 0 : ctas);
+          else if (!whole)
+            p.desc[blockIdx.x] = make_int4(x.b, x.rt, x.h, ctas);
+        }
+        f += last - x.tile;
+        walk.next(x);
+      }
+    }
+  }
+  // The merge kernel waits for this grid alone: this grid has to end after the
+  // one before it, beside which it may have run.
+  if constexpr (kPrefix) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ------------------------------------------------------------------ merge --
+
+struct MergeParams {
+  const float* part_o;
+  const float4* part_ml;
+  const int4* desc;          // one key/value part alone
+  const int2* info;          // a prefix and the sequences
+  int ctas, R, rows, row_tiles, H;
+  // The prefix's parts: closed form, every unit has as many tiles.
+  const float* pre_o;
+  const float4* pre_ml;
+  int pre_R, pre_n, pre_ctas;                       // rows of a tile, key tiles of a unit, CTAs
+  long long pre_per;                                // key tiles of a CTA
+  uint16_t* out;
+  float* lse;
+  int Sq, G, Hq;
+};
+
+constexpr int kMergeWarps = 8;
+
+// One row a CTA: its segments' m, L and M first, then each warp sums every
+// eighth segment and the warps' sums are added in order.
+__global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const MergeParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ float s_red[kMergeWarps][2];
+  __shared__ float s_sum[kMergeWarps];
+  __shared__ float4 s_o[kMergeWarps][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int b, rt, h, first, n, own = -1;
+  if (p.info == nullptr) {
+    const int4 d = p.desc[blockIdx.x];
+    if (d.w < 2) return;
+    b = d.x;
+    rt = d.y;
+    h = d.z;
+    first = blockIdx.x;
+    n = d.w;
+  } else {
+    const int2 d = p.info[blockIdx.x];
+    h = blockIdx.x % p.H;
+    rt = blockIdx.x / p.H % p.row_tiles;
+    b = blockIdx.x / p.H / p.row_tiles;
+    first = d.x;
+    n = d.y == 0 ? 1 : d.y;
+    if (d.y == 0) own = 2 * p.ctas + blockIdx.x;
+  }
+  const int rr = rt * p.R + static_cast<int>(blockIdx.y);
+  if (rr >= p.rows) return;
+  int pn = 0, pfirst = 0, prow = 0;
+  bool pwhole = false;
+  if (p.pre_o != nullptr) {
+    const int pr = b * p.rows + rr;                        // row of the prefix's launch
+    prow = pr % p.pre_R;
+    const int u = pr / p.pre_R * p.H + h;
+    const long long f = static_cast<long long>(u) * p.pre_n;
+    pfirst = static_cast<int>(f / p.pre_per);
+    pn = static_cast<int>((f + p.pre_n - 1) / p.pre_per) - pfirst + 1;
+    pwhole = pn == 1;
+    if (pwhole) pfirst = 2 * p.pre_ctas + u;
+  }
+  const int total = n + pn;
+  auto place = [&](int i, const float*& o, const float4*& ml) {
+    if (i < n) {
+      const int slot = own >= 0 ? own : (i == 0 ? 2 * first + 1 : 2 * (first + i));
+      const int64_t at = static_cast<int64_t>(slot) * p.R + blockIdx.y;
+      o = p.part_o + at * kHeadDim;
+      ml = p.part_ml + at;
+    } else {
+      const int j = i - n;
+      const int slot = pwhole ? pfirst : (j == 0 ? 2 * pfirst + 1 : 2 * (pfirst + j));
+      const int64_t at = static_cast<int64_t>(slot) * p.pre_R + prow;
+      o = p.pre_o + at * kHeadDim;
+      ml = p.pre_ml + at;
+    }
+  };
+  float m = -INFINITY, M = -INFINITY;
+  for (int i = threadIdx.x; i < total; i += kMergeWarps * 32) {
+    const float* o;
+    const float4* ml;
+    place(i, o, ml);
+    const float4 v = *ml;
+    m = fmaxf(m, v.x);
+    M = fmaxf(M, v.z);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d));
+  }
+  if (lane == 0) {
+    s_red[warp][0] = m;
+    s_red[warp][1] = M;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kMergeWarps; ++k) {
+    m = fmaxf(m, s_red[k][0]);
+    M = fmaxf(M, s_red[k][1]);
+  }
+  float L = 0.0f;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int i = warp; i < total; i += kMergeWarps) {
+    const float* o;
+    const float4* ml;
+    place(i, o, ml);
+    const float4 v = *ml;
+    const float4 y = reinterpret_cast<const float4*>(o)[lane];
+    L += v.y * ratio(v.x, m);
+    const float w = ratio(v.z, M);
+    acc.x += y.x * w;
+    acc.y += y.y * w;
+    acc.z += y.z * w;
+    acc.w += y.w * w;
+  }
+  s_o[warp][lane] = acc;
+  if (lane == 0) s_sum[warp] = L;
+  __syncthreads();
+  if (warp != 0) return;
+  L = s_sum[0];
+  acc = s_o[0][lane];
+#pragma unroll
+  for (int k = 1; k < kMergeWarps; ++k) {
+    const float4 y = s_o[k][lane];
+    L += s_sum[k];
+    acc.x += y.x;
+    acc.y += y.y;
+    acc.z += y.z;
+    acc.w += y.w;
+  }
+  const int t = rr / p.G, hq = h * p.G + rr % p.G;
+  const float half = L == 0.0f ? 0.0f : scale2(M - m);
+  const float inv = L == 0.0f ? 0.0f : half / L;
+  uint2 w;
+  w.x = pack_bf16(acc.x * half * inv, acc.y * half * inv);
+  w.y = pack_bf16(acc.z * half * inv, acc.w * half * inv);
+  *reinterpret_cast<uint2*>(p.out + ((static_cast<int64_t>(b) * p.Sq + t) * p.Hq + hq) * kHeadDim + lane * 4) = w;
+  if (p.lse != nullptr && lane == 0)
+    p.lse[(static_cast<int64_t>(b) * p.Hq + hq) * p.Sq + t] = L == 0.0f ? -INFINITY : (m + log2f(L)) * kLn2;
+}
+
+// ------------------------------------------------------------------- host --
+
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+// 16 query rows a tile where they are all, else 32: the products of a tile of
+// 16 rows take as long for 4 rows as for 16, and the keys are converted once
+// for all rows of a tile.
+int rows_per_tile(int rows) { return rows <= 16 ? 16 : 32; }
+
+// One launch's part of the workspace.
+struct Layout {
+  int rows, R, row_tiles, units, slots;
+  size_t o, ml, desc, info, end;
+};
+
+// keep: every unit may also need a slot of its own.
+Layout layout(int rows, int B, int H, bool keep, size_t at) {
+  Layout w;
+  w.rows = rows;
+  w.R = rows_per_tile(rows);
+  w.row_tiles = (rows + w.R - 1) / w.R;
+  w.units = B * w.row_tiles * H;
+  w.slots = 2 * kMaxCtas + (keep ? w.units : 0);
+  w.o = at;
+  w.ml = w.o + align256(static_cast<size_t>(w.slots) * w.R * kHeadDim * sizeof(float));
+  w.desc = w.ml + align256(static_cast<size_t>(w.slots) * w.R * sizeof(float4));
+  w.info = w.desc + align256(kMaxCtas * sizeof(int4));
+  w.end = w.info + (keep ? align256(static_cast<size_t>(w.units) * sizeof(int2)) : 0);
+  return w;
+}
+
+template <typename T>
+T* at(void* base, size_t off) {
+  return reinterpret_cast<T*>(static_cast<uint8_t*>(base) + off);
+}
+
+cudaError_t launch_part(const Params& p, int R, bool prefix, unsigned ctas, cudaStream_t stream) {
+  auto go = [&](auto kernel) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = stream;
+    // The prefix's launch follows the sequences' and needs nothing of it.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = prefix ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+  };
+  if (prefix) return R == 16 ? go(cache_attn_kernel<1, true>) : go(cache_attn_kernel<2, true>);
+  return R == 16 ? go(cache_attn_kernel<1, false>) : go(cache_attn_kernel<2, false>);
+}
+
+unsigned ctas_for(long long tiles) { return static_cast<unsigned>(std::min<long long>(kMaxCtas, std::max(1ll, tiles))); }
+
+}  // namespace
+
+size_t cache_attn_workspace_bytes(int B, int Sq, int Hq, int Hkv, int prefix_len) {
+  const int b = std::min(B, kMaxBatch), rows = Sq * (Hq / Hkv);
+  const bool both = prefix_len > 0;
+  Layout w = layout(rows, b, Hkv, both, 0);
+  if (both) w = layout(b * rows, 1, Hkv, true, w.end);
+  return w.end;
+}
+
+cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream) {
+  const int H = a.cache.H, G = a.Hq / H;
+  const bool both = a.prefix_len > 0;
+  for (int b0 = 0; b0 < a.B; b0 += kMaxBatch) {
+    const int B = std::min(kMaxBatch, a.B - b0);
+    const Layout w = layout(a.Sq * G, B, H, both, 0);
+    Params p;
+    p.cache = a.cache;
+    p.table = a.table;
+    p.table.pages += b0 * a.table.stride;
+    p.lens = a.lens + b0;
+    p.q = a.q + b0 * a.q_sb;
+    p.q_sb = a.q_sb;
+    p.q_ss = a.q_ss;
+    p.out = a.out + static_cast<int64_t>(b0) * a.Sq * a.Hq * kHeadDim;
+    p.lse = a.lse == nullptr ? nullptr : a.lse + static_cast<int64_t>(b0) * a.Sq * a.Hq;
+    p.B = B;
+    p.Sq = a.Sq;
+    p.G = G;
+    p.Hq = a.Hq;
+    p.causal = a.causal;
+    p.prefix_len = a.prefix_len;
+    p.rows = w.rows;
+    p.row_tiles = w.row_tiles;
+    p.c_scale = a.softmax_scale * kLog2e;
+    p.keep = both;
+    p.part_o = at<float>(a.workspace, w.o);
+    p.part_ml = at<float4>(a.workspace, w.ml);
+    p.desc = at<int4>(a.workspace, w.desc);
+    p.info = both ? at<int2>(a.workspace, w.info) : nullptr;
+    p.timeout_ns = a.timeout_ns;
+    p.err = a.err;
+    p.room = static_cast<int>(std::min<int64_t>(kMaxCacheLen, static_cast<int64_t>(a.table.width) << a.cache.page_shift));
+    // The lengths are on the device: as many CTAs as the table has room for.
+    const unsigned ctas = ctas_for(std::min<long long>(kMaxCtas, (static_cast<long long>(p.room) + kTok - 1) / kTok) * w.units);
+    cudaError_t e = launch_part(p, w.R, false, ctas, stream);
+    if (e != cudaSuccess) return e;
+
+    MergeParams mp = {};
+    mp.part_o = p.part_o;
+    mp.part_ml = p.part_ml;
+    mp.desc = p.desc;
+    mp.info = p.info;
+    mp.ctas = ctas;
+    mp.R = w.R;
+    mp.rows = w.rows;
+    mp.row_tiles = w.row_tiles;
+    mp.H = H;
+    mp.out = p.out;
+    mp.lse = p.lse;
+    mp.Sq = a.Sq;
+    mp.G = G;
+    mp.Hq = a.Hq;
+    if (both) {
+      const Layout u = layout(B * a.Sq * G, 1, H, true, w.end);
+      p.table.pages = a.prefix_pages;
+      p.table.width = (a.prefix_len + (1 << a.cache.page_shift) - 1) >> a.cache.page_shift;
+      p.table.stride = 0;
+      p.rows = u.rows;
+      p.row_tiles = u.row_tiles;
+      p.part_o = at<float>(a.workspace, u.o);
+      p.part_ml = at<float4>(a.workspace, u.ml);
+      p.desc = at<int4>(a.workspace, u.desc);
+      p.info = at<int2>(a.workspace, u.info);
+      const int n = (a.prefix_len + kTok - 1) / kTok;
+      const long long tiles = static_cast<long long>(n) * u.units;
+      const unsigned pc = ctas_for(tiles);
+      e = launch_part(p, u.R, true, pc, stream);
+      if (e != cudaSuccess) return e;
+      mp.pre_o = p.part_o;
+      mp.pre_ml = p.part_ml;
+      mp.pre_R = u.R;
+      mp.pre_n = n;
+      mp.pre_per = (tiles + pc - 1) / pc;
+      mp.pre_ctas = pc;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(both ? w.units : ctas, std::min(w.R, w.rows));
+    cfg.blockDim = dim3(kMergeWarps * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, cache_merge_kernel, mp);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace sage

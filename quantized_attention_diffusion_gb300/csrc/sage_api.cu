@@ -323,6 +323,105 @@ sage_status check_workspace(void* ws, size_t bytes, int B, int S, int H) {
   return SAGE_OK;
 }
 
+// A cache and its page table, as the cache entry points take them.
+sage_status check_cache(const sage_kv_cache* c, int D, const int32_t* table, int width, int64_t stride) {
+  if (!c) return fail(SAGE_ERR_INVALID_ARG, "cache is NULL");
+  if (D != kHeadDim)
+    return fail(SAGE_ERR_UNSUPPORTED, "head dimension %d is not supported: this kernel takes D = 128", D);
+  if (c->num_pages < 1 || c->H < 1)
+    return fail(SAGE_ERR_INVALID_ARG, "a cache's num_pages and H must be >= 1 (got %d, %d)", c->num_pages, c->H);
+  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
+    return fail(SAGE_ERR_UNSUPPORTED, "page_size %d is not supported: 16, 32, 64, 128 or 256", c->page_size);
+  sage_status s = check_ptrs({{c->k_codes, "k_codes"}, {c->k_scale, "k_scale"}, {c->v_codes, "v_codes"},
+                              {c->v_scale, "v_scale"}});
+  if (s != SAGE_OK) return s;
+  if (!table) return fail(SAGE_ERR_INVALID_ARG, "block_table is NULL");
+  if (!aligned(table, 4)) return fail(SAGE_ERR_MISALIGNED, "block_table is not 4-byte aligned");
+  if (width < 1 || stride < 0)
+    return fail(SAGE_ERR_INVALID_ARG, "table_width must be >= 1 and table_stride >= 0 (got %d, %lld)", width,
+                static_cast<long long>(stride));
+  return SAGE_OK;
+}
+
+// Device arrays of one int32 per sequence.
+sage_status check_ints(const int32_t* p, const char* name) {
+  if (!p) return fail(SAGE_ERR_INVALID_ARG, "%s is NULL", name);
+  if (!aligned(p, 4)) return fail(SAGE_ERR_MISALIGNED, "%s is not 4-byte aligned", name);
+  return SAGE_OK;
+}
+
+sage_status check_strides(int64_t sb, int64_t ss, const char* name) {
+  if (sb < 0 || ss < 0) return fail(SAGE_ERR_INVALID_ARG, "%s has a negative stride", name);
+  if ((sb | ss) % 8 != 0) return fail(SAGE_ERR_MISALIGNED, "%s's strides are not multiples of 8 elements", name);
+  return SAGE_OK;
+}
+
+CacheView cache_view(const sage_kv_cache* c) {
+  CacheView v;
+  v.k_codes = reinterpret_cast<uint8_t*>(c->k_codes);
+  v.k_scale = c->k_scale;
+  v.v_codes = c->v_codes;
+  v.v_scale = c->v_scale;
+  v.num_pages = c->num_pages;
+  v.H = c->H;
+  v.page_shift = 0;
+  while ((1 << v.page_shift) < c->page_size) ++v.page_shift;
+  return v;
+}
+
+// sage_attn_fwd_cache and, with a prefix, sage_attn_fwd_cache_prefix.
+sage_status run_cache_attention(const void* q, int64_t q_sb, int64_t q_ss, const sage_kv_cache* cache,
+                                const int32_t* prefix_table, int prefix_len, const int32_t* table, int width,
+                                int64_t stride, const int32_t* lens, void* out, float* lse, int B, int Sq, int Hq,
+                                int D, float softmax_scale, int causal, void* ws, size_t ws_bytes, void* stream) {
+  sage_status s = check_cache(cache, D, table, width, stride);
+  if (s == SAGE_OK) s = check_shape(B, Sq, Hq, D);
+  if (s == SAGE_OK && Hq % cache->H != 0)
+    s = fail(SAGE_ERR_INVALID_ARG, "Hq = %d is not a multiple of the cache's H = %d", Hq, cache->H);
+  if (s == SAGE_OK && static_cast<int64_t>(B) * Hq > INT_MAX / Sq)
+    s = fail(SAGE_ERR_INVALID_ARG, "B*Sq*Hq exceeds 2^31-1");
+  if (s == SAGE_OK) s = check_scale(softmax_scale);
+  if (s == SAGE_OK) s = check_ptrs({{q, "q"}, {out, "out"}});
+  if (s == SAGE_OK) s = check_strides(q_sb, q_ss, "q");
+  if (s == SAGE_OK) s = check_out(out);
+  if (s == SAGE_OK && lse) s = check_ptrs({{lse, "lse"}});
+  if (s == SAGE_OK) s = check_ints(lens, "lens");
+  if (s != SAGE_OK) return s;
+  const size_t need = cache_attn_workspace_bytes(B, Sq, Hq, cache->H, prefix_len);
+  if (ws) {
+    if (!aligned(ws, 256)) return fail(SAGE_ERR_MISALIGNED, "workspace is not 256-byte aligned");
+    if (ws_bytes < need)
+      return fail(SAGE_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu bytes needed", ws_bytes, need);
+  }
+  CacheAttnArgs a;
+  a.cache = cache_view(cache);
+  a.table = {table, width, stride};
+  a.lens = lens;
+  a.prefix_pages = prefix_table;
+  a.prefix_len = prefix_len;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_sb = q_sb;
+  a.q_ss = q_ss;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.B = B;
+  a.Sq = Sq;
+  a.Hq = Hq;
+  a.causal = causal != 0;
+  a.softmax_scale = softmax_scale;
+  a.timeout_ns = timeout_ns();
+  cudaError_t e = device_error_word(&a.err);
+  if (e != cudaSuccess) return cuda_fail(e, "device error word");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  auto launch = [&](void* w) {
+    a.workspace = w;
+    if (fault_fires(SAGE_FAULT_ATTN_LAUNCH)) return fail(SAGE_ERR_CUDA, "cache attention launch: injected fault");
+    const cudaError_t err = launch_cache_attention(a, st);
+    return err == cudaSuccess ? SAGE_OK : cuda_fail(err, "cache attention launch");
+  };
+  return ws ? launch(ws) : with_pool_workspace(need, st, launch);
+}
+
 }  // namespace
 
 // The host object behind sage_plan (opaque to callers).
@@ -623,6 +722,98 @@ sage_status sage_attn_fwd_fused_q(const void* q, const void* k, const void* v, v
   });
 }
 
+sage_status sage_kv_cache_write(const sage_kv_cache* cache, const void* k, const void* v, int64_t k_stride_b,
+                                int64_t k_stride_s, int64_t v_stride_b, int64_t v_stride_s, int B, int S, int D,
+                                const int32_t* block_table, int table_width, int64_t table_stride,
+                                const int32_t* start, const int32_t* count, void* stream) {
+  sage_status s = check_cache(cache, D, block_table, table_width, table_stride);
+  if (s == SAGE_OK) s = check_shape(B, S, cache->H, D);
+  if (s == SAGE_OK && static_cast<int64_t>(B) * cache->H > INT_MAX / S)
+    s = fail(SAGE_ERR_INVALID_ARG, "B*S*H exceeds 2^31-1");
+  if (s == SAGE_OK) s = check_ptrs({{k, "k"}, {v, "v"}});
+  if (s == SAGE_OK) s = check_strides(k_stride_b, k_stride_s, "k");
+  if (s == SAGE_OK) s = check_strides(v_stride_b, v_stride_s, "v");
+  if (s == SAGE_OK) s = check_ints(start, "start");
+  if (s == SAGE_OK && count) s = check_ints(count, "count");
+  if (s != SAGE_OK) return s;
+  CacheWriteArgs a;
+  a.cache = cache_view(cache);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.k_sb = k_stride_b;
+  a.k_ss = k_stride_s;
+  a.v_sb = v_stride_b;
+  a.v_ss = v_stride_s;
+  a.B = B;
+  a.S = S;
+  a.table = {block_table, table_width, table_stride};
+  a.start = start;
+  a.count = count;
+  cudaError_t e = device_error_word(&a.err);
+  if (e != cudaSuccess) return cuda_fail(e, "device error word");
+  if (fault_fires(SAGE_FAULT_QUANT_LAUNCH)) return fail(SAGE_ERR_CUDA, "cache write launch: injected fault");
+  e = launch_kv_cache_write(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "cache write launch");
+  return SAGE_OK;
+}
+
+sage_status sage_kv_cache_read(const sage_kv_cache* cache, const int32_t* block_table, int table_width,
+                               int64_t table_stride, const int32_t* lens, void* k, void* v, int B, int S, int D,
+                               void* stream) {
+  sage_status s = check_cache(cache, D, block_table, table_width, table_stride);
+  if (s == SAGE_OK) s = check_shape(B, S, cache->H, D);
+  if (s == SAGE_OK && static_cast<int64_t>(B) * cache->H > INT_MAX / S)
+    s = fail(SAGE_ERR_INVALID_ARG, "B*S*H exceeds 2^31-1");
+  if (s == SAGE_OK) s = check_ptrs({{k, "k"}, {v, "v"}});
+  if (s == SAGE_OK) s = check_ints(lens, "lens");
+  if (s != SAGE_OK) return s;
+  CacheReadArgs a;
+  a.cache = cache_view(cache);
+  a.table = {block_table, table_width, table_stride};
+  a.lens = lens;
+  a.k = static_cast<uint16_t*>(k);
+  a.v = static_cast<uint16_t*>(v);
+  a.B = B;
+  a.S = S;
+  cudaError_t e = device_error_word(&a.err);
+  if (e != cudaSuccess) return cuda_fail(e, "device error word");
+  if (fault_fires(SAGE_FAULT_QUANT_LAUNCH)) return fail(SAGE_ERR_CUDA, "cache read launch: injected fault");
+  e = launch_kv_cache_read(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "cache read launch");
+  return SAGE_OK;
+}
+
+sage_status sage_attn_fwd_cache(const void* q, int64_t q_stride_b, int64_t q_stride_s, const sage_kv_cache* cache,
+                                const int32_t* block_table, int table_width, int64_t table_stride,
+                                const int32_t* lens, void* out, float* lse, int B, int Sq, int Hq, int D,
+                                float softmax_scale, int causal, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  return run_cache_attention(q, q_stride_b, q_stride_s, cache, nullptr, 0, block_table, table_width, table_stride,
+                             lens, out, lse, B, Sq, Hq, D, softmax_scale, causal, workspace, workspace_bytes, stream);
+}
+
+sage_status sage_attn_fwd_cache_prefix(const void* q, int64_t q_stride_b, int64_t q_stride_s,
+                                       const sage_kv_cache* cache, const int32_t* prefix_table, int prefix_len,
+                                       const int32_t* block_table, int table_width, int64_t table_stride,
+                                       const int32_t* lens, void* out, float* lse, int B, int Sq, int Hq, int D,
+                                       float softmax_scale, int causal, void* workspace, size_t workspace_bytes,
+                                       void* stream) {
+  const sage_status s = check_ints(prefix_table, "prefix_table");
+  if (s != SAGE_OK) return s;
+  if (prefix_len < 1 || prefix_len > kMaxCacheLen)
+    return fail(SAGE_ERR_INVALID_ARG, "prefix_len must be in [1, 2^30] (got %d)", prefix_len);
+  return run_cache_attention(q, q_stride_b, q_stride_s, cache, prefix_table, prefix_len, block_table, table_width,
+                             table_stride, lens, out, lse, B, Sq, Hq, D, softmax_scale, causal, workspace,
+                             workspace_bytes, stream);
+}
+
+size_t sage_attn_fwd_cache_workspace_bytes(int B, int Sq, int Hq, int H, int prefix_len) {
+  if (B < 1 || Sq < 1 || Hq < 1 || H < 1 || Hq % H != 0 || prefix_len < 0 || prefix_len > kMaxCacheLen ||
+      static_cast<int64_t>(B) * Hq > INT_MAX || static_cast<int64_t>(B) * Hq > INT_MAX / Sq)
+    return 0;
+  return cache_attn_workspace_bytes(B, Sq, Hq, H, prefix_len);
+}
+
 sage_status sage_debug_fused_q(const void* q, const void* k, const void* v, void* out, int B, int S, int H,
                                int D, float softmax_scale, int8_t* q_i8, float* q_scale, void* stream) {
   sage_status s = check_shape(B, S, H, D);
@@ -696,6 +887,8 @@ sage_status sage_sync_status(void* stream) {
   if (e != cudaSuccess) return cuda_fail(e, "device error word read");
   if (code == SAGE_DEVERR_TIMEOUT)
     return fail(SAGE_ERR_TIMEOUT, "a device-side wait gave up after its time limit");
+  if (code == SAGE_DEVERR_BAD_PAGE)
+    return fail(SAGE_ERR_BAD_PAGE, "a page table led out of the cache, or a position out of its table");
   return SAGE_OK;
 }
 
@@ -718,6 +911,7 @@ const char* sage_status_string(sage_status s) {
     case SAGE_ERR_NO_MEMORY: return "SAGE_ERR_NO_MEMORY";
     case SAGE_ERR_TIMEOUT: return "SAGE_ERR_TIMEOUT";
     case SAGE_ERR_WORKSPACE: return "SAGE_ERR_WORKSPACE";
+    case SAGE_ERR_BAD_PAGE: return "SAGE_ERR_BAD_PAGE";
   }
   return "SAGE_ERR_UNKNOWN";
 }

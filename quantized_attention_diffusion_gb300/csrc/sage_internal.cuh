@@ -15,7 +15,7 @@ constexpr int kQKBlock = 32;    // tokens per Q/K quantisation block
 constexpr int kTile = 128;      // query rows per Q tile and keys per KV tile
 
 // Device error word codes (read back by the host after a stream sync).
-enum : int { SAGE_DEVERR_NONE = 0, SAGE_DEVERR_TIMEOUT = 1 };
+enum : int { SAGE_DEVERR_NONE = 0, SAGE_DEVERR_TIMEOUT = 1, SAGE_DEVERR_BAD_PAGE = 2 };
 
 inline int padded_len(int S) { return (S + kTile - 1) / kTile * kTile; }
 inline int num_blocks(int S) { return (S + kQKBlock - 1) / kQKBlock; }
@@ -84,6 +84,72 @@ cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream);
 // stream capture that launches them does not have to load a module.
 cudaError_t load_attention_kernels();
 cudaError_t load_quantize_kernels();
+
+// ---------------------------------------------------- quantised KV cache --
+
+// A paged cache: K codes int8 and V codes E4M3 [num_pages, H, page, 128],
+// scales fp32 [num_pages, H, page], page = 1 << page_shift tokens.
+struct CacheView {
+  uint8_t* k_codes;
+  float* k_scale;
+  uint8_t* v_codes;
+  float* v_scale;
+  int num_pages, H, page_shift;
+};
+
+// Position i of sequence b is token i % page of page table[b * stride + i / page].
+struct PageTable {
+  const int32_t* pages;
+  int width;
+  int64_t stride;
+};
+
+constexpr int kMaxCacheLen = 1 << 30;   // positions of one sequence
+
+struct CacheWriteArgs {
+  CacheView cache;
+  const uint16_t *k, *v;                 // bf16 [B, S, H, 128], heads dense
+  int64_t k_sb, k_ss, v_sb, v_ss;        // batch and token strides, in elements
+  int B, S;
+  PageTable table;
+  const int32_t* start;                  // [B]: position of each sequence's first new token
+  const int32_t* count;                  // [B] or nullptr: new tokens of each sequence (nullptr: S)
+  int* err;                              // device error word
+};
+cudaError_t launch_kv_cache_write(const CacheWriteArgs& a, cudaStream_t stream);
+
+struct CacheReadArgs {
+  CacheView cache;
+  PageTable table;
+  const int32_t* lens;                   // [B]
+  uint16_t *k, *v;                       // bf16 [B, S, H, 128]
+  int B, S;
+  int* err;
+};
+cudaError_t launch_kv_cache_read(const CacheReadArgs& a, cudaStream_t stream);
+
+struct CacheAttnArgs {
+  CacheView cache;
+  PageTable table;
+  const int32_t* lens;                   // [B]
+  const int32_t* prefix_pages;           // pages of the shared prefix (nullptr: none)
+  int prefix_len;
+  const uint16_t* q;                     // bf16 [B, Sq, Hq, 128], heads dense
+  int64_t q_sb, q_ss;                    // batch and token strides, in elements
+  uint16_t* out;                         // bf16 [B, Sq, Hq, 128]
+  float* lse;                            // fp32 [B, Hq, Sq] or nullptr
+  int B, Sq, Hq;
+  bool causal;
+  float softmax_scale;
+  void* workspace;
+  uint64_t timeout_ns;
+  int* err;
+};
+size_t cache_attn_workspace_bytes(int B, int Sq, int Hq, int Hkv, int prefix_len);
+cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream);
+
+// Address of the current device's error word.
+cudaError_t device_error_word(int** word);
 
 // Records printf-style text as this thread's sage_last_error() message.
 void set_last_error(const char* fmt, ...);

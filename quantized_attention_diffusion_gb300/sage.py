@@ -27,6 +27,7 @@ HEAD_DIM = 128
 _STATUS = {
     0: "SAGE_OK", 1: "SAGE_ERR_INVALID_ARG", 2: "SAGE_ERR_UNSUPPORTED", 3: "SAGE_ERR_MISALIGNED",
     4: "SAGE_ERR_CUDA", 5: "SAGE_ERR_NO_MEMORY", 6: "SAGE_ERR_TIMEOUT", 7: "SAGE_ERR_WORKSPACE",
+    8: "SAGE_ERR_BAD_PAGE",
 }
 EXPORTED = (
     "sage_padded_len", "sage_workspace_bytes", "sage_quantize_qkv", "sage_attn_fwd",
@@ -37,7 +38,8 @@ EXPORTED = (
     "sage_debug_fused_q", "sage_attn_fwd_fused_q", "sage_quantize_qkv_smooth_k",
     "sage_attn_fwd_smooth_k", "sage_attn_fwd_launches", "sage_debug_staging_codes",
     "sage_debug_inject_fault", "sage_debug_pool_state", "sage_plan_create", "sage_plan_launch",
-    "sage_plan_destroy", "sage_plan_create_ex",
+    "sage_plan_destroy", "sage_plan_create_ex", "sage_kv_cache_write", "sage_kv_cache_read",
+    "sage_attn_fwd_cache", "sage_attn_fwd_cache_prefix", "sage_attn_fwd_cache_workspace_bytes",
 )
 
 # Options of sage_plan_create_ex (include/sage.h).
@@ -45,6 +47,17 @@ PLAN_SMOOTH_K, PLAN_FUSED_Q = 1, 2
 
 # Fault sites of sage_debug_inject_fault (include/sage.h).
 FAULT_NONE, FAULT_POOL_ALLOC, FAULT_QUANT_LAUNCH, FAULT_ATTN_LAUNCH = 0, 1, 2, 3
+
+
+# Page sizes of the quantised KV cache (include/sage.h).
+KV_PAGE_SIZES = (16, 32, 64, 128, 256)
+
+
+class _KVCache(ctypes.Structure):
+    """sage_kv_cache (include/sage.h)."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("page_size", ctypes.c_int32)]
 
 
 class SageError(RuntimeError):
@@ -71,7 +84,7 @@ def load_library(path: str = LIB_PATH):
                 f"{path} is missing: build it with `python -m quantized_attention_diffusion_gb300.build`")
         lib = ctypes.CDLL(path)
         P, I, F, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
-        S = ctypes.c_int
+        S, L = ctypes.c_int, ctypes.c_int64
         sigs = {
             "sage_padded_len": (ctypes.c_int64, [I]),
             "sage_attn_fwd_launches": (I, [I, I, I, I, I]),
@@ -96,6 +109,11 @@ def load_library(path: str = LIB_PATH):
             "sage_debug_staging_codes": (S, [P, P, I, I, I, I, P, P, P, P, P]),
             "sage_debug_inject_fault": (S, [I, I]),
             "sage_debug_pool_state": (S, [P, P]),
+            "sage_kv_cache_write": (S, [P, P, P, L, L, L, L, I, I, I, P, I, L, P, P, P]),
+            "sage_kv_cache_read": (S, [P, P, I, L, P, P, P, I, I, I, P]),
+            "sage_attn_fwd_cache": (S, [P, L, L, P, P, I, L, P, P, P, I, I, I, I, F, I, P, Z, P]),
+            "sage_attn_fwd_cache_prefix": (S, [P, L, L, P, P, I, P, I, L, P, P, P, I, I, I, I, F, I, P, Z, P]),
+            "sage_attn_fwd_cache_workspace_bytes": (Z, [I, I, I, I, I]),
             "sage_sync_status": (S, [P]),
             "sage_set_wait_timeout_ns": (None, [ctypes.c_uint64]),
             "sage_set_attention_events": (None, [P, P]),
@@ -507,3 +525,191 @@ def debug_pool_state(device=None):
     with torch.cuda.device(dev):
         _check(lib.sage_debug_pool_state(ctypes.byref(created), ctypes.byref(used)))
     return bool(created.value), int(used.value)
+
+
+def kv_cache_alloc(num_pages: int, H: int, page_size: int = 64, device=None):
+    """Tensors of an empty paged KV cache: (k_codes int8 [num_pages, H,
+    page_size, 128], k_scale fp32 [num_pages, H, page_size], v_codes
+    float8_e4m3fn like k_codes, v_scale like k_scale), the tuple that the other
+    kv_cache_* and attn_fwd_cache* functions take.  Contents are undefined
+    until they are written."""
+    if page_size not in KV_PAGE_SIZES:
+        raise ValueError(f"page_size must be one of {KV_PAGE_SIZES} (got {page_size})")
+    if num_pages < 1 or H < 1:
+        raise ValueError(f"num_pages and H must be >= 1 (got {num_pages}, {H})")
+    dev = torch.device("cuda") if device is None else torch.device(device)
+    codes, scales = (num_pages, H, page_size, HEAD_DIM), (num_pages, H, page_size)
+    return (torch.empty(codes, dtype=torch.int8, device=dev), torch.empty(scales, dtype=torch.float32, device=dev),
+            torch.empty(codes, dtype=torch.float8_e4m3fn, device=dev),
+            torch.empty(scales, dtype=torch.float32, device=dev))
+
+
+def _check_cache(cache):
+    """The cache tuple as a sage_kv_cache, and its device."""
+    if not isinstance(cache, (tuple, list)) or len(cache) != 4:
+        raise TypeError("cache must be (k_codes, k_scale, v_codes, v_scale)")
+    kc, ks, vc, vs = cache
+    dev = kc.device
+    for name, t, dtypes in (("k_codes", kc, (torch.int8,)), ("k_scale", ks, (torch.float32,)),
+                            ("v_codes", vc, (torch.float8_e4m3fn, torch.uint8)), ("v_scale", vs, (torch.float32,))):
+        if t.dtype not in dtypes:
+            raise ValueError(f"{name} must be {dtypes[0]} (got {t.dtype})")
+        if not t.is_cuda or t.device != dev:
+            raise ValueError("the cache must be CUDA tensors on one device")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    shape = kc.shape
+    if len(shape) != 4 or vc.shape != shape or ks.shape != shape[:3] or vs.shape != shape[:3]:
+        raise ValueError(f"a cache is codes [num_pages, H, page_size, 128] and scales [num_pages, H, page_size] "
+                         f"(got {tuple(kc.shape)}, {tuple(ks.shape)}, {tuple(vc.shape)}, {tuple(vs.shape)})")
+    if shape[3] != HEAD_DIM or shape[2] not in KV_PAGE_SIZES or shape[0] < 1 or shape[1] < 1:
+        raise ValueError(f"a cache has 128 channels and pages of {KV_PAGE_SIZES} tokens (got {tuple(shape)})")
+    return _KVCache(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), shape[0], shape[1], shape[2]), dev
+
+
+def _check_rows(name, t, dev, H=None):
+    """bf16 [B, S, H, 128] whose tokens' heads are dense: (batch stride, token
+    stride) in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be bfloat16 (got {t.dtype})")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on the cache's device {dev} (got {t.device})")
+    shape = t.shape
+    if len(shape) != 4 or shape[3] != HEAD_DIM or 0 in shape or (H is not None and shape[2] != H):
+        raise ValueError(f"{name} must be [B, S, {'H' if H is None else H}, 128] (got {tuple(shape)})")
+    sb, ss, sh, sd = t.stride()
+    if sd != 1 or (sh != HEAD_DIM and shape[2] > 1):
+        raise ValueError(f"the heads of a token of {name} must be dense (strides {t.stride()})")
+    return sb if shape[0] > 1 else 0, ss if shape[1] > 1 else 0
+
+
+def _check_table(table, B, dev, name="block_table"):
+    if table.dtype != torch.int32 or table.device != dev or table.dim() != 2 or table.shape[0] != B \
+            or table.shape[1] < 1 or table.stride(1) != 1 and table.shape[1] > 1:
+        raise ValueError(f"{name} must be an int32 [{B}, pages] tensor with dense rows on {dev}")
+    return table.shape[1], table.stride(0) if B > 1 else 0
+
+
+def _check_ints(name, t, n, dev):
+    if t.dtype != torch.int32 or t.device != dev or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor on {dev}")
+
+
+def kv_cache_write(k, v, cache, block_table, start, count=None):
+    """Quantise k and v, bf16 [B, S, H, 128] (slices of a projection are
+    taken as they are), and put token i of sequence b at position start[b] + i of
+    the cache, through sage_kv_cache_write.  ``block_table`` int32 [B, pages]
+    names the pages of each sequence, ``start`` int32 [B]; with ``count`` int32
+    [B] only the first count[b] tokens of a padded sequence are written.
+    Returns ``cache``."""
+    lib = load_library()
+    c, dev = _check_cache(cache)
+    k_sb, k_ss = _check_rows("k", k, dev, c.H)
+    v_sb, v_ss = _check_rows("v", v, dev, c.H)
+    if k.shape != v.shape:
+        raise ValueError(f"k and v must have equal shapes (got {tuple(k.shape)}, {tuple(v.shape)})")
+    B, S = k.shape[:2]
+    width, stride = _check_table(block_table, B, dev)
+    _check_ints("start", start, B, dev)
+    if count is not None:
+        _check_ints("count", count, B, dev)
+    with torch.cuda.device(dev):
+        _check(lib.sage_kv_cache_write(ctypes.byref(c), _ptr(k), _ptr(v), k_sb, k_ss, v_sb, v_ss, B, S, HEAD_DIM,
+                                       _ptr(block_table), width, stride, _ptr(start), _ptr(count), _stream(dev)))
+    return cache
+
+
+def kv_cache_read(cache, block_table, lens, S: int, out=None):
+    """The first S positions of each sequence in the cache as bf16 (k, v),
+    each [B, S, H, 128], zeros from position lens[b] on (sage_kv_cache_read).
+    ``out`` (optional) is the pair of tensors to fill."""
+    lib = load_library()
+    c, dev = _check_cache(cache)
+    if lens.dim() != 1:
+        raise ValueError("lens must be an int32 [B] tensor")
+    B = lens.shape[0]
+    if B < 1 or S < 1:
+        raise ValueError(f"B and S must be >= 1 (got {B}, {S})")
+    width, stride = _check_table(block_table, B, dev)
+    _check_ints("lens", lens, B, dev)
+    shape = (B, int(S), c.H, HEAD_DIM)
+    if out is None:
+        out = (torch.empty(shape, dtype=torch.bfloat16, device=dev), torch.empty(shape, dtype=torch.bfloat16, device=dev))
+    for t in out:
+        if tuple(t.shape) != shape or t.dtype != torch.bfloat16 or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"out must be two contiguous bf16 tensors {shape} on {dev}")
+    with torch.cuda.device(dev):
+        _check(lib.sage_kv_cache_read(ctypes.byref(c), _ptr(block_table), width, stride, _ptr(lens), _ptr(out[0]),
+                                      _ptr(out[1]), B, int(S), HEAD_DIM, _stream(dev)))
+    return out
+
+
+def attn_fwd_cache_workspace_bytes(B: int, Sq: int, Hq: int, H: int, prefix_len: int = 0) -> int:
+    return int(load_library().sage_attn_fwd_cache_workspace_bytes(B, Sq, Hq, H, prefix_len))
+
+
+def _attn_fwd_cache(q, cache, prefix, block_table, lens, softmax_scale, causal, out, lse, return_lse, workspace):
+    lib = load_library()
+    c, dev = _check_cache(cache)
+    q_sb, q_ss = _check_rows("q", q, dev)
+    B, Sq, Hq, D = q.shape
+    if Hq % c.H:
+        raise ValueError(f"q's heads ({Hq}) must be a multiple of the cache's ({c.H})")
+    width, stride = _check_table(block_table, B, dev)
+    _check_ints("lens", lens, B, dev)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(D)
+    if out is None:
+        out = torch.empty((B, Sq, Hq, D), dtype=torch.bfloat16, device=dev)
+    elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != dev:
+        raise ValueError("out must be a contiguous bf16 tensor of q's shape on its device")
+    if lse is None and return_lse:
+        lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=dev)
+    elif lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq, Sq)
+                              or not lse.is_contiguous() or lse.device != dev):
+        raise ValueError("lse must be a contiguous float32 [B, Hq, Sq] tensor on q's device")
+    ws_bytes = 0
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on q's device")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    tail = (_ptr(block_table), width, stride, _ptr(lens), _ptr(out), _ptr(lse), B, Sq, Hq, D, float(softmax_scale),
+            int(bool(causal)), _ptr(workspace), ws_bytes)
+    with torch.cuda.device(dev):
+        if prefix is None:
+            _check(lib.sage_attn_fwd_cache(_ptr(q), q_sb, q_ss, ctypes.byref(c), *tail, _stream(dev)))
+        else:
+            table, length = prefix
+            if length < 1 or table.dim() != 1 or table.shape[0] < -(-length // c.page_size):
+                raise ValueError(f"prefix_table must name the pages of prefix_len >= 1 positions (got "
+                                 f"{tuple(table.shape)} for {length})")
+            _check_ints("prefix_table", table, table.shape[0], dev)
+            _check(lib.sage_attn_fwd_cache_prefix(_ptr(q), q_sb, q_ss, ctypes.byref(c), _ptr(table), length, *tail,
+                                                  _stream(dev)))
+    return (out, lse) if lse is not None else out
+
+
+def attn_fwd_cache(q, cache, block_table, lens, softmax_scale: float | None = None, causal: bool = True, out=None,
+                   lse=None, return_lse: bool = False, workspace=None):
+    """Attention of q, bf16 [B, Sq, Hq, 128], the newest Sq tokens of each
+    sequence, over the lens[b] positions that each has in the cache (their own
+    among them), through sage_attn_fwd_cache: query head h reads key/value head h
+    // (Hq // H).  Returns out bf16 [B, Sq, Hq, 128], and lse fp32 [B, Hq, Sq]
+    with ``return_lse`` or when ``lse`` is given.  With ``causal`` query i sees
+    positions up to lens[b] - Sq + i; a query that sees nothing gives zeros and
+    -inf.  ``workspace`` (optional uint8 CUDA tensor of >=
+    attn_fwd_cache_workspace_bytes) replaces the library's pool."""
+    return _attn_fwd_cache(q, cache, None, block_table, lens, softmax_scale, causal, out, lse, return_lse, workspace)
+
+
+def attn_fwd_cache_prefix(q, cache, prefix_table, prefix_len: int, block_table, lens,
+                          softmax_scale: float | None = None, causal: bool = True, out=None, lse=None,
+                          return_lse: bool = False, workspace=None):
+    """attn_fwd_cache for sequences that all begin with the same prefix_len
+    positions, pages ``prefix_table`` (int32 [pages]): sequence b is the prefix
+    and then the lens[b] positions of its row of ``block_table``.  The prefix is
+    read and multiplied once for all sequences (sage_attn_fwd_cache_prefix)."""
+    return _attn_fwd_cache(q, cache, (prefix_table, int(prefix_len)), block_table, lens, softmax_scale, causal, out,
+                           lse, return_lse, workspace)
