@@ -381,7 +381,7 @@ sage_status sage_kv_cache_write(const sage_kv_cache* cache, const void* k, const
  * precisions or layouts (sage_attn_fwd_cross takes the result).
  *
  *   lens       in : int32 [B]
- *   k, v       out: bf16 [B, S, H, D], 16-byte aligned; position i of sequence
+ *   k, v       out: bf16 [B, S, H, D], 32-byte aligned; position i of sequence
  *                   b is bf16(fp32(code * scale)) for i < lens[b], zero from there
  * One launch.  B * S * H <= 2^31 - 1.  Errors as sage_kv_cache_write.
  */

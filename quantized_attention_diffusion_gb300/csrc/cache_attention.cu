@@ -5,15 +5,16 @@
 // sees, with kc, vc the codes and sk, sv the scales of key j's row:
 //
 //   x_j = (q_i . kc_j) * softmax_scale * log2 e * sk_j
-//   m   = max x_j,   L = sum 2^(x_j - m),   lse = ln 2 * (m + log2 L)
+//   L   = sum 2^(x_j - m),   lse = ln 2 * (m + log2 L)
 //   out = sum 2^(x_j - m) sv_j vc_j / L      (0, and lse = -inf, if no key is seen)
 //
-// The query heads that share a key/value head are rows of one tile, so the
-// cache is read once for all of them.  A row's weights of V are kept apart
-// from its sum: with w_j = x_j + log2 sv_j and M = max w_j the products are
-// formed from 2^(w_j - M), at most 1 whatever the scales of V are, in fp16 (a
-// relative rounding of 2^-11 or less for every weight above 2^-14 of the
-// largest, and 2^-25 of the largest below), and out = 2^(M - m) / L * sum.
+// for any reference m near the largest x_j.  The query heads that share a
+// key/value head are rows of one tile, so the cache is read once for all of
+// them.  A row's weights of V are kept apart from its sum: with y_j = x_j + log2
+// sv_j and a reference M near the largest y_j the products are formed from
+// 2^(y_j - M), below 2^8 whatever the scales of V are, in fp16 (a relative
+// rounding of 2^-11 or less for every weight above 2^-14 of 2^M, and 2^-25 of
+// 2^M below), and out = 2^(M - m) / L * sum.
 // Q enters as fp16 times a power of two that puts the row's largest magnitude
 // in [2^14, 2^15), and K's integer codes are exact in fp16, so that the
 // products of Q and K are exact but for values 2^-28 below the row's largest.
@@ -37,11 +38,13 @@ constexpr uint32_t kOffV = kTok * kHeadDim;
 constexpr uint32_t kOffKs = 2 * kTok * kHeadDim;
 constexpr uint32_t kOffVs = kOffKs + kTok * 4;
 constexpr uint32_t kStageBytes = kOffVs + kTok * 4;
-constexpr uint32_t kMergeBytes = kConsumers * 16 * kHeadDim * 4;
+constexpr uint32_t kMergeBytes = kConsumers * 8 * kHeadDim * 4;
 constexpr uint32_t kSmemBytes = kStages * kStageBytes + kMergeBytes;
 constexpr int kMaxCtas = 2 * 152;                         // two CTAs on each SM
 constexpr int kMaxBatch = 512;                            // sequences of one launch
 constexpr float kLog2e = 1.44269502162933349609375f;      // fp32(log2 e)
+constexpr float kLowest = -1e30f;                         // a reference below every score
+constexpr float kFar = 256.0f;                            // 2^8: weights stay below it (fp16: 65504)
 constexpr float kLn2 = 0.693147182464599609375f;          // fp32(ln 2)
 
 struct Params {
@@ -125,10 +128,15 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory"); }
 
-// 2^(a - b) for a <= b, 0 where both are -inf.
-__device__ __forceinline__ float ratio(float a, float b) { return b == -INFINITY ? 0.0f : ex2_approx(a - b); }
+// Transpose of an 8 x 8 matrix of 16-bit values, two to a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 
-// x * 2^e for a finite e, without an intermediate overflow or underflow.
+// The square root of 2^e: a product with 2^e is taken in two steps, so that
+// nothing in between overflows or vanishes.
 __device__ __forceinline__ float scale2(float e) { return ex2_approx(0.5f * e); }
 
 // A launch's work is a row of key tiles: for each sequence, each tile of query
@@ -203,15 +211,15 @@ struct Walk {
   __device__ int unit(const Place& x) const { return (x.b * p.row_tiles + x.rt) * p.cache.H + x.h; }
 };
 
-template <int RT, bool kPrefix>
-__global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) cache_attn_kernel(const Params p) {
-  constexpr int R = 16 * RT;
+template <int NT, bool kPrefix>
+__global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) cache_attn_kernel(const Params p) {
+  constexpr int R = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kStages], empty[kStages];
   __shared__ int abort_flag;
   __shared__ int s_len[kMaxBatch];
   __shared__ long long s_off[kPrefix ? 2 : kMaxBatch + 1];
-  __shared__ float s_m[kConsumers][16], s_w[kConsumers][16], s_l[kConsumers][16];
+  __shared__ float s_m[kConsumers][8], s_w[kConsumers][8], s_l[kConsumers][8];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_v = &abort_flag;
@@ -322,75 +330,75 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) cache_attn_kernel(c
       }
     } else {
       // ----------------------------------------------------------- compute --
-      // Lane (r, c) = (lane / 4, lane % 4) of the m16n8k16 products: rows r and
-      // r + 8 of A and of the accumulator, column r of B, and k indices 2c,
-      // 2c + 1, 2c + 8, 2c + 9.  The order of the summed index is free as long
-      // as A and B agree, so for Q K^T those are channels 32c + 4i .. + 3 in
-      // product i, which makes a lane's share of a key 32 bytes that lie
-      // together; for P V the output columns are free, and column r of product
-      // j is channel 16r + j, which makes a lane's share of a key 16 bytes.
+      // Keys are the rows of the m16n8k16 products' A and queries the columns of
+      // B, so that up to 8 queries cost 8 columns: S^T = K Q^T, then O^T = V^T
+      // P^T.  Lane (r, c) = (lane / 4, lane % 4) holds rows r and r + 8 of A and of
+      // the accumulator, column r of B, columns 2c and 2c + 1 of the
+      // accumulator, and the summed indices 2c, 2c + 1, 2c + 8, 2c + 9.  The
+      // order of a summed index is free as long as A and B agree, and so is that
+      // of V's channels: in product i of K Q^T those are channels 32c + 4i .. + 3,
+      // so that a lane's share of a key is 32 bytes that lie together, and rows r
+      // and r + 8 of product j of V^T P^T are channels 16r + 2j and 16r + 2j + 1,
+      // 16 bytes that lie together.
       const int r = lane >> 2, c = lane & 3;
-      float* merge = reinterpret_cast<float*>(smem + kStages * kStageBytes);
+      float4* merge = reinterpret_cast<float4*>(smem + kStages * kStageBytes);
       int it = 0;
       bool ok = true;
       for (long long f = f0; f < f1;) {
         const int hi = walk.keys(x.b, x.rt);
         const int last = static_cast<int>(min(static_cast<long long>(x.n), x.tile + (f1 - f)));
-        uint32_t q[RT][8][4];
-        float crow[RT][2];
-        int lim[RT][2];
+        const int rows = min(R, p.rows - x.rt * R);   // of this tile
+        uint32_t q[NT][8][2];
+        float crow[NT][2];           // of queries 2c, 2c + 1, as all arrays with [2] here
+        int lim[NT][2];
         int lo = INT_MAX;            // keys that every row sees
 #pragma unroll
-        for (int a = 0; a < RT; ++a) {
+        for (int a = 0; a < NT; ++a) {
+          const int rr = x.rt * R + a * 8 + r;
+          uint4 w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (rr < p.rows) {
+            const int per_seq = p.Sq * p.G;
+            const int seq = kPrefix ? rr / per_seq : x.b, in = kPrefix ? rr % per_seq : rr;
+            const uint16_t* src = p.q + seq * p.q_sb + (in / p.G) * p.q_ss + (x.h * p.G + in % p.G) * kHeadDim + c * 32;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+          }
+          const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+          uint32_t top = 0u;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) top = max(top, max(u[i] & 0x7FFFu, (u[i] >> 16) & 0x7FFFu));
+          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+          // 2^(141 - exponent of the row's maximum), at most 2^113
+          const uint32_t ex = min(240u, 268u - (top >> 7));
+          const float up = __uint_as_float(ex << 23);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            q[a][i >> 1][i & 1] = pack_f16(__uint_as_float(u[i] << 16) * up, __uint_as_float(u[i] & 0xFFFF0000u) * up);
+          const float back = p.c_scale * __uint_as_float((254u - ex) << 23);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int rr = x.rt * R + a * 16 + e * 8 + r;
-            uint4 w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
-            lim[a][e] = hi;
-            if (rr < p.rows) {
-              lim[a][e] = min(hi, walk.limit(x.b, rr));
-              const int per_seq = p.Sq * p.G;
-              const int seq = kPrefix ? rr / per_seq : x.b, in = kPrefix ? rr % per_seq : rr;
-              const uint16_t* src = p.q + seq * p.q_sb + (in / p.G) * p.q_ss + (x.h * p.G + in % p.G) * kHeadDim + c * 32;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
-            }
+            crow[a][e] = __shfl_sync(0xFFFFFFFFu, back, (2 * c + e) * 4);
+            const int row = x.rt * R + a * 8 + 2 * c + e;
+            lim[a][e] = row < p.rows ? min(hi, walk.limit(x.b, row)) : hi;
             lo = min(lo, lim[a][e]);
-            const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
-            uint32_t top = 0u;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) top = max(top, max(u[i] & 0x7FFFu, (u[i] >> 16) & 0x7FFFu));
-            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            // 2^(141 - exponent of the row's maximum), at most 2^113
-            const uint32_t ex = min(240u, 268u - (top >> 7));
-            const float up = __uint_as_float(ex << 23);
-            crow[a][e] = p.c_scale * __uint_as_float((254u - ex) << 23);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-#pragma unroll
-              for (int g = 0; g < 2; ++g) {
-                const uint32_t v = u[2 * i + g];
-                q[a][i][2 * g + e] = pack_f16(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xFFFF0000u) * up);
-              }
-            }
           }
         }
         lo = __reduce_min_sync(0xFFFFFFFFu, lo);
 
-        float o[RT][16][4];
-        float m[RT][2], mw[RT][2], l[RT][2];
+        float o[NT][8][4];
+        float m[NT][2], mw[NT][2], l[NT][2];
 #pragma unroll
-        for (int a = 0; a < RT; ++a) {
+        for (int a = 0; a < NT; ++a) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
+          for (int j = 0; j < 8; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[a][j][e] = 0.0f;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            m[a][e] = mw[a][e] = -INFINITY;
+            m[a][e] = mw[a][e] = kLowest;
             l[a][e] = 0.0f;
           }
         }
@@ -403,102 +411,104 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) cache_attn_kernel(c
             const uint8_t* st = smem + s * kStageBytes;
             const uint8_t* kp = st + (warp * 16 + r) * kHeadDim + c * 32;
             const uint8_t* vp = st + kOffV + (warp * 16 + 2 * c) * kHeadDim + r * 16;
-            float sc[RT][2][4];
+            float sc[NT][4];
 #pragma unroll
-            for (int a = 0; a < RT; ++a)
+            for (int a = 0; a < NT; ++a)
 #pragma unroll
-              for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sc[a][n][e] = 0.0f;
+              for (int e = 0; e < 4; ++e) sc[a][e] = 0.0f;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              uint4 kw[2];
-#pragma unroll
-              for (int n = 0; n < 2; ++n) kw[n] = *reinterpret_cast<const uint4*>(kp + n * 8 * kHeadDim + half * 16);
+              const uint4 k0 = *reinterpret_cast<const uint4*>(kp + half * 16);
+              const uint4 k1 = *reinterpret_cast<const uint4*>(kp + 8 * kHeadDim + half * 16);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
+                uint32_t ka[4];
+                k_codes_f16(reinterpret_cast<const uint32_t*>(&k0)[i], ka[0], ka[2]);
+                k_codes_f16(reinterpret_cast<const uint32_t*>(&k1)[i], ka[1], ka[3]);
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                  uint32_t b0, b1;
-                  k_codes_f16(reinterpret_cast<const uint32_t*>(&kw[n])[i], b0, b1);
-#pragma unroll
-                  for (int a = 0; a < RT; ++a) mma_f16(sc[a][n], q[a][half * 4 + i], b0, b1);
-                }
-              }
-            }
-            // Scores of rows r (e 0, 1) and r + 8 (e 2, 3) for keys
-            // 8n + 2c, 8n + 2c + 1.
-            float ks[2][2], lv[2][2];
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const float2 k2 = *reinterpret_cast<const float2*>(st + kOffKs + (warp * 16 + n * 8 + 2 * c) * 4);
-              const float2 v2 = *reinterpret_cast<const float2*>(st + kOffVs + (warp * 16 + n * 8 + 2 * c) * 4);
-              ks[n][0] = k2.x;
-              ks[n][1] = k2.y;
-              lv[n][0] = lg2_approx(v2.x);
-              lv[n][1] = lg2_approx(v2.y);
-            }
-            const bool cut = t0 + 16 > lo;          // some row does not see all of these keys
-            uint32_t pa[RT][4];
-#pragma unroll
-            for (int a = 0; a < RT; ++a) {
-              float w[2][4];
-              float mx[2] = {m[a][0], m[a][1]}, mwx[2] = {mw[a][0], mw[a][1]};
-#pragma unroll
-              for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  float v = (sc[a][n][e] * crow[a][e >> 1]) * ks[n][e & 1];
-                  float vw = v + lv[n][e & 1];
-                  if (cut && t0 + n * 8 + 2 * c + (e & 1) >= lim[a][e >> 1]) v = vw = -INFINITY;
-                  sc[a][n][e] = v;
-                  w[n][e] = vw;
-                  mx[e >> 1] = fmaxf(mx[e >> 1], v);
-                  mwx[e >> 1] = fmaxf(mwx[e >> 1], vw);
-                }
-              bool moved = false;
-              float alpha[2];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 1));
-                mwx[e] = fmaxf(mwx[e], __shfl_xor_sync(0xFFFFFFFFu, mwx[e], 1));
-                mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 2));
-                mwx[e] = fmaxf(mwx[e], __shfl_xor_sync(0xFFFFFFFFu, mwx[e], 2));
-                l[a][e] *= ratio(m[a][e], mx[e]);
-                alpha[e] = ratio(mw[a][e], mwx[e]);
-                moved |= mwx[e] != mw[a][e];
-                m[a][e] = mx[e];
-                mw[a][e] = mwx[e];
-                if (mx[e] == -INFINITY) mx[e] = 0.0f;        // 2^(-inf - 0) = 0
-                if (mwx[e] == -INFINITY) mwx[e] = 0.0f;
-              }
-#pragma unroll
-              for (int n = 0; n < 2; ++n) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  l[a][e >> 1] += ex2_approx(sc[a][n][e] - mx[e >> 1]);
-                  w[n][e] = ex2_approx(w[n][e] - mwx[e >> 1]);
-                }
-                pa[a][2 * n] = pack_f16(w[n][0], w[n][1]);
-                pa[a][2 * n + 1] = pack_f16(w[n][2], w[n][3]);
-              }
-              if (__any_sync(0xFFFFFFFFu, moved)) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  o[a][j][0] *= alpha[0];
-                  o[a][j][1] *= alpha[0];
-                  o[a][j][2] *= alpha[1];
-                  o[a][j][3] *= alpha[1];
-                }
+                for (int a = 0; a < NT; ++a) mma_f16(sc[a], ka, q[a][half * 4 + i][0], q[a][half * 4 + i][1]);
               }
             }
             uint4 vw[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int tok = (k >> 1) * 8 + (k & 1);        // this lane's key 2c + tok
-              vw[k] = *reinterpret_cast<const uint4*>(vp + tok * kHeadDim);
+            for (int k = 0; k < 4; ++k)     // keys 2c, 2c + 1, 2c + 8, 2c + 9
+              vw[k] = *reinterpret_cast<const uint4*>(vp + ((k >> 1) * 8 + (k & 1)) * kHeadDim);
+            float ks[2], lv[2];             // of keys r and r + 8
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              ks[n] = *reinterpret_cast<const float*>(st + kOffKs + (warp * 16 + n * 8 + r) * 4);
+              lv[n] = lg2_approx(*reinterpret_cast<const float*>(st + kOffVs + (warp * 16 + n * 8 + r) * 4));
+            }
+            // sc[a][e]: key r + 8 (e / 2), query 2c + e % 2
+            float y[NT][4];
+#pragma unroll
+            for (int a = 0; a < NT; ++a)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                sc[a][e] = (sc[a][e] * crow[a][e & 1]) * ks[e >> 1];
+                y[a][e] = sc[a][e] + lv[e >> 1];
+              }
+            if (t0 + 16 > lo) {             // some row does not see all of these keys
+#pragma unroll
+              for (int a = 0; a < NT; ++a)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (t0 + r + 8 * (e >> 1) >= lim[a][e & 1]) sc[a][e] = y[a][e] = -INFINITY;
               // Codes behind the last key may be anything, NaN too.
-              if (t0 + 16 > hi && t0 + 2 * c + tok >= hi) vw[k] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (t0 + 2 * c + (k >> 1) * 8 + (k & 1) >= hi) vw[k] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            // The references m and M need not be the maxima, only near them:
+            // they move where a weight passes 2^8, which after the first keys is
+            // rare, and otherwise no value crosses lanes.
+            float pl[NT][4], pw[NT][4];
+            bool over = false;
+#pragma unroll
+            for (int a = 0; a < NT; ++a)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                pl[a][e] = ex2_approx(sc[a][e] - m[a][e & 1]);
+                pw[a][e] = ex2_approx(y[a][e] - mw[a][e & 1]);
+                over |= fmaxf(pl[a][e], pw[a][e]) > kFar;
+              }
+            if (__any_sync(0xFFFFFFFFu, over)) {
+#pragma unroll
+              for (int a = 0; a < NT; ++a) {
+                float alpha[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  float mx = fmaxf(fmaxf(sc[a][e], sc[a][e + 2]), m[a][e]);
+                  float wx = fmaxf(fmaxf(y[a][e], y[a][e + 2]), mw[a][e]);
+#pragma unroll
+                  for (int d = 4; d < 32; d <<= 1) {
+                    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+                    wx = fmaxf(wx, __shfl_xor_sync(0xFFFFFFFFu, wx, d));
+                  }
+                  l[a][e] *= ex2_approx(m[a][e] - mx);
+                  alpha[e] = ex2_approx(mw[a][e] - wx);
+                  m[a][e] = mx;
+                  mw[a][e] = wx;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  pl[a][e] = ex2_approx(sc[a][e] - m[a][e & 1]);
+                  pw[a][e] = ex2_approx(y[a][e] - mw[a][e & 1]);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) o[a][j][e] *= alpha[e & 1];
+              }
+            }
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int a = 0; a < NT; ++a) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) l[a][e & 1] += pl[a][e];
+              // (key r, queries 2c, 2c + 1) -> (query r, keys 2c, 2c + 1)
+              pb[a][0] = transpose8(pack_f16(pw[a][0], pw[a][1]));
+              pb[a][1] = transpose8(pack_f16(pw[a][2], pw[a][3]));
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -506,12 +516,12 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) cache_attn_kernel(c
               const uint32_t w2 = reinterpret_cast<const uint32_t*>(&vw[2])[i], w3 = reinterpret_cast<const uint32_t*>(&vw[3])[i];
               const uint32_t a01 = __byte_perm(w0, w1, 0x5140), b01 = __byte_perm(w0, w1, 0x7362);
               const uint32_t a23 = __byte_perm(w2, w3, 0x5140), b23 = __byte_perm(w2, w3, 0x7362);
+              const uint32_t va[4] = {v_codes_f16_lo(a01), v_codes_f16_hi(a01), v_codes_f16_lo(a23), v_codes_f16_hi(a23)};
+              const uint32_t vb[4] = {v_codes_f16_lo(b01), v_codes_f16_hi(b01), v_codes_f16_lo(b23), v_codes_f16_hi(b23)};
 #pragma unroll
-              for (int a = 0; a < RT; ++a) {
-                mma_f16(o[a][4 * i], pa[a], v_codes_f16_lo(a01), v_codes_f16_lo(a23));
-                mma_f16(o[a][4 * i + 1], pa[a], v_codes_f16_hi(a01), v_codes_f16_hi(a23));
-                mma_f16(o[a][4 * i + 2], pa[a], v_codes_f16_lo(b01), v_codes_f16_lo(b23));
-                mma_f16(o[a][4 * i + 3], pa[a], v_codes_f16_hi(b01), v_codes_f16_hi(b23));
+              for (int a = 0; a < NT; ++a) {
+                mma_f16(o[a][2 * i], va, pb[a][0], pb[a][1]);
+                mma_f16(o[a][2 * i + 1], vb, pb[a][0], pb[a][1]);
               }
             }
           }
@@ -519,33 +529,26 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) cache_attn_kernel(c
           if (lane == 0) mbar_arrive(&empty[s]);
         }
 
-        // The four warps' parts of the segment, 16 rows at a time.  A warp
-        // whose wait gave up takes part in the barriers and writes nothing.
+        // The four warps' parts of the segment, 8 rows at a time.  A warp whose
+        // wait gave up takes part in the barriers and writes nothing.
         const bool whole = x.tile == 0 && last == x.n;
         const int slot = !whole ? (x.tile > 0 ? 2 * blockIdx.x : 2 * blockIdx.x + 1)
                                 : 2 * static_cast<int>(gridDim.x) + walk.unit(x);
 #pragma unroll
-        for (int a = 0; a < RT; ++a) {
+        for (int a = 0; a < NT; ++a) {
+          if (a * 8 >= rows) break;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            l[a][e] += __shfl_xor_sync(0xFFFFFFFFu, l[a][e], 1);
-            l[a][e] += __shfl_xor_sync(0xFFFFFFFFu, l[a][e], 2);
-            if (c == 0) {
-              s_m[warp][e * 8 + r] = m[a][e];
-              s_w[warp][e * 8 + r] = mw[a][e];
-              s_l[warp][e * 8 + r] = l[a][e];
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) l[a][e] += __shfl_xor_sync(0xFFFFFFFFu, l[a][e], d);
+            if (r == 0) {
+              s_m[warp][2 * c + e] = m[a][e];
+              s_w[warp][2 * c + e] = mw[a][e];
+              s_l[warp][2 * c + e] = l[a][e];
             }
           }
           consumer_sync();
-          const int row = threadIdx.x >> 3, g8 = threadIdx.x & 7;   // 16 channels of a row a thread
-          float wrow[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float top = s_w[0][e * 8 + r];
-#pragma unroll
-            for (int k = 1; k < kConsumers; ++k) top = fmaxf(top, s_w[k][e * 8 + r]);
-            wrow[e] = ratio(mw[a][e], top);
-          }
+          const int row = threadIdx.x >> 4, g = threadIdx.x & 15;   // 8 channels of a row a thread
           float M = s_w[0][row], mm = s_m[0][row], L = 0.0f;
 #pragma unroll
           for (int k = 1; k < kConsumers; ++k) {
@@ -553,30 +556,33 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) cache_attn_kernel(c
             mm = fmaxf(mm, s_m[k][row]);
           }
 #pragma unroll
-          for (int k = 0; k < kConsumers; ++k) L += s_l[k][row] * ratio(s_m[k][row], mm);
-          // float4 i of channels 32c .. 32c + 31 stands at i ^ (lane % 8): the
+          for (int k = 0; k < kConsumers; ++k) L += s_l[k][row] * ex2_approx(s_m[k][row] - mm);
+          // float4 i of channels 16r .. 16r + 15 stands at 4r + (i ^ c): the
           // eight lanes of a store fall into distinct banks.
-          float4* buf = reinterpret_cast<float4*>(merge) + warp * 16 * 32;
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
+          for (int e = 0; e < 2; ++e) {
+            if (a * 8 + 2 * c + e < rows) {
+              float top = s_w[0][2 * c + e];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int j = (i & 3) * 4, k = 2 * e + (i >> 2);
-              buf[(e * 8 + r) * 32 + c * 8 + (i ^ (lane & 7))] =
-                  make_float4(o[a][j][k] * wrow[e], o[a][j + 1][k] * wrow[e], o[a][j + 2][k] * wrow[e], o[a][j + 3][k] * wrow[e]);
+              for (int k = 1; k < kConsumers; ++k) top = fmaxf(top, s_w[k][2 * c + e]);
+              const float w = ex2_approx(mw[a][e] - top);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                merge[(warp * 8 + 2 * c + e) * 32 + 4 * r + (i ^ c)] =
+                    make_float4(o[a][2 * i][e] * w, o[a][2 * i][e + 2] * w, o[a][2 * i + 1][e] * w, o[a][2 * i + 1][e + 2] * w);
             }
+          }
           consumer_sync();
-          const int rr = x.rt * R + a * 16 + row;
-          if (rr < p.rows && !abort_flag) {
-            float4 sum[4];
+          const int rr = x.rt * R + a * 8 + row;
+          if (a * 8 + row < rows && !abort_flag) {
+            float4 sum[2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int at = g8 * 4 + e, cc = at >> 3;
-              const int idx = row * 32 + cc * 8 + ((at & 7) ^ (((row & 1) << 2) | cc));
-              sum[e] = reinterpret_cast<const float4*>(merge)[idx];
+            for (int e = 0; e < 2; ++e) {
+              const int at = g * 2 + e, idx = row * 32 + (at & ~3) + ((at & 3) ^ (row >> 1));
+              sum[e] = merge[idx];
 #pragma unroll
               for (int k = 1; k < kConsumers; ++k) {
-                const float4 y = reinterpret_cast<const float4*>(merge)[k * 16 * 32 + idx];
+                const float4 y = merge[k * 8 * 32 + idx];
                 sum[e].x += y.x;
                 sum[e].y += y.y;
                 sum[e].z += y.z;
@@ -585,26 +591,20 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) cache_attn_kernel(c
             }
             if (whole && !p.keep) {
               const int t = rr / p.G, hq = x.h * p.G + rr % p.G;
-              const float half = L == 0.0f ? 0.0f : scale2(M - mm);
-              const float inv = L == 0.0f ? 0.0f : half / L;
-              uint32_t w[8];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                w[2 * e] = pack_bf16(sum[e].x * half * inv, sum[e].y * half * inv);
-                w[2 * e + 1] = pack_bf16(sum[e].z * half * inv, sum[e].w * half * inv);
-              }
-              uint4* dst = reinterpret_cast<uint4*>(
-                  p.out + ((static_cast<int64_t>(x.b) * p.Sq + t) * p.Hq + hq) * kHeadDim + g8 * 16);
-              dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-              dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-              if (p.lse != nullptr && g8 == 0)
+              const float half = scale2(M - mm), inv = L == 0.0f ? 0.0f : half / L;
+              const uint4 w = make_uint4(pack_bf16(sum[0].x * half * inv, sum[0].y * half * inv),
+                                         pack_bf16(sum[0].z * half * inv, sum[0].w * half * inv),
+                                         pack_bf16(sum[1].x * half * inv, sum[1].y * half * inv),
+                                         pack_bf16(sum[1].z * half * inv, sum[1].w * half * inv));
+              *reinterpret_cast<uint4*>(p.out + ((static_cast<int64_t>(x.b) * p.Sq + t) * p.Hq + hq) * kHeadDim + g * 8) = w;
+              if (p.lse != nullptr && g == 0)
                 p.lse[(static_cast<int64_t>(x.b) * p.Hq + hq) * p.Sq + t] = L == 0.0f ? -INFINITY : (mm + log2f(L)) * kLn2;
             } else {
-              const int64_t at = static_cast<int64_t>(slot) * R + a * 16 + row;
-              float4* dst = reinterpret_cast<float4*>(p.part_o + at * kHeadDim) + g8 * 4;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) dst[e] = sum[e];
-              if (g8 == 0) p.part_ml[at] = make_float4(mm, L, M, 0.0f);
+              const int64_t at = static_cast<int64_t>(slot) * R + a * 8 + row;
+              float4* dst = reinterpret_cast<float4*>(p.part_o + at * kHeadDim) + g * 2;
+              dst[0] = sum[0];
+              dst[1] = sum[1];
+              if (g == 0) p.part_ml[at] = make_float4(mm, L, M, 0.0f);
             }
           }
         }
@@ -700,7 +700,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const Mer
       ml = p.pre_ml + at;
     }
   };
-  float m = -INFINITY, M = -INFINITY;
+  float m = kLowest, M = kLowest;
   for (int i = threadIdx.x; i < total; i += kMergeWarps * 32) {
     const float* o;
     const float4* ml;
@@ -733,8 +733,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const Mer
     place(i, o, ml);
     const float4 v = *ml;
     const float4 y = reinterpret_cast<const float4*>(o)[lane];
-    L += v.y * ratio(v.x, m);
-    const float w = ratio(v.z, M);
+    L += v.y * ex2_approx(v.x - m);
+    const float w = ex2_approx(v.z - M);
     acc.x += y.x * w;
     acc.y += y.y * w;
     acc.z += y.z * w;
@@ -756,7 +756,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const Mer
     acc.w += y.w;
   }
   const int t = rr / p.G, hq = h * p.G + rr % p.G;
-  const float half = L == 0.0f ? 0.0f : scale2(M - m);
+  const float half = scale2(M - m);
   const float inv = L == 0.0f ? 0.0f : half / L;
   uint2 w;
   w.x = pack_bf16(acc.x * half * inv, acc.y * half * inv);
@@ -770,10 +770,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const Mer
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-// 16 query rows a tile where they are all, else 32: the products of a tile of
-// 16 rows take as long for 4 rows as for 16, and the keys are converted once
-// for all rows of a tile.
-int rows_per_tile(int rows) { return rows <= 16 ? 16 : 32; }
+// 8 or 16 query rows a tile where they are all, else 32: the keys are converted
+// once for all rows of a tile.
+int rows_per_tile(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 
 // One launch's part of the workspace.
 struct Layout {
@@ -819,8 +818,9 @@ cudaError_t launch_part(const Params& p, int R, bool prefix, unsigned ctas, cuda
     cfg.numAttrs = prefix ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, p);
   };
-  if (prefix) return R == 16 ? go(cache_attn_kernel<1, true>) : go(cache_attn_kernel<2, true>);
-  return R == 16 ? go(cache_attn_kernel<1, false>) : go(cache_attn_kernel<2, false>);
+  if (prefix)
+    return R == 8 ? go(cache_attn_kernel<1, true>) : R == 16 ? go(cache_attn_kernel<2, true>) : go(cache_attn_kernel<4, true>);
+  return R == 8 ? go(cache_attn_kernel<1, false>) : R == 16 ? go(cache_attn_kernel<2, false>) : go(cache_attn_kernel<4, false>);
 }
 
 unsigned ctas_for(long long tiles) { return static_cast<unsigned>(std::min<long long>(kMaxCtas, std::max(1ll, tiles))); }

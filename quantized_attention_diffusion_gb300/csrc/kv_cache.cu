@@ -14,9 +14,10 @@
 // nothing but what attends to it.  Reading back gives bf16(fl(code * scale)).
 //
 // Both kernels are bound by HBM: 512 bytes of bf16 and 264 bytes of codes and
-// scales per row.  One warp takes a row, lanes 0-15 its K and lanes 16-31 its
-// V, 8 channels (16 bytes of bf16, 8 of codes) a lane, so that a row's maximum
-// is four shuffles.
+// scales per row.  Eight lanes take a row, 16 channels each, and the four rows
+// of a warp are consecutive tokens of one head, whose codes and scales lie
+// together in a page; a warp does its K and then its V, so that no lane waits
+// for the other formula.
 #include <cuda_runtime.h>
 
 #include "qk_codes.cuh"
@@ -28,9 +29,26 @@ namespace sage {
 namespace {
 
 constexpr int kWarps = 8;      // per CTA
+constexpr int kRows = 4;       // tokens of one step of a warp
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+__device__ __forceinline__ float2 ffma2v(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 
 // Row index of token `pos` of sequence b and head h in the cache, or -1 where
 // the table or the cache does not reach: the caller then skips the row.
@@ -43,97 +61,120 @@ __device__ __forceinline__ int64_t cache_row(const CacheView& c, const PageTable
   return (((static_cast<int64_t>(page) * c.H + h) << c.page_shift) + (pos & ((1 << c.page_shift) - 1)));
 }
 
-// Codes of 8 values of a K row (bytes in channel order).
-__device__ __forceinline__ uint2 encode_k(const float (&x)[8], float sc) {
-  const float rcp = __frcp_rn(sc);
-  float c[8];
-  codes8(x, sc, rcp, sc >= 0x1p-125f && sc <= 0x1p125f, c);
-  uint32_t b[8];
+// -fl(x / sc) of the 8 bf16 values of w, for a scale in [2^-100, 2^125]:
+// Markstein's correction with the negated reciprocal nr = -fl(1 / sc), as in
+// quantize.cu's V encoder.
+__device__ __forceinline__ void quotients(const uint4& w, float sc, float nr, float2 (&y)[4]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  const float2 n2 = make_float2(nr, nr), s2 = make_float2(sc, sc);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) b[i] = (__float_as_uint(c[i] + kRoundMagic) - 0x4B400000u) & 0xFFu;
-  return make_uint2(b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24), b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24));
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = make_float2(bf16_lo(u[i]), bf16_hi(u[i]));
+    const float2 z = fmul2v(x, n2);
+    y[i] = ffma2v(ffma2v(z, s2, x), n2, z);
+  }
 }
 
-// Codes of 8 values of a V row.  The quotient is formed as in quantize.cu's
-// V encoder (Markstein's correction with the negated reciprocal gives
-// -fl(x / sv) for scales in [2^-100, 2^125]), outside that range by division.
-__device__ __forceinline__ uint2 encode_v(const float (&x)[8], float sv) {
-  float y[8];
-  if (sv >= 0x1p-100f && sv <= 0x1p125f) {
-    const float nr = -__frcp_rn(sv);
+// Eight codes, in channel order, of values whose row has scale sc.
+template <bool kIsV>
+__device__ __forceinline__ uint2 encode(const uint4& w, float sc, float nr, bool in_range) {
+  uint32_t code[2] = {0u, 0u};
+  if (in_range) {
+    float2 y[4];
+    quotients(w, sc, nr, y);
+    if constexpr (kIsV) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        code[i] = cvt_e4m3x4(y[2 * i].x, y[2 * i].y, y[2 * i + 1].x, y[2 * i + 1].y) ^ 0x80808080u;
+    } else {
+      // 1.5 * 2^23 - y: its low byte is the two's complement of rint(-y)
+      // (ties to even on either side), at most 127 in magnitude since
+      // |x| <= amax = 127 sc (1 + 2^-24).
+      const float2 magic = make_float2(kRoundMagic, kRoundMagic);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 a = fsub2v(magic, y[2 * i]), b = fsub2v(magic, y[2 * i + 1]);
+        const uint32_t lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
+        const uint32_t hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
+        code[i] = __byte_perm(lo, hi, 0x5410);
+      }
+    }
+  } else if (sc > 0.0f) {        // outside the quotient's range: by division (a scale of 0 or NaN: codes 0)
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float z = x[i] * nr;
-      y[i] = -fmaf(fmaf(z, sv, x[i]), nr, z);
+      const float x = (i & 1) ? bf16_hi(u[i >> 1]) : bf16_lo(u[i >> 1]);
+      uint32_t byte;
+      if constexpr (kIsV)
+        byte = cvt_e4m3x2(__fdiv_rn(x, sc), 0.0f) & 0xFFu;
+      else
+        byte = (__float_as_uint(code_by_division(x, sc) + kRoundMagic) - 0x4B400000u) & 0xFFu;
+      code[i >> 2] |= byte << (8 * (i & 3));
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = sv == 0.0f ? 0.0f : __fdiv_rn(x[i], sv);
   }
-  return make_uint2(cvt_e4m3x4(y[0], y[1], y[2], y[3]), cvt_e4m3x4(y[4], y[5], y[6], y[7]));
+  return make_uint2(code[0], code[1]);
 }
 
-// kRows rows a warp, their loads all in flight before the first is used.
-template <int kRows>
-__global__ void __launch_bounds__(kWarps * 32) kv_cache_write_kernel(const CacheWriteArgs a) {
-  const int lane = threadIdx.x & 31;
-  const bool is_v = lane >= 16;
-  const int c8 = (lane & 15) * 8;
-  const uint32_t total = static_cast<uint32_t>(a.B) * a.S * a.cache.H;      // < 2^31
-  const uint32_t r0 = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * kRows;
-  if (r0 >= total) return;
-  int h = static_cast<int>(r0 % a.cache.H);
-  int s = static_cast<int>(r0 / a.cache.H % a.S);
-  int b = static_cast<int>(r0 / a.cache.H / a.S);
-  uint4 raw[kRows];
-  int64_t row[kRows];
-  bool bad = false;
+// The rows of step i of a warp: head h, tokens 4 j .. 4 j + 3 of sequence b, the
+// head running fastest, then j.
+struct Step {
+  int b, s, h;
+};
+__device__ __forceinline__ Step step_of(uint32_t i, int H, int steps_per_seq) {
+  Step x;
+  const uint32_t j = i / static_cast<uint32_t>(H);
+  x.h = static_cast<int>(i - j * H);
+  x.b = static_cast<int>(j / static_cast<uint32_t>(steps_per_seq));
+  x.s = static_cast<int>(j - x.b * static_cast<uint32_t>(steps_per_seq)) * kRows;
+  return x;
+}
+
+// One tensor's part of a step: w0 and w1 are channels 8 l .. + 7 and 64 + 8 l ..
+// + 7 of the lane's row, l = lane % 8.
+template <bool kIsV>
+__device__ __forceinline__ void write_rows(const uint4& w0, const uint4& w1, uint8_t* codes, float* scales, int64_t row,
+                                           int l) {
+  // Magnitudes compare as integers, infinities and NaN above all others.
+  uint32_t top = 0u;
+  const uint32_t u[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    raw[i] = make_uint4(0u, 0u, 0u, 0u);
-    row[i] = -1;
-    if (r0 + i < total) {
-      const bool live = a.count == nullptr || s < __ldg(a.count + b);
-      if (live) {
-        const uint16_t* src = is_v ? a.v + b * a.v_sb + s * a.v_ss : a.k + b * a.k_sb + s * a.k_ss;
-        raw[i] = __ldcs(reinterpret_cast<const uint4*>(src + h * kHeadDim + c8));
-        row[i] = cache_row(a.cache, a.table, b, static_cast<int64_t>(__ldg(a.start + b)) + s, h);
-        bad |= row[i] < 0;
-      }
-      if (++h == a.cache.H) {
-        h = 0;
-        if (++s == a.S) {
-          s = 0;
-          ++b;
-        }
-      }
-    }
+  for (int e = 0; e < 8; ++e) top = max_u16x2(top, u[e] & 0x7FFF7FFFu);
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1) top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+  top = max(top & 0xFFFFu, top >> 16);
+  const float sc = top < 0x7F80u ? __fdiv_rn(__uint_as_float(top << 16), kIsV ? 448.0f : 127.0f) : __uint_as_float(0x7FC00000u);
+  const bool in_range = sc >= 0x1p-100f && sc <= 0x1p125f;
+  const float nr = -__frcp_rn(sc);
+  const uint2 c0 = encode<kIsV>(w0, sc, nr, in_range), c1 = encode<kIsV>(w1, sc, nr, in_range);
+  if (row >= 0) {
+    uint2* dst = reinterpret_cast<uint2*>(codes + row * kHeadDim) + l;
+    dst[0] = c0;
+    dst[8] = c1;
+    if (l == 0) scales[row] = sc;
   }
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-    // Magnitudes compare as integers, infinities and NaN above all others.
-    uint32_t top = 0u;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
-#pragma unroll
-    for (int off = 8; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
-    const bool finite = top < 0x7F80u;
-    const float sc = finite ? __fdiv_rn(__uint_as_float(top << 16), is_v ? 448.0f : 127.0f) : __uint_as_float(0x7FC00000u);
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[2 * e] = bf16_lo(w[e]);
-      x[2 * e + 1] = bf16_hi(w[e]);
-    }
-    uint2 code = make_uint2(0u, 0u);
-    if (finite) code = is_v ? encode_v(x, sc) : encode_k(x, sc);
-    if (row[i] >= 0) {
-      *reinterpret_cast<uint2*>((is_v ? a.cache.v_codes : a.cache.k_codes) + row[i] * kHeadDim + c8) = code;
-      if (c8 == 0) (is_v ? a.cache.v_scale : a.cache.k_scale)[row[i]] = sc;
-    }
+}
+
+__global__ void __launch_bounds__(kWarps * 32) kv_cache_write_kernel(const CacheWriteArgs a, uint32_t steps,
+                                                                     int steps_per_seq) {
+  const uint32_t i = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (i >= steps) return;                  // warp-uniform
+  const int lane = threadIdx.x & 31, l = lane & 7;
+  Step x = step_of(i, a.cache.H, steps_per_seq);
+  x.s += lane >> 3;
+  const bool live = x.s < a.S && (a.count == nullptr || x.s < __ldg(a.count + x.b));
+  uint4 k0 = make_uint4(0u, 0u, 0u, 0u), k1 = k0, v0 = k0, v1 = k0;
+  if (live) {
+    const uint4* k = reinterpret_cast<const uint4*>(a.k + x.b * a.k_sb + x.s * a.k_ss + x.h * kHeadDim) + l;
+    const uint4* v = reinterpret_cast<const uint4*>(a.v + x.b * a.v_sb + x.s * a.v_ss + x.h * kHeadDim) + l;
+    k0 = __ldcs(k);
+    k1 = __ldcs(k + 8);
+    v0 = __ldcs(v);
+    v1 = __ldcs(v + 8);
   }
-  if (bad && lane == 0) atomicExch(a.err, SAGE_DEVERR_BAD_PAGE);
+  const int64_t row = live ? cache_row(a.cache, a.table, x.b, static_cast<int64_t>(__ldg(a.start + x.b)) + x.s, x.h) : -1;
+  if (live && row < 0 && l == 0) atomicExch(a.err, SAGE_DEVERR_BAD_PAGE);
+  write_rows<false>(k0, k1, a.cache.k_codes, a.cache.k_scale, row, l);
+  write_rows<true>(v0, v1, a.cache.v_codes, a.cache.v_scale, row, l);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -153,94 +194,70 @@ __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t two) {
   return r;
 }
 
-template <int kRows>
-__global__ void __launch_bounds__(kWarps * 32) kv_cache_read_kernel(const CacheReadArgs a) {
-  const int lane = threadIdx.x & 31;
-  const bool is_v = lane >= 16;
-  const int c8 = (lane & 15) * 8;
-  const uint32_t total = static_cast<uint32_t>(a.B) * a.S * a.cache.H;      // < 2^31
-  const uint32_t r0 = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * kRows;
-  if (r0 >= total) return;
-  int h = static_cast<int>(r0 % a.cache.H);
-  int s = static_cast<int>(r0 / a.cache.H % a.S);
-  int b = static_cast<int>(r0 / a.cache.H / a.S);
-  uint2 code[kRows];
-  float sc[kRows];
-  bool bad = false;
+// 16 channels of a row to bf16, one 32-byte store.
+__device__ __forceinline__ void store_row(uint16_t* dst, const float (&x)[16], float sc) {
+  uint32_t w[8];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    code[i] = make_uint2(0u, 0u);
-    sc[i] = 0.0f;
-    if (r0 + i < total) {
-      if (s < __ldg(a.lens + b)) {
-        const int64_t row = cache_row(a.cache, a.table, b, s, h);
-        if (row >= 0) {
-          code[i] = __ldcs(reinterpret_cast<const uint2*>((is_v ? a.cache.v_codes : a.cache.k_codes) + row * kHeadDim + c8));
-          sc[i] = __ldg((is_v ? a.cache.v_scale : a.cache.k_scale) + row);
-        }
-        bad |= row < 0;
-      }
-      if (++h == a.cache.H) {
-        h = 0;
-        if (++s == a.S) {
-          s = 0;
-          ++b;
-        }
-      }
-    }
-  }
-  uint16_t* dst = (is_v ? a.v : a.k) + static_cast<int64_t>(r0) * kHeadDim + c8;
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    if (r0 + i >= total) break;
-    const uint32_t w[2] = {code[i].x, code[i].y};
-    float x[8];
-    if (is_v) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 p = e4m3x2_to_f32(w[e >> 1] >> (16 * (e & 1)));
-        x[2 * e] = p.x;
-        x[2 * e + 1] = p.y;
-      }
-    } else {
-      // byte + 128 in the low bits of 2^23 is exact: no integer conversion.
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t u = ((w[e >> 2] ^ 0x80808080u) >> (8 * (e & 3))) & 0xFFu;
-        x[e] = __uint_as_float(0x4B000000u | u) - 8388736.0f;
-      }
-    }
-    uint4 o;
-    o.x = pack_bf16(x[0] * sc[i], x[1] * sc[i]);
-    o.y = pack_bf16(x[2] * sc[i], x[3] * sc[i]);
-    o.z = pack_bf16(x[4] * sc[i], x[5] * sc[i]);
-    o.w = pack_bf16(x[6] * sc[i], x[7] * sc[i]);
-    __stcs(reinterpret_cast<uint4*>(dst + static_cast<int64_t>(i) * kHeadDim), o);
-  }
-  if (bad && lane == 0) atomicExch(a.err, SAGE_DEVERR_BAD_PAGE);
+  for (int i = 0; i < 8; ++i) w[i] = pack_bf16(x[2 * i] * sc, x[2 * i + 1] * sc);
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 
-// Four rows a warp keep enough loads in flight once every SM has its warps;
-// below that one row a warp spreads the rows over more SMs.
-constexpr uint32_t kManyRows = 152u * 64u * 4u;
+__global__ void __launch_bounds__(kWarps * 32) kv_cache_read_kernel(const CacheReadArgs a, uint32_t steps,
+                                                                    int steps_per_seq) {
+  const uint32_t i = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (i >= steps) return;                  // warp-uniform
+  const int lane = threadIdx.x & 31, l = lane & 7;
+  Step x = step_of(i, a.cache.H, steps_per_seq);
+  x.s += lane >> 3;
+  if (x.s >= a.S) return;
+  uint4 kc = make_uint4(0u, 0u, 0u, 0u), vc = kc;
+  float ks = 0.0f, vs = 0.0f;
+  if (x.s < __ldg(a.lens + x.b)) {
+    const int64_t row = cache_row(a.cache, a.table, x.b, x.s, x.h);
+    if (row >= 0) {
+      kc = __ldcs(reinterpret_cast<const uint4*>(a.cache.k_codes + row * kHeadDim) + l);
+      vc = __ldcs(reinterpret_cast<const uint4*>(a.cache.v_codes + row * kHeadDim) + l);
+      ks = __ldg(a.cache.k_scale + row);
+      vs = __ldg(a.cache.v_scale + row);
+    } else if (l == 0) {
+      atomicExch(a.err, SAGE_DEVERR_BAD_PAGE);
+    }
+  }
+  const int64_t dst = ((static_cast<int64_t>(x.b) * a.S + x.s) * a.cache.H + x.h) * kHeadDim + l * 16;
+  const uint32_t kw[4] = {kc.x, kc.y, kc.z, kc.w}, vw[4] = {vc.x, vc.y, vc.z, vc.w};
+  float y[16];
+  // byte + 128 in the low bits of 2^23 is exact: no integer conversion.
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    y[e] = __uint_as_float(__byte_perm(kw[e >> 2] ^ 0x80808080u, 0x4B000000u, 0x7440 + (e & 3))) - 8388736.0f;
+  store_row(a.k + dst, y, ks);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float2 two = e4m3x2_to_f32(vw[e >> 1] >> (16 * (e & 1)));
+    y[2 * e] = two.x;
+    y[2 * e + 1] = two.y;
+  }
+  store_row(a.v + dst, y, vs);
+}
 
 template <typename Args>
-cudaError_t launch_rows(void (*one)(Args), void (*four)(Args), const Args& a, cudaStream_t stream) {
-  const uint32_t total = static_cast<uint32_t>(a.B) * a.S * a.cache.H;
-  const bool many = total >= kManyRows;
-  const uint32_t per_cta = kWarps * (many ? 4u : 1u);
-  (many ? four : one)<<<(total + per_cta - 1) / per_cta, kWarps * 32, 0, stream>>>(a);
+cudaError_t launch_rows(void (*kernel)(Args, uint32_t, int), const Args& a, cudaStream_t stream) {
+  const int per_seq = (a.S + kRows - 1) / kRows;
+  const uint32_t steps = static_cast<uint32_t>(a.B) * per_seq * a.cache.H;
+  kernel<<<(steps + kWarps - 1) / kWarps, kWarps * 32, 0, stream>>>(a, steps, per_seq);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_kv_cache_write(const CacheWriteArgs& a, cudaStream_t stream) {
-  return launch_rows(kv_cache_write_kernel<1>, kv_cache_write_kernel<4>, a, stream);
+  return launch_rows(kv_cache_write_kernel, a, stream);
 }
 
 cudaError_t launch_kv_cache_read(const CacheReadArgs& a, cudaStream_t stream) {
-  return launch_rows(kv_cache_read_kernel<1>, kv_cache_read_kernel<4>, a, stream);
+  return launch_rows(kv_cache_read_kernel, a, stream);
 }
 
 }  // namespace sage

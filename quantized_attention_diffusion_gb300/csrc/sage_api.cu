@@ -765,6 +765,8 @@ sage_status sage_kv_cache_read(const sage_kv_cache* cache, const int32_t* block_
   if (s == SAGE_OK && static_cast<int64_t>(B) * cache->H > INT_MAX / S)
     s = fail(SAGE_ERR_INVALID_ARG, "B*S*H exceeds 2^31-1");
   if (s == SAGE_OK) s = check_ptrs({{k, "k"}, {v, "v"}});
+  if (s == SAGE_OK && !(aligned(k, 32) && aligned(v, 32)))
+    s = fail(SAGE_ERR_MISALIGNED, "k or v is not 32-byte aligned");
   if (s == SAGE_OK) s = check_ints(lens, "lens");
   if (s != SAGE_OK) return s;
   CacheReadArgs a;

@@ -82,6 +82,7 @@ def test_write_refuses(lib):
 def test_read_refuses(lib):
     assert read(lib, S=0) == INVALID
     assert read(lib, k=0) == INVALID and read(lib, v=FAKE + 8) == MISALIGNED
+    assert read(lib, k=FAKE + 16) == MISALIGNED and b"32-byte" in lib.sage_last_error()
     assert read(lib, lens=0) == INVALID and read(lib, lens=FAKE + 2) == MISALIGNED
     assert read(lib, B=1 << 16, S=1 << 14) == INVALID
 
