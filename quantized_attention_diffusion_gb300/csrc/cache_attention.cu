@@ -33,15 +33,19 @@ namespace {
 constexpr int kTok = 64;                                  // keys per tile
 constexpr int kConsumers = 4;                             // warps that compute, 16 keys of a tile each
 constexpr int kThreads = (kConsumers + 1) * 32;           // and one that copies
-constexpr int kStages = 4;
 constexpr uint32_t kOffV = kTok * kHeadDim;
 constexpr uint32_t kOffKs = 2 * kTok * kHeadDim;
 constexpr uint32_t kOffVs = kOffKs + kTok * 4;
 constexpr uint32_t kStageBytes = kOffVs + kTok * 4;
 constexpr uint32_t kMergeBytes = kConsumers * 8 * kHeadDim * 4;
-constexpr uint32_t kSmemBytes = kStages * kStageBytes + kMergeBytes;
-constexpr int kMaxCtas = 2 * 152;                         // two CTAs on each SM
+constexpr int kSms = 152;
+constexpr int kMaxCtas = 3 * kSms;                        // CTAs of a launch: three on each SM
 constexpr int kMaxBatch = 512;                            // sequences of one launch
+// As many as the registers of NT times 8 query rows allow without spilling much.
+__host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : nt == 2 ? 2 : 1; }
+// Tiles in flight: 9, 8 or 8 on an SM, 135 KB or more.
+__host__ __device__ constexpr int stages_of(int nt) { return nt == 1 ? 3 : nt == 2 ? 4 : 8; }
+constexpr uint32_t smem_of(int nt) { return stages_of(nt) * kStageBytes + kMergeBytes; }
 constexpr float kLog2e = 1.44269502162933349609375f;      // fp32(log2 e)
 constexpr float kLowest = -1e30f;                         // a reference below every score
 constexpr float kFar = 256.0f;                            // 2^8: weights stay below it (fp16: 65504)
@@ -211,9 +215,141 @@ struct Walk {
   __device__ int unit(const Place& x) const { return (x.b * p.row_tiles + x.rt) * p.cache.H + x.h; }
 };
 
+// What a warp holds of a unit's query rows.  Lane (r, c): queries 2c and 2c + 1 of
+// each eight in the arrays with [2], column r (a query) of the products' B in q.
+template <int NT>
+struct QueryRows {
+  uint32_t q[NT][8][2];
+  float crow[NT][2];
+  int lim[NT][2];            // keys that the row sees
+  float o[NT][8][4];         // channels 16r + 2j + e / 2, queries 2c + e % 2
+  float m[NT][2], mw[NT][2], l[NT][2];
+};
+
+// 16 keys, t0 .. t0 + 15, which stand at row `at` of the tile at st.  hi: keys
+// that some row sees; lo: keys that all see.
+template <int NT>
+__device__ __forceinline__ void attend(QueryRows<NT>& z, const uint8_t* st, int t0, int at, int r, int c, int hi, int lo) {
+  float sc[NT][4], y[NT][4];
+#pragma unroll
+  for (int a = 0; a < NT; ++a)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sc[a][e] = 0.0f;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const uint8_t* kp = st + (at + r) * kHeadDim + c * 32 + half * 16;
+    const uint4 k0 = *reinterpret_cast<const uint4*>(kp);
+    const uint4 k1 = *reinterpret_cast<const uint4*>(kp + 8 * kHeadDim);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t ka[4];
+      k_codes_f16(reinterpret_cast<const uint32_t*>(&k0)[i], ka[0], ka[2]);
+      k_codes_f16(reinterpret_cast<const uint32_t*>(&k1)[i], ka[1], ka[3]);
+#pragma unroll
+      for (int a = 0; a < NT; ++a) mma_f16(sc[a], ka, z.q[a][half * 4 + i][0], z.q[a][half * 4 + i][1]);
+    }
+  }
+  // sc[a][e]: key r + 8 (e / 2), query 2c + e % 2
+  float ks[2], lv[2];                 // of keys r and r + 8
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    ks[n] = *reinterpret_cast<const float*>(st + kOffKs + (at + n * 8 + r) * 4);
+    lv[n] = lg2_approx(*reinterpret_cast<const float*>(st + kOffVs + (at + n * 8 + r) * 4));
+  }
+#pragma unroll
+  for (int a = 0; a < NT; ++a)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      sc[a][e] = (sc[a][e] * z.crow[a][e & 1]) * ks[e >> 1];
+      y[a][e] = sc[a][e] + lv[e >> 1];
+    }
+  if (t0 + 16 > lo) {                 // some row does not see all of these keys
+#pragma unroll
+    for (int a = 0; a < NT; ++a)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (t0 + r + 8 * (e >> 1) >= z.lim[a][e & 1]) sc[a][e] = y[a][e] = -INFINITY;
+  }
+  bool over = false;
+  float pl[NT][4], pw[NT][4];
+#pragma unroll
+  for (int a = 0; a < NT; ++a)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      pl[a][e] = ex2_approx(sc[a][e] - z.m[a][e & 1]);
+      pw[a][e] = ex2_approx(y[a][e] - z.mw[a][e & 1]);
+      over |= fmaxf(pl[a][e], pw[a][e]) > kFar;
+    }
+  // The references m and M need not be the maxima, only near them: they move
+  // where a weight passes 2^8, which after the first keys is rare, and
+  // otherwise no value crosses lanes.
+  if (__any_sync(0xFFFFFFFFu, over)) {
+#pragma unroll
+    for (int a = 0; a < NT; ++a) {
+      float alpha[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float mx = fmaxf(z.m[a][e], fmaxf(sc[a][e], sc[a][e + 2]));
+        float wx = fmaxf(z.mw[a][e], fmaxf(y[a][e], y[a][e + 2]));
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+          wx = fmaxf(wx, __shfl_xor_sync(0xFFFFFFFFu, wx, d));
+        }
+        z.l[a][e] *= ex2_approx(z.m[a][e] - mx);
+        alpha[e] = ex2_approx(z.mw[a][e] - wx);
+        z.m[a][e] = mx;
+        z.mw[a][e] = wx;
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+          pl[a][e + k] = ex2_approx(sc[a][e + k] - mx);
+          pw[a][e + k] = ex2_approx(y[a][e + k] - wx);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z.o[a][j][e] *= alpha[e & 1];
+    }
+  }
+  uint32_t pb[NT][2];
+#pragma unroll
+  for (int a = 0; a < NT; ++a) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z.l[a][e & 1] += pl[a][e];
+    // (key r, queries 2c, 2c + 1) -> (query r, keys 2c, 2c + 1)
+    pb[a][0] = transpose8(pack_f16(pw[a][0], pw[a][1]));
+    pb[a][1] = transpose8(pack_f16(pw[a][2], pw[a][3]));
+  }
+  uint4 vw[4];
+  const uint8_t* vp = st + kOffV + (at + 2 * c) * kHeadDim + r * 16;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)         // keys 2c, 2c + 1, 2c + 8, 2c + 9
+    vw[k] = *reinterpret_cast<const uint4*>(vp + ((k >> 1) * 8 + (k & 1)) * kHeadDim);
+  if (t0 + 16 > hi) {                 // codes behind the last key may be anything, NaN too
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (t0 + 2 * c + (k >> 1) * 8 + (k & 1) >= hi) vw[k] = make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w0 = reinterpret_cast<const uint32_t*>(&vw[0])[i], w1 = reinterpret_cast<const uint32_t*>(&vw[1])[i];
+    const uint32_t w2 = reinterpret_cast<const uint32_t*>(&vw[2])[i], w3 = reinterpret_cast<const uint32_t*>(&vw[3])[i];
+    const uint32_t a01 = __byte_perm(w0, w1, 0x5140), b01 = __byte_perm(w0, w1, 0x7362);
+    const uint32_t a23 = __byte_perm(w2, w3, 0x5140), b23 = __byte_perm(w2, w3, 0x7362);
+    const uint32_t va[4] = {v_codes_f16_lo(a01), v_codes_f16_hi(a01), v_codes_f16_lo(a23), v_codes_f16_hi(a23)};
+    const uint32_t vb[4] = {v_codes_f16_lo(b01), v_codes_f16_hi(b01), v_codes_f16_lo(b23), v_codes_f16_hi(b23)};
+#pragma unroll
+    for (int a = 0; a < NT; ++a) {
+      mma_f16(z.o[a][2 * i], va, pb[a][0], pb[a][1]);
+      mma_f16(z.o[a][2 * i + 1], vb, pb[a][0], pb[a][1]);
+    }
+  }
+}
+
 template <int NT, bool kPrefix>
-__global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) cache_attn_kernel(const Params p) {
-  constexpr int R = 8 * NT;
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(const Params p) {
+  constexpr int R = 8 * NT, kStages = stages_of(NT);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kStages], empty[kStages];
   __shared__ int abort_flag;
@@ -348,9 +484,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) cache_attn_kernel(c
         const int hi = walk.keys(x.b, x.rt);
         const int last = static_cast<int>(min(static_cast<long long>(x.n), x.tile + (f1 - f)));
         const int rows = min(R, p.rows - x.rt * R);   // of this tile
-        uint32_t q[NT][8][2];
-        float crow[NT][2];           // of queries 2c, 2c + 1, as all arrays with [2] here
-        int lim[NT][2];
+        QueryRows<NT> z;
         int lo = INT_MAX;            // keys that every row sees
 #pragma unroll
         for (int a = 0; a < NT; ++a) {
@@ -376,30 +510,28 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) cache_attn_kernel(c
           const float up = __uint_as_float(ex << 23);
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            q[a][i >> 1][i & 1] = pack_f16(__uint_as_float(u[i] << 16) * up, __uint_as_float(u[i] & 0xFFFF0000u) * up);
+            z.q[a][i >> 1][i & 1] = pack_f16(__uint_as_float(u[i] << 16) * up, __uint_as_float(u[i] & 0xFFFF0000u) * up);
           const float back = p.c_scale * __uint_as_float((254u - ex) << 23);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            crow[a][e] = __shfl_sync(0xFFFFFFFFu, back, (2 * c + e) * 4);
+            z.crow[a][e] = __shfl_sync(0xFFFFFFFFu, back, (2 * c + e) * 4);
             const int row = x.rt * R + a * 8 + 2 * c + e;
-            lim[a][e] = row < p.rows ? min(hi, walk.limit(x.b, row)) : hi;
-            lo = min(lo, lim[a][e]);
+            z.lim[a][e] = row < p.rows ? min(hi, walk.limit(x.b, row)) : hi;
+            lo = min(lo, z.lim[a][e]);
           }
         }
         lo = __reduce_min_sync(0xFFFFFFFFu, lo);
 
-        float o[NT][8][4];
-        float m[NT][2], mw[NT][2], l[NT][2];
 #pragma unroll
         for (int a = 0; a < NT; ++a) {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[a][j][e] = 0.0f;
+            for (int e = 0; e < 4; ++e) z.o[a][j][e] = 0.0f;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            m[a][e] = mw[a][e] = kLowest;
-            l[a][e] = 0.0f;
+            z.m[a][e] = z.mw[a][e] = kLowest;
+            z.l[a][e] = 0.0f;
           }
         }
 
@@ -407,124 +539,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) cache_attn_kernel(c
           const int s = it % kStages;
           ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&full[s], (it / kStages) & 1, abort_v, p.err, p.timeout_ns));
           const int t0 = t * kTok + warp * 16;      // this warp's first key
-          if (ok && t0 < hi) {
-            const uint8_t* st = smem + s * kStageBytes;
-            const uint8_t* kp = st + (warp * 16 + r) * kHeadDim + c * 32;
-            const uint8_t* vp = st + kOffV + (warp * 16 + 2 * c) * kHeadDim + r * 16;
-            float sc[NT][4];
-#pragma unroll
-            for (int a = 0; a < NT; ++a)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) sc[a][e] = 0.0f;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const uint4 k0 = *reinterpret_cast<const uint4*>(kp + half * 16);
-              const uint4 k1 = *reinterpret_cast<const uint4*>(kp + 8 * kHeadDim + half * 16);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t ka[4];
-                k_codes_f16(reinterpret_cast<const uint32_t*>(&k0)[i], ka[0], ka[2]);
-                k_codes_f16(reinterpret_cast<const uint32_t*>(&k1)[i], ka[1], ka[3]);
-#pragma unroll
-                for (int a = 0; a < NT; ++a) mma_f16(sc[a], ka, q[a][half * 4 + i][0], q[a][half * 4 + i][1]);
-              }
-            }
-            uint4 vw[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)     // keys 2c, 2c + 1, 2c + 8, 2c + 9
-              vw[k] = *reinterpret_cast<const uint4*>(vp + ((k >> 1) * 8 + (k & 1)) * kHeadDim);
-            float ks[2], lv[2];             // of keys r and r + 8
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              ks[n] = *reinterpret_cast<const float*>(st + kOffKs + (warp * 16 + n * 8 + r) * 4);
-              lv[n] = lg2_approx(*reinterpret_cast<const float*>(st + kOffVs + (warp * 16 + n * 8 + r) * 4));
-            }
-            // sc[a][e]: key r + 8 (e / 2), query 2c + e % 2
-            float y[NT][4];
-#pragma unroll
-            for (int a = 0; a < NT; ++a)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                sc[a][e] = (sc[a][e] * crow[a][e & 1]) * ks[e >> 1];
-                y[a][e] = sc[a][e] + lv[e >> 1];
-              }
-            if (t0 + 16 > lo) {             // some row does not see all of these keys
-#pragma unroll
-              for (int a = 0; a < NT; ++a)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (t0 + r + 8 * (e >> 1) >= lim[a][e & 1]) sc[a][e] = y[a][e] = -INFINITY;
-              // Codes behind the last key may be anything, NaN too.
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (t0 + 2 * c + (k >> 1) * 8 + (k & 1) >= hi) vw[k] = make_uint4(0u, 0u, 0u, 0u);
-            }
-            // The references m and M need not be the maxima, only near them:
-            // they move where a weight passes 2^8, which after the first keys is
-            // rare, and otherwise no value crosses lanes.
-            float pl[NT][4], pw[NT][4];
-            bool over = false;
-#pragma unroll
-            for (int a = 0; a < NT; ++a)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                pl[a][e] = ex2_approx(sc[a][e] - m[a][e & 1]);
-                pw[a][e] = ex2_approx(y[a][e] - mw[a][e & 1]);
-                over |= fmaxf(pl[a][e], pw[a][e]) > kFar;
-              }
-            if (__any_sync(0xFFFFFFFFu, over)) {
-#pragma unroll
-              for (int a = 0; a < NT; ++a) {
-                float alpha[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  float mx = fmaxf(fmaxf(sc[a][e], sc[a][e + 2]), m[a][e]);
-                  float wx = fmaxf(fmaxf(y[a][e], y[a][e + 2]), mw[a][e]);
-#pragma unroll
-                  for (int d = 4; d < 32; d <<= 1) {
-                    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
-                    wx = fmaxf(wx, __shfl_xor_sync(0xFFFFFFFFu, wx, d));
-                  }
-                  l[a][e] *= ex2_approx(m[a][e] - mx);
-                  alpha[e] = ex2_approx(mw[a][e] - wx);
-                  m[a][e] = mx;
-                  mw[a][e] = wx;
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  pl[a][e] = ex2_approx(sc[a][e] - m[a][e & 1]);
-                  pw[a][e] = ex2_approx(y[a][e] - mw[a][e & 1]);
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) o[a][j][e] *= alpha[e & 1];
-              }
-            }
-            uint32_t pb[NT][2];
-#pragma unroll
-            for (int a = 0; a < NT; ++a) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) l[a][e & 1] += pl[a][e];
-              // (key r, queries 2c, 2c + 1) -> (query r, keys 2c, 2c + 1)
-              pb[a][0] = transpose8(pack_f16(pw[a][0], pw[a][1]));
-              pb[a][1] = transpose8(pack_f16(pw[a][2], pw[a][3]));
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t w0 = reinterpret_cast<const uint32_t*>(&vw[0])[i], w1 = reinterpret_cast<const uint32_t*>(&vw[1])[i];
-              const uint32_t w2 = reinterpret_cast<const uint32_t*>(&vw[2])[i], w3 = reinterpret_cast<const uint32_t*>(&vw[3])[i];
-              const uint32_t a01 = __byte_perm(w0, w1, 0x5140), b01 = __byte_perm(w0, w1, 0x7362);
-              const uint32_t a23 = __byte_perm(w2, w3, 0x5140), b23 = __byte_perm(w2, w3, 0x7362);
-              const uint32_t va[4] = {v_codes_f16_lo(a01), v_codes_f16_hi(a01), v_codes_f16_lo(a23), v_codes_f16_hi(a23)};
-              const uint32_t vb[4] = {v_codes_f16_lo(b01), v_codes_f16_hi(b01), v_codes_f16_lo(b23), v_codes_f16_hi(b23)};
-#pragma unroll
-              for (int a = 0; a < NT; ++a) {
-                mma_f16(o[a][2 * i], va, pb[a][0], pb[a][1]);
-                mma_f16(o[a][2 * i + 1], vb, pb[a][0], pb[a][1]);
-              }
-            }
-          }
+          if (ok && t0 < hi) attend<NT>(z, smem + s * kStageBytes, t0, warp * 16, r, c, hi, lo);
           __syncwarp();
           if (lane == 0) mbar_arrive(&empty[s]);
         }
@@ -540,11 +555,11 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) cache_attn_kernel(c
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) l[a][e] += __shfl_xor_sync(0xFFFFFFFFu, l[a][e], d);
+            for (int d = 4; d < 32; d <<= 1) z.l[a][e] += __shfl_xor_sync(0xFFFFFFFFu, z.l[a][e], d);
             if (r == 0) {
-              s_m[warp][2 * c + e] = m[a][e];
-              s_w[warp][2 * c + e] = mw[a][e];
-              s_l[warp][2 * c + e] = l[a][e];
+              s_m[warp][2 * c + e] = z.m[a][e];
+              s_w[warp][2 * c + e] = z.mw[a][e];
+              s_l[warp][2 * c + e] = z.l[a][e];
             }
           }
           consumer_sync();
@@ -565,11 +580,11 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) cache_attn_kernel(c
               float top = s_w[0][2 * c + e];
 #pragma unroll
               for (int k = 1; k < kConsumers; ++k) top = fmaxf(top, s_w[k][2 * c + e]);
-              const float w = ex2_approx(mw[a][e] - top);
+              const float w = ex2_approx(z.mw[a][e] - top);
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 merge[(warp * 8 + 2 * c + e) * 32 + 4 * r + (i ^ c)] =
-                    make_float4(o[a][2 * i][e] * w, o[a][2 * i][e + 2] * w, o[a][2 * i + 1][e] * w, o[a][2 * i + 1][e + 2] * w);
+                    make_float4(z.o[a][2 * i][e] * w, z.o[a][2 * i][e + 2] * w, z.o[a][2 * i + 1][e] * w, z.o[a][2 * i + 1][e + 2] * w);
             }
           }
           consumer_sync();
@@ -802,13 +817,14 @@ T* at(void* base, size_t off) {
 }
 
 cudaError_t launch_part(const Params& p, int R, bool prefix, unsigned ctas, cudaStream_t stream) {
+  const uint32_t smem = smem_of(R / 8);
   auto go = [&](auto kernel) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     // The prefix's launch follows the sequences' and needs nothing of it.
     cudaLaunchAttribute attr[1];
@@ -823,7 +839,9 @@ cudaError_t launch_part(const Params& p, int R, bool prefix, unsigned ctas, cuda
   return R == 8 ? go(cache_attn_kernel<1, false>) : R == 16 ? go(cache_attn_kernel<2, false>) : go(cache_attn_kernel<4, false>);
 }
 
-unsigned ctas_for(long long tiles) { return static_cast<unsigned>(std::min<long long>(kMaxCtas, std::max(1ll, tiles))); }
+unsigned ctas_for(long long tiles, int R) {
+  return static_cast<unsigned>(std::min<long long>(kSms * ctas_per_sm(R / 8), std::max(1ll, tiles)));
+}
 
 }  // namespace
 
@@ -869,7 +887,7 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream) 
     p.err = a.err;
     p.room = static_cast<int>(std::min<int64_t>(kMaxCacheLen, static_cast<int64_t>(a.table.width) << a.cache.page_shift));
     // The lengths are on the device: as many CTAs as the table has room for.
-    const unsigned ctas = ctas_for(std::min<long long>(kMaxCtas, (static_cast<long long>(p.room) + kTok - 1) / kTok) * w.units);
+    const unsigned ctas = ctas_for(std::min<long long>(kMaxCtas, (static_cast<long long>(p.room) + kTok - 1) / kTok) * w.units, w.R);
     cudaError_t e = launch_part(p, w.R, false, ctas, stream);
     if (e != cudaSuccess) return e;
 
@@ -901,7 +919,7 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream) 
       p.info = at<int2>(a.workspace, u.info);
       const int n = (a.prefix_len + kTok - 1) / kTok;
       const long long tiles = static_cast<long long>(n) * u.units;
-      const unsigned pc = ctas_for(tiles);
+      const unsigned pc = ctas_for(tiles, u.R);
       e = launch_part(p, u.R, true, pc, stream);
       if (e != cudaSuccess) return e;
       mp.pre_o = p.part_o;
