@@ -329,7 +329,8 @@ sage_status sage_debug_staging_codes(const void* q, const void* k, int B, int S,
  *   v_scale  fp32   [num_pages, H, page_size]      V = v_codes * v_scale
  *
  * All four are device memory that the caller owns, 16-byte aligned.  H is the
- * number of key/value heads; page_size is 16, 32, 64, 128 or 256 tokens.
+ * number of key/value heads; page_size is 16, 32, 64, 128 or 256 tokens;
+ * num_pages * H * page_size <= 2^31 - 1.
  * Position i of sequence b is token i % page_size of page
  * block_table[b * table_stride + i / page_size]; a table has table_width
  * entries a row, of which a call reads those that its positions need.

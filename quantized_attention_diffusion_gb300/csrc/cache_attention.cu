@@ -23,10 +23,11 @@
 #include <cmath>
 #include <cuda_runtime.h>
 
-#include "sage_internal.cuh"
-#include "sm103_ptx.cuh"
+#include "cache_attention.cuh"
 
 namespace sage {
+
+using namespace cache;
 
 namespace {
 
@@ -38,40 +39,13 @@ constexpr uint32_t kOffKs = 2 * kTok * kHeadDim;
 constexpr uint32_t kOffVs = kOffKs + kTok * 4;
 constexpr uint32_t kStageBytes = kOffVs + kTok * 4;
 constexpr uint32_t kMergeBytes = kConsumers * 8 * kHeadDim * 4;
-constexpr int kSms = 152;
 constexpr int kMaxCtas = 3 * kSms;                        // CTAs of a launch: three on each SM
-constexpr int kMaxBatch = 512;                            // sequences of one launch
 // As many as the registers of NT times 8 query rows allow without spilling much.
 __host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : nt == 2 ? 2 : 1; }
 // Tiles in flight: 9, 8 or 8 on an SM, 135 KB or more.
 __host__ __device__ constexpr int stages_of(int nt) { return nt == 1 ? 3 : nt == 2 ? 4 : 8; }
 constexpr uint32_t smem_of(int nt) { return stages_of(nt) * kStageBytes + kMergeBytes; }
-constexpr float kLog2e = 1.44269502162933349609375f;      // fp32(log2 e)
-constexpr float kLowest = -1e30f;                         // a reference below every score
 constexpr float kFar = 256.0f;                            // 2^8: weights stay below it (fp16: 65504)
-constexpr float kLn2 = 0.693147182464599609375f;          // fp32(ln 2)
-
-struct Params {
-  CacheView cache;
-  PageTable table;           // of the sequences, or of the prefix (one row)
-  const int32_t* lens;       // [B] of this launch
-  const uint16_t* q;
-  int64_t q_sb, q_ss;
-  uint16_t* out;
-  float* lse;
-  int B, Sq, G, Hq;          // G query heads share a key/value head
-  int causal, prefix_len;
-  int room;                  // longest sequence the sequences' table can hold
-  int rows, row_tiles;       // query rows of one unit's key/value head, and tiles of them
-  float c_scale;             // softmax_scale * log2 e
-  int keep;                  // 1: every result goes to the workspace (merged with another launch's)
-  float* part_o;             // [slot][R][128]: sums relative to M
-  float4* part_ml;           // [slot][R]: m, L, M
-  int4* desc;                // [CTA]: the unit that begins in this CTA and ends in a later one
-  int2* info;                // [unit], with keep: first CTA and CTAs of the unit (0: its own slot)
-  uint64_t timeout_ns;
-  int* err;
-};
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -79,35 +53,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ float lg2_approx(float x) {
-  float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Four INT8 codes (one word) -> two pairs of fp16: code + 128 is put into the
-// low bits of 1024 and 1152 taken off again, both exact.
-__device__ __forceinline__ void k_codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t u = w ^ 0x80808080u;
-  lo = sub_f16x2(__byte_perm(u, 0x64646464u, 0x4140), 0x64806480u);
-  hi = sub_f16x2(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u);
 }
 
 // Two E4M3 codes in the low or high half of a word -> a pair of fp16.
@@ -138,82 +83,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-
-// The square root of 2^e: a product with 2^e is taken in two steps, so that
-// nothing in between overflows or vanishes.
-__device__ __forceinline__ float scale2(float e) { return ex2_approx(0.5f * e); }
-
-// A launch's work is a row of key tiles: for each sequence, each tile of query
-// rows and each key/value head (a unit) its tiles of 64 keys in order.  CTA c
-// takes tiles [c * per, (c + 1) * per), whatever units they belong to, so that
-// unequal lengths leave no SM idle.  The part of a unit that a CTA has is a
-// segment: a unit of one segment is written out at once, segments of a unit
-// that CTAs share go to the workspace (slot 2c + 1 for the unit that begins
-// in CTA c and ends later, slot 2c for one that began earlier) and the merge
-// kernel joins them in the order of the CTAs.
-struct Place {
-  int b, rt, h, tile, n;     // n: tiles of the unit
-};
-
-template <int R, bool kPrefix>
-struct Walk {
-  const Params& p;
-  const int* s_len;
-  const long long* s_off;
-
-  // Keys that query row rr of sequence b may see, in this launch's keys.
-  __device__ int limit(int b, int rr) const {
-    if constexpr (kPrefix) {
-      if (!p.causal) return p.prefix_len;
-      const int per_seq = p.Sq * p.G, seq = rr / per_seq, t = rr % per_seq / p.G;
-      return max(0, min(p.prefix_len, p.prefix_len + s_len[seq] - p.Sq + t + 1));
-    } else {
-      const int len = s_len[b];
-      return p.causal ? max(0, min(len, len - p.Sq + rr / p.G + 1)) : len;
-    }
-  }
-  // Keys that some row of the unit may see.
-  __device__ int keys(int b, int rt) const {
-    if constexpr (kPrefix) return p.prefix_len;
-    return limit(b, min(p.rows, (rt + 1) * R) - 1);
-  }
-  __device__ int tiles(int b, int rt) const { return max(1, (keys(b, rt) + kTok - 1) / kTok); }
-  __device__ int seqs() const { return kPrefix ? 1 : p.B; }
-
-  __device__ Place locate(long long f) const {
-    Place x;
-    int lo = 0, hi = seqs();
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s_off[mid] * p.cache.H <= f)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    long long rem = f - s_off[lo] * p.cache.H;
-    x.b = lo;
-    x.rt = 0;
-    x.n = tiles(lo, 0);
-    while (rem >= static_cast<long long>(x.n) * p.cache.H) {
-      rem -= static_cast<long long>(x.n) * p.cache.H;
-      x.n = tiles(lo, ++x.rt);
-    }
-    x.h = static_cast<int>(rem / x.n);
-    x.tile = static_cast<int>(rem % x.n);
-    return x;
-  }
-  __device__ void next(Place& x) const {
-    x.tile = 0;
-    if (++x.h < p.cache.H) return;
-    x.h = 0;
-    if (++x.rt == p.row_tiles) {
-      x.rt = 0;
-      ++x.b;
-    }
-    if (x.b < seqs()) x.n = tiles(x.b, x.rt);
-  }
-  __device__ int unit(const Place& x) const { return (x.b * p.row_tiles + x.rt) * p.cache.H + x.h; }
-};
 
 // What a warp holds of a unit's query rows.  Lane (r, c): queries 2c and 2c + 1 of
 // each eight in the arrays with [2], column r (a query) of the products' B in q.
@@ -363,8 +232,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
   // there is room; it waits for this grid before it reads anything from it.
   asm volatile("griddepcontrol.launch_dependents;");
 
-  const Walk<R, kPrefix> walk{p, s_len, s_off};
-  for (int i = threadIdx.x; i < p.B; i += kThreads) s_len[i] = max(0, min(p.room, __ldg(p.lens + i)));
+  const Walk<R, kTok, kPrefix> walk{p, s_len, s_off};
+  walk.load_lengths(s_len);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -374,23 +243,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
     fence_mbarrier_init();
   }
   __syncthreads();
-  if (warp == 0) {   // s_off[b]: tiles of the sequences before b, for one key/value head
-    long long base = 0;
-    for (int b0 = 0; b0 < walk.seqs(); b0 += 32) {
-      long long n = 0;
-      if (b0 + lane < walk.seqs())
-        for (int rt = 0; rt < p.row_tiles; ++rt) n += walk.tiles(b0 + lane, rt);
-      long long sum = n;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long up = __shfl_up_sync(0xFFFFFFFFu, sum, d);
-        if (lane >= d) sum += up;
-      }
-      if (b0 + lane < walk.seqs()) s_off[b0 + lane] = base + sum - n;
-      base += __shfl_sync(0xFFFFFFFFu, sum, 31);
-    }
-    if (lane == 0) s_off[walk.seqs()] = base;
-  }
+  if (warp == 0) walk.sum_tiles(s_off, lane);
   __syncthreads();
 
   const long long total = s_off[walk.seqs()] * p.cache.H;
@@ -493,9 +346,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
 #pragma unroll
           for (int i = 0; i < 4; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
           if (rr < p.rows) {
-            const int per_seq = p.Sq * p.G;
-            const int seq = kPrefix ? rr / per_seq : x.b, in = kPrefix ? rr % per_seq : rr;
-            const uint16_t* src = p.q + seq * p.q_sb + (in / p.G) * p.q_ss + (x.h * p.G + in % p.G) * kHeadDim + c * 32;
+            const uint16_t* src = walk.query(x, rr) + c * 32;
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
           }
@@ -505,8 +356,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
           for (int i = 0; i < 16; ++i) top = max(top, max(u[i] & 0x7FFFu, (u[i] >> 16) & 0x7FFFu));
           top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
           top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-          // 2^(141 - exponent of the row's maximum), at most 2^113
-          const uint32_t ex = min(240u, 268u - (top >> 7));
+          const uint32_t ex = row_exponent(top);
           const float up = __uint_as_float(ex << 23);
 #pragma unroll
           for (int i = 0; i < 16; ++i)
@@ -547,8 +397,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
         // The four warps' parts of the segment, 8 rows at a time.  A warp whose
         // wait gave up takes part in the barriers and writes nothing.
         const bool whole = x.tile == 0 && last == x.n;
-        const int slot = !whole ? (x.tile > 0 ? 2 * blockIdx.x : 2 * blockIdx.x + 1)
-                                : 2 * static_cast<int>(gridDim.x) + walk.unit(x);
 #pragma unroll
         for (int a = 0; a < NT; ++a) {
           if (a * 8 >= rows) break;
@@ -615,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
               if (p.lse != nullptr && g == 0)
                 p.lse[(static_cast<int64_t>(x.b) * p.Hq + hq) * p.Sq + t] = L == 0.0f ? -INFINITY : (mm + log2f(L)) * kLn2;
             } else {
-              const int64_t at = static_cast<int64_t>(slot) * R + a * 8 + row;
+              const int64_t at = static_cast<int64_t>(walk.slot(x, whole)) * p.slot_rows + a * 8 + row;
               float4* dst = reinterpret_cast<float4*>(p.part_o + at * kHeadDim) + g * 2;
               dst[0] = sum[0];
               dst[1] = sum[1];
@@ -623,13 +471,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
             }
           }
         }
-        if (threadIdx.x == 0 && x.tile == 0) {   // the unit begins here: how many CTAs have a part of it
-          const int ctas = static_cast<int>((f + x.n - 1) / per) - static_cast<int>(blockIdx.x) + 1;
-          if (p.keep)
-            p.info[walk.unit(x)] = make_int2(blockIdx.x, whole ? 0 : ctas);
-          else if (!whole)
-            p.desc[blockIdx.x] = make_int4(x.b, x.rt, x.h, ctas);
-        }
+        if (threadIdx.x == 0) walk.tell(x, whole, f, per);
         f += last - x.tile;
         walk.next(x);
       }
@@ -647,11 +489,11 @@ struct MergeParams {
   const float4* part_ml;
   const int4* desc;          // one key/value part alone
   const int2* info;          // a prefix and the sequences
-  int ctas, R, rows, row_tiles, H;
+  int ctas, R, slot_rows, rows, row_tiles, H;
   // The prefix's parts: closed form, every unit has as many tiles.
   const float* pre_o;
   const float4* pre_ml;
-  int pre_R, pre_n, pre_ctas;                       // rows of a tile, key tiles of a unit, CTAs
+  int pre_R, pre_slot_rows, pre_n, pre_ctas;        // rows of a tile and of a slot, key tiles of a unit, CTAs
   long long pre_per;                                // key tiles of a CTA
   uint16_t* out;
   float* lse;
@@ -659,9 +501,12 @@ struct MergeParams {
 };
 
 constexpr int kMergeWarps = 8;
+constexpr int kFewParts = 32;   // parts of a row that one warp joins: one lane each
 
-// One row a CTA: its segments' m, L and M first, then each warp sums every
-// eighth segment and the warps' sums are added in order.
+// Eight rows of a unit a CTA.  Where a row has up to 32 parts a warp takes a row:
+// each lane one part's m, L and M, then the parts' sums in order.  Rows of more
+// parts (few rows over many keys) take the CTA one after another, each warp every
+// eighth part, and the warps' sums are added in order.
 __global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const MergeParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ float s_red[kMergeWarps][2];
@@ -686,112 +531,146 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const Mer
     n = d.y == 0 ? 1 : d.y;
     if (d.y == 0) own = 2 * p.ctas + blockIdx.x;
   }
-  const int rr = rt * p.R + static_cast<int>(blockIdx.y);
-  if (rr >= p.rows) return;
-  int pn = 0, pfirst = 0, prow = 0;
-  bool pwhole = false;
-  if (p.pre_o != nullptr) {
-    const int pr = b * p.rows + rr;                        // row of the prefix's launch
-    prow = pr % p.pre_R;
-    const int u = pr / p.pre_R * p.H + h;
-    const long long f = static_cast<long long>(u) * p.pre_n;
-    pfirst = static_cast<int>(f / p.pre_per);
-    pn = static_cast<int>((f + p.pre_n - 1) / p.pre_per) - pfirst + 1;
-    pwhole = pn == 1;
-    if (pwhole) pfirst = 2 * p.pre_ctas + u;
-  }
-  const int total = n + pn;
-  auto place = [&](int i, const float*& o, const float4*& ml) {
-    if (i < n) {
-      const int slot = own >= 0 ? own : (i == 0 ? 2 * first + 1 : 2 * (first + i));
-      const int64_t at = static_cast<int64_t>(slot) * p.R + blockIdx.y;
-      o = p.part_o + at * kHeadDim;
-      ml = p.part_ml + at;
-    } else {
-      const int j = i - n;
-      const int slot = pwhole ? pfirst : (j == 0 ? 2 * pfirst + 1 : 2 * (pfirst + j));
-      const int64_t at = static_cast<int64_t>(slot) * p.pre_R + prow;
-      o = p.pre_o + at * kHeadDim;
-      ml = p.pre_ml + at;
+  const int row0 = blockIdx.y * kMergeWarps;
+  const int rows = min(kMergeWarps, min(p.R, p.rows - rt * p.R) - row0);
+  for (int i = 0; i < rows; ++i) {
+    const int row = row0 + i, rr = rt * p.R + row;
+    int pn = 0, pslot = 0, prow = 0;
+    if (p.pre_o != nullptr) {
+      const int pr = b * p.rows + rr;                        // row of the prefix's launch
+      prow = pr % p.pre_R;
+      const int u = pr / p.pre_R * p.H + h;
+      const long long f = static_cast<long long>(u) * p.pre_n;
+      pslot = static_cast<int>(f / p.pre_per);
+      pn = static_cast<int>((f + p.pre_n - 1) / p.pre_per) - pslot + 1;
+      pslot = pn == 1 ? 2 * p.pre_ctas + u : 2 * pslot;
     }
-  };
-  float m = kLowest, M = kLowest;
-  for (int i = threadIdx.x; i < total; i += kMergeWarps * 32) {
-    const float* o;
-    const float4* ml;
-    place(i, o, ml);
-    const float4 v = *ml;
-    m = fmaxf(m, v.x);
-    M = fmaxf(M, v.z);
-  }
+    const int total = n + pn;
+    const bool few = total <= kFewParts;
+    if (few && warp != i) continue;                          // warp-uniform; no barrier on this path
+    auto place = [&](int k, const float*& o, const float4*& ml) {
+      if (k < n) {
+        const int slot = own >= 0 ? own : (k == 0 ? 2 * first + 1 : 2 * (first + k));
+        const int64_t at = static_cast<int64_t>(slot) * p.slot_rows + row;
+        o = p.part_o + at * kHeadDim;
+        ml = p.part_ml + at;
+      } else {
+        const int j = k - n;
+        const int slot = pn == 1 ? pslot : (j == 0 ? pslot + 1 : pslot + 2 * j);
+        const int64_t at = static_cast<int64_t>(slot) * p.pre_slot_rows + prow;
+        o = p.pre_o + at * kHeadDim;
+        ml = p.pre_ml + at;
+      }
+    };
+    float m = kLowest, M = kLowest, L = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (few) {
+      float4 mine = make_float4(kLowest, 0.0f, kLowest, 0.0f);
+      const float* o;
+      const float4* ml;
+      if (lane < total) {
+        place(lane, o, ml);
+        mine = *ml;
+      }
+      m = mine.x;
+      M = mine.z;
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-    M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d));
-  }
-  if (lane == 0) {
-    s_red[warp][0] = m;
-    s_red[warp][1] = M;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < kMergeWarps; ++k) {
-    m = fmaxf(m, s_red[k][0]);
-    M = fmaxf(M, s_red[k][1]);
-  }
-  float L = 0.0f;
-  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int d = 16; d > 0; d >>= 1) {
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+        M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d));
+      }
+      const float lw = mine.y * ex2_approx(mine.x - m), w = ex2_approx(mine.z - M);
 #pragma unroll 4
-  for (int i = warp; i < total; i += kMergeWarps) {
-    const float* o;
-    const float4* ml;
-    place(i, o, ml);
-    const float4 v = *ml;
-    const float4 y = reinterpret_cast<const float4*>(o)[lane];
-    L += v.y * ex2_approx(v.x - m);
-    const float w = ex2_approx(v.z - M);
-    acc.x += y.x * w;
-    acc.y += y.y * w;
-    acc.z += y.z * w;
-    acc.w += y.w * w;
-  }
-  s_o[warp][lane] = acc;
-  if (lane == 0) s_sum[warp] = L;
-  __syncthreads();
-  if (warp != 0) return;
-  L = s_sum[0];
-  acc = s_o[0][lane];
+      for (int k = 0; k < total; ++k) {
+        place(k, o, ml);
+        const float4 y = reinterpret_cast<const float4*>(o)[lane];
+        const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
+        L += __shfl_sync(0xFFFFFFFFu, lw, k);
+        acc.x += y.x * wk;
+        acc.y += y.y * wk;
+        acc.z += y.z * wk;
+        acc.w += y.w * wk;
+      }
+    } else {
+      for (int k = threadIdx.x; k < total; k += kMergeWarps * 32) {
+        const float* o;
+        const float4* ml;
+        place(k, o, ml);
+        const float4 v = *ml;
+        m = fmaxf(m, v.x);
+        M = fmaxf(M, v.z);
+      }
 #pragma unroll
-  for (int k = 1; k < kMergeWarps; ++k) {
-    const float4 y = s_o[k][lane];
-    L += s_sum[k];
-    acc.x += y.x;
-    acc.y += y.y;
-    acc.z += y.z;
-    acc.w += y.w;
+      for (int d = 16; d > 0; d >>= 1) {
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+        M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d));
+      }
+      if (lane == 0) {
+        s_red[warp][0] = m;
+        s_red[warp][1] = M;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kMergeWarps; ++k) {
+        m = fmaxf(m, s_red[k][0]);
+        M = fmaxf(M, s_red[k][1]);
+      }
+#pragma unroll 4
+      for (int k = warp; k < total; k += kMergeWarps) {
+        const float* o;
+        const float4* ml;
+        place(k, o, ml);
+        const float4 v = *ml;
+        const float4 y = reinterpret_cast<const float4*>(o)[lane];
+        L += v.y * ex2_approx(v.x - m);
+        const float w = ex2_approx(v.z - M);
+        acc.x += y.x * w;
+        acc.y += y.y * w;
+        acc.z += y.z * w;
+        acc.w += y.w * w;
+      }
+      s_o[warp][lane] = acc;
+      if (lane == 0) s_sum[warp] = L;
+      __syncthreads();
+      L = s_sum[0];
+      acc = s_o[0][lane];
+#pragma unroll
+      for (int k = 1; k < kMergeWarps; ++k) {
+        const float4 y = s_o[k][lane];
+        L += s_sum[k];
+        acc.x += y.x;
+        acc.y += y.y;
+        acc.z += y.z;
+        acc.w += y.w;
+      }
+      __syncthreads();                                       // before the next row's parts are written
+      if (warp != 0) continue;
+    }
+    const int t = rr / p.G, hq = h * p.G + rr % p.G;
+    const float half = scale2(M - m);
+    const float inv = L == 0.0f ? 0.0f : half / L;
+    uint2 w;
+    w.x = pack_bf16(acc.x * half * inv, acc.y * half * inv);
+    w.y = pack_bf16(acc.z * half * inv, acc.w * half * inv);
+    *reinterpret_cast<uint2*>(p.out + ((static_cast<int64_t>(b) * p.Sq + t) * p.Hq + hq) * kHeadDim + lane * 4) = w;
+    if (p.lse != nullptr && lane == 0)
+      p.lse[(static_cast<int64_t>(b) * p.Hq + hq) * p.Sq + t] = L == 0.0f ? -INFINITY : (m + log2f(L)) * kLn2;
   }
-  const int t = rr / p.G, hq = h * p.G + rr % p.G;
-  const float half = scale2(M - m);
-  const float inv = L == 0.0f ? 0.0f : half / L;
-  uint2 w;
-  w.x = pack_bf16(acc.x * half * inv, acc.y * half * inv);
-  w.y = pack_bf16(acc.z * half * inv, acc.w * half * inv);
-  *reinterpret_cast<uint2*>(p.out + ((static_cast<int64_t>(b) * p.Sq + t) * p.Hq + hq) * kHeadDim + lane * 4) = w;
-  if (p.lse != nullptr && lane == 0)
-    p.lse[(static_cast<int64_t>(b) * p.Hq + hq) * p.Sq + t] = L == 0.0f ? -INFINITY : (m + log2f(L)) * kLn2;
 }
 
 // ------------------------------------------------------------------- host --
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-// 8 or 16 query rows a tile where they are all, else 32: the keys are converted
-// once for all rows of a tile.
-int rows_per_tile(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+// 8, 16 or 32 query rows a tile where they are all, else the wide kernel's 256:
+// the keys are read and converted once for all rows of a tile.
+int rows_per_tile(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : kWideRows; }
+int max_ctas(int R) { return kSms * (R == kWideRows ? 1 : ctas_per_sm(R / 8)); }
+int keys_per_tile(int R) { return R == kWideRows ? kWideTok : kTok; }
 
 // One launch's part of the workspace.
 struct Layout {
-  int rows, R, row_tiles, units, slots;
+  int rows, R, slot_rows, row_tiles, units, slots;
   size_t o, ml, desc, info, end;
 };
 
@@ -802,10 +681,11 @@ Layout layout(int rows, int B, int H, bool keep, size_t at) {
   w.R = rows_per_tile(rows);
   w.row_tiles = (rows + w.R - 1) / w.R;
   w.units = B * w.row_tiles * H;
-  w.slots = 2 * kMaxCtas + (keep ? w.units : 0);
+  w.slot_rows = std::min(w.R, rows);
+  w.slots = 2 * max_ctas(w.R) + (keep ? w.units : 0);
   w.o = at;
-  w.ml = w.o + align256(static_cast<size_t>(w.slots) * w.R * kHeadDim * sizeof(float));
-  w.desc = w.ml + align256(static_cast<size_t>(w.slots) * w.R * sizeof(float4));
+  w.ml = w.o + align256(static_cast<size_t>(w.slots) * w.slot_rows * kHeadDim * sizeof(float));
+  w.desc = w.ml + align256(static_cast<size_t>(w.slots) * w.slot_rows * sizeof(float4));
   w.info = w.desc + align256(kMaxCtas * sizeof(int4));
   w.end = w.info + (keep ? align256(static_cast<size_t>(w.units) * sizeof(int2)) : 0);
   return w;
@@ -817,6 +697,7 @@ T* at(void* base, size_t off) {
 }
 
 cudaError_t launch_part(const Params& p, int R, bool prefix, unsigned ctas, cudaStream_t stream) {
+  if (R == kWideRows) return launch_wide(p, prefix, ctas, stream);
   const uint32_t smem = smem_of(R / 8);
   auto go = [&](auto kernel) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -840,7 +721,7 @@ cudaError_t launch_part(const Params& p, int R, bool prefix, unsigned ctas, cuda
 }
 
 unsigned ctas_for(long long tiles, int R) {
-  return static_cast<unsigned>(std::min<long long>(kSms * ctas_per_sm(R / 8), std::max(1ll, tiles)));
+  return static_cast<unsigned>(std::min<long long>(max_ctas(R), std::max(1ll, tiles)));
 }
 
 }  // namespace
@@ -879,6 +760,7 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream) 
     p.row_tiles = w.row_tiles;
     p.c_scale = a.softmax_scale * kLog2e;
     p.keep = both;
+    p.slot_rows = w.slot_rows;
     p.part_o = at<float>(a.workspace, w.o);
     p.part_ml = at<float4>(a.workspace, w.ml);
     p.desc = at<int4>(a.workspace, w.desc);
@@ -887,7 +769,7 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream) 
     p.err = a.err;
     p.room = static_cast<int>(std::min<int64_t>(kMaxCacheLen, static_cast<int64_t>(a.table.width) << a.cache.page_shift));
     // The lengths are on the device: as many CTAs as the table has room for.
-    const unsigned ctas = ctas_for(std::min<long long>(kMaxCtas, (static_cast<long long>(p.room) + kTok - 1) / kTok) * w.units, w.R);
+    const unsigned ctas = ctas_for(std::min<long long>(kMaxCtas, (static_cast<long long>(p.room) + keys_per_tile(w.R) - 1) / keys_per_tile(w.R)) * w.units, w.R);
     cudaError_t e = launch_part(p, w.R, false, ctas, stream);
     if (e != cudaSuccess) return e;
 
@@ -898,6 +780,7 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream) 
     mp.info = p.info;
     mp.ctas = ctas;
     mp.R = w.R;
+    mp.slot_rows = w.slot_rows;
     mp.rows = w.rows;
     mp.row_tiles = w.row_tiles;
     mp.H = H;
@@ -913,11 +796,12 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream) 
       p.table.stride = 0;
       p.rows = u.rows;
       p.row_tiles = u.row_tiles;
+      p.slot_rows = u.slot_rows;
       p.part_o = at<float>(a.workspace, u.o);
       p.part_ml = at<float4>(a.workspace, u.ml);
       p.desc = at<int4>(a.workspace, u.desc);
       p.info = at<int2>(a.workspace, u.info);
-      const int n = (a.prefix_len + kTok - 1) / kTok;
+      const int n = (a.prefix_len + keys_per_tile(u.R) - 1) / keys_per_tile(u.R);
       const long long tiles = static_cast<long long>(n) * u.units;
       const unsigned pc = ctas_for(tiles, u.R);
       e = launch_part(p, u.R, true, pc, stream);
@@ -925,12 +809,13 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream) 
       mp.pre_o = p.part_o;
       mp.pre_ml = p.part_ml;
       mp.pre_R = u.R;
+      mp.pre_slot_rows = u.slot_rows;
       mp.pre_n = n;
       mp.pre_per = (tiles + pc - 1) / pc;
       mp.pre_ctas = pc;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(both ? w.units : ctas, std::min(w.R, w.rows));
+    cfg.gridDim = dim3(both ? w.units : ctas, (std::min(w.R, w.rows) + kMergeWarps - 1) / kMergeWarps);
     cfg.blockDim = dim3(kMergeWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

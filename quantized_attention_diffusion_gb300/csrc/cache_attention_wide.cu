@@ -1,0 +1,609 @@
+// cache_attention_wide.cu -- the attention over the KV cache for many query
+// rows to a key/value head (a shared prefix, a chunk of new tokens), on the
+// tcgen05 tensor cores (sm_103a).
+//
+// The formulas are cache_attention.cu's with one change: the weights enter the
+// second product as bf16(2^(x_j - m) sv_j) with V's codes in bf16 (both exact
+// in range, a weight rounded by 2^-9 at the most), so that one exponential
+// serves the sum and the product, M = m.
+//
+// A CTA owns 256 query rows of one unit and walks its key tiles of 128.  Its two
+// halves are two row tiles of 128, or, where a unit has at most 128 rows, the even
+// and the odd key tiles of the same rows, joined at the end: either way one half's
+// softmax runs while the tensor cores work for the other.
+//
+//   warps 0-3    read K's codes from global memory, convert them to fp16 (exact)
+//                and store them swizzled, two stages; keys behind the last are
+//                stored as zeros
+//   warps 4-7    the same for V's codes, to bf16 (exact)
+//   warps 8-11   softmax of half 0, one thread a row
+//   warps 12-15  the same for half 1
+//   warp 16      one thread issues S_t = Q_t K^T and O_t += P_t V; warps 17-19
+//                only give registers to the softmax
+//
+// TMEM (512 columns): S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512).  P_t
+// (bf16, two to a column) takes the first 64 columns of S_t, each 32 scores'
+// weights over columns that have been read before, and is the product's A
+// operand from there; V is its B operand with the keys as the outer index, as
+// the cache has it.
+//
+// A row's reference m moves where a weight would pass 2^8: then the thread
+// scales the row's sum, its accumulator and the weights of this tile that it
+// has stored already.
+#include <cuda_bf16.h>
+
+#include "cache_attention.cuh"
+
+namespace sage::cache {
+
+namespace {
+
+constexpr int kThreads = 20 * 32;
+// Registers of the five warpgroups: a launch of 640 threads has 96 each, and the
+// softmax needs 120.
+constexpr int kRegsConvert = 72, kRegsSoftmax = 120, kRegsIssue = 96;
+static_assert(2 * kRegsConvert + 2 * kRegsSoftmax + kRegsIssue <= 5 * 96, "more registers than the launch has");
+constexpr uint32_t kHalf = 128 * 128;                   // 128 rows of 64 16-bit values
+constexpr uint32_t kTileBytes = 2 * kHalf;
+constexpr uint32_t kSmemQ = 0;                          // two row tiles
+constexpr uint32_t kSmemK = 2 * kTileBytes;             // two stages
+constexpr uint32_t kSmemV = 4 * kTileBytes;             // two stages
+constexpr uint32_t kSmemBytes = 6 * kTileBytes + 1024;  // and room to align to 1024
+constexpr int kScaleSlots = 4;                          // of ks and vs: up to three tiles ahead of the softmax
+constexpr float kFar = 8.0f;                            // log2 of the largest weight
+
+__host__ __device__ constexpr uint32_t col_s(int t) { return 128u * t; }
+__host__ __device__ constexpr uint32_t col_o(int t) { return 256u + 128u * t; }
+
+struct Barriers {
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], scales[kScaleSlots];
+  uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], half_full, half_read, drain;
+};
+
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// 16 bytes at chunk c (0..15) of row r of a tile: two halves of 64 values, rows of
+// 128 bytes, 128-byte swizzle.
+__device__ __forceinline__ uint32_t tile_offset(int r, int c) {
+  return (c >> 3) * kHalf + (r >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+// Four E4M3 codes -> two pairs of bf16.  A byte s eeee mmm, its sign spread over
+// the half word above it, shifted by four and masked, is the bf16 of exponent
+// field eeee and mantissa mmm0000; times 2^120 that is the code's value,
+// subnormals included.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void v_codes_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  constexpr uint32_t kTwo120 = 0x7B807B80u;
+  asm("prmt.b32 %0, %1, %1, 0x9180;" : "=r"(lo) : "r"(w));   // selector bit 3: the byte's sign, eight times
+  asm("prmt.b32 %0, %1, %1, 0xB3A2;" : "=r"(hi) : "r"(w));
+  lo = mul_bf16x2((lo << 4) & 0x87F087F0u, kTwo120);
+  hi = mul_bf16x2((hi << 4) & 0x87F087F0u, kTwo120);
+}
+
+__device__ __forceinline__ float2 unpack_bf16(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// The rare move of a row's reference: alpha = 2^(old - new) of this thread's row
+// times the accumulator (if it holds anything yet) and the weights of the tile's
+// first `chunks` chunks.  All lanes of a warp together.
+__device__ __forceinline__ void rescale(uint32_t tO, uint32_t tP, int chunks, bool has_o, float alpha) {
+  if (has_o) {
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+      uint32_t o[32];
+      tmem_ld32(tO + 32 * k, o);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+      tmem_st32(tO + 32 * k, o);
+    }
+  }
+  tmem_st_wait();
+#pragma unroll 1
+  for (int k = 0; k < chunks; ++k) {
+    uint32_t w[16];
+    tmem_ld16(tP + 16 * k, w);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float2 x = unpack_bf16(w[i]);
+      w[i] = pack_bf16(x.x * alpha, x.y * alpha);
+    }
+    tmem_st16(tP + 16 * k, w);
+  }
+  tmem_st_wait();
+}
+
+// One row's 128 scores of a tile (TMEM columns tS ..) to weights over them, 32 at a
+// time.  kx, vx: the keys' scales (K's times softmax_scale * log2 e); rk: the row's
+// factor; key0: the tile's first key, of which the row sees those below lim
+// (kCut: not all).  before(): waits for the accumulator's last product.
+template <bool kCut, typename Before>
+__device__ __forceinline__ bool softmax_tile(uint32_t tS, uint32_t tO, const float* kx, const float* vx, float rk, int key0,
+                                             int lim, bool has_o, float& m, float2& l, Before before) {
+  bool ok = true;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t a[32];
+    tmem_ld32(tS + 32 * c, a);
+    tmem_ld_wait();
+    float2 y[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 s4 = reinterpret_cast<const float4*>(kx)[c * 8 + i];
+      y[2 * i] = fmul2v(make_float2(__uint_as_float(a[4 * i]), __uint_as_float(a[4 * i + 1])), make_float2(s4.x, s4.y));
+      y[2 * i + 1] = fmul2v(make_float2(__uint_as_float(a[4 * i + 2]), __uint_as_float(a[4 * i + 3])), make_float2(s4.z, s4.w));
+    }
+    const int left = lim - key0 - 32 * c;                // keys of these that the row sees
+    if constexpr (kCut) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (2 * i >= left) y[i].x = -INFINITY;
+        if (2 * i + 1 >= left) y[i].y = -INFINITY;
+      }
+    }
+    float mx = fmaxf(y[0].x, y[0].y), mx2 = fmaxf(y[1].x, y[1].y);
+#pragma unroll
+    for (int i = 2; i < 16; i += 2) {
+      mx = fmax3(mx, y[i].x, y[i].y);
+      mx2 = fmax3(mx2, y[i + 1].x, y[i + 1].y);
+    }
+    mx = fmaxf(mx, mx2) * rk;
+    if (__any_sync(0xFFFFFFFFu, mx > m + kFar)) {
+      const float to = fmaxf(m, mx), alpha = ex2_approx(m - to);
+      l.x *= alpha;
+      l.y *= alpha;
+      m = to;
+      if (has_o) ok = ok && before();
+      if (ok) rescale(tO, tS, c, has_o, alpha);
+    }
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 s4 = reinterpret_cast<const float4*>(vx)[c * 8 + i];
+      const float2 x0 = ffma2_bc(y[2 * i].x, y[2 * i].y, rk, -m), x1 = ffma2_bc(y[2 * i + 1].x, y[2 * i + 1].y, rk, -m);
+      const float2 p0 = make_float2(ex2_approx(x0.x), ex2_approx(x0.y));
+      const float2 p1 = make_float2(ex2_approx(x1.x), ex2_approx(x1.y));
+      l = fadd2v(l, p0);
+      l = fadd2v(l, p1);
+      float2 w0 = fmul2v(p0, make_float2(s4.x, s4.y)), w1 = fmul2v(p1, make_float2(s4.z, s4.w));
+      if constexpr (kCut) {                              // a scale that is not finite stays behind the limit
+        if (4 * i >= left) w0.x = 0.0f;
+        if (4 * i + 1 >= left) w0.y = 0.0f;
+        if (4 * i + 2 >= left) w1.x = 0.0f;
+        if (4 * i + 3 >= left) w1.y = 0.0f;
+      }
+      w[2 * i] = pack_bf16(w0.x, w0.y);
+      w[2 * i + 1] = pack_bf16(w1.x, w1.y);
+    }
+    tmem_st16(tS + 16 * c, w);
+  }
+  return ok;
+}
+
+template <bool kPrefix>
+__global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __grid_constant__ Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  __shared__ Barriers bars;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ int s_len[kMaxBatch];
+  __shared__ long long s_off[kPrefix ? 2 : kMaxBatch + 1];
+  __shared__ __align__(16) float s_ks[kScaleSlots][kWideTok], s_vs[kScaleSlots][kWideTok];
+  __shared__ float2 s_half[128];                          // m and L of half 1's rows
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_v = &abort_flag;
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  const Walk<kWideRows, kWideTok, kPrefix> walk{p, s_len, s_off};
+  walk.load_lengths(s_len);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars.k_full[s], 128);
+      mbar_init(&bars.k_empty[s], 1);
+      mbar_init(&bars.v_full[s], 128);
+      mbar_init(&bars.v_empty[s], 1);
+      mbar_init(&bars.q_full[s], 128);
+      mbar_init(&bars.s_full[s], 1);
+      mbar_init(&bars.p_full[s], 128);
+      mbar_init(&bars.pv_done[s], 1);
+    }
+    for (int s = 0; s < kScaleSlots; ++s) mbar_init(&bars.scales[s], 256);
+    mbar_init(&bars.half_full, 128);
+    mbar_init(&bars.half_read, 128);
+    mbar_init(&bars.drain, 1);
+    abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 16) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  if (warp == 0) walk.sum_tiles(s_off, lane);
+  __syncthreads();
+
+  const long long total = s_off[walk.seqs()] * p.cache.H;
+  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long f0 = blockIdx.x * per, f1 = min(total, f0 + per);
+  if (!p.keep && threadIdx.x == 0) p.desc[blockIdx.x].w = 0;
+  if (f0 < f1) {
+    Place x = walk.locate(f0);
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_inline(bar, parity & 1u, abort_v, p.err, p.timeout_ns); };
+
+    if (warp < 8) {
+      fewer_registers<kRegsConvert>();
+      // ----------------------------------------------------------- convert --
+      // Step i of a tile takes its keys 16 i .. 16 i + 15, which lie in one page.
+      // Lane bits: 0-1 and 3 the 16 codes of a row, 2 and 4 the row of four: the
+      // eight lanes of a 16-byte store fall into distinct banks.  A tile's codes
+      // are loaded while the one before is converted, its pages one tile earlier.
+      const bool is_v = warp >= 4;
+      const int tid = threadIdx.x & 127;
+      const int sub = 4 * (warp & 3) + ((lane >> 2) & 1) + 2 * (lane >> 4);   // key of a step
+      const int q16 = (lane & 3) + ((lane >> 3) & 1) * 4;                     // 16 codes of a key
+      const int ps = p.cache.page_shift;
+      const uint8_t* codes = (is_v ? p.cache.v_codes : p.cache.k_codes) + q16 * 16;
+      const float* scales = is_v ? p.cache.v_scale : p.cache.k_scale;
+      uint8_t* dst = smem + (is_v ? kSmemV : kSmemK) + tile_offset(sub, 2 * q16);
+      const uint32_t odd = tile_offset(sub, 2 * q16 + 1) - tile_offset(sub, 2 * q16);   // 16 or -16: wraps
+      uint64_t* full = is_v ? bars.v_full : bars.k_full;
+      uint64_t* empty = is_v ? bars.v_empty : bars.k_empty;
+      bool bad = false;
+      // The tile whose codes are loaded next: its keys' page (lane i: of step i), head and bounds.
+      int page = -1, head = 0, t0 = 0, hi = 0;
+      long long g = f0;                  // tiles whose pages have been asked for
+      auto ask = [&]() {
+        page = -1;
+        if (g >= f1) return;
+        head = x.h;
+        t0 = x.tile * kWideTok;
+        hi = walk.keys(x.b, x.rt);
+        const int key = t0 + 16 * lane;
+        if (lane < 8 && key < hi) {
+          page = __ldg(p.table.pages + (kPrefix ? 0 : x.b * p.table.stride) + (key >> ps));
+          if (page < 0 || page >= p.cache.num_pages) {
+            bad = true;
+            page = -1;
+          }
+        }
+        ++g;
+        if (x.tile + 1 < x.n)
+          ++x.tile;
+        else
+          walk.next(x);
+      };
+      uint4 w[8];
+      float scale = 0.0f;
+      auto load = [&]() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int pg = __shfl_sync(0xFFFFFFFFu, page, i), t = t0 + 16 * i;
+          const int row = ((pg * p.cache.H + head) << ps) + (t & ((1 << ps) - 1)) + sub;
+          w[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (pg >= 0 && t + sub < hi) w[i] = __ldg(reinterpret_cast<const uint4*>(codes + static_cast<int64_t>(row) * kHeadDim));
+        }
+        const int pg = __shfl_sync(0xFFFFFFFFu, page, tid >> 4), t = t0 + tid;
+        scale = 0.0f;
+        if (pg >= 0 && t < hi) scale = __ldg(scales + (((pg * p.cache.H + head) << ps) + (t & ((1 << ps) - 1))));
+      };
+      ask();
+      load();
+      ask();
+      int it = 0;
+      for (long long f = f0; f < f1; ++f, ++it) {
+        const int s = it & 1, round = it >> 1;
+        // V's scales may be written before its stage is free: the tile that last
+        // used the slot has been multiplied.
+        if (is_v) {
+          s_vs[it % kScaleSlots][tid] = scale;
+          mbar_arrive(&bars.scales[it % kScaleSlots]);
+        }
+        if (round > 0 && !__all_sync(0xFFFFFFFFu, wait(&empty[s], round - 1))) break;
+        uint8_t* to = dst + s * kTileBytes;
+        if (is_v) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t o[8];
+            v_codes_bf16(w[i].x, o[0], o[1]);
+            v_codes_bf16(w[i].y, o[2], o[3]);
+            v_codes_bf16(w[i].z, o[4], o[5]);
+            v_codes_bf16(w[i].w, o[6], o[7]);
+            *reinterpret_cast<uint4*>(to + i * 2048) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(to + i * 2048 + static_cast<int>(odd)) = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+        } else {
+          s_ks[it % kScaleSlots][tid] = scale * p.c_scale;
+          mbar_arrive(&bars.scales[it % kScaleSlots]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t o[8];
+            k_codes_f16(w[i].x, o[0], o[1]);
+            k_codes_f16(w[i].y, o[2], o[3]);
+            k_codes_f16(w[i].z, o[4], o[5]);
+            k_codes_f16(w[i].w, o[6], o[7]);
+            *reinterpret_cast<uint4*>(to + i * 2048) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(to + i * 2048 + static_cast<int>(odd)) = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        mbar_arrive(&full[s]);
+        load();
+        ask();
+      }
+      if (bad) atomicExch(p.err, SAGE_DEVERR_BAD_PAGE);
+    } else if (warp < 16) {
+      more_registers<kRegsSoftmax>();
+      // ------------------------------------------------- softmax, epilogue --
+      const int t = (warp - 8) >> 2;                       // half
+      const int quarter = warp & 3;                        // TMEM lanes of this warp
+      const int trow = quarter * 32 + lane;
+      const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+      const uint32_t tS = tmem + lanes + col_s(t), tO = tmem + lanes + col_o(t);
+      float* exchange = reinterpret_cast<float*>(smem + kSmemQ + kTileBytes) + trow;   // [channel][row], 64 channels
+      int it = 0;                                          // key tiles of this CTA
+      uint32_t done = 0, joined = 0;                       // tiles and exchanges of this half
+      bool ok = true;
+      for (long long f = f0; f < f1 && ok;) {
+        const int hi = walk.keys(x.b, x.rt);
+        const int last = static_cast<int>(min(static_cast<long long>(x.n), x.tile + (f1 - f)));
+        const int n = last - x.tile;
+        const int rows = min(kWideRows, p.rows - x.rt * kWideRows);
+        const bool whole = x.tile == 0 && last == x.n, by_rows = rows > 128;
+        if (by_rows || t < n) {
+          const int r = (by_rows ? t * 128 : 0) + trow, rr = x.rt * kWideRows + r;
+          const bool valid = r < rows;
+          const int lim = valid ? min(hi, walk.limit(x.b, rr)) : hi;
+          const int lo = __reduce_min_sync(0xFFFFFFFFu, lim);
+          // This thread's query row: fp16 times a power of two.
+          uint32_t top = 0u;
+          const uint16_t* src = walk.query(x, valid ? rr : x.rt * kWideRows);
+#pragma unroll 4
+          for (int i = 0; i < 16; ++i) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(src) + i);
+            const uint32_t a = max((w.x & 0x7FFFu), (w.x >> 16) & 0x7FFFu), b = max((w.y & 0x7FFFu), (w.y >> 16) & 0x7FFFu);
+            const uint32_t d = max((w.z & 0x7FFFu), (w.z >> 16) & 0x7FFFu), e = max((w.w & 0x7FFFu), (w.w >> 16) & 0x7FFFu);
+            top = max(top, max(max(a, b), max(d, e)));
+          }
+          const uint32_t ex = row_exponent(top);
+          const float rk = __uint_as_float((254u - ex) << 23);
+          if (by_rows || t == 0) {
+            const float up = valid ? __uint_as_float(ex << 23) : 0.0f;
+            uint8_t* sQ = smem + kSmemQ + t * kTileBytes;
+#pragma unroll 4
+            for (int i = 0; i < 16; ++i) {
+              const uint4 w = __ldg(reinterpret_cast<const uint4*>(src) + i);
+              const float2 a = unpack_bf16(w.x), b = unpack_bf16(w.y), d = unpack_bf16(w.z), e = unpack_bf16(w.w);
+              *reinterpret_cast<uint4*>(sQ + tile_offset(trow, i)) =
+                  make_uint4(pack_f16(a.x * up, a.y * up), pack_f16(b.x * up, b.y * up), pack_f16(d.x * up, d.y * up),
+                             pack_f16(e.x * up, e.y * up));
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            mbar_arrive(&bars.q_full[t]);
+          }
+
+          float m = kLowest;
+          float2 l = make_float2(0.0f, 0.0f);
+          bool has_o = false;
+          auto before = [&]() {                            // the product of this half's last tile has ended
+            const bool r2 = __all_sync(0xFFFFFFFFu, wait(&bars.pv_done[t], done - 1));
+            tc_fence_after();
+            return r2;
+          };
+          for (int j = by_rows ? 0 : t; j < n; j += by_rows ? 1 : 2) {
+            const int slot = (it + j) % kScaleSlots;
+            ok = wait(&bars.scales[slot], (it + j) / kScaleSlots) && wait(&bars.s_full[t], done);
+            if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+            tc_fence_after();
+            const int key0 = (x.tile + j) * kWideTok;
+            if (key0 + kWideTok > lo)                      // warp-uniform
+              ok = softmax_tile<true>(tS, tO, s_ks[slot], s_vs[slot], rk, key0, lim, has_o, m, l, before);
+            else
+              ok = softmax_tile<false>(tS, tO, s_ks[slot], s_vs[slot], rk, key0, lim, has_o, m, l, before);
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&bars.p_full[t]);
+            ++done;
+            has_o = true;
+          }
+          ok = ok && before();
+          if (!ok) break;
+          float L = l.x + l.y;
+          const bool join = !by_rows && n > 1;
+          if (join && t == 1) {
+            // Half 1 hands over its rows' m, L and sums, 64 channels at a time.
+            s_half[trow] = make_float2(m, L);
+            for (int k = 0; k < 2 && ok; ++k) {
+#pragma unroll 1
+              for (int c = 0; c < 2; ++c) {
+                uint32_t o[32];
+                tmem_ld32(tO + 64 * k + 32 * c, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) exchange[(32 * c + i) * 128] = __uint_as_float(o[i]);
+              }
+              mbar_arrive(&bars.half_full);
+              ok = __all_sync(0xFFFFFFFFu, wait(&bars.half_read, joined++));
+            }
+          } else {
+            float a0 = 1.0f, a1 = 0.0f;
+            const float inv_none = whole && !p.keep ? 1.0f : 0.0f;   // written out, or to the workspace
+            const int64_t at = static_cast<int64_t>(walk.slot(x, whole)) * p.slot_rows + r;
+            const int tok = rr / p.G, hq = x.h * p.G + rr % p.G;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              if (join && (c & 1) == 0) {
+                ok = __all_sync(0xFFFFFFFFu, wait(&bars.half_full, joined));
+                if (!ok) break;
+                if (c == 0) {
+                  const float2 other = s_half[trow];
+                  const float to = fmaxf(m, other.x);
+                  a0 = ex2_approx(m - to);
+                  a1 = ex2_approx(other.x - to);
+                  m = to;
+                  L = L * a0 + other.y * a1;
+                }
+              }
+              const float inv = inv_none != 0.0f ? (L == 0.0f ? 0.0f : 1.0f / L) : 1.0f;
+              uint32_t u[32];
+              tmem_ld32(tO + 32 * c, u);
+              tmem_ld_wait();
+              float o[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                o[i] = __uint_as_float(u[i]);
+                if (join) o[i] = o[i] * a0 + exchange[(32 * (c & 1) + i) * 128] * a1;
+              }
+              if (join && (c & 1) == 1) {
+                mbar_arrive(&bars.half_read);
+                ++joined;
+              }
+              if (valid && inv_none != 0.0f) {
+                uint4* dst = reinterpret_cast<uint4*>(
+                    p.out + ((static_cast<int64_t>(x.b) * p.Sq + tok) * p.Hq + hq) * kHeadDim + 32 * c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  dst[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                      pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+              } else if (valid) {
+                float4* dst = reinterpret_cast<float4*>(p.part_o + at * kHeadDim + 32 * c);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              }
+            }
+            if (valid && inv_none != 0.0f) {
+              if (p.lse != nullptr)
+                p.lse[(static_cast<int64_t>(x.b) * p.Hq + hq) * p.Sq + tok] = L == 0.0f ? -INFINITY : (m + log2f(L)) * kLn2;
+            } else if (valid) {
+              p.part_ml[at] = make_float4(m, L, m, 0.0f);
+            }
+          }
+          tc_fence_before();                               // O may be written again
+        }
+        if (warp == 8 && lane == 0) walk.tell(x, whole, f, per);
+        it += n;
+        f += n;
+        walk.next(x);
+      }
+    } else {
+      fewer_registers<kRegsIssue>();
+      if (warp == 16 && lane == 0) {
+      // -------------------------------------------------------------- issue --
+      constexpr uint32_t kIdescQK = make_idesc_f32acc(128, 128, 0, 0);                   // F16 x F16
+      constexpr uint32_t kIdescPV = make_idesc_f32acc(128, 128, 1, 1) | (1u << 16);      // BF16 x BF16, B's outer index summed
+      const uint32_t q_lo = sw128_desc_lo(smem_addr(smem + kSmemQ)), k_lo = sw128_desc_lo(smem_addr(smem + kSmemK));
+      // V: 64-channel halves kHalf bytes apart, groups of eight keys 1024.
+      const uint32_t v_lo = sw128_desc_lo(smem_addr(smem + kSmemV)) | ((kHalf >> 4) << 16);
+      int it = 0;
+      uint32_t pv[2] = {0u, 0u}, seg[2] = {0u, 0u};        // products P V of each half, segments of each Q tile
+      bool ok = true;
+      auto qk = [&](int t, int qt, int g) {                // S_t of key tile g, Q tile qt
+        const uint32_t a0 = q_lo + qt * (kTileBytes >> 4), b0 = k_lo + (g & 1) * (kTileBytes >> 4);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+          mma_f16_ss(tmem + col_s(t), a0 + off, b0 + off, kIdescQK, k > 0);
+        }
+        mma_commit(&bars.s_full[t]);
+      };
+      auto pv_of = [&](int t, int g, bool first) {
+        const uint32_t b0 = v_lo + (g & 1) * (kTileBytes >> 4);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_f16_ts(tmem + col_o(t), tmem + col_s(t) + 8 * k, b0 + k * (2048 >> 4), kSw128DescHi, kIdescPV, !first || k > 0);
+        mma_commit(&bars.pv_done[t]);
+        ++pv[t];
+      };
+      for (long long f = f0; f < f1 && ok;) {
+        const int last = static_cast<int>(min(static_cast<long long>(x.n), x.tile + (f1 - f)));
+        const int n = last - x.tile;
+        const bool by_rows = p.rows - x.rt * kWideRows > 128;
+        // Step i: half t = i % 2 of key tile j = i / 2, or key tile i in half i % 2.
+        // The scores of step i + 2 follow the weighted sum of step i, whose weights
+        // stand in their columns.
+        const int steps = by_rows ? 2 * n : n;
+        auto scores = [&](int i) {
+          const int t = i & 1, g = it + (by_rows ? i >> 1 : i);
+          if (!by_rows || t == 0) ok = ok && wait(&bars.k_full[g & 1], g >> 1);
+          if (i < 2 && (by_rows || t == 0)) ok = ok && wait(&bars.q_full[t], seg[t]++);
+          if (i >= 2) ok = ok && wait(&bars.pv_done[t], pv[t] - 1);
+          if (!ok) return;
+          tc_fence_after();
+          qk(t, by_rows ? t : 0, g);
+          if (!by_rows || t == 1) mma_commit(&bars.k_empty[g & 1]);
+        };
+        scores(0);
+        if (steps > 1) scores(1);
+        for (int i = 0; i < steps && ok; ++i) {
+          const int t = i & 1, g = it + (by_rows ? i >> 1 : i);
+          if (!by_rows || t == 0) ok = ok && wait(&bars.v_full[g & 1], g >> 1);
+          ok = ok && wait(&bars.p_full[t], pv[t]);
+          if (!ok) break;
+          tc_fence_after();
+          pv_of(t, g, i < 2);
+          if (!by_rows || t == 1) mma_commit(&bars.v_empty[g & 1]);
+          if (i + 2 < steps) scores(i + 2);
+        }
+        it += n;
+        f += n;
+        walk.next(x);
+      }
+      // Every product has to end before TMEM can be released.
+      mma_commit(&bars.drain);
+      int local_abort = 0;
+      (void)mbar_wait_inline(&bars.drain, 0, &local_abort, p.err, p.timeout_ns);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 16) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  // The merge kernel waits for this grid alone: this grid has to end after the
+  // one before it, beside which it may have run.
+  if constexpr (kPrefix) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+}  // namespace
+
+cudaError_t launch_wide(const Params& p, bool prefix, unsigned ctas, cudaStream_t stream) {
+  auto go = [&](auto kernel) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = stream;
+    // The prefix's launch follows the sequences' and needs nothing of it.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = prefix ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+  };
+  return prefix ? go(cache_attn_wide_kernel<true>) : go(cache_attn_wide_kernel<false>);
+}
+
+}  // namespace sage::cache

@@ -332,6 +332,8 @@ sage_status check_cache(const sage_kv_cache* c, int D, const int32_t* table, int
     return fail(SAGE_ERR_INVALID_ARG, "a cache's num_pages and H must be >= 1 (got %d, %d)", c->num_pages, c->H);
   if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
     return fail(SAGE_ERR_UNSUPPORTED, "page_size %d is not supported: 16, 32, 64, 128 or 256", c->page_size);
+  if (static_cast<int64_t>(c->num_pages) * c->H > INT_MAX / c->page_size)
+    return fail(SAGE_ERR_INVALID_ARG, "num_pages * H * page_size exceeds 2^31-1");
   sage_status s = check_ptrs({{c->k_codes, "k_codes"}, {c->k_scale, "k_scale"}, {c->v_codes, "v_codes"},
                               {c->v_scale, "v_scale"}});
   if (s != SAGE_OK) return s;

@@ -47,7 +47,7 @@ BAD_CACHES = [
     (dict(kc=0), INVALID, b"k_codes"), (dict(vs=0), INVALID, b"v_scale"), (dict(vc=FAKE + 8), MISALIGNED, b"v_codes"),
     (dict(ks=FAKE + 4), MISALIGNED, b"k_scale"), (dict(pages=0), INVALID, b"num_pages"), (dict(H=0), INVALID, b"H"),
     (dict(page=8), UNSUPPORTED, b"page_size"), (dict(page=48), UNSUPPORTED, b"page_size"),
-    (dict(page=512), UNSUPPORTED, b"page_size"), (dict(page=-16), UNSUPPORTED, b"page_size"),
+    (dict(pages=1 << 26), INVALID, b"2^31-1"), (dict(page=512), UNSUPPORTED, b"page_size"), (dict(page=-16), UNSUPPORTED, b"page_size"),
 ]
 
 
