@@ -498,19 +498,17 @@ struct MergeParams {
   uint16_t* out;
   float* lse;
   int Sq, G, Hq;
+  int split;                 // warps of a row: a power of two
 };
 
 constexpr int kMergeWarps = 8;
-constexpr int kFewParts = 32;   // parts of a row that one warp joins: one lane each
 
-// Eight rows of a unit a CTA.  Where a row has up to 32 parts a warp takes a row:
-// each lane one part's m, L and M, then the parts' sums in order.  Rows of more
-// parts (few rows over many keys) take the CTA one after another, each warp every
-// eighth part, and the warps' sums are added in order.
+// A CTA takes kMergeWarps / p.split rows of a unit, `split` warps each: a warp goes
+// through the row's parts, 32 at a time with one part's m, L and M a lane, adds
+// those of its turn in order, and the warps' results are joined in order.
 __global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const MergeParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ float s_red[kMergeWarps][2];
-  __shared__ float s_sum[kMergeWarps];
+  __shared__ float s_l[kMergeWarps];
   __shared__ float4 s_o[kMergeWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int b, rt, h, first, n, own = -1;
@@ -531,10 +529,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const Mer
     n = d.y == 0 ? 1 : d.y;
     if (d.y == 0) own = 2 * p.ctas + blockIdx.x;
   }
-  const int row0 = blockIdx.y * kMergeWarps;
-  const int rows = min(kMergeWarps, min(p.R, p.rows - rt * p.R) - row0);
-  for (int i = 0; i < rows; ++i) {
-    const int row = row0 + i, rr = rt * p.R + row;
+  const int turn = warp % p.split;
+  const int row = (blockIdx.y * kMergeWarps + warp) / p.split, rr = rt * p.R + row;
+  const bool live = row < p.R && rr < p.rows;
+  float m = kLowest, M = kLowest, L = 0.0f;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (live) {
     int pn = 0, pslot = 0, prow = 0;
     if (p.pre_o != nullptr) {
       const int pr = b * p.rows + rr;                        // row of the prefix's launch
@@ -546,8 +546,6 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const Mer
       pslot = pn == 1 ? 2 * p.pre_ctas + u : 2 * pslot;
     }
     const int total = n + pn;
-    const bool few = total <= kFewParts;
-    if (few && warp != i) continue;                          // warp-uniform; no barrier on this path
     auto place = [&](int k, const float*& o, const float4*& ml) {
       if (k < n) {
         const int slot = own >= 0 ? own : (k == 0 ? 2 * first + 1 : 2 * (first + k));
@@ -562,27 +560,32 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const Mer
         ml = p.pre_ml + at;
       }
     };
-    float m = kLowest, M = kLowest, L = 0.0f;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (few) {
+    for (int k0 = 0; k0 < total; k0 += 32) {
       float4 mine = make_float4(kLowest, 0.0f, kLowest, 0.0f);
       const float* o;
       const float4* ml;
-      if (lane < total) {
-        place(lane, o, ml);
+      if (k0 + lane < total) {
+        place(k0 + lane, o, ml);
         mine = *ml;
       }
-      m = mine.x;
-      M = mine.z;
+      float to = mine.x, tow = mine.z;
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) {
-        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-        M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d));
+        to = fmaxf(to, __shfl_xor_sync(0xFFFFFFFFu, to, d));
+        tow = fmaxf(tow, __shfl_xor_sync(0xFFFFFFFFu, tow, d));
       }
+      to = fmaxf(to, m);
+      tow = fmaxf(tow, M);
+      const float a = ex2_approx(M - tow);
+      L *= ex2_approx(m - to);
+      acc = make_float4(acc.x * a, acc.y * a, acc.z * a, acc.w * a);
+      m = to;
+      M = tow;
       const float lw = mine.y * ex2_approx(mine.x - m), w = ex2_approx(mine.z - M);
-#pragma unroll 4
-      for (int k = 0; k < total; ++k) {
-        place(k, o, ml);
+      const int end = min(32, total - k0);
+#pragma unroll 8
+      for (int k = turn; k < end; k += p.split) {
+        place(k0 + k, o, ml);
         const float4 y = reinterpret_cast<const float4*>(o)[lane];
         const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
         L += __shfl_sync(0xFFFFFFFFu, lw, k);
@@ -591,71 +594,32 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const Mer
         acc.z += y.z * wk;
         acc.w += y.w * wk;
       }
-    } else {
-      for (int k = threadIdx.x; k < total; k += kMergeWarps * 32) {
-        const float* o;
-        const float4* ml;
-        place(k, o, ml);
-        const float4 v = *ml;
-        m = fmaxf(m, v.x);
-        M = fmaxf(M, v.z);
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) {
-        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-        M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d));
-      }
-      if (lane == 0) {
-        s_red[warp][0] = m;
-        s_red[warp][1] = M;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int k = 0; k < kMergeWarps; ++k) {
-        m = fmaxf(m, s_red[k][0]);
-        M = fmaxf(M, s_red[k][1]);
-      }
-#pragma unroll 4
-      for (int k = warp; k < total; k += kMergeWarps) {
-        const float* o;
-        const float4* ml;
-        place(k, o, ml);
-        const float4 v = *ml;
-        const float4 y = reinterpret_cast<const float4*>(o)[lane];
-        L += v.y * ex2_approx(v.x - m);
-        const float w = ex2_approx(v.z - M);
-        acc.x += y.x * w;
-        acc.y += y.y * w;
-        acc.z += y.z * w;
-        acc.w += y.w * w;
-      }
-      s_o[warp][lane] = acc;
-      if (lane == 0) s_sum[warp] = L;
-      __syncthreads();
-      L = s_sum[0];
-      acc = s_o[0][lane];
-#pragma unroll
-      for (int k = 1; k < kMergeWarps; ++k) {
-        const float4 y = s_o[k][lane];
-        L += s_sum[k];
-        acc.x += y.x;
-        acc.y += y.y;
-        acc.z += y.z;
-        acc.w += y.w;
-      }
-      __syncthreads();                                       // before the next row's parts are written
-      if (warp != 0) continue;
     }
-    const int t = rr / p.G, hq = h * p.G + rr % p.G;
-    const float half = scale2(M - m);
-    const float inv = L == 0.0f ? 0.0f : half / L;
-    uint2 w;
-    w.x = pack_bf16(acc.x * half * inv, acc.y * half * inv);
-    w.y = pack_bf16(acc.z * half * inv, acc.w * half * inv);
-    *reinterpret_cast<uint2*>(p.out + ((static_cast<int64_t>(b) * p.Sq + t) * p.Hq + hq) * kHeadDim + lane * 4) = w;
-    if (p.lse != nullptr && lane == 0)
-      p.lse[(static_cast<int64_t>(b) * p.Hq + hq) * p.Sq + t] = L == 0.0f ? -INFINITY : (m + log2f(L)) * kLn2;
   }
+  if (p.split > 1) {                                         // m and M are the same for all warps of a row
+    s_o[warp][lane] = acc;
+    if (lane == 0) s_l[warp] = L;
+    __syncthreads();
+    if (turn != 0) return;
+    for (int k = 1; k < p.split; ++k) {
+      const float4 y = s_o[warp + k][lane];
+      L += s_l[warp + k];
+      acc.x += y.x;
+      acc.y += y.y;
+      acc.z += y.z;
+      acc.w += y.w;
+    }
+  }
+  if (!live) return;
+  const int t = rr / p.G, hq = h * p.G + rr % p.G;
+  const float half = scale2(M - m);
+  const float inv = L == 0.0f ? 0.0f : half / L;
+  uint2 w;
+  w.x = pack_bf16(acc.x * half * inv, acc.y * half * inv);
+  w.y = pack_bf16(acc.z * half * inv, acc.w * half * inv);
+  *reinterpret_cast<uint2*>(p.out + ((static_cast<int64_t>(b) * p.Sq + t) * p.Hq + hq) * kHeadDim + lane * 4) = w;
+  if (p.lse != nullptr && lane == 0)
+    p.lse[(static_cast<int64_t>(b) * p.Hq + hq) * p.Sq + t] = L == 0.0f ? -INFINITY : (m + log2f(L)) * kLn2;
 }
 
 // ------------------------------------------------------------------- host --
@@ -789,6 +753,7 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream) 
     mp.Sq = a.Sq;
     mp.G = G;
     mp.Hq = a.Hq;
+    int pre_units = 0;
     if (both) {
       const Layout u = layout(B * a.Sq * G, 1, H, true, w.end);
       p.table.pages = a.prefix_pages;
@@ -813,9 +778,16 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream) 
       mp.pre_n = n;
       mp.pre_per = (tiles + pc - 1) / pc;
       mp.pre_ctas = pc;
+      pre_units = u.units;
     }
+    // Warps of a row: so many that each adds about eight parts, and that few rows
+    // leave none idle.
+    const int tile_rows = std::min(w.R, w.rows);
+    const long long parts = ctas / w.units + 1 + (both ? mp.pre_ctas / std::max(1, pre_units) + 1 : 0);
+    mp.split = 1;
+    while (mp.split < kMergeWarps && (mp.split * 8 < parts || mp.split * 2 * tile_rows <= kMergeWarps)) mp.split *= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(both ? w.units : ctas, (std::min(w.R, w.rows) + kMergeWarps - 1) / kMergeWarps);
+    cfg.gridDim = dim3(both ? w.units : ctas, (tile_rows * mp.split + kMergeWarps - 1) / kMergeWarps);
     cfg.blockDim = dim3(kMergeWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -27,9 +27,10 @@
 // operand from there; V is its B operand with the keys as the outer index, as
 // the cache has it.
 //
-// A row's reference m moves where a weight would pass 2^8: then the thread
-// scales the row's sum, its accumulator and the weights of this tile that it
-// has stored already.
+// A row's reference m moves where the sum of 32 weights passes 2^12: then the
+// thread scales the row's sum, its accumulator and the weights of this tile that
+// it has stored already, and forms the 32 again.  bf16 weights keep their
+// precision at any size, so m need not be near the largest score.
 #include <cuda_bf16.h>
 
 #include "cache_attention.cuh"
@@ -50,7 +51,7 @@ constexpr uint32_t kSmemK = 2 * kTileBytes;             // two stages
 constexpr uint32_t kSmemV = 4 * kTileBytes;             // two stages
 constexpr uint32_t kSmemBytes = 6 * kTileBytes + 1024;  // and room to align to 1024
 constexpr int kScaleSlots = 4;                          // of ks and vs: up to three tiles ahead of the softmax
-constexpr float kFar = 8.0f;                            // log2 of the largest weight
+constexpr float kFar = 4096.0f;                         // 2^12: most of 32 weights' sum
 
 __host__ __device__ constexpr uint32_t col_s(int t) { return 128u * t; }
 __host__ __device__ constexpr uint32_t col_o(int t) { return 256u + 128u * t; }
@@ -94,6 +95,13 @@ __device__ __forceinline__ void v_codes_bf16(uint32_t w, uint32_t& lo, uint32_t&
 
 __device__ __forceinline__ float2 unpack_bf16(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ void store32(void* dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f,
+                                        uint32_t g, uint32_t h) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a), "r"(b), "r"(c), "r"(d),
+               "r"(e), "r"(f), "r"(g), "r"(h)
+               : "memory");
 }
 
 // The rare move of a row's reference: alpha = 2^(old - new) of this thread's row
@@ -155,40 +163,42 @@ __device__ __forceinline__ bool softmax_tile(uint32_t tS, uint32_t tO, const flo
         if (2 * i + 1 >= left) y[i].y = -INFINITY;
       }
     }
-    float mx = fmaxf(y[0].x, y[0].y), mx2 = fmaxf(y[1].x, y[1].y);
+    uint32_t w[16];
+    float2 sum;
+    while (true) {
+      sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 2; i < 16; i += 2) {
-      mx = fmax3(mx, y[i].x, y[i].y);
-      mx2 = fmax3(mx2, y[i + 1].x, y[i + 1].y);
-    }
-    mx = fmaxf(mx, mx2) * rk;
-    if (__any_sync(0xFFFFFFFFu, mx > m + kFar)) {
-      const float to = fmaxf(m, mx), alpha = ex2_approx(m - to);
+      for (int i = 0; i < 8; ++i) {
+        const float4 s4 = reinterpret_cast<const float4*>(vx)[c * 8 + i];
+        const float2 x0 = ffma2_bc(y[2 * i].x, y[2 * i].y, rk, -m), x1 = ffma2_bc(y[2 * i + 1].x, y[2 * i + 1].y, rk, -m);
+        const float2 p0 = make_float2(ex2_approx(x0.x), ex2_approx(x0.y));
+        const float2 p1 = make_float2(ex2_approx(x1.x), ex2_approx(x1.y));
+        sum = fadd2v(sum, p0);
+        sum = fadd2v(sum, p1);
+        float2 w0 = fmul2v(p0, make_float2(s4.x, s4.y)), w1 = fmul2v(p1, make_float2(s4.z, s4.w));
+        if constexpr (kCut) {                            // a scale that is not finite stays behind the limit
+          if (4 * i >= left) w0.x = 0.0f;
+          if (4 * i + 1 >= left) w0.y = 0.0f;
+          if (4 * i + 2 >= left) w1.x = 0.0f;
+          if (4 * i + 3 >= left) w1.y = 0.0f;
+        }
+        w[2 * i] = pack_bf16(w0.x, w0.y);
+        w[2 * i + 1] = pack_bf16(w1.x, w1.y);
+      }
+      if (!__any_sync(0xFFFFFFFFu, sum.x + sum.y > kFar)) break;
+      float mx = fmaxf(y[0].x, y[0].y);
+#pragma unroll
+      for (int i = 1; i < 16; ++i) mx = fmax3(mx, y[i].x, y[i].y);
+      const float to = fmaxf(m, mx * rk), alpha = ex2_approx(m - to);
+      const bool still = !__any_sync(0xFFFFFFFFu, to != m);   // an infinite score: no reference helps
       l.x *= alpha;
       l.y *= alpha;
       m = to;
       if (has_o) ok = ok && before();
       if (ok) rescale(tO, tS, c, has_o, alpha);
+      if (still) break;
     }
-    uint32_t w[16];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float4 s4 = reinterpret_cast<const float4*>(vx)[c * 8 + i];
-      const float2 x0 = ffma2_bc(y[2 * i].x, y[2 * i].y, rk, -m), x1 = ffma2_bc(y[2 * i + 1].x, y[2 * i + 1].y, rk, -m);
-      const float2 p0 = make_float2(ex2_approx(x0.x), ex2_approx(x0.y));
-      const float2 p1 = make_float2(ex2_approx(x1.x), ex2_approx(x1.y));
-      l = fadd2v(l, p0);
-      l = fadd2v(l, p1);
-      float2 w0 = fmul2v(p0, make_float2(s4.x, s4.y)), w1 = fmul2v(p1, make_float2(s4.z, s4.w));
-      if constexpr (kCut) {                              // a scale that is not finite stays behind the limit
-        if (4 * i >= left) w0.x = 0.0f;
-        if (4 * i + 1 >= left) w0.y = 0.0f;
-        if (4 * i + 2 >= left) w1.x = 0.0f;
-        if (4 * i + 3 >= left) w1.y = 0.0f;
-      }
-      w[2 * i] = pack_bf16(w0.x, w0.y);
-      w[2 * i + 1] = pack_bf16(w1.x, w1.y);
-    }
+    l = fadd2v(l, sum);
     tmem_st16(tS + 16 * c, w);
   }
   return ok;
@@ -273,17 +283,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
       long long g = f0;                  // tiles whose pages have been asked for
       auto ask = [&]() {
         page = -1;
-        if (g >= f1) return;
+        if (g >= f1) {
+          hi = t0;                       // nothing to load
+          return;
+        }
         head = x.h;
         t0 = x.tile * kWideTok;
         hi = walk.keys(x.b, x.rt);
         const int key = t0 + 16 * lane;
         if (lane < 8 && key < hi) {
           page = __ldg(p.table.pages + (kPrefix ? 0 : x.b * p.table.stride) + (key >> ps));
-          if (page < 0 || page >= p.cache.num_pages) {
-            bad = true;
-            page = -1;
-          }
         }
         ++g;
         if (x.tile + 1 < x.n)
@@ -294,12 +303,29 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
       uint4 w[8];
       float scale = 0.0f;
       auto load = [&]() {
+        const bool gone = page < 0 || page >= p.cache.num_pages;
+        const bool mine = lane < 8 && t0 + 16 * lane < hi;
+        bad |= gone && mine;
+        if (gone) page = -1;
+        // The rows of a step follow those of the step before within a page.
+        const uint8_t* row = codes;
+        if (__any_sync(0xFFFFFFFFu, gone && mine) || t0 + kWideTok > hi) {   // some keys are not there: zeros
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int pg = __shfl_sync(0xFFFFFFFFu, page, i), t = t0 + 16 * i;
-          const int row = ((pg * p.cache.H + head) << ps) + (t & ((1 << ps) - 1)) + sub;
-          w[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (pg >= 0 && t + sub < hi) w[i] = __ldg(reinterpret_cast<const uint4*>(codes + static_cast<int64_t>(row) * kHeadDim));
+          for (int i = 0; i < 8; ++i) {
+            const int pg = __shfl_sync(0xFFFFFFFFu, page, i), t = t0 + 16 * i;
+            row = codes + static_cast<int64_t>(((pg * p.cache.H + head) << ps) + (t & ((1 << ps) - 1)) + sub) * kHeadDim;
+            w[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (pg >= 0 && t + sub < hi) w[i] = __ldg(reinterpret_cast<const uint4*>(row));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (i == 0 || ((16 * i) & ((1 << ps) - 1)) == 0) {               // warp-uniform
+              const int pg = __shfl_sync(0xFFFFFFFFu, page, i);
+              row = codes + static_cast<int64_t>(((pg * p.cache.H + head) << ps) + (i == 0 ? t0 & ((1 << ps) - 1) : 0) + sub - 16 * i) * kHeadDim;
+            }
+            w[i] = __ldg(reinterpret_cast<const uint4*>(row + i * 16 * kHeadDim));
+          }
         }
         const int pg = __shfl_sync(0xFFFFFFFFu, page, tid >> 4), t = t0 + tid;
         scale = 0.0f;
@@ -477,16 +503,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
                 ++joined;
               }
               if (valid && inv_none != 0.0f) {
-                uint4* dst = reinterpret_cast<uint4*>(
-                    p.out + ((static_cast<int64_t>(x.b) * p.Sq + tok) * p.Hq + hq) * kHeadDim + 32 * c);
+                uint16_t* dst = p.out + ((static_cast<int64_t>(x.b) * p.Sq + tok) * p.Hq + hq) * kHeadDim + 32 * c;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  dst[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                      pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+                for (int i = 0; i < 32; i += 16)
+                  store32(dst + i, pack_bf16(o[i] * inv, o[i + 1] * inv), pack_bf16(o[i + 2] * inv, o[i + 3] * inv),
+                          pack_bf16(o[i + 4] * inv, o[i + 5] * inv), pack_bf16(o[i + 6] * inv, o[i + 7] * inv),
+                          pack_bf16(o[i + 8] * inv, o[i + 9] * inv), pack_bf16(o[i + 10] * inv, o[i + 11] * inv),
+                          pack_bf16(o[i + 12] * inv, o[i + 13] * inv), pack_bf16(o[i + 14] * inv, o[i + 15] * inv));
               } else if (valid) {
-                float4* dst = reinterpret_cast<float4*>(p.part_o + at * kHeadDim + 32 * c);
+                float* dst = p.part_o + at * kHeadDim + 32 * c;
+                const uint32_t* v = reinterpret_cast<const uint32_t*>(o);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                for (int i = 0; i < 32; i += 8)
+                  store32(dst + i, v[i], v[i + 1], v[i + 2], v[i + 3], v[i + 4], v[i + 5], v[i + 6], v[i + 7]);
               }
             }
             if (valid && inv_none != 0.0f) {

@@ -88,21 +88,36 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 }
 
 // mbar_wait without a function call, for kernels that move registers between
-// their warpgroups (setmaxnreg), which calls would not allow.
+// their warpgroups (setmaxnreg), which calls would not allow.  A poll suspends the
+// thread for up to 20 us, so that waiting warps leave the issue slots to others.
+__device__ __forceinline__ bool mbar_try_wait_long(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool mbar_wait_inline(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err_word,
                                                  uint64_t timeout_ns) {
   const uint32_t a = smem_addr(bar);
-  if (mbar_try_wait(a, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait(a, parity)) {
+  uint64_t t0 = 0;
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait_long(a, parity)) return true;
+    const uint64_t now = global_timer_ns();
     if (*abort_flag) return false;
-    if (global_timer_ns() - t0 > timeout_ns) {
+    if (t0 == 0) t0 = now;
+    if (now - t0 > timeout_ns) {
       *abort_flag = 1;
       atomicExch(err_word, SAGE_DEVERR_TIMEOUT);
       return false;
     }
   }
-  return true;
 }
 
 // ------------------------------------------------------------------ TMA --
