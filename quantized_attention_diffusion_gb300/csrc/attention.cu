@@ -46,6 +46,7 @@
 // than one thread needs to issue it, so the issue loops are kept short:
 // descriptors are formed from precomputed lower words, and barrier waits
 // inline only their first poll.
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <cuda.h>
@@ -754,8 +755,19 @@ cudaError_t read_and_clear_device_error(int* code, cudaStream_t stream) {
   return e;
 }
 
+// The address is looked up once on each device and kept.
 cudaError_t device_error_word(int** word) {
-  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_sage_error);
+  constexpr int kDevices = 64;
+  static std::atomic<int*> words[kDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kDevices) return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_sage_error);
+  *word = words[dev].load(std::memory_order_acquire);
+  if (*word != nullptr) return cudaSuccess;
+  e = cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_sage_error);
+  if (e == cudaSuccess) words[dev].store(*word, std::memory_order_release);
+  return e;
 }
 
 cudaError_t launch_wait_timeout_probe(uint64_t timeout_ns, cudaStream_t stream) {

@@ -32,6 +32,7 @@ using namespace cache;
 namespace {
 
 constexpr int kTok = 64;                                  // keys per tile
+constexpr int kCost = 2;                                  // of a unit, in tiles
 constexpr int kConsumers = 4;                             // warps that compute, 16 keys of a tile each
 constexpr int kThreads = (kConsumers + 1) * 32;           // and one that copies
 constexpr uint32_t kOffV = kTok * kHeadDim;
@@ -44,7 +45,7 @@ constexpr int kMaxCtas = 3 * kSms;                        // CTAs of a launch: t
 __host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : nt == 2 ? 2 : 1; }
 // Tiles in flight: 9, 8 or 8 on an SM, 135 KB or more.
 __host__ __device__ constexpr int stages_of(int nt) { return nt == 1 ? 3 : nt == 2 ? 4 : 8; }
-constexpr uint32_t smem_of(int nt) { return stages_of(nt) * kStageBytes + kMergeBytes; }
+constexpr uint32_t smem_of(int nt) { return stages_of(nt) * kStageBytes + kMergeBytes + 8 * nt * kHeadDim * 2; }
 constexpr float kFar = 256.0f;                            // 2^8: weights stay below it (fp16: 65504)
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -220,7 +221,7 @@ template <int NT, bool kPrefix>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(const Params p) {
   constexpr int R = 8 * NT, kStages = stages_of(NT);
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t full[kStages], empty[kStages];
+  __shared__ uint64_t full[kStages], empty[kStages], q_full, q_empty;
   __shared__ int abort_flag;
   __shared__ int s_len[kMaxBatch];
   __shared__ long long s_off[kPrefix ? 2 : kMaxBatch + 1];
@@ -232,26 +233,26 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
   // there is room; it waits for this grid before it reads anything from it.
   asm volatile("griddepcontrol.launch_dependents;");
 
-  const Walk<R, kTok, kPrefix> walk{p, s_len, s_off};
-  walk.load_lengths(s_len);
-  if (threadIdx.x == 0) {
+  const Walk<R, kTok, kCost, kPrefix> walk{p, s_len, s_off};
+  walk.plan(s_len, s_off);
+  if (threadIdx.x == 32) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], kConsumers);
     }
+    mbar_init(&q_full, 1);
+    mbar_init(&q_empty, kConsumers);
     abort_flag = 0;
     fence_mbarrier_init();
   }
   __syncthreads();
-  if (warp == 0) walk.sum_tiles(s_off, lane);
-  __syncthreads();
 
   const long long total = s_off[walk.seqs()] * p.cache.H;
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long per = div_floor(total + gridDim.x - 1, gridDim.x);
   const long long f0 = blockIdx.x * per, f1 = min(total, f0 + per);
   if (!p.keep && threadIdx.x == 0) p.desc[blockIdx.x].w = 0;
   if (f0 < f1) {
-    Place x = walk.locate(f0);
+    Place x = walk.locate(f0, static_cast<int>(f1 - f0));
     const uint32_t smem0 = smem_addr(smem);
     if (warp == kConsumers) {
       // ------------------------------------------------------------ copies --
@@ -263,19 +264,34 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
       const int my_run = lane >> 2, part = lane & 3;
       int it = 0;
       bool bad = false, ok = true;
-      for (long long f = f0; f < f1 && ok;) {
+      uint32_t seg = 0;
+      auto pages_of = [&](const Place& at, int first) {    // entry first + lane of the unit's row of the table
+        const int32_t* row = p.table.pages + (kPrefix ? 0 : at.b * p.table.stride);
+        return first + lane < p.table.width ? __ldg(row + first + lane) : -1;
+      };
+      int ahead = x.left > 0 ? pages_of(x, (x.t0 * kTok) >> ps) : -1;
+      while (x.left > 0 && ok) {
         const int hi = walk.keys(x.b, x.rt);
-        const int32_t* row = p.table.pages + (kPrefix ? 0 : x.b * p.table.stride);
-        const int last = static_cast<int>(min(static_cast<long long>(x.n), x.tile + (f1 - f)));
-        int base = (x.tile * kTok) >> ps;
-        int cur = base + lane < p.table.width ? __ldg(row + base + lane) : -1;
-        int nxt = base + 32 + lane < p.table.width ? __ldg(row + base + 32 + lane) : -1;
-        for (int t = x.tile; t < last; ++t, ++it) {
+        int base = (x.t0 * kTok) >> ps, cur = ahead, nxt = -1;
+        if ((((x.t1 - 1) * kTok) >> ps) - base >= 32) nxt = pages_of(x, base + 32);
+        Place after = x;                 // the next segment's pages are on their way during this one
+        walk.next(after);
+        if (after.left > 0) ahead = pages_of(after, (after.t0 * kTok) >> ps);
+        // The unit's queries, once all warps have read the last unit's.
+        const int rows = min(R, p.rows - x.rt * R);
+        if (seg > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(&q_empty, (seg - 1) & 1, abort_v, p.err, p.timeout_ns))) break;
+        if (lane == 0) mbar_arrive_expect_tx(&q_full, rows * kHeadDim * 2);
+        __syncwarp();
+        if (lane < rows)
+          bulk_load(smem0 + kStages * kStageBytes + kMergeBytes + lane * kHeadDim * 2, walk.query(x, x.rt * R + lane),
+                    kHeadDim * 2, smem_addr(&q_full));
+        ++seg;
+        for (int t = x.t0; t < x.t1; ++t, ++it) {
           const int t0 = t * kTok + my_run * run;
           if (((t * kTok) >> ps) - base >= 32) {
             base += 32;
             cur = nxt;
-            nxt = base + 32 + lane < p.table.width ? __ldg(row + base + 32 + lane) : -1;
+            nxt = pages_of(x, base + 32);
           }
           // The tile's pages are base .. base + 31: run <= page and a tile
           // begins at a multiple of 64 keys.
@@ -307,15 +323,16 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
               bulk_load(st + kOffVs + o * 4, p.cache.v_scale + r, run * 4, bar);
           }
         }
-        f += last - x.tile;
-        walk.next(x);
+        x = after;
       }
       if (bad) atomicExch(p.err, SAGE_DEVERR_BAD_PAGE);
-      if (!ok) {   // let the copies in flight land before the CTA can exit
+      if (*abort_v) {   // let the copies in flight land before the CTA can exit
         for (int j = max(0, it - kStages); j < it; ++j) {
           int local_abort = 0;
           (void)mbar_wait(&full[j % kStages], (j / kStages) & 1, &local_abort, p.err, p.timeout_ns);
         }
+        int local_abort = 0;
+        if (seg > 0) (void)mbar_wait(&q_full, (seg - 1) & 1, &local_abort, p.err, p.timeout_ns);
       }
     } else {
       // ----------------------------------------------------------- compute --
@@ -333,24 +350,21 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
       float4* merge = reinterpret_cast<float4*>(smem + kStages * kStageBytes);
       int it = 0;
       bool ok = true;
-      for (long long f = f0; f < f1;) {
+      const uint8_t* queries = smem + kStages * kStageBytes + kMergeBytes;
+      for (uint32_t seg = 0; x.left > 0; ++seg) {
         const int hi = walk.keys(x.b, x.rt);
-        const int last = static_cast<int>(min(static_cast<long long>(x.n), x.tile + (f1 - f)));
         const int rows = min(R, p.rows - x.rt * R);   // of this tile
         QueryRows<NT> z;
         int lo = INT_MAX;            // keys that every row sees
+        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&q_full, seg & 1, abort_v, p.err, p.timeout_ns));
 #pragma unroll
         for (int a = 0; a < NT; ++a) {
-          const int rr = x.rt * R + a * 8 + r;
-          uint4 w[4];
+          uint4 raw[4];              // row r of these eight, a quarter of its channels
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (rr < p.rows) {
-            const uint16_t* src = walk.query(x, rr) + c * 32;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
-          }
-          const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+          for (int i = 0; i < 4; ++i)
+            raw[i] = a * 8 + r < rows ? *reinterpret_cast<const uint4*>(queries + (a * 8 + r) * kHeadDim * 2 + c * 64 + i * 16)
+                                      : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t* u = reinterpret_cast<const uint32_t*>(raw);
           uint32_t top = 0u;
 #pragma unroll
           for (int i = 0; i < 16; ++i) top = max(top, max(u[i] & 0x7FFFu, (u[i] >> 16) & 0x7FFFu));
@@ -370,6 +384,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
             lo = min(lo, z.lim[a][e]);
           }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_empty);
         lo = __reduce_min_sync(0xFFFFFFFFu, lo);
 
 #pragma unroll
@@ -385,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
           }
         }
 
-        for (int t = x.tile; t < last; ++t, ++it) {
+        for (int t = x.t0; t < x.t1; ++t, ++it) {
           const int s = it % kStages;
           ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&full[s], (it / kStages) & 1, abort_v, p.err, p.timeout_ns));
           const int t0 = t * kTok + warp * 16;      // this warp's first key
@@ -396,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
 
         // The four warps' parts of the segment, 8 rows at a time.  A warp whose
         // wait gave up takes part in the barriers and writes nothing.
-        const bool whole = x.tile == 0 && last == x.n;
+        const bool whole = walk.whole(x);
 #pragma unroll
         for (int a = 0; a < NT; ++a) {
           if (a * 8 >= rows) break;
@@ -463,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
               if (p.lse != nullptr && g == 0)
                 p.lse[(static_cast<int64_t>(x.b) * p.Hq + hq) * p.Sq + t] = L == 0.0f ? -INFINITY : (mm + log2f(L)) * kLn2;
             } else {
-              const int64_t at = static_cast<int64_t>(walk.slot(x, whole)) * p.slot_rows + a * 8 + row;
+              const int64_t at = static_cast<int64_t>(walk.slot(x)) * p.slot_rows + a * 8 + row;
               float4* dst = reinterpret_cast<float4*>(p.part_o + at * kHeadDim) + g * 2;
               dst[0] = sum[0];
               dst[1] = sum[1];
@@ -471,8 +487,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
             }
           }
         }
-        if (threadIdx.x == 0) walk.tell(x, whole, f, per);
-        f += last - x.tile;
+        if (threadIdx.x == 0) walk.tell(x, f1, per);
         walk.next(x);
       }
     }
@@ -493,8 +508,8 @@ struct MergeParams {
   // The prefix's parts: closed form, every unit has as many tiles.
   const float* pre_o;
   const float4* pre_ml;
-  int pre_R, pre_slot_rows, pre_n, pre_ctas;        // rows of a tile and of a slot, key tiles of a unit, CTAs
-  long long pre_per;                                // key tiles of a CTA
+  int pre_R, pre_slot_rows, pre_n, pre_cost, pre_ctas;   // rows of a tile and of a slot, a unit's tiles and cost, CTAs
+  long long pre_per;                                     // steps of a CTA
   uint16_t* out;
   float* lse;
   int Sq, G, Hq;
@@ -540,9 +555,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const Mer
       const int pr = b * p.rows + rr;                        // row of the prefix's launch
       prow = pr % p.pre_R;
       const int u = pr / p.pre_R * p.H + h;
-      const long long f = static_cast<long long>(u) * p.pre_n;
-      pslot = static_cast<int>(f / p.pre_per);
-      pn = static_cast<int>((f + p.pre_n - 1) / p.pre_per) - pslot + 1;
+      const long long f = static_cast<long long>(u) * (p.pre_n + p.pre_cost) + p.pre_cost;   // its first tile's step
+      pslot = static_cast<int>(div_floor(f, p.pre_per));
+      pn = static_cast<int>(div_floor(f + p.pre_n - 1, p.pre_per)) - pslot + 1;
       pslot = pn == 1 ? 2 * p.pre_ctas + u : 2 * pslot;
     }
     const int total = n + pn;
@@ -583,16 +598,24 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const Mer
       M = tow;
       const float lw = mine.y * ex2_approx(mine.x - m), w = ex2_approx(mine.z - M);
       const int end = min(32, total - k0);
-#pragma unroll 8
-      for (int k = turn; k < end; k += p.split) {
-        place(k0 + k, o, ml);
-        const float4 y = reinterpret_cast<const float4*>(o)[lane];
-        const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
-        L += __shfl_sync(0xFFFFFFFFu, lw, k);
-        acc.x += y.x * wk;
-        acc.y += y.y * wk;
-        acc.z += y.z * wk;
-        acc.w += y.w * wk;
+      for (int k = turn; k < end; k += 4 * p.split) {        // four parts in flight
+        float4 y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          place(k0 + min(k + i * p.split, end - 1), o, ml);
+          y[i] = reinterpret_cast<const float4*>(o)[lane];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at = k + i * p.split;
+          const float wk = __shfl_sync(0xFFFFFFFFu, w, at & 31), lk = __shfl_sync(0xFFFFFFFFu, lw, at & 31);
+          if (at >= end) break;
+          L += lk;
+          acc.x += y[i].x * wk;
+          acc.y += y[i].y * wk;
+          acc.z += y[i].z * wk;
+          acc.w += y[i].w * wk;
+        }
       }
     }
   }
@@ -631,6 +654,7 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 int rows_per_tile(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : kWideRows; }
 int max_ctas(int R) { return kSms * (R == kWideRows ? 1 : ctas_per_sm(R / 8)); }
 int keys_per_tile(int R) { return R == kWideRows ? kWideTok : kTok; }
+int unit_cost(int R) { return R == kWideRows ? kWideCost : kCost; }
 
 // One launch's part of the workspace.
 struct Layout {
@@ -664,7 +688,8 @@ cudaError_t launch_part(const Params& p, int R, bool prefix, unsigned ctas, cuda
   if (R == kWideRows) return launch_wide(p, prefix, ctas, stream);
   const uint32_t smem = smem_of(R / 8);
   auto go = [&](auto kernel) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    static std::atomic<uint64_t> allowed[2 * 4];       // for each kernel
+    cudaError_t e = allow_smem(kernel, smem, allowed[(prefix ? 4 : 0) + R / 16]);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
@@ -733,7 +758,7 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream) 
     p.err = a.err;
     p.room = static_cast<int>(std::min<int64_t>(kMaxCacheLen, static_cast<int64_t>(a.table.width) << a.cache.page_shift));
     // The lengths are on the device: as many CTAs as the table has room for.
-    const unsigned ctas = ctas_for(std::min<long long>(kMaxCtas, (static_cast<long long>(p.room) + keys_per_tile(w.R) - 1) / keys_per_tile(w.R)) * w.units, w.R);
+    const unsigned ctas = ctas_for(std::min<long long>(kMaxCtas, (static_cast<long long>(p.room) + keys_per_tile(w.R) - 1) / keys_per_tile(w.R) + unit_cost(w.R)) * w.units, w.R);
     cudaError_t e = launch_part(p, w.R, false, ctas, stream);
     if (e != cudaSuccess) return e;
 
@@ -767,8 +792,8 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream) 
       p.desc = at<int4>(a.workspace, u.desc);
       p.info = at<int2>(a.workspace, u.info);
       const int n = (a.prefix_len + keys_per_tile(u.R) - 1) / keys_per_tile(u.R);
-      const long long tiles = static_cast<long long>(n) * u.units;
-      const unsigned pc = ctas_for(tiles, u.R);
+      const long long steps = static_cast<long long>(n + unit_cost(u.R)) * u.units;
+      const unsigned pc = ctas_for(steps, u.R);
       e = launch_part(p, u.R, true, pc, stream);
       if (e != cudaSuccess) return e;
       mp.pre_o = p.part_o;
@@ -776,7 +801,8 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream) 
       mp.pre_R = u.R;
       mp.pre_slot_rows = u.slot_rows;
       mp.pre_n = n;
-      mp.pre_per = (tiles + pc - 1) / pc;
+      mp.pre_cost = unit_cost(u.R);
+      mp.pre_per = (steps + pc - 1) / pc;
       mp.pre_ctas = pc;
       pre_units = u.units;
     }

@@ -13,7 +13,7 @@
 namespace sage::cache {
 
 constexpr int kSms = 152;
-constexpr int kMaxBatch = 512;                            // sequences of one launch
+constexpr int kMaxBatch = 256;                            // sequences of one launch
 constexpr float kLowest = -1e30f;                         // a reference below every score
 constexpr float kLog2e = 1.44269502162933349609375f;      // fp32(log2 e)
 constexpr float kLn2 = 0.693147182464599609375f;          // fp32(ln 2)
@@ -45,20 +45,29 @@ struct Params {
 // nothing in between overflows or vanishes.
 __device__ __forceinline__ float scale2(float e) { return ex2_approx(0.5f * e); }
 
-// A launch's work is a row of key tiles: for each sequence, each tile of query
-// rows and each key/value head (a unit) its tiles of keys in order.  CTA c
-// takes tiles [c * per, (c + 1) * per), whatever units they belong to, so that
-// unequal lengths leave no SM idle.  The part of a unit that a CTA has is a
-// segment: a unit of one segment is written out at once, segments of a unit
-// that CTAs share go to the workspace (slot 2c + 1 for the unit that begins
-// in CTA c and ends later, slot 2c for one that began earlier) and the merge
-// kernel joins them in the order of the CTAs.
+// a / b for a >= 0, b > 0: in 32 bits where they do.
+__device__ __forceinline__ long long div_floor(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+// A launch's work is a row of steps: for each sequence, each tile of query rows
+// and each key/value head (a unit) Cost steps, which stand for what a unit takes
+// however short it is, and one for each of its tiles of keys, in order.  CTA c has
+// steps [c * per, (c + 1) * per), whatever units they belong to, so that unequal
+// lengths leave no SM idle.  The tiles of a unit that a CTA has are a segment: a
+// unit of one segment is written out at once, segments of a unit that CTAs share
+// go to the workspace (slot 2c + 1 for the unit that begins in CTA c and ends
+// later, slot 2c for one that began earlier) and the merge kernel joins them in
+// the order of the CTAs.
 struct Place {
-  int b, rt, h, tile, n;     // n: tiles of the unit
+  int b, rt, h, n;           // a unit and its tiles
+  int skip, left;            // its steps that earlier CTAs have, and steps of this CTA from there on
+  int t0, t1;                // tiles of the segment
 };
 
 // R query rows and Tok keys a tile.
-template <int R, int Tok, bool kPrefix>
+template <int R, int Tok, int Cost, bool kPrefix>
 struct Walk {
   const Params& p;
   const int* s_len;
@@ -83,7 +92,9 @@ struct Walk {
   __device__ int tiles(int b, int rt) const { return max(1, (keys(b, rt) + Tok - 1) / Tok); }
   __device__ int seqs() const { return kPrefix ? 1 : p.B; }
 
-  __device__ Place locate(long long f) const {
+  // The first segment of the CTA that has the steps [f, f + left); x.left is 0
+  // if it has none, which is so too after `next` behind the last.
+  __device__ Place locate(long long f, int left) const {
     Place x;
     int lo = 0, hi = seqs();
     while (hi - lo > 1) {
@@ -97,59 +108,88 @@ struct Walk {
     x.b = lo;
     x.rt = 0;
     x.n = tiles(lo, 0);
-    while (rem >= static_cast<long long>(x.n) * p.cache.H) {
-      rem -= static_cast<long long>(x.n) * p.cache.H;
+    while (rem >= static_cast<long long>(x.n + Cost) * p.cache.H) {
+      rem -= static_cast<long long>(x.n + Cost) * p.cache.H;
       x.n = tiles(lo, ++x.rt);
     }
-    x.h = static_cast<int>(rem / x.n);
-    x.tile = static_cast<int>(rem % x.n);
+    x.h = static_cast<int>(div_floor(rem, x.n + Cost));
+    x.skip = static_cast<int>(rem - static_cast<long long>(x.h) * (x.n + Cost));
+    x.left = left;
+    if (!cut(x)) next(x);
     return x;
   }
+  // The segment's tiles; false if it has none.
+  __device__ bool cut(Place& x) const {
+    x.t0 = max(0, x.skip - Cost);
+    x.t1 = min(x.n, x.skip + x.left - Cost);
+    return x.t1 > x.t0;
+  }
   __device__ void next(Place& x) const {
-    x.tile = 0;
-    if (++x.h < p.cache.H) return;
-    x.h = 0;
-    if (++x.rt == p.row_tiles) {
-      x.rt = 0;
-      ++x.b;
-    }
-    if (x.b < seqs()) x.n = tiles(x.b, x.rt);
-  }
-  // The lengths of the launch's sequences, cut to what their table can hold.
-  __device__ void load_lengths(int* len) const {
-    for (int i = threadIdx.x; i < p.B; i += blockDim.x) len[i] = max(0, min(p.room, __ldg(p.lens + i)));
-  }
-  // One warp: off[b] = tiles of the sequences before b, for one key/value head.
-  __device__ void sum_tiles(long long* off, int lane) const {
-    long long base = 0;
-    for (int b0 = 0; b0 < seqs(); b0 += 32) {
-      long long n = 0;
-      if (b0 + lane < seqs())
-        for (int rt = 0; rt < p.row_tiles; ++rt) n += tiles(b0 + lane, rt);
-      long long sum = n;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long up = __shfl_up_sync(0xFFFFFFFFu, sum, d);
-        if (lane >= d) sum += up;
+    do {
+      x.left -= min(x.left, x.n + Cost - x.skip);
+      x.skip = 0;
+      if (x.left == 0) return;
+      if (++x.h == p.cache.H) {
+        x.h = 0;
+        if (++x.rt == p.row_tiles) {
+          x.rt = 0;
+          ++x.b;
+        }
+        x.n = tiles(x.b, x.rt);
       }
-      if (b0 + lane < seqs()) off[b0 + lane] = base + sum - n;
-      base += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    } while (!cut(x));
+  }
+  __device__ bool whole(const Place& x) const { return x.t0 == 0 && x.t1 == x.n; }
+  // The lengths of the launch's sequences, cut to what their table can hold, and
+  // off[b] = steps of the sequences before b, for one key/value head.  Every thread
+  // calls it; a barrier has to follow.
+  __device__ void plan(int* len, long long* off) const {
+    if constexpr (kPrefix) {
+      for (int i = threadIdx.x; i < p.B; i += blockDim.x) len[i] = max(0, min(p.room, __ldg(p.lens + i)));
+      if (threadIdx.x == 0) {
+        long long n = 0;
+        for (int rt = 0; rt < p.row_tiles; ++rt) n += tiles(0, rt) + Cost;
+        off[0] = 0;
+        off[1] = n;
+      }
+    } else if (threadIdx.x < 32) {
+      const int lane = threadIdx.x;
+      long long base = 0;
+      int next = lane < p.B ? __ldg(p.lens + lane) : 0;
+      for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int b = b0 + lane, mine = max(0, min(p.room, next));
+        if (b + 32 < p.B) next = __ldg(p.lens + b + 32);
+        long long n = 0;
+        if (b < p.B) {
+          len[b] = mine;
+          for (int rt = 0; rt < p.row_tiles; ++rt) n += tiles(b, rt) + Cost;   // reads what this thread has written
+        }
+        long long sum = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const long long up = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+          if (lane >= d) sum += up;
+        }
+        if (b < p.B) off[b] = base + sum - n;
+        base += __shfl_sync(0xFFFFFFFFu, sum, 31);
+      }
+      if (lane == 0) off[p.B] = base;
     }
-    if (lane == 0) off[seqs()] = base;
   }
   // Where a segment's result goes if it is not written out.
-  __device__ int slot(const Place& x, bool whole) const {
-    if (whole) return 2 * static_cast<int>(gridDim.x) + unit(x);
-    return 2 * static_cast<int>(blockIdx.x) + (x.tile > 0 ? 0 : 1);
+  __device__ int slot(const Place& x) const {
+    if (whole(x)) return 2 * static_cast<int>(gridDim.x) + unit(x);
+    return 2 * static_cast<int>(blockIdx.x) + (x.t0 > 0 ? 0 : 1);
   }
-  // For the merge kernel, by one thread where a unit begins: how many CTAs have a
-  // part of it.  f: flat index of its first tile, per: tiles of a CTA.
-  __device__ void tell(const Place& x, bool whole, long long f, long long per) const {
-    if (x.tile != 0) return;
-    const int ctas = static_cast<int>((f + x.n - 1) / per) - static_cast<int>(blockIdx.x) + 1;
+  // For the merge kernel, by one thread where a unit's tiles begin: how many CTAs
+  // have some of them.  f1: the step behind this CTA's last, per: steps of a CTA.
+  __device__ void tell(const Place& x, long long f1, long long per) const {
+    if (x.t0 != 0) return;
+    const long long last = f1 - x.left - x.skip + Cost + x.n - 1;
+    const int ctas = static_cast<int>(div_floor(last, per)) - static_cast<int>(blockIdx.x) + 1;
     if (p.keep)
-      p.info[unit(x)] = make_int2(blockIdx.x, whole ? 0 : ctas);
-    else if (!whole)
+      p.info[unit(x)] = make_int2(blockIdx.x, whole(x) ? 0 : ctas);
+    else if (!whole(x))
       p.desc[blockIdx.x] = make_int4(x.b, x.rt, x.h, ctas);
   }
   // The query row rr of the unit's key/value head, 128 channels.
@@ -196,7 +236,7 @@ __device__ __forceinline__ void k_codes_f16(uint32_t w, uint32_t& lo, uint32_t& 
 
 // The launch of the kernel for many query rows (cache_attention_wide.cu): 256
 // rows and 128 keys a tile, one CTA on each SM.
-constexpr int kWideRows = 256, kWideTok = 128;
+constexpr int kWideRows = 256, kWideTok = 128, kWideCost = 3;
 cudaError_t launch_wide(const Params& p, bool prefix, unsigned ctas, cudaStream_t stream);
 
 }  // namespace sage::cache

@@ -220,9 +220,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
   volatile int* abort_v = &abort_flag;
   asm volatile("griddepcontrol.launch_dependents;");
 
-  const Walk<kWideRows, kWideTok, kPrefix> walk{p, s_len, s_off};
-  walk.load_lengths(s_len);
-  if (threadIdx.x == 0) {
+  const Walk<kWideRows, kWideTok, kWideCost, kPrefix> walk{p, s_len, s_off};
+  walk.plan(s_len, s_off);
+  if (threadIdx.x == 32) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars.k_full[s], 128);
       mbar_init(&bars.k_empty[s], 1);
@@ -248,15 +248,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  if (warp == 0) walk.sum_tiles(s_off, lane);
-  __syncthreads();
 
   const long long total = s_off[walk.seqs()] * p.cache.H;
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long per = div_floor(total + gridDim.x - 1, gridDim.x);
   const long long f0 = blockIdx.x * per, f1 = min(total, f0 + per);
   if (!p.keep && threadIdx.x == 0) p.desc[blockIdx.x].w = 0;
   if (f0 < f1) {
-    Place x = walk.locate(f0);
+    Place x = walk.locate(f0, static_cast<int>(f1 - f0));
     auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_inline(bar, parity & 1u, abort_v, p.err, p.timeout_ns); };
 
     if (warp < 8) {
@@ -280,29 +278,29 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
       bool bad = false;
       // The tile whose codes are loaded next: its keys' page (lane i: of step i), head and bounds.
       int page = -1, head = 0, t0 = 0, hi = 0;
-      long long g = f0;                  // tiles whose pages have been asked for
+      int tile = x.t0;
+      bool more = true, loaded = false;   // tiles to ask for; codes that wait to be converted
       auto ask = [&]() {
         page = -1;
-        if (g >= f1) {
-          hi = t0;                       // nothing to load
-          return;
-        }
+        more = x.left > 0;
+        if (!more) return;
         head = x.h;
-        t0 = x.tile * kWideTok;
+        t0 = tile * kWideTok;
         hi = walk.keys(x.b, x.rt);
         const int key = t0 + 16 * lane;
         if (lane < 8 && key < hi) {
           page = __ldg(p.table.pages + (kPrefix ? 0 : x.b * p.table.stride) + (key >> ps));
         }
-        ++g;
-        if (x.tile + 1 < x.n)
-          ++x.tile;
-        else
+        if (++tile == x.t1) {
           walk.next(x);
+          tile = x.t0;
+        }
       };
       uint4 w[8];
       float scale = 0.0f;
       auto load = [&]() {
+        loaded = more;
+        if (!more) return;
         const bool gone = page < 0 || page >= p.cache.num_pages;
         const bool mine = lane < 8 && t0 + 16 * lane < hi;
         bad |= gone && mine;
@@ -335,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
       load();
       ask();
       int it = 0;
-      for (long long f = f0; f < f1; ++f, ++it) {
+      for (; loaded; ++it) {
         const int s = it & 1, round = it >> 1;
         // V's scales may be written before its stage is free: the tile that last
         // used the slot has been multiplied.
@@ -388,12 +386,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
       int it = 0;                                          // key tiles of this CTA
       uint32_t done = 0, joined = 0;                       // tiles and exchanges of this half
       bool ok = true;
-      for (long long f = f0; f < f1 && ok;) {
+      while (x.left > 0 && ok) {
         const int hi = walk.keys(x.b, x.rt);
-        const int last = static_cast<int>(min(static_cast<long long>(x.n), x.tile + (f1 - f)));
-        const int n = last - x.tile;
+        const int n = x.t1 - x.t0;
         const int rows = min(kWideRows, p.rows - x.rt * kWideRows);
-        const bool whole = x.tile == 0 && last == x.n, by_rows = rows > 128;
+        const bool whole = walk.whole(x), by_rows = rows > 128;
         if (by_rows || t < n) {
           const int r = (by_rows ? t * 128 : 0) + trow, rr = x.rt * kWideRows + r;
           const bool valid = r < rows;
@@ -439,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
             ok = wait(&bars.scales[slot], (it + j) / kScaleSlots) && wait(&bars.s_full[t], done);
             if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
             tc_fence_after();
-            const int key0 = (x.tile + j) * kWideTok;
+            const int key0 = (x.t0 + j) * kWideTok;
             if (key0 + kWideTok > lo)                      // warp-uniform
               ok = softmax_tile<true>(tS, tO, s_ks[slot], s_vs[slot], rk, key0, lim, has_o, m, l, before);
             else
@@ -472,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
           } else {
             float a0 = 1.0f, a1 = 0.0f;
             const float inv_none = whole && !p.keep ? 1.0f : 0.0f;   // written out, or to the workspace
-            const int64_t at = static_cast<int64_t>(walk.slot(x, whole)) * p.slot_rows + r;
+            const int64_t at = static_cast<int64_t>(walk.slot(x)) * p.slot_rows + r;
             const int tok = rr / p.G, hq = x.h * p.G + rr % p.G;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
@@ -527,9 +524,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
           }
           tc_fence_before();                               // O may be written again
         }
-        if (warp == 8 && lane == 0) walk.tell(x, whole, f, per);
+        if (warp == 8 && lane == 0) walk.tell(x, f1, per);
         it += n;
-        f += n;
         walk.next(x);
       }
     } else {
@@ -561,9 +557,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
         mma_commit(&bars.pv_done[t]);
         ++pv[t];
       };
-      for (long long f = f0; f < f1 && ok;) {
-        const int last = static_cast<int>(min(static_cast<long long>(x.n), x.tile + (f1 - f)));
-        const int n = last - x.tile;
+      while (x.left > 0 && ok) {
+        const int n = x.t1 - x.t0;
         const bool by_rows = p.rows - x.rt * kWideRows > 128;
         // Step i: half t = i % 2 of key tile j = i / 2, or key tile i in half i % 2.
         // The scores of step i + 2 follow the weighted sum of step i, whose weights
@@ -592,7 +587,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
           if (i + 2 < steps) scores(i + 2);
         }
         it += n;
-        f += n;
         walk.next(x);
       }
       // Every product has to end before TMEM can be released.
@@ -617,7 +611,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
 
 cudaError_t launch_wide(const Params& p, bool prefix, unsigned ctas, cudaStream_t stream) {
   auto go = [&](auto kernel) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
+    static std::atomic<uint64_t> allowed[2];           // for each kernel
+    cudaError_t e = allow_smem(kernel, kSmemBytes, allowed[prefix]);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);

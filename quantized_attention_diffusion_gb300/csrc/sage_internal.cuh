@@ -2,6 +2,7 @@
 // (kernel launchers and their argument blocks).  Not part of the public ABI.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -147,6 +148,20 @@ struct CacheAttnArgs {
 };
 size_t cache_attn_workspace_bytes(int B, int Sq, int Hq, int Hkv, int prefix_len);
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream);
+
+// cudaFuncSetAttribute for `kernel`'s dynamic shared memory, once on each device:
+// `done` is a bit mask of the devices that have it (static, one for each kernel).
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kernel, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // Address of the current device's error word.
 cudaError_t device_error_word(int** word);

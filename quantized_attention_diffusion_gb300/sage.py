@@ -544,57 +544,80 @@ def kv_cache_alloc(num_pages: int, H: int, page_size: int = 64, device=None):
             torch.empty(scales, dtype=torch.float32, device=dev))
 
 
+# The checks below run on every generation step, so they ask each tensor for as
+# little as they need: device numbers instead of devices, and no context manager
+# where the device is the current one.
+
+_INT8, _FP32, _BF16, _INT32 = torch.int8, torch.float32, torch.bfloat16, torch.int32
+_FP8 = (torch.float8_e4m3fn, torch.uint8)
+
+
 def _check_cache(cache):
-    """The cache tuple as a sage_kv_cache, and its device."""
+    """The cache tuple as a sage_kv_cache, and its device number."""
     if not isinstance(cache, (tuple, list)) or len(cache) != 4:
         raise TypeError("cache must be (k_codes, k_scale, v_codes, v_scale)")
     kc, ks, vc, vs = cache
-    dev = kc.device
-    for name, t, dtypes in (("k_codes", kc, (torch.int8,)), ("k_scale", ks, (torch.float32,)),
-                            ("v_codes", vc, (torch.float8_e4m3fn, torch.uint8)), ("v_scale", vs, (torch.float32,))):
-        if t.dtype not in dtypes:
-            raise ValueError(f"{name} must be {dtypes[0]} (got {t.dtype})")
-        if not t.is_cuda or t.device != dev:
-            raise ValueError("the cache must be CUDA tensors on one device")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    shape = kc.shape
-    if len(shape) != 4 or vc.shape != shape or ks.shape != shape[:3] or vs.shape != shape[:3]:
+    if kc.dtype is not _INT8 or ks.dtype is not _FP32 or vc.dtype not in _FP8 or vs.dtype is not _FP32:
+        for name, t, want in (("k_codes", kc, _INT8), ("k_scale", ks, _FP32), ("v_codes", vc, _FP8[0]), ("v_scale", vs, _FP32)):
+            if t.dtype is not want:
+                raise ValueError(f"{name} must be {want} (got {t.dtype})")
+    dev = kc.get_device()
+    if dev < 0 or ks.get_device() != dev or vc.get_device() != dev or vs.get_device() != dev or not kc.is_cuda:
+        raise ValueError("the cache must be CUDA tensors on one device")
+    if not (kc.is_contiguous() and ks.is_contiguous() and vc.is_contiguous() and vs.is_contiguous()):
+        raise ValueError("the cache's tensors must be contiguous")
+    shape, scales = kc.shape, ks.shape
+    if len(shape) != 4 or vc.shape != shape or scales != shape[:3] or vs.shape != scales:
         raise ValueError(f"a cache is codes [num_pages, H, page_size, 128] and scales [num_pages, H, page_size] "
                          f"(got {tuple(kc.shape)}, {tuple(ks.shape)}, {tuple(vc.shape)}, {tuple(vs.shape)})")
-    if shape[3] != HEAD_DIM or shape[2] not in KV_PAGE_SIZES or shape[0] < 1 or shape[1] < 1:
+    pages, H, page, D = shape
+    if D != HEAD_DIM or page not in KV_PAGE_SIZES or pages < 1 or H < 1:
         raise ValueError(f"a cache has 128 channels and pages of {KV_PAGE_SIZES} tokens (got {tuple(shape)})")
-    return _KVCache(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), shape[0], shape[1], shape[2]), dev
+    return _KVCache(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), pages, H, page), dev
 
 
 def _check_rows(name, t, dev, H=None):
-    """bf16 [B, S, H, 128] whose tokens' heads are dense: (batch stride, token
-    stride) in elements."""
+    """bf16 [B, S, H, 128] whose tokens' heads are dense: the shape, batch stride
+    and token stride (in elements; 0 where there is one)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not _BF16:
         raise ValueError(f"{name} must be bfloat16 (got {t.dtype})")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on the cache's device {dev} (got {t.device})")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the cache's device cuda:{dev} (got {t.device})")
     shape = t.shape
     if len(shape) != 4 or shape[3] != HEAD_DIM or 0 in shape or (H is not None and shape[2] != H):
         raise ValueError(f"{name} must be [B, S, {'H' if H is None else H}, 128] (got {tuple(shape)})")
     sb, ss, sh, sd = t.stride()
     if sd != 1 or (sh != HEAD_DIM and shape[2] > 1):
         raise ValueError(f"the heads of a token of {name} must be dense (strides {t.stride()})")
-    return sb if shape[0] > 1 else 0, ss if shape[1] > 1 else 0
+    return shape, sb if shape[0] > 1 else 0, ss if shape[1] > 1 else 0
 
 
 def _check_table(table, B, dev, name="block_table"):
-    if table.dtype != torch.int32 or table.device != dev or table.dim() != 2 or table.shape[0] != B \
-            or table.shape[1] < 1 or table.stride(1) != 1 and table.shape[1] > 1:
-        raise ValueError(f"{name} must be an int32 [{B}, pages] tensor with dense rows on {dev}")
-    return table.shape[1], table.stride(0) if B > 1 else 0
+    shape = table.shape
+    if table.dtype is not _INT32 or table.get_device() != dev or len(shape) != 2 or shape[0] != B or shape[1] < 1:
+        raise ValueError(f"{name} must be an int32 [{B}, pages] tensor on cuda:{dev}")
+    sb, se = table.stride()
+    if se != 1 and shape[1] > 1:
+        raise ValueError(f"the rows of {name} must be dense")
+    return shape[1], sb if B > 1 else 0
 
 
 def _check_ints(name, t, n, dev):
-    if t.dtype != torch.int32 or t.device != dev or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor on {dev}")
+    if t.dtype is not _INT32 or t.get_device() != dev or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor on cuda:{dev}")
+
+
+def _call(fn, dev, *args):
+    """fn(*args, the current stream of device `dev`), with that device current."""
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        _check(status)
 
 
 def kv_cache_write(k, v, cache, block_table, start, count=None):
@@ -604,20 +627,19 @@ def kv_cache_write(k, v, cache, block_table, start, count=None):
     names the pages of each sequence, ``start`` int32 [B]; with ``count`` int32
     [B] only the first count[b] tokens of a padded sequence are written.
     Returns ``cache``."""
-    lib = load_library()
+    lib = _lib or load_library()
     c, dev = _check_cache(cache)
-    k_sb, k_ss = _check_rows("k", k, dev, c.H)
-    v_sb, v_ss = _check_rows("v", v, dev, c.H)
-    if k.shape != v.shape:
+    shape, k_sb, k_ss = _check_rows("k", k, dev, c.H)
+    v_shape, v_sb, v_ss = _check_rows("v", v, dev, c.H)
+    if shape != v_shape:
         raise ValueError(f"k and v must have equal shapes (got {tuple(k.shape)}, {tuple(v.shape)})")
-    B, S = k.shape[:2]
+    B, S = shape[0], shape[1]
     width, stride = _check_table(block_table, B, dev)
     _check_ints("start", start, B, dev)
     if count is not None:
         _check_ints("count", count, B, dev)
-    with torch.cuda.device(dev):
-        _check(lib.sage_kv_cache_write(ctypes.byref(c), _ptr(k), _ptr(v), k_sb, k_ss, v_sb, v_ss, B, S, HEAD_DIM,
-                                       _ptr(block_table), width, stride, _ptr(start), _ptr(count), _stream(dev)))
+    _call(lib.sage_kv_cache_write, dev, ctypes.byref(c), k.data_ptr(), v.data_ptr(), k_sb, k_ss, v_sb, v_ss, B, S,
+          HEAD_DIM, block_table.data_ptr(), width, stride, start.data_ptr(), None if count is None else count.data_ptr())
     return cache
 
 
@@ -625,24 +647,25 @@ def kv_cache_read(cache, block_table, lens, S: int, out=None):
     """The first S positions of each sequence in the cache as bf16 (k, v),
     each [B, S, H, 128], zeros from position lens[b] on (sage_kv_cache_read).
     ``out`` (optional) is the pair of tensors to fill."""
-    lib = load_library()
+    lib = _lib or load_library()
     c, dev = _check_cache(cache)
     if lens.dim() != 1:
         raise ValueError("lens must be an int32 [B] tensor")
-    B = lens.shape[0]
+    B, S = lens.shape[0], int(S)
     if B < 1 or S < 1:
         raise ValueError(f"B and S must be >= 1 (got {B}, {S})")
     width, stride = _check_table(block_table, B, dev)
     _check_ints("lens", lens, B, dev)
-    shape = (B, int(S), c.H, HEAD_DIM)
+    shape = (B, S, c.H, HEAD_DIM)
     if out is None:
-        out = (torch.empty(shape, dtype=torch.bfloat16, device=dev), torch.empty(shape, dtype=torch.bfloat16, device=dev))
-    for t in out:
-        if tuple(t.shape) != shape or t.dtype != torch.bfloat16 or t.device != dev or not t.is_contiguous():
-            raise ValueError(f"out must be two contiguous bf16 tensors {shape} on {dev}")
-    with torch.cuda.device(dev):
-        _check(lib.sage_kv_cache_read(ctypes.byref(c), _ptr(block_table), width, stride, _ptr(lens), _ptr(out[0]),
-                                      _ptr(out[1]), B, int(S), HEAD_DIM, _stream(dev)))
+        k = torch.empty(shape, dtype=_BF16, device=cache[0].device)
+        out = k, torch.empty_like(k)
+    else:
+        for t in out:
+            if t.shape != shape or t.dtype is not _BF16 or t.get_device() != dev or not t.is_contiguous():
+                raise ValueError(f"out must be two contiguous bf16 tensors {shape} on cuda:{dev}")
+    _call(lib.sage_kv_cache_read, dev, ctypes.byref(c), block_table.data_ptr(), width, stride, lens.data_ptr(),
+          out[0].data_ptr(), out[1].data_ptr(), B, S, HEAD_DIM)
     return out
 
 
@@ -651,10 +674,10 @@ def attn_fwd_cache_workspace_bytes(B: int, Sq: int, Hq: int, H: int, prefix_len:
 
 
 def _attn_fwd_cache(q, cache, prefix, block_table, lens, softmax_scale, causal, out, lse, return_lse, workspace):
-    lib = load_library()
+    lib = _lib or load_library()
     c, dev = _check_cache(cache)
-    q_sb, q_ss = _check_rows("q", q, dev)
-    B, Sq, Hq, D = q.shape
+    shape, q_sb, q_ss = _check_rows("q", q, dev)
+    B, Sq, Hq, D = shape
     if Hq % c.H:
         raise ValueError(f"q's heads ({Hq}) must be a multiple of the cache's ({c.H})")
     width, stride = _check_table(block_table, B, dev)
@@ -662,32 +685,30 @@ def _attn_fwd_cache(q, cache, prefix, block_table, lens, softmax_scale, causal, 
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty((B, Sq, Hq, D), dtype=torch.bfloat16, device=dev)
-    elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != dev:
+        out = torch.empty(shape, dtype=_BF16, device=q.device)
+    elif out.shape != shape or out.dtype is not _BF16 or not out.is_contiguous() or out.get_device() != dev:
         raise ValueError("out must be a contiguous bf16 tensor of q's shape on its device")
-    if lse is None and return_lse:
-        lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=dev)
-    elif lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq, Sq)
-                              or not lse.is_contiguous() or lse.device != dev):
+    if lse is None:
+        if return_lse:
+            lse = torch.empty((B, Hq, Sq), dtype=_FP32, device=q.device)
+    elif lse.dtype is not _FP32 or lse.shape != (B, Hq, Sq) or not lse.is_contiguous() or lse.get_device() != dev:
         raise ValueError("lse must be a contiguous float32 [B, Hq, Sq] tensor on q's device")
     ws_bytes = 0
     if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
+        if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on q's device")
         ws_bytes = workspace.numel() * workspace.element_size()
-    tail = (_ptr(block_table), width, stride, _ptr(lens), _ptr(out), _ptr(lse), B, Sq, Hq, D, float(softmax_scale),
-            int(bool(causal)), _ptr(workspace), ws_bytes)
-    with torch.cuda.device(dev):
-        if prefix is None:
-            _check(lib.sage_attn_fwd_cache(_ptr(q), q_sb, q_ss, ctypes.byref(c), *tail, _stream(dev)))
-        else:
-            table, length = prefix
-            if length < 1 or table.dim() != 1 or table.shape[0] < -(-length // c.page_size):
-                raise ValueError(f"prefix_table must name the pages of prefix_len >= 1 positions (got "
-                                 f"{tuple(table.shape)} for {length})")
-            _check_ints("prefix_table", table, table.shape[0], dev)
-            _check(lib.sage_attn_fwd_cache_prefix(_ptr(q), q_sb, q_ss, ctypes.byref(c), _ptr(table), length, *tail,
-                                                  _stream(dev)))
+    tail = (block_table.data_ptr(), width, stride, lens.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+            B, Sq, Hq, D, softmax_scale, 1 if causal else 0, None if workspace is None else workspace.data_ptr(), ws_bytes)
+    if prefix is None:
+        _call(lib.sage_attn_fwd_cache, dev, q.data_ptr(), q_sb, q_ss, ctypes.byref(c), *tail)
+    else:
+        table, length = prefix
+        if length < 1 or table.dim() != 1 or table.shape[0] < -(-length // c.page_size):
+            raise ValueError(f"prefix_table must name the pages of prefix_len >= 1 positions (got "
+                             f"{tuple(table.shape)} for {length})")
+        _check_ints("prefix_table", table, table.shape[0], dev)
+        _call(lib.sage_attn_fwd_cache_prefix, dev, q.data_ptr(), q_sb, q_ss, ctypes.byref(c), table.data_ptr(), length, *tail)
     return (out, lse) if lse is not None else out
 
 
