@@ -4,7 +4,7 @@
 //
 // The formulas are cache_attention.cu's with one change: the weights enter the
 // second product as bf16(2^(x_j - m) sv_j) with V's codes in bf16 (both exact
-// in range, a weight rounded by 2^-9 at the most), so that one exponential
+// in range, a weight rounded by 2^-8 at the most), so that one exponential
 // serves the sum and the product, M = m.
 //
 // A CTA owns 256 query rows of one unit and walks its key tiles of 128.  Its two
@@ -41,8 +41,8 @@ namespace {
 
 constexpr int kThreads = 20 * 32;
 // Registers of the five warpgroups: a launch of 640 threads has 96 each, and the
-// softmax needs 120.
-constexpr int kRegsConvert = 72, kRegsSoftmax = 120, kRegsIssue = 96;
+// softmax needs 128.
+constexpr int kRegsConvert = 72, kRegsSoftmax = 128, kRegsIssue = 80;
 static_assert(2 * kRegsConvert + 2 * kRegsSoftmax + kRegsIssue <= 5 * 96, "more registers than the launch has");
 constexpr uint32_t kHalf = 128 * 128;                   // 128 rows of 64 16-bit values
 constexpr uint32_t kTileBytes = 2 * kHalf;
@@ -110,27 +110,27 @@ __device__ __forceinline__ void store32(void* dst, uint32_t a, uint32_t b, uint3
 __device__ __forceinline__ void rescale(uint32_t tO, uint32_t tP, int chunks, bool has_o, float alpha) {
   if (has_o) {
 #pragma unroll 1
-    for (int k = 0; k < 4; ++k) {
-      uint32_t o[32];
-      tmem_ld32(tO + 32 * k, o);
+    for (int k = 0; k < 32; ++k) {
+      uint32_t o[4];
+      tmem_ld4(tO + 4 * k, o);
       tmem_ld_wait();
 #pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-      tmem_st32(tO + 32 * k, o);
+      for (int i = 0; i < 4; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+      tmem_st4(tO + 4 * k, o);
     }
   }
   tmem_st_wait();
 #pragma unroll 1
-  for (int k = 0; k < chunks; ++k) {
-    uint32_t w[16];
-    tmem_ld16(tP + 16 * k, w);
+  for (int k = 0; k < 4 * chunks; ++k) {
+    uint32_t w[4];
+    tmem_ld4(tP + 4 * k, w);
     tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < 4; ++i) {
       const float2 x = unpack_bf16(w[i]);
       w[i] = pack_bf16(x.x * alpha, x.y * alpha);
     }
-    tmem_st16(tP + 16 * k, w);
+    tmem_st4(tP + 4 * k, w);
   }
   tmem_st_wait();
 }
@@ -214,6 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
   __shared__ int s_len[kMaxBatch];
   __shared__ long long s_off[kPrefix ? 2 : kMaxBatch + 1];
   __shared__ __align__(16) float s_ks[kScaleSlots][kWideTok], s_vs[kScaleSlots][kWideTok];
+  __shared__ volatile long long s_end, s_per;
   __shared__ float2 s_half[128];                          // m and L of half 1's rows
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -252,6 +253,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
   const long long total = s_off[walk.seqs()] * p.cache.H;
   const long long per = div_floor(total + gridDim.x - 1, gridDim.x);
   const long long f0 = blockIdx.x * per, f1 = min(total, f0 + per);
+  if (threadIdx.x == 8 * 32) {                          // kept here for walk.tell, to save registers
+    s_end = f1;
+    s_per = per;
+  }
   if (!p.keep && threadIdx.x == 0) p.desc[blockIdx.x].w = 0;
   if (f0 < f1) {
     Place x = walk.locate(f0, static_cast<int>(f1 - f0));
@@ -524,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
           }
           tc_fence_before();                               // O may be written again
         }
-        if (warp == 8 && lane == 0) walk.tell(x, f1, per);
+        if (warp == 8 && lane == 0) walk.tell(x, s_end, s_per);
         it += n;
         walk.next(x);
       }
