@@ -18,17 +18,19 @@
 //   warps 4-7    the same for V's codes, to bf16 (exact)
 //   warps 8-11   softmax of half 0, one thread a row
 //   warps 12-15  the same for half 1
-//   warp 16      one thread issues S_t = Q_t K^T and O_t += P_t V; warps 17-19
-//                only give registers to the softmax
+//   warps 16-19  one thread each issues S_0 = Q_0 K^T, S_1 = Q_1 K^T, O_0 += P_0 V,
+//                O_1 += P_1 V
 //
-// TMEM (512 columns): S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512).  P_t
-// (bf16, two to a column) takes the first 64 columns of S_t, each 32 scores'
-// weights over columns that have been read before, and is the product's A
-// operand from there; V is its B operand with the keys as the outer index, as
-// the cache has it.
+// TMEM (512 columns): two buffers of 64 scores for each half, [0,64) and [64,128)
+// of half 0, [128,192) and [192,256) of half 1, then O0 [256,384) O1 [384,512).
+// The scores of a half's next 64 keys are formed while its softmax has the last
+// 64 in hand.  The weights (bf16, two to a column) take the first 32 columns of
+// their scores' buffer, each 32 over columns that have been read before, and are
+// the second product's A operand from there; V is its B operand with the keys as
+// the outer index, as the cache has it.
 //
 // A row's reference m moves where the sum of 32 weights passes 2^12: then the
-// thread scales the row's sum, its accumulator and the weights of this tile that
+// thread scales the row's sum, its accumulator and the weights of this buffer that
 // it has stored already, and forms the 32 again.  bf16 weights keep their
 // precision at any size, so m need not be near the largest score.
 #include <cuda_bf16.h>
@@ -53,12 +55,14 @@ constexpr uint32_t kSmemBytes = 6 * kTileBytes + 1024;  // and room to align to 
 constexpr int kScaleSlots = 4;                          // of ks and vs: up to three tiles ahead of the softmax
 constexpr float kFar = 4096.0f;                         // 2^12: most of 32 weights' sum
 
-__host__ __device__ constexpr uint32_t col_s(int t) { return 128u * t; }
+constexpr int kSub = 64;                                // keys of a score buffer
+__host__ __device__ constexpr uint32_t col_s(int t, int b) { return 128u * t + 64u * b; }
 __host__ __device__ constexpr uint32_t col_o(int t) { return 256u + 128u * t; }
 
 struct Barriers {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], scales[kScaleSlots];
-  uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], half_full, half_read, drain;
+  uint64_t q_full[2], half_full, half_read, drain[4];
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];   // [half][buffer]
 };
 
 template <int N>
@@ -135,16 +139,16 @@ __device__ __forceinline__ void rescale(uint32_t tO, uint32_t tP, int chunks, bo
   tmem_st_wait();
 }
 
-// One row's 128 scores of a tile (TMEM columns tS ..) to weights over them, 32 at a
+// One row's 64 scores of a buffer (TMEM columns tS ..) to weights over them, 32 at a
 // time.  kx, vx: the keys' scales (K's times softmax_scale * log2 e); rk: the row's
-// factor; key0: the tile's first key, of which the row sees those below lim
+// factor; key0: the first key, of which the row sees those below lim
 // (kCut: not all).  before(): waits for the accumulator's last product.
 template <bool kCut, typename Before>
 __device__ __forceinline__ bool softmax_tile(uint32_t tS, uint32_t tO, const float* kx, const float* vx, float rk, int key0,
                                              int lim, bool has_o, float& m, float2& l, Before before) {
   bool ok = true;
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < kSub / 32; ++c) {
     uint32_t a[32];
     tmem_ld32(tS + 32 * c, a);
     tmem_ld_wait();
@@ -226,18 +230,20 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
   if (threadIdx.x == 32) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars.k_full[s], 128);
-      mbar_init(&bars.k_empty[s], 1);
+      mbar_init(&bars.k_empty[s], 2);
       mbar_init(&bars.v_full[s], 128);
-      mbar_init(&bars.v_empty[s], 1);
+      mbar_init(&bars.v_empty[s], 2);
       mbar_init(&bars.q_full[s], 128);
-      mbar_init(&bars.s_full[s], 1);
-      mbar_init(&bars.p_full[s], 128);
-      mbar_init(&bars.pv_done[s], 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&bars.s_full[s][b], 1);
+        mbar_init(&bars.p_full[s][b], 128);
+        mbar_init(&bars.pv_done[s][b], 1);
+      }
     }
     for (int s = 0; s < kScaleSlots; ++s) mbar_init(&bars.scales[s], 256);
     mbar_init(&bars.half_full, 128);
     mbar_init(&bars.half_read, 128);
-    mbar_init(&bars.drain, 1);
+    for (int s = 0; s < 4; ++s) mbar_init(&bars.drain[s], 1);
     abort_flag = 0;
     fence_mbarrier_init();
   }
@@ -386,10 +392,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
       const int quarter = warp & 3;                        // TMEM lanes of this warp
       const int trow = quarter * 32 + lane;
       const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-      const uint32_t tS = tmem + lanes + col_s(t), tO = tmem + lanes + col_o(t);
+      const uint32_t tO = tmem + lanes + col_o(t);
       float* exchange = reinterpret_cast<float*>(smem + kSmemQ + kTileBytes) + trow;   // [channel][row], 64 channels
       int it = 0;                                          // key tiles of this CTA
-      uint32_t done = 0, joined = 0;                       // tiles and exchanges of this half
+      uint32_t done = 0, joined = 0;                       // score buffers (an even number) and exchanges of this half
       bool ok = true;
       while (x.left > 0 && ok) {
         const int hi = walk.keys(x.b, x.rt);
@@ -430,30 +436,31 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
 
           float m = kLowest;
           float2 l = make_float2(0.0f, 0.0f);
-          bool has_o = false;
-          auto before = [&]() {                            // the product of this half's last tile has ended
-            const bool r2 = __all_sync(0xFFFFFFFFu, wait(&bars.pv_done[t], done - 1));
+          int v = 0;                                       // of this half's nv score buffers
+          const int nv = 2 * (by_rows ? n : (n - t + 1) / 2);
+          auto before = [&]() {                            // the product of buffer v - 1 has ended
+            const bool r2 = __all_sync(0xFFFFFFFFu, wait(&bars.pv_done[t][(v - 1) & 1], (done + v - 1) >> 1));
             tc_fence_after();
             return r2;
           };
-          for (int j = by_rows ? 0 : t; j < n; j += by_rows ? 1 : 2) {
-            const int slot = (it + j) % kScaleSlots;
-            ok = wait(&bars.scales[slot], (it + j) / kScaleSlots) && wait(&bars.s_full[t], done);
+          for (v = 0; v < nv; ++v) {
+            const int j = by_rows ? v >> 1 : (v & ~1) + t, slot = (it + j) % kScaleSlots, sub = (v & 1) * kSub;
+            ok = wait(&bars.scales[slot], (it + j) / kScaleSlots) && wait(&bars.s_full[t][v & 1], (done + v) >> 1);
             if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
             tc_fence_after();
-            const int key0 = (x.t0 + j) * kWideTok;
-            if (key0 + kWideTok > lo)                      // warp-uniform
-              ok = softmax_tile<true>(tS, tO, s_ks[slot], s_vs[slot], rk, key0, lim, has_o, m, l, before);
+            const uint32_t tS = tmem + lanes + col_s(t, 0) + sub;
+            const int key0 = (x.t0 + j) * kWideTok + sub;
+            if (key0 + kSub > lo)                          // warp-uniform
+              ok = softmax_tile<true>(tS, tO, s_ks[slot] + sub, s_vs[slot] + sub, rk, key0, lim, v > 0, m, l, before);
             else
-              ok = softmax_tile<false>(tS, tO, s_ks[slot], s_vs[slot], rk, key0, lim, has_o, m, l, before);
+              ok = softmax_tile<false>(tS, tO, s_ks[slot] + sub, s_vs[slot] + sub, rk, key0, lim, v > 0, m, l, before);
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(&bars.p_full[t]);
-            ++done;
-            has_o = true;
+            mbar_arrive(&bars.p_full[t][v & 1]);
           }
           ok = ok && before();
           if (!ok) break;
+          done += nv;
           float L = l.x + l.y;
           const bool join = !by_rows && n > 1;
           if (join && t == 1) {
@@ -535,69 +542,75 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
       }
     } else {
       fewer_registers<kRegsIssue>();
-      if (warp == 16 && lane == 0) {
-      // -------------------------------------------------------------- issue --
-      constexpr uint32_t kIdescQK = make_idesc_f32acc(128, 128, 0, 0);                   // F16 x F16
-      constexpr uint32_t kIdescPV = make_idesc_f32acc(128, 128, 1, 1) | (1u << 16);      // BF16 x BF16, B's outer index summed
-      const uint32_t q_lo = sw128_desc_lo(smem_addr(smem + kSmemQ)), k_lo = sw128_desc_lo(smem_addr(smem + kSmemK));
-      // V: 64-channel halves kHalf bytes apart, groups of eight keys 1024.
-      const uint32_t v_lo = sw128_desc_lo(smem_addr(smem + kSmemV)) | ((kHalf >> 4) << 16);
-      int it = 0;
-      uint32_t pv[2] = {0u, 0u}, seg[2] = {0u, 0u};        // products P V of each half, segments of each Q tile
-      bool ok = true;
-      auto qk = [&](int t, int qt, int g) {                // S_t of key tile g, Q tile qt
-        const uint32_t a0 = q_lo + qt * (kTileBytes >> 4), b0 = k_lo + (g & 1) * (kTileBytes >> 4);
+      if (lane == 0) {
+        // ------------------------------------------------------------ issue --
+        // One thread for each product of each half, so that none waits for
+        // another's operands.  Buffer v of half t: 64 keys, v & 1 of key tile v / 2,
+        // or of key tile 2 (v / 2) + t.
+        const int t = warp & 1;
+        const bool is_pv = warp >= 18;
+        constexpr uint32_t kIdescQK = make_idesc_f32acc(128, kSub, 0, 0);                  // F16 x F16
+        constexpr uint32_t kIdescPV = make_idesc_f32acc(128, 128, 1, 1) | (1u << 16);      // BF16 x BF16, B's outer index summed
+        const uint32_t q_lo = sw128_desc_lo(smem_addr(smem + kSmemQ));
+        const uint32_t k_lo = sw128_desc_lo(smem_addr(smem + kSmemK));
+        // V: 64-channel halves kHalf bytes apart, groups of eight keys 1024.
+        const uint32_t v_lo = sw128_desc_lo(smem_addr(smem + kSmemV)) | ((kHalf >> 4) << 16);
+        uint64_t* full = is_pv ? bars.v_full : bars.k_full;
+        uint64_t* empty = is_pv ? bars.v_empty : bars.k_empty;
+        int it = 0;
+        uint32_t done = 0, seg0 = 0, seg1 = 0;             // score buffers of this half; segments, and those by rows
+        bool ok = true;
+#pragma unroll 1
+        while (x.left > 0 && ok) {
+          const int n = x.t1 - x.t0;
+          const bool by_rows = p.rows - x.rt * kWideRows > 128;
+          const int qt = by_rows ? t : 0;
+          if (!is_pv) ok = wait(&bars.q_full[qt], qt == 0 ? seg0 : seg1);
+          ++seg0;
+          seg1 += by_rows;
+#pragma unroll 1
+          for (int j = 0; j < n && ok; ++j) {
+            const int g = it + j, s = g & 1;
+            if (!(ok = wait(&full[s], g >> 1))) break;
+            if (!by_rows && (j & 1) != t) {                // the other half's tile
+              mbar_arrive(&empty[s]);
+              continue;
+            }
+#pragma unroll 1
+            for (int sub = 0; sub < 2; ++sub, ++done) {
+              const uint32_t buf = tmem + col_s(t, 0) + sub * kSub;
+              if (is_pv) {
+                if (!(ok = wait(&bars.p_full[t][sub], done >> 1))) break;
+                tc_fence_after();
+                const uint32_t b0 = v_lo + s * (kTileBytes >> 4) + sub * (kSub * 128 >> 4);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-          mma_f16_ss(tmem + col_s(t), a0 + off, b0 + off, kIdescQK, k > 0);
-        }
-        mma_commit(&bars.s_full[t]);
-      };
-      auto pv_of = [&](int t, int g, bool first) {
-        const uint32_t b0 = v_lo + (g & 1) * (kTileBytes >> 4);
+                for (int k = 0; k < kSub / 16; ++k)
+                  mma_f16_ts(tmem + col_o(t), buf + 8 * k, b0 + k * (2048 >> 4), kSw128DescHi, kIdescPV,
+                             j > 1 || (by_rows && j > 0) || sub > 0 || k > 0);
+                mma_commit(&bars.pv_done[t][sub]);
+              } else {
+                // The buffer's last weights have been used.
+                if (done >= 2 && !(ok = wait(&bars.pv_done[t][sub], (done - 2) >> 1))) break;
+                tc_fence_after();
+                const uint32_t a0 = q_lo + qt * (kTileBytes >> 4);
+                const uint32_t b0 = k_lo + s * (kTileBytes >> 4) + sub * (kSub * 128 >> 4);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_f16_ts(tmem + col_o(t), tmem + col_s(t) + 8 * k, b0 + k * (2048 >> 4), kSw128DescHi, kIdescPV, !first || k > 0);
-        mma_commit(&bars.pv_done[t]);
-        ++pv[t];
-      };
-      while (x.left > 0 && ok) {
-        const int n = x.t1 - x.t0;
-        const bool by_rows = p.rows - x.rt * kWideRows > 128;
-        // Step i: half t = i % 2 of key tile j = i / 2, or key tile i in half i % 2.
-        // The scores of step i + 2 follow the weighted sum of step i, whose weights
-        // stand in their columns.
-        const int steps = by_rows ? 2 * n : n;
-        auto scores = [&](int i) {
-          const int t = i & 1, g = it + (by_rows ? i >> 1 : i);
-          if (!by_rows || t == 0) ok = ok && wait(&bars.k_full[g & 1], g >> 1);
-          if (i < 2 && (by_rows || t == 0)) ok = ok && wait(&bars.q_full[t], seg[t]++);
-          if (i >= 2) ok = ok && wait(&bars.pv_done[t], pv[t] - 1);
-          if (!ok) return;
-          tc_fence_after();
-          qk(t, by_rows ? t : 0, g);
-          if (!by_rows || t == 1) mma_commit(&bars.k_empty[g & 1]);
-        };
-        scores(0);
-        if (steps > 1) scores(1);
-        for (int i = 0; i < steps && ok; ++i) {
-          const int t = i & 1, g = it + (by_rows ? i >> 1 : i);
-          if (!by_rows || t == 0) ok = ok && wait(&bars.v_full[g & 1], g >> 1);
-          ok = ok && wait(&bars.p_full[t], pv[t]);
-          if (!ok) break;
-          tc_fence_after();
-          pv_of(t, g, i < 2);
-          if (!by_rows || t == 1) mma_commit(&bars.v_empty[g & 1]);
-          if (i + 2 < steps) scores(i + 2);
+                for (int k = 0; k < 8; ++k) {
+                  const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+                  mma_f16_ss(buf, a0 + off, b0 + off, kIdescQK, k > 0);
+                }
+                mma_commit(&bars.s_full[t][sub]);
+              }
+            }
+            mma_commit(&empty[s]);
+          }
+          it += n;
+          walk.next(x);
         }
-        it += n;
-        walk.next(x);
-      }
-      // Every product has to end before TMEM can be released.
-      mma_commit(&bars.drain);
-      int local_abort = 0;
-      (void)mbar_wait_inline(&bars.drain, 0, &local_abort, p.err, p.timeout_ns);
+        // Every product has to end before TMEM can be released.
+        mma_commit(&bars.drain[warp - 16]);
+        int local_abort = 0;
+        (void)mbar_wait_inline(&bars.drain[warp - 16], 0, &local_abort, p.err, p.timeout_ns);
       }
     }
   }
