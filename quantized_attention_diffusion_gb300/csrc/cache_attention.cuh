@@ -108,6 +108,11 @@ struct Walk {
     x.b = lo;
     x.rt = 0;
     x.n = tiles(lo, 0);
+    if constexpr (kPrefix) {             // all row tiles see the same keys
+      const long long each = static_cast<long long>(x.n + Cost) * p.cache.H;
+      x.rt = static_cast<int>(div_floor(rem, each));
+      rem -= x.rt * each;
+    }
     while (rem >= static_cast<long long>(x.n + Cost) * p.cache.H) {
       rem -= static_cast<long long>(x.n + Cost) * p.cache.H;
       x.n = tiles(lo, ++x.rt);
@@ -147,10 +152,8 @@ struct Walk {
     if constexpr (kPrefix) {
       for (int i = threadIdx.x; i < p.B; i += blockDim.x) len[i] = max(0, min(p.room, __ldg(p.lens + i)));
       if (threadIdx.x == 0) {
-        long long n = 0;
-        for (int rt = 0; rt < p.row_tiles; ++rt) n += tiles(0, rt) + Cost;
         off[0] = 0;
-        off[1] = n;
+        off[1] = static_cast<long long>(p.row_tiles) * (tiles(0, 0) + Cost);
       }
     } else if (threadIdx.x < 32) {
       const int lane = threadIdx.x;

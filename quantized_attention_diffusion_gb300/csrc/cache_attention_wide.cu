@@ -2,10 +2,14 @@
 // rows to a key/value head (a shared prefix, a chunk of new tokens), on the
 // tcgen05 tensor cores (sm_103a).
 //
-// The formulas are cache_attention.cu's with one change: the weights enter the
-// second product as bf16(2^(x_j - m) sv_j) with V's codes in bf16 (both exact
-// in range, a weight rounded by 2^-8 at the most), so that one exponential
-// serves the sum and the product, M = m.
+// The formulas are cache_attention.cu's with one change: the second product is that
+// of bf16(2^(x_j - m)) and bf16(sv_j vc_j), each rounded by 2^-8 at the most (the
+// values are those that reading the cache back gives; bf16 has the range of both),
+// so that one exponential serves the sum and the product, M = m, and V's scales
+// cost the softmax nothing: a load of a scale that all rows need takes shared
+// memory as long as 128 bytes do, and that path is what bounds this kernel.  The sum L
+// is of the weights before they are rounded.  A scale of V that is not finite stays
+// with the weights, since a row that does not see its key must not meet it.
 //
 // A CTA owns 256 query rows of one unit and walks its key tiles of 128.  Its two
 // halves are two row tiles of 128, or, where a unit has at most 128 rows, the even
@@ -15,11 +19,11 @@
 //   warps 0-3    read K's codes from global memory, convert them to fp16 (exact)
 //                and store them swizzled, two stages; keys behind the last are
 //                stored as zeros
-//   warps 4-7    the same for V's codes, to bf16 (exact)
+//   warps 4-7    the same for V's codes, times their scales to bf16
 //   warps 8-11   softmax of half 0, one thread a row
 //   warps 12-15  the same for half 1
 //   warps 16-19  one thread each issues S_0 = Q_0 K^T, S_1 = Q_1 K^T, O_0 += P_0 V,
-//                O_1 += P_1 V
+//                O_1 += P_1 V; what it has to know of a tile stands beside the stage
 //
 // TMEM (512 columns): two buffers of 64 scores for each half, [0,64) and [64,128)
 // of half 0, [128,192) and [192,256) of half 1, then O0 [256,384) O1 [384,512).
@@ -29,10 +33,10 @@
 // the second product's A operand from there; V is its B operand with the keys as
 // the outer index, as the cache has it.
 //
-// A row's reference m moves where the sum of 32 weights passes 2^12: then the
-// thread scales the row's sum, its accumulator and the weights of this buffer that
-// it has stored already, and forms the 32 again.  bf16 weights keep their
-// precision at any size, so m need not be near the largest score.
+// A row's reference m moves where the sum of a buffer's weights passes 2^12: then
+// the thread scales the row's sum and its accumulator and forms the weights again.
+// bf16 weights keep their precision at any size, so m need not be near the largest
+// score.
 #include <cuda_bf16.h>
 
 #include "cache_attention.cuh"
@@ -44,7 +48,7 @@ namespace {
 constexpr int kThreads = 20 * 32;
 // Registers of the five warpgroups: a launch of 640 threads has 96 each, and the
 // softmax needs 128.
-constexpr int kRegsConvert = 72, kRegsSoftmax = 128, kRegsIssue = 80;
+constexpr int kRegsConvert = 88, kRegsSoftmax = 128, kRegsIssue = 48;
 static_assert(2 * kRegsConvert + 2 * kRegsSoftmax + kRegsIssue <= 5 * 96, "more registers than the launch has");
 constexpr uint32_t kHalf = 128 * 128;                   // 128 rows of 64 16-bit values
 constexpr uint32_t kTileBytes = 2 * kHalf;
@@ -53,15 +57,22 @@ constexpr uint32_t kSmemK = 2 * kTileBytes;             // two stages
 constexpr uint32_t kSmemV = 4 * kTileBytes;             // two stages
 constexpr uint32_t kSmemBytes = 6 * kTileBytes + 1024;  // and room to align to 1024
 constexpr int kScaleSlots = 4;                          // of ks and vs: up to three tiles ahead of the softmax
-constexpr float kFar = 4096.0f;                         // 2^12: most of 32 weights' sum
+constexpr float kFar = 4096.0f;                         // 2^12: most of 64 weights' sum
 
 constexpr int kSub = 64;                                // keys of a score buffer
 __host__ __device__ constexpr uint32_t col_s(int t, int b) { return 128u * t + 64u * b; }
 __host__ __device__ constexpr uint32_t col_o(int t) { return 256u + 128u * t; }
 
+// What the issuing threads know of a stage's tile.
+constexpr int kTileOf = 3;        // 0, 1 or 2: the segment's first tile, its second, a later one
+constexpr int kTileOdd = 4;       // an odd tile of its segment
+constexpr int kTileByRows = 8;    // the halves are row tiles
+constexpr int kTileMore = 16;     // the segment has more than one tile
+constexpr int kTileEnd = 32;      // no tile: the CTA has no more
+
 struct Barriers {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], scales[kScaleSlots];
-  uint64_t q_full[2], half_full, half_read, drain[4];
+  uint64_t q_full[3], half_full, half_read, drain[4];     // of Q tile 0, of 1, and of 0 for half 1
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];   // [half][buffer]
 };
 
@@ -80,21 +91,37 @@ __device__ __forceinline__ uint32_t tile_offset(int r, int c) {
   return (c >> 3) * kHalf + (r >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
-// Four E4M3 codes -> two pairs of bf16.  A byte s eeee mmm, its sign spread over
-// the half word above it, shifted by four and masked, is the bf16 of exponent
-// field eeee and mantissa mmm0000; times 2^120 that is the code's value,
-// subnormals included.
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
+// 16 bytes that are read once: no line of L1 for them.
+__device__ __forceinline__ uint4 load_once(const uint8_t* src) {
+  uint4 w;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "l"(src));
+  return w;
 }
-__device__ __forceinline__ void v_codes_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  constexpr uint32_t kTwo120 = 0x7B807B80u;
-  asm("prmt.b32 %0, %1, %1, 0x9180;" : "=r"(lo) : "r"(w));   // selector bit 3: the byte's sign, eight times
-  asm("prmt.b32 %0, %1, %1, 0xB3A2;" : "=r"(hi) : "r"(w));
-  lo = mul_bf16x2((lo << 4) & 0x87F087F0u, kTwo120);
-  hi = mul_bf16x2((hi << 4) & 0x87F087F0u, kTwo120);
+
+// Four E4M3 codes times a scale, in fp32, each rounded to bf16.
+__device__ __forceinline__ void v_values_bf16(uint32_t w, float scale, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t"
+      ".reg .b16 l, h, a, b, c, d;\n\t"
+      ".reg .b32 p, q;\n\t"
+      ".reg .f32 x, y, z, w;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 p, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 q, h;\n\t"
+      "mov.b32 {a, b}, p;\n\t"
+      "mov.b32 {c, d}, q;\n\t"
+      "cvt.f32.f16 x, a;\n\t"
+      "cvt.f32.f16 y, b;\n\t"
+      "cvt.f32.f16 z, c;\n\t"
+      "cvt.f32.f16 w, d;\n\t"
+      "mul.rn.f32 x, x, %3;\n\t"
+      "mul.rn.f32 y, y, %3;\n\t"
+      "mul.rn.f32 z, z, %3;\n\t"
+      "mul.rn.f32 w, w, %3;\n\t"
+      "cvt.rn.bf16x2.f32 %0, y, x;\n\t"
+      "cvt.rn.bf16x2.f32 %1, w, z;\n\t"
+      "}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w), "f"(scale));
 }
 
 __device__ __forceinline__ float2 unpack_bf16(uint32_t w) {
@@ -173,14 +200,16 @@ __device__ __forceinline__ bool softmax_tile(uint32_t tS, uint32_t tO, const flo
       sum = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float4 s4 = reinterpret_cast<const float4*>(vx)[c * 8 + i];
         const float2 x0 = ffma2_bc(y[2 * i].x, y[2 * i].y, rk, -m), x1 = ffma2_bc(y[2 * i + 1].x, y[2 * i + 1].y, rk, -m);
         const float2 p0 = make_float2(ex2_approx(x0.x), ex2_approx(x0.y));
         const float2 p1 = make_float2(ex2_approx(x1.x), ex2_approx(x1.y));
         sum = fadd2v(sum, p0);
         sum = fadd2v(sum, p1);
-        float2 w0 = fmul2v(p0, make_float2(s4.x, s4.y)), w1 = fmul2v(p1, make_float2(s4.z, s4.w));
+        float2 w0 = p0, w1 = p1;
         if constexpr (kCut) {                            // a scale that is not finite stays behind the limit
+          const float4 s4 = reinterpret_cast<const float4*>(vx)[c * 8 + i];
+          w0 = fmul2v(p0, make_float2(s4.x, s4.y));
+          w1 = fmul2v(p1, make_float2(s4.z, s4.w));
           if (4 * i >= left) w0.x = 0.0f;
           if (4 * i + 1 >= left) w0.y = 0.0f;
           if (4 * i + 2 >= left) w1.x = 0.0f;
@@ -193,7 +222,8 @@ __device__ __forceinline__ bool softmax_tile(uint32_t tS, uint32_t tO, const flo
       float mx = fmaxf(y[0].x, y[0].y);
 #pragma unroll
       for (int i = 1; i < 16; ++i) mx = fmax3(mx, y[i].x, y[i].y);
-      const float to = fmaxf(m, mx * rk), alpha = ex2_approx(m - to);
+      const float to = sum.x + sum.y > kFar ? fmaxf(m, mx * rk) : m;   // a row's result is its own alone
+      const float alpha = ex2_approx(m - to);
       const bool still = !__any_sync(0xFFFFFFFFu, to != m);   // an infinite score: no reference helps
       l.x *= alpha;
       l.y *= alpha;
@@ -218,6 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
   __shared__ int s_len[kMaxBatch];
   __shared__ long long s_off[kPrefix ? 2 : kMaxBatch + 1];
   __shared__ __align__(16) float s_ks[kScaleSlots][kWideTok], s_vs[kScaleSlots][kWideTok];
+  __shared__ __align__(16) int s_odd[kScaleSlots][4];     // of a V warp's keys some have a scale that is not finite
+  __shared__ int s_info[2][2];                            // [K, V][stage]
   __shared__ volatile long long s_end, s_per;
   __shared__ float2 s_half[128];                          // m and L of half 1's rows
 
@@ -233,13 +265,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
       mbar_init(&bars.k_empty[s], 2);
       mbar_init(&bars.v_full[s], 128);
       mbar_init(&bars.v_empty[s], 2);
-      mbar_init(&bars.q_full[s], 128);
       for (int b = 0; b < 2; ++b) {
         mbar_init(&bars.s_full[s][b], 1);
         mbar_init(&bars.p_full[s][b], 128);
         mbar_init(&bars.pv_done[s][b], 1);
       }
     }
+    for (int s = 0; s < 3; ++s) mbar_init(&bars.q_full[s], 128);
     for (int s = 0; s < kScaleSlots; ++s) mbar_init(&bars.scales[s], 256);
     mbar_init(&bars.half_full, 128);
     mbar_init(&bars.half_read, 128);
@@ -279,6 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
       const int tid = threadIdx.x & 127;
       const int sub = 4 * (warp & 3) + ((lane >> 2) & 1) + 2 * (lane >> 4);   // key of a step
       const int q16 = (lane & 3) + ((lane >> 3) & 1) * 4;                     // 16 codes of a key
+      const int scale_key = is_v ? 16 * (lane >> 2) + 4 * (warp & 3) + (lane & 3) : tid;   // the key whose scale it loads
       const int ps = p.cache.page_shift;
       const uint8_t* codes = (is_v ? p.cache.v_codes : p.cache.k_codes) + q16 * 16;
       const float* scales = is_v ? p.cache.v_scale : p.cache.k_scale;
@@ -289,12 +322,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
       bool bad = false;
       // The tile whose codes are loaded next: its keys' page (lane i: of step i), head and bounds.
       int page = -1, head = 0, t0 = 0, hi = 0;
-      int tile = x.t0;
+      int tile = x.t0, info = 0, info_next = 0;
       bool more = true, loaded = false;   // tiles to ask for; codes that wait to be converted
       auto ask = [&]() {
         page = -1;
         more = x.left > 0;
         if (!more) return;
+        const int j = tile - x.t0;
+        info_next = min(j, 2) | ((j & 1) != 0 ? kTileOdd : 0) | (p.rows - x.rt * kWideRows > 128 ? kTileByRows : 0) |
+                    (x.t1 - x.t0 > 1 ? kTileMore : 0);
         head = x.h;
         t0 = tile * kWideTok;
         hi = walk.keys(x.b, x.rt);
@@ -311,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
       float scale = 0.0f;
       auto load = [&]() {
         loaded = more;
+        info = info_next;
         if (!more) return;
         const bool gone = page < 0 || page >= p.cache.num_pages;
         const bool mine = lane < 8 && t0 + 16 * lane < hi;
@@ -324,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
             const int pg = __shfl_sync(0xFFFFFFFFu, page, i), t = t0 + 16 * i;
             row = codes + static_cast<int64_t>(((pg * p.cache.H + head) << ps) + (t & ((1 << ps) - 1)) + sub) * kHeadDim;
             w[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (pg >= 0 && t + sub < hi) w[i] = __ldg(reinterpret_cast<const uint4*>(row));
+            if (pg >= 0 && t + sub < hi) w[i] = load_once(row);
           }
         } else {
 #pragma unroll
@@ -333,10 +370,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
               const int pg = __shfl_sync(0xFFFFFFFFu, page, i);
               row = codes + static_cast<int64_t>(((pg * p.cache.H + head) << ps) + (i == 0 ? t0 & ((1 << ps) - 1) : 0) + sub - 16 * i) * kHeadDim;
             }
-            w[i] = __ldg(reinterpret_cast<const uint4*>(row + i * 16 * kHeadDim));
+            w[i] = load_once(row + i * 16 * kHeadDim);
           }
         }
-        const int pg = __shfl_sync(0xFFFFFFFFu, page, tid >> 4), t = t0 + tid;
+        const int pg = __shfl_sync(0xFFFFFFFFu, page, scale_key >> 4), t = t0 + scale_key;
         scale = 0.0f;
         if (pg >= 0 && t < hi) scale = __ldg(scales + (((pg * p.cache.H + head) << ps) + (t & ((1 << ps) - 1))));
       };
@@ -349,7 +386,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
         // V's scales may be written before its stage is free: the tile that last
         // used the slot has been multiplied.
         if (is_v) {
-          s_vs[it % kScaleSlots][tid] = scale;
+          const bool odd_scale = !(fabsf(scale) < INFINITY);
+          s_vs[it % kScaleSlots][scale_key] = odd_scale ? scale : 1.0f;
+          if (odd_scale) scale = 1.0f;
+          const bool some = __any_sync(0xFFFFFFFFu, odd_scale);
+          if (lane == 0) s_odd[it % kScaleSlots][warp & 3] = some;
           mbar_arrive(&bars.scales[it % kScaleSlots]);
         }
         if (round > 0 && !__all_sync(0xFFFFFFFFu, wait(&empty[s], round - 1))) break;
@@ -357,11 +398,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
         if (is_v) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
+            const float sv = __shfl_sync(0xFFFFFFFFu, scale, 4 * i + (sub & 3));
             uint32_t o[8];
-            v_codes_bf16(w[i].x, o[0], o[1]);
-            v_codes_bf16(w[i].y, o[2], o[3]);
-            v_codes_bf16(w[i].z, o[4], o[5]);
-            v_codes_bf16(w[i].w, o[6], o[7]);
+            v_values_bf16(w[i].x, sv, o[0], o[1]);
+            v_values_bf16(w[i].y, sv, o[2], o[3]);
+            v_values_bf16(w[i].z, sv, o[4], o[5]);
+            v_values_bf16(w[i].w, sv, o[6], o[7]);
             *reinterpret_cast<uint4*>(to + i * 2048) = make_uint4(o[0], o[1], o[2], o[3]);
             *reinterpret_cast<uint4*>(to + i * 2048 + static_cast<int>(odd)) = make_uint4(o[4], o[5], o[6], o[7]);
           }
@@ -379,10 +421,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
             *reinterpret_cast<uint4*>(to + i * 2048 + static_cast<int>(odd)) = make_uint4(o[4], o[5], o[6], o[7]);
           }
         }
+        if (tid == 0) s_info[is_v][s] = info;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         mbar_arrive(&full[s]);
         load();
         ask();
+      }
+      if (!loaded && (it < 2 || __all_sync(0xFFFFFFFFu, wait(&empty[it & 1], (it >> 1) - 1)))) {
+        if (tid == 0) s_info[is_v][it & 1] = kTileEnd;
+        mbar_arrive(&full[it & 1]);
       }
       if (bad) atomicExch(p.err, SAGE_DEVERR_BAD_PAGE);
     } else if (warp < 16) {
@@ -407,31 +454,51 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
           const bool valid = r < rows;
           const int lim = valid ? min(hi, walk.limit(x.b, rr)) : hi;
           const int lo = __reduce_min_sync(0xFFFFFFFFu, lim);
-          // This thread's query row: fp16 times a power of two.
-          uint32_t top = 0u;
-          const uint16_t* src = walk.query(x, valid ? rr : x.rt * kWideRows);
-#pragma unroll 4
-          for (int i = 0; i < 16; ++i) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(src) + i);
-            const uint32_t a = max((w.x & 0x7FFFu), (w.x >> 16) & 0x7FFFu), b = max((w.y & 0x7FFFu), (w.y >> 16) & 0x7FFFu);
-            const uint32_t d = max((w.z & 0x7FFFu), (w.z >> 16) & 0x7FFFu), e = max((w.w & 0x7FFFu), (w.w >> 16) & 0x7FFFu);
-            top = max(top, max(max(a, b), max(d, e)));
-          }
-          const uint32_t ex = row_exponent(top);
-          const float rk = __uint_as_float((254u - ex) << 23);
-          if (by_rows || t == 0) {
-            const float up = valid ? __uint_as_float(ex << 23) : 0.0f;
-            uint8_t* sQ = smem + kSmemQ + t * kTileBytes;
-#pragma unroll 4
-            for (int i = 0; i < 16; ++i) {
-              const uint4 w = __ldg(reinterpret_cast<const uint4*>(src) + i);
-              const float2 a = unpack_bf16(w.x), b = unpack_bf16(w.y), d = unpack_bf16(w.z), e = unpack_bf16(w.w);
-              *reinterpret_cast<uint4*>(sQ + tile_offset(trow, i)) =
-                  make_uint4(pack_f16(a.x * up, a.y * up), pack_f16(b.x * up, b.y * up), pack_f16(d.x * up, d.y * up),
-                             pack_f16(e.x * up, e.y * up));
+          // The warp's query rows, two at a time, 8 channels a lane: fp16 times a power
+          // of two.  Thread `lane` keeps its row's factor.
+          float rk = 0.0f;
+          {
+            const bool store = by_rows || t == 0;
+            const int pair = lane >> 4, chunk = lane & 15;
+            const uint64_t own = valid ? reinterpret_cast<uint64_t>(walk.query(x, rr)) : 0;
+            uint8_t* sQ = smem + kSmemQ + (by_rows ? t * kTileBytes : 0);
+#pragma unroll 1
+            for (int i0 = 0; i0 < 32; i0 += 16) {
+              uint4 w[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint64_t src = __shfl_sync(0xFFFFFFFFu, own, i0 + 2 * i + pair);
+                w[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (src != 0) w[i] = __ldg(reinterpret_cast<const uint4*>(src) + chunk);
+              }
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                uint32_t top = 0u, out[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top = max(top, max(u[k] & 0x7FFFu, (u[k] >> 16) & 0x7FFFu));
+#pragma unroll
+                for (int d = 1; d < 16; d <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                const uint32_t ex = row_exponent(top);
+                const float up = __uint_as_float(ex << 23), back = __uint_as_float((254u - ex) << 23);
+                const float mine = __shfl_sync(0xFFFFFFFFu, back, (lane & 1) << 4);
+                if (lane >> 1 == (i0 >> 1) + i) rk = mine;
+                if (store) {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const float2 a = unpack_bf16(u[k]);
+                    out[k] = pack_f16(a.x * up, a.y * up);
+                  }
+                  *reinterpret_cast<uint4*>(sQ + tile_offset(quarter * 32 + i0 + 2 * i + pair, chunk)) =
+                      make_uint4(out[0], out[1], out[2], out[3]);
+                }
+              }
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            mbar_arrive(&bars.q_full[t]);
+            if (store) {
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              mbar_arrive(&bars.q_full[t]);
+              if (!by_rows && n > 1) mbar_arrive(&bars.q_full[2]);
+            }
           }
 
           float m = kLowest;
@@ -450,7 +517,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
             tc_fence_after();
             const uint32_t tS = tmem + lanes + col_s(t, 0) + sub;
             const int key0 = (x.t0 + j) * kWideTok + sub;
-            if (key0 + kSub > lo)                          // warp-uniform
+            const int4 odd = *reinterpret_cast<const int4*>(s_odd[slot]);
+            if (key0 + kSub > lo || (odd.x | odd.y | odd.z | odd.w) != 0)   // warp-uniform
               ok = softmax_tile<true>(tS, tO, s_ks[slot] + sub, s_vs[slot] + sub, rk, key0, lim, v > 0, m, l, before);
             else
               ok = softmax_tile<false>(tS, tO, s_ks[slot] + sub, s_vs[slot] + sub, rk, key0, lim, v > 0, m, l, before);
@@ -540,6 +608,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
         it += n;
         walk.next(x);
       }
+      // After a wait that gave up: the merge kernel reads every unit's entry.
+      if (warp == 8 && lane == 0) {
+        for (; x.left > 0; walk.next(x)) walk.tell(x, s_end, s_per);
+      }
     } else {
       fewer_registers<kRegsIssue>();
       if (lane == 0) {
@@ -557,55 +629,63 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
         const uint32_t v_lo = sw128_desc_lo(smem_addr(smem + kSmemV)) | ((kHalf >> 4) << 16);
         uint64_t* full = is_pv ? bars.v_full : bars.k_full;
         uint64_t* empty = is_pv ? bars.v_empty : bars.k_empty;
-        int it = 0;
-        uint32_t done = 0, seg0 = 0, seg1 = 0;             // score buffers of this half; segments, and those by rows
-        bool ok = true;
+        const int* info = s_info[is_pv];
+        uint32_t done = 0, seen = 0, seen_odd = 0;         // score buffers of this half; its Q tiles, by rows and not
 #pragma unroll 1
-        while (x.left > 0 && ok) {
-          const int n = x.t1 - x.t0;
-          const bool by_rows = p.rows - x.rt * kWideRows > 128;
-          const int qt = by_rows ? t : 0;
-          if (!is_pv) ok = wait(&bars.q_full[qt], qt == 0 ? seg0 : seg1);
-          ++seg0;
-          seg1 += by_rows;
-#pragma unroll 1
-          for (int j = 0; j < n && ok; ++j) {
-            const int g = it + j, s = g & 1;
-            if (!(ok = wait(&full[s], g >> 1))) break;
-            if (!by_rows && (j & 1) != t) {                // the other half's tile
-              mbar_arrive(&empty[s]);
-              continue;
-            }
-#pragma unroll 1
-            for (int sub = 0; sub < 2; ++sub, ++done) {
-              const uint32_t buf = tmem + col_s(t, 0) + sub * kSub;
-              if (is_pv) {
-                if (!(ok = wait(&bars.p_full[t][sub], done >> 1))) break;
-                tc_fence_after();
-                const uint32_t b0 = v_lo + s * (kTileBytes >> 4) + sub * (kSub * 128 >> 4);
-#pragma unroll
-                for (int k = 0; k < kSub / 16; ++k)
-                  mma_f16_ts(tmem + col_o(t), buf + 8 * k, b0 + k * (2048 >> 4), kSw128DescHi, kIdescPV,
-                             j > 1 || (by_rows && j > 0) || sub > 0 || k > 0);
-                mma_commit(&bars.pv_done[t][sub]);
-              } else {
-                // The buffer's last weights have been used.
-                if (done >= 2 && !(ok = wait(&bars.pv_done[t][sub], (done - 2) >> 1))) break;
-                tc_fence_after();
-                const uint32_t a0 = q_lo + qt * (kTileBytes >> 4);
-                const uint32_t b0 = k_lo + s * (kTileBytes >> 4) + sub * (kSub * 128 >> 4);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-                  mma_f16_ss(buf, a0 + off, b0 + off, kIdescQK, k > 0);
-                }
-                mma_commit(&bars.s_full[t][sub]);
-              }
-            }
-            mma_commit(&empty[s]);
+        for (int g = 0;; ++g) {
+          const int s = g & 1;
+          if (!wait(&full[s], g >> 1)) break;
+          const int tile = *const_cast<const volatile int*>(&info[s]);
+          if ((tile & kTileEnd) != 0) break;
+          const bool by_rows = (tile & kTileByRows) != 0;
+          // Each of Q's barriers is waited for by one thread in every one of its phases,
+          // so that it is never two phases ahead of that thread.
+          if (!is_pv && (tile & kTileOf) == 0) {
+            bool ok = true;
+            if (t == 0)
+              ok = wait(&bars.q_full[0], seen++);
+            else if (by_rows)
+              ok = wait(&bars.q_full[1], seen++);
+            else if ((tile & kTileMore) != 0)
+              ok = wait(&bars.q_full[2], seen_odd++);
+            if (!ok) break;
           }
-          it += n;
-          walk.next(x);
+          if (!by_rows && ((tile & kTileOdd) != 0) != (t == 1)) {   // the other half's tile
+            // A run of segments of one tile frees K's stages without half 1: its
+            // softmax must not fall behind the scales.
+            if (!is_pv && (tile & kTileMore) == 0 && done > 0 && !wait(&bars.pv_done[t][(done - 1) & 1], (done - 1) >> 1)) break;
+            mbar_arrive(&empty[s]);
+            continue;
+          }
+          const bool fresh = (tile & kTileOf) == 0 || (!by_rows && (tile & kTileOf) == 1);   // this half's first
+          bool ok = true;
+#pragma unroll 1
+          for (int sub = 0; sub < 2; ++sub, ++done) {
+            const uint32_t buf = tmem + col_s(t, 0) + sub * kSub;
+            if (is_pv) {
+              if (!(ok = wait(&bars.p_full[t][sub], done >> 1))) break;
+              tc_fence_after();
+              const uint32_t b0 = v_lo + s * (kTileBytes >> 4) + sub * (kSub * 128 >> 4);
+#pragma unroll
+              for (int k = 0; k < kSub / 16; ++k)
+                mma_f16_ts(tmem + col_o(t), buf + 8 * k, b0 + k * (2048 >> 4), kSw128DescHi, kIdescPV, !fresh || sub > 0 || k > 0);
+              mma_commit(&bars.pv_done[t][sub]);
+            } else {
+              // The buffer's last weights have been used.
+              if (done >= 2 && !(ok = wait(&bars.pv_done[t][sub], (done - 2) >> 1))) break;
+              tc_fence_after();
+              const uint32_t a0 = q_lo + (by_rows ? t : 0) * (kTileBytes >> 4);
+              const uint32_t b0 = k_lo + s * (kTileBytes >> 4) + sub * (kSub * 128 >> 4);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+                mma_f16_ss(buf, a0 + off, b0 + off, kIdescQK, k > 0);
+              }
+              mma_commit(&bars.s_full[t][sub]);
+            }
+          }
+          if (!ok) break;
+          mma_commit(&empty[s]);
         }
         // Every product has to end before TMEM can be released.
         mma_commit(&bars.drain[warp - 16]);

@@ -98,8 +98,10 @@ def reference(q, rows, causal, scale, weight=2.0 ** -11):
                dx <= 264 u X, and a running maximum near x costs one rounding
                more of |x|: 2 u X
       weights  ex2.approx: 2^-22 relative; `weight`: a rounding of 2^-11 to fp16,
-               or 2^-25 of the largest weight times scale if smaller (of 2^-8
-               to bf16 where a key/value head has many rows); log2 of the
+               or 2^-25 of the largest weight times scale if smaller (where a
+               key/value head has many rows the weight and the value times its
+               scale are rounded to bf16, 2^-8 each: (1 + 2^-8)^2 - 1 = 2^-7 + 2^-16
+               for their product); log2 of the
                scale: 2^-22 absolute and a rounding of |x| + |log2 sv|
       sums     fp32, n keys: n 2u of the sum of magnitudes at the most
       out      one rounding to bf16: 2^-8 of |out|
