@@ -46,7 +46,7 @@ __host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : nt 
 // Tiles in flight: 9, 8 or 8 on an SM, 135 KB or more.
 __host__ __device__ constexpr int stages_of(int nt) { return nt == 1 ? 3 : nt == 2 ? 4 : 8; }
 constexpr uint32_t smem_of(int nt) { return stages_of(nt) * kStageBytes + kMergeBytes + 8 * nt * kHeadDim * 2; }
-constexpr float kFar = 256.0f;                            // 2^8: weights stay below it (fp16: 65504)
+constexpr float kFar = 256.0f, kFarLog2 = 8.0f;           // weights stay near or below it (fp16: 65504)
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -165,6 +165,10 @@ __device__ __forceinline__ void attend(QueryRows<NT>& z, const uint8_t* st, int 
         for (int d = 4; d < 32; d <<= 1) {
           mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
           wx = fmaxf(wx, __shfl_xor_sync(0xFFFFFFFFu, wx, d));
+        }
+        if (!(mx - z.m[a][e] > kFarLog2 || wx - z.mw[a][e] > kFarLog2)) {   // a row's result is its own alone
+          mx = z.m[a][e];
+          wx = z.mw[a][e];
         }
         z.l[a][e] *= ex2_approx(z.m[a][e] - mx);
         alpha[e] = ex2_approx(z.mw[a][e] - wx);
@@ -721,6 +725,18 @@ size_t cache_attn_workspace_bytes(int B, int Sq, int Hq, int Hkv, int prefix_len
   Layout w = layout(rows, b, Hkv, both, 0);
   if (both) w = layout(b * rows, 1, Hkv, true, w.end);
   return w.end;
+}
+
+bool cache_attn_fits(int B, int Sq, int Hq, int Hkv, int page_size, int table_width, int prefix_len) {
+  const auto fits = [](int64_t keys, int64_t rows, int64_t seqs, int64_t H) {
+    const int R = rows_per_tile(static_cast<int>(rows));
+    const int64_t tiles = (keys + keys_per_tile(R) - 1) / keys_per_tile(R) + unit_cost(R);   // of a unit, at most 2^25
+    const int64_t units = seqs * ((rows + R - 1) / R) * H;                                   // at most 2^31
+    return tiles * units / max_ctas(R) < INT_MAX;
+  };
+  const int64_t b = std::min(B, kMaxBatch), rows = static_cast<int64_t>(Sq) * (Hq / Hkv);
+  return fits(std::min<int64_t>(kMaxCacheLen, static_cast<int64_t>(table_width) * page_size), rows, b, Hkv) &&
+         (prefix_len == 0 || fits(prefix_len, b * rows, 1, Hkv));
 }
 
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream) {

@@ -382,6 +382,8 @@ sage_status run_cache_attention(const void* q, int64_t q_sb, int64_t q_ss, const
     s = fail(SAGE_ERR_INVALID_ARG, "Hq = %d is not a multiple of the cache's H = %d", Hq, cache->H);
   if (s == SAGE_OK && static_cast<int64_t>(B) * Hq > INT_MAX / Sq)
     s = fail(SAGE_ERR_INVALID_ARG, "B*Sq*Hq exceeds 2^31-1");
+  if (s == SAGE_OK && !cache_attn_fits(B, Sq, Hq, cache->H, cache->page_size, width, prefix_len))
+    s = fail(SAGE_ERR_INVALID_ARG, "B = %d, Sq = %d, Hq = %d over tables of %d pages is too much for one call", B, Sq, Hq, width);
   if (s == SAGE_OK) s = check_scale(softmax_scale);
   if (s == SAGE_OK) s = check_ptrs({{q, "q"}, {out, "out"}});
   if (s == SAGE_OK) s = check_strides(q_sb, q_ss, "q");

@@ -147,6 +147,9 @@ struct CacheAttnArgs {
   int* err;
 };
 size_t cache_attn_workspace_bytes(int B, int Sq, int Hq, int Hkv, int prefix_len);
+// Whether a CTA's share of the work, for the longest sequences that the table has
+// room for, is counted in 31 bits.
+bool cache_attn_fits(int B, int Sq, int Hq, int Hkv, int page_size, int table_width, int prefix_len);
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream);
 
 // cudaFuncSetAttribute for `kernel`'s dynamic shared memory, once on each device:

@@ -136,3 +136,11 @@ def test_binding_refuses():
         qad.kv_cache_read(c[:3], table, lens, 1)
     with pytest.raises(ValueError, match="k_codes must be"):
         qad.kv_cache_read((c[0].float(),) + c[1:], table, lens, 1)
+
+
+def test_attention_refuses_more_than_a_launch_counts(lib):
+    # 2^23 units of 2^23 tiles of keys: no CTA's share fits 31 bits
+    big = dict(c=cache(H=128), B=256, Sq=65535, Hq=128, width=(1 << 31) - 1)
+    assert attn(lib, **big) == INVALID and b"too much for one call" in lib.sage_last_error()
+    assert attn(lib, **dict(big, width=1), prefix=(FAKE, 1 << 30)) == INVALID
+    assert b"too much for one call" in lib.sage_last_error()
