@@ -2,14 +2,12 @@
 // rows to a key/value head (a shared prefix, a chunk of new tokens), on the
 // tcgen05 tensor cores (sm_103a).
 //
-// The formulas are cache_attention.cu's with one change: the second product is that
-// of bf16(2^(x_j - m)) and bf16(sv_j vc_j), each rounded by 2^-8 at the most (the
-// values are those that reading the cache back gives; bf16 has the range of both),
-// so that one exponential serves the sum and the product, M = m, and V's scales
-// cost the softmax nothing: a load of a scale that all rows need takes shared
-// memory as long as 128 bytes do, and that path is what bounds this kernel.  The sum L
-// is of the weights before they are rounded.  A scale of V that is not finite stays
-// with the weights, since a row that does not see its key must not meet it.
+// The formulas are cache_attention.cu's with one exponential a score: p = 2^(x - R)
+// serves the sum L, in fp32, and, times the key's scale of V and rounded to fp16, the
+// second product.  R is near the largest x + log2 sv so far, but at most 60 from the
+// largest x; where V's scales are farther, a row's weights take a factor
+// f = 2^(R - M) more (1 otherwise) and its accumulator stands relative to M.  R and M
+// are whole numbers.  V's codes are exact in fp16.
 //
 // A CTA owns 256 query rows of one unit and walks its key tiles of 128.  Its two
 // halves are two row tiles of 128, or, where a unit has at most 128 rows, the even
@@ -19,7 +17,7 @@
 //   warps 0-3    read K's codes from global memory, convert them to fp16 (exact)
 //                and store them swizzled, two stages; keys behind the last are
 //                stored as zeros
-//   warps 4-7    the same for V's codes, times their scales to bf16
+//   warps 4-7    the same for V's codes, with the largest of their scales
 //   warps 8-11   softmax of half 0, one thread a row
 //   warps 12-15  the same for half 1
 //   warps 16-19  one thread each issues S_0 = Q_0 K^T, S_1 = Q_1 K^T, O_0 += P_0 V,
@@ -28,16 +26,17 @@
 // TMEM (512 columns): two buffers of 64 scores for each half, [0,64) and [64,128)
 // of half 0, [128,192) and [192,256) of half 1, then O0 [256,384) O1 [384,512).
 // The scores of a half's next 64 keys are formed while its softmax has the last
-// 64 in hand.  The weights (bf16, two to a column) take the first 32 columns of
+// 64 in hand.  The weights (fp16, two to a column) take the first 32 columns of
 // their scores' buffer, each 32 over columns that have been read before, and are
 // the second product's A operand from there; V is its B operand with the keys as
 // the outer index, as the cache has it.
 //
-// A row's reference m moves where the sum of a buffer's weights passes 2^12: then
-// the thread scales the row's sum and its accumulator and forms the weights again.
-// bf16 weights keep their precision at any size, so m need not be near the largest
-// score.
+// A row's references move where 32 weights may pass 2^14 in sum, by a whole number:
+// then the thread scales the row's sum, its accumulator and the weights of this
+// buffer that it has stored already by a power of two, which is exact, and forms
+// the 32 again.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "cache_attention.cuh"
 
@@ -48,7 +47,7 @@ namespace {
 constexpr int kThreads = 20 * 32;
 // Registers of the five warpgroups: a launch of 640 threads has 96 each, and the
 // softmax needs 128.
-constexpr int kRegsConvert = 88, kRegsSoftmax = 128, kRegsIssue = 48;
+constexpr int kRegsConvert = 88, kRegsSoftmax = 120, kRegsIssue = 64;
 static_assert(2 * kRegsConvert + 2 * kRegsSoftmax + kRegsIssue <= 5 * 96, "more registers than the launch has");
 constexpr uint32_t kHalf = 128 * 128;                   // 128 rows of 64 16-bit values
 constexpr uint32_t kTileBytes = 2 * kHalf;
@@ -57,7 +56,9 @@ constexpr uint32_t kSmemK = 2 * kTileBytes;             // two stages
 constexpr uint32_t kSmemV = 4 * kTileBytes;             // two stages
 constexpr uint32_t kSmemBytes = 6 * kTileBytes + 1024;  // and room to align to 1024
 constexpr int kScaleSlots = 4;                          // of ks and vs: up to three tiles ahead of the softmax
-constexpr float kFar = 4096.0f;                         // 2^12: most of 64 weights' sum
+constexpr float kFar = 16384.0f;                        // 2^14: most of 32 weights' sum (fp16: 65504)
+constexpr float kFarSum = 0x1p70f, kTiny = 0x1p-56f;    // most of 32 p's sum, and kFar / kFarSum
+constexpr float kReach = 60.0f, kReachV = 140.0f;       // of R, and of M, below the largest score
 
 constexpr int kSub = 64;                                // keys of a score buffer
 __host__ __device__ constexpr uint32_t col_s(int t, int b) { return 128u * t + 64u * b; }
@@ -98,30 +99,11 @@ __device__ __forceinline__ uint4 load_once(const uint8_t* src) {
   return w;
 }
 
-// Four E4M3 codes times a scale, in fp32, each rounded to bf16.
-__device__ __forceinline__ void v_values_bf16(uint32_t w, float scale, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t"
-      ".reg .b16 l, h, a, b, c, d;\n\t"
-      ".reg .b32 p, q;\n\t"
-      ".reg .f32 x, y, z, w;\n\t"
-      "mov.b32 {l, h}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 p, l;\n\t"
-      "cvt.rn.f16x2.e4m3x2 q, h;\n\t"
-      "mov.b32 {a, b}, p;\n\t"
-      "mov.b32 {c, d}, q;\n\t"
-      "cvt.f32.f16 x, a;\n\t"
-      "cvt.f32.f16 y, b;\n\t"
-      "cvt.f32.f16 z, c;\n\t"
-      "cvt.f32.f16 w, d;\n\t"
-      "mul.rn.f32 x, x, %3;\n\t"
-      "mul.rn.f32 y, y, %3;\n\t"
-      "mul.rn.f32 z, z, %3;\n\t"
-      "mul.rn.f32 w, w, %3;\n\t"
-      "cvt.rn.bf16x2.f32 %0, y, x;\n\t"
-      "cvt.rn.bf16x2.f32 %1, w, z;\n\t"
-      "}"
+// Four E4M3 codes -> two pairs of fp16, exactly.
+__device__ __forceinline__ void v_codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
       : "=r"(lo), "=r"(hi)
-      : "r"(w), "f"(scale));
+      : "r"(w));
 }
 
 __device__ __forceinline__ float2 unpack_bf16(uint32_t w) {
@@ -135,10 +117,55 @@ __device__ __forceinline__ void store32(void* dst, uint32_t a, uint32_t b, uint3
                : "memory");
 }
 
-// The rare move of a row's reference: alpha = 2^(old - new) of this thread's row
-// times the accumulator (if it holds anything yet) and the weights of the tile's
-// first `chunks` chunks.  All lanes of a warp together.
-__device__ __forceinline__ void rescale(uint32_t tO, uint32_t tP, int chunks, bool has_o, float alpha) {
+// What a thread knows of its row.
+struct Row {
+  float rk;                  // its factor
+  float R, M, f;             // references of L and of the accumulator, f = 2^(R - M)
+  float2 l;                  // L in two parts
+};
+
+// 2^n for a whole n of at most 127, 0 below the range.
+__device__ __forceinline__ float power_of_two(float n) {
+  return n < -126.0f ? 0.0f : __int_as_float((127 + static_cast<int>(n)) << 23);
+}
+
+// The rare move of a row's references to its largest score and weight so far, in
+// the 32 scores at tS of which it sees `left`; -> whether they moved, and the
+// accumulator's factor.
+__device__ __forceinline__ bool move_references(uint32_t tS, const float* kx, const float* vx, int left, bool far, Row& z,
+                                                float& alpha) {
+  float xm = -INFINITY, ym = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < 32; c += 16) {
+    uint32_t a[16];
+    tmem_ld16(tS + c, a);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float x = c + i < left ? __uint_as_float(a[i]) * kx[c + i] * z.rk : -INFINITY;
+      xm = fmaxf(xm, x);
+      ym = fmaxf(ym, x + lg2_approx(vx[c + i]));
+    }
+  }
+  float R = z.R, M = z.M;
+  if (far) {                                               // a row's result is its own alone
+    M = fmaxf(M, ceilf(fmaxf(ym, xm - kReachV)));
+    R = fmaxf(R, fminf(fmaxf(M, ceilf(xm) - kReach), ceilf(xm) + kReach));
+  }
+  const bool moved = R != z.R || M != z.M;
+  const float less = power_of_two(z.R - R);
+  alpha = power_of_two(z.M - M);
+  z.l.x *= less;
+  z.l.y *= less;
+  z.R = R;
+  z.M = M;
+  z.f = power_of_two(R - M);
+  return moved;
+}
+
+// The accumulator times alpha, of this thread's row (if it holds anything yet), and
+// the buffer's first 32 weights if they are there.  All lanes of a warp together.
+__device__ __forceinline__ void rescale(uint32_t tO, uint32_t tP, bool has_o, bool has_p, float alpha) {
   if (has_o) {
 #pragma unroll 1
     for (int k = 0; k < 32; ++k) {
@@ -151,91 +178,63 @@ __device__ __forceinline__ void rescale(uint32_t tO, uint32_t tP, int chunks, bo
     }
   }
   tmem_st_wait();
+  if (has_p) {
 #pragma unroll 1
-  for (int k = 0; k < 4 * chunks; ++k) {
-    uint32_t w[4];
-    tmem_ld4(tP + 4 * k, w);
-    tmem_ld_wait();
+    for (int k = 0; k < 4; ++k) {
+      uint32_t w[4];
+      tmem_ld4(tP + 4 * k, w);
+      tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 x = unpack_bf16(w[i]);
-      w[i] = pack_bf16(x.x * alpha, x.y * alpha);
+      for (int i = 0; i < 4; ++i) {
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        w[i] = pack_f16(x.x * alpha, x.y * alpha);
+      }
+      tmem_st4(tP + 4 * k, w);
     }
-    tmem_st4(tP + 4 * k, w);
   }
   tmem_st_wait();
 }
 
-// One row's 64 scores of a buffer (TMEM columns tS ..) to weights over them, 32 at a
-// time.  kx, vx: the keys' scales (K's times softmax_scale * log2 e); rk: the row's
-// factor; key0: the first key, of which the row sees those below lim
-// (kCut: not all).  before(): waits for the accumulator's last product.
-template <bool kCut, typename Before>
-__device__ __forceinline__ bool softmax_tile(uint32_t tS, uint32_t tO, const float* kx, const float* vx, float rk, int key0,
-                                             int lim, bool has_o, float& m, float2& l, Before before) {
-  bool ok = true;
-#pragma unroll 1
-  for (int c = 0; c < kSub / 32; ++c) {
-    uint32_t a[32];
-    tmem_ld32(tS + 32 * c, a);
-    tmem_ld_wait();
-    float2 y[16];
+// 32 of a row's scores (TMEM columns tS ..) to weights, and the sum of the p's.
+// kx, vx: the keys' scales (K's times softmax_scale * log2 e); top: at least V's
+// largest; left: keys of these that the row sees.  kSlow: not all, or a scale is not
+// finite, or a row's f is not 1.  -> whether the references have to move.
+template <bool kSlow>
+__device__ __forceinline__ bool weigh(uint32_t tS, const float* kx, const float* vx, float top, int left, const Row& z,
+                                      uint32_t (&w)[16], float2& sum) {
+  uint32_t a[32];
+  tmem_ld32(tS, a);
+  tmem_ld_wait();
+  sum = make_float2(0.0f, 0.0f);
+  float2 sumw = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float4 s4 = reinterpret_cast<const float4*>(kx)[c * 8 + i];
-      y[2 * i] = fmul2v(make_float2(__uint_as_float(a[4 * i]), __uint_as_float(a[4 * i + 1])), make_float2(s4.x, s4.y));
-      y[2 * i + 1] = fmul2v(make_float2(__uint_as_float(a[4 * i + 2]), __uint_as_float(a[4 * i + 3])), make_float2(s4.z, s4.w));
-    }
-    const int left = lim - key0 - 32 * c;                // keys of these that the row sees
-    if constexpr (kCut) {
+  for (int i = 0; i < 8; ++i) {
+    const float4 k4 = reinterpret_cast<const float4*>(kx)[i], v4 = reinterpret_cast<const float4*>(vx)[i];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        if (2 * i >= left) y[i].x = -INFINITY;
-        if (2 * i + 1 >= left) y[i].y = -INFINITY;
+    for (int e = 0; e < 2; ++e) {
+      const int at = 4 * i + 2 * e;
+      const float2 k2 = e == 0 ? make_float2(k4.x, k4.y) : make_float2(k4.z, k4.w);
+      float2 v2 = e == 0 ? make_float2(v4.x, v4.y) : make_float2(v4.z, v4.w);
+      const float2 y = fmul2v(make_float2(__uint_as_float(a[at]), __uint_as_float(a[at + 1])), k2);
+      float2 x = ffma2_bc(y.x, y.y, z.rk, -z.R);
+      if constexpr (kSlow) {
+        if (at >= left) x.x = -INFINITY;
+        if (at + 1 >= left) x.y = -INFINITY;
+        v2 = fmul2v(v2, make_float2(z.f, z.f));
       }
-    }
-    uint32_t w[16];
-    float2 sum;
-    while (true) {
-      sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 x0 = ffma2_bc(y[2 * i].x, y[2 * i].y, rk, -m), x1 = ffma2_bc(y[2 * i + 1].x, y[2 * i + 1].y, rk, -m);
-        const float2 p0 = make_float2(ex2_approx(x0.x), ex2_approx(x0.y));
-        const float2 p1 = make_float2(ex2_approx(x1.x), ex2_approx(x1.y));
-        sum = fadd2v(sum, p0);
-        sum = fadd2v(sum, p1);
-        float2 w0 = p0, w1 = p1;
-        if constexpr (kCut) {                            // a scale that is not finite stays behind the limit
-          const float4 s4 = reinterpret_cast<const float4*>(vx)[c * 8 + i];
-          w0 = fmul2v(p0, make_float2(s4.x, s4.y));
-          w1 = fmul2v(p1, make_float2(s4.z, s4.w));
-          if (4 * i >= left) w0.x = 0.0f;
-          if (4 * i + 1 >= left) w0.y = 0.0f;
-          if (4 * i + 2 >= left) w1.x = 0.0f;
-          if (4 * i + 3 >= left) w1.y = 0.0f;
-        }
-        w[2 * i] = pack_bf16(w0.x, w0.y);
-        w[2 * i + 1] = pack_bf16(w1.x, w1.y);
+      const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+      sum = fadd2v(sum, p);
+      float2 q = fmul2v(p, v2);
+      if constexpr (kSlow) {                               // a scale that is not finite stays behind the limit
+        if (at >= left) q.x = 0.0f;
+        if (at + 1 >= left) q.y = 0.0f;
+        sumw = fadd2v(sumw, q);
       }
-      if (!__any_sync(0xFFFFFFFFu, sum.x + sum.y > kFar)) break;
-      float mx = fmaxf(y[0].x, y[0].y);
-#pragma unroll
-      for (int i = 1; i < 16; ++i) mx = fmax3(mx, y[i].x, y[i].y);
-      const float to = sum.x + sum.y > kFar ? fmaxf(m, mx * rk) : m;   // a row's result is its own alone
-      const float alpha = ex2_approx(m - to);
-      const bool still = !__any_sync(0xFFFFFFFFu, to != m);   // an infinite score: no reference helps
-      l.x *= alpha;
-      l.y *= alpha;
-      m = to;
-      if (has_o) ok = ok && before();
-      if (ok) rescale(tO, tS, c, has_o, alpha);
-      if (still) break;
+      w[at / 2] = pack_f16(q.x, q.y);
     }
-    l = fadd2v(l, sum);
-    tmem_st16(tS + 16 * c, w);
   }
-  return ok;
+  const float total = sum.x + sum.y;
+  return kSlow ? total > kFarSum || !(sumw.x + sumw.y <= kFar) : total * top > kFar;
 }
 
 template <bool kPrefix>
@@ -248,10 +247,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
   __shared__ int s_len[kMaxBatch];
   __shared__ long long s_off[kPrefix ? 2 : kMaxBatch + 1];
   __shared__ __align__(16) float s_ks[kScaleSlots][kWideTok], s_vs[kScaleSlots][kWideTok];
-  __shared__ __align__(16) int s_odd[kScaleSlots][4];     // of a V warp's keys some have a scale that is not finite
+  __shared__ __align__(16) float s_top[kScaleSlots][4];   // of a V warp's keys: the largest scale, or infinity
   __shared__ int s_info[2][2];                            // [K, V][stage]
   __shared__ volatile long long s_end, s_per;
-  __shared__ float2 s_half[128];                          // m and L of half 1's rows
+  __shared__ float4 s_half[128];                          // R, L and M of half 1's rows
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_v = &abort_flag;
@@ -386,11 +385,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
         // V's scales may be written before its stage is free: the tile that last
         // used the slot has been multiplied.
         if (is_v) {
-          const bool odd_scale = !(fabsf(scale) < INFINITY);
-          s_vs[it % kScaleSlots][scale_key] = odd_scale ? scale : 1.0f;
-          if (odd_scale) scale = 1.0f;
-          const bool some = __any_sync(0xFFFFFFFFu, odd_scale);
-          if (lane == 0) s_odd[it % kScaleSlots][warp & 3] = some;
+          s_vs[it % kScaleSlots][scale_key] = scale;
+          // Magnitudes compare as integers, infinities and NaN above all others.
+          const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(scale) & 0x7FFFFFFFu);
+          if (lane == 0) s_top[it % kScaleSlots][warp & 3] = __uint_as_float(min(top, 0x7F800000u));
           mbar_arrive(&bars.scales[it % kScaleSlots]);
         }
         if (round > 0 && !__all_sync(0xFFFFFFFFu, wait(&empty[s], round - 1))) break;
@@ -398,12 +396,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
         if (is_v) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float sv = __shfl_sync(0xFFFFFFFFu, scale, 4 * i + (sub & 3));
             uint32_t o[8];
-            v_values_bf16(w[i].x, sv, o[0], o[1]);
-            v_values_bf16(w[i].y, sv, o[2], o[3]);
-            v_values_bf16(w[i].z, sv, o[4], o[5]);
-            v_values_bf16(w[i].w, sv, o[6], o[7]);
+            v_codes_f16(w[i].x, o[0], o[1]);
+            v_codes_f16(w[i].y, o[2], o[3]);
+            v_codes_f16(w[i].z, o[4], o[5]);
+            v_codes_f16(w[i].w, o[6], o[7]);
             *reinterpret_cast<uint4*>(to + i * 2048) = make_uint4(o[0], o[1], o[2], o[3]);
             *reinterpret_cast<uint4*>(to + i * 2048 + static_cast<int>(odd)) = make_uint4(o[4], o[5], o[6], o[7]);
           }
@@ -456,7 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
           const int lo = __reduce_min_sync(0xFFFFFFFFu, lim);
           // The warp's query rows, two at a time, 8 channels a lane: fp16 times a power
           // of two.  Thread `lane` keeps its row's factor.
-          float rk = 0.0f;
+          Row z;
+          z.rk = 0.0f;
           {
             const bool store = by_rows || t == 0;
             const int pair = lane >> 4, chunk = lane & 15;
@@ -482,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
                 const uint32_t ex = row_exponent(top);
                 const float up = __uint_as_float(ex << 23), back = __uint_as_float((254u - ex) << 23);
                 const float mine = __shfl_sync(0xFFFFFFFFu, back, (lane & 1) << 4);
-                if (lane >> 1 == (i0 >> 1) + i) rk = mine;
+                if (lane >> 1 == (i0 >> 1) + i) z.rk = mine;
                 if (store) {
 #pragma unroll
                   for (int k = 0; k < 4; ++k) {
@@ -501,8 +499,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
             }
           }
 
-          float m = kLowest;
-          float2 l = make_float2(0.0f, 0.0f);
+          z.R = z.M = kLowest;
+          z.f = 1.0f;
+          z.l = make_float2(0.0f, 0.0f);
           int v = 0;                                       // of this half's nv score buffers
           const int nv = 2 * (by_rows ? n : (n - t + 1) / 2);
           auto before = [&]() {                            // the product of buffer v - 1 has ended
@@ -517,11 +516,31 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
             tc_fence_after();
             const uint32_t tS = tmem + lanes + col_s(t, 0) + sub;
             const int key0 = (x.t0 + j) * kWideTok + sub;
-            const int4 odd = *reinterpret_cast<const int4*>(s_odd[slot]);
-            if (key0 + kSub > lo || (odd.x | odd.y | odd.z | odd.w) != 0)   // warp-uniform
-              ok = softmax_tile<true>(tS, tO, s_ks[slot] + sub, s_vs[slot] + sub, rk, key0, lim, v > 0, m, l, before);
-            else
-              ok = softmax_tile<false>(tS, tO, s_ks[slot] + sub, s_vs[slot] + sub, rk, key0, lim, v > 0, m, l, before);
+            const float4 top4 = *reinterpret_cast<const float4*>(s_top[slot]);
+            const float top = fmaxf(fmaxf(fmaxf(top4.x, top4.y), fmaxf(top4.z, top4.w)), kTiny);
+#pragma unroll 1
+            for (int c = 0; c < kSub && ok; c += 32) {
+              const float *kx = s_ks[slot] + sub + c, *vx = s_vs[slot] + sub + c;
+              const int left = lim - key0 - c;
+              uint32_t w[16];
+              float2 sum;
+              while (true) {
+                bool far;
+                if (key0 + kSub > lo || top == INFINITY || __any_sync(0xFFFFFFFFu, z.f != 1.0f))   // warp-uniform
+                  far = weigh<true>(tS + c, kx, vx, top, left, z, w, sum);
+                else
+                  far = weigh<false>(tS + c, kx, vx, top, left, z, w, sum);
+                if (!__any_sync(0xFFFFFFFFu, far)) break;
+                float alpha;
+                if (!__any_sync(0xFFFFFFFFu, move_references(tS + c, kx, vx, left, far, z, alpha))) break;   // in range as it is
+                if (v > 0) ok = before();
+                if (!ok) break;
+                rescale(tO, tS, v > 0, c > 0, alpha);
+              }
+              z.l = fadd2v(z.l, sum);
+              tmem_st16(tS + c / 2, w);
+            }
+            if (!ok) break;
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&bars.p_full[t][v & 1]);
@@ -529,11 +548,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
           ok = ok && before();
           if (!ok) break;
           done += nv;
-          float L = l.x + l.y;
+          float L = z.l.x + z.l.y;
           const bool join = !by_rows && n > 1;
           if (join && t == 1) {
             // Half 1 hands over its rows' m, L and sums, 64 channels at a time.
-            s_half[trow] = make_float2(m, L);
+            s_half[trow] = make_float4(z.R, L, z.M, 0.0f);
             for (int k = 0; k < 2 && ok; ++k) {
 #pragma unroll 1
               for (int c = 0; c < 2; ++c) {
@@ -557,15 +576,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
                 ok = __all_sync(0xFFFFFFFFu, wait(&bars.half_full, joined));
                 if (!ok) break;
                 if (c == 0) {
-                  const float2 other = s_half[trow];
-                  const float to = fmaxf(m, other.x);
-                  a0 = ex2_approx(m - to);
-                  a1 = ex2_approx(other.x - to);
-                  m = to;
-                  L = L * a0 + other.y * a1;
+                  const float4 other = s_half[trow];
+                  const float to = fmaxf(z.R, other.x), top = fmaxf(z.M, other.z);
+                  L = L * ex2_approx(z.R - to) + other.y * ex2_approx(other.x - to);
+                  a0 = ex2_approx(z.M - top);
+                  a1 = ex2_approx(other.z - top);
+                  z.R = to;
+                  z.M = top;
                 }
               }
-              const float inv = inv_none != 0.0f ? (L == 0.0f ? 0.0f : 1.0f / L) : 1.0f;
+              const float half = scale2(z.M - z.R), inv = L == 0.0f ? 0.0f : half / L;
               uint32_t u[32];
               tmem_ld32(tO + 32 * c, u);
               tmem_ld_wait();
@@ -583,10 +603,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
                 uint16_t* dst = p.out + ((static_cast<int64_t>(x.b) * p.Sq + tok) * p.Hq + hq) * kHeadDim + 32 * c;
 #pragma unroll
                 for (int i = 0; i < 32; i += 16)
-                  store32(dst + i, pack_bf16(o[i] * inv, o[i + 1] * inv), pack_bf16(o[i + 2] * inv, o[i + 3] * inv),
-                          pack_bf16(o[i + 4] * inv, o[i + 5] * inv), pack_bf16(o[i + 6] * inv, o[i + 7] * inv),
-                          pack_bf16(o[i + 8] * inv, o[i + 9] * inv), pack_bf16(o[i + 10] * inv, o[i + 11] * inv),
-                          pack_bf16(o[i + 12] * inv, o[i + 13] * inv), pack_bf16(o[i + 14] * inv, o[i + 15] * inv));
+                  store32(dst + i, pack_bf16(o[i] * half * inv, o[i + 1] * half * inv), pack_bf16(o[i + 2] * half * inv, o[i + 3] * half * inv),
+                          pack_bf16(o[i + 4] * half * inv, o[i + 5] * half * inv), pack_bf16(o[i + 6] * half * inv, o[i + 7] * half * inv),
+                          pack_bf16(o[i + 8] * half * inv, o[i + 9] * half * inv), pack_bf16(o[i + 10] * half * inv, o[i + 11] * half * inv),
+                          pack_bf16(o[i + 12] * half * inv, o[i + 13] * half * inv), pack_bf16(o[i + 14] * half * inv, o[i + 15] * half * inv));
               } else if (valid) {
                 float* dst = p.part_o + at * kHeadDim + 32 * c;
                 const uint32_t* v = reinterpret_cast<const uint32_t*>(o);
@@ -597,9 +617,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
             }
             if (valid && inv_none != 0.0f) {
               if (p.lse != nullptr)
-                p.lse[(static_cast<int64_t>(x.b) * p.Hq + hq) * p.Sq + tok] = L == 0.0f ? -INFINITY : (m + log2f(L)) * kLn2;
+                p.lse[(static_cast<int64_t>(x.b) * p.Hq + hq) * p.Sq + tok] = L == 0.0f ? -INFINITY : (z.R + log2f(L)) * kLn2;
             } else if (valid) {
-              p.part_ml[at] = make_float4(m, L, m, 0.0f);
+              p.part_ml[at] = make_float4(z.R, L, z.M, 0.0f);
             }
           }
           tc_fence_before();                               // O may be written again
@@ -622,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
         const int t = warp & 1;
         const bool is_pv = warp >= 18;
         constexpr uint32_t kIdescQK = make_idesc_f32acc(128, kSub, 0, 0);                  // F16 x F16
-        constexpr uint32_t kIdescPV = make_idesc_f32acc(128, 128, 1, 1) | (1u << 16);      // BF16 x BF16, B's outer index summed
+        constexpr uint32_t kIdescPV = make_idesc_f32acc(128, 128, 0, 0) | (1u << 16);      // F16 x F16, B's outer index summed
         const uint32_t q_lo = sw128_desc_lo(smem_addr(smem + kSmemQ));
         const uint32_t k_lo = sw128_desc_lo(smem_addr(smem + kSmemK));
         // V: 64-channel halves kHalf bytes apart, groups of eight keys 1024.

@@ -87,7 +87,7 @@ def join(a, b):
     return tuple(torch.cat([x, y]) for x, y in zip(a, b))
 
 
-def reference(q, rows, causal, scale, weight=2.0 ** -11):
+def reference(q, rows, causal, scale):
     """q bf16 [Sq, Hq, 128] over dense rows (codes and scales, n keys): (out,
     lse, bound of |out error|, bound of |lse error|) in float64.
 
@@ -97,11 +97,8 @@ def reference(q, rows, causal, scale, weight=2.0 ** -11):
                core may truncate its partial sums, hence 2u each), so
                dx <= 264 u X, and a running maximum near x costs one rounding
                more of |x|: 2 u X
-      weights  ex2.approx: 2^-22 relative; `weight`: a rounding of 2^-11 to fp16,
-               or 2^-25 of the largest weight times scale if smaller (where a
-               key/value head has many rows the weight and the value times its
-               scale are rounded to bf16, 2^-8 each: (1 + 2^-8)^2 - 1 = 2^-7 + 2^-16
-               for their product); log2 of the
+      weights  ex2.approx: 2^-22 relative; a rounding of 2^-11 to fp16, or
+               2^-25 of the largest weight times scale if smaller; log2 of the
                scale: 2^-22 absolute and a rounding of |x| + |log2 sv|
       sums     fp32, n keys: n 2u of the sum of magnitudes at the most
       out      one rounding to bf16: 2^-8 of |out|
@@ -135,7 +132,7 @@ def reference(q, rows, causal, scale, weight=2.0 ** -11):
         mass = p @ vabs
         dx = 266 * u * torch.where(seen, mag, torch.zeros_like(mag)).amax(-1)
         dlog = (torch.log2(torch.nan_to_num(vs[:, g], nan=1.0).clamp(min=2.0 ** -140)).abs().amax() + 64) * 2 * u
-        rel = 2 * dx + 2.0 ** -21 + weight + 2 * n * u + dlog
+        rel = 2 * dx + 2.0 ** -21 + 2.0 ** -11 + 2 * n * u + dlog
         largest = (p * torch.nan_to_num(vs[:, g], nan=0.0)[None]).amax(-1)
         tol[:, h] = 2.0 ** -8 * out[:, h].abs() + rel[:, None] * mass + 2.0 ** -25 * largest[:, None] * vc[:, g].abs().sum(0)[None]
         ltol[h] = 2 * dx + 2.0 ** -20 + 2 * n * u + torch.where(live, z, torch.zeros_like(z)).abs() * 4 * u
