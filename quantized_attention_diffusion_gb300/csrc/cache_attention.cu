@@ -40,6 +40,7 @@ constexpr uint32_t kOffKs = 2 * kTok * kHeadDim;
 constexpr uint32_t kOffVs = kOffKs + kTok * 4;
 constexpr uint32_t kStageBytes = kOffVs + kTok * 4;
 constexpr uint32_t kMergeBytes = kConsumers * 8 * kHeadDim * 4;
+constexpr int kClusterTiles = 16;                         // most tiles of a CTA of a cluster
 constexpr int kMaxCtas = 3 * kSms;                        // CTAs of a launch: three on each SM
 // As many as the registers of NT times 8 query rows allow without spilling much.
 __host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : nt == 2 ? 2 : 1; }
@@ -221,6 +222,109 @@ __device__ __forceinline__ void attend(QueryRows<NT>& z, const uint8_t* st, int 
   }
 }
 
+// The unit's query rows (bf16 in shared memory) as a warp holds them, nothing attended
+// to yet.
+template <int NT>
+__device__ __forceinline__ void load_queries(QueryRows<NT>& z, const uint8_t* queries, int rows, float c_scale, int r, int c) {
+#pragma unroll
+  for (int a = 0; a < NT; ++a) {
+    uint4 raw[4];              // row r of these eight, a quarter of its channels
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      raw[i] = a * 8 + r < rows ? *reinterpret_cast<const uint4*>(queries + (a * 8 + r) * kHeadDim * 2 + c * 64 + i * 16)
+                                : make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(raw);
+    uint32_t top = 0u;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = max(top, max(u[i] & 0x7FFFu, (u[i] >> 16) & 0x7FFFu));
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    const uint32_t ex = row_exponent(top);
+    const float up = __uint_as_float(ex << 23);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      z.q[a][i >> 1][i & 1] = pack_f16(__uint_as_float(u[i] << 16) * up, __uint_as_float(u[i] & 0xFFFF0000u) * up);
+    const float back = c_scale * __uint_as_float((254u - ex) << 23);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) z.crow[a][e] = __shfl_sync(0xFFFFFFFFu, back, (2 * c + e) * 4);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z.o[a][j][e] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      z.m[a][e] = z.mw[a][e] = kLowest;
+      z.l[a][e] = 0.0f;
+    }
+  }
+}
+
+// What the warps' join takes in shared memory, one set a CTA.
+struct JoinStats {
+  float m[kConsumers][8], w[kConsumers][8], l[kConsumers][8];
+};
+
+// The four warps' parts of rows 8a .. 8a + 7, joined: this thread gets channels
+// 8 (thread % 16) .. of row 8a + thread / 16 relative to M, and the row's m, L, M.
+// `merge`: 8 rows of each warp.
+template <int NT>
+__device__ __forceinline__ float4 join_warps(QueryRows<NT>& z, int a, int rows, JoinStats& s, float4* merge, float4 (&sum)[2]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) z.l[a][e] += __shfl_xor_sync(0xFFFFFFFFu, z.l[a][e], d);
+    if (r == 0) {
+      s.m[warp][2 * c + e] = z.m[a][e];
+      s.w[warp][2 * c + e] = z.mw[a][e];
+      s.l[warp][2 * c + e] = z.l[a][e];
+    }
+  }
+  consumer_sync();
+  const int row = threadIdx.x >> 4, g = threadIdx.x & 15;
+  float M = s.w[0][row], mm = s.m[0][row], L = 0.0f;
+#pragma unroll
+  for (int k = 1; k < kConsumers; ++k) {
+    M = fmaxf(M, s.w[k][row]);
+    mm = fmaxf(mm, s.m[k][row]);
+  }
+#pragma unroll
+  for (int k = 0; k < kConsumers; ++k) L += s.l[k][row] * ex2_approx(s.m[k][row] - mm);
+  // float4 i of channels 16r .. 16r + 15 stands at 4r + (i ^ c): the eight lanes of
+  // a store fall into distinct banks.
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    if (a * 8 + 2 * c + e < rows) {
+      float top = s.w[0][2 * c + e];
+#pragma unroll
+      for (int k = 1; k < kConsumers; ++k) top = fmaxf(top, s.w[k][2 * c + e]);
+      const float w = ex2_approx(z.mw[a][e] - top);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        merge[(warp * 8 + 2 * c + e) * 32 + 4 * r + (i ^ c)] =
+            make_float4(z.o[a][2 * i][e] * w, z.o[a][2 * i][e + 2] * w, z.o[a][2 * i + 1][e] * w, z.o[a][2 * i + 1][e + 2] * w);
+    }
+  }
+  consumer_sync();
+  sum[0] = sum[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (a * 8 + row < rows) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int at = g * 2 + e, idx = row * 32 + (at & ~3) + ((at & 3) ^ (row >> 1));
+      sum[e] = merge[idx];
+#pragma unroll
+      for (int k = 1; k < kConsumers; ++k) {
+        const float4 y = merge[k * 8 * 32 + idx];
+        sum[e].x += y.x;
+        sum[e].y += y.y;
+        sum[e].z += y.z;
+        sum[e].w += y.w;
+      }
+    }
+  }
+  return make_float4(mm, L, M, 0.0f);
+}
+
 template <int NT, bool kPrefix>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(const Params p) {
   constexpr int R = 8 * NT, kStages = stages_of(NT);
@@ -229,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
   __shared__ int abort_flag;
   __shared__ int s_len[kMaxBatch];
   __shared__ long long s_off[kPrefix ? 2 : kMaxBatch + 1];
-  __shared__ float s_m[kConsumers][8], s_w[kConsumers][8], s_l[kConsumers][8];
+  __shared__ JoinStats stats;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_v = &abort_flag;
@@ -361,49 +465,18 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
         QueryRows<NT> z;
         int lo = INT_MAX;            // keys that every row sees
         ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&q_full, seg & 1, abort_v, p.err, p.timeout_ns));
+        load_queries<NT>(z, queries, rows, p.c_scale, r, c);
 #pragma unroll
-        for (int a = 0; a < NT; ++a) {
-          uint4 raw[4];              // row r of these eight, a quarter of its channels
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            raw[i] = a * 8 + r < rows ? *reinterpret_cast<const uint4*>(queries + (a * 8 + r) * kHeadDim * 2 + c * 64 + i * 16)
-                                      : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t* u = reinterpret_cast<const uint32_t*>(raw);
-          uint32_t top = 0u;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) top = max(top, max(u[i] & 0x7FFFu, (u[i] >> 16) & 0x7FFFu));
-          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-          const uint32_t ex = row_exponent(top);
-          const float up = __uint_as_float(ex << 23);
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            z.q[a][i >> 1][i & 1] = pack_f16(__uint_as_float(u[i] << 16) * up, __uint_as_float(u[i] & 0xFFFF0000u) * up);
-          const float back = p.c_scale * __uint_as_float((254u - ex) << 23);
+        for (int a = 0; a < NT; ++a)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            z.crow[a][e] = __shfl_sync(0xFFFFFFFFu, back, (2 * c + e) * 4);
             const int row = x.rt * R + a * 8 + 2 * c + e;
             z.lim[a][e] = row < p.rows ? min(hi, walk.limit(x.b, row)) : hi;
             lo = min(lo, z.lim[a][e]);
           }
-        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_empty);
         lo = __reduce_min_sync(0xFFFFFFFFu, lo);
-
-#pragma unroll
-        for (int a = 0; a < NT; ++a) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) z.o[a][j][e] = 0.0f;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            z.m[a][e] = z.mw[a][e] = kLowest;
-            z.l[a][e] = 0.0f;
-          }
-        }
 
         for (int t = x.t0; t < x.t1; ++t, ++it) {
           const int s = it % kStages;
@@ -420,58 +493,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
 #pragma unroll
         for (int a = 0; a < NT; ++a) {
           if (a * 8 >= rows) break;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) z.l[a][e] += __shfl_xor_sync(0xFFFFFFFFu, z.l[a][e], d);
-            if (r == 0) {
-              s_m[warp][2 * c + e] = z.m[a][e];
-              s_w[warp][2 * c + e] = z.mw[a][e];
-              s_l[warp][2 * c + e] = z.l[a][e];
-            }
-          }
-          consumer_sync();
+          float4 sum[2];
+          const float4 mlm = join_warps<NT>(z, a, rows, stats, merge, sum);
+          const float mm = mlm.x, L = mlm.y, M = mlm.z;
           const int row = threadIdx.x >> 4, g = threadIdx.x & 15;   // 8 channels of a row a thread
-          float M = s_w[0][row], mm = s_m[0][row], L = 0.0f;
-#pragma unroll
-          for (int k = 1; k < kConsumers; ++k) {
-            M = fmaxf(M, s_w[k][row]);
-            mm = fmaxf(mm, s_m[k][row]);
-          }
-#pragma unroll
-          for (int k = 0; k < kConsumers; ++k) L += s_l[k][row] * ex2_approx(s_m[k][row] - mm);
-          // float4 i of channels 16r .. 16r + 15 stands at 4r + (i ^ c): the
-          // eight lanes of a store fall into distinct banks.
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (a * 8 + 2 * c + e < rows) {
-              float top = s_w[0][2 * c + e];
-#pragma unroll
-              for (int k = 1; k < kConsumers; ++k) top = fmaxf(top, s_w[k][2 * c + e]);
-              const float w = ex2_approx(z.mw[a][e] - top);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                merge[(warp * 8 + 2 * c + e) * 32 + 4 * r + (i ^ c)] =
-                    make_float4(z.o[a][2 * i][e] * w, z.o[a][2 * i][e + 2] * w, z.o[a][2 * i + 1][e] * w, z.o[a][2 * i + 1][e + 2] * w);
-            }
-          }
-          consumer_sync();
           const int rr = x.rt * R + a * 8 + row;
           if (a * 8 + row < rows && !abort_flag) {
-            float4 sum[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int at = g * 2 + e, idx = row * 32 + (at & ~3) + ((at & 3) ^ (row >> 1));
-              sum[e] = merge[idx];
-#pragma unroll
-              for (int k = 1; k < kConsumers; ++k) {
-                const float4 y = merge[k * 8 * 32 + idx];
-                sum[e].x += y.x;
-                sum[e].y += y.y;
-                sum[e].z += y.z;
-                sum[e].w += y.w;
-              }
-            }
             if (whole && !p.keep) {
               const int t = rr / p.G, hq = x.h * p.G + rr % p.G;
               const float half = scale2(M - mm), inv = L == 0.0f ? 0.0f : half / L;
@@ -499,6 +526,215 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
   // The merge kernel waits for this grid alone: this grid has to end after the
   // one before it, beside which it may have run.
   if constexpr (kPrefix) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ---------------------------------------------------------------- cluster --
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Every thread of the cluster; shared memory written before is seen by all after.
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// The address of this CTA's shared-memory `addr` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 load_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+// Few units of short sequences: a cluster of up to eight CTAs takes a unit, its CTAs
+// the key tiles in turn (the prefix's, if there is one, before the sequence's own), and
+// they join their parts through one another's shared memory: one launch and no
+// workspace where the kernel above takes two, or three behind a prefix.  A prefix is
+// then read once for each sequence, from L2.  What bounds it is one chain of
+// latencies: the length, the pages, the copies, the products, the join.
+template <int NT, bool kPrefix>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_cluster_kernel(const Params p, const int32_t* prefix_pages, int ctas) {
+  constexpr int R = 8 * NT, kStages = stages_of(NT);
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full[kStages], empty[kStages], q_full;
+  __shared__ int abort_flag;
+  __shared__ JoinStats stats;
+  __shared__ float4 s_ml[R];
+  static_assert(R * kHeadDim * 4 <= kStages * kStageBytes, "a unit's part in the place of the tiles");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_v = &abort_flag;
+  const int rank = static_cast<int>(cluster_rank());
+  const int unit = blockIdx.x / ctas, b = unit / p.cache.H, h = unit % p.cache.H;
+  const int np = kPrefix ? (p.prefix_len + kTok - 1) / kTok : 0;      // tiles of the prefix
+  const int len_raw = __ldg(p.lens + b);
+  if (threadIdx.x == 32) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kConsumers);
+    }
+    mbar_init(&q_full, 1);
+    abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  __syncthreads();
+  const int rows = p.rows;
+  float4* merge = reinterpret_cast<float4*>(smem + kStages * kStageBytes);
+  const uint8_t* queries = smem + kStages * kStageBytes + kMergeBytes;
+  const uint32_t smem0 = smem_addr(smem);
+
+  if (warp == kConsumers) {
+    // -------------------------------------------------------------- copies --
+    const int ps = p.cache.page_shift;
+    const int run = min(kTok, 1 << ps), runs = kTok / run;
+    const int my_run = lane >> 2, part = lane & 3;       // as in the kernel above
+    if (lane == 0) mbar_arrive_expect_tx(&q_full, rows * kHeadDim * 2);
+    __syncwarp();
+    if (lane < rows)
+      bulk_load(smem0 + kStages * kStageBytes + kMergeBytes + lane * kHeadDim * 2,
+                p.q + b * p.q_sb + (lane / p.G) * p.q_ss + (h * p.G + lane % p.G) * kHeadDim, kHeadDim * 2, smem_addr(&q_full));
+    // The page of this lane's run of tile t, wherever the sequence ends: on its way
+    // before its length is known.
+    auto page_of = [&](int t) {
+      const bool pre = kPrefix && t < np;
+      const int at = ((pre ? t : t - np) * kTok + my_run * run) >> ps;
+      const int width = pre ? ((p.prefix_len - 1) >> ps) + 1 : p.table.width;
+      const int32_t* row = pre ? prefix_pages : p.table.pages + b * p.table.stride;
+      return my_run < runs && at < width ? __ldg(row + at) : -1;
+    };
+    int next = page_of(rank);
+    const int len = max(0, min(p.room, len_raw)), n = np + (len + kTok - 1) / kTok;
+    int it = 0;
+    bool bad = false;
+    for (int t = rank; t < n; t += ctas, ++it) {
+      int page = next;
+      if (t + ctas < n) next = page_of(t + ctas);
+      const bool pre = kPrefix && t < np;
+      const int first = (pre ? t : t - np) * kTok, hi = pre ? p.prefix_len : len;
+      const int t0 = first + my_run * run;
+      const bool live = my_run < runs && t0 < hi;
+      if (live && (page < 0 || page >= p.cache.num_pages)) {
+        bad = true;
+        page = 0;        // a page that exists: the result is void, the read is not out of bounds
+      }
+      const int s = it % kStages, round = it / kStages;
+      if (round > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[s], (round - 1) & 1, abort_v, p.err, p.timeout_ns))) break;
+      const int n_live = (min(kTok, hi - first) + run - 1) / run;
+      if (lane == 0) mbar_arrive_expect_tx(&full[s], n_live * run * (2 * kHeadDim + 8));
+      __syncwarp();
+      if (live) {
+        const int64_t r = ((static_cast<int64_t>(page) * p.cache.H + h) << ps) + (t0 & ((1 << ps) - 1));
+        const uint32_t bar = smem_addr(&full[s]), st = smem0 + s * kStageBytes;
+        const int o = my_run * run;
+        if (part == 0)
+          bulk_load(st + o * kHeadDim, p.cache.k_codes + r * kHeadDim, run * kHeadDim, bar);
+        else if (part == 1)
+          bulk_load(st + kOffV + o * kHeadDim, p.cache.v_codes + r * kHeadDim, run * kHeadDim, bar);
+        else if (part == 2)
+          bulk_load(st + kOffKs + o * 4, p.cache.k_scale + r, run * 4, bar);
+        else
+          bulk_load(st + kOffVs + o * 4, p.cache.v_scale + r, run * 4, bar);
+      }
+    }
+    if (bad) atomicExch(p.err, SAGE_DEVERR_BAD_PAGE);
+    if (*abort_v) {   // let the copies in flight land before the CTA can exit
+      for (int j = max(0, it - kStages); j < it; ++j) {
+        int local_abort = 0;
+        (void)mbar_wait(&full[j % kStages], (j / kStages) & 1, &local_abort, p.err, p.timeout_ns);
+      }
+      int local_abort = 0;
+      (void)mbar_wait(&q_full, 0, &local_abort, p.err, p.timeout_ns);
+    }
+  } else {
+    // ------------------------------------------------------------- compute --
+    const int r = lane >> 2, c = lane & 3;
+    QueryRows<NT> z;
+    bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&q_full, 0, abort_v, p.err, p.timeout_ns));
+    load_queries<NT>(z, queries, rows, p.c_scale, r, c);
+    const int len = max(0, min(p.room, len_raw)), n = np + (len + kTok - 1) / kTok;
+    int hi = 0, lo = 0;
+    // What the rows see of the prefix, or of the sequence's own keys.
+    auto part_of = [&](bool pre) {
+      hi = lo = pre ? p.prefix_len : len;
+#pragma unroll
+      for (int a = 0; a < NT; ++a)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int row = a * 8 + 2 * c + e;
+          int seen = hi;
+          if (p.causal && row < rows) seen = max(0, min(hi, (pre ? p.prefix_len : 0) + len - p.Sq + row / p.G + 1));
+          z.lim[a][e] = seen;
+          lo = min(lo, seen);
+        }
+      lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+    };
+    bool pre = kPrefix && rank < np;
+    part_of(pre);
+    int it = 0;
+    for (int t = rank; t < n; t += ctas, ++it) {
+      if (kPrefix && pre && t >= np) {
+        pre = false;
+        part_of(false);
+      }
+      const int s = it % kStages;
+      ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&full[s], (it / kStages) & 1, abort_v, p.err, p.timeout_ns));
+      const int t0 = (pre ? t : t - np) * kTok + warp * 16;
+      if (ok && t0 < hi) attend<NT>(z, smem + s * kStageBytes, t0, warp * 16, r, c, hi, lo);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+    }
+    // This CTA's part goes where the tiles were: all warps are behind them after
+    // the first barrier of join_warps.
+#pragma unroll
+    for (int a = 0; a < NT; ++a) {
+      if (a * 8 >= rows) break;
+      float4 sum[2];
+      const float4 mlm = join_warps<NT>(z, a, rows, stats, merge, sum);
+      const int row = threadIdx.x >> 4, g = threadIdx.x & 15;
+      float4* dst = reinterpret_cast<float4*>(smem + (a * 8 + row) * kHeadDim * 4) + g * 2;
+      dst[0] = sum[0];
+      dst[1] = sum[1];
+      if (g == 0) s_ml[a * 8 + row] = mlm;
+    }
+  }
+  __syncwarp();
+  cluster_sync_all();
+  if (warp < kConsumers) {
+    // A warp a row, four channels a lane.
+    for (int row = rank * kConsumers + warp; row < rows; row += ctas * kConsumers) {
+      float m = kLowest, M = kLowest, L = 0.0f;
+      float4 ml[8], acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f), part[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        ml[k] = make_float4(kLowest, 0.0f, kLowest, 0.0f);
+        part[k] = acc;
+        if (k < ctas) {
+          ml[k] = load_cluster4(in_cta(smem_addr(&s_ml[row]), k));
+          part[k] = load_cluster4(in_cta(smem0 + row * kHeadDim * 4 + lane * 16, k));
+        }
+        m = fmaxf(m, ml[k].x);
+        M = fmaxf(M, ml[k].z);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        L += ml[k].y * ex2_approx(ml[k].x - m);
+        const float w = ex2_approx(ml[k].z - M);
+        acc = make_float4(acc.x + part[k].x * w, acc.y + part[k].y * w, acc.z + part[k].z * w, acc.w + part[k].w * w);
+      }
+      const int t = row / p.G, hq = h * p.G + row % p.G;
+      const float half = scale2(M - m), inv = L == 0.0f ? 0.0f : half / L;
+      const uint2 w = make_uint2(pack_bf16(acc.x * half * inv, acc.y * half * inv), pack_bf16(acc.z * half * inv, acc.w * half * inv));
+      *reinterpret_cast<uint2*>(p.out + ((static_cast<int64_t>(b) * p.Sq + t) * p.Hq + hq) * kHeadDim + lane * 4) = w;
+      if (p.lse != nullptr && lane == 0)
+        p.lse[(static_cast<int64_t>(b) * p.Hq + hq) * p.Sq + t] = L == 0.0f ? -INFINITY : (m + log2f(L)) * kLn2;
+    }
+  }
+  __syncwarp();
+  cluster_sync_all();            // no CTA ends while another reads from it
 }
 
 // ------------------------------------------------------------------ merge --
@@ -717,6 +953,75 @@ unsigned ctas_for(long long tiles, int R) {
   return static_cast<unsigned>(std::min<long long>(max_ctas(R), std::max(1ll, tiles)));
 }
 
+// CTAs of a unit's cluster where one launch of clusters does it all, or 0: where the
+// SMs hold all clusters at once and no CTA can have more than 16 tiles.  Both sides,
+// us, 4 rows to each of 8 key/value heads, keys full: 1 sequence of 1024 keys 8.4
+// (above: 12.4), of 8192 18.5 (16.5); 12 of 4096 23.8 (27.3); 48 of 1024 23.9 (29.4),
+// of 2048 40.0 (45.6; half full 34.9 against 32.9).  32 rows, 4 of 4096 28.8 (35.0).
+// Behind a prefix of 1024, 6 sequences, 2 heads 8.7 (18.6); 24, 8 heads, 16.5 (27.7),
+// of 4096 41.1 (32.9).
+int cluster_ctas(const CacheAttnArgs& a) {
+  const int rows = a.Sq * (a.Hq / a.cache.H);
+  if (rows > 32) return 0;
+  const int64_t units = static_cast<int64_t>(a.B) * a.cache.H;
+  const int64_t room = std::min<int64_t>(kMaxCacheLen, static_cast<int64_t>(a.table.width) << a.cache.page_shift);
+  const int64_t tiles = (room + kTok - 1) / kTok + (a.prefix_len + kTok - 1) / kTok;
+  const int most = max_ctas(rows_per_tile(rows));
+  int ctas = 8;
+  while (ctas > 1 && (units * ctas > most || tiles <= ctas / 2)) ctas /= 2;
+  return units * ctas <= most && tiles <= static_cast<int64_t>(kClusterTiles) * ctas ? ctas : 0;
+}
+
+cudaError_t launch_clusters(const CacheAttnArgs& a, int ctas, cudaStream_t stream) {
+  Params p = {};
+  p.cache = a.cache;
+  p.table = a.table;
+  p.lens = a.lens;
+  p.q = a.q;
+  p.q_sb = a.q_sb;
+  p.q_ss = a.q_ss;
+  p.out = a.out;
+  p.lse = a.lse;
+  p.B = a.B;
+  p.Sq = a.Sq;
+  p.G = a.Hq / a.cache.H;
+  p.Hq = a.Hq;
+  p.causal = a.causal;
+  p.prefix_len = a.prefix_len;
+  p.room = static_cast<int>(std::min<int64_t>(kMaxCacheLen, static_cast<int64_t>(a.table.width) << a.cache.page_shift));
+  p.rows = a.Sq * p.G;
+  p.c_scale = a.softmax_scale * kLog2e;
+  p.timeout_ns = a.timeout_ns;
+  p.err = a.err;
+  const int R = rows_per_tile(p.rows);
+  const uint32_t smem = smem_of(R / 8);
+  auto go = [&](auto kernel) {
+    static std::atomic<uint64_t> allowed[2 * 4];       // for each kernel
+    cudaError_t e = allow_smem(kernel, smem, allowed[(a.prefix_len > 0 ? 4 : 0) + R / 16]);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.B) * a.cache.H * ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p, a.prefix_pages, ctas);
+  };
+  if (a.prefix_len > 0)
+    return R == 8    ? go(cache_attn_cluster_kernel<1, true>)
+           : R == 16 ? go(cache_attn_cluster_kernel<2, true>)
+                     : go(cache_attn_cluster_kernel<4, true>);
+  return R == 8    ? go(cache_attn_cluster_kernel<1, false>)
+         : R == 16 ? go(cache_attn_cluster_kernel<2, false>)
+                   : go(cache_attn_cluster_kernel<4, false>);
+}
+
 }  // namespace
 
 size_t cache_attn_workspace_bytes(int B, int Sq, int Hq, int Hkv, int prefix_len) {
@@ -739,7 +1044,10 @@ bool cache_attn_fits(int B, int Sq, int Hq, int Hkv, int page_size, int table_wi
          (prefix_len == 0 || fits(prefix_len, b * rows, 1, Hkv));
 }
 
+bool cache_attn_needs_workspace(const CacheAttnArgs& a) { return cluster_ctas(a) == 0; }
+
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream) {
+  if (const int ctas = cluster_ctas(a); ctas > 0) return launch_clusters(a, ctas, stream);
   const int H = a.cache.H, G = a.Hq / H;
   const bool both = a.prefix_len > 0;
   for (int b0 = 0; b0 < a.B; b0 += kMaxBatch) {

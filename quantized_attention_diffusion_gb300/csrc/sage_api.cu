@@ -423,7 +423,7 @@ sage_status run_cache_attention(const void* q, int64_t q_sb, int64_t q_ss, const
     const cudaError_t err = launch_cache_attention(a, st);
     return err == cudaSuccess ? SAGE_OK : cuda_fail(err, "cache attention launch");
   };
-  return ws ? launch(ws) : with_pool_workspace(need, st, launch);
+  return ws || !cache_attn_needs_workspace(a) ? launch(ws) : with_pool_workspace(need, st, launch);
 }
 
 }  // namespace

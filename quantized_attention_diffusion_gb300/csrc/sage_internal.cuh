@@ -150,6 +150,8 @@ size_t cache_attn_workspace_bytes(int B, int Sq, int Hq, int Hkv, int prefix_len
 // Whether a CTA's share of the work, for the longest sequences that the table has
 // room for, is counted in 31 bits.
 bool cache_attn_fits(int B, int Sq, int Hq, int Hkv, int page_size, int table_width, int prefix_len);
+// Few units of short sequences need none (a.workspace may be null then).
+bool cache_attn_needs_workspace(const CacheAttnArgs& a);
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream);
 
 // cudaFuncSetAttribute for `kernel`'s dynamic shared memory, once on each device:

@@ -229,6 +229,36 @@ def test_shared_prefix(P, lens, Sq, H, G, page, causal):
     _check(out, lse, q, c, causal, prefix=B)
 
 
+def _roomy(table, page):
+    """The table with room for far more keys: the work is cut up over all CTAs
+    whatever the lengths, where a narrow table lets clusters of CTAs take a unit each."""
+    width = -(-20000 // page)
+    return torch.nn.functional.pad(table, (0, max(0, width - table.shape[1])), value=-1)
+
+
+@pytest.mark.parametrize("lens,Sq,H,G,page", [(n, 1, H, G, page) for n, H, G, page in STEP] + CHUNK[:6])
+def test_room_does_not_matter(lens, Sq, H, G, page):
+    import quantized_attention_diffusion_gb300 as qad
+    c = Cache(lens, H, page, seed=Sq + G, recipe="sharp")
+    q = _q(len(lens), Sq, H * G, seed=G + 1)
+    for table in (c.table, _roomy(c.table, page)):
+        out, lse = qad.attn_fwd_cache(q.cuda(), c.gpu(), table.cuda(), ints(lens), return_lse=True)
+        _check(out, lse, q, c, True)
+
+
+@pytest.mark.parametrize("P,lens,Sq,H,G,page", PREFIX + [(2000, [5], 4, 2, 8, 16), (65, [63, 64, 65, 0], 2, 2, 4, 128), (1999, [48], 1, 1, 1, 64)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_room_does_not_matter_behind_a_prefix(P, lens, Sq, H, G, page, causal):
+    import quantized_attention_diffusion_gb300 as qad
+    c = Cache(lens, H, page, seed=P, extra=[P], recipe="sharp")
+    B = len(lens)
+    q = _q(B, Sq, H * G, seed=P + 2)
+    for table in (c.table, _roomy(c.table, page)):
+        out, lse = qad.attn_fwd_cache_prefix(q.cuda(), c.gpu(), table[B, :-(-P // page)].cuda(), P, table[:B].cuda(), ints(lens),
+                                             causal=causal, return_lse=True)
+        _check(out, lse, q, c, causal, prefix=B)
+
+
 def test_softmax_scale_and_large_scores():
     """Scores of hundreds: weights of one key only, and the running maximum's path."""
     import quantized_attention_diffusion_gb300 as qad
@@ -445,7 +475,7 @@ def test_two_streams_and_a_graph_that_follows_the_lengths():
 @pytest.mark.parametrize("site", ["FAULT_POOL_ALLOC", "FAULT_ATTN_LAUNCH"])
 def test_injected_failures_leave_the_next_call_right(site):
     import quantized_attention_diffusion_gb300 as qad
-    c = Cache([300], 1, 32, seed=28)
+    c = Cache([300], 1, 32, seed=28, width=1000)             # room for more than one launch of clusters takes
     q = _q(1, 1, 4, seed=29).cuda()
     args = (q, c.gpu(), c.table.cuda(), ints([300]))
     want = bits(qad.attn_fwd_cache(*args))
