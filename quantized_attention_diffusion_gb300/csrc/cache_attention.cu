@@ -40,12 +40,12 @@ constexpr uint32_t kOffKs = 2 * kTok * kHeadDim;
 constexpr uint32_t kOffVs = kOffKs + kTok * 4;
 constexpr uint32_t kStageBytes = kOffVs + kTok * 4;
 constexpr uint32_t kMergeBytes = kConsumers * 8 * kHeadDim * 4;
-constexpr int kClusterTiles = 16;                         // most tiles of a CTA of a cluster
+constexpr int kClusterTiles = 16;                         // most tiles of an SM slot, in clusters
 constexpr int kMaxCtas = 3 * kSms;                        // CTAs of a launch: three on each SM
 // As many as the registers of NT times 8 query rows allow without spilling much.
-__host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : nt == 2 ? 2 : 1; }
-// Tiles in flight: 9, 8 or 8 on an SM, 135 KB or more.
-__host__ __device__ constexpr int stages_of(int nt) { return nt == 1 ? 3 : nt == 2 ? 4 : 8; }
+__host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
+// Tiles in flight: 9 or 8 on an SM, 135 KB or more.
+__host__ __device__ constexpr int stages_of(int nt) { return nt == 1 ? 3 : 4; }
 constexpr uint32_t smem_of(int nt) { return stages_of(nt) * kStageBytes + kMergeBytes + 8 * nt * kHeadDim * 2; }
 constexpr float kFar = 256.0f, kFarLog2 = 8.0f;           // weights stay near or below it (fp16: 65504)
 
@@ -556,9 +556,9 @@ __device__ __forceinline__ float4 load_cluster4(uint32_t addr) {
 // workspace where the kernel above takes two, or three behind a prefix.  A prefix is
 // then read once for each sequence, from L2.  What bounds it is one chain of
 // latencies: the length, the pages, the copies, the products, the join.
-template <int NT, bool kPrefix>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_cluster_kernel(const Params p, const int32_t* prefix_pages, int ctas) {
-  constexpr int R = 8 * NT, kStages = stages_of(NT);
+template <bool kPrefix>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(1)) cache_attn_cluster_kernel(const Params p, const int32_t* prefix_pages, int ctas) {
+  constexpr int R = 8, kStages = stages_of(1);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kStages], empty[kStages], q_full;
   __shared__ int abort_flag;
@@ -569,7 +569,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_cluster_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_v = &abort_flag;
   const int rank = static_cast<int>(cluster_rank());
-  const int unit = blockIdx.x / ctas, b = unit / p.cache.H, h = unit % p.cache.H;
+  const int unit = blockIdx.x / ctas, h = unit % p.cache.H;
+  const int rt = unit / p.cache.H % p.row_tiles, b = unit / p.cache.H / p.row_tiles;
   const int np = kPrefix ? (p.prefix_len + kTok - 1) / kTok : 0;      // tiles of the prefix
   const int len_raw = __ldg(p.lens + b);
   if (threadIdx.x == 32) {
@@ -582,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_cluster_
     fence_mbarrier_init();
   }
   __syncthreads();
-  const int rows = p.rows;
+  const int row0 = rt * R, rows = min(R, p.rows - row0);
   float4* merge = reinterpret_cast<float4*>(smem + kStages * kStageBytes);
   const uint8_t* queries = smem + kStages * kStageBytes + kMergeBytes;
   const uint32_t smem0 = smem_addr(smem);
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_cluster_
     __syncwarp();
     if (lane < rows)
       bulk_load(smem0 + kStages * kStageBytes + kMergeBytes + lane * kHeadDim * 2,
-                p.q + b * p.q_sb + (lane / p.G) * p.q_ss + (h * p.G + lane % p.G) * kHeadDim, kHeadDim * 2, smem_addr(&q_full));
+                p.q + b * p.q_sb + ((row0 + lane) / p.G) * p.q_ss + (h * p.G + (row0 + lane) % p.G) * kHeadDim, kHeadDim * 2, smem_addr(&q_full));
     // The page of this lane's run of tile t, wherever the sequence ends: on its way
     // before its length is known.
     auto page_of = [&](int t) {
@@ -652,24 +653,22 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_cluster_
   } else {
     // ------------------------------------------------------------- compute --
     const int r = lane >> 2, c = lane & 3;
-    QueryRows<NT> z;
+    QueryRows<1> z;
     bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&q_full, 0, abort_v, p.err, p.timeout_ns));
-    load_queries<NT>(z, queries, rows, p.c_scale, r, c);
+    load_queries<1>(z, queries, rows, p.c_scale, r, c);
     const int len = max(0, min(p.room, len_raw)), n = np + (len + kTok - 1) / kTok;
     int hi = 0, lo = 0;
     // What the rows see of the prefix, or of the sequence's own keys.
     auto part_of = [&](bool pre) {
       hi = lo = pre ? p.prefix_len : len;
 #pragma unroll
-      for (int a = 0; a < NT; ++a)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int row = a * 8 + 2 * c + e;
-          int seen = hi;
-          if (p.causal && row < rows) seen = max(0, min(hi, (pre ? p.prefix_len : 0) + len - p.Sq + row / p.G + 1));
-          z.lim[a][e] = seen;
-          lo = min(lo, seen);
-        }
+      for (int e = 0; e < 2; ++e) {
+        const int row = 2 * c + e;
+        int seen = hi;
+        if (p.causal && row < rows) seen = max(0, min(hi, (pre ? p.prefix_len : 0) + len - p.Sq + (row0 + row) / p.G + 1));
+        z.lim[0][e] = seen;
+        lo = min(lo, seen);
+      }
       lo = __reduce_min_sync(0xFFFFFFFFu, lo);
     };
     bool pre = kPrefix && rank < np;
@@ -683,23 +682,19 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_cluster_
       const int s = it % kStages;
       ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&full[s], (it / kStages) & 1, abort_v, p.err, p.timeout_ns));
       const int t0 = (pre ? t : t - np) * kTok + warp * 16;
-      if (ok && t0 < hi) attend<NT>(z, smem + s * kStageBytes, t0, warp * 16, r, c, hi, lo);
+      if (ok && t0 < hi) attend<1>(z, smem + s * kStageBytes, t0, warp * 16, r, c, hi, lo);
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
     }
     // This CTA's part goes where the tiles were: all warps are behind them after
     // the first barrier of join_warps.
-#pragma unroll
-    for (int a = 0; a < NT; ++a) {
-      if (a * 8 >= rows) break;
-      float4 sum[2];
-      const float4 mlm = join_warps<NT>(z, a, rows, stats, merge, sum);
-      const int row = threadIdx.x >> 4, g = threadIdx.x & 15;
-      float4* dst = reinterpret_cast<float4*>(smem + (a * 8 + row) * kHeadDim * 4) + g * 2;
-      dst[0] = sum[0];
-      dst[1] = sum[1];
-      if (g == 0) s_ml[a * 8 + row] = mlm;
-    }
+    float4 sum[2];
+    const float4 mlm = join_warps<1>(z, 0, rows, stats, merge, sum);
+    const int row = threadIdx.x >> 4, g = threadIdx.x & 15;
+    float4* dst = reinterpret_cast<float4*>(smem + row * kHeadDim * 4) + g * 2;
+    dst[0] = sum[0];
+    dst[1] = sum[1];
+    if (g == 0) s_ml[row] = mlm;
   }
   __syncwarp();
   cluster_sync_all();
@@ -725,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_cluster_
         const float w = ex2_approx(ml[k].z - M);
         acc = make_float4(acc.x + part[k].x * w, acc.y + part[k].y * w, acc.z + part[k].z * w, acc.w + part[k].w * w);
       }
-      const int t = row / p.G, hq = h * p.G + row % p.G;
+      const int t = (row0 + row) / p.G, hq = h * p.G + (row0 + row) % p.G;
       const float half = scale2(M - m), inv = L == 0.0f ? 0.0f : half / L;
       const uint2 w = make_uint2(pack_bf16(acc.x * half * inv, acc.y * half * inv), pack_bf16(acc.z * half * inv, acc.w * half * inv));
       *reinterpret_cast<uint2*>(p.out + ((static_cast<int64_t>(b) * p.Sq + t) * p.Hq + hq) * kHeadDim + lane * 4) = w;
@@ -889,9 +884,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const Mer
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-// 8, 16 or 32 query rows a tile where they are all, else the wide kernel's 256:
-// the keys are read and converted once for all rows of a tile.
-int rows_per_tile(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : kWideRows; }
+// 8 or 16 query rows a tile where they are all, else the wide kernel's 256: the keys
+// are read and converted once for all rows of a tile.  32 sequences of 16384 keys, 8
+// key/value heads, us: 16 rows 223, as two tiles of eight 325, in the wide kernel 424;
+// 24 rows in the wide kernel 424, as three tiles of eight 482.
+int rows_per_tile(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : kWideRows; }
 int max_ctas(int R) { return kSms * (R == kWideRows ? 1 : ctas_per_sm(R / 8)); }
 int keys_per_tile(int R) { return R == kWideRows ? kWideTok : kTok; }
 int unit_cost(int R) { return R == kWideRows ? kWideCost : kCost; }
@@ -928,8 +925,8 @@ cudaError_t launch_part(const Params& p, int R, bool prefix, unsigned ctas, cuda
   if (R == kWideRows) return launch_wide(p, prefix, ctas, stream);
   const uint32_t smem = smem_of(R / 8);
   auto go = [&](auto kernel) {
-    static std::atomic<uint64_t> allowed[2 * 4];       // for each kernel
-    cudaError_t e = allow_smem(kernel, smem, allowed[(prefix ? 4 : 0) + R / 16]);
+    static std::atomic<uint64_t> allowed[2 * 2];       // for each kernel
+    cudaError_t e = allow_smem(kernel, smem, allowed[(prefix ? 2 : 0) + R / 16]);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
@@ -945,31 +942,35 @@ cudaError_t launch_part(const Params& p, int R, bool prefix, unsigned ctas, cuda
     return cudaLaunchKernelEx(&cfg, kernel, p);
   };
   if (prefix)
-    return R == 8 ? go(cache_attn_kernel<1, true>) : R == 16 ? go(cache_attn_kernel<2, true>) : go(cache_attn_kernel<4, true>);
-  return R == 8 ? go(cache_attn_kernel<1, false>) : R == 16 ? go(cache_attn_kernel<2, false>) : go(cache_attn_kernel<4, false>);
+    return R == 8 ? go(cache_attn_kernel<1, true>) : go(cache_attn_kernel<2, true>);
+  return R == 8 ? go(cache_attn_kernel<1, false>) : go(cache_attn_kernel<2, false>);
 }
 
 unsigned ctas_for(long long tiles, int R) {
   return static_cast<unsigned>(std::min<long long>(max_ctas(R), std::max(1ll, tiles)));
 }
 
-// CTAs of a unit's cluster where one launch of clusters does it all, or 0: where the
-// SMs hold all clusters at once and no CTA can have more than 16 tiles.  Both sides,
-// us, 4 rows to each of 8 key/value heads, keys full: 1 sequence of 1024 keys 8.4
-// (above: 12.4), of 8192 18.5 (16.5); 12 of 4096 23.8 (27.3); 48 of 1024 23.9 (29.4),
-// of 2048 40.0 (45.6; half full 34.9 against 32.9).  32 rows, 4 of 4096 28.8 (35.0).
-// Behind a prefix of 1024, 6 sequences, 2 heads 8.7 (18.6); 24, 8 heads, 16.5 (27.7),
-// of 4096 41.1 (32.9).
+// CTAs of a unit's cluster where one launch of clusters does it all, or 0: where no SM
+// slot (three on each SM) has more than 16 tiles to do, one CTA after another, and, for
+// more than 32 rows, which the wide kernel takes together, no more than two CTAs.
+// Both sides, us (clusters, the kernels above or the wide one), 8 key/value heads of
+// full sequences: 4 rows: 1 of 1024 keys 8.3, 12.4; 1 of 8192 18.6, 16.5; 12 of 4096
+// 23.8, 27.3; 48 of 1024 23.9, 29.4; 100 of 512 28.8, 34.0; 48 of 2048 40.0, 45.6 (half full
+// 34.9, 32.9).  32 rows: 1 of 1024 10.4, 19.1; 4 of 2048 20.6, 25.8; 64 of 128 37.0, 47.2.
+// 64 rows: 4 of 1024 20.6, 24.7; 12 of 512 28.8, 29.3; 24 of 256 (four CTAs) 36.1, 32.8.
+// 256 rows, 2 heads: 1 of 4096 20.6, 43.4; 24 of 256 (four CTAs) 37.0, 28.9.  Behind a prefix of
+// 1024, 4 rows: 6 sequences, 2 heads 8.7, 18.6; 24, 8 heads, 16.5, 27.7, of 4096 41.1, 32.9.
 int cluster_ctas(const CacheAttnArgs& a) {
-  const int rows = a.Sq * (a.Hq / a.cache.H);
-  if (rows > 32) return 0;
-  const int64_t units = static_cast<int64_t>(a.B) * a.cache.H;
+  const int64_t rows = static_cast<int64_t>(a.Sq) * (a.Hq / a.cache.H);
+  const int64_t units = a.B * ((rows + 7) / 8) * a.cache.H;   // of eight rows
   const int64_t room = std::min<int64_t>(kMaxCacheLen, static_cast<int64_t>(a.table.width) << a.cache.page_shift);
   const int64_t tiles = (room + kTok - 1) / kTok + (a.prefix_len + kTok - 1) / kTok;
-  const int most = max_ctas(rows_per_tile(rows));
+  const int most = max_ctas(8);
   int ctas = 8;
   while (ctas > 1 && (units * ctas > most || tiles <= ctas / 2)) ctas /= 2;
-  return units * ctas <= most && tiles <= static_cast<int64_t>(kClusterTiles) * ctas ? ctas : 0;
+  const int64_t waves = (units * ctas + most - 1) / most;
+  if (waves > (rows <= 32 ? kClusterTiles : 2)) return 0;
+  return waves * ((tiles + ctas - 1) / ctas) <= kClusterTiles ? ctas : 0;
 }
 
 cudaError_t launch_clusters(const CacheAttnArgs& a, int ctas, cudaStream_t stream) {
@@ -990,17 +991,17 @@ cudaError_t launch_clusters(const CacheAttnArgs& a, int ctas, cudaStream_t strea
   p.prefix_len = a.prefix_len;
   p.room = static_cast<int>(std::min<int64_t>(kMaxCacheLen, static_cast<int64_t>(a.table.width) << a.cache.page_shift));
   p.rows = a.Sq * p.G;
+  p.row_tiles = (p.rows + 7) / 8;
   p.c_scale = a.softmax_scale * kLog2e;
   p.timeout_ns = a.timeout_ns;
   p.err = a.err;
-  const int R = rows_per_tile(p.rows);
-  const uint32_t smem = smem_of(R / 8);
+  const uint32_t smem = smem_of(1);
   auto go = [&](auto kernel) {
-    static std::atomic<uint64_t> allowed[2 * 4];       // for each kernel
-    cudaError_t e = allow_smem(kernel, smem, allowed[(a.prefix_len > 0 ? 4 : 0) + R / 16]);
+    static std::atomic<uint64_t> allowed[2];           // for each kernel
+    cudaError_t e = allow_smem(kernel, smem, allowed[a.prefix_len > 0]);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.B) * a.cache.H * ctas);
+    cfg.gridDim = dim3(static_cast<unsigned>(a.B) * p.row_tiles * a.cache.H * ctas);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -1013,13 +1014,7 @@ cudaError_t launch_clusters(const CacheAttnArgs& a, int ctas, cudaStream_t strea
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, p, a.prefix_pages, ctas);
   };
-  if (a.prefix_len > 0)
-    return R == 8    ? go(cache_attn_cluster_kernel<1, true>)
-           : R == 16 ? go(cache_attn_cluster_kernel<2, true>)
-                     : go(cache_attn_cluster_kernel<4, true>);
-  return R == 8    ? go(cache_attn_cluster_kernel<1, false>)
-         : R == 16 ? go(cache_attn_cluster_kernel<2, false>)
-                   : go(cache_attn_cluster_kernel<4, false>);
+  return a.prefix_len > 0 ? go(cache_attn_cluster_kernel<true>) : go(cache_attn_cluster_kernel<false>);
 }
 
 }  // namespace

@@ -37,6 +37,12 @@ def _q(B, Sq, Hq, seed, mul=1.0):
     return (torch.randn((B, Sq, Hq, D), generator=g) * mul).to(torch.bfloat16)
 
 
+def _roomy(c):
+    """The cache's table with room for far more keys than clusters of CTAs take."""
+    width = -(-20000 // c.page)
+    return torch.nn.functional.pad(c.table, (0, max(0, width - c.table.shape[1])), value=-1)
+
+
 def _check(out, lse, q, c, causal, scale=SCALE, prefix=None, what=""):
     for b in range(q.shape[0]):
         rows = c.dense(b) if prefix is None else join(c.dense(prefix), c.dense(b))
@@ -64,10 +70,11 @@ def test_shapes(lens, Sq, H, G, page, causal):
     import quantized_attention_diffusion_gb300 as qad
     c = Cache(lens, H, page, seed=Sq + G, recipe="sharp")
     q = _q(len(lens), Sq, H * G, seed=Sq)
-    out, lse = qad.attn_fwd_cache(q.cuda(), c.gpu(), c.table.cuda(), ints(lens), causal=causal, return_lse=True)
-    _check(out, lse, q, c, causal)
-    again = qad.attn_fwd_cache(q.cuda(), c.gpu(), c.table.cuda(), ints(lens), causal=causal)
-    assert torch.equal(bits(again), bits(out))
+    for table in (c.table.cuda(), _roomy(c).cuda()):
+        out, lse = qad.attn_fwd_cache(q.cuda(), c.gpu(), table, ints(lens), causal=causal, return_lse=True)
+        _check(out, lse, q, c, causal)
+        again = qad.attn_fwd_cache(q.cuda(), c.gpu(), table, ints(lens), causal=causal)
+        assert torch.equal(bits(again), bits(out))
 
 
 @pytest.mark.parametrize("P,lens,Sq,H,G", [(1, [0, 3] * 20, 1, 2, 1), (128, [1] * 40, 1, 1, 1), (513, [9, 0] * 70, 1, 1, 1), (900, [7, 60, 5], 5, 2, 10)])
@@ -78,7 +85,7 @@ def test_prefixes(P, lens, Sq, H, G, causal):
     c = Cache(lens, H, 32, seed=P, extra=[P], recipe="sharp")
     wide = _q(B, Sq + 2, H * G + 3, seed=P + 1).cuda()
     q = wide[:, 1:1 + Sq, 2:2 + H * G]                      # queries sliced out of something larger
-    out, lse = qad.attn_fwd_cache_prefix(q, c.gpu(), c.table[B].cuda(), P, c.table[:B].cuda(), ints(lens), causal=causal,
+    out, lse = qad.attn_fwd_cache_prefix(q, c.gpu(), c.table[B].cuda(), P, _roomy(c)[:B].cuda(), ints(lens), causal=causal,
                                          return_lse=True)
     _check(out, lse, q.cpu(), c, causal, prefix=B)
 
@@ -105,7 +112,7 @@ def test_rising_and_falling_scores(Sq, G, span):
     import quantized_attention_diffusion_gb300 as qad
     lens = [1300, 77]
     c, q = _ramp(lens, 2, Sq, G, span, seed=int(abs(span)) + Sq)
-    out, lse = qad.attn_fwd_cache(q.cuda(), c.gpu(), c.table.cuda(), ints(lens), return_lse=True)
+    out, lse = qad.attn_fwd_cache(q.cuda(), c.gpu(), _roomy(c).cuda(), ints(lens), return_lse=True)
     _check(out, lse, q, c, True)
 
 
@@ -125,7 +132,7 @@ def test_scales_of_v_of_any_size(name, f, Sq):
     import quantized_attention_diffusion_gb300 as qad
     c = Cache([500, 150], 2, 32, seed=3, v_scale=f)
     q = _q(2, Sq, 2, seed=4)
-    out, lse = qad.attn_fwd_cache(q.cuda(), c.gpu(), c.table.cuda(), ints([500, 150]), return_lse=True)
+    out, lse = qad.attn_fwd_cache(q.cuda(), c.gpu(), _roomy(c).cuda(), ints([500, 150]), return_lse=True)
     _check(out, lse, q, c, True, what=name)
 
 
@@ -135,7 +142,7 @@ def test_queries_of_any_size(mul):
     c = Cache([300], 1, 32, seed=8)
     q = _q(1, 37, 2, seed=9, mul=mul)
     scale = SCALE * (2.0 ** -40 if mul > 1 else 1.0)
-    out, lse = qad.attn_fwd_cache(q.cuda(), c.gpu(), c.table.cuda(), ints([300]), softmax_scale=scale, return_lse=True)
+    out, lse = qad.attn_fwd_cache(q.cuda(), c.gpu(), _roomy(c).cuda(), ints([300]), softmax_scale=scale, return_lse=True)
     _check(out, lse, q, c, True, scale=scale)
 
 
@@ -146,7 +153,7 @@ def test_a_row_that_is_not_finite_reaches_only_what_sees_it(Sq, value):
     lens, H = [350, 290], 2
     c = Cache(lens, H, 32, seed=10)
     q = _q(2, Sq, 4, seed=11)
-    clean, clean_lse = qad.attn_fwd_cache(q.cuda(), c.gpu(), c.table.cuda(), ints(lens), return_lse=True)
+    clean, clean_lse = qad.attn_fwd_cache(q.cuda(), c.gpu(), _roomy(c).cuda(), ints(lens), return_lse=True)
     at = 350 - 20             # seen by the last twenty queries of sequence 0
     p, o = int(c.table[0, at // 32]), at % 32
     for which in ("k", "v", "both"):
@@ -156,7 +163,7 @@ def test_a_row_that_is_not_finite_reaches_only_what_sees_it(Sq, value):
         if which != "k":
             gpu[3][p, 1, o] = value
             gpu[2].view(torch.uint8)[p, 1, o] = 0           # as the cache has such a row
-        out, lse = qad.attn_fwd_cache(q.cuda(), gpu, c.table.cuda(), ints(lens), return_lse=True)
+        out, lse = qad.attn_fwd_cache(q.cuda(), gpu, _roomy(c).cuda(), ints(lens), return_lse=True)
         if which != "k" or math.isnan(value):
             assert torch.isnan(out[0, Sq - 20:, 2:]).all(), which
         assert torch.equal(bits(out[0, :Sq - 20]), bits(clean[0, :Sq - 20])), which
@@ -168,12 +175,12 @@ def test_scores_beyond_fp32_end_and_stay_in_their_rows():
     import quantized_attention_diffusion_gb300 as qad
     c = Cache([400], 1, 32, seed=12)
     q = _q(1, 50, 1, seed=13)
-    clean = qad.attn_fwd_cache(q.cuda(), c.gpu(), c.table.cuda(), ints([400]))
+    clean = qad.attn_fwd_cache(q.cuda(), c.gpu(), _roomy(c).cuda(), ints([400]))
     q[0, 7] = q[0, 7] * 2.0 ** 126
-    out = qad.attn_fwd_cache(q.cuda(), c.gpu(), c.table.cuda(), ints([400]))
+    out = qad.attn_fwd_cache(q.cuda(), c.gpu(), _roomy(c).cuda(), ints([400]))
     rest = [i for i in range(50) if i != 7]
     ro, _, to, _ = reference(q[0, rest].contiguous(), c.dense(0), False, SCALE)
-    full = qad.attn_fwd_cache(q.cuda(), c.gpu(), c.table.cuda(), ints([400]), causal=False)
+    full = qad.attn_fwd_cache(q.cuda(), c.gpu(), _roomy(c).cuda(), ints([400]), causal=False)
     assert_within(full[0, rest], ro, to)
     assert torch.allclose(out[0, rest].float(), clean[0, rest].float(), rtol=2.0 ** -6, atol=2.0 ** -6)
 
@@ -185,7 +192,7 @@ def test_bad_pages_are_reported_and_reach_nothing_else(Sq):
     lens = [200, 400, 300]
     c = Cache(lens, 2, 32, seed=20, extra=[170])
     q = _q(3, Sq, 2, seed=21)
-    table = c.table.clone()
+    table = _roomy(c)
     table[1, 1] = c.num_pages
     table[1, 2] = -5
     table[1, 9] = -2 ** 31
@@ -199,9 +206,9 @@ def test_bad_pages_are_reported_and_reach_nothing_else(Sq):
     # A bad page of the prefix.
     pre = c.table[3].clone()
     pre[4] = 2 ** 31 - 1
-    qad.attn_fwd_cache_prefix(q.cuda(), c.gpu(), pre.cuda(), 170, c.table[:3].cuda(), ints(lens))
+    qad.attn_fwd_cache_prefix(q.cuda(), c.gpu(), pre.cuda(), 170, _roomy(c)[:3].cuda(), ints(lens))
     assert qad.sync_status() == bad_page
-    qad.attn_fwd_cache_prefix(q.cuda(), c.gpu(), pre.cuda(), 128, c.table[:3].cuda(), ints(lens))   # not reached
+    qad.attn_fwd_cache_prefix(q.cuda(), c.gpu(), pre.cuda(), 128, _roomy(c)[:3].cuda(), ints(lens))   # not reached
     assert qad.sync_status() == 0
 
 
@@ -219,9 +226,9 @@ def test_the_workspace_ends_where_it_says_and_the_cache_is_only_read():
         lse = torch.full((4, H * G, Sq), -7.0, device="cuda")
         kw = dict(out=out[:3], lse=lse[:3], workspace=buf[:need])
         if prefix:
-            qad.attn_fwd_cache_prefix(q, gpu, c.table[3].cuda(), prefix, c.table[:3].cuda(), ints(lens), **kw)
+            qad.attn_fwd_cache_prefix(q, gpu, c.table[3].cuda(), prefix, _roomy(c)[:3].cuda(), ints(lens), **kw)
         else:
-            qad.attn_fwd_cache(q, gpu, c.table[:3].cuda(), ints(lens), **kw)
+            qad.attn_fwd_cache(q, gpu, _roomy(c)[:3].cuda(), ints(lens), **kw)
         assert (buf[need:] == 0x5A).all() and (out[3] == -7).all() and (lse[3] == -7).all()
         _check(out[:3], lse[:3], q.cpu(), c, True, prefix=3 if prefix else None)
     for a, b in zip(before, gpu):
@@ -232,7 +239,7 @@ def test_codes_of_v_as_bytes_and_pages_that_sequences_share():
     import quantized_attention_diffusion_gb300 as qad
     c = Cache([320], 2, 64, seed=32)
     kc, ks, vc, vs = c.gpu()
-    table = c.table.cuda().expand(3, -1)                     # one table for three sequences
+    table = _roomy(c).cuda().expand(3, -1)                   # one table for three sequences
     lens = [320, 100, 64]
     for Sq in (1, 40):
         q = _q(3, Sq, 4, seed=33 + Sq).cuda()
@@ -249,7 +256,7 @@ def test_captured_and_replayed_on_another_stream():
     import quantized_attention_diffusion_gb300 as qad
     c = Cache([900, 300], 2, 64, seed=34, extra=[400])
     q = _q(2, 80, 4, seed=35).cuda()
-    gpu, table, pre = c.gpu(), c.table[:2].cuda(), c.table[2].cuda()
+    gpu, table, pre = c.gpu(), _roomy(c)[:2].cuda(), c.table[2].cuda()
     first, second = ints([900, 300]), ints([80, 0])
     want = [(bits(qad.attn_fwd_cache(q, gpu, table, n)), bits(qad.attn_fwd_cache_prefix(q, gpu, pre, 400, table, n)))
             for n in (first, second)]
