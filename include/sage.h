@@ -403,14 +403,18 @@ sage_status sage_kv_cache_read(const sage_kv_cache* cache, const int32_t* block_
  *                   Sq + i; zero: it sees all lens[b]
  *   out        out: bf16 [B, Sq, Hq, D], 32-byte aligned: softmax(q K^T *
  *                   softmax_scale) V with K and V as the cache's codes and
- *                   scales say, FP32 scores, weights and sums; zeros for a
- *                   query that sees nothing
+ *                   scales say, FP32 scores and sums, each weight (times its
+ *                   key's scale of V) rounded to fp16 before it multiplies V's
+ *                   code; zeros for a query that sees nothing.  A query's
+ *                   scores have to be finite in FP32
  *   lse        out: fp32 [B, Hq, Sq] or NULL: log sum exp of the scores (-inf
  *                   for a query that sees nothing)
  *   workspace  caller-owned, 256-byte aligned, of at least
  *              sage_attn_fwd_cache_workspace_bytes(...) bytes, or NULL with
  *              workspace_bytes 0: taken from the library's pool in stream order.
- *              Calls that share a workspace must not overlap on the GPU.
+ *              Calls that share a workspace must not overlap on the GPU.  Few
+ *              short sequences (by what block_table has room for) need none and
+ *              leave it alone.
  * Sq = 1 is the generation step, Sq > 1 a chunk of a prompt or drafted tokens.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, NO_MEMORY, CUDA.
  */
@@ -427,7 +431,8 @@ sage_status sage_attn_fwd_cache(const void* q, int64_t q_stride_b, int64_t q_str
  * followed by the lens[b] positions of its row of block_table, and the result
  * is that of sage_attn_fwd_cache on the sequences put together (up to the
  * order of the sums); the prefix is read and multiplied once for the queries of
- * all sequences.  prefix_len >= 1 is a host value of at most 2^30, and need
+ * all sequences, or, where a few sequences and a short prefix are done sooner
+ * that way, by each.  prefix_len >= 1 is a host value of at most 2^30, and need
  * not fill its last page.  With causal, query i of sequence b sees the
  * positions <= prefix_len + lens[b] - Sq + i of the whole.
  * Other arguments and errors as sage_attn_fwd_cache.

@@ -15,12 +15,22 @@
 // 2^(y_j - M), below 2^8 whatever the scales of V are, in fp16 (a relative
 // rounding of 2^-11 or less for every weight above 2^-14 of 2^M, and 2^-25 of
 // 2^M below), and out = 2^(M - m) / L * sum.
+// fp16 and not bf16: its step is an eighth.
+//
+// Three kernels share the work.  cache_attn_kernel (up to 16 rows to a key/value head)
+// is bound by HBM, 264 bytes a key: one token of 65536 keys x 24 heads 70 us, 5.9 TB/s,
+// 0.87 of the measured copy rate; 48 ragged sequences of up to 16384 keys x 8 heads
+// 115 us, 0.88.  What is left is the start of each CTA's ring and the merge launch.
+// cache_attn_cluster_kernel takes what is too small for that, cache_attention_wide.cu
+// more rows.
+//
 // Q enters as fp16 times a power of two that puts the row's largest magnitude
 // in [2^14, 2^15), and K's integer codes are exact in fp16, so that the
 // products of Q and K are exact but for values 2^-28 below the row's largest.
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 #include <cuda_runtime.h>
 
 #include "cache_attention.cuh"
@@ -32,7 +42,7 @@ using namespace cache;
 namespace {
 
 constexpr int kTok = 64;                                  // keys per tile
-constexpr int kCost = 2;                                  // of a unit, in tiles
+constexpr int kCost = 2;                                  // of a unit, in tiles (1, 4 and 6: the same within 1%)
 constexpr int kConsumers = 4;                             // warps that compute, 16 keys of a tile each
 constexpr int kThreads = (kConsumers + 1) * 32;           // and one that copies
 constexpr uint32_t kOffV = kTok * kHeadDim;
@@ -42,7 +52,8 @@ constexpr uint32_t kStageBytes = kOffVs + kTok * 4;
 constexpr uint32_t kMergeBytes = kConsumers * 8 * kHeadDim * 4;
 constexpr int kClusterTiles = 16;                         // most tiles of an SM slot, in clusters
 constexpr int kMaxCtas = 3 * kSms;                        // CTAs of a launch: three on each SM
-// As many as the registers of NT times 8 query rows allow without spilling much.
+// As many as the registers of NT times 8 query rows allow without spilling much
+// (65536 keys x 24 heads, one row: three 74 us, two 79).
 __host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
 // Tiles in flight: 9 or 8 on an SM, 135 KB or more.
 __host__ __device__ constexpr int stages_of(int nt) { return nt == 1 ? 3 : 4; }
@@ -556,8 +567,8 @@ __device__ __forceinline__ float4 load_cluster4(uint32_t addr) {
 // workspace where the kernel above takes two, or three behind a prefix.  A prefix is
 // then read once for each sequence, from L2.  What bounds it is one chain of
 // latencies: the length, the pages, the copies, the products, the join.
-template <bool kPrefix>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(1)) cache_attn_cluster_kernel(const Params p, const int32_t* prefix_pages, int ctas) {
+template <int ctas, bool kPrefix>
+__global__ void __cluster_dims__(ctas, 1, 1) __launch_bounds__(kThreads, ctas_per_sm(1)) cache_attn_cluster_kernel(const Params p, const int32_t* prefix_pages) {
   constexpr int R = 8, kStages = stages_of(1);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kStages], empty[kStages], q_full;
@@ -702,20 +713,16 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(1)) cache_attn_cluster_k
     // A warp a row, four channels a lane.
     for (int row = rank * kConsumers + warp; row < rows; row += ctas * kConsumers) {
       float m = kLowest, M = kLowest, L = 0.0f;
-      float4 ml[8], acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f), part[8];
+      float4 ml[ctas], part[ctas], acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        ml[k] = make_float4(kLowest, 0.0f, kLowest, 0.0f);
-        part[k] = acc;
-        if (k < ctas) {
-          ml[k] = load_cluster4(in_cta(smem_addr(&s_ml[row]), k));
-          part[k] = load_cluster4(in_cta(smem0 + row * kHeadDim * 4 + lane * 16, k));
-        }
+      for (int k = 0; k < ctas; ++k) {
+        ml[k] = load_cluster4(in_cta(smem_addr(&s_ml[row]), k));
+        part[k] = load_cluster4(in_cta(smem0 + row * kHeadDim * 4 + lane * 16, k));
         m = fmaxf(m, ml[k].x);
         M = fmaxf(M, ml[k].z);
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < ctas; ++k) {
         L += ml[k].y * ex2_approx(ml[k].x - m);
         const float w = ex2_approx(ml[k].z - M);
         acc = make_float4(acc.x + part[k].x * w, acc.y + part[k].y * w, acc.z + part[k].z * w, acc.w + part[k].w * w);
@@ -996,25 +1003,19 @@ cudaError_t launch_clusters(const CacheAttnArgs& a, int ctas, cudaStream_t strea
   p.timeout_ns = a.timeout_ns;
   p.err = a.err;
   const uint32_t smem = smem_of(1);
-  auto go = [&](auto kernel) {
+  auto go = [&](auto size) {
+    constexpr int kCtas = decltype(size)::value;
     static std::atomic<uint64_t> allowed[2];           // for each kernel
-    cudaError_t e = allow_smem(kernel, smem, allowed[a.prefix_len > 0]);
+    auto kernel = a.prefix_len > 0 ? cache_attn_cluster_kernel<kCtas, true> : cache_attn_cluster_kernel<kCtas, false>;
+    const cudaError_t e = allow_smem(kernel, smem, allowed[a.prefix_len > 0]);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.B) * p.row_tiles * a.cache.H * ctas);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ctas;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p, a.prefix_pages, ctas);
+    kernel<<<static_cast<unsigned>(a.B) * p.row_tiles * a.cache.H * kCtas, kThreads, smem, stream>>>(p, a.prefix_pages);
+    return cudaGetLastError();
   };
-  return a.prefix_len > 0 ? go(cache_attn_cluster_kernel<true>) : go(cache_attn_cluster_kernel<false>);
+  return ctas == 8   ? go(std::integral_constant<int, 8>())
+         : ctas == 4 ? go(std::integral_constant<int, 4>())
+         : ctas == 2 ? go(std::integral_constant<int, 2>())
+                     : go(std::integral_constant<int, 1>());
 }
 
 }  // namespace

@@ -31,6 +31,16 @@
 // the second product's A operand from there; V is its B operand with the keys as
 // the outer index, as the cache has it.
 //
+// What bounds it is the path of 128 bytes a clock that shared memory, L1, TMEM loads and
+// stores and the products' operands in shared memory share (l1tex at 60% of its peak and the
+// tensor cores' reads beside it), and in tiles of at most 128 rows the conversion, whose
+// loads wait for L1 lines that 200 KB of shared memory leave few of.  2 x 1000 tokens
+// x 16 heads over up to 9000 keys: 203 us, 614 TFLOP/s, 0.32 of the measured bf16 rate
+// (the same rows in mma.sync tiles of 32: 842 us); 24 x 5 tokens x 16 heads over a prefix
+// of 32760: 83 us.  With V's scales multiplied into bf16 values the chunk took 183 us, and
+// its outputs were 1.6 times as far from 64 bits.  64 keys a tile (more copies in flight,
+// twice the barriers) took 244 us; TMEM shapes that give a thread four rows, 238 us.
+//
 // A row's references move where 32 weights may pass 2^14 in sum, by a whole number:
 // then the thread scales the row's sum, its accumulator and the weights of this
 // buffer that it has stored already by a power of two, which is exact, and forms
@@ -45,8 +55,8 @@ namespace sage::cache {
 namespace {
 
 constexpr int kThreads = 20 * 32;
-// Registers of the five warpgroups: a launch of 640 threads has 96 each, and the
-// softmax needs 128.
+// Registers of the five warpgroups: a launch of 640 threads has 96 each; with these
+// nothing spills.
 constexpr int kRegsConvert = 88, kRegsSoftmax = 120, kRegsIssue = 64;
 static_assert(2 * kRegsConvert + 2 * kRegsSoftmax + kRegsIssue <= 5 * 96, "more registers than the launch has");
 constexpr uint32_t kHalf = 128 * 128;                   // 128 rows of 64 16-bit values

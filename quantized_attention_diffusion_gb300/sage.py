@@ -716,12 +716,13 @@ def attn_fwd_cache(q, cache, block_table, lens, softmax_scale: float | None = No
                    lse=None, return_lse: bool = False, workspace=None):
     """Attention of q, bf16 [B, Sq, Hq, 128], the newest Sq tokens of each
     sequence, over the lens[b] positions that each has in the cache (their own
-    among them), through sage_attn_fwd_cache: query head h reads key/value head h
-    // (Hq // H).  Returns out bf16 [B, Sq, Hq, 128], and lse fp32 [B, Hq, Sq]
+    among them), through sage_attn_fwd_cache: query head h reads key/value head
+    h // (Hq // H).  Returns out bf16 [B, Sq, Hq, 128], and lse fp32 [B, Hq, Sq]
     with ``return_lse`` or when ``lse`` is given.  With ``causal`` query i sees
     positions up to lens[b] - Sq + i; a query that sees nothing gives zeros and
     -inf.  ``workspace`` (optional uint8 CUDA tensor of >=
-    attn_fwd_cache_workspace_bytes) replaces the library's pool."""
+    attn_fwd_cache_workspace_bytes) replaces the library's pool; few short
+    sequences need none."""
     return _attn_fwd_cache(q, cache, None, block_table, lens, softmax_scale, causal, out, lse, return_lse, workspace)
 
 
@@ -731,6 +732,7 @@ def attn_fwd_cache_prefix(q, cache, prefix_table, prefix_len: int, block_table, 
     """attn_fwd_cache for sequences that all begin with the same prefix_len
     positions, pages ``prefix_table`` (int32 [pages]): sequence b is the prefix
     and then the lens[b] positions of its row of ``block_table``.  The prefix is
-    read and multiplied once for all sequences (sage_attn_fwd_cache_prefix)."""
+    read and multiplied once for all sequences, unless a few and a short prefix
+    are done sooner without (sage_attn_fwd_cache_prefix)."""
     return _attn_fwd_cache(q, cache, (prefix_table, int(prefix_len)), block_table, lens, softmax_scale, causal, out,
                            lse, return_lse, workspace)
