@@ -333,7 +333,7 @@ sage_status sage_debug_staging_codes(const void* q, const void* k, int B, int S,
  * num_pages * H * page_size <= 2^31 - 1.
  * Position i of sequence b is token i % page_size of page
  * block_table[b * table_stride + i / page_size]; a table has table_width
- * entries a row, of which a call reads those that its positions need.
+ * entries a row, of which a call uses those that its positions need.
  * Sequences may share pages; a page that a call writes has one owner and one
  * place in its table (else those positions' contents are unspecified).
  * Lengths, starts and counts are device arrays, so that a recorded graph

@@ -164,6 +164,13 @@ def _q(B, Sq, Hq, seed, mul=1.0):
     return (torch.randn((B, Sq, Hq, D), generator=g) * mul).to(torch.bfloat16)
 
 
+def _roomy(table, page):
+    """The table with room for far more keys: the work is cut up over all CTAs
+    whatever the lengths, where a narrow table lets clusters of CTAs take a unit each."""
+    width = -(-20000 // page)
+    return torch.nn.functional.pad(table, (0, max(0, width - table.shape[1])), value=-1)
+
+
 def _check(out, lse, q, c, causal, scale=SCALE, prefix=None, what=""):
     for b in range(q.shape[0]):
         rows = c.dense(b) if prefix is None else join(c.dense(prefix), c.dense(b))
@@ -227,13 +234,6 @@ def test_shared_prefix(P, lens, Sq, H, G, page, causal):
     out, lse = qad.attn_fwd_cache_prefix(q.cuda(), c.gpu(), c.table[B].cuda(), P, c.table[:B].cuda(), ints(lens),
                                          causal=causal, return_lse=True)
     _check(out, lse, q, c, causal, prefix=B)
-
-
-def _roomy(table, page):
-    """The table with room for far more keys: the work is cut up over all CTAs
-    whatever the lengths, where a narrow table lets clusters of CTAs take a unit each."""
-    width = -(-20000 // page)
-    return torch.nn.functional.pad(table, (0, max(0, width - table.shape[1])), value=-1)
 
 
 @pytest.mark.parametrize("lens,Sq,H,G,page", [(n, 1, H, G, page) for n, H, G, page in STEP] + CHUNK[:6])
@@ -353,10 +353,11 @@ def test_more_sequences_than_one_launch_takes():
     c = Cache(lens, 1, 16, seed=16, extra=[70])
     q = _q(B, 1, 2, seed=17)
     gpu = c.gpu()
-    out, lse = qad.attn_fwd_cache(q.cuda(), gpu, c.table[:B].cuda(), ints(lens), return_lse=True)
-    _check(out, lse, q, c, True)
-    out, lse = qad.attn_fwd_cache_prefix(q.cuda(), gpu, c.table[B].cuda(), 70, c.table[:B].cuda(), ints(lens), return_lse=True)
-    _check(out, lse, q, c, True, prefix=B)
+    for table in (c.table[:B].cuda(), _roomy(c.table[:B], 16).cuda()):
+        out, lse = qad.attn_fwd_cache(q.cuda(), gpu, table, ints(lens), return_lse=True)
+        _check(out, lse, q, c, True)
+        out, lse = qad.attn_fwd_cache_prefix(q.cuda(), gpu, c.table[B].cuda(), 70, table, ints(lens), return_lse=True)
+        _check(out, lse, q, c, True, prefix=B)
 
 
 def test_pages_behind_four_gigabytes():
@@ -374,12 +375,21 @@ def test_pages_behind_four_gigabytes():
     kr, vr = qad.kv_cache_read(cache, table, ints([n]), n)
     assert torch.equal(bits(kr), bits((codes[0].float() * codes[1][..., None]).to(torch.bfloat16)))
     assert torch.equal(bits(vr), bits((codes[2].float() * codes[3][..., None]).to(torch.bfloat16)))
-    q = _q(1, 1, 4, seed=19)
     rows = (codes[0][0].double(), codes[1][0].double(), codes[2][0].float().double(), codes[3][0].double())
-    ro, rl, to, tl = reference(q[0], rows, True, SCALE)
-    out, lse = qad.attn_fwd_cache(q.cuda(), cache, table, ints([n]), return_lse=True)
-    assert_within(out[0], ro, to)
-    assert_within(lse[0], rl, tl)
+    for Sq in (1, 5, 40):
+        q = _q(1, Sq, 4, seed=19 + Sq)
+        ro, rl, to, tl = reference(q[0], rows, True, SCALE)
+        for t in (table, _roomy(table, page)):
+            out, lse = qad.attn_fwd_cache(q.cuda(), cache, t, ints([n]), return_lse=True)
+            assert_within(out[0], ro, to)
+            assert_within(lse[0], rl, tl)
+        new = ints([70001]).view(1, 1)                      # the prefix's pages, and one behind
+        codes_at = tuple(torch.cat([x, x[page:2 * page]]) for x in rows)
+        ro, rl, to, tl = reference(q[0], codes_at, False, SCALE)
+        for t in (new, _roomy(new, page)):
+            out, lse = qad.attn_fwd_cache_prefix(q.cuda(), cache, table[0], n, t, ints([page]), causal=False, return_lse=True)
+            assert_within(out[0], ro, to)
+            assert_within(lse[0], rl, tl)
 
 
 # ---------------------------------------------------- bad pages, streams --
@@ -393,11 +403,15 @@ def test_pages_outside_the_cache_are_reported_and_reach_nothing_else():
     table = c.table.clone()
     table[1, 1] = c.num_pages
     table[1, 2] = -5
-    out = qad.attn_fwd_cache(q.cuda(), c.gpu(), table.cuda(), ints(lens))
-    assert qad.sync_status() == bad_page and qad.sync_status() == 0
-    for b in (0, 2):
-        ro, _, to, _ = reference(q[b], c.dense(b), True, SCALE)
-        assert_within(out[b], ro, to)
+    for tab in (table, _roomy(table, 32)):
+        out = qad.attn_fwd_cache(q.cuda(), c.gpu(), tab.cuda(), ints(lens))
+        assert qad.sync_status() == bad_page and qad.sync_status() == 0
+        for b in (0, 2):
+            ro, _, to, _ = reference(q[b], c.dense(b), True, SCALE)
+            assert_within(out[b], ro, to)
+        pre = torch.tensor([c.num_pages + 5, int(c.table[2, 0])], dtype=torch.int32)
+        qad.attn_fwd_cache_prefix(q.cuda(), c.gpu(), pre.cuda(), 40, _roomy(c.table, 32).cuda() if tab is not table else c.table.cuda(), ints(lens))
+        assert qad.sync_status() == bad_page and qad.sync_status() == 0
     k, v = qad.kv_cache_read(c.gpu(), table.cuda(), ints(lens), 300)
     assert qad.sync_status() == bad_page
     assert (k[1, 32:96] == 0).all() and torch.isfinite(k).all() and torch.isfinite(v).all()
@@ -436,11 +450,14 @@ def test_negative_lengths_are_empty():
     assert (k[0] == 0).all() and (k[1] != 0).any()
 
 
-def test_two_streams_and_a_graph_that_follows_the_lengths():
+@pytest.mark.parametrize("room", ["little", "much"])
+def test_two_streams_and_a_graph_that_follows_the_lengths(room):
     import quantized_attention_diffusion_gb300 as qad
     c = Cache([500, 900], 2, 64, seed=26, extra=[300])
     q = _q(2, 1, 8, seed=27).cuda()
     gpu, table, pre = c.gpu(), c.table[:2].cuda(), c.table[2].cuda()
+    if room == "much":
+        table = _roomy(table, 64)
     short, long = ints([100, 3]), ints([500, 900])
     want = [(bits(qad.attn_fwd_cache(q, gpu, table, n)), bits(qad.attn_fwd_cache_prefix(q, gpu, pre, 300, table, n)))
             for n in (short, long)]
