@@ -561,14 +561,46 @@ __device__ __forceinline__ float4 load_cluster4(uint32_t addr) {
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
   return v;
 }
+// The parts of a prefix's launch: closed form, since every unit has as many tiles.
+struct PrefixParts {
+  const float* o;
+  const float4* ml;
+  int R, slot_rows, n, cost, ctas;   // rows of a tile and of a slot, a unit's tiles and cost, CTAs
+  long long per;                     // steps of a CTA
+};
+
+// The parts that hold row `pr` of the prefix's rows, key/value head h of H.
+struct RowParts {
+  int n, slot, row;
+  __device__ RowParts(const PrefixParts& p, int pr, int h, int H) {
+    row = pr % p.R;
+    const int u = pr / p.R * H + h;
+    const long long f = static_cast<long long>(u) * (p.n + p.cost) + p.cost;   // its first tile's step
+    slot = static_cast<int>(div_floor(f, p.per));
+    n = static_cast<int>(div_floor(f + p.n - 1, p.per)) - slot + 1;
+    slot = n == 1 ? 2 * p.ctas + u : 2 * slot;
+  }
+  // Where part j stands among the slots' rows.
+  __device__ int64_t at(const PrefixParts& p, int j) const {
+    return static_cast<int64_t>(n == 1 ? slot : j == 0 ? slot + 1 : slot + 2 * j) * p.slot_rows + row;
+  }
+};
+
+// What the cluster kernel finds before a sequence's own keys.
+enum Before { kNothing, kPrefixTiles, kPrefixParts };
+
 // Few units of short sequences: a cluster of up to eight CTAs takes a unit, its CTAs
 // the key tiles in turn (the prefix's, if there is one, before the sequence's own), and
 // they join their parts through one another's shared memory: one launch and no
-// workspace where the kernel above takes two, or three behind a prefix.  A prefix is
-// then read once for each sequence, from L2.  What bounds it is one chain of
+// workspace where the kernel above takes two, or three behind a prefix.  A short prefix is
+// then read once for each sequence, from L2; behind a longer one, multiplied for all
+// sequences in a launch before (kPrefixParts), the join takes that launch's parts in
+// and no merge kernel follows.  What bounds it is one chain of
 // latencies: the length, the pages, the copies, the products, the join.
-template <int ctas, bool kPrefix>
-__global__ void __cluster_dims__(ctas, 1, 1) __launch_bounds__(kThreads, ctas_per_sm(1)) cache_attn_cluster_kernel(const Params p, const int32_t* prefix_pages) {
+template <int ctas, Before kBefore>
+__global__ void __cluster_dims__(ctas, 1, 1) __launch_bounds__(kThreads, ctas_per_sm(1))
+    cache_attn_cluster_kernel(const Params p, const int32_t* prefix_pages, const PrefixParts parts) {
+  constexpr bool kPrefix = kBefore == kPrefixTiles;
   constexpr int R = 8, kStages = stages_of(1);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kStages], empty[kStages], q_full;
@@ -709,6 +741,7 @@ __global__ void __cluster_dims__(ctas, 1, 1) __launch_bounds__(kThreads, ctas_pe
   }
   __syncwarp();
   cluster_sync_all();
+  if constexpr (kBefore == kPrefixParts) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp < kConsumers) {
     // A warp a row, four channels a lane.
     for (int row = rank * kConsumers + warp; row < rows; row += ctas * kConsumers) {
@@ -726,6 +759,43 @@ __global__ void __cluster_dims__(ctas, 1, 1) __launch_bounds__(kThreads, ctas_pe
         L += ml[k].y * ex2_approx(ml[k].x - m);
         const float w = ex2_approx(ml[k].z - M);
         acc = make_float4(acc.x + part[k].x * w, acc.y + part[k].y * w, acc.z + part[k].z * w, acc.w + part[k].w * w);
+      }
+      if constexpr (kBefore == kPrefixParts) {
+        const RowParts of(parts, b * p.rows + row0 + row, h, p.cache.H);
+        for (int k0 = 0; k0 < of.n; k0 += 32) {
+          float4 mine = make_float4(kLowest, 0.0f, kLowest, 0.0f);
+          if (k0 + lane < of.n) mine = parts.ml[of.at(parts, k0 + lane)];
+          float to = mine.x, tow = mine.z;
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) {
+            to = fmaxf(to, __shfl_xor_sync(0xFFFFFFFFu, to, d));
+            tow = fmaxf(tow, __shfl_xor_sync(0xFFFFFFFFu, tow, d));
+          }
+          to = fmaxf(to, m);
+          tow = fmaxf(tow, M);
+          const float a = ex2_approx(M - tow);
+          L *= ex2_approx(m - to);
+          acc = make_float4(acc.x * a, acc.y * a, acc.z * a, acc.w * a);
+          m = to;
+          M = tow;
+          float lw = mine.y * ex2_approx(mine.x - m);
+          const float w = ex2_approx(mine.z - M);
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) lw += __shfl_xor_sync(0xFFFFFFFFu, lw, d);
+          L += lw;
+          const int end = min(32, of.n - k0);
+          for (int k = 0; k < end; k += 8) {                   // eight parts in flight
+            float4 y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              y[i] = reinterpret_cast<const float4*>(parts.o + of.at(parts, k0 + min(k + i, end - 1)) * kHeadDim)[lane];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float wk = k + i < end ? __shfl_sync(0xFFFFFFFFu, w, (k + i) & 31) : 0.0f;
+              if (k + i < end) acc = make_float4(acc.x + y[i].x * wk, acc.y + y[i].y * wk, acc.z + y[i].z * wk, acc.w + y[i].w * wk);
+            }
+          }
+        }
       }
       const int t = (row0 + row) / p.G, hq = h * p.G + (row0 + row) % p.G;
       const float half = scale2(M - m), inv = L == 0.0f ? 0.0f : half / L;
@@ -747,11 +817,7 @@ struct MergeParams {
   const int4* desc;          // one key/value part alone
   const int2* info;          // a prefix and the sequences
   int ctas, R, slot_rows, rows, row_tiles, H;
-  // The prefix's parts: closed form, every unit has as many tiles.
-  const float* pre_o;
-  const float4* pre_ml;
-  int pre_R, pre_slot_rows, pre_n, pre_cost, pre_ctas;   // rows of a tile and of a slot, a unit's tiles and cost, CTAs
-  long long pre_per;                                     // steps of a CTA
+  PrefixParts pre;           // o null: none
   uint16_t* out;
   float* lse;
   int Sq, G, Hq;
@@ -792,17 +858,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const Mer
   float m = kLowest, M = kLowest, L = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (live) {
-    int pn = 0, pslot = 0, prow = 0;
-    if (p.pre_o != nullptr) {
-      const int pr = b * p.rows + rr;                        // row of the prefix's launch
-      prow = pr % p.pre_R;
-      const int u = pr / p.pre_R * p.H + h;
-      const long long f = static_cast<long long>(u) * (p.pre_n + p.pre_cost) + p.pre_cost;   // its first tile's step
-      pslot = static_cast<int>(div_floor(f, p.pre_per));
-      pn = static_cast<int>(div_floor(f + p.pre_n - 1, p.pre_per)) - pslot + 1;
-      pslot = pn == 1 ? 2 * p.pre_ctas + u : 2 * pslot;
-    }
-    const int total = n + pn;
+    const bool behind = p.pre.o != nullptr;
+    const RowParts of(p.pre, b * p.rows + rr, h, p.H);       // row b * rows + rr of the prefix's launch
+    const int total = n + (behind ? of.n : 0);
     auto place = [&](int k, const float*& o, const float4*& ml) {
       if (k < n) {
         const int slot = own >= 0 ? own : (k == 0 ? 2 * first + 1 : 2 * (first + k));
@@ -810,11 +868,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const Mer
         o = p.part_o + at * kHeadDim;
         ml = p.part_ml + at;
       } else {
-        const int j = k - n;
-        const int slot = pn == 1 ? pslot : (j == 0 ? pslot + 1 : pslot + 2 * j);
-        const int64_t at = static_cast<int64_t>(slot) * p.pre_slot_rows + prow;
-        o = p.pre_o + at * kHeadDim;
-        ml = p.pre_ml + at;
+        const int64_t at = of.at(p.pre, k - n);
+        o = p.pre.o + at * kHeadDim;
+        ml = p.pre.ml + at;
       }
     };
     for (int k0 = 0; k0 < total; k0 += 32) {
@@ -928,8 +984,9 @@ T* at(void* base, size_t off) {
   return reinterpret_cast<T*>(static_cast<uint8_t*>(base) + off);
 }
 
-cudaError_t launch_part(const Params& p, int R, bool prefix, unsigned ctas, cudaStream_t stream) {
-  if (R == kWideRows) return launch_wide(p, prefix, ctas, stream);
+// beside: the launch before is this call's, and nothing of it is needed.
+cudaError_t launch_part(const Params& p, int R, bool prefix, bool beside, unsigned ctas, cudaStream_t stream) {
+  if (R == kWideRows) return launch_wide(p, prefix, beside, ctas, stream);
   const uint32_t smem = smem_of(R / 8);
   auto go = [&](auto kernel) {
     static std::atomic<uint64_t> allowed[2 * 2];       // for each kernel
@@ -940,12 +997,11 @@ cudaError_t launch_part(const Params& p, int R, bool prefix, unsigned ctas, cuda
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    // The prefix's launch follows the sequences' and needs nothing of it.
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = prefix ? 1 : 0;
+    cfg.numAttrs = beside ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, p);
   };
   if (prefix)
@@ -967,11 +1023,11 @@ unsigned ctas_for(long long tiles, int R) {
 // 64 rows: 4 of 1024 20.6, 24.7; 12 of 512 28.8, 29.3; 24 of 256 (four CTAs) 36.1, 32.8.
 // 256 rows, 2 heads: 1 of 4096 20.6, 43.4; 24 of 256 (four CTAs) 37.0, 28.9.  Behind a prefix of
 // 1024, 4 rows: 6 sequences, 2 heads 8.7, 18.6; 24, 8 heads, 16.5, 27.7, of 4096 41.1, 32.9.
-int cluster_ctas(const CacheAttnArgs& a) {
+int cluster_ctas(const CacheAttnArgs& a, int prefix_len) {
   const int64_t rows = static_cast<int64_t>(a.Sq) * (a.Hq / a.cache.H);
   const int64_t units = a.B * ((rows + 7) / 8) * a.cache.H;   // of eight rows
   const int64_t room = std::min<int64_t>(kMaxCacheLen, static_cast<int64_t>(a.table.width) << a.cache.page_shift);
-  const int64_t tiles = (room + kTok - 1) / kTok + (a.prefix_len + kTok - 1) / kTok;
+  const int64_t tiles = (room + kTok - 1) / kTok + (prefix_len + kTok - 1) / kTok;
   const int most = max_ctas(8);
   int ctas = 8;
   while (ctas > 1 && (units * ctas > most || tiles <= ctas / 2)) ctas /= 2;
@@ -980,7 +1036,21 @@ int cluster_ctas(const CacheAttnArgs& a) {
   return waves * ((tiles + ctas - 1) / ctas) <= kClusterTiles ? ctas : 0;
 }
 
-cudaError_t launch_clusters(const CacheAttnArgs& a, int ctas, cudaStream_t stream) {
+// The same for the sequences' own keys behind a prefix that has a launch of its own,
+// whose parts the clusters join: where no row has more than 48 of those, which one warp
+// goes through (the merge kernel has up to eight on a row), and there are at most two
+// CTAs to an SM slot.  Both sides, us, of 64 .. 512 keys behind 16384, 4 rows, 8 heads:
+// 8 sequences 34.0, 40.1 .. 35.3, 39.9; 64 53.5, 56.4 .. 68.4, 66.9.  24 x 5 rows, 16 heads
+// behind 32768 76, 81 .. 81, 89; 128 (five CTAs) 305, 296.  2 heads, 8 rows (76 parts a
+// row) behind 8192: 8 sequences 33.4, 26.8.
+int joining_ctas(const CacheAttnArgs& a) {
+  const int rows = a.Sq * (a.Hq / a.cache.H);
+  if (a.B > kMaxBatch || static_cast<int64_t>(a.B) * ((rows + 7) / 8) * a.cache.H > 2 * max_ctas(8)) return 0;
+  const int all = a.B * rows, R = rows_per_tile(all), units = (all + R - 1) / R * a.cache.H;
+  return max_ctas(R) / units + 1 <= 48 ? cluster_ctas(a, 0) : 0;
+}
+
+cudaError_t launch_clusters(const CacheAttnArgs& a, int ctas, const PrefixParts* parts, cudaStream_t stream) {
   Params p = {};
   p.cache = a.cache;
   p.table = a.table;
@@ -1005,12 +1075,25 @@ cudaError_t launch_clusters(const CacheAttnArgs& a, int ctas, cudaStream_t strea
   const uint32_t smem = smem_of(1);
   auto go = [&](auto size) {
     constexpr int kCtas = decltype(size)::value;
-    static std::atomic<uint64_t> allowed[2];           // for each kernel
-    auto kernel = a.prefix_len > 0 ? cache_attn_cluster_kernel<kCtas, true> : cache_attn_cluster_kernel<kCtas, false>;
-    const cudaError_t e = allow_smem(kernel, smem, allowed[a.prefix_len > 0]);
+    static std::atomic<uint64_t> allowed[3];           // for each kernel
+    const int which = parts != nullptr ? kPrefixParts : a.prefix_len > 0 ? kPrefixTiles : kNothing;
+    auto kernel = which == kPrefixParts   ? cache_attn_cluster_kernel<kCtas, kPrefixParts>
+                  : which == kPrefixTiles ? cache_attn_cluster_kernel<kCtas, kPrefixTiles>
+                                          : cache_attn_cluster_kernel<kCtas, kNothing>;
+    const cudaError_t e = allow_smem(kernel, smem, allowed[which]);
     if (e != cudaSuccess) return e;
-    kernel<<<static_cast<unsigned>(a.B) * p.row_tiles * a.cache.H * kCtas, kThreads, smem, stream>>>(p, a.prefix_pages);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.B) * p.row_tiles * a.cache.H * kCtas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    // Behind the prefix's launch, whose parts are waited for before the join.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = which == kPrefixParts ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p, a.prefix_pages, parts != nullptr ? *parts : PrefixParts{});
   };
   return ctas == 8   ? go(std::integral_constant<int, 8>())
          : ctas == 4 ? go(std::integral_constant<int, 4>())
@@ -1040,16 +1123,17 @@ bool cache_attn_fits(int B, int Sq, int Hq, int Hkv, int page_size, int table_wi
          (prefix_len == 0 || fits(prefix_len, b * rows, 1, Hkv));
 }
 
-bool cache_attn_needs_workspace(const CacheAttnArgs& a) { return cluster_ctas(a) == 0; }
+bool cache_attn_needs_workspace(const CacheAttnArgs& a) { return cluster_ctas(a, a.prefix_len) == 0; }
 
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream) {
-  if (const int ctas = cluster_ctas(a); ctas > 0) return launch_clusters(a, ctas, stream);
+  if (const int ctas = cluster_ctas(a, a.prefix_len); ctas > 0) return launch_clusters(a, ctas, nullptr, stream);
   const int H = a.cache.H, G = a.Hq / H;
   const bool both = a.prefix_len > 0;
+  const int join_ctas = both ? joining_ctas(a) : 0;
   for (int b0 = 0; b0 < a.B; b0 += kMaxBatch) {
     const int B = std::min(kMaxBatch, a.B - b0);
     const Layout w = layout(a.Sq * G, B, H, both, 0);
-    Params p;
+    Params p = {};
     p.cache = a.cache;
     p.table = a.table;
     p.table.pages += b0 * a.table.stride;
@@ -1079,10 +1163,12 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream) 
     p.room = static_cast<int>(std::min<int64_t>(kMaxCacheLen, static_cast<int64_t>(a.table.width) << a.cache.page_shift));
     // The lengths are on the device: as many CTAs as the table has room for.
     const unsigned ctas = ctas_for(std::min<long long>(kMaxCtas, (static_cast<long long>(p.room) + keys_per_tile(w.R) - 1) / keys_per_tile(w.R) + unit_cost(w.R)) * w.units, w.R);
-    cudaError_t e = launch_part(p, w.R, false, ctas, stream);
+    cudaError_t e = join_ctas > 0 ? cudaSuccess : launch_part(p, w.R, false, false, ctas, stream);
     if (e != cudaSuccess) return e;
 
     MergeParams mp = {};
+    mp.pre.R = 1;                                          // no division by zero where there is none
+    mp.pre.per = 1;
     mp.part_o = p.part_o;
     mp.part_ml = p.part_ml;
     mp.desc = p.desc;
@@ -1114,22 +1200,23 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream) 
       const int n = (a.prefix_len + keys_per_tile(u.R) - 1) / keys_per_tile(u.R);
       const long long steps = static_cast<long long>(n + unit_cost(u.R)) * u.units;
       const unsigned pc = ctas_for(steps, u.R);
-      e = launch_part(p, u.R, true, pc, stream);
+      e = launch_part(p, u.R, true, join_ctas == 0, pc, stream);
       if (e != cudaSuccess) return e;
-      mp.pre_o = p.part_o;
-      mp.pre_ml = p.part_ml;
-      mp.pre_R = u.R;
-      mp.pre_slot_rows = u.slot_rows;
-      mp.pre_n = n;
-      mp.pre_cost = unit_cost(u.R);
-      mp.pre_per = (steps + pc - 1) / pc;
-      mp.pre_ctas = pc;
+      mp.pre.o = p.part_o;
+      mp.pre.ml = p.part_ml;
+      mp.pre.R = u.R;
+      mp.pre.slot_rows = u.slot_rows;
+      mp.pre.n = n;
+      mp.pre.cost = unit_cost(u.R);
+      mp.pre.per = (steps + pc - 1) / pc;
+      mp.pre.ctas = pc;
+      if (join_ctas > 0) return launch_clusters(a, join_ctas, &mp.pre, stream);
       pre_units = u.units;
     }
     // Warps of a row: so many that each adds about eight parts, and that few rows
     // leave none idle.
     const int tile_rows = std::min(w.R, w.rows);
-    const long long parts = ctas / w.units + 1 + (both ? mp.pre_ctas / std::max(1, pre_units) + 1 : 0);
+    const long long parts = ctas / w.units + 1 + (both ? mp.pre.ctas / std::max(1, pre_units) + 1 : 0);
     mp.split = 1;
     while (mp.split < kMergeWarps && (mp.split * 8 < parts || mp.split * 2 * tile_rows <= kMergeWarps)) mp.split *= 2;
     cudaLaunchConfig_t cfg = {};

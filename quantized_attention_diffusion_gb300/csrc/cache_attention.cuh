@@ -240,6 +240,6 @@ __device__ __forceinline__ void k_codes_f16(uint32_t w, uint32_t& lo, uint32_t& 
 // The launch of the kernel for many query rows (cache_attention_wide.cu): 256
 // rows and 128 keys a tile, one CTA on each SM.
 constexpr int kWideRows = 256, kWideTok = 128, kWideCost = 3;
-cudaError_t launch_wide(const Params& p, bool prefix, unsigned ctas, cudaStream_t stream);
+cudaError_t launch_wide(const Params& p, bool prefix, bool beside, unsigned ctas, cudaStream_t stream);
 
 }  // namespace sage::cache

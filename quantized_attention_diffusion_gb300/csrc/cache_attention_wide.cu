@@ -737,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
 
 }  // namespace
 
-cudaError_t launch_wide(const Params& p, bool prefix, unsigned ctas, cudaStream_t stream) {
+cudaError_t launch_wide(const Params& p, bool prefix, bool beside, unsigned ctas, cudaStream_t stream) {
   auto go = [&](auto kernel) {
     static std::atomic<uint64_t> allowed[2];           // for each kernel
     cudaError_t e = allow_smem(kernel, kSmemBytes, allowed[prefix]);
@@ -747,12 +747,12 @@ cudaError_t launch_wide(const Params& p, bool prefix, unsigned ctas, cudaStream_
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = stream;
-    // The prefix's launch follows the sequences' and needs nothing of it.
+    // beside: the launch before is this call's, and nothing of it is needed.
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = prefix ? 1 : 0;
+    cfg.numAttrs = beside ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, p);
   };
   return prefix ? go(cache_attn_wide_kernel<true>) : go(cache_attn_wide_kernel<false>);

@@ -259,6 +259,37 @@ def test_room_does_not_matter_behind_a_prefix(P, lens, Sq, H, G, page, causal):
         _check(out, lse, q, c, causal, prefix=B)
 
 
+LONG = [
+    # prefix, lens, Sq, H, G, page: more of a prefix than clusters take, little room behind it
+    (9000, [5, 0, 63], 1, 10, 1, 64), (9000, [64, 1], 1, 8, 8, 128), (9001, [3, 70, 0, 9] * 3, 1, 4, 4, 16), (8300, [7, 2, 20], 3, 8, 5, 32),
+]
+
+
+@pytest.mark.parametrize("P,lens,Sq,H,G,page", LONG)
+@pytest.mark.parametrize("causal", [True, False])
+def test_joined_behind_a_long_prefix(P, lens, Sq, H, G, page, causal):
+    import quantized_attention_diffusion_gb300 as qad
+    B = len(lens)
+    c = Cache(lens, H, page, seed=P + Sq, extra=[P], recipe="sharp")
+    q = _q(B, Sq, H * G, seed=P + 2).cuda()
+    gpu, pre, own = c.gpu(), c.table[B].cuda(), c.table[:B, :-(-max(lens) // page)].contiguous().cuda()
+    need = qad.attn_fwd_cache_workspace_bytes(B, Sq, H * G, H, P)
+    buf = torch.full((need + 256,), 0x5A, dtype=torch.uint8, device="cuda")
+    out, lse = qad.attn_fwd_cache_prefix(q, gpu, pre, P, own, ints(lens), causal=causal, return_lse=True, workspace=buf[:need])
+    _check(out, lse, q.cpu(), c, causal, prefix=B)
+    assert (buf[need:] == 0x5A).all()
+    n, none = ints(lens), torch.zeros(B, dtype=torch.int32, device="cuda")
+    want = bits(qad.attn_fwd_cache_prefix(q, gpu, pre, P, own, none, causal=causal))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        again = qad.attn_fwd_cache_prefix(q, gpu, pre, P, own, n, causal=causal)
+    g.replay()
+    assert torch.equal(bits(again), bits(out))
+    n.zero_()
+    g.replay()
+    assert torch.equal(bits(again), want)
+
+
 def test_softmax_scale_and_large_scores():
     """Scores of hundreds: weights of one key only, and the running maximum's path."""
     import quantized_attention_diffusion_gb300 as qad
