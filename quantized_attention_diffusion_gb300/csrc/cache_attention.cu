@@ -14,8 +14,7 @@
 // sv_j and a reference M near the largest y_j the products are formed from
 // 2^(y_j - M), below 2^8 whatever the scales of V are, in fp16 (a relative
 // rounding of 2^-11 or less for every weight above 2^-14 of 2^M, and 2^-25 of
-// 2^M below), and out = 2^(M - m) / L * sum.
-// fp16 and not bf16: its step is an eighth.
+// 2^M below; bf16's step is eight times as wide), and out = 2^(M - m) / L * sum.
 //
 // Three kernels share the work.  cache_attn_kernel (up to 16 rows to a key/value head)
 // is bound by HBM, 264 bytes a key: one token of 65536 keys x 24 heads 70 us, 5.9 TB/s,
