@@ -45,7 +45,6 @@
 // then the thread scales the row's sum, its accumulator and the weights of this
 // buffer that it has stored already by a power of two, which is exact, and forms
 // the 32 again.
-#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "cache_attention.cuh"
@@ -59,6 +58,7 @@ constexpr int kThreads = 20 * 32;
 // nothing spills.
 constexpr int kRegsConvert = 88, kRegsSoftmax = 120, kRegsIssue = 64;
 static_assert(2 * kRegsConvert + 2 * kRegsSoftmax + kRegsIssue <= 5 * 96, "more registers than the launch has");
+static_assert(kRegsConvert <= 96 && kRegsIssue <= 96 && kRegsSoftmax >= 96, "a share given up cannot grow, one taken cannot shrink");
 constexpr uint32_t kHalf = 128 * 128;                   // 128 rows of 64 16-bit values
 constexpr uint32_t kTileBytes = 2 * kHalf;
 constexpr uint32_t kSmemQ = 0;                          // two row tiles
