@@ -685,7 +685,7 @@ def _attn_fwd_cache(q, cache, prefix, block_table, lens, softmax_scale, causal, 
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=q.device)
+        out = torch.empty_like(q) if q.is_contiguous() else torch.empty(shape, dtype=_BF16, device=q.device)
     elif out.shape != shape or out.dtype is not _BF16 or not out.is_contiguous() or out.get_device() != dev:
         raise ValueError("out must be a contiguous bf16 tensor of q's shape on its device")
     if lse is None:
