@@ -521,7 +521,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
           };
           for (v = 0; v < nv; ++v) {
             const int j = by_rows ? v >> 1 : (v & ~1) + t, slot = (it + j) % kScaleSlots, sub = (v & 1) * kSub;
-            ok = wait(&bars.scales[slot], (it + j) / kScaleSlots) && wait(&bars.s_full[t][v & 1], (done + v) >> 1);
+            // In this order: a half passes over tiles that are not its own, and only the
+            // scores say that the slot's phase before this tile's has ended.
+            ok = wait(&bars.s_full[t][v & 1], (done + v) >> 1) && wait(&bars.scales[slot], (it + j) / kScaleSlots);
             if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
             tc_fence_after();
             const uint32_t tS = tmem + lanes + col_s(t, 0) + sub;
@@ -667,6 +669,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
           if (!wait(&full[s], g >> 1)) break;
           const int tile = *const_cast<const volatile int*>(&info[s]);
           if ((tile & kTileEnd) != 0) break;
+          // The scales of the tile two before have been there for long; with them, since
+          // scales come in order, the last phase of this tile's slot has ended, and a
+          // softmax that has the scores waits for the right one.  (A wait for a parity
+          // tells a phase from the next one alone.)  These threads see every tile, and
+          // no slot is used again before they have freed a stage behind it.
+          if (!is_pv && g >= 2 && !wait(&bars.scales[(g - 2) % kScaleSlots], (g - 2) / kScaleSlots)) break;
           const bool by_rows = (tile & kTileByRows) != 0;
           // Each of Q's barriers is waited for by one thread in every one of its phases,
           // so that it is never two phases ahead of that thread.
