@@ -337,7 +337,10 @@ sage_status sage_debug_staging_codes(const void* q, const void* k, int B, int S,
  * Sequences may share pages; a page that a call writes has one owner and one
  * place in its table (else those positions' contents are unspecified).
  * Lengths, starts and counts are device arrays, so that a recorded graph
- * follows them; a sequence has at most 2^30 positions.
+ * follows them; a sequence has at most 2^30 positions.  For the attention a
+ * length of 2^30 or more means all that its row of the table has room for (or
+ * 2^30, if that is less), and any other length behind the table is an error as
+ * below.
  * A table entry outside [0, num_pages), or a position that the table does not
  * reach, is an error that the device finds: the position is not written, or
  * reads as zeros (sage_kv_cache_read), or makes its sequence's attention

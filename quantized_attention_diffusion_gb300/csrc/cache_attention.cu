@@ -650,7 +650,7 @@ __global__ void __cluster_dims__(ctas, 1, 1) __launch_bounds__(kThreads, ctas_pe
       return my_run < runs && at < width ? __ldg(row + at) : -1;
     };
     int next = page_of(rank);
-    const int len = max(0, min(p.room, len_raw)), n = np + (len + kTok - 1) / kTok;
+    const int len = held(len_raw, p), n = np + (len + kTok - 1) / kTok;
     int it = 0;
     bool bad = false;
     for (int t = rank; t < n; t += ctas, ++it) {

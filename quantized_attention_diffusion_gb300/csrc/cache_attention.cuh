@@ -66,6 +66,13 @@ struct Place {
   int t0, t1;                // tiles of the segment
 };
 
+// A sequence's length, cut to what its table has room for: an error, except that
+// kMaxCacheLen or more asks for just that.
+__device__ __forceinline__ int held(int len, const Params& p) {
+  if (len > p.room && len < kMaxCacheLen) atomicExch(p.err, SAGE_DEVERR_BAD_PAGE);
+  return max(0, min(p.room, len));
+}
+
 // R query rows and Tok keys a tile.
 template <int R, int Tok, int Cost, bool kPrefix>
 struct Walk {
@@ -150,7 +157,7 @@ struct Walk {
   // calls it; a barrier has to follow.
   __device__ void plan(int* len, long long* off) const {
     if constexpr (kPrefix) {
-      for (int i = threadIdx.x; i < p.B; i += blockDim.x) len[i] = max(0, min(p.room, __ldg(p.lens + i)));
+      for (int i = threadIdx.x; i < p.B; i += blockDim.x) len[i] = held(__ldg(p.lens + i), p);
       if (threadIdx.x == 0) {
         off[0] = 0;
         off[1] = static_cast<long long>(p.row_tiles) * (tiles(0, 0) + Cost);
@@ -160,7 +167,7 @@ struct Walk {
       long long base = 0;
       int next = lane < p.B ? __ldg(p.lens + lane) : 0;
       for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const int b = b0 + lane, mine = max(0, min(p.room, next));
+        const int b = b0 + lane, mine = held(next, p);
         if (b + 32 < p.B) next = __ldg(p.lens + b + 32);
         long long n = 0;
         if (b < p.B) {

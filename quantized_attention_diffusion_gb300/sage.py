@@ -720,7 +720,9 @@ def attn_fwd_cache(q, cache, block_table, lens, softmax_scale: float | None = No
     h // (Hq // H).  Returns out bf16 [B, Sq, Hq, 128], and lse fp32 [B, Hq, Sq]
     with ``return_lse`` or when ``lse`` is given.  With ``causal`` query i sees
     positions up to lens[b] - Sq + i; a query that sees nothing gives zeros and
-    -inf.  ``workspace`` (optional uint8 CUDA tensor of >=
+    -inf.  A length behind what ``block_table`` has room for is reported by
+    sync_status (SAGE_ERR_BAD_PAGE), except that 2**30 or more means all of it.
+    ``workspace`` (optional uint8 CUDA tensor of >=
     attn_fwd_cache_workspace_bytes) replaces the library's pool; few short
     sequences need none."""
     return _attn_fwd_cache(q, cache, None, block_table, lens, softmax_scale, causal, out, lse, return_lse, workspace)
