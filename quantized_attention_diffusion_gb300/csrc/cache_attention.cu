@@ -11,10 +11,12 @@
 // for any reference m near the largest x_j.  The query heads that share a
 // key/value head are rows of one tile, so the cache is read once for all of
 // them.  A row's weights of V are kept apart from its sum: with y_j = x_j + log2
-// sv_j and a reference M near the largest y_j the products are formed from
-// 2^(y_j - M), below 2^8 whatever the scales of V are, in fp16 (a relative
-// rounding of 2^-11 or less for every weight above 2^-14 of 2^M, and 2^-25 of
-// 2^M below; bf16's step is eight times as wide), and out = 2^(M - m) / L * sum.
+// sv_j and a reference M some 8 below the largest y_j the products are formed from
+// 2^(y_j - M), below 2^15 whatever the scales of V are, in fp16: the largest weight is
+// 2^8 or more, so that every weight down to 2^-22 of it is rounded by 2^-11 of itself at
+// most, and those below by 2^-33 of the largest (bf16's step is eight times as wide;
+// with M at the largest itself 65536 equal weights of 2^-18.7 lose 1% of their sum).
+// out = 2^(M - m) / L * sum.
 //
 // Three kernels share the work.  cache_attn_kernel (up to 16 rows to a key/value head)
 // is bound by HBM, 264 bytes a key: one token of 65536 keys x 24 heads 70 us, 5.9 TB/s,
@@ -57,7 +59,8 @@ __host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; 
 // Tiles in flight: 9 or 8 on an SM, 135 KB or more.
 __host__ __device__ constexpr int stages_of(int nt) { return nt == 1 ? 3 : 4; }
 constexpr uint32_t smem_of(int nt) { return stages_of(nt) * kStageBytes + kMergeBytes + 8 * nt * kHeadDim * 2; }
-constexpr float kFar = 256.0f, kFarLog2 = 8.0f;           // weights stay near or below it (fp16: 65504)
+constexpr float kFar = 32768.0f, kFarLog2 = 15.0f;        // most of a weight (fp16: 65504)
+constexpr float kAbove = 8.0f;                            // a reference M that moves goes so far below the largest
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -162,7 +165,7 @@ __device__ __forceinline__ void attend(QueryRows<NT>& z, const uint8_t* st, int 
       over |= fmaxf(pl[a][e], pw[a][e]) > kFar;
     }
   // The references m and M need not be the maxima, only near them: they move
-  // where a weight passes 2^8, which after the first keys is rare, and
+  // where a weight passes 2^15, which after the first keys is rare, and
   // otherwise no value crosses lanes.
   if (__any_sync(0xFFFFFFFFu, over)) {
 #pragma unroll
@@ -177,7 +180,9 @@ __device__ __forceinline__ void attend(QueryRows<NT>& z, const uint8_t* st, int 
           mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
           wx = fmaxf(wx, __shfl_xor_sync(0xFFFFFFFFu, wx, d));
         }
-        if (!(mx - z.m[a][e] > kFarLog2 || wx - z.mw[a][e] > kFarLog2)) {   // a row's result is its own alone
+        if (mx - z.m[a][e] > kFarLog2 || wx - z.mw[a][e] > kFarLog2) {
+          wx = fmaxf(z.mw[a][e], wx - kAbove);
+        } else {                      // a row's result is its own alone
           mx = z.m[a][e];
           wx = z.mw[a][e];
         }

@@ -4,7 +4,8 @@
 //
 // The formulas are cache_attention.cu's with one exponential a score: p = 2^(x - R)
 // serves the sum L, in fp32, and, times the key's scale of V and rounded to fp16, the
-// second product.  R is near the largest x + log2 sv so far, but at most 60 from the
+// second product.  R is some 6 below the largest x + log2 sv so far (weights down to
+// 2^-19 of the largest keep all their bits), but at most 60 from the
 // largest x; where V's scales are farther, a row's weights take a factor
 // f = 2^(R - M) more (1 otherwise) and its accumulator stands relative to M.  R and M
 // are whole numbers.  V's codes are exact in fp16.
@@ -41,7 +42,7 @@
 // its outputs were 1.6 times as far from 64 bits.  64 keys a tile (more copies in flight,
 // twice the barriers) took 244 us; TMEM shapes that give a thread four rows, 238 us.
 //
-// A row's references move where 32 weights may pass 2^14 in sum, by a whole number:
+// A row's references move where 32 weights may pass 2^15 in sum, by a whole number:
 // then the thread scales the row's sum, its accumulator and the weights of this
 // buffer that it has stored already by a power of two, which is exact, and forms
 // the 32 again.
@@ -66,8 +67,10 @@ constexpr uint32_t kSmemK = 2 * kTileBytes;             // two stages
 constexpr uint32_t kSmemV = 4 * kTileBytes;             // two stages
 constexpr uint32_t kSmemBytes = 6 * kTileBytes + 1024;  // and room to align to 1024
 constexpr int kScaleSlots = 4;                          // of ks and vs: up to three tiles ahead of the softmax
-constexpr float kFar = 16384.0f;                        // 2^14: most of 32 weights' sum (fp16: 65504)
-constexpr float kFarSum = 0x1p70f, kTiny = 0x1p-56f;    // most of 32 p's sum, and kFar / kFarSum
+constexpr float kFar = 32768.0f;                        // 2^15: most of 32 weights' sum (fp16: 65504)
+constexpr float kAbove = 6.0f;                          // a reference that moves goes so far below the largest weight:
+                                                        // 32 of that are a sixteenth of kFar
+constexpr float kFarSum = 0x1p70f, kTiny = 0x1p-55f;    // most of 32 p's sum, and kFar / kFarSum
 constexpr float kReach = 60.0f, kReachV = 140.0f;       // of R, and of M, below the largest score
 
 constexpr int kSub = 64;                                // keys of a score buffer
@@ -159,7 +162,7 @@ __device__ __forceinline__ bool move_references(uint32_t tS, const float* kx, co
   }
   float R = z.R, M = z.M;
   if (far) {                                               // a row's result is its own alone
-    M = fmaxf(M, ceilf(fmaxf(ym, xm - kReachV)));
+    M = fmaxf(M, ceilf(fmaxf(ym, xm - kReachV)) - kAbove);
     R = fmaxf(R, fminf(fmaxf(M, ceilf(xm) - kReach), ceilf(xm) + kReach));
   }
   const bool moved = R != z.R || M != z.M;
