@@ -409,7 +409,8 @@ sage_status sage_kv_cache_read(const sage_kv_cache* cache, const int32_t* block_
  *                   scales say, FP32 scores and sums, each weight (times its
  *                   key's scale of V) rounded to fp16 before it multiplies V's
  *                   code; zeros for a query that sees nothing.  A query's
- *                   scores have to be finite in FP32
+ *                   scores times log2 e have to be below 2^127 in magnitude,
+ *                   q and K below 2^90
  *   lse        out: fp32 [B, Hq, Sq] or NULL: log sum exp of the scores (-inf
  *                   for a query that sees nothing)
  *   workspace  caller-owned, 256-byte aligned, of at least

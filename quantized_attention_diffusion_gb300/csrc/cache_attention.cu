@@ -10,13 +10,14 @@
 //
 // for any reference m near the largest x_j.  The query heads that share a
 // key/value head are rows of one tile, so the cache is read once for all of
-// them.  A row's weights of V are kept apart from its sum: with y_j = x_j + log2
-// sv_j and a reference M some 8 below the largest y_j the products are formed from
-// 2^(y_j - M), below 2^15 whatever the scales of V are, in fp16: the largest weight is
-// 2^8 or more, so that every weight down to 2^-22 of it is rounded by 2^-11 of itself at
-// most, and those below by 2^-33 of the largest (bf16's step is eight times as wide;
-// with M at the largest itself 65536 equal weights of 2^-18.7 lose 1% of their sum).
-// out = 2^(M - m) / L * sum.
+// them.  A row's weights of V have a reference of their own, m + d, some 8 below the
+// largest x_j + log2 sv_j: the products are formed from 2^((x_j - m) + (log2 sv_j - d)),
+// below 2^15 whatever the scales of V are, in fp16.  The largest weight is 2^8 or more,
+// so that every weight down to 2^-22 of it is rounded by 2^-11 of itself at most, and
+// those below by 2^-33 of the largest (bf16's step is eight times as wide; with the
+// largest weight at 1, 65536 equal weights of 2^-18.7 lose 1% of their sum).  Then
+// out = 2^d / L * sum.  Scores come into the weights by their differences alone, as in
+// L: where they are so large that log2 sv is nothing to them, both still agree.
 //
 // Three kernels share the work.  cache_attn_kernel (up to 16 rows to a key/value head)
 // is bound by HBM, 264 bytes a key: one token of 65536 keys x 24 heads 70 us, 5.9 TB/s,
@@ -60,7 +61,8 @@ __host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; 
 __host__ __device__ constexpr int stages_of(int nt) { return nt == 1 ? 3 : 4; }
 constexpr uint32_t smem_of(int nt) { return stages_of(nt) * kStageBytes + kMergeBytes + 8 * nt * kHeadDim * 2; }
 constexpr float kFar = 32768.0f, kFarLog2 = 15.0f;        // most of a weight (fp16: 65504)
-constexpr float kAbove = 8.0f;                            // a reference M that moves goes so far below the largest
+constexpr float kAbove = 8.0f;                            // a weights' reference that moves goes so far below the largest
+constexpr float kLeast = -160.0f;                         // of d: scales of V are 0 or 2^-149 at least
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -104,17 +106,18 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 template <int NT>
 struct QueryRows {
   uint32_t q[NT][8][2];
-  float crow[NT][2];
+  float rk[NT][2];           // the row's factor
   int lim[NT][2];            // keys that the row sees
   float o[NT][8][4];         // channels 16r + 2j + e / 2, queries 2c + e % 2
-  float m[NT][2], mw[NT][2], l[NT][2];
+  float m[NT][2], d[NT][2], l[NT][2];
 };
 
 // 16 keys, t0 .. t0 + 15, which stand at row `at` of the tile at st.  hi: keys
 // that some row sees; lo: keys that all see.
 template <int NT>
-__device__ __forceinline__ void attend(QueryRows<NT>& z, const uint8_t* st, int t0, int at, int r, int c, int hi, int lo) {
-  float sc[NT][4], y[NT][4];
+__device__ __forceinline__ void attend(QueryRows<NT>& z, const uint8_t* st, float c_scale, int t0, int at, int r, int c, int hi,
+                                       int lo) {
+  float sc[NT][4], lw[NT][4];
 #pragma unroll
   for (int a = 0; a < NT; ++a)
 #pragma unroll
@@ -134,25 +137,28 @@ __device__ __forceinline__ void attend(QueryRows<NT>& z, const uint8_t* st, int 
     }
   }
   // sc[a][e]: key r + 8 (e / 2), query 2c + e % 2
-  float ks[2], lv[2];                 // of keys r and r + 8
+  float ks[2], lv[2];                 // of keys r and r + 8; K's times softmax_scale * log2 e
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
-    ks[n] = *reinterpret_cast<const float*>(st + kOffKs + (at + n * 8 + r) * 4);
+    ks[n] = *reinterpret_cast<const float*>(st + kOffKs + (at + n * 8 + r) * 4) * c_scale;
     lv[n] = lg2_approx(*reinterpret_cast<const float*>(st + kOffVs + (at + n * 8 + r) * 4));
   }
 #pragma unroll
   for (int a = 0; a < NT; ++a)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      sc[a][e] = (sc[a][e] * z.crow[a][e & 1]) * ks[e >> 1];
-      y[a][e] = sc[a][e] + lv[e >> 1];
+      sc[a][e] = __fmul_rn(sc[a][e] * z.rk[a][e & 1], ks[e >> 1]);     // rk is a power of two: rounded once
+      lw[a][e] = lv[e >> 1] - z.d[a][e & 1];
     }
   if (t0 + 16 > lo) {                 // some row does not see all of these keys
 #pragma unroll
     for (int a = 0; a < NT; ++a)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (t0 + r + 8 * (e >> 1) >= z.lim[a][e & 1]) sc[a][e] = y[a][e] = -INFINITY;
+        if (t0 + r + 8 * (e >> 1) >= z.lim[a][e & 1]) {
+          sc[a][e] = -INFINITY;
+          lw[a][e] = 0.0f;            // the scale may be anything
+        }
   }
   bool over = false;
   float pl[NT][4], pw[NT][4];
@@ -160,11 +166,12 @@ __device__ __forceinline__ void attend(QueryRows<NT>& z, const uint8_t* st, int 
   for (int a = 0; a < NT; ++a)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      pl[a][e] = ex2_approx(sc[a][e] - z.m[a][e & 1]);
-      pw[a][e] = ex2_approx(y[a][e] - z.mw[a][e & 1]);
+      const float t = sc[a][e] - z.m[a][e & 1];
+      pl[a][e] = ex2_approx(t);
+      pw[a][e] = ex2_approx(t + lw[a][e]);
       over |= fmaxf(pl[a][e], pw[a][e]) > kFar;
     }
-  // The references m and M need not be the maxima, only near them: they move
+  // The references m and m + d need not be the maxima, only near them: they move
   // where a weight passes 2^15, which after the first keys is rare, and
   // otherwise no value crosses lanes.
   if (__any_sync(0xFFFFFFFFu, over)) {
@@ -174,26 +181,25 @@ __device__ __forceinline__ void attend(QueryRows<NT>& z, const uint8_t* st, int 
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float mx = fmaxf(z.m[a][e], fmaxf(sc[a][e], sc[a][e + 2]));
-        float wx = fmaxf(z.mw[a][e], fmaxf(y[a][e], y[a][e + 2]));
+        float wx = fmaxf((sc[a][e] - mx) + lv[0], (sc[a][e + 2] - mx) + lv[1]);   // a masked key's is -inf or NaN
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
-          wx = fmaxf(wx, __shfl_xor_sync(0xFFFFFFFFu, wx, d));
-        }
-        if (mx - z.m[a][e] > kFarLog2 || wx - z.mw[a][e] > kFarLog2) {
-          wx = fmaxf(z.mw[a][e], wx - kAbove);
-        } else {                      // a row's result is its own alone
-          mx = z.m[a][e];
-          wx = z.mw[a][e];
-        }
+        for (int d = 4; d < 32; d <<= 1)
+          larger(mx, wx, __shfl_xor_sync(0xFFFFFFFFu, mx, d), __shfl_xor_sync(0xFFFFFFFFu, wx, d));
+        const float up = mx - z.m[a][e];
+        float dn = z.d[a][e];
+        if (up > kFarLog2 || up + (wx - dn) > kFarLog2)
+          dn = fmaxf(fmaxf(wx - kAbove, dn - up), kLeast);
+        else
+          mx = z.m[a][e];             // a row's result is its own alone
         z.l[a][e] *= ex2_approx(z.m[a][e] - mx);
-        alpha[e] = ex2_approx(z.mw[a][e] - wx);
+        alpha[e] = ex2_approx((z.m[a][e] - mx) + (z.d[a][e] - dn));
         z.m[a][e] = mx;
-        z.mw[a][e] = wx;
+        z.d[a][e] = dn;
 #pragma unroll
         for (int k = 0; k < 4; k += 2) {
-          pl[a][e + k] = ex2_approx(sc[a][e + k] - mx);
-          pw[a][e + k] = ex2_approx(y[a][e + k] - wx);
+          const float t = sc[a][e + k] - mx;
+          pl[a][e + k] = ex2_approx(t);
+          pw[a][e + k] = t == -INFINITY ? 0.0f : ex2_approx(t + (lv[k >> 1] - dn));
         }
       }
 #pragma unroll
@@ -240,7 +246,7 @@ __device__ __forceinline__ void attend(QueryRows<NT>& z, const uint8_t* st, int 
 // The unit's query rows (bf16 in shared memory) as a warp holds them, nothing attended
 // to yet.
 template <int NT>
-__device__ __forceinline__ void load_queries(QueryRows<NT>& z, const uint8_t* queries, int rows, float c_scale, int r, int c) {
+__device__ __forceinline__ void load_queries(QueryRows<NT>& z, const uint8_t* queries, int rows, int r, int c) {
 #pragma unroll
   for (int a = 0; a < NT; ++a) {
     uint4 raw[4];              // row r of these eight, a quarter of its channels
@@ -259,28 +265,28 @@ __device__ __forceinline__ void load_queries(QueryRows<NT>& z, const uint8_t* qu
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       z.q[a][i >> 1][i & 1] = pack_f16(__uint_as_float(u[i] << 16) * up, __uint_as_float(u[i] & 0xFFFF0000u) * up);
-    const float back = c_scale * __uint_as_float((254u - ex) << 23);
+    const float back = __uint_as_float((254u - ex) << 23);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) z.crow[a][e] = __shfl_sync(0xFFFFFFFFu, back, (2 * c + e) * 4);
+    for (int e = 0; e < 2; ++e) z.rk[a][e] = __shfl_sync(0xFFFFFFFFu, back, (2 * c + e) * 4);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) z.o[a][j][e] = 0.0f;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      z.m[a][e] = z.mw[a][e] = kLowest;
-      z.l[a][e] = 0.0f;
+      z.m[a][e] = kLowest;
+      z.d[a][e] = z.l[a][e] = 0.0f;
     }
   }
 }
 
 // What the warps' join takes in shared memory, one set a CTA.
 struct JoinStats {
-  float m[kConsumers][8], w[kConsumers][8], l[kConsumers][8];
+  float m[kConsumers][8], d[kConsumers][8], l[kConsumers][8];
 };
 
 // The four warps' parts of rows 8a .. 8a + 7, joined: this thread gets channels
-// 8 (thread % 16) .. of row 8a + thread / 16 relative to M, and the row's m, L, M.
+// 8 (thread % 16) .. of row 8a + thread / 16 relative to m + d, and the row's m, L, d.
 // `merge`: 8 rows of each warp.
 template <int NT>
 __device__ __forceinline__ float4 join_warps(QueryRows<NT>& z, int a, int rows, JoinStats& s, float4* merge, float4 (&sum)[2]) {
@@ -291,29 +297,31 @@ __device__ __forceinline__ float4 join_warps(QueryRows<NT>& z, int a, int rows, 
     for (int d = 4; d < 32; d <<= 1) z.l[a][e] += __shfl_xor_sync(0xFFFFFFFFu, z.l[a][e], d);
     if (r == 0) {
       s.m[warp][2 * c + e] = z.m[a][e];
-      s.w[warp][2 * c + e] = z.mw[a][e];
+      s.d[warp][2 * c + e] = z.d[a][e];
       s.l[warp][2 * c + e] = z.l[a][e];
     }
   }
   consumer_sync();
   const int row = threadIdx.x >> 4, g = threadIdx.x & 15;
-  float M = s.w[0][row], mm = s.m[0][row], L = 0.0f;
+  // The largest m of a row, and the largest reference relative to it.
+  auto refs = [&](int row, float& m, float& d) {
+    m = s.m[0][row];
+    d = s.d[0][row];
 #pragma unroll
-  for (int k = 1; k < kConsumers; ++k) {
-    M = fmaxf(M, s.w[k][row]);
-    mm = fmaxf(mm, s.m[k][row]);
-  }
+    for (int k = 1; k < kConsumers; ++k) larger(m, d, s.m[k][row], s.d[k][row]);
+  };
+  float m, d, L = 0.0f;
+  refs(row, m, d);
 #pragma unroll
-  for (int k = 0; k < kConsumers; ++k) L += s.l[k][row] * ex2_approx(s.m[k][row] - mm);
+  for (int k = 0; k < kConsumers; ++k) L += s.l[k][row] * ex2_approx(s.m[k][row] - m);
   // float4 i of channels 16r .. 16r + 15 stands at 4r + (i ^ c): the eight lanes of
   // a store fall into distinct banks.
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     if (a * 8 + 2 * c + e < rows) {
-      float top = s.w[0][2 * c + e];
-#pragma unroll
-      for (int k = 1; k < kConsumers; ++k) top = fmaxf(top, s.w[k][2 * c + e]);
-      const float w = ex2_approx(z.mw[a][e] - top);
+      float mr, dr;
+      refs(2 * c + e, mr, dr);
+      const float w = ex2_approx((z.m[a][e] - mr) + (z.d[a][e] - dr));
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         merge[(warp * 8 + 2 * c + e) * 32 + 4 * r + (i ^ c)] =
@@ -337,7 +345,7 @@ __device__ __forceinline__ float4 join_warps(QueryRows<NT>& z, int a, int rows, 
       }
     }
   }
-  return make_float4(mm, L, M, 0.0f);
+  return make_float4(m, L, d, 0.0f);
 }
 
 template <int NT, bool kPrefix>
@@ -480,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
         QueryRows<NT> z;
         int lo = INT_MAX;            // keys that every row sees
         ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&q_full, seg & 1, abort_v, p.err, p.timeout_ns));
-        load_queries<NT>(z, queries, rows, p.c_scale, r, c);
+        load_queries<NT>(z, queries, rows, r, c);
 #pragma unroll
         for (int a = 0; a < NT; ++a)
 #pragma unroll
@@ -497,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
           const int s = it % kStages;
           ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&full[s], (it / kStages) & 1, abort_v, p.err, p.timeout_ns));
           const int t0 = t * kTok + warp * 16;      // this warp's first key
-          if (ok && t0 < hi) attend<NT>(z, smem + s * kStageBytes, t0, warp * 16, r, c, hi, lo);
+          if (ok && t0 < hi) attend<NT>(z, smem + s * kStageBytes, p.c_scale, t0, warp * 16, r, c, hi, lo);
           __syncwarp();
           if (lane == 0) mbar_arrive(&empty[s]);
         }
@@ -509,27 +517,27 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
         for (int a = 0; a < NT; ++a) {
           if (a * 8 >= rows) break;
           float4 sum[2];
-          const float4 mlm = join_warps<NT>(z, a, rows, stats, merge, sum);
-          const float mm = mlm.x, L = mlm.y, M = mlm.z;
+          const float4 mld = join_warps<NT>(z, a, rows, stats, merge, sum);
+          const float m = mld.x, L = mld.y, d = mld.z;
           const int row = threadIdx.x >> 4, g = threadIdx.x & 15;   // 8 channels of a row a thread
           const int rr = x.rt * R + a * 8 + row;
           if (a * 8 + row < rows && !abort_flag) {
             if (whole && !p.keep) {
               const int t = rr / p.G, hq = x.h * p.G + rr % p.G;
-              const float half = scale2(M - mm), inv = L == 0.0f ? 0.0f : half / L;
+              const float half = scale2(d), inv = L == 0.0f ? 0.0f : half / L;
               const uint4 w = make_uint4(pack_bf16(sum[0].x * half * inv, sum[0].y * half * inv),
                                          pack_bf16(sum[0].z * half * inv, sum[0].w * half * inv),
                                          pack_bf16(sum[1].x * half * inv, sum[1].y * half * inv),
                                          pack_bf16(sum[1].z * half * inv, sum[1].w * half * inv));
               *reinterpret_cast<uint4*>(p.out + ((static_cast<int64_t>(x.b) * p.Sq + t) * p.Hq + hq) * kHeadDim + g * 8) = w;
               if (p.lse != nullptr && g == 0)
-                p.lse[(static_cast<int64_t>(x.b) * p.Hq + hq) * p.Sq + t] = L == 0.0f ? -INFINITY : (mm + log2f(L)) * kLn2;
+                p.lse[(static_cast<int64_t>(x.b) * p.Hq + hq) * p.Sq + t] = L == 0.0f ? -INFINITY : (m + log2f(L)) * kLn2;
             } else {
               const int64_t at = static_cast<int64_t>(walk.slot(x)) * p.slot_rows + a * 8 + row;
               float4* dst = reinterpret_cast<float4*>(p.part_o + at * kHeadDim) + g * 2;
               dst[0] = sum[0];
               dst[1] = sum[1];
-              if (g == 0) p.part_ml[at] = make_float4(mm, L, M, 0.0f);
+              if (g == 0) p.part_ml[at] = make_float4(m, L, d, 0.0f);
             }
           }
         }
@@ -565,6 +573,25 @@ __device__ __forceinline__ float4 load_cluster4(uint32_t addr) {
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
   return v;
 }
+// A row's parts, one (m, L, d) a lane, beside its m, d and L so far: the references
+// move to the largest of all, and L with them; -> the factor of the sums so far, and
+// each lane's L and factor in part.y and part.z.  The whole warp together.
+__device__ __forceinline__ float take_in(float4& part, float& m, float& d, float& L) {
+  float mx = m, dx = d;
+  larger(mx, dx, part.x, part.z);
+#pragma unroll
+  for (int i = 16; i > 0; i >>= 1)
+    larger(mx, dx, __shfl_xor_sync(0xFFFFFFFFu, mx, i), __shfl_xor_sync(0xFFFFFFFFu, dx, i));
+  const float to = part.x - mx;
+  L *= ex2_approx(m - mx);
+  const float less = ex2_approx((m - mx) + (d - dx));
+  part.y *= ex2_approx(to);
+  part.z = ex2_approx(to + (part.z - dx));
+  m = mx;
+  d = dx;
+  return less;
+}
+
 // The parts of a prefix's launch: closed form, since every unit has as many tiles.
 struct PrefixParts {
   const float* o;
@@ -702,7 +729,7 @@ __global__ void __cluster_dims__(ctas, 1, 1) __launch_bounds__(kThreads, ctas_pe
     const int r = lane >> 2, c = lane & 3;
     QueryRows<1> z;
     bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&q_full, 0, abort_v, p.err, p.timeout_ns));
-    load_queries<1>(z, queries, rows, p.c_scale, r, c);
+    load_queries<1>(z, queries, rows, r, c);
     const int len = max(0, min(p.room, len_raw)), n = np + (len + kTok - 1) / kTok;
     int hi = 0, lo = 0;
     // What the rows see of the prefix, or of the sequence's own keys.
@@ -729,19 +756,19 @@ __global__ void __cluster_dims__(ctas, 1, 1) __launch_bounds__(kThreads, ctas_pe
       const int s = it % kStages;
       ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&full[s], (it / kStages) & 1, abort_v, p.err, p.timeout_ns));
       const int t0 = (pre ? t : t - np) * kTok + warp * 16;
-      if (ok && t0 < hi) attend<1>(z, smem + s * kStageBytes, t0, warp * 16, r, c, hi, lo);
+      if (ok && t0 < hi) attend<1>(z, smem + s * kStageBytes, p.c_scale, t0, warp * 16, r, c, hi, lo);
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
     }
     // This CTA's part goes where the tiles were: all warps are behind them after
     // the first barrier of join_warps.
     float4 sum[2];
-    const float4 mlm = join_warps<1>(z, 0, rows, stats, merge, sum);
+    const float4 mld = join_warps<1>(z, 0, rows, stats, merge, sum);
     const int row = threadIdx.x >> 4, g = threadIdx.x & 15;
     float4* dst = reinterpret_cast<float4*>(smem + row * kHeadDim * 4) + g * 2;
     dst[0] = sum[0];
     dst[1] = sum[1];
-    if (g == 0) s_ml[row] = mlm;
+    if (g == 0) s_ml[row] = mld;
   }
   __syncwarp();
   cluster_sync_all();
@@ -749,41 +776,31 @@ __global__ void __cluster_dims__(ctas, 1, 1) __launch_bounds__(kThreads, ctas_pe
   if (warp < kConsumers) {
     // A warp a row, four channels a lane.
     for (int row = rank * kConsumers + warp; row < rows; row += ctas * kConsumers) {
-      float m = kLowest, M = kLowest, L = 0.0f;
+      float m = kLowest, d = kLowest, L = 0.0f;
       float4 ml[ctas], part[ctas], acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int k = 0; k < ctas; ++k) {
         ml[k] = load_cluster4(in_cta(smem_addr(&s_ml[row]), k));
         part[k] = load_cluster4(in_cta(smem0 + row * kHeadDim * 4 + lane * 16, k));
         m = fmaxf(m, ml[k].x);
-        M = fmaxf(M, ml[k].z);
       }
+#pragma unroll
+      for (int k = 0; k < ctas; ++k) d = fmaxf(d, (ml[k].x - m) + ml[k].z);
 #pragma unroll
       for (int k = 0; k < ctas; ++k) {
         L += ml[k].y * ex2_approx(ml[k].x - m);
-        const float w = ex2_approx(ml[k].z - M);
+        const float w = ex2_approx((ml[k].x - m) + (ml[k].z - d));
         acc = make_float4(acc.x + part[k].x * w, acc.y + part[k].y * w, acc.z + part[k].z * w, acc.w + part[k].w * w);
       }
       if constexpr (kBefore == kPrefixParts) {
         const RowParts of(parts, b * p.rows + row0 + row, h, p.cache.H);
         for (int k0 = 0; k0 < of.n; k0 += 32) {
-          float4 mine = make_float4(kLowest, 0.0f, kLowest, 0.0f);
+          float4 mine = make_float4(kLowest, 0.0f, 0.0f, 0.0f);
           if (k0 + lane < of.n) mine = parts.ml[of.at(parts, k0 + lane)];
-          float to = mine.x, tow = mine.z;
-#pragma unroll
-          for (int d = 16; d > 0; d >>= 1) {
-            to = fmaxf(to, __shfl_xor_sync(0xFFFFFFFFu, to, d));
-            tow = fmaxf(tow, __shfl_xor_sync(0xFFFFFFFFu, tow, d));
-          }
-          to = fmaxf(to, m);
-          tow = fmaxf(tow, M);
-          const float a = ex2_approx(M - tow);
-          L *= ex2_approx(m - to);
-          acc = make_float4(acc.x * a, acc.y * a, acc.z * a, acc.w * a);
-          m = to;
-          M = tow;
-          float lw = mine.y * ex2_approx(mine.x - m);
-          const float w = ex2_approx(mine.z - M);
+          const float less = take_in(mine, m, d, L);
+          acc = make_float4(acc.x * less, acc.y * less, acc.z * less, acc.w * less);
+          float lw = mine.y;
+          const float w = mine.z;
 #pragma unroll
           for (int d = 16; d > 0; d >>= 1) lw += __shfl_xor_sync(0xFFFFFFFFu, lw, d);
           L += lw;
@@ -802,7 +819,7 @@ __global__ void __cluster_dims__(ctas, 1, 1) __launch_bounds__(kThreads, ctas_pe
         }
       }
       const int t = (row0 + row) / p.G, hq = h * p.G + (row0 + row) % p.G;
-      const float half = scale2(M - m), inv = L == 0.0f ? 0.0f : half / L;
+      const float half = scale2(d), inv = L == 0.0f ? 0.0f : half / L;
       const uint2 w = make_uint2(pack_bf16(acc.x * half * inv, acc.y * half * inv), pack_bf16(acc.z * half * inv, acc.w * half * inv));
       *reinterpret_cast<uint2*>(p.out + ((static_cast<int64_t>(b) * p.Sq + t) * p.Hq + hq) * kHeadDim + lane * 4) = w;
       if (p.lse != nullptr && lane == 0)
@@ -831,7 +848,7 @@ struct MergeParams {
 constexpr int kMergeWarps = 8;
 
 // A CTA takes kMergeWarps / p.split rows of a unit, `split` warps each: a warp goes
-// through the row's parts, 32 at a time with one part's m, L and M a lane, adds
+// through the row's parts, 32 at a time with one part's m, L and d a lane, adds
 // those of its turn in order, and the warps' results are joined in order.
 __global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const MergeParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -859,7 +876,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const Mer
   const int turn = warp % p.split;
   const int row = (blockIdx.y * kMergeWarps + warp) / p.split, rr = rt * p.R + row;
   const bool live = row < p.R && rr < p.rows;
-  float m = kLowest, M = kLowest, L = 0.0f;
+  float m = kLowest, d = kLowest, L = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (live) {
     const bool behind = p.pre.o != nullptr;
@@ -878,27 +895,16 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const Mer
       }
     };
     for (int k0 = 0; k0 < total; k0 += 32) {
-      float4 mine = make_float4(kLowest, 0.0f, kLowest, 0.0f);
+      float4 mine = make_float4(kLowest, 0.0f, 0.0f, 0.0f);
       const float* o;
       const float4* ml;
       if (k0 + lane < total) {
         place(k0 + lane, o, ml);
         mine = *ml;
       }
-      float to = mine.x, tow = mine.z;
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) {
-        to = fmaxf(to, __shfl_xor_sync(0xFFFFFFFFu, to, d));
-        tow = fmaxf(tow, __shfl_xor_sync(0xFFFFFFFFu, tow, d));
-      }
-      to = fmaxf(to, m);
-      tow = fmaxf(tow, M);
-      const float a = ex2_approx(M - tow);
-      L *= ex2_approx(m - to);
-      acc = make_float4(acc.x * a, acc.y * a, acc.z * a, acc.w * a);
-      m = to;
-      M = tow;
-      const float lw = mine.y * ex2_approx(mine.x - m), w = ex2_approx(mine.z - M);
+      const float less = take_in(mine, m, d, L);
+      acc = make_float4(acc.x * less, acc.y * less, acc.z * less, acc.w * less);
+      const float lw = mine.y, w = mine.z;
       const int end = min(32, total - k0);
       for (int k = turn; k < end; k += 4 * p.split) {        // four parts in flight
         float4 y[4];
@@ -921,7 +927,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const Mer
       }
     }
   }
-  if (p.split > 1) {                                         // m and M are the same for all warps of a row
+  if (p.split > 1) {                                         // m and d are the same for all warps of a row
     s_o[warp][lane] = acc;
     if (lane == 0) s_l[warp] = L;
     __syncthreads();
@@ -937,7 +943,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const Mer
   }
   if (!live) return;
   const int t = rr / p.G, hq = h * p.G + rr % p.G;
-  const float half = scale2(M - m);
+  const float half = scale2(d);
   const float inv = L == 0.0f ? 0.0f : half / L;
   uint2 w;
   w.x = pack_bf16(acc.x * half * inv, acc.y * half * inv);

@@ -14,7 +14,7 @@ namespace sage::cache {
 
 constexpr int kSms = 152;
 constexpr int kMaxBatch = 256;                            // sequences of one launch
-constexpr float kLowest = -1e30f;                         // a reference below every score
+constexpr float kLowest = -3.4028234663852886e38f;        // the lowest fp32: a reference below every score
 constexpr float kLog2e = 1.44269502162933349609375f;      // fp32(log2 e)
 constexpr float kLn2 = 0.693147182464599609375f;          // fp32(ln 2)
 
@@ -33,8 +33,8 @@ struct Params {
   float c_scale;             // softmax_scale * log2 e
   int keep;                  // 1: every result goes to the workspace (merged with another launch's)
   int slot_rows;             // rows of a slot: a full tile's, or all there are
-  float* part_o;             // [slot][slot_rows][128]: sums relative to M
-  float4* part_ml;           // [slot][slot_rows]: m, L, M
+  float* part_o;             // [slot][slot_rows][128]: sums relative to m + d
+  float4* part_ml;           // [slot][slot_rows]: m, L, d
   int4* desc;                // [CTA]: the unit that begins in this CTA and ends in a later one
   int2* info;                // [unit], with keep: first CTA and CTAs of the unit (0: its own slot)
   uint64_t timeout_ns;
@@ -234,6 +234,14 @@ __device__ __forceinline__ float lg2_approx(float x) {
   float y;
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// (m, d) becomes the larger of two scores and, relative to it, the larger of two
+// references m + d.
+__device__ __forceinline__ void larger(float& m, float& d, float m2, float d2) {
+  const float mx = fmaxf(m, m2);
+  d = fmaxf((m - mx) + d, (m2 - mx) + d2);
+  m = mx;
 }
 
 // Four INT8 codes (one word) -> two pairs of fp16: code + 128 is put into the

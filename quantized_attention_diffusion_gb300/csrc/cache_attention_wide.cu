@@ -6,9 +6,9 @@
 // serves the sum L, in fp32, and, times the key's scale of V and rounded to fp16, the
 // second product.  R is some 6 below the largest x + log2 sv so far (weights down to
 // 2^-19 of the largest keep all their bits), but at most 60 from the
-// largest x; where V's scales are farther, a row's weights take a factor
-// f = 2^(R - M) more (1 otherwise) and its accumulator stands relative to M.  R and M
-// are whole numbers.  V's codes are exact in fp16.
+// largest x; where V's scales are farther, a row's weights take a factor f = 2^-D more
+// (1 otherwise) and its accumulator stands relative to R + D.  R and D are whole
+// numbers.  V's codes are exact in fp16.
 //
 // A CTA owns 256 query rows of one unit and walks its key tiles of 128.  Its two
 // halves are two row tiles of 128, or, where a unit has at most 128 rows, the even
@@ -71,7 +71,7 @@ constexpr float kFar = 32768.0f;                        // 2^15: most of 32 weig
 constexpr float kAbove = 6.0f;                          // a reference that moves goes so far below the largest weight:
                                                         // 32 of that are a sixteenth of kFar
 constexpr float kFarSum = 0x1p70f, kTiny = 0x1p-55f;    // most of 32 p's sum, and kFar / kFarSum
-constexpr float kReach = 60.0f, kReachV = 140.0f;       // of R, and of M, below the largest score
+constexpr float kReach = 60.0f, kReachV = 140.0f;       // of R, and of R + D, below the largest score
 
 constexpr int kSub = 64;                                // keys of a score buffer
 __host__ __device__ constexpr uint32_t col_s(int t, int b) { return 128u * t + 64u * b; }
@@ -133,7 +133,7 @@ __device__ __forceinline__ void store32(void* dst, uint32_t a, uint32_t b, uint3
 // What a thread knows of its row.
 struct Row {
   float rk;                  // its factor
-  float R, M, f;             // references of L and of the accumulator, f = 2^(R - M)
+  float R, D, f;             // the reference of L, the accumulator's relative to it, f = 2^-D
   float2 l;                  // L in two parts
 };
 
@@ -147,32 +147,31 @@ __device__ __forceinline__ float power_of_two(float n) {
 // accumulator's factor.
 __device__ __forceinline__ bool move_references(uint32_t tS, const float* kx, const float* vx, int left, bool far, Row& z,
                                                 float& alpha) {
-  float xm = -INFINITY, ym = -INFINITY;
+  float xm = -INFINITY, ym = -INFINITY;                    // ym: relative to xm
 #pragma unroll 1
-  for (int c = 0; c < 32; c += 16) {
-    uint32_t a[16];
-    tmem_ld16(tS + c, a);
+  for (int c = 0; c < 32; c += 4) {
+    uint32_t a[4];
+    tmem_ld4(tS + c, a);
     tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float x = c + i < left ? __uint_as_float(a[i]) * kx[c + i] * z.rk : -INFINITY;
-      xm = fmaxf(xm, x);
-      ym = fmaxf(ym, x + lg2_approx(vx[c + i]));
-    }
+    for (int i = 0; i < 4; ++i)
+      larger(xm, ym, c + i < left ? __fmul_rn(__uint_as_float(a[i]) * kx[c + i], z.rk) : -INFINITY, lg2_approx(vx[c + i]));
   }
-  float R = z.R, M = z.M;
-  if (far) {                                               // a row's result is its own alone
-    M = fmaxf(M, ceilf(fmaxf(ym, xm - kReachV)) - kAbove);
-    R = fmaxf(R, fminf(fmaxf(M, ceilf(xm) - kReach), ceilf(xm) + kReach));
+  const float top = ceilf(xm);
+  float R = z.R, D = z.D;
+  if (far && fabsf(top) < INFINITY) {                      // a row's result is its own alone
+    const float below = fmaxf(ym - (top - xm), -kReachV) - kAbove;      // of the accumulator's reference, from top
+    R = fmaxf(R, top + fminf(fmaxf(ceilf(below), -kReach), kReach));
+    D = fmaxf(D + (z.R - R), ceilf(below) + (top - R));
   }
-  const bool moved = R != z.R || M != z.M;
+  const bool moved = R != z.R || D != z.D;
   const float less = power_of_two(z.R - R);
-  alpha = power_of_two(z.M - M);
+  alpha = power_of_two((z.R - R) + (z.D - D));
   z.l.x *= less;
   z.l.y *= less;
   z.R = R;
-  z.M = M;
-  z.f = power_of_two(R - M);
+  z.D = D;
+  z.f = power_of_two(-D);
   return moved;
 }
 
@@ -229,7 +228,7 @@ __device__ __forceinline__ bool weigh(uint32_t tS, const float* kx, const float*
       const float2 k2 = e == 0 ? make_float2(k4.x, k4.y) : make_float2(k4.z, k4.w);
       float2 v2 = e == 0 ? make_float2(v4.x, v4.y) : make_float2(v4.z, v4.w);
       const float2 y = fmul2v(make_float2(__uint_as_float(a[at]), __uint_as_float(a[at + 1])), k2);
-      float2 x = ffma2_bc(y.x, y.y, z.rk, -z.R);
+      float2 x = ffma2_bc(y.x, y.y, z.rk, -z.R);           // rk is a power of two: y * rk is exact
       if constexpr (kSlow) {
         if (at >= left) x.x = -INFINITY;
         if (at + 1 >= left) x.y = -INFINITY;
@@ -263,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
   __shared__ __align__(16) float s_top[kScaleSlots][4];   // of a V warp's keys: the largest scale, or infinity
   __shared__ int s_info[2][2];                            // [K, V][stage]
   __shared__ volatile long long s_end, s_per;
-  __shared__ float4 s_half[128];                          // R, L and M of half 1's rows
+  __shared__ float4 s_half[128];                          // R, L and D of half 1's rows
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_v = &abort_flag;
@@ -512,7 +511,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
             }
           }
 
-          z.R = z.M = kLowest;
+          z.R = kLowest;
+          z.D = 0.0f;
           z.f = 1.0f;
           z.l = make_float2(0.0f, 0.0f);
           int v = 0;                                       // of this half's nv score buffers
@@ -566,8 +566,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
           float L = z.l.x + z.l.y;
           const bool join = !by_rows && n > 1;
           if (join && t == 1) {
-            // Half 1 hands over its rows' m, L and sums, 64 channels at a time.
-            s_half[trow] = make_float4(z.R, L, z.M, 0.0f);
+            // Half 1 hands over its rows' R, L, D and sums, 64 channels at a time.
+            s_half[trow] = make_float4(z.R, L, z.D, 0.0f);
             for (int k = 0; k < 2 && ok; ++k) {
 #pragma unroll 1
               for (int c = 0; c < 2; ++c) {
@@ -592,15 +592,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
                 if (!ok) break;
                 if (c == 0) {
                   const float4 other = s_half[trow];
-                  const float to = fmaxf(z.R, other.x), top = fmaxf(z.M, other.z);
-                  L = L * ex2_approx(z.R - to) + other.y * ex2_approx(other.x - to);
-                  a0 = ex2_approx(z.M - top);
-                  a1 = ex2_approx(other.z - top);
+                  const float to = fmaxf(z.R, other.x), r0 = z.R - to, r1 = other.x - to;
+                  const float top = fmaxf(r0 + z.D, r1 + other.z);
+                  L = L * ex2_approx(r0) + other.y * ex2_approx(r1);
+                  a0 = ex2_approx(r0 + (z.D - top));
+                  a1 = ex2_approx(r1 + (other.z - top));
                   z.R = to;
-                  z.M = top;
+                  z.D = top;
                 }
               }
-              const float half = scale2(z.M - z.R), inv = L == 0.0f ? 0.0f : half / L;
+              const float half = scale2(z.D), inv = L == 0.0f ? 0.0f : half / L;
               uint32_t u[32];
               tmem_ld32(tO + 32 * c, u);
               tmem_ld_wait();
@@ -634,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
               if (p.lse != nullptr)
                 p.lse[(static_cast<int64_t>(x.b) * p.Hq + hq) * p.Sq + tok] = L == 0.0f ? -INFINITY : (z.R + log2f(L)) * kLn2;
             } else if (valid) {
-              p.part_ml[at] = make_float4(z.R, L, z.M, 0.0f);
+              p.part_ml[at] = make_float4(z.R, L, z.D, 0.0f);
             }
           }
           tc_fence_before();                               // O may be written again
