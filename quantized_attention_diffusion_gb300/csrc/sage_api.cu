@@ -146,14 +146,21 @@ sage_status pool_alloc(void** ptr, size_t bytes, cudaStream_t stream, const char
       props.location.type = cudaMemLocationTypeDevice;
       props.location.id = dev;
       cudaMemPool_t fresh = nullptr;
-      cudaError_t e = cudaMemPoolCreate(&fresh, &props);
-      if (e != cudaSuccess) return cuda_fail(e, "memory pool creation");
+      // The first call may be one that is being captured: making a pool records
+      // nothing, and is let through in the relaxed mode only.
+      cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+      cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+      if (e != cudaSuccess) return cuda_fail(e, "stream capture mode");
       uint64_t thr = UINT64_MAX;
-      e = cudaMemPoolSetAttribute(fresh, cudaMemPoolAttrReleaseThreshold, &thr);
-      if (e != cudaSuccess) {
-        (void)cudaMemPoolDestroy(fresh);
-        return cuda_fail(e, "memory pool release threshold");
+      const char* step = "memory pool creation";
+      e = cudaMemPoolCreate(&fresh, &props);
+      if (e == cudaSuccess) {
+        step = "memory pool release threshold";
+        e = cudaMemPoolSetAttribute(fresh, cudaMemPoolAttrReleaseThreshold, &thr);
+        if (e != cudaSuccess) (void)cudaMemPoolDestroy(fresh);
       }
+      (void)cudaThreadExchangeStreamCaptureMode(&mode);
+      if (e != cudaSuccess) return cuda_fail(e, step);
       g_pools[dev] = fresh;
     }
     pool = g_pools[dev];

@@ -77,12 +77,10 @@ def test_equal_scores_of_any_size(Sq, G, room, prefix, power, sign):
         assert float((out.double().cpu() - each(v[0, which].double())).abs().max()) <= 2.0 ** -8, which
 
 
-@pytest.mark.parametrize("Sq,G,room,prefix", PATHS)
-def test_a_sequence_without_keys_and_one_of_far_scores(Sq, G, room, prefix):
+@pytest.mark.parametrize("Sq,G,room", [p[:3] for p in PATHS if p[3] == 0])
+def test_a_sequence_without_keys_and_one_of_far_scores(Sq, G, room):
     """Next to scores of -2^124 a row that sees nothing stays a row of zeros and -inf."""
     import quantized_attention_diffusion_gb300 as qad
-    if prefix:
-        pytest.skip("a prefix has at least one key")
     H, page = 1, 64
     cache = qad.kv_cache_alloc(5, H, page)
     k = torch.zeros((1, 300, H, D), dtype=torch.bfloat16)
