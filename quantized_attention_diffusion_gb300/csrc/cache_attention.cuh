@@ -85,7 +85,7 @@ struct Walk {
     if constexpr (kPrefix) {
       if (!p.causal) return p.prefix_len;
       const int per_seq = p.Sq * p.G, seq = rr / per_seq, t = rr % per_seq / p.G;
-      return max(0, min(p.prefix_len, p.prefix_len + s_len[seq] - p.Sq + t + 1));
+      return max(0, p.prefix_len + min(0, s_len[seq] - p.Sq + t + 1));   // the sum of both lengths may be 2^31
     } else {
       const int len = s_len[b];
       return p.causal ? max(0, min(len, len - p.Sq + rr / p.G + 1)) : len;
