@@ -382,7 +382,9 @@ sage_status sage_kv_cache_write(const sage_kv_cache* cache, const void* k, const
 
 /*
  * sage_kv_cache_read -- read sequences back as bf16, for attention in other
- * precisions or layouts (sage_attn_fwd_cross takes the result).
+ * precisions or layouts.  (sage_attn_fwd_cross has no lengths and no grouped
+ * heads: it takes the result where every sequence has S positions and K and V
+ * as many heads as q.)
  *
  *   lens       in : int32 [B]
  *   k, v       out: bf16 [B, S, H, D], 32-byte aligned; position i of sequence
@@ -420,6 +422,11 @@ sage_status sage_kv_cache_read(const sage_kv_cache* cache, const int32_t* block_
  *              short sequences (by what block_table has room for) need none and
  *              leave it alone.
  * Sq = 1 is the generation step, Sq > 1 a chunk of a prompt or drafted tokens.
+ * q[b, Sq - 1] is the last position of sequence b, whatever the others' lengths.
+ * Where sequences have unequal numbers of new tokens, c[b] <= Sq, their queries
+ * therefore stand at the end, in q[b, Sq - c[b] ..], and the rows in front of
+ * them are padding whose results mean nothing; sage_kv_cache_write with a count
+ * has the tokens at the front, in k[b, .. c[b] - 1].
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, NO_MEMORY, CUDA.
  */
 sage_status sage_attn_fwd_cache(const void* q, int64_t q_stride_b, int64_t q_stride_s, const sage_kv_cache* cache,
@@ -435,8 +442,8 @@ sage_status sage_attn_fwd_cache(const void* q, int64_t q_stride_b, int64_t q_str
  * followed by the lens[b] positions of its row of block_table, and the result
  * is that of sage_attn_fwd_cache on the sequences put together (up to the
  * order of the sums); the prefix is read and multiplied once for the queries of
- * all sequences, or, where a few sequences and a short prefix are done sooner
- * that way, by each.  prefix_len >= 1 is a host value of at most 2^30, and need
+ * all sequences (above 256, of every 256), or, where a few sequences and a short
+ * prefix are done sooner that way, by each.  prefix_len >= 1 is a host value of at most 2^30, and need
  * not fill its last page.  With causal, query i of sequence b sees the
  * positions <= prefix_len + lens[b] - Sq + i of the whole.
  * Other arguments and errors as sage_attn_fwd_cache.

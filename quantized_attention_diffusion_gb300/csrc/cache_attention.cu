@@ -20,9 +20,9 @@
 // L: where they are so large that log2 sv is nothing to them, both still agree.
 //
 // Three kernels share the work.  cache_attn_kernel (up to 16 rows to a key/value head)
-// is bound by HBM, 264 bytes a key: one token of 65536 keys x 24 heads 70 us, 5.9 TB/s,
-// 0.87 of the measured copy rate; 48 ragged sequences of up to 16384 keys x 8 heads
-// 115 us, 0.88.  What is left is the start of each CTA's ring and the merge launch.
+// is bound by HBM, 264 bytes a key: one token of 65536 keys x 24 heads 71.7 us, 5.8 TB/s,
+// 0.85 of the measured copy rate; 48 ragged sequences of up to 16384 keys x 8 heads
+// 116.9 us, 0.87.  What is left is the start of each CTA's ring and the merge launch.
 // cache_attn_cluster_kernel takes what is too small for that, cache_attention_wide.cu
 // more rows.
 //

@@ -34,11 +34,11 @@
 //
 // What bounds it is the path of 128 bytes a clock that shared memory, L1, TMEM loads and
 // stores and the products' operands in shared memory share (l1tex at 60% of its peak and the
-// tensor cores' reads beside it), and in tiles of at most 128 rows the conversion, whose
+// tensor cores active for 30% of the time beside it), and in tiles of at most 128 rows the conversion, whose
 // loads wait for L1 lines that 200 KB of shared memory leave few of.  2 x 1000 tokens
-// x 16 heads over up to 9000 keys: 203 to 209 us, 600 TFLOP/s, 0.31 of the measured bf16
+// x 16 heads over up to 9000 keys: 212 to 214 us, 585 TFLOP/s, 0.31 of the measured bf16
 // rate (the same rows in mma.sync tiles of 32: 842 us); 24 x 5 tokens x 16 heads behind a
-// prefix of 32760, all in all: 77 us.  With V's scales multiplied into bf16 values the chunk took 183 us, and
+// prefix of 32760, all in all: 78 us.  With V's scales multiplied into bf16 values the chunk took 183 us, and
 // its outputs were 1.6 times as far from 64 bits.  64 keys a tile (more copies in flight,
 // twice the barriers) took 244 us; TMEM shapes that give a thread four rows, 238 us.
 //

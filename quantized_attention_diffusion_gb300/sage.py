@@ -720,7 +720,8 @@ def attn_fwd_cache(q, cache, block_table, lens, softmax_scale: float | None = No
     h // (Hq // H).  Returns out bf16 [B, Sq, Hq, 128], and lse fp32 [B, Hq, Sq]
     with ``return_lse`` or when ``lse`` is given.  With ``causal`` query i sees
     positions up to lens[b] - Sq + i; a query that sees nothing gives zeros and
-    -inf.  A length behind what ``block_table`` has room for is reported by
+    -inf.  A sequence with fewer than Sq new tokens has its queries at the end,
+    q[b, Sq - c:], behind padding (kv_cache_write has its tokens at the front).  A length behind what ``block_table`` has room for is reported by
     sync_status (SAGE_ERR_BAD_PAGE), except that 2**30 or more means all of it.
     ``workspace`` (optional uint8 CUDA tensor of >=
     attn_fwd_cache_workspace_bytes) replaces the library's pool; few short
@@ -734,7 +735,7 @@ def attn_fwd_cache_prefix(q, cache, prefix_table, prefix_len: int, block_table, 
     """attn_fwd_cache for sequences that all begin with the same prefix_len
     positions, pages ``prefix_table`` (int32 [pages]): sequence b is the prefix
     and then the lens[b] positions of its row of ``block_table``.  The prefix is
-    read and multiplied once for all sequences, unless a few and a short prefix
-    are done sooner without (sage_attn_fwd_cache_prefix)."""
+    read and multiplied once for all sequences (above 256, for every 256), unless
+    a few and a short prefix are done sooner without (sage_attn_fwd_cache_prefix)."""
     return _attn_fwd_cache(q, cache, (prefix_table, int(prefix_len)), block_table, lens, softmax_scale, causal, out,
                            lse, return_lse, workspace)
