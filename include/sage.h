@@ -443,7 +443,8 @@ sage_status sage_attn_fwd_cache(const void* q, int64_t q_stride_b, int64_t q_str
  * is that of sage_attn_fwd_cache on the sequences put together (up to the
  * order of the sums); the prefix is read and multiplied once for the queries of
  * all sequences (above 256, of every 256), or, where a few sequences and a short
- * prefix are done sooner that way, by each.  prefix_len >= 1 is a host value of at most 2^30, and need
+ * prefix are done sooner that way, by each.  prefix_len >= 1 is a host value of
+ * at most 2^30, and need
  * not fill its last page.  With causal, query i of sequence b sees the
  * positions <= prefix_len + lens[b] - Sq + i of the whole.
  * Other arguments and errors as sage_attn_fwd_cache.

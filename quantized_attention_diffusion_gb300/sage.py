@@ -661,6 +661,8 @@ def kv_cache_read(cache, block_table, lens, S: int, out=None):
         k = torch.empty(shape, dtype=_BF16, device=cache[0].device)
         out = k, torch.empty_like(k)
     else:
+        if len(out) != 2 or out[0].data_ptr() == out[1].data_ptr():
+            raise ValueError("out must be two tensors, one for k and one for v")
         for t in out:
             if t.shape != shape or t.dtype is not _BF16 or t.get_device() != dev or not t.is_contiguous():
                 raise ValueError(f"out must be two contiguous bf16 tensors {shape} on cuda:{dev}")
@@ -721,8 +723,9 @@ def attn_fwd_cache(q, cache, block_table, lens, softmax_scale: float | None = No
     with ``return_lse`` or when ``lse`` is given.  With ``causal`` query i sees
     positions up to lens[b] - Sq + i; a query that sees nothing gives zeros and
     -inf.  A sequence with fewer than Sq new tokens has its queries at the end,
-    q[b, Sq - c:], behind padding (kv_cache_write has its tokens at the front).  A length behind what ``block_table`` has room for is reported by
-    sync_status (SAGE_ERR_BAD_PAGE), except that 2**30 or more means all of it.
+    q[b, Sq - c:], behind padding (kv_cache_write has its tokens at the front).
+    A length behind what ``block_table`` has room for is reported by sync_status
+    (SAGE_ERR_BAD_PAGE), except that 2**30 or more means all of it.
     ``workspace`` (optional uint8 CUDA tensor of >=
     attn_fwd_cache_workspace_bytes) replaces the library's pool; few short
     sequences need none."""
