@@ -50,7 +50,8 @@ typedef enum sage_status {
   SAGE_ERR_NO_MEMORY = 5,   /* workspace allocation failed */
   SAGE_ERR_TIMEOUT = 6,     /* a device wait gave up (reported by sage_sync_status) */
   SAGE_ERR_WORKSPACE = 7,   /* caller workspace smaller than the call's *_workspace_bytes() */
-  SAGE_ERR_BAD_PAGE = 8     /* a page table led out of the cache (reported by sage_sync_status) */
+  SAGE_ERR_BAD_PAGE = 8,    /* a page table led out of the cache (reported by sage_sync_status) */
+  SAGE_ERR_NO_PAGES = 9     /* a free list had too few pages (reported by sage_sync_status) */
 } sage_status;
 
 /* Head dimension, Q/K quantisation block and tile sizes of this library. */
@@ -456,6 +457,207 @@ sage_status sage_attn_fwd_cache_prefix(const void* q, int64_t q_stride_b, int64_
                                        float softmax_scale, int causal, void* workspace, size_t workspace_bytes,
                                        void* stream);
 
+/*
+ * The same cache in 4 bits: 76 bytes a token and head for K and as many for V,
+ * where 8 bits take 132.  No counterpart on the pages.
+ *
+ *   k_codes  E2M1   [num_pages, H, page_size, 64]   channel 2i in the low half of byte i
+ *   k_block  E4M3FN [num_pages, H, page_size, 8]    a scale for each 16 channels
+ *   k_scale  fp32   [num_pages, H, page_size]       a power of two, 0 or NaN
+ *   v_codes, v_block, v_scale the same:  value = code * block * scale
+ *
+ * Everything else, the entry points' arguments, limits and errors too, as
+ * sage_kv_cache and the entry points over it: sage_kv4_cache_write,
+ * sage_kv4_cache_read, sage_attn_fwd_kv4_cache, sage_attn_fwd_kv4_cache_prefix
+ * (sage_attn_fwd_cache_workspace_bytes says what the last two need).
+ *
+ * Quantisation of a row x (one token of one head): scale = 2^k, the least with
+ * max |x| <= 2688 * 2^k (2688 = 6 * 448) and k >= -126; for each 16 channels
+ * block = e4m3_rn(max |x| * 2^-k / 6) and code = e2m1_rn_satfinite(x * 2^-k /
+ * block), 0 where block is 0 (fp32 divisions to nearest even, ties to even).  A
+ * row of zeros has scale, blocks and codes 0; a row with an infinity or a NaN
+ * has a NaN scale, blocks and codes 0: it reads back as NaN.  Values have at most
+ * six significant bits: sage_kv4_cache_read is exact but for those that pass
+ * bf16's smallest.
+ */
+typedef struct sage_kv4_cache {
+  uint8_t* k_codes;
+  uint8_t* k_block;
+  float* k_scale;
+  uint8_t* v_codes;
+  uint8_t* v_block;
+  float* v_scale;
+  int32_t num_pages;
+  int32_t H;
+  int32_t page_size;
+} sage_kv4_cache;
+
+sage_status sage_kv4_cache_write(const sage_kv4_cache* cache, const void* k, const void* v, int64_t k_stride_b,
+                                 int64_t k_stride_s, int64_t v_stride_b, int64_t v_stride_s, int B, int S, int D,
+                                 const int32_t* block_table, int table_width, int64_t table_stride,
+                                 const int32_t* start, const int32_t* count, void* stream);
+sage_status sage_kv4_cache_read(const sage_kv4_cache* cache, const int32_t* block_table, int table_width,
+                                int64_t table_stride, const int32_t* lens, void* k, void* v, int B, int S, int D,
+                                void* stream);
+sage_status sage_attn_fwd_kv4_cache(const void* q, int64_t q_stride_b, int64_t q_stride_s, const sage_kv4_cache* cache,
+                                    const int32_t* block_table, int table_width, int64_t table_stride,
+                                    const int32_t* lens, void* out, float* lse, int B, int Sq, int Hq, int D,
+                                    float softmax_scale, int causal, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+sage_status sage_attn_fwd_kv4_cache_prefix(const void* q, int64_t q_stride_b, int64_t q_stride_s,
+                                           const sage_kv4_cache* cache, const int32_t* prefix_table, int prefix_len,
+                                           const int32_t* block_table, int table_width, int64_t table_stride,
+                                           const int32_t* lens, void* out, float* lse, int B, int Sq, int Hq, int D,
+                                           float softmax_scale, int causal, void* workspace, size_t workspace_bytes,
+                                           void* stream);
+
+/*
+ * Rotary positions.  No counterpart on the pages.  Pair i of the first `dim`
+ * channels of a head is turned by position[axis] * f_i radians, the axis the one
+ * whose section the pair is in (sections[a] pairs of axis a, in order; text has one
+ * axis, video three): (a, b) becomes factor * (a cos - b sin, a sin + b cos).
+ *
+ *   freq         device, uint64 [dim / 2], 8-byte aligned: f_i / (2 pi) in units of
+ *                2^-64, so that the angle is exact modulo a revolution for every
+ *                int32 position
+ *   dim          32, 64, 96 or 128; channels from dim on are left as they are
+ *   interleaved  non-zero: pair i is channels (2i, 2i + 1); 0: (i, i + dim / 2)
+ *   axes         1 to 4; sections[0 .. axes - 1] add up to dim / 2
+ *   factor       of sine and cosine, finite (1 but for SAGE_ROPE_YARN)
+ */
+typedef struct sage_rope {
+  const uint64_t* freq;
+  int32_t dim;
+  int32_t interleaved;
+  int32_t axes;
+  int32_t sections[4];
+  float factor;
+} sage_rope;
+
+/* Scaling of positions for contexts longer than a model was made for. */
+enum {
+  SAGE_ROPE_PLAIN = 0,   /* f_i = base^(-2i / dim) */
+  SAGE_ROPE_LINEAR = 1,  /* f_i / factor */
+  SAGE_ROPE_NTK = 2,     /* base * factor^(dim / (dim - 2)) for base */
+  SAGE_ROPE_YARN = 3,    /* pairs that turn `high` times or more in original_len stay, those that turn `low`
+                            times or less are divided by factor, in between linear in i; sine and cosine
+                            times 0.1 ln factor + 1 */
+  SAGE_ROPE_BANDS = 4    /* the same, linear in the turns and with nothing on sine and cosine */
+};
+
+/*
+ * sage_rope_frequencies -- the table of sage_rope for `dim` channels of one axis
+ * (an even number up to 128), into HOST memory: freq[dim / 2] and the factor of
+ * sine and cosine.  original_len, low and high (turns; usually 1 and 32, or 1 and
+ * 4) are for YARN and BANDS.  Host arithmetic in double; no CUDA call.
+ * sage_rope_frequency -- the entry of any frequency, |radians| <= 3 a position (0
+ * for others).  Errors: INVALID_ARG, UNSUPPORTED.
+ */
+sage_status sage_rope_frequencies(int dim, double base, int scaling, double factor, double original_len, double low,
+                                  double high, uint64_t* freq, double* attention_factor);
+uint64_t sage_rope_frequency(double radians);
+
+/*
+ * sage_qk_norm_rope -- RMS norm of each head of q and k, then the rotation.
+ *
+ *   q, k       in : bf16 [B, S, Hq, D], [B, S, Hk, D], strides as
+ *                   sage_kv_cache_write's; Hk may be 0 (k and k_out then NULL)
+ *   rope       host, or NULL: no rotation (positions is not read)
+ *   positions  in : int32, axis a of token (b, s) at b * pos_stride_b + s *
+ *                   pos_stride_s + a (strides >= 0; 0 shares them)
+ *   eps        in : finite, >= 0: x * w / sqrt(mean x^2 + eps); -1: no norm
+ *   q_weight, k_weight in : bf16 [D], or NULL for ones
+ *   q_out, k_out out: bf16, dense; may be q and k where those are dense.  fp32
+ *                   arithmetic, rounded once
+ * One launch.  B * S * (Hq + Hk) <= 2^31 - 1.  Errors: INVALID_ARG, UNSUPPORTED,
+ * MISALIGNED, CUDA.
+ */
+sage_status sage_qk_norm_rope(const void* q, const void* k, int64_t q_stride_b, int64_t q_stride_s, int64_t k_stride_b,
+                              int64_t k_stride_s, int B, int S, int Hq, int Hk, int D, const sage_rope* rope,
+                              const int32_t* positions, int64_t pos_stride_b, int64_t pos_stride_s, const void* q_weight,
+                              const void* k_weight, float eps, void* q_out, void* k_out, void* stream);
+
+/*
+ * sage_kv_cache_append, sage_kv4_cache_append -- sage_qk_norm_rope whose K goes, as
+ * bf16 would and then quantised, into the cache, with V beside it: the bits of
+ * sage_qk_norm_rope and sage_kv_cache_write in one launch.
+ *
+ *   q, k, v  in : bf16 [B, S, Hq, D], [B, S, H, D] twice (H of the cache); Hq may
+ *                 be 0 (q and q_out then NULL).  Packed tokens are B = 1
+ *   slots    in : int32 [B * S]: token (b, s) goes to token slot % page_size of page
+ *                 slot / page_size; a negative slot: nowhere (its q is formed all
+ *                 the same).  A slot behind the cache is not written, and
+ *                 sage_sync_status() reports SAGE_ERR_BAD_PAGE.  Two tokens in one
+ *                 slot leave it unspecified
+ *   rope .. eps, q_out: as sage_qk_norm_rope
+ * B * S * (Hq + 2 H) <= 2^31 - 1.  Errors as sage_qk_norm_rope.
+ */
+sage_status sage_kv_cache_append(const sage_kv_cache* cache, const void* q, const void* k, const void* v, int64_t q_stride_b,
+                                 int64_t q_stride_s, int64_t k_stride_b, int64_t k_stride_s, int64_t v_stride_b,
+                                 int64_t v_stride_s, int B, int S, int Hq, int D, const sage_rope* rope,
+                                 const int32_t* positions, int64_t pos_stride_b, int64_t pos_stride_s, const void* q_weight,
+                                 const void* k_weight, float eps, const int32_t* slots, void* q_out, void* stream);
+sage_status sage_kv4_cache_append(const sage_kv4_cache* cache, const void* q, const void* k, const void* v,
+                                  int64_t q_stride_b, int64_t q_stride_s, int64_t k_stride_b, int64_t k_stride_s,
+                                  int64_t v_stride_b, int64_t v_stride_s, int B, int S, int Hq, int D,
+                                  const sage_rope* rope, const int32_t* positions, int64_t pos_stride_b,
+                                  int64_t pos_stride_s, const void* q_weight, const void* k_weight, float eps,
+                                  const int32_t* slots, void* q_out, void* stream);
+
+/* Where the tokens of a call stand: one behind another, or [B, tokens] with a
+ * sequence's tokens at the front or (as sage_attn_fwd_cache wants its queries) at the
+ * end of its row. */
+enum { SAGE_TOKENS_PACKED = 0, SAGE_TOKENS_FRONT = 1, SAGE_TOKENS_END = 2 };
+
+/*
+ * sage_kv_pages_reserve -- pages for new tokens off a free list, and with them the
+ * block table's new entries, the slots and the positions of the tokens.  No
+ * counterpart on the pages.  All arrays are device int32.
+ *
+ *   free_pages  in : [num_pages], a stack of which the first free_count[0] are free
+ *   lens        in : [B] tokens that each sequence holds in the cache
+ *   counts      in : [B] tokens that it gets
+ *   block_table in/out: [B, table_width], rows table_stride apart
+ *   layout, tokens: SAGE_TOKENS_*; rows of slots and positions (packed: all, else of
+ *               each sequence)
+ *   start       out: [B] = lens           (for sage_kv_cache_write)
+ *   taken       out: [B] tokens that got their place: counts[b], or 0
+ *   new_lens    out: [B] = start + taken; may be lens
+ *   first       out: [B] row of the sequence's first token
+ *   free_left   out: [1] pages left; may be free_count
+ *   slots       out: int32, a slot (as sage_kv_cache_append takes) for each row, -1
+ *               for padding and for tokens that got no place
+ *   positions   out: the row's position in its sequence, 0 where its slot is -1
+ * A sequence is served if it needs no new page, or if the pages that it and all
+ * sequences before it need are free together; page j that it takes is
+ * free_pages[free_count - 1 - (pages that those before it need) - j].  Where one is not
+ * served its table and length stay, and sage_sync_status() reports
+ * SAGE_ERR_NO_PAGES.  A negative length or count, more positions than the table has
+ * room for or than 2^30, more tokens than `tokens`, a free_count out of range or a page
+ * that is not one is reported as SAGE_ERR_BAD_PAGE; such a sequence (token, page) is
+ * not served (has slot -1), and nothing out of bounds is touched.
+ * One or two launches.  B <= 2^20.  Errors: INVALID_ARG, UNSUPPORTED (page_size,
+ * layout), MISALIGNED, CUDA.
+ */
+sage_status sage_kv_pages_reserve(const int32_t* free_pages, const int32_t* free_count, int num_pages, int page_size,
+                                  const int32_t* lens, const int32_t* counts, int B, int32_t* block_table, int table_width,
+                                  int64_t table_stride, int layout, int tokens, int32_t* start, int32_t* taken,
+                                  int32_t* new_lens, int32_t* first, int32_t* free_left, int32_t* slots,
+                                  int32_t* positions, void* stream);
+
+/*
+ * sage_kv_pages_release -- sequences cut to keep[b] tokens (0: a finished one; a
+ * keep of lens[b] or more changes nothing): the pages behind go back to the free
+ * list, so that a reservation of the same sequences taken back leaves it as it was.
+ * free_pages, free_count, lens and block_table (released entries become -1) are
+ * written in place.  A page in several tables is given back once for each: keep
+ * shared pages out.  Errors as sage_kv_pages_reserve; a table entry that is no page,
+ * or more pages than the list has room for, is reported as SAGE_ERR_BAD_PAGE.
+ */
+sage_status sage_kv_pages_release(int32_t* free_pages, int32_t* free_count, int num_pages, int page_size, int32_t* lens,
+                                  const int32_t* keep, int B, int32_t* block_table, int table_width, int64_t table_stride,
+                                  void* stream);
+
 /* Bytes of device workspace sage_attn_fwd_cache (prefix_len 0) or
  * sage_attn_fwd_cache_prefix need, H key/value heads (0 for invalid sizes). */
 size_t sage_attn_fwd_cache_workspace_bytes(int B, int Sq, int Hq, int H, int prefix_len);
@@ -464,7 +666,8 @@ size_t sage_attn_fwd_cache_workspace_bytes(int B, int Sq, int Hq, int H, int pre
 enum {
   SAGE_FAULT_NONE = 0,          /* disarm */
   SAGE_FAULT_POOL_ALLOC = 1,    /* a workspace / scratch allocation (the library's pool, or a plan's workspace) */
-  SAGE_FAULT_QUANT_LAUNCH = 2,  /* the Q/K quantisation launch of the attention entry points; a cache write or read */
+  SAGE_FAULT_QUANT_LAUNCH = 2,  /* the Q/K quantisation launch of the attention entry points; a cache write, read
+                                   or append, sage_qk_norm_rope, sage_kv_pages_* */
   SAGE_FAULT_ATTN_LAUNCH = 3    /* the attention kernel launch (over a cache: the first) */
 };
 
@@ -500,8 +703,8 @@ sage_status sage_debug_pool_state(int* created, uint64_t* used_bytes);
 sage_status sage_debug_wait_timeout(uint64_t timeout_ns, void* stream);
 
 /* Synchronise `stream`, then report (and clear) the device error word of the
- * current device: SAGE_OK, SAGE_ERR_TIMEOUT, SAGE_ERR_BAD_PAGE, or
- * SAGE_ERR_CUDA if the stream itself failed. */
+ * current device: SAGE_OK, SAGE_ERR_TIMEOUT, SAGE_ERR_BAD_PAGE,
+ * SAGE_ERR_NO_PAGES, or SAGE_ERR_CUDA if the stream itself failed. */
 sage_status sage_sync_status(void* stream);
 
 /* Limit, in nanoseconds, of every device-side wait in later launches from

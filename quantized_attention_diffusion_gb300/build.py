@@ -18,8 +18,8 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libsage.so")
 INCLUDE = os.path.join(ROOT, "include")
 SOURCES = ["sage_api.cu", "quantize.cu", "attention.cu", "quantize_noalloc.cu", "kv_cache.cu", "cache_attention.cu",
-           "cache_attention_wide.cu"]
-HEADERS = ["sage_internal.cuh", "sm103_ptx.cuh", "qk_codes.cuh", "cache_attention.cuh"]
+           "cache_attention_wide.cu", "qk_rope.cu", "kv_pages.cu"]
+HEADERS = ["sage_internal.cuh", "sm103_ptx.cuh", "qk_codes.cuh", "kv_rows.cuh", "cache_attention.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

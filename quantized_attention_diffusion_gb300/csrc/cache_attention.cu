@@ -47,19 +47,28 @@ constexpr int kTok = 64;                                  // keys per tile
 constexpr int kCost = 2;                                  // of a unit, in tiles (1, 4 and 6: the same within 1%)
 constexpr int kConsumers = 4;                             // warps that compute, 16 keys of a tile each
 constexpr int kThreads = (kConsumers + 1) * 32;           // and one that copies
-constexpr uint32_t kOffV = kTok * kHeadDim;
-constexpr uint32_t kOffKs = 2 * kTok * kHeadDim;
-constexpr uint32_t kOffVs = kOffKs + kTok * 4;
-constexpr uint32_t kStageBytes = kOffVs + kTok * 4;
+// A tile as it stands in shared memory, of a cache of kBits.
+template <int kBits>
+struct Tile {
+  static constexpr uint32_t kRow = kHeadDim * kBits / 8;            // bytes of a row's codes
+  static constexpr uint32_t kOffV = kTok * kRow;
+  static constexpr uint32_t kOffKs = 2 * kTok * kRow;
+  static constexpr uint32_t kOffVs = kOffKs + kTok * 4;
+  static constexpr uint32_t kOffKb = kOffVs + kTok * 4;             // 4 bits: block scales, eight a row
+  static constexpr uint32_t kOffVb = kOffKb + kTok * 8;
+  static constexpr uint32_t kBytes = kBits == 8 ? kOffKb : kOffVb + kTok * 8;
+  static constexpr uint32_t kRowBytes = 2 * kRow + 8 + (kBits == 8 ? 0 : 16);   // of a key
+};
 constexpr uint32_t kMergeBytes = kConsumers * 8 * kHeadDim * 4;
 constexpr int kClusterTiles = 16;                         // most tiles of an SM slot, in clusters
 constexpr int kMaxCtas = 3 * kSms;                        // CTAs of a launch: three on each SM
 // As many as the registers of NT times 8 query rows allow without spilling much
 // (65536 keys x 24 heads, one row: three 74 us, two 79).
 __host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
-// Tiles in flight: 9 or 8 on an SM, 135 KB or more.
-__host__ __device__ constexpr int stages_of(int nt) { return nt == 1 ? 3 : 4; }
-constexpr uint32_t smem_of(int nt) { return stages_of(nt) * kStageBytes + kMergeBytes + 8 * nt * kHeadDim * 2; }
+// Tiles in flight: 9 or 8 on an SM, 135 KB or more; in 4 bits 15 or 16.
+__host__ __device__ constexpr int stages_of(int nt, int bits) { return bits == 8 ? (nt == 1 ? 3 : 4) : (nt == 1 ? 5 : 8); }
+template <int kBits>
+constexpr uint32_t smem_of(int nt) { return stages_of(nt, kBits) * Tile<kBits>::kBytes + kMergeBytes + 8 * nt * kHeadDim * 2; }
 constexpr float kFar = 32768.0f, kFarLog2 = 15.0f;        // most of a weight (fp16: 65504)
 constexpr float kAbove = 8.0f;                            // a weights' reference that moves goes so far below the largest
 constexpr float kLeast = -160.0f;                         // of d: scales of V are 0 or 2^-149 at least
@@ -101,6 +110,27 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
+// A tile's run of keys is copied in parts by as many lanes: K, V and their scales, in 4
+// bits their block scales too.
+template <int kBits>
+constexpr int kPartBits = kBits == 8 ? 2 : 3;
+template <int kBits>
+__device__ __forceinline__ void copy_part(const CacheView& cache, int part, uint32_t st, uint32_t bar, int64_t row, int o, int run) {
+  using T = Tile<kBits>;
+  if (part == 0)
+    bulk_load(st + o * T::kRow, cache.k_codes + row * T::kRow, run * T::kRow, bar);
+  else if (part == 1)
+    bulk_load(st + T::kOffV + o * T::kRow, cache.v_codes + row * T::kRow, run * T::kRow, bar);
+  else if (part == 2)
+    bulk_load(st + T::kOffKs + o * 4, cache.k_scale + row, run * 4, bar);
+  else if (part == 3)
+    bulk_load(st + T::kOffVs + o * 4, cache.v_scale + row, run * 4, bar);
+  else if (kBits == 4 && part == 4)
+    bulk_load(st + T::kOffKb + o * 8, cache.k_block + row * 8, run * 8, bar);
+  else if (kBits == 4 && part == 5)
+    bulk_load(st + T::kOffVb + o * 8, cache.v_block + row * 8, run * 8, bar);
+}
+
 // What a warp holds of a unit's query rows.  Lane (r, c): queries 2c and 2c + 1 of
 // each eight in the arrays with [2], column r (a query) of the products' B in q.
 template <int NT>
@@ -114,34 +144,70 @@ struct QueryRows {
 
 // 16 keys, t0 .. t0 + 15, which stand at row `at` of the tile at st.  hi: keys
 // that some row sees; lo: keys that all see.
-template <int NT>
+template <int NT, int kBits>
 __device__ __forceinline__ void attend(QueryRows<NT>& z, const uint8_t* st, float c_scale, int t0, int at, int r, int c, int hi,
                                        int lo) {
+  using T = Tile<kBits>;
+  // Row r of K's products is key r; in 4 bits keys 2 and 3 change places, and 6 and 7,
+  // so that the lanes of a load of V, 64 bytes a key, meet in fewer banks.
+  const int key = kBits == 8 ? r : r ^ ((r >> 1) & 1);
+  const int odd = kBits == 8 ? 0 : c & 1;
   float sc[NT][4], lw[NT][4];
 #pragma unroll
   for (int a = 0; a < NT; ++a)
 #pragma unroll
     for (int e = 0; e < 4; ++e) sc[a][e] = 0.0f;
+  if constexpr (kBits == 8) {
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const uint8_t* kp = st + (at + r) * kHeadDim + c * 32 + half * 16;
-    const uint4 k0 = *reinterpret_cast<const uint4*>(kp);
-    const uint4 k1 = *reinterpret_cast<const uint4*>(kp + 8 * kHeadDim);
+    for (int half = 0; half < 2; ++half) {
+      const uint8_t* kp = st + (at + r) * kHeadDim + c * 32 + half * 16;
+      const uint4 k0 = *reinterpret_cast<const uint4*>(kp);
+      const uint4 k1 = *reinterpret_cast<const uint4*>(kp + 8 * kHeadDim);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t ka[4];
-      k_codes_f16(reinterpret_cast<const uint32_t*>(&k0)[i], ka[0], ka[2]);
-      k_codes_f16(reinterpret_cast<const uint32_t*>(&k1)[i], ka[1], ka[3]);
+      for (int i = 0; i < 4; ++i) {
+        uint32_t ka[4];
+        k_codes_f16(reinterpret_cast<const uint32_t*>(&k0)[i], ka[0], ka[2]);
+        k_codes_f16(reinterpret_cast<const uint32_t*>(&k1)[i], ka[1], ka[3]);
 #pragma unroll
-      for (int a = 0; a < NT; ++a) mma_f16(sc[a], ka, z.q[a][half * 4 + i][0], z.q[a][half * 4 + i][1]);
+        for (int a = 0; a < NT; ++a) mma_f16(sc[a], ka, z.q[a][half * 4 + i][0], z.q[a][half * 4 + i][1]);
+      }
+    }
+  } else {
+    // A lane's 32 channels of a key are 16 bytes and two blocks.
+    uint4 kw[2];
+    uint32_t sb[2][2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      kw[n] = *reinterpret_cast<const uint4*>(st + (at + key + 8 * n) * T::kRow + c * 16);
+      uint32_t two;
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(two) : "h"(*reinterpret_cast<const uint16_t*>(st + T::kOffKb + (at + key + 8 * n) * 8 + 2 * c)));
+      sb[n][0] = __byte_perm(two, two, 0x1010);
+      sb[n][1] = __byte_perm(two, two, 0x3232);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {              // products 2i and 2i + 1
+      uint32_t h0[4], h1[4];
+      e2m1x8_f16(reinterpret_cast<const uint32_t*>(&kw[0])[i], h0);
+      e2m1x8_f16(reinterpret_cast<const uint32_t*>(&kw[1])[i], h1);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        h0[j] = mul_f16x2(h0[j], sb[0][i >> 1]);
+        h1[j] = mul_f16x2(h1[j], sb[1][i >> 1]);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t ka[4] = {h0[2 * j], h1[2 * j], h0[2 * j + 1], h1[2 * j + 1]};
+#pragma unroll
+        for (int a = 0; a < NT; ++a) mma_f16(sc[a], ka, z.q[a][2 * i + j][0], z.q[a][2 * i + j][1]);
+      }
     }
   }
-  // sc[a][e]: key r + 8 (e / 2), query 2c + e % 2
-  float ks[2], lv[2];                 // of keys r and r + 8; K's times softmax_scale * log2 e
+  // sc[a][e]: key `key` + 8 (e / 2), query 2c + e % 2
+  float ks[2], lv[2];                 // of both keys; K's times softmax_scale * log2 e
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
-    ks[n] = *reinterpret_cast<const float*>(st + kOffKs + (at + n * 8 + r) * 4) * c_scale;
-    lv[n] = lg2_approx(*reinterpret_cast<const float*>(st + kOffVs + (at + n * 8 + r) * 4));
+    ks[n] = *reinterpret_cast<const float*>(st + T::kOffKs + (at + n * 8 + key) * 4) * c_scale;
+    lv[n] = lg2_approx(*reinterpret_cast<const float*>(st + T::kOffVs + (at + n * 8 + key) * 4));
   }
 #pragma unroll
   for (int a = 0; a < NT; ++a)
@@ -155,7 +221,7 @@ __device__ __forceinline__ void attend(QueryRows<NT>& z, const uint8_t* st, floa
     for (int a = 0; a < NT; ++a)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (t0 + r + 8 * (e >> 1) >= z.lim[a][e & 1]) {
+        if (t0 + key + 8 * (e >> 1) >= z.lim[a][e & 1]) {
           sc[a][e] = -INFINITY;
           lw[a][e] = 0.0f;            // the scale may be anything
         }
@@ -217,28 +283,70 @@ __device__ __forceinline__ void attend(QueryRows<NT>& z, const uint8_t* st, floa
     pb[a][0] = transpose8(pack_f16(pw[a][0], pw[a][1]));
     pb[a][1] = transpose8(pack_f16(pw[a][2], pw[a][3]));
   }
-  uint4 vw[4];
-  const uint8_t* vp = st + kOffV + (at + 2 * c) * kHeadDim + r * 16;
+  if constexpr (kBits == 8) {
+    uint4 vw[4];
+    const uint8_t* vp = st + T::kOffV + (at + 2 * c) * kHeadDim + r * 16;
 #pragma unroll
-  for (int k = 0; k < 4; ++k)         // keys 2c, 2c + 1, 2c + 8, 2c + 9
-    vw[k] = *reinterpret_cast<const uint4*>(vp + ((k >> 1) * 8 + (k & 1)) * kHeadDim);
-  if (t0 + 16 > hi) {                 // codes behind the last key may be anything, NaN too
+    for (int k = 0; k < 4; ++k)         // keys 2c, 2c + 1, 2c + 8, 2c + 9
+      vw[k] = *reinterpret_cast<const uint4*>(vp + ((k >> 1) * 8 + (k & 1)) * kHeadDim);
+    if (t0 + 16 > hi) {                 // codes behind the last key may be anything, NaN too
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (t0 + 2 * c + (k >> 1) * 8 + (k & 1) >= hi) vw[k] = make_uint4(0u, 0u, 0u, 0u);
-  }
+      for (int k = 0; k < 4; ++k)
+        if (t0 + 2 * c + (k >> 1) * 8 + (k & 1) >= hi) vw[k] = make_uint4(0u, 0u, 0u, 0u);
+    }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t w0 = reinterpret_cast<const uint32_t*>(&vw[0])[i], w1 = reinterpret_cast<const uint32_t*>(&vw[1])[i];
-    const uint32_t w2 = reinterpret_cast<const uint32_t*>(&vw[2])[i], w3 = reinterpret_cast<const uint32_t*>(&vw[3])[i];
-    const uint32_t a01 = __byte_perm(w0, w1, 0x5140), b01 = __byte_perm(w0, w1, 0x7362);
-    const uint32_t a23 = __byte_perm(w2, w3, 0x5140), b23 = __byte_perm(w2, w3, 0x7362);
-    const uint32_t va[4] = {v_codes_f16_lo(a01), v_codes_f16_hi(a01), v_codes_f16_lo(a23), v_codes_f16_hi(a23)};
-    const uint32_t vb[4] = {v_codes_f16_lo(b01), v_codes_f16_hi(b01), v_codes_f16_lo(b23), v_codes_f16_hi(b23)};
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w0 = reinterpret_cast<const uint32_t*>(&vw[0])[i], w1 = reinterpret_cast<const uint32_t*>(&vw[1])[i];
+      const uint32_t w2 = reinterpret_cast<const uint32_t*>(&vw[2])[i], w3 = reinterpret_cast<const uint32_t*>(&vw[3])[i];
+      const uint32_t a01 = __byte_perm(w0, w1, 0x5140), b01 = __byte_perm(w0, w1, 0x7362);
+      const uint32_t a23 = __byte_perm(w2, w3, 0x5140), b23 = __byte_perm(w2, w3, 0x7362);
+      const uint32_t va[4] = {v_codes_f16_lo(a01), v_codes_f16_hi(a01), v_codes_f16_lo(a23), v_codes_f16_hi(a23)};
+      const uint32_t vb[4] = {v_codes_f16_lo(b01), v_codes_f16_hi(b01), v_codes_f16_lo(b23), v_codes_f16_hi(b23)};
 #pragma unroll
-    for (int a = 0; a < NT; ++a) {
-      mma_f16(z.o[a][2 * i], va, pb[a][0], pb[a][1]);
-      mma_f16(z.o[a][2 * i + 1], vb, pb[a][0], pb[a][1]);
+      for (int a = 0; a < NT; ++a) {
+        mma_f16(z.o[a][2 * i], va, pb[a][0], pb[a][1]);
+        mma_f16(z.o[a][2 * i + 1], vb, pb[a][0], pb[a][1]);
+      }
+    }
+  } else {
+    // A lane's 16 channels of a key are eight bytes and one block.  Bytes of the
+    // codes of keys A and B, even channels in one word and odd ones in another, are
+    // the pairs that the products take; so are the scales.
+    uint2 vw[4];
+    uint32_t sv[4];
+    const uint8_t* vp = st + T::kOffV + at * T::kRow + r * 8;
+    const uint8_t* vb = st + T::kOffVb + at * 8 + r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {       // keys 2c, 2c + 1, 2c + 8, 2c + 9, as the rows of K's products have them
+      const int at_key = (k >> 1) * 8 + 2 * c + ((k & 1) ^ odd);
+      vw[k] = *reinterpret_cast<const uint2*>(vp + at_key * T::kRow);
+      sv[k] = vb[at_key * 8];
+    }
+    if (t0 + 16 > hi) {                 // scales behind the last key may be anything, NaN too; codes are finite
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (t0 + 2 * c + (k >> 1) * 8 + ((k & 1) ^ odd) >= hi) sv[k] = 0u;
+    }
+    uint32_t s2[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2[k]) : "h"(static_cast<uint16_t>(sv[2 * k] | sv[2 * k + 1] << 8)));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t even[2][4], odds[2][4];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t w0 = i == 0 ? vw[2 * k].x : vw[2 * k].y, w1 = i == 0 ? vw[2 * k + 1].x : vw[2 * k + 1].y;
+        e2m1x8_f16((w0 & 0x0F0F0F0Fu) | ((w1 << 4) & 0xF0F0F0F0u), even[k]);
+        e2m1x8_f16(((w0 >> 4) & 0x0F0F0F0Fu) | (w1 & 0xF0F0F0F0u), odds[k]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t va[4] = {mul_f16x2(even[0][j], s2[0]), mul_f16x2(odds[0][j], s2[0]), mul_f16x2(even[1][j], s2[1]),
+                                mul_f16x2(odds[1][j], s2[1])};
+#pragma unroll
+        for (int a = 0; a < NT; ++a) mma_f16(z.o[a][4 * i + j], va, pb[a][0], pb[a][1]);
+      }
     }
   }
 }
@@ -348,9 +456,10 @@ __device__ __forceinline__ float4 join_warps(QueryRows<NT>& z, int a, int rows, 
   return make_float4(m, L, d, 0.0f);
 }
 
-template <int NT, bool kPrefix>
+template <int NT, bool kPrefix, int kBits>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(const Params p) {
-  constexpr int R = 8 * NT, kStages = stages_of(NT);
+  constexpr int R = 8 * NT, kStages = stages_of(NT, kBits);
+  constexpr uint32_t kStageBytes = Tile<kBits>::kBytes;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kStages], empty[kStages], q_full, q_empty;
   __shared__ int abort_flag;
@@ -388,11 +497,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
     if (warp == kConsumers) {
       // ------------------------------------------------------------ copies --
       // A tile is 1, 2 or 4 runs of keys that lie together in a page; lane
-      // 4i + k copies part k (K, V, their scales) of run i.  Every lane holds a
+      // 4i + k (in 4 bits 8i + k) copies part k of run i.  Every lane holds a
       // page number of the unit's table, reloaded for the next 32 pages.
       const int ps = p.cache.page_shift;
       const int run = min(kTok, 1 << ps), runs = kTok / run;
-      const int my_run = lane >> 2, part = lane & 3;
+      const int my_run = lane >> kPartBits<kBits>, part = lane & ((1 << kPartBits<kBits>) - 1);
       int it = 0;
       bool bad = false, ok = true;
       uint32_t seg = 0;
@@ -438,20 +547,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
             break;
           }
           const int n_live = (min(kTok, hi - t * kTok) + run - 1) / run;   // <= 0 for a unit without keys
-          if (lane == 0) mbar_arrive_expect_tx(&full[s], max(0, n_live) * run * (2 * kHeadDim + 8));
+          if (lane == 0) mbar_arrive_expect_tx(&full[s], max(0, n_live) * run * Tile<kBits>::kRowBytes);
           __syncwarp();
           if (live) {
             const int64_t r = ((static_cast<int64_t>(page) * p.cache.H + x.h) << ps) + (t0 & ((1 << ps) - 1));
             const uint32_t bar = smem_addr(&full[s]), st = smem0 + s * kStageBytes;
             const int o = my_run * run;
-            if (part == 0)
-              bulk_load(st + o * kHeadDim, p.cache.k_codes + r * kHeadDim, run * kHeadDim, bar);
-            else if (part == 1)
-              bulk_load(st + kOffV + o * kHeadDim, p.cache.v_codes + r * kHeadDim, run * kHeadDim, bar);
-            else if (part == 2)
-              bulk_load(st + kOffKs + o * 4, p.cache.k_scale + r, run * 4, bar);
-            else
-              bulk_load(st + kOffVs + o * 4, p.cache.v_scale + r, run * 4, bar);
+            copy_part<kBits>(p.cache, part, st, bar, r, o, run);
           }
         }
         x = after;
@@ -505,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
           const int s = it % kStages;
           ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&full[s], (it / kStages) & 1, abort_v, p.err, p.timeout_ns));
           const int t0 = t * kTok + warp * 16;      // this warp's first key
-          if (ok && t0 < hi) attend<NT>(z, smem + s * kStageBytes, p.c_scale, t0, warp * 16, r, c, hi, lo);
+          if (ok && t0 < hi) attend<NT, kBits>(z, smem + s * kStageBytes, p.c_scale, t0, warp * 16, r, c, hi, lo);
           __syncwarp();
           if (lane == 0) mbar_arrive(&empty[s]);
         }
@@ -628,11 +730,12 @@ enum Before { kNothing, kPrefixTiles, kPrefixParts };
 // sequences in a launch before (kPrefixParts), the join takes that launch's parts in
 // and no merge kernel follows.  What bounds it is one chain of
 // latencies: the length, the pages, the copies, the products, the join.
-template <int ctas, Before kBefore>
+template <int ctas, Before kBefore, int kBits>
 __global__ void __cluster_dims__(ctas, 1, 1) __launch_bounds__(kThreads, ctas_per_sm(1))
     cache_attn_cluster_kernel(const Params p, const int32_t* prefix_pages, const PrefixParts parts) {
   constexpr bool kPrefix = kBefore == kPrefixTiles;
-  constexpr int R = 8, kStages = stages_of(1);
+  constexpr int R = 8, kStages = stages_of(1, kBits);
+  constexpr uint32_t kStageBytes = Tile<kBits>::kBytes;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kStages], empty[kStages], q_full;
   __shared__ int abort_flag;
@@ -666,7 +769,7 @@ __global__ void __cluster_dims__(ctas, 1, 1) __launch_bounds__(kThreads, ctas_pe
     // -------------------------------------------------------------- copies --
     const int ps = p.cache.page_shift;
     const int run = min(kTok, 1 << ps), runs = kTok / run;
-    const int my_run = lane >> 2, part = lane & 3;       // as in the kernel above
+    const int my_run = lane >> kPartBits<kBits>, part = lane & ((1 << kPartBits<kBits>) - 1);       // as in the kernel above
     if (lane == 0) mbar_arrive_expect_tx(&q_full, rows * kHeadDim * 2);
     __syncwarp();
     if (lane < rows)
@@ -699,20 +802,13 @@ __global__ void __cluster_dims__(ctas, 1, 1) __launch_bounds__(kThreads, ctas_pe
       const int s = it % kStages, round = it / kStages;
       if (round > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[s], (round - 1) & 1, abort_v, p.err, p.timeout_ns))) break;
       const int n_live = (min(kTok, hi - first) + run - 1) / run;
-      if (lane == 0) mbar_arrive_expect_tx(&full[s], n_live * run * (2 * kHeadDim + 8));
+      if (lane == 0) mbar_arrive_expect_tx(&full[s], n_live * run * Tile<kBits>::kRowBytes);
       __syncwarp();
       if (live) {
         const int64_t r = ((static_cast<int64_t>(page) * p.cache.H + h) << ps) + (t0 & ((1 << ps) - 1));
         const uint32_t bar = smem_addr(&full[s]), st = smem0 + s * kStageBytes;
         const int o = my_run * run;
-        if (part == 0)
-          bulk_load(st + o * kHeadDim, p.cache.k_codes + r * kHeadDim, run * kHeadDim, bar);
-        else if (part == 1)
-          bulk_load(st + kOffV + o * kHeadDim, p.cache.v_codes + r * kHeadDim, run * kHeadDim, bar);
-        else if (part == 2)
-          bulk_load(st + kOffKs + o * 4, p.cache.k_scale + r, run * 4, bar);
-        else
-          bulk_load(st + kOffVs + o * 4, p.cache.v_scale + r, run * 4, bar);
+        copy_part<kBits>(p.cache, part, st, bar, r, o, run);
       }
     }
     if (bad) atomicExch(p.err, SAGE_DEVERR_BAD_PAGE);
@@ -756,7 +852,7 @@ __global__ void __cluster_dims__(ctas, 1, 1) __launch_bounds__(kThreads, ctas_pe
       const int s = it % kStages;
       ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&full[s], (it / kStages) & 1, abort_v, p.err, p.timeout_ns));
       const int t0 = (pre ? t : t - np) * kTok + warp * 16;
-      if (ok && t0 < hi) attend<1>(z, smem + s * kStageBytes, p.c_scale, t0, warp * 16, r, c, hi, lo);
+      if (ok && t0 < hi) attend<1, kBits>(z, smem + s * kStageBytes, p.c_scale, t0, warp * 16, r, c, hi, lo);
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
     }
@@ -997,10 +1093,11 @@ T* at(void* base, size_t off) {
 // beside: the launch before is this call's, and nothing of it is needed.
 cudaError_t launch_part(const Params& p, int R, bool prefix, bool beside, unsigned ctas, cudaStream_t stream) {
   if (R == kWideRows) return launch_wide(p, prefix, beside, ctas, stream);
-  const uint32_t smem = smem_of(R / 8);
+  const bool in8 = p.cache.bits == 8;
+  const uint32_t smem = in8 ? smem_of<8>(R / 8) : smem_of<4>(R / 8);
   auto go = [&](auto kernel) {
-    static std::atomic<uint64_t> allowed[2 * 2];       // for each kernel
-    cudaError_t e = allow_smem(kernel, smem, allowed[(prefix ? 2 : 0) + R / 16]);
+    static std::atomic<uint64_t> allowed[2 * 2 * 2];   // for each kernel
+    cudaError_t e = allow_smem(kernel, smem, allowed[(in8 ? 0 : 4) + (prefix ? 2 : 0) + R / 16]);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
@@ -1014,9 +1111,13 @@ cudaError_t launch_part(const Params& p, int R, bool prefix, bool beside, unsign
     cfg.numAttrs = beside ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, p);
   };
-  if (prefix)
-    return R == 8 ? go(cache_attn_kernel<1, true>) : go(cache_attn_kernel<2, true>);
-  return R == 8 ? go(cache_attn_kernel<1, false>) : go(cache_attn_kernel<2, false>);
+  auto of = [&](auto bits) {
+    constexpr int kBits = decltype(bits)::value;
+    if (prefix)
+      return R == 8 ? go(cache_attn_kernel<1, true, kBits>) : go(cache_attn_kernel<2, true, kBits>);
+    return R == 8 ? go(cache_attn_kernel<1, false, kBits>) : go(cache_attn_kernel<2, false, kBits>);
+  };
+  return in8 ? of(std::integral_constant<int, 8>()) : of(std::integral_constant<int, 4>());
 }
 
 unsigned ctas_for(long long tiles, int R) {
@@ -1082,14 +1183,14 @@ cudaError_t launch_clusters(const CacheAttnArgs& a, int ctas, const PrefixParts*
   p.c_scale = a.softmax_scale * kLog2e;
   p.timeout_ns = a.timeout_ns;
   p.err = a.err;
-  const uint32_t smem = smem_of(1);
-  auto go = [&](auto size) {
-    constexpr int kCtas = decltype(size)::value;
+  auto go = [&](auto size, auto bits) {
+    constexpr int kCtas = decltype(size)::value, kBits = decltype(bits)::value;
+    constexpr uint32_t smem = smem_of<kBits>(1);
     static std::atomic<uint64_t> allowed[3];           // for each kernel
     const int which = parts != nullptr ? kPrefixParts : a.prefix_len > 0 ? kPrefixTiles : kNothing;
-    auto kernel = which == kPrefixParts   ? cache_attn_cluster_kernel<kCtas, kPrefixParts>
-                  : which == kPrefixTiles ? cache_attn_cluster_kernel<kCtas, kPrefixTiles>
-                                          : cache_attn_cluster_kernel<kCtas, kNothing>;
+    auto kernel = which == kPrefixParts   ? cache_attn_cluster_kernel<kCtas, kPrefixParts, kBits>
+                  : which == kPrefixTiles ? cache_attn_cluster_kernel<kCtas, kPrefixTiles, kBits>
+                                          : cache_attn_cluster_kernel<kCtas, kNothing, kBits>;
     const cudaError_t e = allow_smem(kernel, smem, allowed[which]);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -1105,10 +1206,13 @@ cudaError_t launch_clusters(const CacheAttnArgs& a, int ctas, const PrefixParts*
     cfg.numAttrs = which == kPrefixParts ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, p, a.prefix_pages, parts != nullptr ? *parts : PrefixParts{});
   };
-  return ctas == 8   ? go(std::integral_constant<int, 8>())
-         : ctas == 4 ? go(std::integral_constant<int, 4>())
-         : ctas == 2 ? go(std::integral_constant<int, 2>())
-                     : go(std::integral_constant<int, 1>());
+  auto of = [&](auto bits) {
+    return ctas == 8   ? go(std::integral_constant<int, 8>(), bits)
+           : ctas == 4 ? go(std::integral_constant<int, 4>(), bits)
+           : ctas == 2 ? go(std::integral_constant<int, 2>(), bits)
+                       : go(std::integral_constant<int, 1>(), bits);
+  };
+  return a.cache.bits == 8 ? of(std::integral_constant<int, 8>()) : of(std::integral_constant<int, 4>());
 }
 
 }  // namespace

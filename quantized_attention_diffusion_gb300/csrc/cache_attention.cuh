@@ -252,6 +252,20 @@ __device__ __forceinline__ void k_codes_f16(uint32_t w, uint32_t& lo, uint32_t& 
   hi = sub_f16x2(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u);
 }
 
+// Pairs of E2M1 codes in bytes 0 .. 3 of a word -> pairs of fp16.
+__device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // The launch of the kernel for many query rows (cache_attention_wide.cu): 256
 // rows and 128 keys a tile, one CTA on each SM.
 constexpr int kWideRows = 256, kWideTok = 128, kWideCost = 3;

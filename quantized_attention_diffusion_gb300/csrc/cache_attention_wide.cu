@@ -46,6 +46,7 @@
 // then the thread scales the row's sum, its accumulator and the weights of this
 // buffer that it has stored already by a power of two, which is exact, and forms
 // the 32 again.
+#include <type_traits>
 #include <cuda_fp16.h>
 
 #include "cache_attention.cuh"
@@ -118,6 +119,49 @@ __device__ __forceinline__ void v_codes_f16(uint32_t w, uint32_t& lo, uint32_t& 
       : "=r"(lo), "=r"(hi)
       : "r"(w));
 }
+
+// 16 codes of a row as they are in global memory, and their fp16 values.
+template <int kBits>
+struct Codes;
+template <>
+struct Codes<8> {
+  uint4 w;
+  __device__ void load(const uint8_t* codes, const uint8_t*) { w = load_once(codes); }
+  template <bool kIsV>
+  __device__ void values(uint32_t (&o)[8]) const {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (kIsV)
+        v_codes_f16(u[i], o[2 * i], o[2 * i + 1]);
+      else
+        k_codes_f16(u[i], o[2 * i], o[2 * i + 1]);
+    }
+  }
+};
+// One block: its codes times its scale, 6 significant bits, exact in fp16.
+template <>
+struct Codes<4> {
+  uint2 w;
+  uint32_t block;
+  __device__ void load(const uint8_t* codes, const uint8_t* blocks) {
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(codes));
+    asm volatile("ld.global.nc.L1::no_allocate.u8 %0, [%1];" : "=r"(block) : "l"(blocks));
+  }
+  template <bool>
+  __device__ void values(uint32_t (&o)[8]) const {
+    uint32_t s2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"(static_cast<uint16_t>(block * 0x0101u)));
+    const uint32_t u[2] = {w.x, w.y};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t h[4];
+      e2m1x8_f16(u[i], h);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[4 * i + j] = mul_f16x2(h[j], s2);
+    }
+  }
+};
 
 __device__ __forceinline__ float2 unpack_bf16(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
@@ -249,7 +293,7 @@ __device__ __forceinline__ bool weigh(uint32_t tS, const float* kx, const float*
   return kSlow ? total > kFarSum || !(sumw.x + sumw.y <= kFar) : total * top > kFar;
 }
 
-template <bool kPrefix>
+template <bool kPrefix, int kBits>
 __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -324,7 +368,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
       const int q16 = (lane & 3) + ((lane >> 3) & 1) * 4;                     // 16 codes of a key
       const int scale_key = is_v ? 16 * (lane >> 2) + 4 * (warp & 3) + (lane & 3) : tid;   // the key whose scale it loads
       const int ps = p.cache.page_shift;
-      const uint8_t* codes = (is_v ? p.cache.v_codes : p.cache.k_codes) + q16 * 16;
+      constexpr int kRow = kHeadDim * kBits / 8;                              // bytes of a key's codes
+      const uint8_t* codes = (is_v ? p.cache.v_codes : p.cache.k_codes) + q16 * (kRow / 8);
+      const uint8_t* blocks = kBits == 8 ? nullptr : (is_v ? p.cache.v_block : p.cache.k_block) + q16;
       const float* scales = is_v ? p.cache.v_scale : p.cache.k_scale;
       uint8_t* dst = smem + (is_v ? kSmemV : kSmemK) + tile_offset(sub, 2 * q16);
       const uint32_t odd = tile_offset(sub, 2 * q16 + 1) - tile_offset(sub, 2 * q16);   // 16 or -16: wraps
@@ -354,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
           tile = x.t0;
         }
       };
-      uint4 w[8];
+      Codes<kBits> w[8];
       float scale = 0.0f;
       auto load = [&]() {
         loaded = more;
@@ -365,23 +411,25 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
         bad |= gone && mine;
         if (gone) page = -1;
         // The rows of a step follow those of the step before within a page.
-        const uint8_t* row = codes;
         if (__any_sync(0xFFFFFFFFu, gone && mine) || t0 + kWideTok > hi) {   // some keys are not there: zeros
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int pg = __shfl_sync(0xFFFFFFFFu, page, i), t = t0 + 16 * i;
-            row = codes + static_cast<int64_t>(((pg * p.cache.H + head) << ps) + (t & ((1 << ps) - 1)) + sub) * kHeadDim;
-            w[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (pg >= 0 && t + sub < hi) w[i] = load_once(row);
+            const int64_t row = ((pg * p.cache.H + head) << ps) + (t & ((1 << ps) - 1)) + sub;
+            w[i] = Codes<kBits>{};
+            if (pg >= 0 && t + sub < hi) w[i].load(codes + row * kRow, blocks + row * 8);
           }
         } else {
+          const uint8_t *row = codes, *block = blocks;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             if (i == 0 || ((16 * i) & ((1 << ps) - 1)) == 0) {               // warp-uniform
               const int pg = __shfl_sync(0xFFFFFFFFu, page, i);
-              row = codes + static_cast<int64_t>(((pg * p.cache.H + head) << ps) + (i == 0 ? t0 & ((1 << ps) - 1) : 0) + sub - 16 * i) * kHeadDim;
+              const int64_t at = ((pg * p.cache.H + head) << ps) + (i == 0 ? t0 & ((1 << ps) - 1) : 0) + sub - 16 * i;
+              row = codes + at * kRow;
+              if constexpr (kBits == 4) block = blocks + at * 8;
             }
-            w[i] = load_once(row + i * 16 * kHeadDim);
+            w[i].load(row + i * 16 * kRow, block + i * 16 * 8);
           }
         }
         const int pg = __shfl_sync(0xFFFFFFFFu, page, scale_key >> 4), t = t0 + scale_key;
@@ -405,31 +453,23 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
         }
         if (round > 0 && !__all_sync(0xFFFFFFFFu, wait(&empty[s], round - 1))) break;
         uint8_t* to = dst + s * kTileBytes;
-        if (is_v) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint32_t o[8];
-            v_codes_f16(w[i].x, o[0], o[1]);
-            v_codes_f16(w[i].y, o[2], o[3]);
-            v_codes_f16(w[i].z, o[4], o[5]);
-            v_codes_f16(w[i].w, o[6], o[7]);
-            *reinterpret_cast<uint4*>(to + i * 2048) = make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(to + i * 2048 + static_cast<int>(odd)) = make_uint4(o[4], o[5], o[6], o[7]);
-          }
-        } else {
+        if (!is_v) {
           s_ks[it % kScaleSlots][tid] = scale * p.c_scale;
           mbar_arrive(&bars.scales[it % kScaleSlots]);
+        }
+        auto convert = [&](auto v) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             uint32_t o[8];
-            k_codes_f16(w[i].x, o[0], o[1]);
-            k_codes_f16(w[i].y, o[2], o[3]);
-            k_codes_f16(w[i].z, o[4], o[5]);
-            k_codes_f16(w[i].w, o[6], o[7]);
+            w[i].template values<decltype(v)::value>(o);
             *reinterpret_cast<uint4*>(to + i * 2048) = make_uint4(o[0], o[1], o[2], o[3]);
             *reinterpret_cast<uint4*>(to + i * 2048 + static_cast<int>(odd)) = make_uint4(o[4], o[5], o[6], o[7]);
           }
-        }
+        };
+        if (kBits == 8 && is_v)
+          convert(std::true_type());
+        else
+          convert(std::false_type());
         if (tid == 0) s_info[is_v][s] = info;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         mbar_arrive(&full[s]);
@@ -751,8 +791,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
 
 cudaError_t launch_wide(const Params& p, bool prefix, bool beside, unsigned ctas, cudaStream_t stream) {
   auto go = [&](auto kernel) {
-    static std::atomic<uint64_t> allowed[2];           // for each kernel
-    cudaError_t e = allow_smem(kernel, kSmemBytes, allowed[prefix]);
+    static std::atomic<uint64_t> allowed[2 * 2];       // for each kernel
+    cudaError_t e = allow_smem(kernel, kSmemBytes, allowed[(p.cache.bits == 8 ? 0 : 2) + prefix]);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
@@ -767,7 +807,8 @@ cudaError_t launch_wide(const Params& p, bool prefix, bool beside, unsigned ctas
     cfg.numAttrs = beside ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, p);
   };
-  return prefix ? go(cache_attn_wide_kernel<true>) : go(cache_attn_wide_kernel<false>);
+  if (p.cache.bits == 8) return prefix ? go(cache_attn_wide_kernel<true, 8>) : go(cache_attn_wide_kernel<false, 8>);
+  return prefix ? go(cache_attn_wide_kernel<true, 4>) : go(cache_attn_wide_kernel<false, 4>);
 }
 
 }  // namespace sage::cache

@@ -24,35 +24,16 @@
 // length, page, row): 5.6 us for 8 tokens, 4.4 us for 3 x 333 read.
 #include <cuda_runtime.h>
 
-#include "qk_codes.cuh"
-#include "sage_internal.cuh"
-#include "sm103_ptx.cuh"
+#include "kv_rows.cuh"
 
 namespace sage {
 
 namespace {
 
+using namespace rows;
+
 constexpr int kWarps = 8;      // per CTA
 constexpr int kRows = 4;       // tokens of one step of a warp
-
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
-__device__ __forceinline__ float2 ffma2v(float2 a, float2 b, float2 c) {
-  float2 r;
-  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
-      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 
 // Row index of token `pos` of sequence b and head h in the cache, or -1 where
 // the table or the cache does not reach: the caller then skips the row.
@@ -63,60 +44,6 @@ __device__ __forceinline__ int64_t cache_row(const CacheView& c, const PageTable
   const int page = __ldg(t.pages + b * t.stride + i);
   if (page < 0 || page >= c.num_pages) return -1;
   return (((static_cast<int64_t>(page) * c.H + h) << c.page_shift) + (pos & ((1 << c.page_shift) - 1)));
-}
-
-// -fl(x / sc) of the 8 bf16 values of w, for a scale in [2^-100, 2^125]:
-// Markstein's correction with the negated reciprocal nr = -fl(1 / sc), as in
-// quantize.cu's V encoder.
-__device__ __forceinline__ void quotients(const uint4& w, float sc, float nr, float2 (&y)[4]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-  const float2 n2 = make_float2(nr, nr), s2 = make_float2(sc, sc);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 x = make_float2(bf16_lo(u[i]), bf16_hi(u[i]));
-    const float2 z = fmul2v(x, n2);
-    y[i] = ffma2v(ffma2v(z, s2, x), n2, z);
-  }
-}
-
-// Eight codes, in channel order, of values whose row has scale sc.
-template <bool kIsV>
-__device__ __forceinline__ uint2 encode(const uint4& w, float sc, float nr, bool in_range) {
-  uint32_t code[2] = {0u, 0u};
-  if (in_range) {
-    float2 y[4];
-    quotients(w, sc, nr, y);
-    if constexpr (kIsV) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        code[i] = cvt_e4m3x4(y[2 * i].x, y[2 * i].y, y[2 * i + 1].x, y[2 * i + 1].y) ^ 0x80808080u;
-    } else {
-      // 1.5 * 2^23 - y: its low byte is the two's complement of rint(-y)
-      // (ties to even on either side), at most 127 in magnitude since
-      // |x| <= amax = 127 sc (1 + 2^-24).
-      const float2 magic = make_float2(kRoundMagic, kRoundMagic);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float2 a = fsub2v(magic, y[2 * i]), b = fsub2v(magic, y[2 * i + 1]);
-        const uint32_t lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
-        const uint32_t hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
-        code[i] = __byte_perm(lo, hi, 0x5410);
-      }
-    }
-  } else if (sc > 0.0f) {        // outside the quotient's range: by division (a scale of 0 or NaN: codes 0)
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float x = (i & 1) ? bf16_hi(u[i >> 1]) : bf16_lo(u[i >> 1]);
-      uint32_t byte;
-      if constexpr (kIsV)
-        byte = cvt_e4m3x2(__fdiv_rn(x, sc), 0.0f) & 0xFFu;
-      else
-        byte = (__float_as_uint(code_by_division(x, sc) + kRoundMagic) - 0x4B400000u) & 0xFFu;
-      code[i >> 2] |= byte << (8 * (i & 3));
-    }
-  }
-  return make_uint2(code[0], code[1]);
 }
 
 // The rows of step i of a warp: head h, tokens 4 j .. 4 j + 3 of sequence b, the
@@ -133,31 +60,7 @@ __device__ __forceinline__ Step step_of(uint32_t i, int H, int steps_per_seq) {
   return x;
 }
 
-// One tensor's part of a step: w0 and w1 are channels 8 l .. + 7 and 64 + 8 l ..
-// + 7 of the lane's row, l = lane % 8.
-template <bool kIsV>
-__device__ __forceinline__ void write_rows(const uint4& w0, const uint4& w1, uint8_t* codes, float* scales, int64_t row,
-                                           int l) {
-  // Magnitudes compare as integers, infinities and NaN above all others.
-  uint32_t top = 0u;
-  const uint32_t u[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-  for (int e = 0; e < 8; ++e) top = max_u16x2(top, u[e] & 0x7FFF7FFFu);
-#pragma unroll
-  for (int d = 1; d < 8; d <<= 1) top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-  top = max(top & 0xFFFFu, top >> 16);
-  const float sc = top < 0x7F80u ? __fdiv_rn(__uint_as_float(top << 16), kIsV ? 448.0f : 127.0f) : __uint_as_float(0x7FC00000u);
-  const bool in_range = sc >= 0x1p-100f && sc <= 0x1p125f;
-  const float nr = -__frcp_rn(sc);
-  const uint2 c0 = encode<kIsV>(w0, sc, nr, in_range), c1 = encode<kIsV>(w1, sc, nr, in_range);
-  if (row >= 0) {
-    uint2* dst = reinterpret_cast<uint2*>(codes + row * kHeadDim) + l;
-    dst[0] = c0;
-    dst[8] = c1;
-    if (l == 0) scales[row] = sc;
-  }
-}
-
+template <int kBits>
 __global__ void __launch_bounds__(kWarps * 32) kv_cache_write_kernel(const CacheWriteArgs a, uint32_t steps,
                                                                      int steps_per_seq) {
   const uint32_t i = blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -177,25 +80,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv_cache_write_kernel(const Cache
   }
   const int64_t row = live ? cache_row(a.cache, a.table, x.b, static_cast<int64_t>(__ldg(a.start + x.b)) + x.s, x.h) : -1;
   if (live && row < 0 && l == 0) atomicExch(a.err, SAGE_DEVERR_BAD_PAGE);
-  write_rows<false>(k0, k1, a.cache.k_codes, a.cache.k_scale, row, l);
-  write_rows<true>(v0, v1, a.cache.v_codes, a.cache.v_scale, row, l);
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// Two E4M3 codes -> two floats, exactly.
-__device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t two) {
-  uint32_t h2;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(two)));
-  float2 r;
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "r"(h2));
-  return r;
+  put_row<kBits, false>(a.cache, k0, k1, row, l, l, l + 8);
+  put_row<kBits, true>(a.cache, v0, v1, row, l, l, l + 8);
 }
 
 // 16 channels of a row to bf16, one 32-byte store.
@@ -246,6 +132,48 @@ __global__ void __launch_bounds__(kWarps * 32) kv_cache_read_kernel(const CacheR
   store_row(a.v + dst, y, vs);
 }
 
+// The same from 4 bits: eight bytes of codes and one block scale a lane.
+__global__ void __launch_bounds__(kWarps * 32) kv4_cache_read_kernel(const CacheReadArgs a, uint32_t steps,
+                                                                     int steps_per_seq) {
+  const uint32_t i = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (i >= steps) return;                  // warp-uniform
+  const int lane = threadIdx.x & 31, l = lane & 7;
+  Step x = step_of(i, a.cache.H, steps_per_seq);
+  x.s += lane >> 3;
+  if (x.s >= a.S) return;
+  uint2 kc = make_uint2(0u, 0u), vc = kc;
+  uint32_t kb = 0u, vb = 0u;
+  float ks = 0.0f, vs = 0.0f;
+  if (x.s < __ldg(a.lens + x.b)) {
+    const int64_t row = cache_row(a.cache, a.table, x.b, x.s, x.h);
+    if (row >= 0) {
+      kc = __ldcs(reinterpret_cast<const uint2*>(a.cache.k_codes + row * 64) + l);
+      vc = __ldcs(reinterpret_cast<const uint2*>(a.cache.v_codes + row * 64) + l);
+      kb = __ldcs(a.cache.k_block + row * 8 + l);
+      vb = __ldcs(a.cache.v_block + row * 8 + l);
+      ks = __ldg(a.cache.k_scale + row);
+      vs = __ldg(a.cache.v_scale + row);
+    } else if (l == 0) {
+      atomicExch(a.err, SAGE_DEVERR_BAD_PAGE);
+    }
+  }
+  const int64_t dst = ((static_cast<int64_t>(x.b) * a.S + x.s) * a.cache.H + x.h) * kHeadDim + l * 16;
+  auto store = [&](uint16_t* to, const uint2& c, uint32_t block, float sc) {
+    float lo[8], hi[8], y[16];
+    e2m1x8_to_f32(c.x, lo);
+    e2m1x8_to_f32(c.y, hi);
+    const float sb = e4m3x2_to_f32(block).x;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      y[e] = lo[e] * sb;                     // 6 significant bits: exact
+      y[8 + e] = hi[e] * sb;
+    }
+    store_row(to + dst, y, sc);
+  };
+  store(a.k, kc, kb, ks);
+  store(a.v, vc, vb, vs);
+}
+
 template <typename Args>
 cudaError_t launch_rows(void (*kernel)(Args, uint32_t, int), const Args& a, cudaStream_t stream) {
   const int per_seq = (a.S + kRows - 1) / kRows;
@@ -257,11 +185,11 @@ cudaError_t launch_rows(void (*kernel)(Args, uint32_t, int), const Args& a, cuda
 }  // namespace
 
 cudaError_t launch_kv_cache_write(const CacheWriteArgs& a, cudaStream_t stream) {
-  return launch_rows(kv_cache_write_kernel, a, stream);
+  return a.cache.bits == 8 ? launch_rows(kv_cache_write_kernel<8>, a, stream) : launch_rows(kv_cache_write_kernel<4>, a, stream);
 }
 
 cudaError_t launch_kv_cache_read(const CacheReadArgs& a, cudaStream_t stream) {
-  return launch_rows(kv_cache_read_kernel, a, stream);
+  return a.cache.bits == 8 ? launch_rows(kv_cache_read_kernel, a, stream) : launch_rows(kv4_cache_read_kernel, a, stream);
 }
 
 }  // namespace sage

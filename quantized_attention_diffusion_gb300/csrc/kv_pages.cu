@@ -1,0 +1,275 @@
+// kv_pages.cu -- pages of the KV cache given to new tokens and taken back, on the
+// GPU: block tables, slots and positions from lengths and counts (sm_103a).
+//
+// Sequence b holds len tokens in held = ceil(len / page) pages and asks for need =
+// ceil((len + count) / page) - held more.  With upto_b the sum of need over sequences
+// 0 .. b, the sequences with need = 0 or upto_b <= free are served: page j of b is
+// entry free - 1 - (upto_b - need_b) - j of the free list, a stack.  Taking back puts
+// pages where this found them, in the same order.
+//
+// A few hundred bytes for a generation step: what it costs is the launch and a chain
+// of loads, sums over the warps and barriers.  One CTA does the sums, 1024 sequences at a
+// time, and the pages of all of them with one search for each; it does the tokens
+// too where they are few, and otherwise a second kernel does, a CTA for each 1024
+// tokens of a sequence at most.
+#include <algorithm>
+#include <climits>
+#include <cuda_runtime.h>
+
+#include "sage_internal.cuh"
+
+namespace sage {
+
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kFewTokens = 8192;       // of a call that needs no second kernel
+constexpr int kFillThreads = 256;
+
+// Inclusive sums of a and b over the block; `part` has 2 x 32 values.  All threads.
+__device__ __forceinline__ void block_sums(long long& a, long long& b, long long (*part)[32]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long x = __shfl_up_sync(0xFFFFFFFFu, a, d), y = __shfl_up_sync(0xFFFFFFFFu, b, d);
+    if (lane >= d) {
+      a += x;
+      b += y;
+    }
+  }
+  if (lane == 31) {
+    part[0][warp] = a;
+    part[1][warp] = b;
+  }
+  __syncthreads();
+  if (warp < 2) {
+    long long x = part[warp][lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long y = __shfl_up_sync(0xFFFFFFFFu, x, d);
+      if (lane >= d) x += y;
+    }
+    part[warp][lane] = x;
+  }
+  __syncthreads();
+  if (warp > 0) {
+    a += part[0][warp - 1];
+    b += part[1][warp - 1];
+  }
+}
+
+// The first of n ascending values that is above x (n if none is).
+__device__ __forceinline__ int above(const long long* v, int n, long long x) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (v[mid] > x)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  return lo;
+}
+
+// -1 where the table or the free list named a page that there is not.
+__device__ __forceinline__ int slot_of(const PagesArgs& a, int b, int pos) {
+  const int page = a.table[b * a.table_stride + (pos >> a.page_shift)];
+  if (page < 0 || page >= a.num_pages) {
+    atomicExch(a.err, SAGE_DEVERR_BAD_PAGE);
+    return -1;
+  }
+  return (page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+}
+
+__global__ void __launch_bounds__(kThreads) reserve_kernel(const PagesArgs a, int do_tokens) {
+  __shared__ long long s_upto[kThreads], s_rows[kThreads], part[2][32];
+  __shared__ int s_start[kThreads], s_count[kThreads], s_served[kThreads];
+  __shared__ long long s_gone;
+  const int tid = threadIdx.x;
+  const int page = 1 << a.page_shift;
+  // The tokens of a padded call need nothing from the sums but who is served.
+  const int raw = __ldg(a.free_count);
+  const int free = max(0, min(raw, a.num_pages));
+  bool bad = raw != free;
+  if (tid == 0) s_gone = 0;
+  long long pages_before = 0, rows_before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    const int b = b0 + tid, n = min(kThreads, a.B - b0);
+    int len = 0, count = 0;
+    bool fits = true;
+    if (b < a.B) {
+      len = a.lens[b];
+      count = __ldg(a.counts + b);
+      fits = len >= 0 && count >= 0 && static_cast<long long>(len) + count <= a.room && (a.layout == kPagesPacked || count <= a.tokens);
+      if (!fits) bad = true;
+    }
+    const int held = fits ? (len + page - 1) >> a.page_shift : 0;
+    const int need = fits ? ((len + count + page - 1) >> a.page_shift) - held : 0;
+    long long upto = need, rows = max(0, count);
+    __syncthreads();                         // the arrays of the sequences before have been read
+    block_sums(upto, rows, part);
+    const bool served = fits && (need == 0 || pages_before + upto <= free);
+    if (b < a.B && fits && !served) atomicExch(a.err, SAGE_DEVERR_NO_PAGES);
+    s_upto[tid] = upto;
+    s_rows[tid] = rows;
+    s_start[tid] = len;
+    s_count[tid] = count;
+    s_served[tid] = served ? 1 : 0;
+    if (b < a.B) {
+      const int taken = served ? count : 0;
+      a.start[b] = len;
+      a.taken[b] = taken;
+      a.new_lens[b] = len + taken;
+      const long long at = a.layout == kPagesPacked ? rows_before + rows - max(0, count)
+                                                    : static_cast<long long>(b) * a.tokens + (a.layout == kPagesEnd ? a.tokens - min(a.tokens, max(0, count)) : 0);
+      a.first[b] = static_cast<int>(min(at, static_cast<long long>(INT_MAX)));
+      if (served && need > 0) atomicMax(&s_gone, pages_before + upto);
+    }
+    __syncthreads();
+    // The pages of these sequences, those of the served.
+    const long long total = s_upto[n - 1];
+    for (long long j = tid; j < total && pages_before + j < free; j += kThreads) {
+      const int i = above(s_upto, n, j);
+      if (s_served[i] == 0) break;           // nor is any behind it
+      const long long in = j - (i > 0 ? s_upto[i - 1] : 0);
+      const int at = ((s_start[i] + page - 1) >> a.page_shift) + static_cast<int>(in);
+      a.table[(b0 + i) * a.table_stride + at] = __ldg(a.free_pages + (free - 1 - (pages_before + j)));
+    }
+    pages_before += total;
+    rows_before += s_rows[n - 1];
+  }
+  __syncthreads();
+  if (a.layout == kPagesPacked && rows_before > a.tokens) bad = true;   // tokens without a slot
+  if (bad) atomicExch(a.err, SAGE_DEVERR_BAD_PAGE);
+  if (tid == 0) *a.free_left = free - static_cast<int>(s_gone);
+  if (do_tokens) {                           // B <= kThreads: all sequences are in the arrays
+    const int rows = a.layout == kPagesPacked ? a.tokens : a.tokens * a.B;
+    for (int r = tid; r < rows; r += kThreads) {
+      int b, i;
+      if (a.layout == kPagesPacked) {
+        b = above(s_rows, a.B, r);
+        i = b < a.B ? r - static_cast<int>(b > 0 ? s_rows[b - 1] : 0) : 0;
+      } else {
+        b = r / a.tokens;
+        i = r - b * a.tokens - (a.layout == kPagesEnd ? a.tokens - s_count[b] : 0);
+      }
+      const bool live = b < a.B && s_served[b] != 0 && i >= 0 && i < s_count[b];
+      const int pos = live ? s_start[b] + i : 0;
+      a.slots[r] = live ? slot_of(a, b, pos) : -1;
+      a.positions[r] = pos;
+    }
+  }
+}
+
+// Slots and positions of sequence blockIdx.x's tokens; for packed tokens block B has
+// the rows behind the last.
+__global__ void __launch_bounds__(kFillThreads) fill_kernel(const PagesArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int b = blockIdx.x;
+  const bool packed = a.layout == kPagesPacked;
+  const int step = gridDim.y * kFillThreads, i0 = blockIdx.y * kFillThreads + threadIdx.x;
+  if (b == a.B) {
+    const long long end = static_cast<long long>(a.first[a.B - 1]) + max(0, __ldg(a.counts + a.B - 1));
+    for (long long r = end + i0; r < a.tokens; r += step) {
+      a.slots[r] = -1;
+      a.positions[r] = 0;
+    }
+    return;
+  }
+  const int count = max(0, __ldg(a.counts + b)), taken = a.taken[b], start = a.start[b];
+  const long long base = packed ? a.first[b] : static_cast<long long>(b) * a.tokens;
+  const int skip = a.layout == kPagesEnd ? a.tokens - min(a.tokens, count) : 0;
+  const long long rows = packed ? min(static_cast<long long>(count), a.tokens - base) : a.tokens;
+  for (long long r = i0; r < rows; r += step) {
+    const long long i = r - skip;
+    const bool live = i >= 0 && i < taken;
+    const int pos = live ? start + static_cast<int>(i) : 0;
+    a.slots[base + r] = live ? slot_of(a, b, pos) : -1;
+    a.positions[base + r] = pos;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) release_kernel(const ReleaseArgs a) {
+  __shared__ long long s_upto[kThreads], part[2][32];
+  __shared__ int s_kept[kThreads];
+  const int tid = threadIdx.x;
+  const int page = 1 << a.page_shift;
+  const int raw = *a.free_count;
+  const int free = max(0, min(raw, a.num_pages));
+  bool bad = raw != free;
+  // The sum of all, for the order of the stack: page j of what is given back, counted
+  // over the sequences, goes to entry free + total - 1 - j.
+  long long total = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    long long before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+      const int b = b0 + tid, n = min(kThreads, a.B - b0);
+      int len = 0, keep = 0;
+      bool fits = false;
+      if (b < a.B) {
+        len = a.lens[b];
+        keep = max(0, __ldg(a.keep + b));
+        fits = len >= 0 && len <= a.room;
+        if (!fits) bad = true;
+      }
+      const bool less = fits && keep < len;
+      const int kept = less ? (keep + page - 1) >> a.page_shift : 0;
+      const int give = less ? ((len + page - 1) >> a.page_shift) - kept : 0;
+      long long upto = give, none = 0;
+      __syncthreads();
+      block_sums(upto, none, part);
+      s_upto[tid] = upto;
+      s_kept[tid] = kept;
+      __syncthreads();
+      const long long here = s_upto[n - 1];
+      if (pass == 1) {
+        for (long long j = tid; j < here; j += kThreads) {
+          const int i = above(s_upto, n, j);
+          const int at = s_kept[i] + static_cast<int>(j - (i > 0 ? s_upto[i - 1] : 0));
+          int32_t* entry = a.table + (b0 + i) * a.table_stride + at;
+          const int p = *entry;
+          const long long to = free + total - 1 - (before + j);
+          if (p < 0 || p >= a.num_pages || to >= a.num_pages) bad = true;
+          if (to < a.num_pages) a.free_pages[to] = p;
+          *entry = -1;
+        }
+        if (less) a.lens[b] = keep;
+      }
+      before += here;
+    }
+    total = before;
+  }
+  if (bad) atomicExch(a.err, SAGE_DEVERR_BAD_PAGE);
+  __syncthreads();                           // free_count has been read by all
+  if (tid == 0) *a.free_count = static_cast<int>(min(static_cast<long long>(a.num_pages), free + total));
+}
+
+}  // namespace
+
+cudaError_t launch_pages_reserve(const PagesArgs& a, cudaStream_t stream) {
+  const bool packed = a.layout == kPagesPacked;
+  const int64_t rows = packed ? a.tokens : static_cast<int64_t>(a.tokens) * a.B;
+  const bool one = a.B <= kThreads && rows <= kFewTokens;
+  reserve_kernel<<<1, kThreads, 0, stream>>>(a, one ? 1 : 0);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || one) return e;
+  const int64_t each = packed ? a.tokens / a.B + 1 : a.tokens;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.B) + (packed ? 1u : 0u),
+                     static_cast<unsigned>(std::min<int64_t>(64, (each + 1023) / 1024)));
+  cfg.blockDim = dim3(kFillThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fill_kernel, a);
+}
+
+cudaError_t launch_pages_release(const ReleaseArgs& a, cudaStream_t stream) {
+  release_kernel<<<1, kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace sage

@@ -1,6 +1,7 @@
 // sage_api.cu -- the extern "C" boundary: argument checks, workspace layout,
 // stream-ordered scratch, launch sequences and error mapping.  Declarations
 // and their contracts are in include/sage.h.
+#include <algorithm>
 #include <atomic>
 #include <cinttypes>
 #include <climits>
@@ -330,26 +331,72 @@ sage_status check_workspace(void* ws, size_t bytes, int B, int S, int H) {
   return SAGE_OK;
 }
 
-// A cache and its page table, as the cache entry points take them.
-sage_status check_cache(const sage_kv_cache* c, int D, const int32_t* table, int width, int64_t stride) {
-  if (!c) return fail(SAGE_ERR_INVALID_ARG, "cache is NULL");
-  if (D != kHeadDim)
-    return fail(SAGE_ERR_UNSUPPORTED, "head dimension %d is not supported: this kernel takes D = 128", D);
-  if (c->num_pages < 1 || c->H < 1)
-    return fail(SAGE_ERR_INVALID_ARG, "a cache's num_pages and H must be >= 1 (got %d, %d)", c->num_pages, c->H);
-  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
-    return fail(SAGE_ERR_UNSUPPORTED, "page_size %d is not supported: 16, 32, 64, 128 or 256", c->page_size);
-  if (static_cast<int64_t>(c->num_pages) * c->H > INT_MAX / c->page_size)
-    return fail(SAGE_ERR_INVALID_ARG, "num_pages * H * page_size exceeds 2^31-1");
-  sage_status s = check_ptrs({{c->k_codes, "k_codes"}, {c->k_scale, "k_scale"}, {c->v_codes, "v_codes"},
-                              {c->v_scale, "v_scale"}});
-  if (s != SAGE_OK) return s;
+// A cache of 8 or of 4 bits as the kernels take it, page_shift still to be found.
+CacheView cache_view(const sage_kv_cache& c) {
+  CacheView v = {};
+  v.k_codes = reinterpret_cast<uint8_t*>(c.k_codes);
+  v.k_scale = c.k_scale;
+  v.v_codes = c.v_codes;
+  v.v_scale = c.v_scale;
+  v.num_pages = c.num_pages;
+  v.H = c.H;
+  v.bits = 8;
+  return v;
+}
+
+CacheView cache_view(const sage_kv4_cache& c) {
+  CacheView v = {};
+  v.k_codes = c.k_codes;
+  v.k_block = c.k_block;
+  v.k_scale = c.k_scale;
+  v.v_codes = c.v_codes;
+  v.v_block = c.v_block;
+  v.v_scale = c.v_scale;
+  v.num_pages = c.num_pages;
+  v.H = c.H;
+  v.bits = 4;
+  return v;
+}
+
+sage_status check_page_size(int page_size, int* shift) {
+  if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)))
+    return fail(SAGE_ERR_UNSUPPORTED, "page_size %d is not supported: 16, 32, 64, 128 or 256", page_size);
+  *shift = 0;
+  while ((1 << *shift) < page_size) ++*shift;
+  return SAGE_OK;
+}
+
+sage_status check_table(const int32_t* table, int width, int64_t stride) {
   if (!table) return fail(SAGE_ERR_INVALID_ARG, "block_table is NULL");
   if (!aligned(table, 4)) return fail(SAGE_ERR_MISALIGNED, "block_table is not 4-byte aligned");
   if (width < 1 || stride < 0)
     return fail(SAGE_ERR_INVALID_ARG, "table_width must be >= 1 and table_stride >= 0 (got %d, %lld)", width,
                 static_cast<long long>(stride));
   return SAGE_OK;
+}
+
+template <typename Cache>
+sage_status check_cache(const Cache* c, int D, CacheView* view) {
+  if (!c) return fail(SAGE_ERR_INVALID_ARG, "cache is NULL");
+  if (D != kHeadDim)
+    return fail(SAGE_ERR_UNSUPPORTED, "head dimension %d is not supported: this kernel takes D = 128", D);
+  if (c->num_pages < 1 || c->H < 1)
+    return fail(SAGE_ERR_INVALID_ARG, "a cache's num_pages and H must be >= 1 (got %d, %d)", c->num_pages, c->H);
+  *view = cache_view(*c);
+  sage_status s = check_page_size(c->page_size, &view->page_shift);
+  if (s != SAGE_OK) return s;
+  if (static_cast<int64_t>(c->num_pages) * c->H > INT_MAX / c->page_size)
+    return fail(SAGE_ERR_INVALID_ARG, "num_pages * H * page_size exceeds 2^31-1");
+  s = check_ptrs({{c->k_codes, "k_codes"}, {c->k_scale, "k_scale"}, {c->v_codes, "v_codes"}, {c->v_scale, "v_scale"}});
+  if (s == SAGE_OK && view->bits == 4) s = check_ptrs({{view->k_block, "k_block"}, {view->v_block, "v_block"}});
+  return s;
+}
+
+// A cache and its page table, as the cache entry points take them.
+template <typename Cache>
+sage_status check_cache(const Cache* c, int D, const int32_t* table, int width, int64_t stride, CacheView* view) {
+  const sage_status s = check_cache(c, D, view);
+  return s == SAGE_OK ? check_table(table, width, stride) : s;
 }
 
 // Device arrays of one int32 per sequence.
@@ -365,25 +412,13 @@ sage_status check_strides(int64_t sb, int64_t ss, const char* name) {
   return SAGE_OK;
 }
 
-CacheView cache_view(const sage_kv_cache* c) {
-  CacheView v;
-  v.k_codes = reinterpret_cast<uint8_t*>(c->k_codes);
-  v.k_scale = c->k_scale;
-  v.v_codes = c->v_codes;
-  v.v_scale = c->v_scale;
-  v.num_pages = c->num_pages;
-  v.H = c->H;
-  v.page_shift = 0;
-  while ((1 << v.page_shift) < c->page_size) ++v.page_shift;
-  return v;
-}
-
-// sage_attn_fwd_cache and, with a prefix, sage_attn_fwd_cache_prefix.
-sage_status run_cache_attention(const void* q, int64_t q_sb, int64_t q_ss, const sage_kv_cache* cache,
-                                const int32_t* prefix_table, int prefix_len, const int32_t* table, int width,
-                                int64_t stride, const int32_t* lens, void* out, float* lse, int B, int Sq, int Hq,
+// sage_attn_fwd_cache and, with a prefix, sage_attn_fwd_cache_prefix, and their 4-bit forms.
+template <typename Cache>
+sage_status run_cache_attention(const void* q, int64_t q_sb, int64_t q_ss, const Cache* cache, const int32_t* prefix_table,
+                                int prefix_len, const int32_t* table, int width, int64_t stride, const int32_t* lens, void* out, float* lse, int B, int Sq, int Hq,
                                 int D, float softmax_scale, int causal, void* ws, size_t ws_bytes, void* stream) {
-  sage_status s = check_cache(cache, D, table, width, stride);
+  CacheAttnArgs a;
+  sage_status s = check_cache(cache, D, table, width, stride, &a.cache);
   if (s == SAGE_OK) s = check_shape(B, Sq, Hq, D);
   if (s == SAGE_OK && Hq % cache->H != 0)
     s = fail(SAGE_ERR_INVALID_ARG, "Hq = %d is not a multiple of the cache's H = %d", Hq, cache->H);
@@ -404,8 +439,6 @@ sage_status run_cache_attention(const void* q, int64_t q_sb, int64_t q_ss, const
     if (ws_bytes < need)
       return fail(SAGE_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu bytes needed", ws_bytes, need);
   }
-  CacheAttnArgs a;
-  a.cache = cache_view(cache);
   a.table = {table, width, stride};
   a.lens = lens;
   a.prefix_pages = prefix_table;
@@ -431,6 +464,191 @@ sage_status run_cache_attention(const void* q, int64_t q_sb, int64_t q_ss, const
     return err == cudaSuccess ? SAGE_OK : cuda_fail(err, "cache attention launch");
   };
   return ws || !cache_attn_needs_workspace(a) ? launch(ws) : with_pool_workspace(need, st, launch);
+}
+
+template <typename Cache>
+sage_status run_prefix_attention(const void* q, int64_t q_sb, int64_t q_ss, const Cache* cache, const int32_t* prefix_table,
+                                 int prefix_len, const int32_t* table, int width, int64_t stride, const int32_t* lens,
+                                 void* out, float* lse, int B, int Sq, int Hq, int D, float softmax_scale, int causal,
+                                 void* ws, size_t ws_bytes, void* stream) {
+  const sage_status s = check_ints(prefix_table, "prefix_table");
+  if (s != SAGE_OK) return s;
+  if (prefix_len < 1 || prefix_len > kMaxCacheLen)
+    return fail(SAGE_ERR_INVALID_ARG, "prefix_len must be in [1, 2^30] (got %d)", prefix_len);
+  return run_cache_attention(q, q_sb, q_ss, cache, prefix_table, prefix_len, table, width, stride, lens, out, lse, B, Sq, Hq,
+                             D, softmax_scale, causal, ws, ws_bytes, stream);
+}
+
+template <typename Cache>
+sage_status run_cache_write(const Cache* cache, const void* k, const void* v, int64_t k_stride_b, int64_t k_stride_s,
+                            int64_t v_stride_b, int64_t v_stride_s, int B, int S, int D,
+                            const int32_t* block_table, int table_width, int64_t table_stride,
+                            const int32_t* start, const int32_t* count, void* stream) {
+  CacheWriteArgs a;
+  sage_status s = check_cache(cache, D, block_table, table_width, table_stride, &a.cache);
+  if (s == SAGE_OK) s = check_shape(B, S, cache->H, D);
+  if (s == SAGE_OK && static_cast<int64_t>(B) * cache->H > INT_MAX / S)
+    s = fail(SAGE_ERR_INVALID_ARG, "B*S*H exceeds 2^31-1");
+  if (s == SAGE_OK) s = check_ptrs({{k, "k"}, {v, "v"}});
+  if (s == SAGE_OK) s = check_strides(k_stride_b, k_stride_s, "k");
+  if (s == SAGE_OK) s = check_strides(v_stride_b, v_stride_s, "v");
+  if (s == SAGE_OK) s = check_ints(start, "start");
+  if (s == SAGE_OK && count) s = check_ints(count, "count");
+  if (s != SAGE_OK) return s;
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.k_sb = k_stride_b;
+  a.k_ss = k_stride_s;
+  a.v_sb = v_stride_b;
+  a.v_ss = v_stride_s;
+  a.B = B;
+  a.S = S;
+  a.table = {block_table, table_width, table_stride};
+  a.start = start;
+  a.count = count;
+  cudaError_t e = device_error_word(&a.err);
+  if (e != cudaSuccess) return cuda_fail(e, "device error word");
+  if (fault_fires(SAGE_FAULT_QUANT_LAUNCH)) return fail(SAGE_ERR_CUDA, "cache write launch: injected fault");
+  e = launch_kv_cache_write(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "cache write launch");
+  return SAGE_OK;
+}
+
+template <typename Cache>
+sage_status run_cache_read(const Cache* cache, const int32_t* block_table, int table_width, int64_t table_stride,
+                           const int32_t* lens, void* k, void* v, int B, int S, int D, void* stream) {
+  CacheReadArgs a;
+  sage_status s = check_cache(cache, D, block_table, table_width, table_stride, &a.cache);
+  if (s == SAGE_OK) s = check_shape(B, S, cache->H, D);
+  if (s == SAGE_OK && static_cast<int64_t>(B) * cache->H > INT_MAX / S)
+    s = fail(SAGE_ERR_INVALID_ARG, "B*S*H exceeds 2^31-1");
+  if (s == SAGE_OK) s = check_ptrs({{k, "k"}, {v, "v"}});
+  if (s == SAGE_OK && !(aligned(k, 32) && aligned(v, 32)))
+    s = fail(SAGE_ERR_MISALIGNED, "k or v is not 32-byte aligned");
+  if (s == SAGE_OK) s = check_ints(lens, "lens");
+  if (s != SAGE_OK) return s;
+  a.table = {block_table, table_width, table_stride};
+  a.lens = lens;
+  a.k = static_cast<uint16_t*>(k);
+  a.v = static_cast<uint16_t*>(v);
+  a.B = B;
+  a.S = S;
+  cudaError_t e = device_error_word(&a.err);
+  if (e != cudaSuccess) return cuda_fail(e, "device error word");
+  if (fault_fires(SAGE_FAULT_QUANT_LAUNCH)) return fail(SAGE_ERR_CUDA, "cache read launch: injected fault");
+  e = launch_kv_cache_read(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "cache read launch");
+  return SAGE_OK;
+}
+
+// F = f / (2 pi) in 2^-64, to the nearest: 1 / (2 pi) in two doubles and the product's
+// rounding error, for |f| <= 3.
+uint64_t revolutions(double f) {
+  constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;   // 1 / (2 pi)
+  const double p = f * kHi, e = std::fma(f, kHi, -p) + f * kLo;
+  const double whole = std::ldexp(p, 32), up = std::floor(whole);      // upper 32 bits
+  const double rest = std::ldexp(whole - up, 32) + std::ldexp(e, 64);  // below 2^32 and a rounding
+  return (static_cast<uint64_t>(static_cast<int64_t>(up)) << 32) + static_cast<uint64_t>(std::llrint(rest));
+}
+
+// Norm and rotation as sage_qk_norm_rope and sage_kv_cache_append take them.
+sage_status turn_args(TurnArgs* a, const sage_rope* rope, const int32_t* positions, int64_t p_sb, int64_t p_ss,
+                      const void* q_weight, const void* k_weight, float eps) {
+  if (!(eps >= 0.0f) || std::isinf(eps)) {
+    if (eps != -1.0f) return fail(SAGE_ERR_INVALID_ARG, "eps must be finite and >= 0, or -1 for no norm (got %g)", eps);
+    if (q_weight || k_weight) return fail(SAGE_ERR_INVALID_ARG, "weights without a norm");
+  }
+  if (q_weight && !aligned(q_weight, 16)) return fail(SAGE_ERR_MISALIGNED, "q_weight is not 16-byte aligned");
+  if (k_weight && !aligned(k_weight, 16)) return fail(SAGE_ERR_MISALIGNED, "k_weight is not 16-byte aligned");
+  a->norm = eps >= 0.0f;
+  a->eps = eps;
+  a->q_weight = static_cast<const uint16_t*>(q_weight);
+  a->k_weight = static_cast<const uint16_t*>(k_weight);
+  if (!rope) return SAGE_OK;
+  if (rope->dim < 32 || rope->dim > kHeadDim || rope->dim % 32 != 0)
+    return fail(SAGE_ERR_UNSUPPORTED, "%d rotated channels are not supported: 32, 64, 96 or 128", rope->dim);
+  if (rope->axes < 1 || rope->axes > kMaxAxes)
+    return fail(SAGE_ERR_UNSUPPORTED, "%d axes are not supported: 1 to %d", rope->axes, kMaxAxes);
+  int pairs = 0;
+  for (int i = 0; i < rope->axes; ++i) {
+    if (rope->sections[i] < 0 || rope->sections[i] > kHeadDim)
+      return fail(SAGE_ERR_INVALID_ARG, "section %d has %d pairs", i, rope->sections[i]);
+    pairs += rope->sections[i];
+    a->rope.ends[i] = pairs;
+  }
+  for (int i = rope->axes; i < kMaxAxes; ++i) a->rope.ends[i] = pairs;
+  if (pairs != rope->dim / 2)
+    return fail(SAGE_ERR_INVALID_ARG, "the sections have %d pairs, the rotated channels %d", pairs, rope->dim / 2);
+  if (!std::isfinite(rope->factor)) return fail(SAGE_ERR_INVALID_ARG, "factor must be finite (got %g)", rope->factor);
+  if (!rope->freq) return fail(SAGE_ERR_INVALID_ARG, "freq is NULL");
+  if (!aligned(rope->freq, 8)) return fail(SAGE_ERR_MISALIGNED, "freq is not 8-byte aligned");
+  sage_status s = check_ints(positions, "positions");
+  if (s != SAGE_OK) return s;
+  if (p_sb < 0 || p_ss < 0) return fail(SAGE_ERR_INVALID_ARG, "positions has a negative stride");
+  a->rope.freq = rope->freq;
+  a->rope.rot = rope->dim;
+  a->rope.interleaved = rope->interleaved != 0;
+  a->rope.axes = rope->axes;
+  a->rope.factor = rope->factor;
+  a->positions = positions;
+  a->p_sb = p_sb;
+  a->p_ss = p_ss;
+  return SAGE_OK;
+}
+
+template <typename Cache>
+sage_status run_cache_append(const Cache* cache, const void* q, const void* k, const void* v, int64_t q_sb, int64_t q_ss,
+                             int64_t k_sb, int64_t k_ss, int64_t v_sb, int64_t v_ss, int B, int S, int Hq, int D,
+                             const sage_rope* rope, const int32_t* positions, int64_t p_sb, int64_t p_ss,
+                             const void* q_weight, const void* k_weight, float eps, const int32_t* slots, void* q_out,
+                             void* stream) {
+  TurnArgs a = {};
+  sage_status s = check_cache(cache, D, &a.cache);
+  if (s == SAGE_OK) s = check_shape(B, S, cache->H, D);
+  if (s == SAGE_OK && Hq < 0) s = fail(SAGE_ERR_INVALID_ARG, "Hq must be >= 0 (got %d)", Hq);
+  if (s == SAGE_OK && (static_cast<int64_t>(Hq) + 2ll * cache->H) * B > INT_MAX / S)
+    s = fail(SAGE_ERR_INVALID_ARG, "B*S*(Hq+2H) exceeds 2^31-1");
+  if (s == SAGE_OK) s = check_ptrs({{k, "k"}, {v, "v"}});
+  if (s == SAGE_OK && Hq > 0) s = check_ptrs({{q, "q"}, {q_out, "q_out"}});
+  if (s == SAGE_OK && Hq > 0) s = check_strides(q_sb, q_ss, "q");
+  if (s == SAGE_OK) s = check_strides(k_sb, k_ss, "k");
+  if (s == SAGE_OK) s = check_strides(v_sb, v_ss, "v");
+  if (s == SAGE_OK) s = check_ints(slots, "slots");
+  if (s == SAGE_OK) s = turn_args(&a, rope, positions, p_sb, p_ss, q_weight, k_weight, eps);
+  if (s != SAGE_OK) return s;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.q_sb = q_sb;
+  a.q_ss = q_ss;
+  a.k_sb = k_sb;
+  a.k_ss = k_ss;
+  a.v_sb = v_sb;
+  a.v_ss = v_ss;
+  a.B = B;
+  a.S = S;
+  a.Hq = Hq;
+  a.Hk = cache->H;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.slots = slots;
+  cudaError_t e = device_error_word(&a.err);
+  if (e != cudaSuccess) return cuda_fail(e, "device error word");
+  if (fault_fires(SAGE_FAULT_QUANT_LAUNCH)) return fail(SAGE_ERR_CUDA, "cache append launch: injected fault");
+  e = launch_turn(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SAGE_OK : cuda_fail(e, "cache append launch");
+}
+
+sage_status check_pages(int num_pages, int page_size, int B, const int32_t* table, int width, int64_t stride, int* shift,
+                        int64_t* room) {
+  sage_status s = check_page_size(page_size, shift);
+  if (s == SAGE_OK && (num_pages < 1 || num_pages > INT_MAX / page_size))
+    s = fail(SAGE_ERR_INVALID_ARG, "num_pages must be >= 1 and num_pages * page_size at most 2^31-1 (got %d)", num_pages);
+  if (s == SAGE_OK && (B < 1 || B > (1 << 20))) s = fail(SAGE_ERR_INVALID_ARG, "B must be in [1, 2^20] (got %d)", B);
+  if (s == SAGE_OK) s = check_table(table, width, stride);
+  if (s == SAGE_OK && B > 1 && stride < width)
+    s = fail(SAGE_ERR_INVALID_ARG, "rows of block_table that overlap (stride %lld, width %d)", static_cast<long long>(stride), width);
+  *room = std::min<int64_t>(kMaxCacheLen, static_cast<int64_t>(width) << *shift);
+  return s;
 }
 
 }  // namespace
@@ -737,63 +955,184 @@ sage_status sage_kv_cache_write(const sage_kv_cache* cache, const void* k, const
                                 int64_t k_stride_s, int64_t v_stride_b, int64_t v_stride_s, int B, int S, int D,
                                 const int32_t* block_table, int table_width, int64_t table_stride,
                                 const int32_t* start, const int32_t* count, void* stream) {
-  sage_status s = check_cache(cache, D, block_table, table_width, table_stride);
-  if (s == SAGE_OK) s = check_shape(B, S, cache->H, D);
-  if (s == SAGE_OK && static_cast<int64_t>(B) * cache->H > INT_MAX / S)
-    s = fail(SAGE_ERR_INVALID_ARG, "B*S*H exceeds 2^31-1");
-  if (s == SAGE_OK) s = check_ptrs({{k, "k"}, {v, "v"}});
-  if (s == SAGE_OK) s = check_strides(k_stride_b, k_stride_s, "k");
-  if (s == SAGE_OK) s = check_strides(v_stride_b, v_stride_s, "v");
-  if (s == SAGE_OK) s = check_ints(start, "start");
-  if (s == SAGE_OK && count) s = check_ints(count, "count");
-  if (s != SAGE_OK) return s;
-  CacheWriteArgs a;
-  a.cache = cache_view(cache);
-  a.k = static_cast<const uint16_t*>(k);
-  a.v = static_cast<const uint16_t*>(v);
-  a.k_sb = k_stride_b;
-  a.k_ss = k_stride_s;
-  a.v_sb = v_stride_b;
-  a.v_ss = v_stride_s;
-  a.B = B;
-  a.S = S;
-  a.table = {block_table, table_width, table_stride};
-  a.start = start;
-  a.count = count;
-  cudaError_t e = device_error_word(&a.err);
-  if (e != cudaSuccess) return cuda_fail(e, "device error word");
-  if (fault_fires(SAGE_FAULT_QUANT_LAUNCH)) return fail(SAGE_ERR_CUDA, "cache write launch: injected fault");
-  e = launch_kv_cache_write(a, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "cache write launch");
-  return SAGE_OK;
+  return run_cache_write(cache, k, v, k_stride_b, k_stride_s, v_stride_b, v_stride_s, B, S, D, block_table, table_width,
+                         table_stride, start, count, stream);
+}
+
+sage_status sage_kv4_cache_write(const sage_kv4_cache* cache, const void* k, const void* v, int64_t k_stride_b,
+                                 int64_t k_stride_s, int64_t v_stride_b, int64_t v_stride_s, int B, int S, int D,
+                                 const int32_t* block_table, int table_width, int64_t table_stride,
+                                 const int32_t* start, const int32_t* count, void* stream) {
+  return run_cache_write(cache, k, v, k_stride_b, k_stride_s, v_stride_b, v_stride_s, B, S, D, block_table, table_width,
+                         table_stride, start, count, stream);
 }
 
 sage_status sage_kv_cache_read(const sage_kv_cache* cache, const int32_t* block_table, int table_width,
                                int64_t table_stride, const int32_t* lens, void* k, void* v, int B, int S, int D,
                                void* stream) {
-  sage_status s = check_cache(cache, D, block_table, table_width, table_stride);
-  if (s == SAGE_OK) s = check_shape(B, S, cache->H, D);
-  if (s == SAGE_OK && static_cast<int64_t>(B) * cache->H > INT_MAX / S)
-    s = fail(SAGE_ERR_INVALID_ARG, "B*S*H exceeds 2^31-1");
-  if (s == SAGE_OK) s = check_ptrs({{k, "k"}, {v, "v"}});
-  if (s == SAGE_OK && !(aligned(k, 32) && aligned(v, 32)))
-    s = fail(SAGE_ERR_MISALIGNED, "k or v is not 32-byte aligned");
-  if (s == SAGE_OK) s = check_ints(lens, "lens");
+  return run_cache_read(cache, block_table, table_width, table_stride, lens, k, v, B, S, D, stream);
+}
+
+sage_status sage_kv4_cache_read(const sage_kv4_cache* cache, const int32_t* block_table, int table_width,
+                                int64_t table_stride, const int32_t* lens, void* k, void* v, int B, int S, int D,
+                                void* stream) {
+  return run_cache_read(cache, block_table, table_width, table_stride, lens, k, v, B, S, D, stream);
+}
+
+sage_status sage_kv_cache_append(const sage_kv_cache* cache, const void* q, const void* k, const void* v, int64_t q_stride_b,
+                                 int64_t q_stride_s, int64_t k_stride_b, int64_t k_stride_s, int64_t v_stride_b,
+                                 int64_t v_stride_s, int B, int S, int Hq, int D, const sage_rope* rope,
+                                 const int32_t* positions, int64_t pos_stride_b, int64_t pos_stride_s, const void* q_weight,
+                                 const void* k_weight, float eps, const int32_t* slots, void* q_out, void* stream) {
+  return run_cache_append(cache, q, k, v, q_stride_b, q_stride_s, k_stride_b, k_stride_s, v_stride_b, v_stride_s, B, S, Hq,
+                          D, rope, positions, pos_stride_b, pos_stride_s, q_weight, k_weight, eps, slots, q_out, stream);
+}
+
+sage_status sage_kv4_cache_append(const sage_kv4_cache* cache, const void* q, const void* k, const void* v,
+                                  int64_t q_stride_b, int64_t q_stride_s, int64_t k_stride_b, int64_t k_stride_s,
+                                  int64_t v_stride_b, int64_t v_stride_s, int B, int S, int Hq, int D,
+                                  const sage_rope* rope, const int32_t* positions, int64_t pos_stride_b,
+                                  int64_t pos_stride_s, const void* q_weight, const void* k_weight, float eps,
+                                  const int32_t* slots, void* q_out, void* stream) {
+  return run_cache_append(cache, q, k, v, q_stride_b, q_stride_s, k_stride_b, k_stride_s, v_stride_b, v_stride_s, B, S, Hq,
+                          D, rope, positions, pos_stride_b, pos_stride_s, q_weight, k_weight, eps, slots, q_out, stream);
+}
+
+sage_status sage_qk_norm_rope(const void* q, const void* k, int64_t q_stride_b, int64_t q_stride_s, int64_t k_stride_b,
+                              int64_t k_stride_s, int B, int S, int Hq, int Hk, int D, const sage_rope* rope,
+                              const int32_t* positions, int64_t pos_stride_b, int64_t pos_stride_s, const void* q_weight,
+                              const void* k_weight, float eps, void* q_out, void* k_out, void* stream) {
+  TurnArgs a = {};
+  sage_status s = check_shape(B, S, Hq, D);
+  if (s == SAGE_OK && Hk < 0) s = fail(SAGE_ERR_INVALID_ARG, "Hk must be >= 0 (got %d)", Hk);
+  if (s == SAGE_OK && (static_cast<int64_t>(Hq) + Hk) * B > INT_MAX / S)
+    s = fail(SAGE_ERR_INVALID_ARG, "B*S*(Hq+Hk) exceeds 2^31-1");
+  if (s == SAGE_OK) s = check_ptrs({{q, "q"}, {q_out, "q_out"}});
+  if (s == SAGE_OK) s = check_strides(q_stride_b, q_stride_s, "q");
+  if (s == SAGE_OK && Hk > 0) s = check_ptrs({{k, "k"}, {k_out, "k_out"}});
+  if (s == SAGE_OK && Hk > 0) s = check_strides(k_stride_b, k_stride_s, "k");
+  if (s == SAGE_OK) s = turn_args(&a, rope, positions, pos_stride_b, pos_stride_s, q_weight, k_weight, eps);
   if (s != SAGE_OK) return s;
-  CacheReadArgs a;
-  a.cache = cache_view(cache);
-  a.table = {block_table, table_width, table_stride};
-  a.lens = lens;
-  a.k = static_cast<uint16_t*>(k);
-  a.v = static_cast<uint16_t*>(v);
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.q_sb = q_stride_b;
+  a.q_ss = q_stride_s;
+  a.k_sb = k_stride_b;
+  a.k_ss = k_stride_s;
   a.B = B;
   a.S = S;
+  a.Hq = Hq;
+  a.Hk = Hk;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k_out = static_cast<uint16_t*>(k_out);
+  if (fault_fires(SAGE_FAULT_QUANT_LAUNCH)) return fail(SAGE_ERR_CUDA, "norm and rotation launch: injected fault");
+  const cudaError_t e = launch_turn(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SAGE_OK : cuda_fail(e, "norm and rotation launch");
+}
+
+sage_status sage_rope_frequencies(int dim, double base, int scaling, double factor, double original_len, double low,
+                                  double high, uint64_t* freq, double* attention_factor) {
+  if (!freq || !attention_factor) return fail(SAGE_ERR_INVALID_ARG, "freq and attention_factor must not be NULL");
+  if (dim < 2 || dim > kHeadDim || dim % 2 != 0)
+    return fail(SAGE_ERR_INVALID_ARG, "dim must be even and in [2, 128] (got %d)", dim);
+  if (!std::isfinite(base) || base <= 1.0) return fail(SAGE_ERR_INVALID_ARG, "base must be finite and > 1 (got %g)", base);
+  if (scaling < SAGE_ROPE_PLAIN || scaling > SAGE_ROPE_BANDS)
+    return fail(SAGE_ERR_UNSUPPORTED, "scaling %d is not one of SAGE_ROPE_*", scaling);
+  if (scaling != SAGE_ROPE_PLAIN && (!std::isfinite(factor) || factor < 1.0))
+    return fail(SAGE_ERR_INVALID_ARG, "factor must be finite and >= 1 (got %g)", factor);
+  const bool by_len = scaling == SAGE_ROPE_YARN || scaling == SAGE_ROPE_BANDS;
+  if (by_len && (!std::isfinite(original_len) || original_len < 1.0 || !std::isfinite(low) || !std::isfinite(high) || low <= 0.0 || high <= low))
+    return fail(SAGE_ERR_INVALID_ARG, "original_len must be >= 1 and 0 < low < high (got %g, %g, %g)", original_len, low, high);
+  constexpr double kTwoPi = 6.283185307179586476925286766559;
+  if (scaling == SAGE_ROPE_NTK && dim > 2) base *= std::pow(factor, dim / (dim - 2.0));
+  double lo = 0.0, hi = 0.0;                 // of the ramp over the pairs
+  if (scaling == SAGE_ROPE_YARN) {
+    lo = std::max(0.0, std::floor(dim * std::log(original_len / (high * kTwoPi)) / (2.0 * std::log(base))));
+    hi = std::min(dim - 1.0, std::ceil(dim * std::log(original_len / (low * kTwoPi)) / (2.0 * std::log(base))));
+  }
+  for (int i = 0; i < dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / dim);
+    if (scaling == SAGE_ROPE_LINEAR) f /= factor;
+    if (scaling == SAGE_ROPE_YARN) {
+      const double ramp = std::min(1.0, std::max(0.0, (i - lo) / std::max(1e-3, hi - lo)));
+      f = f / factor * ramp + f * (1.0 - ramp);
+    }
+    if (scaling == SAGE_ROPE_BANDS) {
+      const double keep = std::min(1.0, std::max(0.0, (original_len * f / kTwoPi - low) / (high - low)));
+      f = f / factor * (1.0 - keep) + f * keep;
+    }
+    freq[i] = revolutions(f);
+  }
+  *attention_factor = scaling == SAGE_ROPE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0;
+  return SAGE_OK;
+}
+
+uint64_t sage_rope_frequency(double radians) { return std::isfinite(radians) && std::fabs(radians) <= 3.0 ? revolutions(radians) : 0; }
+
+sage_status sage_kv_pages_reserve(const int32_t* free_pages, const int32_t* free_count, int num_pages, int page_size,
+                                  const int32_t* lens, const int32_t* counts, int B, int32_t* block_table, int table_width,
+                                  int64_t table_stride, int layout, int tokens, int32_t* start, int32_t* taken,
+                                  int32_t* new_lens, int32_t* first, int32_t* free_left, int32_t* slots,
+                                  int32_t* positions, void* stream) {
+  PagesArgs a = {};
+  sage_status s = check_pages(num_pages, page_size, B, block_table, table_width, table_stride, &a.page_shift, &a.room);
+  if (s == SAGE_OK && (layout < SAGE_TOKENS_PACKED || layout > SAGE_TOKENS_END))
+    s = fail(SAGE_ERR_UNSUPPORTED, "layout %d is not one of SAGE_TOKENS_*", layout);
+  if (s == SAGE_OK && (tokens < 1 || (layout != SAGE_TOKENS_PACKED && tokens > INT_MAX / B)))
+    s = fail(SAGE_ERR_INVALID_ARG, "tokens must be >= 1, B * tokens at most 2^31-1 (got %d)", tokens);
+  const std::pair<const int32_t*, const char*> arrays[] = {
+      {free_pages, "free_pages"}, {free_count, "free_count"}, {lens, "lens"}, {counts, "counts"}, {start, "start"}, {taken, "taken"},
+      {new_lens, "new_lens"}, {first, "first"}, {free_left, "free_left"}, {slots, "slots"}, {positions, "positions"}};
+  for (auto& x : arrays)
+    if (s == SAGE_OK) s = check_ints(x.first, x.second);
+  if (s != SAGE_OK) return s;
+  a.free_pages = free_pages;
+  a.free_count = free_count;
+  a.lens = lens;
+  a.counts = counts;
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.num_pages = num_pages;
+  a.B = B;
+  a.layout = layout;
+  a.tokens = tokens;
+  a.start = start;
+  a.taken = taken;
+  a.new_lens = new_lens;
+  a.first = first;
+  a.free_left = free_left;
+  a.slots = slots;
+  a.positions = positions;
   cudaError_t e = device_error_word(&a.err);
   if (e != cudaSuccess) return cuda_fail(e, "device error word");
-  if (fault_fires(SAGE_FAULT_QUANT_LAUNCH)) return fail(SAGE_ERR_CUDA, "cache read launch: injected fault");
-  e = launch_kv_cache_read(a, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "cache read launch");
-  return SAGE_OK;
+  if (fault_fires(SAGE_FAULT_QUANT_LAUNCH)) return fail(SAGE_ERR_CUDA, "page reservation launch: injected fault");
+  e = launch_pages_reserve(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SAGE_OK : cuda_fail(e, "page reservation launch");
+}
+
+sage_status sage_kv_pages_release(int32_t* free_pages, int32_t* free_count, int num_pages, int page_size, int32_t* lens,
+                                  const int32_t* keep, int B, int32_t* block_table, int table_width, int64_t table_stride,
+                                  void* stream) {
+  ReleaseArgs a = {};
+  sage_status s = check_pages(num_pages, page_size, B, block_table, table_width, table_stride, &a.page_shift, &a.room);
+  if (s == SAGE_OK) s = check_ints(free_pages, "free_pages");
+  if (s == SAGE_OK) s = check_ints(free_count, "free_count");
+  if (s == SAGE_OK) s = check_ints(lens, "lens");
+  if (s == SAGE_OK) s = check_ints(keep, "keep");
+  if (s != SAGE_OK) return s;
+  a.free_pages = free_pages;
+  a.free_count = free_count;
+  a.lens = lens;
+  a.keep = keep;
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.num_pages = num_pages;
+  a.B = B;
+  cudaError_t e = device_error_word(&a.err);
+  if (e != cudaSuccess) return cuda_fail(e, "device error word");
+  if (fault_fires(SAGE_FAULT_QUANT_LAUNCH)) return fail(SAGE_ERR_CUDA, "page release launch: injected fault");
+  e = launch_pages_release(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SAGE_OK : cuda_fail(e, "page release launch");
 }
 
 sage_status sage_attn_fwd_cache(const void* q, int64_t q_stride_b, int64_t q_stride_s, const sage_kv_cache* cache,
@@ -811,13 +1150,29 @@ sage_status sage_attn_fwd_cache_prefix(const void* q, int64_t q_stride_b, int64_
                                        const int32_t* lens, void* out, float* lse, int B, int Sq, int Hq, int D,
                                        float softmax_scale, int causal, void* workspace, size_t workspace_bytes,
                                        void* stream) {
-  const sage_status s = check_ints(prefix_table, "prefix_table");
-  if (s != SAGE_OK) return s;
-  if (prefix_len < 1 || prefix_len > kMaxCacheLen)
-    return fail(SAGE_ERR_INVALID_ARG, "prefix_len must be in [1, 2^30] (got %d)", prefix_len);
-  return run_cache_attention(q, q_stride_b, q_stride_s, cache, prefix_table, prefix_len, block_table, table_width,
-                             table_stride, lens, out, lse, B, Sq, Hq, D, softmax_scale, causal, workspace,
-                             workspace_bytes, stream);
+  return run_prefix_attention(q, q_stride_b, q_stride_s, cache, prefix_table, prefix_len, block_table, table_width,
+                              table_stride, lens, out, lse, B, Sq, Hq, D, softmax_scale, causal, workspace,
+                              workspace_bytes, stream);
+}
+
+sage_status sage_attn_fwd_kv4_cache(const void* q, int64_t q_stride_b, int64_t q_stride_s, const sage_kv4_cache* cache,
+                                    const int32_t* block_table, int table_width, int64_t table_stride,
+                                    const int32_t* lens, void* out, float* lse, int B, int Sq, int Hq, int D,
+                                    float softmax_scale, int causal, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  return run_cache_attention(q, q_stride_b, q_stride_s, cache, nullptr, 0, block_table, table_width, table_stride,
+                             lens, out, lse, B, Sq, Hq, D, softmax_scale, causal, workspace, workspace_bytes, stream);
+}
+
+sage_status sage_attn_fwd_kv4_cache_prefix(const void* q, int64_t q_stride_b, int64_t q_stride_s,
+                                           const sage_kv4_cache* cache, const int32_t* prefix_table, int prefix_len,
+                                           const int32_t* block_table, int table_width, int64_t table_stride,
+                                           const int32_t* lens, void* out, float* lse, int B, int Sq, int Hq, int D,
+                                           float softmax_scale, int causal, void* workspace, size_t workspace_bytes,
+                                           void* stream) {
+  return run_prefix_attention(q, q_stride_b, q_stride_s, cache, prefix_table, prefix_len, block_table, table_width,
+                              table_stride, lens, out, lse, B, Sq, Hq, D, softmax_scale, causal, workspace,
+                              workspace_bytes, stream);
 }
 
 size_t sage_attn_fwd_cache_workspace_bytes(int B, int Sq, int Hq, int H, int prefix_len) {
@@ -902,6 +1257,8 @@ sage_status sage_sync_status(void* stream) {
     return fail(SAGE_ERR_TIMEOUT, "a device-side wait gave up after its time limit");
   if (code == SAGE_DEVERR_BAD_PAGE)
     return fail(SAGE_ERR_BAD_PAGE, "a page table led out of the cache, or a position out of its table");
+  if (code == SAGE_DEVERR_NO_PAGES)
+    return fail(SAGE_ERR_NO_PAGES, "the free list had too few pages for all sequences");
   return SAGE_OK;
 }
 
@@ -925,6 +1282,7 @@ const char* sage_status_string(sage_status s) {
     case SAGE_ERR_TIMEOUT: return "SAGE_ERR_TIMEOUT";
     case SAGE_ERR_WORKSPACE: return "SAGE_ERR_WORKSPACE";
     case SAGE_ERR_BAD_PAGE: return "SAGE_ERR_BAD_PAGE";
+    case SAGE_ERR_NO_PAGES: return "SAGE_ERR_NO_PAGES";
   }
   return "SAGE_ERR_UNKNOWN";
 }

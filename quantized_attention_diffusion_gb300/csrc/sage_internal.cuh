@@ -16,7 +16,7 @@ constexpr int kQKBlock = 32;    // tokens per Q/K quantisation block
 constexpr int kTile = 128;      // query rows per Q tile and keys per KV tile
 
 // Device error word codes (read back by the host after a stream sync).
-enum : int { SAGE_DEVERR_NONE = 0, SAGE_DEVERR_TIMEOUT = 1, SAGE_DEVERR_BAD_PAGE = 2 };
+enum : int { SAGE_DEVERR_NONE = 0, SAGE_DEVERR_TIMEOUT = 1, SAGE_DEVERR_BAD_PAGE = 2, SAGE_DEVERR_NO_PAGES = 3 };
 
 inline int padded_len(int S) { return (S + kTile - 1) / kTile * kTile; }
 inline int num_blocks(int S) { return (S + kQKBlock - 1) / kQKBlock; }
@@ -89,13 +89,15 @@ cudaError_t load_quantize_kernels();
 // ---------------------------------------------------- quantised KV cache --
 
 // A paged cache: K codes int8 and V codes E4M3 [num_pages, H, page, 128],
-// scales fp32 [num_pages, H, page], page = 1 << page_shift tokens.
+// scales fp32 [num_pages, H, page], page = 1 << page_shift tokens; or, in 4 bits,
+// E2M1 codes [.., 64] (two to a byte), E4M3 block scales [.., 8] and the scales.
 struct CacheView {
   uint8_t* k_codes;
   float* k_scale;
   uint8_t* v_codes;
   float* v_scale;
-  int num_pages, H, page_shift;
+  uint8_t *k_block, *v_block;            // nullptr in 8 bits
+  int num_pages, H, page_shift, bits;
 };
 
 // Position i of sequence b is token i % page of page table[b * stride + i / page].
@@ -128,6 +130,60 @@ struct CacheReadArgs {
   int* err;
 };
 cudaError_t launch_kv_cache_read(const CacheReadArgs& a, cudaStream_t stream);
+
+// Rotary positions: pair i of the first `rot` channels turns by its axis' position
+// times freq[i] 2^-64 revolutions; axis a has the pairs from ends[a - 1] up to ends[a].
+constexpr int kMaxAxes = 4;
+struct RopeView {
+  const uint64_t* freq;                  // [rot / 2]
+  int rot, interleaved, axes;
+  int ends[kMaxAxes];
+  float factor;                          // of sine and cosine
+};
+
+struct TurnArgs {
+  const uint16_t *q, *k, *v;             // bf16 [B, S, H, 128], heads dense
+  int64_t q_sb, q_ss, k_sb, k_ss, v_sb, v_ss;   // batch and token strides, in elements
+  int B, S, Hq, Hk;
+  RopeView rope;
+  const int32_t* positions;              // [B, S, axes], strides p_sb, p_ss
+  int64_t p_sb, p_ss;
+  const uint16_t *q_weight, *k_weight;   // bf16 [128] or nullptr
+  bool norm;
+  float eps;
+  uint16_t *q_out, *k_out;               // bf16 [B, S, H, 128]
+  const int32_t* slots;                  // [B * S], or nullptr: k goes to k_out
+  CacheView cache;
+  int* err;
+};
+cudaError_t launch_turn(const TurnArgs& a, cudaStream_t stream);
+
+enum : int { kPagesPacked = 0, kPagesFront = 1, kPagesEnd = 2 };
+struct PagesArgs {
+  const int32_t *free_pages, *free_count;   // [num_pages], [1]
+  const int32_t *lens, *counts;             // [B]
+  int32_t* table;                           // [B, width], stride table_stride
+  int64_t table_stride;
+  int num_pages, page_shift, B, layout;
+  int tokens;                               // packed: rows; else rows of each sequence
+  int64_t room;                             // positions that a row of the table has room for
+  int32_t *start, *taken, *new_lens, *first;   // [B]
+  int32_t* free_left;                       // [1]
+  int32_t *slots, *positions;
+  int* err;
+};
+cudaError_t launch_pages_reserve(const PagesArgs& a, cudaStream_t stream);
+
+struct ReleaseArgs {
+  int32_t *free_pages, *free_count, *lens;
+  const int32_t* keep;
+  int32_t* table;
+  int64_t table_stride;
+  int num_pages, page_shift, B;
+  int64_t room;
+  int* err;
+};
+cudaError_t launch_pages_release(const ReleaseArgs& a, cudaStream_t stream);
 
 struct CacheAttnArgs {
   CacheView cache;

@@ -17,6 +17,7 @@ import ctypes
 import math
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -27,7 +28,7 @@ HEAD_DIM = 128
 _STATUS = {
     0: "SAGE_OK", 1: "SAGE_ERR_INVALID_ARG", 2: "SAGE_ERR_UNSUPPORTED", 3: "SAGE_ERR_MISALIGNED",
     4: "SAGE_ERR_CUDA", 5: "SAGE_ERR_NO_MEMORY", 6: "SAGE_ERR_TIMEOUT", 7: "SAGE_ERR_WORKSPACE",
-    8: "SAGE_ERR_BAD_PAGE",
+    8: "SAGE_ERR_BAD_PAGE", 9: "SAGE_ERR_NO_PAGES",
 }
 EXPORTED = (
     "sage_padded_len", "sage_workspace_bytes", "sage_quantize_qkv", "sage_attn_fwd",
@@ -40,6 +41,9 @@ EXPORTED = (
     "sage_debug_inject_fault", "sage_debug_pool_state", "sage_plan_create", "sage_plan_launch",
     "sage_plan_destroy", "sage_plan_create_ex", "sage_kv_cache_write", "sage_kv_cache_read",
     "sage_attn_fwd_cache", "sage_attn_fwd_cache_prefix", "sage_attn_fwd_cache_workspace_bytes",
+    "sage_kv4_cache_write", "sage_kv4_cache_read", "sage_attn_fwd_kv4_cache", "sage_attn_fwd_kv4_cache_prefix",
+    "sage_rope_frequencies", "sage_rope_frequency", "sage_qk_norm_rope", "sage_kv_cache_append",
+    "sage_kv4_cache_append", "sage_kv_pages_reserve", "sage_kv_pages_release",
 )
 
 # Options of sage_plan_create_ex (include/sage.h).
@@ -58,6 +62,19 @@ class _KVCache(ctypes.Structure):
     _fields_ = [("k_codes", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int32), ("H", ctypes.c_int32),
                 ("page_size", ctypes.c_int32)]
+
+
+class _KV4Cache(ctypes.Structure):
+    """sage_kv4_cache (include/sage.h)."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_block", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_block", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("H", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
+class _Rope(ctypes.Structure):
+    """sage_rope (include/sage.h)."""
+    _fields_ = [("freq", ctypes.c_void_p), ("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 4), ("factor", ctypes.c_float)]
 
 
 class SageError(RuntimeError):
@@ -84,7 +101,7 @@ def load_library(path: str = LIB_PATH):
                 f"{path} is missing: build it with `python -m quantized_attention_diffusion_gb300.build`")
         lib = ctypes.CDLL(path)
         P, I, F, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
-        S, L = ctypes.c_int, ctypes.c_int64
+        S, L, D = ctypes.c_int, ctypes.c_int64, ctypes.c_double
         sigs = {
             "sage_padded_len": (ctypes.c_int64, [I]),
             "sage_attn_fwd_launches": (I, [I, I, I, I, I]),
@@ -114,6 +131,17 @@ def load_library(path: str = LIB_PATH):
             "sage_attn_fwd_cache": (S, [P, L, L, P, P, I, L, P, P, P, I, I, I, I, F, I, P, Z, P]),
             "sage_attn_fwd_cache_prefix": (S, [P, L, L, P, P, I, P, I, L, P, P, P, I, I, I, I, F, I, P, Z, P]),
             "sage_attn_fwd_cache_workspace_bytes": (Z, [I, I, I, I, I]),
+            "sage_kv4_cache_write": (S, [P, P, P, L, L, L, L, I, I, I, P, I, L, P, P, P]),
+            "sage_kv4_cache_read": (S, [P, P, I, L, P, P, P, I, I, I, P]),
+            "sage_attn_fwd_kv4_cache": (S, [P, L, L, P, P, I, L, P, P, P, I, I, I, I, F, I, P, Z, P]),
+            "sage_attn_fwd_kv4_cache_prefix": (S, [P, L, L, P, P, I, P, I, L, P, P, P, I, I, I, I, F, I, P, Z, P]),
+            "sage_rope_frequencies": (S, [I, D, I, D, D, D, D, P, P]),
+            "sage_rope_frequency": (ctypes.c_uint64, [D]),
+            "sage_qk_norm_rope": (S, [P, P, L, L, L, L, I, I, I, I, I, P, P, L, L, P, P, F, P, P, P]),
+            "sage_kv_cache_append": (S, [P, P, P, P, L, L, L, L, L, L, I, I, I, I, P, P, L, L, P, P, F, P, P, P]),
+            "sage_kv4_cache_append": (S, [P, P, P, P, L, L, L, L, L, L, I, I, I, I, P, P, L, L, P, P, F, P, P, P]),
+            "sage_kv_pages_reserve": (S, [P, P, I, I, P, P, I, P, I, L, I, I, P, P, P, P, P, P, P, P]),
+            "sage_kv_pages_release": (S, [P, P, I, I, P, P, I, P, I, L, P]),
             "sage_sync_status": (S, [P]),
             "sage_set_wait_timeout_ns": (None, [ctypes.c_uint64]),
             "sage_set_attention_events": (None, [P, P]),
@@ -527,21 +555,30 @@ def debug_pool_state(device=None):
     return bool(created.value), int(used.value)
 
 
-def kv_cache_alloc(num_pages: int, H: int, page_size: int = 64, device=None):
+def kv_cache_alloc(num_pages: int, H: int, page_size: int = 64, device=None, bits: int = 8):
     """Tensors of an empty paged KV cache: (k_codes int8 [num_pages, H,
     page_size, 128], k_scale fp32 [num_pages, H, page_size], v_codes
-    float8_e4m3fn like k_codes, v_scale like k_scale), the tuple that the other
-    kv_cache_* and attn_fwd_cache* functions take.  Contents are undefined
-    until they are written."""
+    float8_e4m3fn like k_codes, v_scale like k_scale), or with ``bits`` 4
+    (k_codes uint8 [num_pages, H, page_size, 64], k_block float8_e4m3fn
+    [num_pages, H, page_size, 8], k_scale, and the same for v): the tuple that the
+    other kv_cache_* and attn_fwd_cache* functions take, of either kind.
+    Contents are undefined until they are written."""
     if page_size not in KV_PAGE_SIZES:
         raise ValueError(f"page_size must be one of {KV_PAGE_SIZES} (got {page_size})")
     if num_pages < 1 or H < 1:
         raise ValueError(f"num_pages and H must be >= 1 (got {num_pages}, {H})")
+    if bits not in (4, 8):
+        raise ValueError(f"bits must be 8 or 4 (got {bits})")
     dev = torch.device("cuda") if device is None else torch.device(device)
-    codes, scales = (num_pages, H, page_size, HEAD_DIM), (num_pages, H, page_size)
-    return (torch.empty(codes, dtype=torch.int8, device=dev), torch.empty(scales, dtype=torch.float32, device=dev),
-            torch.empty(codes, dtype=torch.float8_e4m3fn, device=dev),
-            torch.empty(scales, dtype=torch.float32, device=dev))
+    scales = (num_pages, H, page_size)
+
+    def tensor(n, dtype):
+        return torch.empty(scales + (n,) if n else scales, dtype=dtype, device=dev)
+
+    if bits == 4:
+        return tuple(tensor(n, t) for _ in "kv" for n, t in ((64, torch.uint8), (8, torch.float8_e4m3fn), (0, torch.float32)))
+    return (tensor(HEAD_DIM, torch.int8), tensor(0, torch.float32), tensor(HEAD_DIM, torch.float8_e4m3fn),
+            tensor(0, torch.float32))
 
 
 # The checks below run on every generation step, so they ask each tensor for as
@@ -552,8 +589,32 @@ _INT8, _FP32, _BF16, _INT32 = torch.int8, torch.float32, torch.bfloat16, torch.i
 _FP8 = (torch.float8_e4m3fn, torch.uint8)
 
 
+def _check_kv4_cache(cache):
+    """The tuple of a 4-bit cache as a sage_kv4_cache, and its device number."""
+    kc, kb, ks, vc, vb, vs = cache
+    for name, t, want in (("k_codes", kc, (torch.uint8,)), ("k_block", kb, _FP8), ("k_scale", ks, (_FP32,)),
+                          ("v_codes", vc, (torch.uint8,)), ("v_block", vb, _FP8), ("v_scale", vs, (_FP32,))):
+        if t.dtype not in want:
+            raise ValueError(f"{name} must be {want[0]} (got {t.dtype})")
+    dev = kc.get_device()
+    scales = ks.shape
+    if not kc.is_cuda or any(t.get_device() != dev for t in cache):
+        raise ValueError("the cache must be CUDA tensors on one device")
+    if not all(t.is_contiguous() for t in cache):
+        raise ValueError("the cache's tensors must be contiguous")
+    if len(scales) != 3 or vs.shape != scales or any(t.shape != scales + (n,) for t, n in ((kc, 64), (vc, 64), (kb, 8), (vb, 8))):
+        raise ValueError("a cache of 4 bits is codes [num_pages, H, page_size, 64], blocks [.., 8] and scales [num_pages, H, "
+                         f"page_size] (got {[tuple(t.shape) for t in cache]})")
+    pages, H, page = scales
+    if page not in KV_PAGE_SIZES or pages < 1 or H < 1:
+        raise ValueError(f"a cache has pages of {KV_PAGE_SIZES} tokens (got {tuple(scales)})")
+    return _KV4Cache(kc.data_ptr(), kb.data_ptr(), ks.data_ptr(), vc.data_ptr(), vb.data_ptr(), vs.data_ptr(), pages, H, page), dev
+
+
 def _check_cache(cache):
-    """The cache tuple as a sage_kv_cache, and its device number."""
+    """The cache tuple as a sage_kv_cache or a sage_kv4_cache, and its device number."""
+    if isinstance(cache, (tuple, list)) and len(cache) == 6:
+        return _check_kv4_cache(cache)
     if not isinstance(cache, (tuple, list)) or len(cache) != 4:
         raise TypeError("cache must be (k_codes, k_scale, v_codes, v_scale)")
     kc, ks, vc, vs = cache
@@ -638,7 +699,7 @@ def kv_cache_write(k, v, cache, block_table, start, count=None):
     _check_ints("start", start, B, dev)
     if count is not None:
         _check_ints("count", count, B, dev)
-    _call(lib.sage_kv_cache_write, dev, ctypes.byref(c), k.data_ptr(), v.data_ptr(), k_sb, k_ss, v_sb, v_ss, B, S,
+    _call(lib.sage_kv_cache_write if len(cache) == 4 else lib.sage_kv4_cache_write, dev, ctypes.byref(c), k.data_ptr(), v.data_ptr(), k_sb, k_ss, v_sb, v_ss, B, S,
           HEAD_DIM, block_table.data_ptr(), width, stride, start.data_ptr(), None if count is None else count.data_ptr())
     return cache
 
@@ -666,7 +727,7 @@ def kv_cache_read(cache, block_table, lens, S: int, out=None):
         for t in out:
             if t.shape != shape or t.dtype is not _BF16 or t.get_device() != dev or not t.is_contiguous():
                 raise ValueError(f"out must be two contiguous bf16 tensors {shape} on cuda:{dev}")
-    _call(lib.sage_kv_cache_read, dev, ctypes.byref(c), block_table.data_ptr(), width, stride, lens.data_ptr(),
+    _call(lib.sage_kv_cache_read if len(cache) == 4 else lib.sage_kv4_cache_read, dev, ctypes.byref(c), block_table.data_ptr(), width, stride, lens.data_ptr(),
           out[0].data_ptr(), out[1].data_ptr(), B, S, HEAD_DIM)
     return out
 
@@ -703,14 +764,14 @@ def _attn_fwd_cache(q, cache, prefix, block_table, lens, softmax_scale, causal, 
     tail = (block_table.data_ptr(), width, stride, lens.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
             B, Sq, Hq, D, softmax_scale, 1 if causal else 0, None if workspace is None else workspace.data_ptr(), ws_bytes)
     if prefix is None:
-        _call(lib.sage_attn_fwd_cache, dev, q.data_ptr(), q_sb, q_ss, ctypes.byref(c), *tail)
+        _call(lib.sage_attn_fwd_cache if len(cache) == 4 else lib.sage_attn_fwd_kv4_cache, dev, q.data_ptr(), q_sb, q_ss, ctypes.byref(c), *tail)
     else:
         table, length = prefix
         if length < 1 or table.dim() != 1 or table.shape[0] < -(-length // c.page_size):
             raise ValueError(f"prefix_table must name the pages of prefix_len >= 1 positions (got "
                              f"{tuple(table.shape)} for {length})")
         _check_ints("prefix_table", table, table.shape[0], dev)
-        _call(lib.sage_attn_fwd_cache_prefix, dev, q.data_ptr(), q_sb, q_ss, ctypes.byref(c), table.data_ptr(), length, *tail)
+        _call(lib.sage_attn_fwd_cache_prefix if len(cache) == 4 else lib.sage_attn_fwd_kv4_cache_prefix, dev, q.data_ptr(), q_sb, q_ss, ctypes.byref(c), table.data_ptr(), length, *tail)
     return (out, lse) if lse is not None else out
 
 
@@ -742,3 +803,244 @@ def attn_fwd_cache_prefix(q, cache, prefix_table, prefix_len: int, block_table, 
     a few and a short prefix are done sooner without (sage_attn_fwd_cache_prefix)."""
     return _attn_fwd_cache(q, cache, (prefix_table, int(prefix_len)), block_table, lens, softmax_scale, causal, out,
                            lse, return_lse, workspace)
+
+
+# Scaling of positions and where tokens stand (include/sage.h).
+ROPE_SCALINGS = ("plain", "linear", "ntk", "yarn", "bands")
+TOKEN_LAYOUTS = ("packed", "front", "end")
+
+
+class Rope:
+    """Rotary positions of the first ``dim`` channels (32, 64, 96 or 128) of a head
+    (sage_rope): pairs (2i, 2i + 1) with ``interleaved``, else (i, i + dim / 2).
+
+    ``sections`` names the pairs of each of up to four axes (for images and videos),
+    which have frequencies base ** (-2i / (2 * pairs)) of their own; without it there is
+    one axis.  ``scaling``: None, ("linear", factor), ("ntk", factor), ("yarn", factor,
+    original_len[, low, high]) or ("bands", factor, original_len[, low, high]).
+    ``freqs`` (dim / 2 radians a position, at most 3) replaces base and scaling.
+    ``freq`` is the table on the device, ``factor`` what sine and cosine are
+    multiplied by (given, it replaces the scaling's)."""
+
+    def __init__(self, dim: int = HEAD_DIM, base: float = 10000.0, interleaved: bool = False, sections=None, scaling=None,
+                 freqs=None, factor: float | None = None, device=None):
+        lib = load_library()
+        if dim not in (32, 64, 96, 128):
+            raise ValueError(f"dim must be 32, 64, 96 or 128 (got {dim})")
+        self.dim, self.interleaved = int(dim), bool(interleaved)
+        self.sections = (self.dim // 2,) if sections is None else tuple(int(n) for n in sections)
+        if not 1 <= len(self.sections) <= 4 or min(self.sections) < 1 or sum(self.sections) != self.dim // 2:
+            raise ValueError(f"sections must be 1 to 4 numbers >= 1 that add up to {self.dim // 2} (got {self.sections})")
+        table, own = [], ctypes.c_double(1.0)
+        if freqs is not None:
+            freqs = [float(f) for f in freqs]
+            if scaling is not None or len(freqs) != self.dim // 2 or not all(abs(f) <= 3.0 for f in freqs):
+                raise ValueError(f"freqs must be {self.dim // 2} numbers of at most 3, without scaling")
+            table = [lib.sage_rope_frequency(f) for f in freqs]
+        else:
+            kind, *rest = scaling if scaling is not None else ("plain",)
+            if kind not in ROPE_SCALINGS or len(rest) not in {"plain": (0,), "linear": (1,), "ntk": (1,)}.get(kind, (2, 4)):
+                raise ValueError(f"scaling must be (kind, factor[, original_len[, low, high]]), kind one of {ROPE_SCALINGS} (got {scaling})")
+            rest = [float(x) for x in rest] + [1.0, 0.0, 1.0, 32.0 if kind == "yarn" else 4.0][len(rest):]
+            for n in self.sections:
+                part = (ctypes.c_uint64 * n)()
+                _check(lib.sage_rope_frequencies(2 * n, float(base), ROPE_SCALINGS.index(kind), *rest, part, ctypes.byref(own)))
+                table += list(part)
+        self.factor = own.value if factor is None else float(factor)
+        dev = torch.device("cuda") if device is None else torch.device(device)
+        signed = [f - (1 << 64) if f >> 63 else f for f in table]
+        self.freq = torch.tensor(signed, dtype=torch.int64, device=dev)
+        self._c = _Rope(self.freq.data_ptr(), self.dim, int(self.interleaved), len(self.sections),
+                        (ctypes.c_int32 * 4)(*self.sections), self.factor)
+
+
+def _check_turn(rope, positions, q_weight, k_weight, eps, B, S, dev):
+    """The arguments of norm and rotation: (rope, positions, their strides, weights, eps)."""
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None and (w.dtype is not _BF16 or w.shape != (HEAD_DIM,) or not w.is_contiguous() or w.get_device() != dev):
+            raise ValueError(f"{name} must be a contiguous bf16 [128] tensor on cuda:{dev}")
+    if eps is None and not (q_weight is None and k_weight is None):
+        raise ValueError("weights without a norm: give eps")
+    if eps is not None and not 0.0 <= eps < math.inf:
+        raise ValueError(f"eps must be finite and >= 0 (got {eps})")
+    tail = (None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
+            -1.0 if eps is None else eps)
+    if rope is None:
+        if positions is not None:
+            raise ValueError("positions without rope")
+        return (None, None, 0, 0) + tail
+    if not isinstance(rope, Rope):
+        raise TypeError("rope must be a Rope")
+    if rope.freq.get_device() != dev:
+        raise ValueError(f"rope must be on cuda:{dev}")
+    if not isinstance(positions, torch.Tensor):
+        raise TypeError("rope needs positions, a torch.Tensor")
+    axes = len(rope.sections)
+    shape = positions.shape
+    if axes == 1 and (len(shape) < 1 or shape[-1] != 1 or (len(shape) == 1 and S == 1)):
+        positions = positions.unsqueeze(-1)
+        shape = positions.shape
+    if len(shape) == 2:
+        # [S, axes] for all batches, or, for packed tokens or one token of each sequence, [B * S, axes]
+        if shape[0] == S:
+            positions = positions.unsqueeze(0).expand(B, -1, -1)
+        elif shape[0] == B * S:
+            positions = positions.view(B, S, axes)
+        shape = positions.shape
+    if positions.dtype is not _INT32 or positions.get_device() != dev or shape != (B, S, axes):
+        raise ValueError(f"positions must be int32 [{B}, {S}{', ' + str(axes) if axes > 1 else ''}] on cuda:{dev} "
+                         f"(got {positions.dtype} {tuple(shape)})")
+    sb, ss, sa = positions.stride()
+    if axes > 1 and sa != 1:
+        raise ValueError("the axes of a position must be dense")
+    return (ctypes.byref(rope._c), positions.data_ptr(), sb if B > 1 else 0, ss if S > 1 else 0) + tail
+
+
+def _check_out(name, t, shape, dev):
+    if t.shape != shape or t.dtype is not _BF16 or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name} must be a contiguous bf16 tensor {tuple(shape)} on cuda:{dev}")
+    return t
+
+
+def qk_norm_rope(q, k=None, rope=None, positions=None, q_weight=None, k_weight=None, eps: float | None = None, out=None):
+    """RMS norm of each head of q, bf16 [B, S, Hq, 128], and k, bf16 [B, S, Hk,
+    128] (slices of a projection are taken as they are), with ``eps`` and the
+    weights bf16 [128] of each if given, then the rotation by ``rope`` at
+    ``positions``, int32 [B, S] ([B, S, axes] for several axes, [S] or [S, axes]
+    the same for all of the batch), in one pass (sage_qk_norm_rope).  Returns the
+    dense (q, k), or q alone without k.  ``out``: the pair (or the tensor) to fill,
+    which may be q and k themselves."""
+    lib = _lib or load_library()
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    dev = q.get_device()
+    shape, q_sb, q_ss = _check_rows("q", q, dev)
+    B, S, Hq, D = shape
+    Hk = k_sb = k_ss = 0
+    if k is not None:
+        k_shape, k_sb, k_ss = _check_rows("k", k, dev)
+        Hk = k_shape[2]
+        if k_shape[:2] != shape[:2]:
+            raise ValueError(f"q and k must have equal batches and lengths (got {tuple(q.shape)}, {tuple(k.shape)})")
+    turn = _check_turn(rope, positions, q_weight, k_weight, eps, B, S, dev)
+    if out is None:
+        q_out = torch.empty(shape, dtype=_BF16, device=q.device)
+        k_out = None if k is None else torch.empty(k_shape, dtype=_BF16, device=q.device)
+    else:
+        q_out, k_out = (out, None) if k is None else out
+        _check_out("out", q_out, shape, dev)
+        if k is not None:
+            _check_out("out", k_out, k_shape, dev)
+            if k_out.data_ptr() == q_out.data_ptr():
+                raise ValueError("out must be two tensors, one for q and one for k")
+    _call(lib.sage_qk_norm_rope, dev, q.data_ptr(), None if k is None else k.data_ptr(), q_sb, q_ss, k_sb, k_ss, B, S, Hq, Hk, D,
+          *turn, q_out.data_ptr(), None if k is None else k_out.data_ptr())
+    return q_out if k is None else (q_out, k_out)
+
+
+def kv_cache_append(q, k, v, cache, slots, rope=None, positions=None, q_weight=None, k_weight=None, eps: float | None = None,
+                    out=None):
+    """qk_norm_rope of q, bf16 [B, S, Hq, 128], and k, with k and v, bf16 [B, S, H,
+    128], quantised and put into ``cache`` (of 8 or 4 bits) in the same pass: token (b,
+    s) goes to ``slots``, int32 [B, S] (kv_pages_reserve makes them; a negative one is
+    not written).  Tokens may be packed as [1, T, ...] with slots and positions [T].
+    Returns the dense q (``out`` if given); q None: None (sage_kv_cache_append)."""
+    lib = _lib or load_library()
+    c, dev = _check_cache(cache)
+    shape, k_sb, k_ss = _check_rows("k", k, dev, c.H)
+    v_shape, v_sb, v_ss = _check_rows("v", v, dev, c.H)
+    if shape != v_shape:
+        raise ValueError(f"k and v must have equal shapes (got {tuple(k.shape)}, {tuple(v.shape)})")
+    B, S, _, D = shape
+    Hq = q_sb = q_ss = 0
+    if q is not None:
+        q_shape, q_sb, q_ss = _check_rows("q", q, dev)
+        Hq = q_shape[2]
+        if q_shape[:2] != shape[:2]:
+            raise ValueError(f"q and k must have equal batches and lengths (got {tuple(q.shape)}, {tuple(k.shape)})")
+        out = torch.empty(q_shape, dtype=_BF16, device=q.device) if out is None else _check_out("out", out, q_shape, dev)
+    elif out is not None or q_weight is not None:
+        raise ValueError("out and q_weight without q")
+    turn = _check_turn(rope, positions, q_weight, k_weight, eps, B, S, dev)
+    if slots.dtype is not _INT32 or slots.get_device() != dev or slots.numel() != B * S or not slots.is_contiguous():
+        raise ValueError(f"slots must be a contiguous int32 [{B}, {S}] tensor on cuda:{dev}")
+    _call(lib.sage_kv_cache_append if len(cache) == 4 else lib.sage_kv4_cache_append, dev, ctypes.byref(c),
+          None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), q_sb, q_ss, k_sb, k_ss, v_sb, v_ss, B, S, Hq, D,
+          *turn, slots.data_ptr(), None if q is None else out.data_ptr())
+    return out
+
+
+class PagePlan(NamedTuple):
+    """What kv_pages_reserve gives, int32 tensors: ``start``, ``taken``, ``lens`` and
+    ``first`` [B], ``free_count`` [1], ``slots`` and ``positions`` [tokens] (packed) or
+    [B, tokens]."""
+    start: torch.Tensor
+    taken: torch.Tensor
+    lens: torch.Tensor
+    first: torch.Tensor
+    free_count: torch.Tensor
+    slots: torch.Tensor
+    positions: torch.Tensor
+
+
+def _check_free(free_pages, free_count, lens, page_size):
+    """(num_pages, B, device) of a free list and lengths."""
+    dev = free_pages.get_device()
+    if not free_pages.is_cuda or free_pages.dim() != 1 or free_pages.shape[0] < 1:
+        raise ValueError("free_pages must be an int32 [num_pages] CUDA tensor")
+    _check_ints("free_pages", free_pages, free_pages.shape[0], dev)
+    _check_ints("free_count", free_count, 1, dev)
+    if page_size not in KV_PAGE_SIZES:
+        raise ValueError(f"page_size must be one of {KV_PAGE_SIZES} (got {page_size})")
+    if lens.dim() != 1 or lens.shape[0] < 1:
+        raise ValueError("lens must be an int32 [B] tensor")
+    _check_ints("lens", lens, lens.shape[0], dev)
+    return free_pages.shape[0], lens.shape[0], dev
+
+
+def kv_pages_reserve(free_pages, free_count, lens, counts, block_table, page_size: int, tokens: int, layout: str = "packed",
+                     out: PagePlan | None = None):
+    """Pages for counts[b] more tokens of each sequence of lens[b], off the stack
+    ``free_pages`` (int32 [num_pages], the first free_count[0] free): fills
+    ``block_table`` (int32 [B, pages]) and returns a PagePlan with the tokens' slots
+    and positions (sage_kv_pages_reserve).  ``layout``: "packed" tokens one behind
+    another, ``tokens`` in all, or [B, tokens] with a sequence's at the "front" or
+    the "end" of its row.  Sequences for which there are too few pages get none (taken
+    0), and sync_status reports SAGE_ERR_NO_PAGES.  ``out``: the PagePlan to fill, of
+    which lens and free_count may be the arguments."""
+    lib = _lib or load_library()
+    num_pages, B, dev = _check_free(free_pages, free_count, lens, page_size)
+    _check_ints("counts", counts, B, dev)
+    width, stride = _check_table(block_table, B, dev)
+    tokens = int(tokens)
+    if layout not in TOKEN_LAYOUTS:
+        raise ValueError(f"layout must be one of {TOKEN_LAYOUTS} (got {layout!r})")
+    if tokens < 1:
+        raise ValueError(f"tokens must be >= 1 (got {tokens})")
+    rows = (tokens,) if layout == "packed" else (B, tokens)
+    if out is None:
+        n = math.prod(rows)
+        flat = torch.empty(4 * B + 1 + 2 * n, dtype=_INT32, device=free_pages.device)
+        parts = flat.split([B, B, B, B, 1, n, n])
+        out = PagePlan(*parts[:5], parts[5].view(rows), parts[6].view(rows))
+    else:
+        for name, t, shape in zip(PagePlan._fields, out, ((B,),) * 4 + ((1,), rows, rows)):
+            if t.dtype is not _INT32 or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+                raise ValueError(f"out.{name} must be a contiguous int32 {shape} tensor on cuda:{dev}")
+    _call(lib.sage_kv_pages_reserve, dev, free_pages.data_ptr(), free_count.data_ptr(), num_pages, page_size, lens.data_ptr(),
+          counts.data_ptr(), B, block_table.data_ptr(), width, stride, TOKEN_LAYOUTS.index(layout), tokens,
+          *(t.data_ptr() for t in out))
+    return out
+
+
+def kv_pages_release(free_pages, free_count, lens, keep, block_table, page_size: int):
+    """Cut sequences to keep[b] tokens (0: all of a finished one), in place: their
+    pages behind that go back to the free list (sage_kv_pages_release)."""
+    lib = _lib or load_library()
+    num_pages, B, dev = _check_free(free_pages, free_count, lens, page_size)
+    _check_ints("keep", keep, B, dev)
+    width, stride = _check_table(block_table, B, dev)
+    _call(lib.sage_kv_pages_release, dev, free_pages.data_ptr(), free_count.data_ptr(), num_pages, page_size, lens.data_ptr(),
+          keep.data_ptr(), B, block_table.data_ptr(), width, stride)
