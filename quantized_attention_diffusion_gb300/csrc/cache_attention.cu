@@ -57,7 +57,6 @@ struct Tile {
   static constexpr uint32_t kOffKb = kOffVs + kTok * 4;             // 4 bits: block scales, eight a row
   static constexpr uint32_t kOffVb = kOffKb + kTok * 8;
   static constexpr uint32_t kBytes = kBits == 8 ? kOffKb : kOffVb + kTok * 8;
-  static constexpr uint32_t kRowBytes = 2 * kRow + 8 + (kBits == 8 ? 0 : 16);   // of a key
 };
 constexpr uint32_t kMergeBytes = kConsumers * 8 * kHeadDim * 4;
 constexpr int kClusterTiles = 16;                         // most tiles of an SM slot, in clusters
@@ -74,7 +73,7 @@ constexpr float kAbove = 8.0f;                            // a weights' referenc
 constexpr float kLeast = -160.0f;                         // of d: scales of V are 0 or 2^-149 at least
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -110,10 +109,16 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-// A tile's run of keys is copied in parts by as many lanes: K, V and their scales, in 4
-// bits their block scales too.
+// A tile's run of keys is copied in parts by as many lanes: K, V and, in 8 bits, their
+// scales.  A bulk copy costs an SM some 60 ns however small it is (65536 keys x 24 heads
+// in 4 bits, copies alone: six a tile 58 us, four 49, two 38), so that the scales of 4
+// bits, 1.5 of 9.5 KB, go by 16 bytes a lane instead (copy_scales).
 template <int kBits>
-constexpr int kPartBits = kBits == 8 ? 2 : 3;
+constexpr int kPartBits = kBits == 8 ? 2 : 1;
+template <int kBits>
+constexpr uint32_t kBulkBytes = Tile<kBits>::kRow * 2 + (kBits == 8 ? 8 : 0);   // of a key
+template <int kBits>
+constexpr uint32_t kFullCount = kBits == 8 ? 1 : 33;     // arrivals that make a tile full
 template <int kBits>
 __device__ __forceinline__ void copy_part(const CacheView& cache, int part, uint32_t st, uint32_t bar, int64_t row, int o, int run) {
   using T = Tile<kBits>;
@@ -123,12 +128,32 @@ __device__ __forceinline__ void copy_part(const CacheView& cache, int part, uint
     bulk_load(st + T::kOffV + o * T::kRow, cache.v_codes + row * T::kRow, run * T::kRow, bar);
   else if (part == 2)
     bulk_load(st + T::kOffKs + o * 4, cache.k_scale + row, run * 4, bar);
-  else if (part == 3)
+  else
     bulk_load(st + T::kOffVs + o * 4, cache.v_scale + row, run * 4, bar);
-  else if (kBits == 4 && part == 4)
-    bulk_load(st + T::kOffKb + o * 8, cache.k_block + row * 8, run * 8, bar);
-  else if (kBits == 4 && part == 5)
-    bulk_load(st + T::kOffVb + o * 8, cache.v_block + row * 8, run * 8, bar);
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// The block scales and scales of the 4-bit tile of keys first .. first + 63, those before
+// hi; every lane counts for `bar` when its copies have landed.  `page`: of run i of the
+// tile in lane 2i.  The whole warp together.
+__device__ __forceinline__ void copy_scales(const CacheView& cache, uint32_t st, uint32_t bar, int page, int h, int first, int hi) {
+  using T = Tile<4>;
+  const int lane = threadIdx.x & 31, ps = cache.page_shift, shift = min(6, ps), mask = (1 << ps) - 1;
+  const int two = 2 * lane, four = 4 * (lane & 15);          // the first of this lane's keys
+  const int p2 = __shfl_sync(0xFFFFFFFFu, page, (two >> shift) << 1);
+  const int p4 = __shfl_sync(0xFFFFFFFFu, page, (four >> shift) << 1);
+  if (first + two < hi) {
+    const int64_t row = ((static_cast<int64_t>(p2) * cache.H + h) << ps) + ((first + two) & mask);
+    copy16(st + T::kOffKb + two * 8, cache.k_block + row * 8);
+    copy16(st + T::kOffVb + two * 8, cache.v_block + row * 8);
+  }
+  if (first + four < hi) {
+    const int64_t row = ((static_cast<int64_t>(p4) * cache.H + h) << ps) + ((first + four) & mask);
+    copy16(st + (lane < 16 ? T::kOffKs : T::kOffVs) + four * 4, (lane < 16 ? cache.k_scale : cache.v_scale) + row);
+  }
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // What a warp holds of a unit's query rows.  Lane (r, c): queries 2c and 2c + 1 of
@@ -142,101 +167,209 @@ struct QueryRows {
   float m[NT][2], d[NT][2], l[NT][2];
 };
 
-// 16 keys, t0 .. t0 + 15, which stand at row `at` of the tile at st.  hi: keys
-// that some row sees; lo: keys that all see.
-template <int NT, int kBits>
-__device__ __forceinline__ void attend(QueryRows<NT>& z, const uint8_t* st, float c_scale, int t0, int at, int r, int c, int hi,
-                                       int lo) {
-  using T = Tile<kBits>;
-  // Row r of K's products is key r; in 4 bits keys 2 and 3 change places, and 6 and 7,
-  // so that the lanes of a load of V, 64 bytes a key, meet in fewer banks.
-  const int key = kBits == 8 ? r : r ^ ((r >> 1) & 1);
-  const int odd = kBits == 8 ? 0 : c & 1;
-  float sc[NT][4], lw[NT][4];
+// Row r of K's products is key keyrow(r) of 16: in 4 bits keys 2 and 3 change places, and
+// 6 and 7, so that the lanes of a load of V, 64 bytes a key, meet in fewer banks.
+template <int kBits>
+__device__ __forceinline__ int keyrow(int r) { return kBits == 8 ? r : r ^ ((r >> 1) & 1); }
+
+// Scores of 16 keys, whose rows begin at row `at` of the tile at st, before any
+// factor: sc[a][e] is key keyrow(r) + 8 (e / 2), query 2c + e % 2.
+template <int NT>
+__device__ __forceinline__ void scores8(const QueryRows<NT>& z, const uint8_t* st, int at, int r, int c, float (&sc)[NT][4]) {
 #pragma unroll
   for (int a = 0; a < NT; ++a)
 #pragma unroll
     for (int e = 0; e < 4; ++e) sc[a][e] = 0.0f;
-  if constexpr (kBits == 8) {
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const uint8_t* kp = st + (at + r) * kHeadDim + c * 32 + half * 16;
-      const uint4 k0 = *reinterpret_cast<const uint4*>(kp);
-      const uint4 k1 = *reinterpret_cast<const uint4*>(kp + 8 * kHeadDim);
+  for (int half = 0; half < 2; ++half) {
+    const uint8_t* kp = st + (at + r) * kHeadDim + c * 32 + half * 16;
+    const uint4 k0 = *reinterpret_cast<const uint4*>(kp);
+    const uint4 k1 = *reinterpret_cast<const uint4*>(kp + 8 * kHeadDim);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t ka[4];
-        k_codes_f16(reinterpret_cast<const uint32_t*>(&k0)[i], ka[0], ka[2]);
-        k_codes_f16(reinterpret_cast<const uint32_t*>(&k1)[i], ka[1], ka[3]);
+    for (int i = 0; i < 4; ++i) {
+      uint32_t ka[4];
+      k_codes_f16(reinterpret_cast<const uint32_t*>(&k0)[i], ka[0], ka[2]);
+      k_codes_f16(reinterpret_cast<const uint32_t*>(&k1)[i], ka[1], ka[3]);
 #pragma unroll
-        for (int a = 0; a < NT; ++a) mma_f16(sc[a], ka, z.q[a][half * 4 + i][0], z.q[a][half * 4 + i][1]);
-      }
-    }
-  } else {
-    // A lane's 32 channels of a key are 16 bytes and two blocks.
-    uint4 kw[2];
-    uint32_t sb[2][2];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      kw[n] = *reinterpret_cast<const uint4*>(st + (at + key + 8 * n) * T::kRow + c * 16);
-      uint32_t two;
-      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(two) : "h"(*reinterpret_cast<const uint16_t*>(st + T::kOffKb + (at + key + 8 * n) * 8 + 2 * c)));
-      sb[n][0] = __byte_perm(two, two, 0x1010);
-      sb[n][1] = __byte_perm(two, two, 0x3232);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {              // products 2i and 2i + 1
-      uint32_t h0[4], h1[4];
-      e2m1x8_f16(reinterpret_cast<const uint32_t*>(&kw[0])[i], h0);
-      e2m1x8_f16(reinterpret_cast<const uint32_t*>(&kw[1])[i], h1);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        h0[j] = mul_f16x2(h0[j], sb[0][i >> 1]);
-        h1[j] = mul_f16x2(h1[j], sb[1][i >> 1]);
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t ka[4] = {h0[2 * j], h1[2 * j], h0[2 * j + 1], h1[2 * j + 1]};
-#pragma unroll
-        for (int a = 0; a < NT; ++a) mma_f16(sc[a], ka, z.q[a][2 * i + j][0], z.q[a][2 * i + j][1]);
-      }
+      for (int a = 0; a < NT; ++a) mma_f16(sc[a], ka, z.q[a][half * 4 + i][0], z.q[a][half * 4 + i][1]);
     }
   }
-  // sc[a][e]: key `key` + 8 (e / 2), query 2c + e % 2
-  float ks[2], lv[2];                 // of both keys; K's times softmax_scale * log2 e
+}
+
+// The same from 4 bits: a lane's 32 channels of a key are 16 bytes and two blocks.  The
+// products of each block add up by themselves, two chains half as long.
+template <int NT>
+__device__ __forceinline__ void scores4(const QueryRows<NT>& z, const uint8_t* st, int at, int r, int c, float (&sc)[NT][4]) {
+  using T = Tile<4>;
+  float more[NT][4];
+#pragma unroll
+  for (int a = 0; a < NT; ++a)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sc[a][e] = more[a][e] = 0.0f;
+  uint4 kw[2];
+  uint32_t sb[2][2];
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
-    ks[n] = *reinterpret_cast<const float*>(st + T::kOffKs + (at + n * 8 + key) * 4) * c_scale;
-    lv[n] = lg2_approx(*reinterpret_cast<const float*>(st + T::kOffVs + (at + n * 8 + key) * 4));
+    const int key = at + keyrow<4>(r) + 8 * n;
+    kw[n] = *reinterpret_cast<const uint4*>(st + key * T::kRow + c * 16);
+    uint32_t two;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(two) : "h"(*reinterpret_cast<const uint16_t*>(st + T::kOffKb + key * 8 + 2 * c)));
+    sb[n][0] = __byte_perm(two, two, 0x1010);
+    sb[n][1] = __byte_perm(two, two, 0x3232);
+  }
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int i = (w >> 1) | (w & 1) << 1;         // words 0, 2, 1, 3: products 2i and 2i + 1
+    uint32_t h0[4], h1[4];
+    e2m1x8_f16(reinterpret_cast<const uint32_t*>(&kw[0])[i], h0);
+    e2m1x8_f16(reinterpret_cast<const uint32_t*>(&kw[1])[i], h1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      h0[j] = mul_f16x2(h0[j], sb[0][i >> 1]);
+      h1[j] = mul_f16x2(h1[j], sb[1][i >> 1]);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t ka[4] = {h0[2 * j], h1[2 * j], h0[2 * j + 1], h1[2 * j + 1]};
+#pragma unroll
+      for (int a = 0; a < NT; ++a) mma_f16(i < 2 ? sc[a] : more[a], ka, z.q[a][2 * i + j][0], z.q[a][2 * i + j][1]);
+    }
   }
 #pragma unroll
   for (int a = 0; a < NT; ++a)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      sc[a][e] = __fmul_rn(sc[a][e] * z.rk[a][e & 1], ks[e >> 1]);     // rk is a power of two: rounded once
-      lw[a][e] = lv[e >> 1] - z.d[a][e & 1];
+    for (int e = 0; e < 4; ++e) sc[a][e] += more[a][e];
+}
+
+// O^T += V^T P^T of 16 keys; some: some of them are keys that no row sees.
+template <int NT>
+__device__ __forceinline__ void values8(QueryRows<NT>& z, const uint8_t* st, int at, int t0, int hi, int r, int c,
+                                        const uint32_t (&pb)[NT][2]) {
+  uint4 vw[4];
+  const uint8_t* vp = st + Tile<8>::kOffV + (at + 2 * c) * kHeadDim + r * 16;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)         // keys 2c, 2c + 1, 2c + 8, 2c + 9
+    vw[k] = *reinterpret_cast<const uint4*>(vp + ((k >> 1) * 8 + (k & 1)) * kHeadDim);
+  if (t0 + 16 > hi) {                 // codes behind the last key may be anything, NaN too
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (t0 + 2 * c + (k >> 1) * 8 + (k & 1) >= hi) vw[k] = make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w0 = reinterpret_cast<const uint32_t*>(&vw[0])[i], w1 = reinterpret_cast<const uint32_t*>(&vw[1])[i];
+    const uint32_t w2 = reinterpret_cast<const uint32_t*>(&vw[2])[i], w3 = reinterpret_cast<const uint32_t*>(&vw[3])[i];
+    const uint32_t a01 = __byte_perm(w0, w1, 0x5140), b01 = __byte_perm(w0, w1, 0x7362);
+    const uint32_t a23 = __byte_perm(w2, w3, 0x5140), b23 = __byte_perm(w2, w3, 0x7362);
+    const uint32_t va[4] = {v_codes_f16_lo(a01), v_codes_f16_hi(a01), v_codes_f16_lo(a23), v_codes_f16_hi(a23)};
+    const uint32_t vb[4] = {v_codes_f16_lo(b01), v_codes_f16_hi(b01), v_codes_f16_lo(b23), v_codes_f16_hi(b23)};
+#pragma unroll
+    for (int a = 0; a < NT; ++a) {
+      mma_f16(z.o[a][2 * i], va, pb[a][0], pb[a][1]);
+      mma_f16(z.o[a][2 * i + 1], vb, pb[a][0], pb[a][1]);
     }
-  if (t0 + 16 > lo) {                 // some row does not see all of these keys
+  }
+}
+
+// The same from 4 bits: a lane's 16 channels of a key are eight bytes and one block.
+// Bytes of the codes of keys A and B, even channels in one word and odd ones in
+// another, are the pairs that the products take; so are the scales.
+template <int NT>
+__device__ __forceinline__ void values4(QueryRows<NT>& z, const uint8_t* st, int at, int t0, int hi, int r, int c,
+                                        const uint32_t (&pb)[NT][2]) {
+  using T = Tile<4>;
+  uint2 vw[4];
+  uint32_t sv[4];
+  const uint8_t* vp = st + T::kOffV + at * T::kRow + r * 8;
+  const uint8_t* vb = st + T::kOffVb + at * 8 + r;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {       // the keys of rows 2c, 2c + 1, 2c + 8, 2c + 9 of K's products
+    const int key = (k >> 1) * 8 + keyrow<4>(2 * c + (k & 1));
+    vw[k] = *reinterpret_cast<const uint2*>(vp + key * T::kRow);
+    sv[k] = vb[key * 8];
+  }
+  if (t0 + 16 > hi) {                 // scales behind the last key may be anything, NaN too; codes are finite
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (t0 + (k >> 1) * 8 + keyrow<4>(2 * c + (k & 1)) >= hi) sv[k] = 0u;
+  }
+  uint32_t s2[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2[k]) : "h"(static_cast<uint16_t>(sv[2 * k] | sv[2 * k + 1] << 8)));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t even[2][4], odds[2][4];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t w0 = i == 0 ? vw[2 * k].x : vw[2 * k].y, w1 = i == 0 ? vw[2 * k + 1].x : vw[2 * k + 1].y;
+      e2m1x8_f16((w0 & 0x0F0F0F0Fu) | ((w1 << 4) & 0xF0F0F0F0u), even[k]);
+      e2m1x8_f16(((w0 >> 4) & 0x0F0F0F0Fu) | (w1 & 0xF0F0F0F0u), odds[k]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t va[4] = {mul_f16x2(even[0][j], s2[0]), mul_f16x2(odds[0][j], s2[0]), mul_f16x2(even[1][j], s2[1]),
+                              mul_f16x2(odds[1][j], s2[1])};
+#pragma unroll
+      for (int a = 0; a < NT; ++a) mma_f16(z.o[a][4 * i + j], va, pb[a][0], pb[a][1]);
+    }
+  }
+}
+
+// kN times 16 keys together: keys t0[n] .. t0[n] + 15, which stand at row `at` of the
+// tile at st[n].  hi: keys that some row sees; lo: keys that all see.
+template <int NT, int kBits, int kN>
+__device__ __forceinline__ void attend(QueryRows<NT>& z, const uint8_t* const (&st)[kN], float c_scale, const int (&t0)[kN], int at,
+                                       int r, int c, int hi, int lo) {
+  using T = Tile<kBits>;
+  float sc[kN][NT][4], lw[kN][NT][4], lv[kN][2];
+  const int key = keyrow<kBits>(r);
+#pragma unroll
+  for (int n = 0; n < kN; ++n) {
+    if constexpr (kBits == 8)
+      scores8<NT>(z, st[n], at, r, c, sc[n]);
+    else
+      scores4<NT>(z, st[n], at, r, c, sc[n]);
+  }
+#pragma unroll
+  for (int n = 0; n < kN; ++n) {
+    float ks[2];                        // of keys `key` and key + 8; K's times softmax_scale * log2 e
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      ks[k] = *reinterpret_cast<const float*>(st[n] + T::kOffKs + (at + k * 8 + key) * 4) * c_scale;
+      lv[n][k] = lg2_approx(*reinterpret_cast<const float*>(st[n] + T::kOffVs + (at + k * 8 + key) * 4));
+    }
 #pragma unroll
     for (int a = 0; a < NT; ++a)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (t0 + key + 8 * (e >> 1) >= z.lim[a][e & 1]) {
-          sc[a][e] = -INFINITY;
-          lw[a][e] = 0.0f;            // the scale may be anything
-        }
+      for (int e = 0; e < 4; ++e) {
+        sc[n][a][e] = __fmul_rn(sc[n][a][e] * z.rk[a][e & 1], ks[e >> 1]);     // rk is a power of two: rounded once
+        lw[n][a][e] = lv[n][e >> 1] - z.d[a][e & 1];
+      }
+    if (t0[n] + 16 > lo) {              // some row does not see all of these keys
+#pragma unroll
+      for (int a = 0; a < NT; ++a)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (t0[n] + key + 8 * (e >> 1) >= z.lim[a][e & 1]) {
+            sc[n][a][e] = -INFINITY;
+            lw[n][a][e] = 0.0f;         // the scale may be anything
+          }
+    }
   }
   bool over = false;
-  float pl[NT][4], pw[NT][4];
+  float pl[kN][NT][4], pw[kN][NT][4];
 #pragma unroll
-  for (int a = 0; a < NT; ++a)
+  for (int n = 0; n < kN; ++n)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float t = sc[a][e] - z.m[a][e & 1];
-      pl[a][e] = ex2_approx(t);
-      pw[a][e] = ex2_approx(t + lw[a][e]);
-      over |= fmaxf(pl[a][e], pw[a][e]) > kFar;
-    }
+    for (int a = 0; a < NT; ++a)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float t = sc[n][a][e] - z.m[a][e & 1];
+        pl[n][a][e] = ex2_approx(t);
+        pw[n][a][e] = ex2_approx(t + lw[n][a][e]);
+        over |= fmaxf(pl[n][a][e], pw[n][a][e]) > kFar;
+      }
   // The references m and m + d need not be the maxima, only near them: they move
   // where a weight passes 2^15, which after the first keys is rare, and
   // otherwise no value crosses lanes.
@@ -246,8 +379,12 @@ __device__ __forceinline__ void attend(QueryRows<NT>& z, const uint8_t* st, floa
       float alpha[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float mx = fmaxf(z.m[a][e], fmaxf(sc[a][e], sc[a][e + 2]));
-        float wx = fmaxf((sc[a][e] - mx) + lv[0], (sc[a][e + 2] - mx) + lv[1]);   // a masked key's is -inf or NaN
+        float mx = z.m[a][e];
+#pragma unroll
+        for (int n = 0; n < kN; ++n) mx = fmaxf(mx, fmaxf(sc[n][a][e], sc[n][a][e + 2]));
+        float wx = -INFINITY;           // a masked key's is -inf or NaN
+#pragma unroll
+        for (int n = 0; n < kN; ++n) wx = fmaxf(wx, fmaxf((sc[n][a][e] - mx) + lv[n][0], (sc[n][a][e + 2] - mx) + lv[n][1]));
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1)
           larger(mx, wx, __shfl_xor_sync(0xFFFFFFFFu, mx, d), __shfl_xor_sync(0xFFFFFFFFu, wx, d));
@@ -262,11 +399,13 @@ __device__ __forceinline__ void attend(QueryRows<NT>& z, const uint8_t* st, floa
         z.m[a][e] = mx;
         z.d[a][e] = dn;
 #pragma unroll
-        for (int k = 0; k < 4; k += 2) {
-          const float t = sc[a][e + k] - mx;
-          pl[a][e + k] = ex2_approx(t);
-          pw[a][e + k] = t == -INFINITY ? 0.0f : ex2_approx(t + (lv[k >> 1] - dn));
-        }
+        for (int n = 0; n < kN; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; k += 2) {
+            const float t = sc[n][a][e + k] - mx;
+            pl[n][a][e + k] = ex2_approx(t);
+            pw[n][a][e + k] = t == -INFINITY ? 0.0f : ex2_approx(t + (lv[n][k >> 1] - dn));
+          }
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -274,80 +413,21 @@ __device__ __forceinline__ void attend(QueryRows<NT>& z, const uint8_t* st, floa
         for (int e = 0; e < 4; ++e) z.o[a][j][e] *= alpha[e & 1];
     }
   }
-  uint32_t pb[NT][2];
 #pragma unroll
-  for (int a = 0; a < NT; ++a) {
+  for (int n = 0; n < kN; ++n) {
+    uint32_t pb[NT][2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) z.l[a][e & 1] += pl[a][e];
-    // (key r, queries 2c, 2c + 1) -> (query r, keys 2c, 2c + 1)
-    pb[a][0] = transpose8(pack_f16(pw[a][0], pw[a][1]));
-    pb[a][1] = transpose8(pack_f16(pw[a][2], pw[a][3]));
-  }
-  if constexpr (kBits == 8) {
-    uint4 vw[4];
-    const uint8_t* vp = st + T::kOffV + (at + 2 * c) * kHeadDim + r * 16;
+    for (int a = 0; a < NT; ++a) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)         // keys 2c, 2c + 1, 2c + 8, 2c + 9
-      vw[k] = *reinterpret_cast<const uint4*>(vp + ((k >> 1) * 8 + (k & 1)) * kHeadDim);
-    if (t0 + 16 > hi) {                 // codes behind the last key may be anything, NaN too
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (t0 + 2 * c + (k >> 1) * 8 + (k & 1) >= hi) vw[k] = make_uint4(0u, 0u, 0u, 0u);
+      for (int e = 0; e < 4; ++e) z.l[a][e & 1] += pl[n][a][e];
+      // (key r, queries 2c, 2c + 1) -> (query r, keys 2c, 2c + 1)
+      pb[a][0] = transpose8(pack_f16(pw[n][a][0], pw[n][a][1]));
+      pb[a][1] = transpose8(pack_f16(pw[n][a][2], pw[n][a][3]));
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t w0 = reinterpret_cast<const uint32_t*>(&vw[0])[i], w1 = reinterpret_cast<const uint32_t*>(&vw[1])[i];
-      const uint32_t w2 = reinterpret_cast<const uint32_t*>(&vw[2])[i], w3 = reinterpret_cast<const uint32_t*>(&vw[3])[i];
-      const uint32_t a01 = __byte_perm(w0, w1, 0x5140), b01 = __byte_perm(w0, w1, 0x7362);
-      const uint32_t a23 = __byte_perm(w2, w3, 0x5140), b23 = __byte_perm(w2, w3, 0x7362);
-      const uint32_t va[4] = {v_codes_f16_lo(a01), v_codes_f16_hi(a01), v_codes_f16_lo(a23), v_codes_f16_hi(a23)};
-      const uint32_t vb[4] = {v_codes_f16_lo(b01), v_codes_f16_hi(b01), v_codes_f16_lo(b23), v_codes_f16_hi(b23)};
-#pragma unroll
-      for (int a = 0; a < NT; ++a) {
-        mma_f16(z.o[a][2 * i], va, pb[a][0], pb[a][1]);
-        mma_f16(z.o[a][2 * i + 1], vb, pb[a][0], pb[a][1]);
-      }
-    }
-  } else {
-    // A lane's 16 channels of a key are eight bytes and one block.  Bytes of the
-    // codes of keys A and B, even channels in one word and odd ones in another, are
-    // the pairs that the products take; so are the scales.
-    uint2 vw[4];
-    uint32_t sv[4];
-    const uint8_t* vp = st + T::kOffV + at * T::kRow + r * 8;
-    const uint8_t* vb = st + T::kOffVb + at * 8 + r;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {       // keys 2c, 2c + 1, 2c + 8, 2c + 9, as the rows of K's products have them
-      const int at_key = (k >> 1) * 8 + 2 * c + ((k & 1) ^ odd);
-      vw[k] = *reinterpret_cast<const uint2*>(vp + at_key * T::kRow);
-      sv[k] = vb[at_key * 8];
-    }
-    if (t0 + 16 > hi) {                 // scales behind the last key may be anything, NaN too; codes are finite
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (t0 + 2 * c + (k >> 1) * 8 + ((k & 1) ^ odd) >= hi) sv[k] = 0u;
-    }
-    uint32_t s2[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2[k]) : "h"(static_cast<uint16_t>(sv[2 * k] | sv[2 * k + 1] << 8)));
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint32_t even[2][4], odds[2][4];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint32_t w0 = i == 0 ? vw[2 * k].x : vw[2 * k].y, w1 = i == 0 ? vw[2 * k + 1].x : vw[2 * k + 1].y;
-        e2m1x8_f16((w0 & 0x0F0F0F0Fu) | ((w1 << 4) & 0xF0F0F0F0u), even[k]);
-        e2m1x8_f16(((w0 >> 4) & 0x0F0F0F0Fu) | (w1 & 0xF0F0F0F0u), odds[k]);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t va[4] = {mul_f16x2(even[0][j], s2[0]), mul_f16x2(odds[0][j], s2[0]), mul_f16x2(even[1][j], s2[1]),
-                                mul_f16x2(odds[1][j], s2[1])};
-#pragma unroll
-        for (int a = 0; a < NT; ++a) mma_f16(z.o[a][4 * i + j], va, pb[a][0], pb[a][1]);
-      }
-    }
+    if constexpr (kBits == 8)
+      values8<NT>(z, st[n], at, t0[n], hi, r, c, pb);
+    else
+      values4<NT>(z, st[n], at, t0[n], hi, r, c, pb);
   }
 }
 
@@ -477,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
   walk.plan(s_len, s_off);
   if (threadIdx.x == 32) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], kFullCount<kBits>);
       mbar_init(&empty[s], kConsumers);
     }
     mbar_init(&q_full, 1);
@@ -497,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
     if (warp == kConsumers) {
       // ------------------------------------------------------------ copies --
       // A tile is 1, 2 or 4 runs of keys that lie together in a page; lane
-      // 4i + k (in 4 bits 8i + k) copies part k of run i.  Every lane holds a
+      // 4i + k (in 4 bits 2i + k) copies part k of run i.  Every lane holds a
       // page number of the unit's table, reloaded for the next 32 pages.
       const int ps = p.cache.page_shift;
       const int run = min(kTok, 1 << ps), runs = kTok / run;
@@ -547,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
             break;
           }
           const int n_live = (min(kTok, hi - t * kTok) + run - 1) / run;   // <= 0 for a unit without keys
-          if (lane == 0) mbar_arrive_expect_tx(&full[s], max(0, n_live) * run * Tile<kBits>::kRowBytes);
+          if (lane == 0) mbar_arrive_expect_tx(&full[s], max(0, n_live) * run * kBulkBytes<kBits>);
           __syncwarp();
           if (live) {
             const int64_t r = ((static_cast<int64_t>(page) * p.cache.H + x.h) << ps) + (t0 & ((1 << ps) - 1));
@@ -555,6 +635,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
             const int o = my_run * run;
             copy_part<kBits>(p.cache, part, st, bar, r, o, run);
           }
+          if constexpr (kBits == 4) copy_scales(p.cache, smem0 + s * kStageBytes, smem_addr(&full[s]), page, x.h, t * kTok, hi);
         }
         x = after;
       }
@@ -603,11 +684,28 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
         if (lane == 0) mbar_arrive(&q_empty);
         lo = __reduce_min_sync(0xFFFFFFFFu, lo);
 
-        for (int t = x.t0; t < x.t1; ++t, ++it) {
+        int t = x.t0;
+        if constexpr (kBits == 4 && NT == 1) {
+          // Two tiles at a time: twice as much to do between one dependence and the next.
+          for (; t + 1 < x.t1; t += 2, it += 2) {
+            const int s0 = it % kStages, s1 = (it + 1) % kStages;
+            ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&full[s0], (it / kStages) & 1, abort_v, p.err, p.timeout_ns));
+            ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&full[s1], ((it + 1) / kStages) & 1, abort_v, p.err, p.timeout_ns));
+            const int t0 = t * kTok + warp * 16;
+            if (ok && t0 < hi)
+              attend<NT, kBits, 2>(z, {smem + s0 * kStageBytes, smem + s1 * kStageBytes}, p.c_scale, {t0, t0 + kTok}, warp * 16, r, c, hi, lo);
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&empty[s0]);
+              mbar_arrive(&empty[s1]);
+            }
+          }
+        }
+        for (; t < x.t1; ++t, ++it) {
           const int s = it % kStages;
           ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&full[s], (it / kStages) & 1, abort_v, p.err, p.timeout_ns));
           const int t0 = t * kTok + warp * 16;      // this warp's first key
-          if (ok && t0 < hi) attend<NT, kBits>(z, smem + s * kStageBytes, p.c_scale, t0, warp * 16, r, c, hi, lo);
+          if (ok && t0 < hi) attend<NT, kBits, 1>(z, {smem + s * kStageBytes}, p.c_scale, {t0}, warp * 16, r, c, hi, lo);
           __syncwarp();
           if (lane == 0) mbar_arrive(&empty[s]);
         }
@@ -752,7 +850,7 @@ __global__ void __cluster_dims__(ctas, 1, 1) __launch_bounds__(kThreads, ctas_pe
   const int len_raw = __ldg(p.lens + b);
   if (threadIdx.x == 32) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], kFullCount<kBits>);
       mbar_init(&empty[s], kConsumers);
     }
     mbar_init(&q_full, 1);
@@ -802,7 +900,7 @@ __global__ void __cluster_dims__(ctas, 1, 1) __launch_bounds__(kThreads, ctas_pe
       const int s = it % kStages, round = it / kStages;
       if (round > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[s], (round - 1) & 1, abort_v, p.err, p.timeout_ns))) break;
       const int n_live = (min(kTok, hi - first) + run - 1) / run;
-      if (lane == 0) mbar_arrive_expect_tx(&full[s], n_live * run * Tile<kBits>::kRowBytes);
+      if (lane == 0) mbar_arrive_expect_tx(&full[s], n_live * run * kBulkBytes<kBits>);
       __syncwarp();
       if (live) {
         const int64_t r = ((static_cast<int64_t>(page) * p.cache.H + h) << ps) + (t0 & ((1 << ps) - 1));
@@ -810,6 +908,7 @@ __global__ void __cluster_dims__(ctas, 1, 1) __launch_bounds__(kThreads, ctas_pe
         const int o = my_run * run;
         copy_part<kBits>(p.cache, part, st, bar, r, o, run);
       }
+      if constexpr (kBits == 4) copy_scales(p.cache, smem0 + s * kStageBytes, smem_addr(&full[s]), page, h, first, hi);
     }
     if (bad) atomicExch(p.err, SAGE_DEVERR_BAD_PAGE);
     if (*abort_v) {   // let the copies in flight land before the CTA can exit
@@ -852,7 +951,7 @@ __global__ void __cluster_dims__(ctas, 1, 1) __launch_bounds__(kThreads, ctas_pe
       const int s = it % kStages;
       ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&full[s], (it / kStages) & 1, abort_v, p.err, p.timeout_ns));
       const int t0 = (pre ? t : t - np) * kTok + warp * 16;
-      if (ok && t0 < hi) attend<1, kBits>(z, smem + s * kStageBytes, p.c_scale, t0, warp * 16, r, c, hi, lo);
+      if (ok && t0 < hi) attend<1, kBits, 1>(z, {smem + s * kStageBytes}, p.c_scale, {t0}, warp * 16, r, c, hi, lo);
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
     }
