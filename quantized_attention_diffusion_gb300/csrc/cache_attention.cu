@@ -43,13 +43,17 @@ using namespace cache;
 
 namespace {
 
-constexpr int kTok = 64;                                  // keys per tile
-constexpr int kCost = 2;                                  // of a unit, in tiles (1, 4 and 6: the same within 1%)
-constexpr int kConsumers = 4;                             // warps that compute, 16 keys of a tile each
+// Keys per tile.  In 4 bits a warp's work on 16 of them is done twice before the next
+// wait (65536 keys x 24 heads: TIME64 us with 64, TIME128 with 128).
+__host__ __device__ constexpr int tok_of(int bits) { return bits == 8 ? 64 : 128; }
+// Of a unit, in tiles (of 64 keys, 1, 4 and 6: the same within 1%).
+__host__ __device__ constexpr int cost_of(int bits) { return bits == 8 ? 2 : 1; }
+constexpr int kConsumers = 4;                             // warps that compute, a quarter of a tile's keys each
 constexpr int kThreads = (kConsumers + 1) * 32;           // and one that copies
 // A tile as it stands in shared memory, of a cache of kBits.
 template <int kBits>
 struct Tile {
+  static constexpr int kTok = tok_of(kBits);
   static constexpr uint32_t kRow = kHeadDim * kBits / 8;            // bytes of a row's codes
   static constexpr uint32_t kOffV = kTok * kRow;
   static constexpr uint32_t kOffKs = 2 * kTok * kRow;
@@ -59,13 +63,13 @@ struct Tile {
   static constexpr uint32_t kBytes = kBits == 8 ? kOffKb : kOffVb + kTok * 8;
 };
 constexpr uint32_t kMergeBytes = kConsumers * 8 * kHeadDim * 4;
-constexpr int kClusterTiles = 16;                         // most tiles of an SM slot, in clusters
+constexpr int kClusterKeys = 1024;                        // most keys of an SM slot, in clusters
 constexpr int kMaxCtas = 3 * kSms;                        // CTAs of a launch: three on each SM
 // As many as the registers of NT times 8 query rows allow without spilling much
 // (65536 keys x 24 heads, one row: three 74 us, two 79).
 __host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
-// Tiles in flight: 9 or 8 on an SM, 135 KB or more; in 4 bits 15 or 16.
-__host__ __device__ constexpr int stages_of(int nt, int bits) { return bits == 8 ? (nt == 1 ? 3 : 4) : (nt == 1 ? 5 : 8); }
+// Tiles in flight: 9 or 8 on an SM, 135 KB or more; in 4 bits 6 or 8, 114 KB or more.
+__host__ __device__ constexpr int stages_of(int nt, int bits) { return bits == 8 ? (nt == 1 ? 3 : 4) : (nt == 1 ? 2 : 4); }
 template <int kBits>
 constexpr uint32_t smem_of(int nt) { return stages_of(nt, kBits) * Tile<kBits>::kBytes + kMergeBytes + 8 * nt * kHeadDim * 2; }
 constexpr float kFar = 32768.0f, kFarLog2 = 15.0f;        // most of a weight (fp16: 65504)
@@ -135,23 +139,30 @@ __device__ __forceinline__ void copy_part(const CacheView& cache, int part, uint
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-// The block scales and scales of the 4-bit tile of keys first .. first + 63, those before
+// The block scales and scales of the 4-bit tile of keys first .. first + 127, those before
 // hi; every lane counts for `bar` when its copies have landed.  `page`: of run i of the
 // tile in lane 2i.  The whole warp together.
 __device__ __forceinline__ void copy_scales(const CacheView& cache, uint32_t st, uint32_t bar, int page, int h, int first, int hi) {
   using T = Tile<4>;
-  const int lane = threadIdx.x & 31, ps = cache.page_shift, shift = min(6, ps), mask = (1 << ps) - 1;
-  const int two = 2 * lane, four = 4 * (lane & 15);          // the first of this lane's keys
-  const int p2 = __shfl_sync(0xFFFFFFFFu, page, (two >> shift) << 1);
-  const int p4 = __shfl_sync(0xFFFFFFFFu, page, (four >> shift) << 1);
-  if (first + two < hi) {
-    const int64_t row = ((static_cast<int64_t>(p2) * cache.H + h) << ps) + ((first + two) & mask);
-    copy16(st + T::kOffKb + two * 8, cache.k_block + row * 8);
-    copy16(st + T::kOffVb + two * 8, cache.v_block + row * 8);
+  const int lane = threadIdx.x & 31, ps = cache.page_shift, shift = min(7, ps), mask = (1 << ps) - 1;
+  auto row_of = [&](int key) {
+    const int pg = __shfl_sync(0xFFFFFFFFu, page, (key >> shift) << 1);
+    return ((static_cast<int64_t>(pg) * cache.H + h) << ps) + ((first + key) & mask);
+  };
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {              // two keys a lane
+    const int key = 64 * i + 2 * lane;
+    const int64_t row = row_of(key);
+    if (first + key < hi) {
+      copy16(st + T::kOffKb + key * 8, cache.k_block + row * 8);
+      copy16(st + T::kOffVb + key * 8, cache.v_block + row * 8);
+    }
   }
-  if (first + four < hi) {
-    const int64_t row = ((static_cast<int64_t>(p4) * cache.H + h) << ps) + ((first + four) & mask);
-    copy16(st + (lane < 16 ? T::kOffKs : T::kOffVs) + four * 4, (lane < 16 ? cache.k_scale : cache.v_scale) + row);
+  const int key = 4 * lane;                  // four
+  const int64_t row = row_of(key);
+  if (first + key < hi) {
+    copy16(st + T::kOffKs + key * 4, cache.k_scale + row);
+    copy16(st + T::kOffVs + key * 4, cache.v_scale + row);
   }
   asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
 }
@@ -316,28 +327,28 @@ __device__ __forceinline__ void values4(QueryRows<NT>& z, const uint8_t* st, int
   }
 }
 
-// kN times 16 keys together: keys t0[n] .. t0[n] + 15, which stand at row `at` of the
-// tile at st[n].  hi: keys that some row sees; lo: keys that all see.
+// 16 kN keys, t0 and on, which stand at row `at` and on of the tile at st.  hi: keys
+// that some row sees; lo: keys that all see.
 template <int NT, int kBits, int kN>
-__device__ __forceinline__ void attend(QueryRows<NT>& z, const uint8_t* const (&st)[kN], float c_scale, const int (&t0)[kN], int at,
-                                       int r, int c, int hi, int lo) {
+__device__ __forceinline__ void attend(QueryRows<NT>& z, const uint8_t* st, float c_scale, int t0, int at, int r, int c, int hi,
+                                       int lo) {
   using T = Tile<kBits>;
   float sc[kN][NT][4], lw[kN][NT][4], lv[kN][2];
   const int key = keyrow<kBits>(r);
 #pragma unroll
   for (int n = 0; n < kN; ++n) {
     if constexpr (kBits == 8)
-      scores8<NT>(z, st[n], at, r, c, sc[n]);
+      scores8<NT>(z, st, at + 16 * n, r, c, sc[n]);
     else
-      scores4<NT>(z, st[n], at, r, c, sc[n]);
+      scores4<NT>(z, st, at + 16 * n, r, c, sc[n]);
   }
 #pragma unroll
   for (int n = 0; n < kN; ++n) {
     float ks[2];                        // of keys `key` and key + 8; K's times softmax_scale * log2 e
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      ks[k] = *reinterpret_cast<const float*>(st[n] + T::kOffKs + (at + k * 8 + key) * 4) * c_scale;
-      lv[n][k] = lg2_approx(*reinterpret_cast<const float*>(st[n] + T::kOffVs + (at + k * 8 + key) * 4));
+      ks[k] = *reinterpret_cast<const float*>(st + T::kOffKs + (at + 16 * n + k * 8 + key) * 4) * c_scale;
+      lv[n][k] = lg2_approx(*reinterpret_cast<const float*>(st + T::kOffVs + (at + 16 * n + k * 8 + key) * 4));
     }
 #pragma unroll
     for (int a = 0; a < NT; ++a)
@@ -346,12 +357,12 @@ __device__ __forceinline__ void attend(QueryRows<NT>& z, const uint8_t* const (&
         sc[n][a][e] = __fmul_rn(sc[n][a][e] * z.rk[a][e & 1], ks[e >> 1]);     // rk is a power of two: rounded once
         lw[n][a][e] = lv[n][e >> 1] - z.d[a][e & 1];
       }
-    if (t0[n] + 16 > lo) {              // some row does not see all of these keys
+    if (t0 + 16 * n + 16 > lo) {              // some row does not see all of these keys
 #pragma unroll
       for (int a = 0; a < NT; ++a)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (t0[n] + key + 8 * (e >> 1) >= z.lim[a][e & 1]) {
+          if (t0 + 16 * n + key + 8 * (e >> 1) >= z.lim[a][e & 1]) {
             sc[n][a][e] = -INFINITY;
             lw[n][a][e] = 0.0f;         // the scale may be anything
           }
@@ -425,10 +436,20 @@ __device__ __forceinline__ void attend(QueryRows<NT>& z, const uint8_t* const (&
       pb[a][1] = transpose8(pack_f16(pw[n][a][2], pw[n][a][3]));
     }
     if constexpr (kBits == 8)
-      values8<NT>(z, st[n], at, t0[n], hi, r, c, pb);
+      values8<NT>(z, st, at + 16 * n, t0 + 16 * n, hi, r, c, pb);
     else
-      values4<NT>(z, st[n], at, t0[n], hi, r, c, pb);
+      values4<NT>(z, st, at + 16 * n, t0 + 16 * n, hi, r, c, pb);
   }
+}
+
+// A warp's quarter of a tile.  With 16 rows its registers do for 16 keys at a time.
+template <int NT, int kBits>
+__device__ __forceinline__ void attend_quarter(QueryRows<NT>& z, const uint8_t* st, float c_scale, int t0, int at, int r, int c,
+                                               int hi, int lo) {
+  constexpr int kN = tok_of(kBits) / (16 * kConsumers), kStep = NT == 1 ? kN : 1;
+#pragma unroll
+  for (int n = 0; n < kN; n += kStep)
+    if (t0 + 16 * n < hi) attend<NT, kBits, kStep>(z, st, c_scale, t0 + 16 * n, at + 16 * n, r, c, hi, lo);
 }
 
 // The unit's query rows (bf16 in shared memory) as a warp holds them, nothing attended
@@ -540,6 +561,7 @@ template <int NT, bool kPrefix, int kBits>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(const Params p) {
   constexpr int R = 8 * NT, kStages = stages_of(NT, kBits);
   constexpr uint32_t kStageBytes = Tile<kBits>::kBytes;
+  constexpr int kTok = tok_of(kBits), kCost = cost_of(kBits);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kStages], empty[kStages], q_full, q_empty;
   __shared__ int abort_flag;
@@ -684,28 +706,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) cache_attn_kernel(c
         if (lane == 0) mbar_arrive(&q_empty);
         lo = __reduce_min_sync(0xFFFFFFFFu, lo);
 
-        int t = x.t0;
-        if constexpr (kBits == 4 && NT == 1) {
-          // Two tiles at a time: twice as much to do between one dependence and the next.
-          for (; t + 1 < x.t1; t += 2, it += 2) {
-            const int s0 = it % kStages, s1 = (it + 1) % kStages;
-            ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&full[s0], (it / kStages) & 1, abort_v, p.err, p.timeout_ns));
-            ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&full[s1], ((it + 1) / kStages) & 1, abort_v, p.err, p.timeout_ns));
-            const int t0 = t * kTok + warp * 16;
-            if (ok && t0 < hi)
-              attend<NT, kBits, 2>(z, {smem + s0 * kStageBytes, smem + s1 * kStageBytes}, p.c_scale, {t0, t0 + kTok}, warp * 16, r, c, hi, lo);
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&empty[s0]);
-              mbar_arrive(&empty[s1]);
-            }
-          }
-        }
-        for (; t < x.t1; ++t, ++it) {
+        for (int t = x.t0; t < x.t1; ++t, ++it) {
           const int s = it % kStages;
           ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&full[s], (it / kStages) & 1, abort_v, p.err, p.timeout_ns));
-          const int t0 = t * kTok + warp * 16;      // this warp's first key
-          if (ok && t0 < hi) attend<NT, kBits, 1>(z, {smem + s * kStageBytes}, p.c_scale, {t0}, warp * 16, r, c, hi, lo);
+          const int at = warp * (kTok / kConsumers);   // this warp's first key
+          if (ok) attend_quarter<NT, kBits>(z, smem + s * kStageBytes, p.c_scale, t * kTok + at, at, r, c, hi, lo);
           __syncwarp();
           if (lane == 0) mbar_arrive(&empty[s]);
         }
@@ -832,7 +837,7 @@ template <int ctas, Before kBefore, int kBits>
 __global__ void __cluster_dims__(ctas, 1, 1) __launch_bounds__(kThreads, ctas_per_sm(1))
     cache_attn_cluster_kernel(const Params p, const int32_t* prefix_pages, const PrefixParts parts) {
   constexpr bool kPrefix = kBefore == kPrefixTiles;
-  constexpr int R = 8, kStages = stages_of(1, kBits);
+  constexpr int R = 8, kStages = stages_of(1, kBits), kTok = tok_of(kBits);
   constexpr uint32_t kStageBytes = Tile<kBits>::kBytes;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kStages], empty[kStages], q_full;
@@ -950,8 +955,8 @@ __global__ void __cluster_dims__(ctas, 1, 1) __launch_bounds__(kThreads, ctas_pe
       }
       const int s = it % kStages;
       ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&full[s], (it / kStages) & 1, abort_v, p.err, p.timeout_ns));
-      const int t0 = (pre ? t : t - np) * kTok + warp * 16;
-      if (ok && t0 < hi) attend<1, kBits, 1>(z, {smem + s * kStageBytes}, p.c_scale, {t0}, warp * 16, r, c, hi, lo);
+      const int at = warp * (kTok / kConsumers);
+      if (ok) attend_quarter<1, kBits>(z, smem + s * kStageBytes, p.c_scale, (pre ? t : t - np) * kTok + at, at, r, c, hi, lo);
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
     }
@@ -1158,8 +1163,8 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 // 24 rows in the wide kernel 424, as three tiles of eight 482.
 int rows_per_tile(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : kWideRows; }
 int max_ctas(int R) { return kSms * (R == kWideRows ? 1 : ctas_per_sm(R / 8)); }
-int keys_per_tile(int R) { return R == kWideRows ? kWideTok : kTok; }
-int unit_cost(int R) { return R == kWideRows ? kWideCost : kCost; }
+int keys_per_tile(int R, int bits) { return R == kWideRows ? kWideTok : tok_of(bits); }
+int unit_cost(int R, int bits) { return R == kWideRows ? kWideCost : cost_of(bits); }
 
 // One launch's part of the workspace.
 struct Layout {
@@ -1237,13 +1242,14 @@ int cluster_ctas(const CacheAttnArgs& a, int prefix_len) {
   const int64_t rows = static_cast<int64_t>(a.Sq) * (a.Hq / a.cache.H);
   const int64_t units = a.B * ((rows + 7) / 8) * a.cache.H;   // of eight rows
   const int64_t room = std::min<int64_t>(kMaxCacheLen, static_cast<int64_t>(a.table.width) << a.cache.page_shift);
-  const int64_t tiles = (room + kTok - 1) / kTok + (prefix_len + kTok - 1) / kTok;
+  const int tok = tok_of(a.cache.bits), most_tiles = kClusterKeys / tok;
+  const int64_t tiles = (room + tok - 1) / tok + (prefix_len + tok - 1) / tok;
   const int most = max_ctas(8);
   int ctas = 8;
   while (ctas > 1 && (units * ctas > most || tiles <= ctas / 2)) ctas /= 2;
   const int64_t waves = (units * ctas + most - 1) / most;
-  if (waves > (rows <= 32 ? kClusterTiles : 2)) return 0;
-  return waves * ((tiles + ctas - 1) / ctas) <= kClusterTiles ? ctas : 0;
+  if (waves > (rows <= 32 ? most_tiles : 2)) return 0;
+  return waves * ((tiles + ctas - 1) / ctas) <= most_tiles ? ctas : 0;
 }
 
 // The same for the sequences' own keys behind a prefix that has a launch of its own,
@@ -1327,7 +1333,7 @@ size_t cache_attn_workspace_bytes(int B, int Sq, int Hq, int Hkv, int prefix_len
 bool cache_attn_fits(int B, int Sq, int Hq, int Hkv, int page_size, int table_width, int prefix_len) {
   const auto fits = [](int64_t keys, int64_t rows, int64_t seqs, int64_t H) {
     const int R = rows_per_tile(static_cast<int>(rows));
-    const int64_t tiles = (keys + keys_per_tile(R) - 1) / keys_per_tile(R) + unit_cost(R);   // of a unit, at most 2^25
+    const int64_t tiles = (keys + keys_per_tile(R, 8) - 1) / keys_per_tile(R, 8) + unit_cost(R, 8);   // of a unit, at most 2^25; fewer in 4 bits
     const int64_t units = seqs * ((rows + R - 1) / R) * H;                                   // at most 2^31
     return tiles * units / max_ctas(R) < INT_MAX;
   };
@@ -1340,7 +1346,7 @@ bool cache_attn_needs_workspace(const CacheAttnArgs& a) { return cluster_ctas(a,
 
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream) {
   if (const int ctas = cluster_ctas(a, a.prefix_len); ctas > 0) return launch_clusters(a, ctas, nullptr, stream);
-  const int H = a.cache.H, G = a.Hq / H;
+  const int H = a.cache.H, G = a.Hq / H, bits = a.cache.bits;
   const bool both = a.prefix_len > 0;
   const int join_ctas = both ? joining_ctas(a) : 0;
   for (int b0 = 0; b0 < a.B; b0 += kMaxBatch) {
@@ -1375,7 +1381,7 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream) 
     p.err = a.err;
     p.room = static_cast<int>(std::min<int64_t>(kMaxCacheLen, static_cast<int64_t>(a.table.width) << a.cache.page_shift));
     // The lengths are on the device: as many CTAs as the table has room for.
-    const unsigned ctas = ctas_for(std::min<long long>(kMaxCtas, (static_cast<long long>(p.room) + keys_per_tile(w.R) - 1) / keys_per_tile(w.R) + unit_cost(w.R)) * w.units, w.R);
+    const unsigned ctas = ctas_for(std::min<long long>(kMaxCtas, (static_cast<long long>(p.room) + keys_per_tile(w.R, bits) - 1) / keys_per_tile(w.R, bits) + unit_cost(w.R, bits)) * w.units, w.R);
     cudaError_t e = join_ctas > 0 ? cudaSuccess : launch_part(p, w.R, false, false, ctas, stream);
     if (e != cudaSuccess) return e;
 
@@ -1410,8 +1416,8 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream) 
       p.part_ml = at<float4>(a.workspace, u.ml);
       p.desc = at<int4>(a.workspace, u.desc);
       p.info = at<int2>(a.workspace, u.info);
-      const int n = (a.prefix_len + keys_per_tile(u.R) - 1) / keys_per_tile(u.R);
-      const long long steps = static_cast<long long>(n + unit_cost(u.R)) * u.units;
+      const int n = (a.prefix_len + keys_per_tile(u.R, bits) - 1) / keys_per_tile(u.R, bits);
+      const long long steps = static_cast<long long>(n + unit_cost(u.R, bits)) * u.units;
       const unsigned pc = ctas_for(steps, u.R);
       e = launch_part(p, u.R, true, join_ctas == 0, pc, stream);
       if (e != cudaSuccess) return e;
@@ -1420,7 +1426,7 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream) 
       mp.pre.R = u.R;
       mp.pre.slot_rows = u.slot_rows;
       mp.pre.n = n;
-      mp.pre.cost = unit_cost(u.R);
+      mp.pre.cost = unit_cost(u.R, bits);
       mp.pre.per = (steps + pc - 1) / pc;
       mp.pre.ctas = pc;
       if (join_ctas > 0) return launch_clusters(a, join_ctas, &mp.pre, stream);
