@@ -147,19 +147,19 @@ __device__ __forceinline__ void copy_scales(const CacheView& cache, uint32_t st,
   const int lane = threadIdx.x & 31, ps = cache.page_shift, shift = min(7, ps), mask = (1 << ps) - 1;
   auto row_of = [&](int key) {
     const int pg = __shfl_sync(0xFFFFFFFFu, page, (key >> shift) << 1);
-    return ((static_cast<int64_t>(pg) * cache.H + h) << ps) + ((first + key) & mask);
+    return static_cast<uint32_t>(((pg * cache.H + h) << ps) + ((first + key) & mask));    // below 2^31, as all rows are
   };
 #pragma unroll
   for (int i = 0; i < 2; ++i) {              // two keys a lane
     const int key = 64 * i + 2 * lane;
-    const int64_t row = row_of(key);
+    const uint64_t row = row_of(key);
     if (first + key < hi) {
       copy16(st + T::kOffKb + key * 8, cache.k_block + row * 8);
       copy16(st + T::kOffVb + key * 8, cache.v_block + row * 8);
     }
   }
   const int key = 4 * lane;                  // four
-  const int64_t row = row_of(key);
+  const uint64_t row = row_of(key);
   if (first + key < hi) {
     copy16(st + T::kOffKs + key * 4, cache.k_scale + row);
     copy16(st + T::kOffVs + key * 4, cache.v_scale + row);

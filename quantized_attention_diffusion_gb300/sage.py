@@ -585,24 +585,29 @@ def kv_cache_alloc(num_pages: int, H: int, page_size: int = 64, device=None, bit
 # little as they need: device numbers instead of devices, and no context manager
 # where the device is the current one.
 
-_INT8, _FP32, _BF16, _INT32 = torch.int8, torch.float32, torch.bfloat16, torch.int32
+_INT8, _UINT8, _FP32, _BF16, _INT32 = torch.int8, torch.uint8, torch.float32, torch.bfloat16, torch.int32
 _FP8 = (torch.float8_e4m3fn, torch.uint8)
 
 
 def _check_kv4_cache(cache):
     """The tuple of a 4-bit cache as a sage_kv4_cache, and its device number."""
     kc, kb, ks, vc, vb, vs = cache
-    for name, t, want in (("k_codes", kc, (torch.uint8,)), ("k_block", kb, _FP8), ("k_scale", ks, (_FP32,)),
-                          ("v_codes", vc, (torch.uint8,)), ("v_block", vb, _FP8), ("v_scale", vs, (_FP32,))):
-        if t.dtype not in want:
-            raise ValueError(f"{name} must be {want[0]} (got {t.dtype})")
+    if kc.dtype is not _UINT8 or vc.dtype is not _UINT8 or kb.dtype not in _FP8 or vb.dtype not in _FP8 \
+            or ks.dtype is not _FP32 or vs.dtype is not _FP32:
+        for name, t, want in (("k_codes", kc, (_UINT8,)), ("k_block", kb, _FP8), ("k_scale", ks, (_FP32,)),
+                              ("v_codes", vc, (_UINT8,)), ("v_block", vb, _FP8), ("v_scale", vs, (_FP32,))):
+            if t.dtype not in want:
+                raise ValueError(f"{name} must be {want[0]} (got {t.dtype})")
     dev = kc.get_device()
-    scales = ks.shape
-    if not kc.is_cuda or any(t.get_device() != dev for t in cache):
+    if dev < 0 or kb.get_device() != dev or ks.get_device() != dev or vc.get_device() != dev or vb.get_device() != dev \
+            or vs.get_device() != dev or not kc.is_cuda:
         raise ValueError("the cache must be CUDA tensors on one device")
-    if not all(t.is_contiguous() for t in cache):
+    if not (kc.is_contiguous() and kb.is_contiguous() and ks.is_contiguous() and vc.is_contiguous() and vb.is_contiguous()
+            and vs.is_contiguous()):
         raise ValueError("the cache's tensors must be contiguous")
-    if len(scales) != 3 or vs.shape != scales or any(t.shape != scales + (n,) for t, n in ((kc, 64), (vc, 64), (kb, 8), (vb, 8))):
+    shape, blocks, scales = kc.shape, kb.shape, ks.shape
+    if len(shape) != 4 or len(blocks) != 4 or shape[3] != 64 or blocks[3] != 8 or scales != shape[:3] or blocks[:3] != scales \
+            or vc.shape != shape or vb.shape != blocks or vs.shape != scales:
         raise ValueError("a cache of 4 bits is codes [num_pages, H, page_size, 64], blocks [.., 8] and scales [num_pages, H, "
                          f"page_size] (got {[tuple(t.shape) for t in cache]})")
     pages, H, page = scales
@@ -876,21 +881,19 @@ def _check_turn(rope, positions, q_weight, k_weight, eps, B, S, dev):
     if not isinstance(positions, torch.Tensor):
         raise TypeError("rope needs positions, a torch.Tensor")
     axes = len(rope.sections)
-    shape = positions.shape
-    if axes == 1 and (len(shape) < 1 or shape[-1] != 1 or (len(shape) == 1 and S == 1)):
-        positions = positions.unsqueeze(-1)
-        shape = positions.shape
+    shape, strides = positions.shape, positions.stride()
+    if axes == 1 and (len(shape) != 3) and (len(shape) == 1 or shape[-1] != 1 or shape == (B, S)):
+        shape, strides = (*shape, 1), (*strides, 1)      # one axis may be left out
     if len(shape) == 2:
         # [S, axes] for all batches, or, for packed tokens or one token of each sequence, [B * S, axes]
         if shape[0] == S:
-            positions = positions.unsqueeze(0).expand(B, -1, -1)
+            shape, strides = (B, *shape), (0, *strides)
         elif shape[0] == B * S:
-            positions = positions.view(B, S, axes)
-        shape = positions.shape
+            shape, strides = (B, S, shape[1]), (S * strides[0], *strides)
     if positions.dtype is not _INT32 or positions.get_device() != dev or shape != (B, S, axes):
         raise ValueError(f"positions must be int32 [{B}, {S}{', ' + str(axes) if axes > 1 else ''}] on cuda:{dev} "
-                         f"(got {positions.dtype} {tuple(shape)})")
-    sb, ss, sa = positions.stride()
+                         f"(got {positions.dtype} {tuple(positions.shape)})")
+    sb, ss, sa = strides
     if axes > 1 and sa != 1:
         raise ValueError("the axes of a position must be dense")
     return (ctypes.byref(rope._c), positions.data_ptr(), sb if B > 1 else 0, ss if S > 1 else 0) + tail
@@ -1019,19 +1022,22 @@ def kv_pages_reserve(free_pages, free_count, lens, counts, block_table, page_siz
         raise ValueError(f"layout must be one of {TOKEN_LAYOUTS} (got {layout!r})")
     if tokens < 1:
         raise ValueError(f"tokens must be >= 1 (got {tokens})")
-    rows = (tokens,) if layout == "packed" else (B, tokens)
+    packed = layout == "packed"
+    rows = (tokens,) if packed else (B, tokens)
     if out is None:
-        n = math.prod(rows)
+        n = tokens if packed else B * tokens
         flat = torch.empty(4 * B + 1 + 2 * n, dtype=_INT32, device=free_pages.device)
-        parts = flat.split([B, B, B, B, 1, n, n])
-        out = PagePlan(*parts[:5], parts[5].view(rows), parts[6].view(rows))
+        start, taken, new_lens, first, left, slots, positions = flat.split_with_sizes((B, B, B, B, 1, n, n))
+        out = PagePlan(start, taken, new_lens, first, left, slots if packed else slots.view(rows), positions if packed else positions.view(rows))
+        at, b = flat.data_ptr(), 4 * B
+        ptrs = (at, at + b, at + 2 * b, at + 3 * b, at + 4 * b, at + 4 * b + 4, at + 4 * b + 4 + 4 * n)
     else:
         for name, t, shape in zip(PagePlan._fields, out, ((B,),) * 4 + ((1,), rows, rows)):
             if t.dtype is not _INT32 or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
                 raise ValueError(f"out.{name} must be a contiguous int32 {shape} tensor on cuda:{dev}")
+        ptrs = [t.data_ptr() for t in out]
     _call(lib.sage_kv_pages_reserve, dev, free_pages.data_ptr(), free_count.data_ptr(), num_pages, page_size, lens.data_ptr(),
-          counts.data_ptr(), B, block_table.data_ptr(), width, stride, TOKEN_LAYOUTS.index(layout), tokens,
-          *(t.data_ptr() for t in out))
+          counts.data_ptr(), B, block_table.data_ptr(), width, stride, TOKEN_LAYOUTS.index(layout), tokens, *ptrs)
     return out
 
 
