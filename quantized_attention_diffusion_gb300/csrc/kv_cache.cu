@@ -46,27 +46,27 @@ __device__ __forceinline__ int64_t cache_row(const CacheView& c, const PageTable
   return (((static_cast<int64_t>(page) * c.H + h) << c.page_shift) + (pos & ((1 << c.page_shift) - 1)));
 }
 
-// The rows of step i of a warp: head h, tokens 4 j .. 4 j + 3 of sequence b, the
+// The rows of step i of a warp: head h, tokens kTokens j and on of sequence b, the
 // head running fastest, then j.
 struct Step {
   int b, s, h;
 };
+template <int kTokens>
 __device__ __forceinline__ Step step_of(uint32_t i, int H, int steps_per_seq) {
   Step x;
   const uint32_t j = i / static_cast<uint32_t>(H);
   x.h = static_cast<int>(i - j * H);
   x.b = static_cast<int>(j / static_cast<uint32_t>(steps_per_seq));
-  x.s = static_cast<int>(j - x.b * static_cast<uint32_t>(steps_per_seq)) * kRows;
+  x.s = static_cast<int>(j - x.b * static_cast<uint32_t>(steps_per_seq)) * kTokens;
   return x;
 }
 
-template <int kBits>
 __global__ void __launch_bounds__(kWarps * 32) kv_cache_write_kernel(const CacheWriteArgs a, uint32_t steps,
                                                                      int steps_per_seq) {
   const uint32_t i = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (i >= steps) return;                  // warp-uniform
   const int lane = threadIdx.x & 31, l = lane & 7;
-  Step x = step_of(i, a.cache.H, steps_per_seq);
+  Step x = step_of<kRows>(i, a.cache.H, steps_per_seq);
   x.s += lane >> 3;
   const bool live = x.s < a.S && (a.count == nullptr || x.s < __ldg(a.count + x.b));
   uint4 k0 = make_uint4(0u, 0u, 0u, 0u), k1 = k0, v0 = k0, v1 = k0;
@@ -80,8 +80,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv_cache_write_kernel(const Cache
   }
   const int64_t row = live ? cache_row(a.cache, a.table, x.b, static_cast<int64_t>(__ldg(a.start + x.b)) + x.s, x.h) : -1;
   if (live && row < 0 && l == 0) atomicExch(a.err, SAGE_DEVERR_BAD_PAGE);
-  put_row<kBits, false>(a.cache, k0, k1, row, l, l, l + 8);
-  put_row<kBits, true>(a.cache, v0, v1, row, l, l, l + 8);
+  put_row<8, false>(a.cache, k0, k1, row, l, l, l + 8);
+  put_row<8, true>(a.cache, v0, v1, row, l, l, l + 8);
 }
 
 // 16 channels of a row to bf16, one 32-byte store.
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_cache_read_kernel(const CacheR
   const uint32_t i = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (i >= steps) return;                  // warp-uniform
   const int lane = threadIdx.x & 31, l = lane & 7;
-  Step x = step_of(i, a.cache.H, steps_per_seq);
+  Step x = step_of<kRows>(i, a.cache.H, steps_per_seq);
   x.s += lane >> 3;
   if (x.s >= a.S) return;
   uint4 kc = make_uint4(0u, 0u, 0u, 0u), vc = kc;
@@ -132,13 +132,45 @@ __global__ void __launch_bounds__(kWarps * 32) kv_cache_read_kernel(const CacheR
   store_row(a.v + dst, y, vs);
 }
 
-// The same from 4 bits: eight bytes of codes and one block scale a lane.
+// The same into 4 bits.  Eight tokens a warp, four lanes and 32 channels each: what a
+// row needs once is shared by twice as many as above (4 x up to 16384 tokens of 8 heads:
+// 38 us; by eight lanes a row 45, the issue slots the bound).
+constexpr int kRows4 = 8;
+__global__ void __launch_bounds__(kWarps * 32) kv4_cache_write_kernel(const CacheWriteArgs a, uint32_t steps,
+                                                                      int steps_per_seq) {
+  const uint32_t i = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (i >= steps) return;                  // warp-uniform
+  const int lane = threadIdx.x & 31, l = lane & 3;
+  Step x = step_of<kRows4>(i, a.cache.H, steps_per_seq);
+  x.s += lane >> 2;
+  const bool live = x.s < a.S && (a.count == nullptr || x.s < __ldg(a.count + x.b));
+  if (!__any_sync(0xFFFFFFFFu, live)) return;
+  uint4 k[4], v[4];
+  const int c[4] = {l, l + 4, l + 8, l + 12};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) k[j] = v[j] = make_uint4(0u, 0u, 0u, 0u);
+  if (live) {
+    const uint4* kp = reinterpret_cast<const uint4*>(a.k + x.b * a.k_sb + x.s * a.k_ss + x.h * kHeadDim);
+    const uint4* vp = reinterpret_cast<const uint4*>(a.v + x.b * a.v_sb + x.s * a.v_ss + x.h * kHeadDim);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      k[j] = __ldcs(kp + c[j]);
+      v[j] = __ldcs(vp + c[j]);
+    }
+  }
+  const int64_t row = live ? cache_row(a.cache, a.table, x.b, static_cast<int64_t>(__ldg(a.start + x.b)) + x.s, x.h) : -1;
+  if (live && row < 0 && l == 0) atomicExch(a.err, SAGE_DEVERR_BAD_PAGE);
+  write_rows4<4>(k, a.cache.k_codes, a.cache.k_block, a.cache.k_scale, row, l, c);
+  write_rows4<4>(v, a.cache.v_codes, a.cache.v_block, a.cache.v_scale, row, l, c);
+}
+
+// Reading back from 4 bits: eight bytes of codes and one block scale a lane.
 __global__ void __launch_bounds__(kWarps * 32) kv4_cache_read_kernel(const CacheReadArgs a, uint32_t steps,
                                                                      int steps_per_seq) {
   const uint32_t i = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (i >= steps) return;                  // warp-uniform
   const int lane = threadIdx.x & 31, l = lane & 7;
-  Step x = step_of(i, a.cache.H, steps_per_seq);
+  Step x = step_of<kRows>(i, a.cache.H, steps_per_seq);
   x.s += lane >> 3;
   if (x.s >= a.S) return;
   uint2 kc = make_uint2(0u, 0u), vc = kc;
@@ -175,8 +207,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_cache_read_kernel(const Cache
 }
 
 template <typename Args>
-cudaError_t launch_rows(void (*kernel)(Args, uint32_t, int), const Args& a, cudaStream_t stream) {
-  const int per_seq = (a.S + kRows - 1) / kRows;
+cudaError_t launch_rows(void (*kernel)(Args, uint32_t, int), int tokens, const Args& a, cudaStream_t stream) {
+  const int per_seq = (a.S + tokens - 1) / tokens;
   const uint32_t steps = static_cast<uint32_t>(a.B) * per_seq * a.cache.H;
   kernel<<<(steps + kWarps - 1) / kWarps, kWarps * 32, 0, stream>>>(a, steps, per_seq);
   return cudaGetLastError();
@@ -185,11 +217,11 @@ cudaError_t launch_rows(void (*kernel)(Args, uint32_t, int), const Args& a, cuda
 }  // namespace
 
 cudaError_t launch_kv_cache_write(const CacheWriteArgs& a, cudaStream_t stream) {
-  return a.cache.bits == 8 ? launch_rows(kv_cache_write_kernel<8>, a, stream) : launch_rows(kv_cache_write_kernel<4>, a, stream);
+  return a.cache.bits == 8 ? launch_rows(kv_cache_write_kernel, kRows, a, stream) : launch_rows(kv4_cache_write_kernel, kRows4, a, stream);
 }
 
 cudaError_t launch_kv_cache_read(const CacheReadArgs& a, cudaStream_t stream) {
-  return a.cache.bits == 8 ? launch_rows(kv_cache_read_kernel, a, stream) : launch_rows(kv4_cache_read_kernel, a, stream);
+  return launch_rows(a.cache.bits == 8 ? kv_cache_read_kernel : kv4_cache_read_kernel, kRows, a, stream);
 }
 
 }  // namespace sage

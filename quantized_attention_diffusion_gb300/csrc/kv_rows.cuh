@@ -147,10 +147,21 @@ __device__ __forceinline__ uint32_t cvt_e2m1x8(const float2 (&y)[4]) {
   return r;
 }
 
-// The codes of the 8 bf16 values of w, times `inv` (a power of two), over sb > 0.
+// fl(1 / sb) of a block's scale, 0 for 0: one Newton step from the hardware's
+// approximation, which is within an ulp.  (Of the eight significands that E4M3 has,
+// that gives the rounded value from as far as three ulp.)
+__device__ __forceinline__ float inverse(float sb) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(sb));
+  r = fmaf(r, fmaf(-sb, r, 1.0f), r);
+  return sb > 0.0f ? r : 0.0f;
+}
+
+// The codes of the 8 bf16 values of w, times `inv` (a power of two), over sb; 0 if that
+// is 0.
 __device__ __forceinline__ uint32_t encode4(const uint4& w, float inv, float sb) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-  const float nr = -__frcp_rn(sb);
+  const float nr = -inverse(sb);
   const float2 n2 = make_float2(nr, nr), s2 = make_float2(sb, sb), i2 = make_float2(inv, inv);
   float2 y[4];
 #pragma unroll
@@ -159,7 +170,15 @@ __device__ __forceinline__ uint32_t encode4(const uint4& w, float inv, float sb)
     const float2 z = fmul2v(x, n2);
     y[i] = ffma2v(ffma2v(z, s2, x), n2, z);
   }
-  return cvt_e2m1x8(y) ^ 0x88888888u;
+  return sb > 0.0f ? cvt_e2m1x8(y) ^ 0x88888888u : 0u;
+}
+
+// fl(x / 6) for the x that count, 0 or 2^-100 .. 2688: a product with fl(1 / 6) and
+// Markstein's correction (smaller ones are 0 in E4M3 either way).
+__device__ __forceinline__ float sixth(float x) {
+  constexpr float r = 1.0f / 6.0f;
+  const float q = x * r;
+  return fmaf(fmaf(q, -6.0f, x), r, q);
 }
 
 __device__ __forceinline__ uint32_t top_of(const uint4& w) {
@@ -167,37 +186,46 @@ __device__ __forceinline__ uint32_t top_of(const uint4& w) {
   return max_u16x2(max_u16x2(w.x & m, w.y & m), max_u16x2(w.z & m, w.w & m));
 }
 
-// write_rows for 4 bits: the chunks c0 of lanes l and l ^ 1 are one block of 16
-// channels, and so are their chunks c1.
-__device__ __forceinline__ void write_rows4(const uint4& w0, const uint4& w1, uint8_t* codes, uint8_t* blocks, float* scales,
-                                            int64_t row, int l, int c0, int c1) {
-  uint32_t t0 = top_of(w0), t1 = top_of(w1);
-  t0 = max_u16x2(t0, __shfl_xor_sync(0xFFFFFFFFu, t0, 1));
-  t1 = max_u16x2(t1, __shfl_xor_sync(0xFFFFFFFFu, t1, 1));
-  uint32_t top = max_u16x2(t0, t1);
+// write_rows for 4 bits, of rows of 16 / kN lanes: a lane has the chunks c[i] in w[i], and
+// those of lanes l and l ^ 1 are one block of 16 channels.
+template <int kN>
+__device__ __forceinline__ void write_rows4(const uint4 (&w)[kN], uint8_t* codes, uint8_t* blocks, float* scales, int64_t row,
+                                            int l, const int (&c)[kN]) {
+  uint32_t t[kN], top = 0u;
 #pragma unroll
-  for (int d = 2; d < 8; d <<= 1) top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+  for (int i = 0; i < kN; ++i) {
+    t[i] = top_of(w[i]);
+    t[i] = max_u16x2(t[i], __shfl_xor_sync(0xFFFFFFFFu, t[i], 1));
+    top = max_u16x2(top, t[i]);
+  }
+#pragma unroll
+  for (int d = 2; d < 16 / kN; d <<= 1) top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
   top = max(top & 0xFFFFu, top >> 16);
-  t0 = max(t0 & 0xFFFFu, t0 >> 16);
-  t1 = max(t1 & 0xFFFFu, t1 >> 16);
+  // A row of zeros or with an infinity or a NaN: blocks and codes 0.
   const bool some = top > 0u && top < 0x7F80u;
   // 2688 = (1 + 40 / 128) * 2^11
   const uint32_t field = static_cast<uint32_t>(max(1, static_cast<int>(top >> 7) - 11 + ((top & 0x7Fu) > 40u ? 1 : 0)));
   const float inv = __uint_as_float((254u - field) << 23);
-  uint32_t b0 = 0u, b1 = 0u, y0 = 0u, y1 = 0u;
-  if (some) {
-    b0 = cvt_e4m3x2(__fdiv_rn(__uint_as_float(t0 << 16) * inv, 6.0f), 0.0f) & 0xFFu;
-    b1 = cvt_e4m3x2(__fdiv_rn(__uint_as_float(t1 << 16) * inv, 6.0f), 0.0f) & 0xFFu;
-    if (b0 != 0u) y0 = encode4(w0, inv, e4m3x2_to_f32(b0).x);
-    if (b1 != 0u) y1 = encode4(w1, inv, e4m3x2_to_f32(b1).x);
+  uint32_t block[kN], code[kN];
+#pragma unroll
+  for (int i = 0; i < kN; i += 2) {
+    float x[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) x[e] = sixth(some ? __uint_as_float(max(t[i + e] << 16, t[i + e] & 0xFFFF0000u)) * inv : 0.0f);
+    const uint32_t both = cvt_e4m3x2(x[0], x[1]);
+    const float2 sb = e4m3x2_to_f32(both);
+    block[i] = both & 0xFFu;
+    block[i + 1] = both >> 8;
+    code[i] = encode4(w[i], inv, sb.x);
+    code[i + 1] = encode4(w[i + 1], inv, sb.y);
   }
   if (row >= 0) {
     uint32_t* dst = reinterpret_cast<uint32_t*>(codes + row * 64);
-    dst[c0] = y0;
-    dst[c1] = y1;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) dst[c[i]] = code[i];
     if ((l & 1) == 0) {
-      blocks[row * 8 + (c0 >> 1)] = static_cast<uint8_t>(b0);
-      blocks[row * 8 + (c1 >> 1)] = static_cast<uint8_t>(b1);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) blocks[row * 8 + (c[i] >> 1)] = static_cast<uint8_t>(block[i]);
     }
     if (l == 0) scales[row] = some ? __uint_as_float(field << 23) : top == 0u ? 0.0f : __uint_as_float(0x7FC00000u);
   }
@@ -225,7 +253,8 @@ __device__ __forceinline__ void put_row(const CacheView& c, const uint4& w0, con
   if constexpr (kBits == 8)
     write_rows<kIsV>(w0, w1, kIsV ? c.v_codes : c.k_codes, kIsV ? c.v_scale : c.k_scale, row, l, c0, c1);
   else
-    write_rows4(w0, w1, kIsV ? c.v_codes : c.k_codes, kIsV ? c.v_block : c.k_block, kIsV ? c.v_scale : c.k_scale, row, l, c0, c1);
+    write_rows4<2>({w0, w1}, kIsV ? c.v_codes : c.k_codes, kIsV ? c.v_block : c.k_block, kIsV ? c.v_scale : c.k_scale, row, l,
+                   {c0, c1});
 }
 
 }  // namespace sage::rows
