@@ -567,8 +567,8 @@ uint64_t sage_rope_frequency(double radians);
  *                   pos_stride_s + a (strides >= 0; 0 shares them)
  *   eps        in : finite, >= 0: x * w / sqrt(mean x^2 + eps); -1: no norm
  *   q_weight, k_weight in : bf16 [D], or NULL for ones
- *   q_out, k_out out: bf16, dense; may be q and k where those are dense.  fp32
- *                   arithmetic, rounded once
+ *   q_out, k_out out: bf16, dense; may be q and k where those are dense, and
+ *                   otherwise overlap no input.  fp32 arithmetic, rounded once
  * One launch.  B * S * (Hq + Hk) <= 2^31 - 1.  Errors: INVALID_ARG, UNSUPPORTED,
  * MISALIGNED, CUDA.
  */

@@ -551,6 +551,28 @@ uint64_t revolutions(double f) {
   return (static_cast<uint64_t>(static_cast<int64_t>(up)) << 32) + static_cast<uint64_t>(std::llrint(rest));
 }
 
+// The elements from the first to the last of a [B, S, H, 128] tensor of 16-bit values.
+struct Extent {
+  uintptr_t first, end;
+  Extent(const void* p, int64_t sb, int64_t ss, int B, int S, int H)
+      : first(reinterpret_cast<uintptr_t>(p)),
+        end(p && H > 0 ? first + 2 * static_cast<uintptr_t>((B - 1) * sb + (S - 1) * ss + static_cast<int64_t>(H) * kHeadDim) : first) {}
+  bool meets(const Extent& x) const { return first < x.end && x.first < end; }
+};
+
+// An output takes no input's place but, where that is dense, its own input's: other rows
+// might be written before they are read.
+sage_status check_place(const char* name, const Extent& out, const Extent& own, bool dense, std::initializer_list<Extent> others) {
+  bool bad = out.meets(own) && !(dense && out.first == own.first);
+  for (const Extent& x : others) bad = bad || out.meets(x);
+  return bad ? fail(SAGE_ERR_INVALID_ARG, "%s overlaps an input or another output", name) : SAGE_OK;
+}
+
+bool is_dense(int64_t sb, int64_t ss, int B, int S, int H) {
+  const int64_t row = static_cast<int64_t>(H) * kHeadDim;
+  return (S == 1 || ss == row) && (B == 1 || sb == S * row);
+}
+
 // Norm and rotation as sage_qk_norm_rope and sage_kv_cache_append take them.
 sage_status turn_args(TurnArgs* a, const sage_rope* rope, const int32_t* positions, int64_t p_sb, int64_t p_ss,
                       const void* q_weight, const void* k_weight, float eps) {
@@ -616,6 +638,13 @@ sage_status run_cache_append(const Cache* cache, const void* q, const void* k, c
   if (s == SAGE_OK) s = check_ints(slots, "slots");
   if (s == SAGE_OK) s = turn_args(&a, rope, positions, p_sb, p_ss, q_weight, k_weight, eps);
   if (s != SAGE_OK) return s;
+  if (Hq > 0) {
+    const int64_t q_row = static_cast<int64_t>(Hq) * kHeadDim;
+    const Extent qo(q_out, S * q_row, q_row, B, S, Hq), qi(q, q_sb, q_ss, B, S, Hq);
+    const Extent ki(k, k_sb, k_ss, B, S, cache->H), vi(v, v_sb, v_ss, B, S, cache->H);
+    s = check_place("q_out", qo, qi, is_dense(q_sb, q_ss, B, S, Hq), {ki, vi});
+    if (s != SAGE_OK) return s;
+  }
   a.q = static_cast<const uint16_t*>(q);
   a.k = static_cast<const uint16_t*>(k);
   a.v = static_cast<const uint16_t*>(v);
@@ -1012,6 +1041,12 @@ sage_status sage_qk_norm_rope(const void* q, const void* k, int64_t q_stride_b, 
   if (s == SAGE_OK && Hk > 0) s = check_ptrs({{k, "k"}, {k_out, "k_out"}});
   if (s == SAGE_OK && Hk > 0) s = check_strides(k_stride_b, k_stride_s, "k");
   if (s == SAGE_OK) s = turn_args(&a, rope, positions, pos_stride_b, pos_stride_s, q_weight, k_weight, eps);
+  if (s != SAGE_OK) return s;
+  const Extent qi(q, q_stride_b, q_stride_s, B, S, Hq), ki(k, k_stride_b, k_stride_s, B, S, Hk);
+  const int64_t q_row = static_cast<int64_t>(Hq) * kHeadDim, k_row = static_cast<int64_t>(Hk) * kHeadDim;
+  const Extent qo(q_out, S * q_row, q_row, B, S, Hq), ko(k_out, S * k_row, k_row, B, S, Hk);
+  s = check_place("q_out", qo, qi, is_dense(q_stride_b, q_stride_s, B, S, Hq), {ki, ko});
+  if (s == SAGE_OK && Hk > 0) s = check_place("k_out", ko, ki, is_dense(k_stride_b, k_stride_s, B, S, Hk), {qi});
   if (s != SAGE_OK) return s;
   a.q = static_cast<const uint16_t*>(q);
   a.k = static_cast<const uint16_t*>(k);

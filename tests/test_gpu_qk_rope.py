@@ -241,6 +241,9 @@ def test_injected_faults_and_refusals():
             call()
         call()
     w = torch.ones(D, dtype=torch.bfloat16, device="cuda")
+    flat = torch.zeros((1, 8, 2, D), dtype=torch.bfloat16, device="cuda")
+    dq = torch.zeros((1, 3, 2, D), dtype=torch.bfloat16, device="cuda")
+    dk = torch.zeros_like(dq)
     refused = [
         (lambda: qad.qk_norm_rope(q, k, rope), TypeError), (lambda: qad.qk_norm_rope(q, k, None, pos), ValueError),
         (lambda: qad.qk_norm_rope(q, k, rope, pos.long()), ValueError), (lambda: qad.qk_norm_rope(q, k, rope, pos[:2]), ValueError),
@@ -249,6 +252,9 @@ def test_injected_faults_and_refusals():
         (lambda: qad.qk_norm_rope(q, k, rope, pos, eps=-1.0), ValueError), (lambda: qad.qk_norm_rope(q, k, rope, pos, eps=math.nan), ValueError),
         (lambda: qad.qk_norm_rope(q.float(), k, rope, pos), ValueError), (lambda: qad.qk_norm_rope(q, k[:, :2], rope, pos), ValueError),
         (lambda: qad.qk_norm_rope(q, k, rope, pos, out=(torch.empty_like(k.contiguous()),) * 2), ValueError),
+        (lambda: qad.qk_norm_rope(dq, dk, rope, pos, out=(dk, dq)), qad.SageError),
+        (lambda: qad.qk_norm_rope(flat[:1, 1:4], None, rope, pos, out=flat[:1, :3]), qad.SageError),
+        (lambda: qad.kv_cache_append(dq[:, :, :2].contiguous(), dk, v, cache, slots, rope, pos, out=dk), qad.SageError),
         (lambda: qad.kv_cache_append(q, k, v, cache, slots[:2], rope, pos), ValueError),
         (lambda: qad.kv_cache_append(q, k, v, cache, slots.long(), rope, pos), ValueError),
         (lambda: qad.kv_cache_append(q, k, v[:, :, :1], cache, slots, rope, pos), ValueError),
