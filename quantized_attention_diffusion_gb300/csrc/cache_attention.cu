@@ -1153,6 +1153,78 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const Mer
     p.lse[(static_cast<int64_t>(b) * p.Hq + hq) * p.Sq + t] = L == 0.0f ? -INFINITY : (m + log2f(L)) * kLn2;
 }
 
+// The same where a unit has many rows and few parts: a warp takes kMergeRows rows side by
+// side, so that their loads are in flight together, and the sums are those of one warp a
+// row above, in the same order (2 x 1000 tokens, 16 / 4 heads over 8000 keys, 32000 rows in
+// two parts or three: MERGENEW us, by the kernel above 28).
+constexpr int kMergeRows = 4;
+__global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_rows_kernel(const MergeParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4 unit = p.desc[blockIdx.x];
+  const int n = unit.w;
+  const int row0 = (blockIdx.y * kMergeWarps + warp) * kMergeRows;
+  if (n < 2 || row0 >= min(p.R, p.rows - unit.y * p.R)) return;      // warp-uniform
+  auto at = [&](int k, int i) {                                      // row row0 + i of part k, where there is one
+    const int slot = k == 0 ? 2 * static_cast<int>(blockIdx.x) + 1 : 2 * (static_cast<int>(blockIdx.x) + k);
+    return static_cast<int64_t>(slot) * p.slot_rows + min(row0 + i, p.slot_rows - 1);
+  };
+  float m[kMergeRows], d[kMergeRows], L[kMergeRows];
+  float4 acc[kMergeRows];
+#pragma unroll
+  for (int i = 0; i < kMergeRows; ++i) {
+    m[i] = d[i] = kLowest;
+    L[i] = 0.0f;
+    acc[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
+  for (int k0 = 0; k0 < n; k0 += 32) {
+    float4 mine[kMergeRows];
+#pragma unroll
+    for (int i = 0; i < kMergeRows; ++i) {
+      mine[i] = make_float4(kLowest, 0.0f, 0.0f, 0.0f);
+      if (k0 + lane < n) mine[i] = p.part_ml[at(k0 + lane, i)];
+    }
+#pragma unroll
+    for (int i = 0; i < kMergeRows; ++i) {
+      const float less = take_in(mine[i], m[i], d[i], L[i]);
+      acc[i] = make_float4(acc[i].x * less, acc[i].y * less, acc[i].z * less, acc[i].w * less);
+    }
+    const int end = min(32, n - k0);
+    for (int k = 0; k < end; k += 2) {
+      float4 y[2][kMergeRows];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < kMergeRows; ++i)
+          y[j][i] = reinterpret_cast<const float4*>(p.part_o + at(k0 + min(k + j, end - 1), i) * kHeadDim)[lane];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (k + j >= end) break;
+#pragma unroll
+        for (int i = 0; i < kMergeRows; ++i) {
+          const float w = __shfl_sync(0xFFFFFFFFu, mine[i].z, k + j);
+          L[i] += __shfl_sync(0xFFFFFFFFu, mine[i].y, k + j);
+          acc[i].x += y[j][i].x * w;
+          acc[i].y += y[j][i].y * w;
+          acc[i].z += y[j][i].z * w;
+          acc[i].w += y[j][i].w * w;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kMergeRows; ++i) {
+    const int rr = unit.y * p.R + row0 + i;
+    if (row0 + i >= p.R || rr >= p.rows) break;
+    const int t = rr / p.G, hq = unit.z * p.G + rr % p.G;
+    const float half = scale2(d[i]), inv = L[i] == 0.0f ? 0.0f : half / L[i];
+    const uint2 w = make_uint2(pack_bf16(acc[i].x * half * inv, acc[i].y * half * inv), pack_bf16(acc[i].z * half * inv, acc[i].w * half * inv));
+    *reinterpret_cast<uint2*>(p.out + ((static_cast<int64_t>(unit.x) * p.Sq + t) * p.Hq + hq) * kHeadDim + lane * 4) = w;
+    if (p.lse != nullptr && lane == 0)
+      p.lse[(static_cast<int64_t>(unit.x) * p.Hq + hq) * p.Sq + t] = L[i] == 0.0f ? -INFINITY : (m[i] + log2f(L[i])) * kLn2;
+  }
+}
+
 // ------------------------------------------------------------------- host --
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -1439,7 +1511,9 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream) 
     mp.split = 1;
     while (mp.split < kMergeWarps && (mp.split * 8 < parts || mp.split * 2 * tile_rows <= kMergeWarps)) mp.split *= 2;
     cudaLaunchConfig_t cfg = {};
+    const bool by_rows = !both && mp.split == 1 && w.R == kWideRows;
     cfg.gridDim = dim3(both ? w.units : ctas, (tile_rows * mp.split + kMergeWarps - 1) / kMergeWarps);
+    if (by_rows) cfg.gridDim.y = (tile_rows + kMergeWarps * kMergeRows - 1) / (kMergeWarps * kMergeRows);
     cfg.blockDim = dim3(kMergeWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -1447,7 +1521,7 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t stream) 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, cache_merge_kernel, mp);
+    e = cudaLaunchKernelEx(&cfg, by_rows ? cache_merge_rows_kernel : cache_merge_kernel, mp);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
