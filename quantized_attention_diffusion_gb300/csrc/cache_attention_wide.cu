@@ -128,7 +128,7 @@ struct Codes<8> {
   uint4 w;
   __device__ void load(const uint8_t* codes, const uint8_t*) { w = load_once(codes); }
   template <bool kIsV>
-  __device__ void values(uint32_t (&o)[8]) const {
+  __device__ void values(uint32_t (&o)[8], uint32_t) const {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -139,7 +139,8 @@ struct Codes<8> {
     }
   }
 };
-// One block: its codes times its scale, 6 significant bits, exact in fp16.
+// One block: its codes times its scale, 6 significant bits, exact in fp16, and times
+// `fold` (two fp16, a power of two down to 2^-14 or 0), exact as well.
 template <>
 struct Codes<4> {
   uint2 w;
@@ -149,9 +150,10 @@ struct Codes<4> {
     asm volatile("ld.global.nc.L1::no_allocate.u8 %0, [%1];" : "=r"(block) : "l"(blocks));
   }
   template <bool>
-  __device__ void values(uint32_t (&o)[8]) const {
+  __device__ void values(uint32_t (&o)[8], uint32_t fold) const {
     uint32_t s2;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"(static_cast<uint16_t>(block * 0x0101u)));
+    s2 = mul_f16x2(s2, fold);
     const uint32_t u[2] = {w.x, w.y};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -293,6 +295,48 @@ __device__ __forceinline__ bool weigh(uint32_t tS, const float* kx, const float*
   return kSlow ? total > kFarSum || !(sumw.x + sumw.y <= kFar) : total * top > kFar;
 }
 
+// Of a 4-bit cache's tile: for its keys 16 i + 4 g + 0 .. 3, the one scale of K (times
+// softmax_scale * log2 e) and of V that stand for all of them, the rows' own being in the
+// values; negative where the rows' scales were too far apart for that.
+struct Even {
+  float4 k, v;
+  __device__ bool holds() const { return fminf(fminf(fminf(k.x, k.y), fminf(k.z, k.w)), fminf(fminf(v.x, v.y), fminf(v.z, v.w))) > 0.0f; }
+};
+
+// weigh where that holds and the row sees all of the keys: weights 2^(x + log2 v - R) at
+// once, and L's p from their sums, since the scales are powers of two.  Five instructions
+// for two scores where the arrays of scales take eight and a load.
+__device__ __forceinline__ bool weigh_even(uint32_t tS, const Even& ev, const Row& z, uint32_t (&w)[16], float2& sum) {
+  uint32_t a[32];
+  tmem_ld32(tS, a);
+  const float k[4] = {ev.k.x * z.rk, ev.k.y * z.rk, ev.k.z * z.rk, ev.k.w * z.rk};
+  const float v[4] = {ev.v.x, ev.v.y, ev.v.z, ev.v.w};
+  float2 q[4];
+  tmem_ld_wait();
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const float b = static_cast<float>(static_cast<int>(__float_as_uint(v[g]) >> 23) - 127) - z.R;
+    q[g] = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int at = 4 * g; at < 32; at += (at & 2) ? 14 : 2) {
+      const float2 x = ffma2_bc(__uint_as_float(a[at]), __uint_as_float(a[at + 1]), k[g], b);
+      const float2 y = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+      q[g] = fadd2v(q[g], y);
+      w[at / 2] = pack_f16(y.x, y.y);
+    }
+  }
+  sum = make_float2(0.0f, 0.0f);
+  float all = 0.0f;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const float back = __uint_as_float((254u << 23) - __float_as_uint(v[g]));      // 1 / v
+    all += q[g].x + q[g].y;
+    sum.x += q[g].x * back;
+    sum.y += q[g].y * back;
+  }
+  return all > kFar || sum.x + sum.y > kFarSum;
+}
+
 template <bool kPrefix, int kBits>
 __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -304,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
   __shared__ long long s_off[kPrefix ? 2 : kMaxBatch + 1];
   __shared__ __align__(16) float s_ks[kScaleSlots][kWideTok], s_vs[kScaleSlots][kWideTok];
   __shared__ __align__(16) float s_top[kScaleSlots][4];   // of a V warp's keys: the largest scale, or infinity
+  __shared__ __align__(16) float s_even[2][kScaleSlots][4];   // 4 bits: Even's k and v
   __shared__ int s_info[2][2];                            // [K, V][stage]
   __shared__ volatile long long s_end, s_per;
   __shared__ float4 s_half[128];                          // R, L and D of half 1's rows
@@ -366,7 +411,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
       const int tid = threadIdx.x & 127;
       const int sub = 4 * (warp & 3) + ((lane >> 2) & 1) + 2 * (lane >> 4);   // key of a step
       const int q16 = (lane & 3) + ((lane >> 3) & 1) * 4;                     // 16 codes of a key
-      const int scale_key = is_v ? 16 * (lane >> 2) + 4 * (warp & 3) + (lane & 3) : tid;   // the key whose scale it loads
+      // The key whose scale it loads; of V, and in 4 bits, one that its warp converts.
+      const int scale_key = is_v || kBits == 4 ? 16 * (lane >> 2) + 4 * (warp & 3) + (lane & 3) : tid;
       const int ps = p.cache.page_shift;
       constexpr int kRow = kHeadDim * kBits / 8;                              // bytes of a key's codes
       const uint8_t* codes = (is_v ? p.cache.v_codes : p.cache.k_codes) + q16 * (kRow / 8);
@@ -401,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
         }
       };
       Codes<kBits> w[8];
-      float scale = 0.0f;
+      float scale = 0.0f, even_k = 0.0f;
       auto load = [&]() {
         loaded = more;
         info = info_next;
@@ -411,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
         bad |= gone && mine;
         if (gone) page = -1;
         // The rows of a step follow those of the step before within a page.
-        if (__any_sync(0xFFFFFFFFu, gone && mine) || t0 + kWideTok > hi) {   // some keys are not there: zeros
+        if (unlikely(__any_sync(0xFFFFFFFFu, gone && mine) || t0 + kWideTok > hi)) {   // some keys are not there: zeros
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int pg = __shfl_sync(0xFFFFFFFFu, page, i), t = t0 + 16 * i;
@@ -442,6 +488,23 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
       int it = 0;
       for (; loaded; ++it) {
         const int s = it & 1, round = it >> 1;
+        // In 4 bits a warp's 32 keys get the largest of their scales, and the values the
+        // rest, where that is a power of two down to 2^-14 for all of them.  Rows of zeros in
+        // V alone have no scale that could stand for theirs in the references.
+        uint32_t ratio = 0x3C003C00u;
+        if constexpr (kBits == 4) {
+          const uint32_t bits = __float_as_uint(scale);
+          const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, bits), least = __reduce_min_sync(0xFFFFFFFFu, bits == 0u ? 0x7F000000u : bits);
+          const uint32_t top = most == 0u ? 0x3F800000u : most;          // no scale but 0: any
+          const bool even = most < 0x7F800000u && (most == 0u ? !is_v : most - least <= 14u << 23) &&
+                            !__any_sync(0xFFFFFFFFu, (bits & 0x7FFFFFu) != 0u);
+          if (even) {
+            ratio = bits == 0u ? 0u : ((15u << 10) - ((top - bits) >> 13)) * 0x10001u;
+            scale = __uint_as_float(top);
+          }
+          if (is_v && lane == 0) s_even[1][it % kScaleSlots][warp & 3] = even ? scale : -1.0f;
+          if (!is_v) even_k = even ? scale * p.c_scale : -1.0f;
+        }
         // V's scales may be written before its stage is free: the tile that last
         // used the slot has been multiplied.
         if (is_v) {
@@ -451,17 +514,20 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
           if (lane == 0) s_top[it % kScaleSlots][warp & 3] = __uint_as_float(min(top, 0x7F800000u));
           mbar_arrive(&bars.scales[it % kScaleSlots]);
         }
-        if (round > 0 && !__all_sync(0xFFFFFFFFu, wait(&empty[s], round - 1))) break;
+        if (unlikely(round > 0 && !__all_sync(0xFFFFFFFFu, wait(&empty[s], round - 1)))) break;
         uint8_t* to = dst + s * kTileBytes;
         if (!is_v) {
-          s_ks[it % kScaleSlots][tid] = scale * p.c_scale;
+          s_ks[it % kScaleSlots][scale_key] = scale * p.c_scale;
+          if (kBits == 4 && lane == 0) s_even[0][it % kScaleSlots][warp & 3] = even_k;
           mbar_arrive(&bars.scales[it % kScaleSlots]);
         }
         auto convert = [&](auto v) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             uint32_t o[8];
-            w[i].template values<decltype(v)::value>(o);
+            // Step i's row of this lane: its scale is with lane 4 i + sub % 4 of the warp.
+            const uint32_t fold = kBits == 4 ? __shfl_sync(0xFFFFFFFFu, ratio, 4 * i + (sub & 3)) : 0u;
+            w[i].template values<decltype(v)::value>(o, fold);
             *reinterpret_cast<uint4*>(to + i * 2048) = make_uint4(o[0], o[1], o[2], o[3]);
             *reinterpret_cast<uint4*>(to + i * 2048 + static_cast<int>(odd)) = make_uint4(o[4], o[5], o[6], o[7]);
           }
@@ -567,25 +633,36 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
             // In this order: a half passes over tiles that are not its own, and only the
             // scores say that the slot's phase before this tile's has ended.
             ok = wait(&bars.s_full[t][v & 1], (done + v) >> 1) && wait(&bars.scales[slot], (it + j) / kScaleSlots);
-            if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+            if (unlikely(!(ok = __all_sync(0xFFFFFFFFu, ok)))) break;
             tc_fence_after();
             const uint32_t tS = tmem + lanes + col_s(t, 0) + sub;
             const int key0 = (x.t0 + j) * kWideTok + sub;
             const float4 top4 = *reinterpret_cast<const float4*>(s_top[slot]);
             const float top = fmaxf(fmaxf(fmaxf(top4.x, top4.y), fmaxf(top4.z, top4.w)), kTiny);
+            Even ev;
+            if constexpr (kBits == 4) {
+              ev.k = *reinterpret_cast<const float4*>(s_even[0][slot]);
+              ev.v = *reinterpret_cast<const float4*>(s_even[1][slot]);
+            }
+            const bool even = kBits == 4 && ev.holds();
 #pragma unroll 1
             for (int c = 0; c < kSub && ok; c += 32) {
               const float *kx = s_ks[slot] + sub + c, *vx = s_vs[slot] + sub + c;
               const int left = lim - key0 - c;
               uint32_t w[16];
               float2 sum;
+              // What is rare is told to the compiler, which puts it out of the way: with five
+              // kinds of warps at work a jump waits some 100 cycles for its instructions.
               while (true) {
                 bool far;
-                if (key0 + kSub > lo || top == INFINITY || __any_sync(0xFFFFFFFFu, z.f != 1.0f))   // warp-uniform
-                  far = weigh<true>(tS + c, kx, vx, top, left, z, w, sum);
-                else
+                const bool slow = key0 + kSub > lo || top == INFINITY || __any_sync(0xFFFFFFFFu, z.f != 1.0f);   // warp-uniform
+                if (kBits == 4 && likely(even && !slow))
+                  far = weigh_even(tS + c, ev, z, w, sum);
+                else if (likely(!slow))
                   far = weigh<false>(tS + c, kx, vx, top, left, z, w, sum);
-                if (!__any_sync(0xFFFFFFFFu, far)) break;
+                else
+                  far = weigh<true>(tS + c, kx, vx, top, left, z, w, sum);
+                if (likely(!__any_sync(0xFFFFFFFFu, far))) break;
                 float alpha;
                 if (!__any_sync(0xFFFFFFFFu, move_references(tS + c, kx, vx, left, far, z, alpha))) break;   // in range as it is
                 if (v > 0) ok = before();
@@ -595,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
               z.l = fadd2v(z.l, sum);
               tmem_st16(tS + c / 2, w);
             }
-            if (!ok) break;
+            if (unlikely(!ok)) break;
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&bars.p_full[t][v & 1]);

@@ -87,6 +87,10 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   return mbar_wait_slow(a, parity, abort_flag, err_word, timeout_ns);
 }
 
+// What nearly always holds, or nearly never: the compiler lays code out by it.
+__device__ __forceinline__ bool likely(bool x) { return __builtin_expect(x, 1); }
+__device__ __forceinline__ bool unlikely(bool x) { return __builtin_expect(x, 0); }
+
 // mbar_wait without a function call, for kernels that move registers between
 // their warpgroups (setmaxnreg), which calls would not allow.  A poll suspends the
 // thread for up to 20 us, so that waiting warps leave the issue slots to others.
@@ -104,6 +108,7 @@ __device__ __forceinline__ bool mbar_try_wait_long(uint32_t bar, uint32_t parity
 __device__ __forceinline__ bool mbar_wait_inline(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err_word,
                                                  uint64_t timeout_ns) {
   const uint32_t a = smem_addr(bar);
+  if (likely(mbar_try_wait_long(a, parity))) return true;
   uint64_t t0 = 0;
   while (true) {
 #pragma unroll 1
