@@ -644,27 +644,41 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
               ev.k = *reinterpret_cast<const float4*>(s_even[0][slot]);
               ev.v = *reinterpret_cast<const float4*>(s_even[1][slot]);
             }
-            const bool even = kBits == 4 && ev.holds();
+            // What is usual stands in a line and what is rare out of the way: with five kinds
+            // of warps at work a jump waits some 100 cycles for its instructions.
+            const float *kx = s_ks[slot] + sub, *vx = s_vs[slot] + sub;
+            int c = 0;                                     // scores that are done
+            const bool all_seen = key0 + kSub <= lo && top < INFINITY;
+            if (likely(all_seen && (kBits == 8 || ev.holds()) && !__any_sync(0xFFFFFFFFu, z.f != 1.0f))) {
+#pragma unroll
+              for (int i = 0; i < kSub; i += 32) {
+                uint32_t w[16];
+                float2 sum;
+                bool far;
+                if constexpr (kBits == 4)
+                  far = weigh_even(tS + i, ev, z, w, sum);
+                else
+                  far = weigh<false>(tS + i, kx + i, vx + i, top, 32, z, w, sum);
+                if (unlikely(__any_sync(0xFFFFFFFFu, far))) break;
+                z.l = fadd2v(z.l, sum);
+                tmem_st16(tS + i / 2, w);
+                c = i + 32;
+              }
+            }
 #pragma unroll 1
-            for (int c = 0; c < kSub && ok; c += 32) {
-              const float *kx = s_ks[slot] + sub + c, *vx = s_vs[slot] + sub + c;
+            for (; c < kSub && ok; c += 32) {
               const int left = lim - key0 - c;
               uint32_t w[16];
               float2 sum;
-              // What is rare is told to the compiler, which puts it out of the way: with five
-              // kinds of warps at work a jump waits some 100 cycles for its instructions.
               while (true) {
                 bool far;
-                const bool slow = key0 + kSub > lo || top == INFINITY || __any_sync(0xFFFFFFFFu, z.f != 1.0f);   // warp-uniform
-                if (kBits == 4 && likely(even && !slow))
-                  far = weigh_even(tS + c, ev, z, w, sum);
-                else if (likely(!slow))
-                  far = weigh<false>(tS + c, kx, vx, top, left, z, w, sum);
+                if (!all_seen || __any_sync(0xFFFFFFFFu, z.f != 1.0f))   // warp-uniform
+                  far = weigh<true>(tS + c, kx + c, vx + c, top, left, z, w, sum);
                 else
-                  far = weigh<true>(tS + c, kx, vx, top, left, z, w, sum);
-                if (likely(!__any_sync(0xFFFFFFFFu, far))) break;
+                  far = weigh<false>(tS + c, kx + c, vx + c, top, left, z, w, sum);
+                if (!__any_sync(0xFFFFFFFFu, far)) break;
                 float alpha;
-                if (!__any_sync(0xFFFFFFFFu, move_references(tS + c, kx, vx, left, far, z, alpha))) break;   // in range as it is
+                if (!__any_sync(0xFFFFFFFFu, move_references(tS + c, kx + c, vx + c, left, far, z, alpha))) break;   // in range as it is
                 if (v > 0) ok = before();
                 if (!ok) break;
                 rescale(tO, tS, v > 0, c > 0, alpha);
