@@ -303,38 +303,58 @@ struct Even {
   __device__ bool holds() const { return fminf(fminf(fminf(k.x, k.y), fminf(k.z, k.w)), fminf(fminf(v.x, v.y), fminf(v.z, v.w))) > 0.0f; }
 };
 
-// weigh where that holds and the row sees all of the keys: weights 2^(x + log2 v - R) at
-// once, and L's p from their sums, since the scales are powers of two.  Five instructions
-// for two scores where the arrays of scales take eight and a load.
-__device__ __forceinline__ bool weigh_even(uint32_t tS, const Even& ev, const Row& z, uint32_t (&w)[16], float2& sum) {
-  uint32_t a[32];
-  tmem_ld32(tS, a);
+// weigh of a buffer's 64 scores where that holds and the row sees all of the keys:
+// weights 2^(x + log2 v - R) at once, and L's p from their sums, since the scales are
+// powers of two.  Five instructions for two scores where the arrays of scales take eight
+// and a load; the next 16 scores are loaded meanwhile.  -> scores whose weights are
+// stored: 64, or fewer where the references have to move first.
+__device__ __forceinline__ int weigh_even(uint32_t tS, const Even& ev, Row& z) {
+  uint32_t next[16];
+  tmem_ld16(tS, next);
   const float k[4] = {ev.k.x * z.rk, ev.k.y * z.rk, ev.k.z * z.rk, ev.k.w * z.rk};
   const float v[4] = {ev.v.x, ev.v.y, ev.v.z, ev.v.w};
-  float2 q[4];
-  tmem_ld_wait();
+  float b[4], back[4];                       // log2 v - R, 1 / v
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
-    const float b = static_cast<float>(static_cast<int>(__float_as_uint(v[g]) >> 23) - 127) - z.R;
-    q[g] = make_float2(0.0f, 0.0f);
+    b[g] = static_cast<float>(static_cast<int>(__float_as_uint(v[g]) >> 23) - 127) - z.R;
+    back[g] = __uint_as_float((254u << 23) - __float_as_uint(v[g]));
+  }
 #pragma unroll
-    for (int at = 4 * g; at < 32; at += (at & 2) ? 14 : 2) {
-      const float2 x = ffma2_bc(__uint_as_float(a[at]), __uint_as_float(a[at + 1]), k[g], b);
-      const float2 y = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-      q[g] = fadd2v(q[g], y);
-      w[at / 2] = pack_f16(y.x, y.y);
+  for (int c = 0; c < kSub; c += 32) {
+    float2 q[4];
+    uint32_t w[16];
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+      uint32_t a[16];
+      tmem_ld_wait16(next);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) a[i] = next[i];
+      if (c + h + 16 < kSub) tmem_ld16(tS + c + h + 16, next);
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const int g = i >> 2;
+        const float2 x = ffma2_bc(__uint_as_float(a[i]), __uint_as_float(a[i + 1]), k[g], b[g]);
+        const float2 y = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+        q[g] = h == 0 && (i & 2) == 0 ? y : fadd2v(q[g], y);
+        w[(h + i) / 2] = pack_f16(y.x, y.y);
+      }
     }
-  }
-  sum = make_float2(0.0f, 0.0f);
-  float all = 0.0f;
+    float2 sum = make_float2(0.0f, 0.0f);
+    float all = 0.0f;
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const float back = __uint_as_float((254u << 23) - __float_as_uint(v[g]));      // 1 / v
-    all += q[g].x + q[g].y;
-    sum.x += q[g].x * back;
-    sum.y += q[g].y * back;
+    for (int g = 0; g < 4; ++g) {
+      all += q[g].x + q[g].y;
+      sum.x += q[g].x * back[g];
+      sum.y += q[g].y * back[g];
+    }
+    if (unlikely(__any_sync(0xFFFFFFFFu, all > kFar || sum.x + sum.y > kFarSum))) {
+      tmem_ld_wait16(next);
+      return c;
+    }
+    z.l = fadd2v(z.l, sum);
+    tmem_st16(tS + c / 2, w);
   }
-  return all > kFar || sum.x + sum.y > kFarSum;
+  return kSub;
 }
 
 template <bool kPrefix, int kBits>
@@ -632,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
             const int j = by_rows ? v >> 1 : (v & ~1) + t, slot = (it + j) % kScaleSlots, sub = (v & 1) * kSub;
             // In this order: a half passes over tiles that are not its own, and only the
             // scores say that the slot's phase before this tile's has ended.
-            ok = wait(&bars.s_full[t][v & 1], (done + v) >> 1) && wait(&bars.scales[slot], (it + j) / kScaleSlots);
+            ok = wait(&bars.s_full[t][v & 1], (done + v) >> 1) && ((v & 1) != 0 || wait(&bars.scales[slot], (it + j) / kScaleSlots));
             if (unlikely(!(ok = __all_sync(0xFFFFFFFFu, ok)))) break;
             tc_fence_after();
             const uint32_t tS = tmem + lanes + col_s(t, 0) + sub;
@@ -650,19 +670,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
             int c = 0;                                     // scores that are done
             const bool all_seen = key0 + kSub <= lo && top < INFINITY;
             if (likely(all_seen && (kBits == 8 || ev.holds()) && !__any_sync(0xFFFFFFFFu, z.f != 1.0f))) {
+              if constexpr (kBits == 4) {
+                c = weigh_even(tS, ev, z);
+              } else {
 #pragma unroll
-              for (int i = 0; i < kSub; i += 32) {
-                uint32_t w[16];
-                float2 sum;
-                bool far;
-                if constexpr (kBits == 4)
-                  far = weigh_even(tS + i, ev, z, w, sum);
-                else
-                  far = weigh<false>(tS + i, kx + i, vx + i, top, 32, z, w, sum);
-                if (unlikely(__any_sync(0xFFFFFFFFu, far))) break;
-                z.l = fadd2v(z.l, sum);
-                tmem_st16(tS + i / 2, w);
-                c = i + 32;
+                for (int i = 0; i < kSub; i += 32) {
+                  uint32_t w[16];
+                  float2 sum;
+                  if (unlikely(__any_sync(0xFFFFFFFFu, weigh<false>(tS + i, kx + i, vx + i, top, 32, z, w, sum)))) break;
+                  z.l = fadd2v(z.l, sum);
+                  tmem_st16(tS + i / 2, w);
+                  c = i + 32;
+                }
               }
             }
 #pragma unroll 1
