@@ -9,9 +9,11 @@
 //
 // A few hundred bytes for a generation step: what it costs is the launch and a chain
 // of loads, sums over the warps and barriers.  One CTA does the sums, 1024 sequences at a
-// time, and the pages of all of them with one search for each; it does the tokens
-// too where they are few, and otherwise a second kernel does, a CTA for each 1024
-// tokens of a sequence at most.
+// time; where tokens are few it does them and the pages too, a search for each (48
+// sequences, one token each: 3.2 us), and otherwise a second kernel does, a CTA or some
+// for a sequence.  Up to 1024 sequences its CTAs find their pages by a sum of their own
+// over what the first has written (256 sequences, 190000 tokens in 12000 new pages:
+// 8.6 us for both; with all pages in the first kernel 16.6).
 #include <algorithm>
 #include <climits>
 #include <cuda_runtime.h>
@@ -72,8 +74,7 @@ __device__ __forceinline__ int above(const long long* v, int n, long long x) {
 }
 
 // -1 where the table or the free list named a page that there is not.
-__device__ __forceinline__ int slot_of(const PagesArgs& a, int b, int pos) {
-  const int page = a.table[b * a.table_stride + (pos >> a.page_shift)];
+__device__ __forceinline__ int slot_in(const PagesArgs& a, int page, int pos) {
   if (page < 0 || page >= a.num_pages) {
     atomicExch(a.err, SAGE_DEVERR_BAD_PAGE);
     return -1;
@@ -81,7 +82,11 @@ __device__ __forceinline__ int slot_of(const PagesArgs& a, int b, int pos) {
   return (page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
 }
 
-__global__ void __launch_bounds__(kThreads) reserve_kernel(const PagesArgs a, int do_tokens) {
+__device__ __forceinline__ int slot_of(const PagesArgs& a, int b, int pos) {
+  return slot_in(a, a.table[b * a.table_stride + (pos >> a.page_shift)], pos);
+}
+
+__global__ void __launch_bounds__(kThreads) reserve_kernel(const PagesArgs a, int do_tokens, int do_pages) {
   __shared__ long long s_upto[kThreads], s_rows[kThreads], part[2][32];
   __shared__ int s_start[kThreads], s_count[kThreads], s_served[kThreads];
   __shared__ long long s_gone;
@@ -128,7 +133,7 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const PagesArgs a, in
     __syncthreads();
     // The pages of these sequences, those of the served.
     const long long total = s_upto[n - 1];
-    for (long long j = tid; j < total && pages_before + j < free; j += kThreads) {
+    for (long long j = tid; do_pages && j < total && pages_before + j < free; j += kThreads) {
       const int i = above(s_upto, n, j);
       if (s_served[i] == 0) break;           // nor is any behind it
       const long long in = j - (i > 0 ? s_upto[i - 1] : 0);
@@ -162,12 +167,14 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const PagesArgs a, in
 }
 
 // Slots and positions of sequence blockIdx.x's tokens; for packed tokens block B has
-// the rows behind the last.
-__global__ void __launch_bounds__(kFillThreads) fill_kernel(const PagesArgs a) {
+// the rows behind the last.  do_pages: and its new pages, which the first kernel has left:
+// a sequence that was served, and it alone, has taken tokens that need some.
+__global__ void __launch_bounds__(kFillThreads) fill_kernel(const PagesArgs a, int do_pages) {
+  __shared__ int s_before, s_all;            // pages of the sequences before this one, of all
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int b = blockIdx.x;
+  const int b = blockIdx.x, tid = threadIdx.x;
   const bool packed = a.layout == kPagesPacked;
-  const int step = gridDim.y * kFillThreads, i0 = blockIdx.y * kFillThreads + threadIdx.x;
+  const int step = gridDim.y * kFillThreads, i0 = blockIdx.y * kFillThreads + tid;
   if (b == a.B) {
     const long long end = static_cast<long long>(a.first[a.B - 1]) + max(0, __ldg(a.counts + a.B - 1));
     for (long long r = end + i0; r < a.tokens; r += step) {
@@ -177,6 +184,32 @@ __global__ void __launch_bounds__(kFillThreads) fill_kernel(const PagesArgs a) {
     return;
   }
   const int count = max(0, __ldg(a.counts + b)), taken = a.taken[b], start = a.start[b];
+  const int page = 1 << a.page_shift;
+  int held = INT_MAX, top = 0;               // the page of index j >= held is free_pages[top - (j - held)]
+  if (do_pages) {                            // the sums are of pages that there are: below 2^31
+    if (tid == 0) s_before = s_all = 0;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int i = tid; i < a.B; i += kFillThreads) {
+      const int t = a.taken[i], n = a.start[i];
+      const int need = t > 0 ? ((n + t + page - 1) >> a.page_shift) - ((n + page - 1) >> a.page_shift) : 0;
+      all += need;
+      before += i < b ? need : 0;
+    }
+    all = __reduce_add_sync(0xFFFFFFFFu, all);
+    before = __reduce_add_sync(0xFFFFFFFFu, before);
+    if ((tid & 31) == 0) {
+      atomicAdd(&s_all, all);
+      atomicAdd(&s_before, before);
+    }
+    __syncthreads();
+    if (taken > 0) {
+      held = (start + page - 1) >> a.page_shift;
+      top = *a.free_left + s_all - 1 - s_before;
+      const int end = (start + taken + page - 1) >> a.page_shift;
+      for (int j = held + i0; j < end; j += step) a.table[b * a.table_stride + j] = __ldg(a.free_pages + (top - (j - held)));
+    }
+  }
   const long long base = packed ? a.first[b] : static_cast<long long>(b) * a.tokens;
   const int skip = a.layout == kPagesEnd ? a.tokens - min(a.tokens, count) : 0;
   const long long rows = packed ? min(static_cast<long long>(count), a.tokens - base) : a.tokens;
@@ -184,7 +217,12 @@ __global__ void __launch_bounds__(kFillThreads) fill_kernel(const PagesArgs a) {
     const long long i = r - skip;
     const bool live = i >= 0 && i < taken;
     const int pos = live ? start + static_cast<int>(i) : 0;
-    a.slots[base + r] = live ? slot_of(a, b, pos) : -1;
+    int slot = -1;
+    if (live) {
+      const int j = pos >> a.page_shift;
+      slot = slot_in(a, j >= held ? __ldg(a.free_pages + (top - (j - held))) : a.table[b * a.table_stride + j], pos);
+    }
+    a.slots[base + r] = slot;
     a.positions[base + r] = pos;
   }
 }
@@ -250,7 +288,8 @@ cudaError_t launch_pages_reserve(const PagesArgs& a, cudaStream_t stream) {
   const bool packed = a.layout == kPagesPacked;
   const int64_t rows = packed ? a.tokens : static_cast<int64_t>(a.tokens) * a.B;
   const bool one = a.B <= kThreads && rows <= kFewTokens;
-  reserve_kernel<<<1, kThreads, 0, stream>>>(a, one ? 1 : 0);
+  const int fill_pages = !one && a.B <= kThreads ? 1 : 0;
+  reserve_kernel<<<1, kThreads, 0, stream>>>(a, one ? 1 : 0, fill_pages ? 0 : 1);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || one) return e;
   const int64_t each = packed ? a.tokens / a.B + 1 : a.tokens;
@@ -264,7 +303,7 @@ cudaError_t launch_pages_reserve(const PagesArgs& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fill_kernel, a);
+  return cudaLaunchKernelEx(&cfg, fill_kernel, a, fill_pages);
 }
 
 cudaError_t launch_pages_release(const ReleaseArgs& a, cudaStream_t stream) {
