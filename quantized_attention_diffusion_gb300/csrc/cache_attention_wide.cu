@@ -32,15 +32,19 @@
 // the second product's A operand from there; V is its B operand with the keys as
 // the outer index, as the cache has it.
 //
-// What bounds it is the path of 128 bytes a clock that shared memory, L1, TMEM loads and
-// stores and the products' operands in shared memory share (l1tex at 60% of its peak and the
-// tensor cores active for 30% of the time beside it), and in tiles of at most 128 rows the conversion, whose
-// loads wait for L1 lines that 200 KB of shared memory leave few of.  2 x 1000 tokens
-// x 16 heads over up to 9000 keys: 212 to 214 us, 585 TFLOP/s, 0.31 of the measured bf16
-// rate (the same rows in mma.sync tiles of 32: 842 us); 24 x 5 tokens x 16 heads behind a
-// prefix of 32760, all in all: 78 us.  With V's scales multiplied into bf16 values the chunk took 183 us, and
-// its outputs were 1.6 times as far from 64 bits.  64 keys a tile (more copies in flight,
-// twice the barriers) took 244 us; TMEM shapes that give a thread four rows, 238 us.
+// What bounds it is the issue of the softmax's and the conversion's instructions (61% of
+// the slots in 4 bits, the tensor cores active for 38% of the time beside it): a warp's 64
+// scores take 1650 of a buffer's 1950 clocks.  2 x 1000 tokens x 16 heads over up to 9000
+// keys: 173 us in 8 bits, 149 us in 4, 0.39 and 0.45 of the measured bf16 rate (per 8000
+// keys more, 108 us in 4 bits, 0.64 of it; the rest is the start, the parts and their
+// merge); 24 x 5 tokens x 16 heads behind a prefix of 32760, all in all: 72 and 73 us.
+// Until its jumps were few (what is rare told to the compiler, the usual path in a line)
+// the 8-bit chunk took 207 us: each jump waits for its instructions, since five kinds of
+// warps share their cache.
+//
+// A 4-bit cache's scales are powers of two: where those of a warp's 32 keys are near one
+// another, one of them stands for all and the values take the rest, exactly, so that the
+// softmax needs no scale a key (Even, below).
 //
 // A row's references move where 32 weights may pass 2^15 in sum, by a whole number:
 // then the thread scales the row's sum, its accumulator and the weights of this

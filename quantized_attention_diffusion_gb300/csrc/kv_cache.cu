@@ -22,6 +22,10 @@
 // 814 MB at 6.3 TB/s, 0.92 of the measured copy rate; 4 x 16384 tokens of 8 heads are read
 // back in 62 us, 0.93 of it.  Small calls cost a launch and three loads in a row (start or
 // length, page, row): 5.6 us for 8 tokens, 4.4 us for 3 x 333 read.
+//
+// In 4 bits (kv_rows.cuh has the formulas) a row is 76 bytes.  Writing it is bound by the
+// issue slots, reading it back by HBM: 4 x up to 16384 tokens of 8 heads 38 us (0.73 of
+// the copy rate) and 49 us (0.94).
 #include <cuda_runtime.h>
 
 #include "kv_rows.cuh"

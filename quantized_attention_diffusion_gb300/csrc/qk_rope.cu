@@ -10,9 +10,12 @@
 // as they are.  The angle of pair i at position p is p * f_i.  F_i = f_i / (2 pi) in
 // 2^-64 stands in the table, so that p * F_i modulo 2^64 is the angle in revolutions
 // with nothing lost, however far the position; its upper half goes to sine and
-// cosine.  x * w is exact in fp32 (both bf16); the norm's factor comes last.
+// cosine.  They take the weights, and the norm's factor comes last.
 //
-// Bound by HBM: 512 bytes a row of Q (and of K to bf16).  Eight lanes take a row, 16
+// Bound by HBM: 512 bytes a row of Q (and of K to bf16): 32760 tokens of 40 + 40 heads
+// 221 us, 6.1 TB/s, 0.90 of the measured copy rate; 17000 packed tokens of 32 + 8 + 8
+// heads into 8 bits 67 us, 0.86.  48 tokens take 3.4 us: a launch, the slot or the
+// position, a row.  Eight lanes take a row, 16
 // channels each, chosen so that a lane holds both channels of its pairs whichever
 // way they are laid out: nothing crosses lanes but the norm's sum.  The sines and
 // cosines of a token, times the weights, are formed once for up to 16 heads of one of
