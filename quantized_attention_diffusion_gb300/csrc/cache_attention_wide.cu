@@ -655,7 +655,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
           for (v = 0; v < nv; ++v) {
             const int j = by_rows ? v >> 1 : (v & ~1) + t, slot = (it + j) % kScaleSlots, sub = (v & 1) * kSub;
             // In this order: a half passes over tiles that are not its own, and only the
-            // scores say that the slot's phase before this tile's has ended.
+            // scores say that the slot's phase before this tile's has ended.  A tile's second
+            // buffer finds the scales that its first has waited for.
             ok = wait(&bars.s_full[t][v & 1], (done + v) >> 1) && ((v & 1) != 0 || wait(&bars.scales[slot], (it + j) / kScaleSlots));
             if (unlikely(!(ok = __all_sync(0xFFFFFFFFu, ok)))) break;
             tc_fence_after();

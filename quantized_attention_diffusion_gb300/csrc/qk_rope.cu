@@ -270,10 +270,10 @@ cudaError_t launch_turn(const TurnArgs& a, cudaStream_t stream) {
   int all = 0;
   for (int per = kMaxHeads;; per = (per + 1) / 2) {
     all = 0;
-    for (int i = 0; i < 3; ++i) all += split.parts[i] = (H[i] + per - 1) / per;
+    for (int i = 0; i < 3; ++i) all += split.parts[i] = H[i] / per + (H[i] % per != 0 ? 1 : 0);
     if (per == 1 || groups * all >= 152 * 16) break;
   }
-  for (int i = 0; i < 3; ++i) split.heads[i] = split.parts[i] == 0 ? 0 : (H[i] + split.parts[i] - 1) / split.parts[i];
+  for (int i = 0; i < 3; ++i) split.heads[i] = split.parts[i] == 0 ? 0 : H[i] / split.parts[i] + (H[i] % split.parts[i] != 0 ? 1 : 0);
   const uint32_t items = static_cast<uint32_t>(groups * all);
   const unsigned ctas = (items + kWarps - 1) / kWarps;
   auto go = [&](auto kernel) {

@@ -58,7 +58,7 @@ class Cache4:
     """A CPU model of a paged 4-bit cache of normal data; NaN scales and blocks and odd
     codes where nothing is written."""
 
-    def __init__(self, lens, H, page, seed, width=None, spare=2, recipe="normal", v_scale=None, extra=()):
+    def __init__(self, lens, H, page, seed, width=None, spare=2, recipe="normal", v_scale=None, k_scale=None, extra=()):
         g = torch.Generator().manual_seed(seed)
         self.lens, self.H, self.page = list(lens), H, page
         need = [-(-n // page) for n in list(lens) + list(extra)]
@@ -84,6 +84,8 @@ class Cache4:
                 k = k * torch.where(torch.rand((n, H, 1), generator=g) < 0.02, 12.0, 1.0)
             if v_scale is not None:
                 v = v * v_scale(n, g)
+            if k_scale is not None:
+                k = k * k_scale(n, g)
             rows = quantize4(k.to(torch.bfloat16)) + quantize4(v.to(torch.bfloat16)) if n else None
             if n:
                 p = self.table[b].long()[torch.arange(n) // page]
