@@ -602,36 +602,31 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
             const int pair = lane >> 4, chunk = lane & 15;
             const uint64_t own = valid ? reinterpret_cast<uint64_t>(walk.query(x, rr)) : 0;
             uint8_t* sQ = smem + kSmemQ + (by_rows ? t * kTileBytes : 0);
-#pragma unroll 1
-            for (int i0 = 0; i0 < 32; i0 += 16) {
-              uint4 w[8];
+            uint4 w[16];                     // all on their way at once
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const uint64_t src = __shfl_sync(0xFFFFFFFFu, own, i0 + 2 * i + pair);
-                w[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (src != 0) w[i] = __ldg(reinterpret_cast<const uint4*>(src) + chunk);
-              }
+            for (int i = 0; i < 16; ++i) {
+              const uint64_t src = __shfl_sync(0xFFFFFFFFu, own, 2 * i + pair);
+              w[i] = make_uint4(0u, 0u, 0u, 0u);
+              if (src != 0) w[i] = __ldg(reinterpret_cast<const uint4*>(src) + chunk);
+            }
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-                uint32_t top = 0u, out[4];
+            for (int i = 0; i < 16; ++i) {
+              const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+              uint32_t out[4];
+              uint32_t two = max_u16x2(max_u16x2(u[0] & 0x7FFF7FFFu, u[1] & 0x7FFF7FFFu), max_u16x2(u[2] & 0x7FFF7FFFu, u[3] & 0x7FFF7FFFu));
 #pragma unroll
-                for (int k = 0; k < 4; ++k) top = max(top, max(u[k] & 0x7FFFu, (u[k] >> 16) & 0x7FFFu));
+              for (int d = 1; d < 16; d <<= 1) two = max_u16x2(two, __shfl_xor_sync(0xFFFFFFFFu, two, d));
+              const uint32_t ex = row_exponent(max(two & 0xFFFFu, two >> 16));
+              const float up = __uint_as_float(ex << 23), back = __uint_as_float((254u - ex) << 23);
+              const float mine = __shfl_sync(0xFFFFFFFFu, back, (lane & 1) << 4);
+              if (lane >> 1 == i) z.rk = mine;
+              if (store) {
 #pragma unroll
-                for (int d = 1; d < 16; d <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                const uint32_t ex = row_exponent(top);
-                const float up = __uint_as_float(ex << 23), back = __uint_as_float((254u - ex) << 23);
-                const float mine = __shfl_sync(0xFFFFFFFFu, back, (lane & 1) << 4);
-                if (lane >> 1 == (i0 >> 1) + i) z.rk = mine;
-                if (store) {
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    const float2 a = unpack_bf16(u[k]);
-                    out[k] = pack_f16(a.x * up, a.y * up);
-                  }
-                  *reinterpret_cast<uint4*>(sQ + tile_offset(quarter * 32 + i0 + 2 * i + pair, chunk)) =
-                      make_uint4(out[0], out[1], out[2], out[3]);
+                for (int k = 0; k < 4; ++k) {
+                  const float2 a = unpack_bf16(u[k]);
+                  out[k] = pack_f16(a.x * up, a.y * up);
                 }
+                *reinterpret_cast<uint4*>(sQ + tile_offset(quarter * 32 + 2 * i + pair, chunk)) = make_uint4(out[0], out[1], out[2], out[3]);
               }
             }
             if (store) {

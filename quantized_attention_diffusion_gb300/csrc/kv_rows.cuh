@@ -23,12 +23,6 @@ __device__ __forceinline__ float2 ffma2v(float2 a, float2 b, float2 c) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
 // -fl(x / sc) of the 8 bf16 values of w, for a scale in [2^-100, 2^125]:
 // Markstein's correction with the negated reciprocal nr = -fl(1 / sc), as in
 // quantize.cu's V encoder.

@@ -380,6 +380,12 @@ __device__ __forceinline__ float2 ffma2_bc(float a0, float a1, float b, float c)
   return r;
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // (a0, a1) * b on the packed FP32 pipe.
 __device__ __forceinline__ float2 fmul2(float a0, float a1, float b) {
   float2 r;
