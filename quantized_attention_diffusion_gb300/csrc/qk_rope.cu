@@ -265,16 +265,17 @@ cudaError_t launch_turn(const TurnArgs& a, cudaStream_t stream) {
   const int bits = a.slots == nullptr ? 0 : a.cache.bits;
   const int H[3] = {a.Hq, a.Hk, bits == 0 ? 0 : a.Hk};
   const int64_t groups = (static_cast<int64_t>(a.B) * a.S + kTokens - 1) / kTokens;
-  // As few sines as the heads allow, but warps for every SM, and parts of like size.
+  // Parts of up to 16 heads, so that there are few sines, or of fewer while all warps are
+  // resident at once (20 on an SM; 2 x 333 tokens of 24 + 24 heads: parts of four 4.8 us, of
+  // two, in two waves, 6.1).
+  const auto parts_of = [&](int per, int i) { return H[i] / per + (H[i] % per != 0 ? 1 : 0); };
+  const auto warps = [&](int per) { return groups * (static_cast<int64_t>(parts_of(per, 0)) + parts_of(per, 1) + parts_of(per, 2)); };
+  int per = kMaxHeads;
+  while (per > 1 && warps(per / 2) <= 152 * 20) per /= 2;
   Split split = {};
-  int all = 0;
-  for (int per = kMaxHeads;; per = (per + 1) / 2) {
-    all = 0;
-    for (int i = 0; i < 3; ++i) all += split.parts[i] = H[i] / per + (H[i] % per != 0 ? 1 : 0);
-    if (per == 1 || groups * all >= 152 * 16) break;
-  }
+  for (int i = 0; i < 3; ++i) split.parts[i] = parts_of(per, i);
   for (int i = 0; i < 3; ++i) split.heads[i] = split.parts[i] == 0 ? 0 : H[i] / split.parts[i] + (H[i] % split.parts[i] != 0 ? 1 : 0);
-  const uint32_t items = static_cast<uint32_t>(groups * all);
+  const uint32_t items = static_cast<uint32_t>(warps(per));
   const unsigned ctas = (items + kWarps - 1) / kWarps;
   auto go = [&](auto kernel) {
     kernel<<<ctas, kWarps * 32, 0, stream>>>(a, split, items);
