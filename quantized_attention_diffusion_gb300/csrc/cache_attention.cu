@@ -840,8 +840,12 @@ enum Before { kNothing, kPrefixTiles, kPrefixParts };
 // sequences in a launch before (kPrefixParts), the join takes that launch's parts in
 // and no merge kernel follows.  What bounds it is one chain of
 // latencies: the length, the pages, the copies, the products, the join.
-template <int ctas, Before kBefore, int kBits>
-__global__ void __cluster_dims__(ctas, 1, 1) __launch_bounds__(kThreads, ctas_per_sm(1))
+//
+// kPerSm: CTAs on an SM, three, or four with a few registers spilled where that saves a
+// second round of them (4 bits behind a prefix of 16384, 4 rows: 64 sequences x 8 heads 46
+// us, of three on an SM 53; 56 sequences, one round either way, 46.8 and 43.9).
+template <int ctas, Before kBefore, int kBits, int kPerSm>
+__global__ void __cluster_dims__(ctas, 1, 1) __launch_bounds__(kThreads, kPerSm)
     cache_attn_cluster_kernel(const Params p, const int32_t* prefix_pages, const PrefixParts parts) {
   constexpr bool kPrefix = kBefore == kPrefixTiles;
   constexpr int R = 8, kStages = stages_of(1, kBits), kTok = tok_of(kBits);
@@ -871,8 +875,11 @@ __global__ void __cluster_dims__(ctas, 1, 1) __launch_bounds__(kThreads, ctas_pe
   }
   __syncthreads();
   const int row0 = rt * R, rows = min(R, p.rows - row0);
-  float4* merge = reinterpret_cast<float4*>(smem + kStages * kStageBytes);
-  const uint8_t* queries = smem + kStages * kStageBytes + kMergeBytes;
+  // The parts are joined where the tiles were, behind the place of this CTA's result.
+  constexpr uint32_t kMergeAt = kBits == 8 ? kStages * kStageBytes : R * kHeadDim * 4, kQueriesAt = kStages * kStageBytes + (kBits == 8 ? kMergeBytes : 0);
+  static_assert(kBits == 8 || kMergeAt + kMergeBytes <= kStages * kStageBytes, "room for the parts");
+  float4* merge = reinterpret_cast<float4*>(smem + kMergeAt);
+  const uint8_t* queries = smem + kQueriesAt;
   const uint32_t smem0 = smem_addr(smem);
 
   if (warp == kConsumers) {
@@ -883,7 +890,7 @@ __global__ void __cluster_dims__(ctas, 1, 1) __launch_bounds__(kThreads, ctas_pe
     if (lane == 0) mbar_arrive_expect_tx(&q_full, rows * kHeadDim * 2);
     __syncwarp();
     if (lane < rows)
-      bulk_load(smem0 + kStages * kStageBytes + kMergeBytes + lane * kHeadDim * 2,
+      bulk_load(smem0 + kQueriesAt + lane * kHeadDim * 2,
                 p.q + b * p.q_sb + ((row0 + lane) / p.G) * p.q_ss + (h * p.G + (row0 + lane) % p.G) * kHeadDim, kHeadDim * 2, smem_addr(&q_full));
     // The page of this lane's run of tile t, wherever the sequence ends: on its way
     // before its length is known.
@@ -1369,13 +1376,23 @@ cudaError_t launch_clusters(const CacheAttnArgs& a, int ctas, const PrefixParts*
   p.err = a.err;
   auto go = [&](auto size, auto bits) {
     constexpr int kCtas = decltype(size)::value, kBits = decltype(bits)::value;
-    constexpr uint32_t smem = smem_of<kBits>(1);
-    static std::atomic<uint64_t> allowed[3];           // for each kernel
+    constexpr uint32_t smem = smem_of<kBits>(1) - (kBits == 8 ? 0 : kMergeBytes);
+    static std::atomic<uint64_t> allowed[4];           // for each kernel
     const int which = parts != nullptr ? kPrefixParts : a.prefix_len > 0 ? kPrefixTiles : kNothing;
-    auto kernel = which == kPrefixParts   ? cache_attn_cluster_kernel<kCtas, kPrefixParts, kBits>
-                  : which == kPrefixTiles ? cache_attn_cluster_kernel<kCtas, kPrefixTiles, kBits>
-                                          : cache_attn_cluster_kernel<kCtas, kNothing, kBits>;
-    const cudaError_t e = allow_smem(kernel, smem, allowed[which]);
+    constexpr int kPerSm = ctas_per_sm(1);
+    auto kernel = which == kPrefixParts   ? cache_attn_cluster_kernel<kCtas, kPrefixParts, kBits, kPerSm>
+                  : which == kPrefixTiles ? cache_attn_cluster_kernel<kCtas, kPrefixTiles, kBits, kPerSm>
+                                          : cache_attn_cluster_kernel<kCtas, kNothing, kBits, kPerSm>;
+    int kind = which;
+    if constexpr (kCtas == 1 && kBits == 4) {
+      const int64_t all = static_cast<int64_t>(a.B) * p.row_tiles * a.cache.H;
+      const auto rounds = [&](int per_sm) { return (all + per_sm * kSms - 1) / (per_sm * kSms); };
+      if (which == kPrefixParts && rounds(kPerSm + 1) < rounds(kPerSm)) {
+        kernel = cache_attn_cluster_kernel<1, kPrefixParts, 4, kPerSm + 1>;
+        kind = 3;
+      }
+    }
+    const cudaError_t e = allow_smem(kernel, smem, allowed[kind]);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.B) * p.row_tiles * a.cache.H * kCtas);

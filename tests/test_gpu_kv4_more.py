@@ -181,3 +181,20 @@ def test_a_generation_step_of_two_requests_that_share_pages():
         vc, vb, vs = quantize4(vv)
         ref, _, tol, _ = reference(q[b], (values4(kc, kb), ks.double(), values4(vc, vb), vs.double()), True, SCALE)
         assert_within(out[b], ref, tol)
+
+
+@pytest.mark.parametrize("B,H,prefix", [(60, 8, 3000), (40, 8, 3000), (80, 8, 2500)])
+def test_many_sequences_behind_a_prefix(B, H, prefix):
+    """A unit for each sequence and head: more than fit an SM three at a time, fewer, and
+    more than fit four at a time."""
+    import quantized_attention_diffusion_gb300 as qad
+    from tests.cache_common import join
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, 90, (B,), generator=g).tolist()
+    cache = Cache4(lens, H, 16, seed=B, extra=(prefix,))
+    q = randn(B, B, 1, 2 * H, D)
+    table = cache.table.cuda()
+    width = max(1, -(-max(lens) // 16))
+    out, lse = qad.attn_fwd_cache_prefix(q.cuda(), cache.gpu(), table[B, :-(-prefix // 16)].contiguous(), prefix,
+                                         table[:B, :width].contiguous(), ints(lens), return_lse=True)
+    check(cache, q, out, lse, True, lambda b: join(cache.dense(B), cache.dense(b)))
