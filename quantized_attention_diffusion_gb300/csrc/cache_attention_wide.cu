@@ -609,18 +609,29 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
               w[i] = make_uint4(0u, 0u, 0u, 0u);
               if (src != 0) w[i] = __ldg(reinterpret_cast<const uint4*>(src) + chunk);
             }
+            // The largest magnitudes of 16 rows over 16 lanes: each step halves the rows that a
+            // lane has in hand, until lane `chunk` has row 2 chunk + pair.
+            uint32_t two[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              two[i] = max_u16x2(max_u16x2(w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu), max_u16x2(w[i].z & 0x7FFF7FFFu, w[i].w & 0x7FFF7FFFu));
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1) {
+              const bool high = (lane & d) != 0;
+#pragma unroll
+              for (int i = 0; i < d; ++i) {
+                const uint32_t give = high ? two[i] : two[i + d], keep = high ? two[i + d] : two[i];
+                two[i] = max_u16x2(keep, __shfl_xor_sync(0xFFFFFFFFu, give, d));
+              }
+            }
+            const uint32_t ex = row_exponent(max(two[0] & 0xFFFFu, two[0] >> 16));
+            z.rk = __uint_as_float((254u - __shfl_sync(0xFFFFFFFFu, ex, ((lane & 1) << 4) | (lane >> 1))) << 23);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-              uint32_t out[4];
-              uint32_t two = max_u16x2(max_u16x2(u[0] & 0x7FFF7FFFu, u[1] & 0x7FFF7FFFu), max_u16x2(u[2] & 0x7FFF7FFFu, u[3] & 0x7FFF7FFFu));
-#pragma unroll
-              for (int d = 1; d < 16; d <<= 1) two = max_u16x2(two, __shfl_xor_sync(0xFFFFFFFFu, two, d));
-              const uint32_t ex = row_exponent(max(two & 0xFFFFu, two >> 16));
-              const float up = __uint_as_float(ex << 23), back = __uint_as_float((254u - ex) << 23);
-              const float mine = __shfl_sync(0xFFFFFFFFu, back, (lane & 1) << 4);
-              if (lane >> 1 == i) z.rk = mine;
+              const float up = __uint_as_float(__shfl_sync(0xFFFFFFFFu, ex, (lane & 16) | i) << 23);
               if (store) {
+                const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                uint32_t out[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                   const float2 a = unpack_bf16(u[k]);
