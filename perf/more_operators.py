@@ -472,8 +472,8 @@ def _run_own(s):
     case, op = s["case"], s["case"]["op"]
     if op == "pages":
         r = qad.kv_pages_reserve(s["free_pages"], s["free_count"], s["lens"], s["counts"], s["table"], case["page"], s["tokens"], case["layout"])
-        return dict(start=r.start, taken=r.taken, lens=r.lens, free_count=r.free_count, table=s["table"], slots=r.slots.view(-1),
-                    positions=r.positions.view(-1))
+        slots, positions = (r.slots, r.positions) if case["layout"] == "packed" else (r.slots.view(-1), r.positions.view(-1))
+        return dict(start=r.start, taken=r.taken, lens=r.lens, free_count=r.free_count, table=s["table"], slots=slots, positions=positions)
     if op == "rope":
         return qad.qk_norm_rope(s["q"], s["k"], s["rope"], s["positions"], q_weight=s["q_weight"], k_weight=s["k_weight"],
                                 eps=EPS if case["norm"] else None)
