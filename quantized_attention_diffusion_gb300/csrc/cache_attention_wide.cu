@@ -35,9 +35,9 @@
 // What bounds it is the issue of the softmax's and the conversion's instructions (61% of
 // the slots in 4 bits, the tensor cores active for 38% of the time beside it): a warp's 64
 // scores take 1650 of a buffer's 1950 clocks.  2 x 1000 tokens x 16 heads over up to 9000
-// keys: 173 us in 8 bits, 149 us in 4, 0.39 and 0.45 of the measured bf16 rate (per 8000
+// keys: 173 us in 8 bits, 147 us in 4, 0.39 and 0.46 of the measured bf16 rate (per 8000
 // keys more, 108 us in 4 bits, 0.64 of it; the rest is the start, the parts and their
-// merge); 24 x 5 tokens x 16 heads behind a prefix of 32760, all in all: 72 and 73 us.
+// merge); 24 x 5 tokens x 16 heads behind a prefix of 32760, all in all: 70 and 69 us.
 // Until its jumps were few (what is rare told to the compiler, the usual path in a line)
 // the 8-bit chunk took 207 us: each jump waits for its instructions, since five kinds of
 // warps share their cache.
