@@ -12,7 +12,7 @@
 // time; where tokens are few it does them and the pages too, a search for each (48
 // sequences, one token each: 3.2 us), and otherwise a second kernel does, a CTA or some
 // for a sequence.  Up to 1024 sequences its CTAs find their pages by a sum of their own
-// over what the first has written (256 sequences, 190000 tokens in 12000 new pages:
+// over what the first has written (256 sequences, 200000 tokens in 12000 new pages:
 // 8.6 us for both; with all pages in the first kernel 16.6).
 #include <algorithm>
 #include <climits>

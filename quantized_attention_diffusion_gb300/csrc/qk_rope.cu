@@ -13,8 +13,8 @@
 // cosine.  They take the weights, and the norm's factor comes last.
 //
 // Bound by HBM: 512 bytes a row of Q (and of K to bf16): 32760 tokens of 40 + 40 heads
-// 221 us, 6.1 TB/s, 0.90 of the measured copy rate; 17000 packed tokens of 32 + 8 + 8
-// heads into 8 bits 67 us, 0.86.  48 tokens take 3.6 us: a launch, the slot or the
+// 221 us, 6.1 TB/s, 0.90 of the measured copy rate; 15000 packed tokens of 32 + 8 + 8
+// heads into 8 bits 67 us, 0.74.  48 tokens take 3.6 us: a launch, the slot or the
 // position, a row.  Eight lanes take a row, 16
 // channels each, chosen so that a lane holds both channels of its pairs whichever
 // way they are laid out: nothing crosses lanes but the norm's sum.  The sines and
