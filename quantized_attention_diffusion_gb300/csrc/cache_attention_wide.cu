@@ -76,6 +76,7 @@ constexpr float kFar = 32768.0f;                        // 2^15: most of 32 weig
 constexpr float kAbove = 6.0f;                          // a reference that moves goes so far below the largest weight:
                                                         // 32 of that are a sixteenth of kFar
 constexpr float kFarSum = 0x1p70f, kTiny = 0x1p-55f;    // most of 32 p's sum, and kFar / kFarSum
+constexpr float kNear = 4096.0f;                        // most of |R| in weigh_even
 constexpr float kReach = 60.0f, kReachV = 140.0f;       // of R, and of R + D, below the largest score
 
 constexpr int kSub = 64;                                // keys of a score buffer
@@ -307,9 +308,11 @@ struct Even {
   __device__ bool holds() const { return fminf(fminf(fminf(k.x, k.y), fminf(k.z, k.w)), fminf(fminf(v.x, v.y), fminf(v.z, v.w))) > 0.0f; }
 };
 
-// weigh of a buffer's 64 scores where that holds and the row sees all of the keys:
-// weights 2^(x + log2 v - R) at once, and L's p from their sums, since the scales are
-// powers of two.  Five instructions for two scores where the arrays of scales take eight
+// weigh of a buffer's 64 scores where that holds, the row sees all of the keys and R is
+// near: weights 2^(x + log2 v - R) at once, and L's p from their sums, since the scales are
+// powers of two.  The product in x is not rounded by itself, as weigh and R have it, and log2 v
+// joins R first: of an R up to kNear the first is 2^-12 of log2 at the most and the second
+// exact, and rows farther out take weigh.  Five instructions for two scores where the arrays of scales take eight
 // and a load; the next 16 scores are loaded meanwhile.  -> scores whose weights are
 // stored: 64, or fewer where the references have to move first.
 __device__ __forceinline__ int weigh_even(uint32_t tS, const Even& ev, Row& z) {
@@ -680,7 +683,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
             const float *kx = s_ks[slot] + sub, *vx = s_vs[slot] + sub;
             int c = 0;                                     // scores that are done
             const bool all_seen = key0 + kSub <= lo && top < INFINITY;
-            if (likely(all_seen && (kBits == 8 || ev.holds()) && !__any_sync(0xFFFFFFFFu, z.f != 1.0f))) {
+            const bool usual = z.f == 1.0f && (kBits == 8 || fabsf(z.R) <= kNear);
+            if (likely(all_seen && (kBits == 8 || ev.holds()) && __all_sync(0xFFFFFFFFu, usual))) {
               if constexpr (kBits == 4) {
                 c = weigh_even(tS, ev, z);
               } else {
