@@ -77,6 +77,7 @@ constexpr float kAbove = 6.0f;                          // a reference that move
                                                         // 32 of that are a sixteenth of kFar
 constexpr float kFarSum = 0x1p70f, kTiny = 0x1p-55f;    // most of 32 p's sum, and kFar / kFarSum
 constexpr float kNear = 4096.0f;                        // most of |R| in weigh_even
+constexpr float kLarge = 0x1p60f;                       // most of a row's factor and of K's scale there: their product is finite
 constexpr float kReach = 60.0f, kReachV = 140.0f;       // of R, and of R + D, below the largest score
 
 constexpr int kSub = 64;                                // keys of a score buffer
@@ -517,7 +518,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
         const int s = it & 1, round = it >> 1;
         // In 4 bits a warp's 32 keys get the largest of their scales, and the values the
         // rest, where that is a power of two down to 2^-14 for all of them.  Rows of zeros in
-        // V alone have no scale that could stand for theirs in the references.
+        // V alone have no scale that could stand for theirs in the references.  K's may not be
+        // so large that it could not be multiplied by a row's factor first.
         uint32_t ratio = 0x3C003C00u;
         if constexpr (kBits == 4) {
           const uint32_t bits = __float_as_uint(scale);
@@ -530,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
             scale = __uint_as_float(top);
           }
           if (is_v && lane == 0) s_even[1][it % kScaleSlots][warp & 3] = even ? scale : -1.0f;
-          if (!is_v) even_k = even ? scale * p.c_scale : -1.0f;
+          if (!is_v) even_k = even && scale * p.c_scale <= kLarge ? scale * p.c_scale : -1.0f;
         }
         // V's scales may be written before its stage is free: the tile that last
         // used the slot has been multiplied.
@@ -683,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
             const float *kx = s_ks[slot] + sub, *vx = s_vs[slot] + sub;
             int c = 0;                                     // scores that are done
             const bool all_seen = key0 + kSub <= lo && top < INFINITY;
-            const bool usual = z.f == 1.0f && (kBits == 8 || fabsf(z.R) <= kNear);
+            const bool usual = z.f == 1.0f && (kBits == 8 || (fabsf(z.R) <= kNear && z.rk <= kLarge));
             if (likely(all_seen && (kBits == 8 || ev.holds()) && __all_sync(0xFFFFFFFFu, usual))) {
               if constexpr (kBits == 4) {
                 c = weigh_even(tS, ev, z);

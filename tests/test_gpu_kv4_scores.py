@@ -121,3 +121,16 @@ def test_equal_scores_of_any_size(path, size, power, sign):
         x[which, :, 0] *= 0.5 if sign < 0 else 2.0                # the largest score is that key's alone
         out, _ = Keys(path, x, v).attend(q)
         assert_out(out, v[which], G, size, f"key {which}")
+
+
+@pytest.mark.parametrize("power", [60, 76, 90, 100, 116])
+@pytest.mark.parametrize("path", PATHS)
+def test_rows_of_any_size_at_right_angles(path, power):
+    """Rows of Q and K of about 2^power whose products are zero: the mean of V."""
+    G, H, n, prefix = path[2], path[3], path[4], path[6]
+    k = torch.zeros((prefix + n, H, D), dtype=torch.float64)
+    k[..., 0] = ODD * 2.0 ** (power - 2)
+    v = signs(path, power, 0.75)
+    out, lse = Keys(path, k, v).attend(queries(path, 1, 2.0 ** power))
+    assert_out(out, v.mean(0), G, 0.75, "all equal")
+    assert float((lse.double().cpu() - math.log(prefix + n)).abs().max()) <= 2.0 ** -10
