@@ -77,6 +77,7 @@ constexpr float kAbove = 6.0f;                          // a reference that move
                                                         // 32 of that are a sixteenth of kFar
 constexpr float kFarSum = 0x1p70f, kTiny = 0x1p-55f;    // most of 32 p's sum, and kFar / kFarSum
 constexpr float kNear = 4096.0f;                        // most of |R| in weigh_even
+constexpr float kSmall = 0x1p-70f;                      // least of L times V's scale there
 constexpr float kLarge = 0x1p60f;                       // most of a row's factor and of K's scale there: their product is finite
 constexpr float kReach = 60.0f, kReachV = 140.0f;       // of R, and of R + D, below the largest score
 
@@ -306,14 +307,17 @@ __device__ __forceinline__ bool weigh(uint32_t tS, const float* kx, const float*
 // values; negative where the rows' scales were too far apart for that.
 struct Even {
   float4 k, v;
-  __device__ bool holds() const { return fminf(fminf(fminf(k.x, k.y), fminf(k.z, k.w)), fminf(fminf(v.x, v.y), fminf(v.z, v.w))) > 0.0f; }
+  __device__ float least_k() const { return fminf(fminf(k.x, k.y), fminf(k.z, k.w)); }
+  __device__ float least_v() const { return fminf(fminf(v.x, v.y), fminf(v.z, v.w)); }
 };
 
-// weigh of a buffer's 64 scores where that holds, the row sees all of the keys and R is
+// weigh of a buffer's 64 scores where those are positive, the row sees all of the keys and R is
 // near: weights 2^(x + log2 v - R) at once, and L's p from their sums, since the scales are
 // powers of two.  The product in x is not rounded by itself, as weigh and R have it, and log2 v
 // joins R first: of an R up to kNear the first is 2^-12 of log2 at the most and the second
-// exact, and rows farther out take weigh.  Five instructions for two scores where the arrays of scales take eight
+// exact, and rows farther out take weigh.  So do rows whose L times the smallest v is below
+// kSmall: a weight below 2^-126 is 0, and the p that L then lacks is less than 2^-126 / v,
+// 2^-56 of L (2^30 keys: 2^-26).  Five instructions for two scores where the arrays of scales take eight
 // and a load; the next 16 scores are loaded meanwhile.  -> scores whose weights are
 // stored: 64, or fewer where the references have to move first.
 __device__ __forceinline__ int weigh_even(uint32_t tS, const Even& ev, Row& z) {
@@ -685,8 +689,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
             const float *kx = s_ks[slot] + sub, *vx = s_vs[slot] + sub;
             int c = 0;                                     // scores that are done
             const bool all_seen = key0 + kSub <= lo && top < INFINITY;
-            const bool usual = z.f == 1.0f && (kBits == 8 || (fabsf(z.R) <= kNear && z.rk <= kLarge));
-            if (likely(all_seen && (kBits == 8 || ev.holds()) && __all_sync(0xFFFFFFFFu, usual))) {
+            bool usual = z.f == 1.0f;
+            if constexpr (kBits == 4)
+              usual = usual && ev.least_k() > 0.0f && fabsf(z.R) <= kNear && z.rk <= kLarge && (z.l.x + z.l.y) * ev.least_v() >= kSmall;
+            if (likely(all_seen && __all_sync(0xFFFFFFFFu, usual))) {
               if constexpr (kBits == 4) {
                 c = weigh_even(tS, ev, z);
               } else {

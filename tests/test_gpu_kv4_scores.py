@@ -134,3 +134,23 @@ def test_rows_of_any_size_at_right_angles(path, power):
     out, lse = Keys(path, k, v).attend(queries(path, 1, 2.0 ** power))
     assert_out(out, v.mean(0), G, 0.75, "all equal")
     assert float((lse.double().cpu() - math.log(prefix + n)).abs().max()) <= 2.0 ** -10
+
+
+@pytest.mark.parametrize("near,far", [(4, -126), (4, -121), (20, -100), (0, -90), (-11, -126), (60, -40), (-60, -126), (100, -20)])
+@pytest.mark.parametrize("path", PATHS)
+def test_values_far_below_others_keep_their_probability(path, near, far):
+    """The first 64 keys have scores of 0 and V of 1536 2^near, all others scores of -3.375
+    (4.9 in log2) and V of 1536 2^far, which adds nothing to an output but to the sum of
+    the probabilities that it is divided by."""
+    G, H, n, prefix = path[2], path[3], path[4], path[6]
+    total = prefix + n
+    k = torch.zeros((total, H, D), dtype=torch.float64)
+    k[64:, :, 0] = ODD
+    v = torch.full((total, H, D), 1536.0 * 2.0 ** far, dtype=torch.float64)
+    v[:64] = 1536.0 * 2.0 ** near
+    out, lse = Keys(path, k, v).attend(queries(path, 0, -1.0))
+    L = 64.0 + (total - 64) * math.exp(-0.5 * ODD)
+    want = (64.0 * v[0] + (total - 64) * math.exp(-0.5 * ODD) * v[64]) / L
+    # bf16, the weights' fp16, and sums as above
+    assert float((out.double().cpu() / want.repeat_interleave(G, dim=0) - 1).abs().max()) <= 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -12
+    assert float((lse.double().cpu() - math.log(L)).abs().max()) <= 2.0 ** -10
