@@ -5,7 +5,8 @@
 // ceil((len + count) / page) - held more.  With upto_b the sum of need over sequences
 // 0 .. b, the sequences with need = 0 or upto_b <= free are served: page j of b is
 // entry free - 1 - (upto_b - need_b) - j of the free list, a stack.  Taking back puts
-// pages where this found them, in the same order.
+// pages where this found them, in the same order.  Of packed tokens a sequence's have to
+// have rows as well; behind one that has too few none is served that has tokens.
 //
 // A few hundred bytes for a generation step: what it costs is the launch and a chain
 // of loads, sums over the warps and barriers.  One CTA does the sums, 1024 sequences at a
@@ -73,6 +74,9 @@ __device__ __forceinline__ int above(const long long* v, int n, long long x) {
   return lo;
 }
 
+// The rows that a sequence's tokens take, served or not: none of a count that is not one.
+__device__ __forceinline__ int rows_of(const PagesArgs& a, int count) { return count >= 0 && count <= a.tokens ? count : 0; }
+
 // -1 where the table or the free list named a page that there is not.
 __device__ __forceinline__ int slot_in(const PagesArgs& a, int page, int pos) {
   if (page < 0 || page >= a.num_pages) {
@@ -105,16 +109,17 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const PagesArgs a, in
     if (b < a.B) {
       len = a.lens[b];
       count = __ldg(a.counts + b);
-      fits = len >= 0 && count >= 0 && static_cast<long long>(len) + count <= a.room && (a.layout == kPagesPacked || count <= a.tokens);
+      fits = len >= 0 && count >= 0 && static_cast<long long>(len) + count <= a.room && count <= a.tokens;
       if (!fits) bad = true;
     }
     const int held = fits ? (len + page - 1) >> a.page_shift : 0;
     const int need = fits ? ((len + count + page - 1) >> a.page_shift) - held : 0;
-    long long upto = need, rows = max(0, count);
+    long long upto = need, rows = rows_of(a, count);
     __syncthreads();                         // the arrays of the sequences before have been read
     block_sums(upto, rows, part);
-    const bool served = fits && (need == 0 || pages_before + upto <= free);
-    if (b < a.B && fits && !served) atomicExch(a.err, SAGE_DEVERR_NO_PAGES);
+    const bool has_rows = a.layout != kPagesPacked || count == 0 || rows_before + rows <= a.tokens;
+    const bool served = fits && has_rows && (need == 0 || pages_before + upto <= free);
+    if (b < a.B && fits && has_rows && !served) atomicExch(a.err, SAGE_DEVERR_NO_PAGES);
     s_upto[tid] = upto;
     s_rows[tid] = rows;
     s_start[tid] = len;
@@ -125,8 +130,8 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const PagesArgs a, in
       a.start[b] = len;
       a.taken[b] = taken;
       a.new_lens[b] = len + taken;
-      const long long at = a.layout == kPagesPacked ? rows_before + rows - max(0, count)
-                                                    : static_cast<long long>(b) * a.tokens + (a.layout == kPagesEnd ? a.tokens - min(a.tokens, max(0, count)) : 0);
+      const long long at = a.layout == kPagesPacked ? rows_before + rows - rows_of(a, count)
+                                                    : static_cast<long long>(b) * a.tokens + (a.layout == kPagesEnd ? a.tokens - rows_of(a, count) : 0);
       a.first[b] = static_cast<int>(min(at, static_cast<long long>(INT_MAX)));
       if (served && need > 0) atomicMax(&s_gone, pages_before + upto);
     }
@@ -156,7 +161,7 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const PagesArgs a, in
         i = b < a.B ? r - static_cast<int>(b > 0 ? s_rows[b - 1] : 0) : 0;
       } else {
         b = r / a.tokens;
-        i = r - b * a.tokens - (a.layout == kPagesEnd ? a.tokens - s_count[b] : 0);
+        i = r - b * a.tokens - (a.layout == kPagesEnd ? a.tokens - rows_of(a, s_count[b]) : 0);
       }
       const bool live = b < a.B && s_served[b] != 0 && i >= 0 && i < s_count[b];
       const int pos = live ? s_start[b] + i : 0;
@@ -176,14 +181,14 @@ __global__ void __launch_bounds__(kFillThreads) fill_kernel(const PagesArgs a, i
   const bool packed = a.layout == kPagesPacked;
   const int step = gridDim.y * kFillThreads, i0 = blockIdx.y * kFillThreads + tid;
   if (b == a.B) {
-    const long long end = static_cast<long long>(a.first[a.B - 1]) + max(0, __ldg(a.counts + a.B - 1));
+    const long long end = static_cast<long long>(a.first[a.B - 1]) + rows_of(a, __ldg(a.counts + a.B - 1));
     for (long long r = end + i0; r < a.tokens; r += step) {
       a.slots[r] = -1;
       a.positions[r] = 0;
     }
     return;
   }
-  const int count = max(0, __ldg(a.counts + b)), taken = a.taken[b], start = a.start[b];
+  const int count = rows_of(a, __ldg(a.counts + b)), taken = a.taken[b], start = a.start[b];
   const int page = 1 << a.page_shift;
   int held = INT_MAX, top = 0;               // the page of index j >= held is free_pages[top - (j - held)]
   if (do_pages) {                            // the sums are of pages that there are: below 2^31
@@ -211,7 +216,7 @@ __global__ void __launch_bounds__(kFillThreads) fill_kernel(const PagesArgs a, i
     }
   }
   const long long base = packed ? a.first[b] : static_cast<long long>(b) * a.tokens;
-  const int skip = a.layout == kPagesEnd ? a.tokens - min(a.tokens, count) : 0;
+  const int skip = a.layout == kPagesEnd ? a.tokens - count : 0;
   const long long rows = packed ? min(static_cast<long long>(count), a.tokens - base) : a.tokens;
   for (long long r = i0; r < rows; r += step) {
     const long long i = r - skip;

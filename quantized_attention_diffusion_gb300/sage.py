@@ -1011,8 +1011,9 @@ def kv_pages_reserve(free_pages, free_count, lens, counts, block_table, page_siz
     and positions (sage_kv_pages_reserve).  ``layout``: "packed" tokens one behind
     another, ``tokens`` in all, or [B, tokens] with a sequence's at the "front" or
     the "end" of its row.  Sequences for which there are too few pages get none (taken
-    0), and sync_status reports SAGE_ERR_NO_PAGES.  ``out``: the PagePlan to fill, of
-    which lens and free_count may be the arguments."""
+    0), and sync_status reports SAGE_ERR_NO_PAGES; those for whose tokens there are too
+    few rows SAGE_ERR_BAD_PAGE.  ``out``: the PagePlan to fill, of which lens and
+    free_count may be the arguments."""
     lib = _lib or load_library()
     num_pages, B, dev = _check_free(free_pages, free_count, lens, page_size)
     _check_ints("counts", counts, B, dev)

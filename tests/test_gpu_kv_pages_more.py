@@ -1,0 +1,91 @@
+"""What kv_pages_reserve and kv_pages_release do with what is wrong on the device: tokens
+without a row, errors that are pending, table entries that are no pages."""
+import random
+
+import pytest
+import torch
+
+from tests.cache_common import ints
+from tests.gpu_common import ensure_library
+
+pytestmark = pytest.mark.gpu
+PAGE = 16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    return ensure_library()
+
+
+@pytest.fixture(autouse=True)
+def no_device_error():
+    import quantized_attention_diffusion_gb300 as qad
+    yield
+    assert qad.sync_status() == 0
+
+
+def pages_of(n):
+    return -(-n // PAGE)
+
+
+# One kernel; two; two of which the first finds the pages.
+@pytest.mark.parametrize("B,new,rows", [(5, 9, 0.6), (300, 40, 0.5), (300, 90, 0.7), (1024, 20, 0.99), (1500, 30, 0.5), (2500, 3, 0.0)])
+def test_packed_tokens_without_a_row_are_not_served(B, new, rows):
+    """Sequences are served while their tokens have rows; one whose count alone is above
+    `tokens` takes none, as one with a negative count."""
+    import quantized_attention_diffusion_gb300 as qad
+    r = random.Random(B + new)
+    lens = [r.randint(0, 50) for _ in range(B)]
+    counts = [r.randint(0, new) for _ in range(B)]
+    tokens = max(new, int(rows * sum(counts)))
+    for b in (2, B // 3):
+        counts[b] = r.choice([-1, tokens + 1, tokens + 500])
+    counts[B // 4] = 0
+    width = pages_of(max(50 + max(counts), 1))
+    need = sum(pages_of(n + max(c, 0)) for n, c in zip(lens, counts))
+    pool = list(range(need + 3))
+    r.shuffle(pool)
+    table, at = [], 0
+    for n in lens:
+        table.append(pool[at:at + pages_of(n)] + [-1] * (width - pages_of(n)))
+        at += pages_of(n)
+    free, stack = len(pool) - at, pool[at:] + [-7] * at
+
+    want_table, taken, first, slots, positions = [list(x) for x in table], [], [], [-1] * tokens, [0] * tokens
+    row, gone = 0, 0
+    for b, (n, c) in enumerate(zip(lens, counts)):
+        takes = c if 0 <= c <= tokens else 0
+        ok = 0 <= c <= tokens and (c == 0 or row + c <= tokens)
+        first.append(row)
+        taken.append(c if ok else 0)
+        if ok:
+            for j in range(pages_of(n), pages_of(n + c)):
+                want_table[b][j] = stack[free - 1 - gone]
+                gone += 1
+            for i in range(c):
+                slots[row + i] = want_table[b][(n + i) // PAGE] * PAGE + (n + i) % PAGE
+                positions[row + i] = n + i
+        row += takes
+    assert row > tokens and sum(taken) <= tokens
+
+    t = torch.tensor(table, dtype=torch.int32, device="cuda")
+    got = qad.kv_pages_reserve(ints(stack), ints([free]), ints(lens), ints(counts), t, PAGE, tokens)
+    assert qad.sync_status() == 8
+    assert got.taken.tolist() == taken and got.first.tolist() == first
+    assert got.lens.tolist() == [n + c for n, c in zip(lens, taken)]
+    assert got.free_count.tolist() == [free - gone]
+    assert t.tolist() == want_table
+    assert got.slots.tolist() == slots and got.positions.tolist() == positions
+
+
+def test_a_batch_whose_rows_are_just_enough_or_one_too_few():
+    import quantized_attention_diffusion_gb300 as qad
+    for tokens, taken, left in ((6, [3, 0, 3], 2), (5, [3, 0, 0], 3), (3, [3, 0, 0], 3), (2, [0, 0, 0], 4)):
+        table = torch.full((3, 2), -1, dtype=torch.int32, device="cuda")
+        got = qad.kv_pages_reserve(ints([0, 1, 2, 3]), ints([4]), ints([0] * 3), ints([3, 0, 3]), table, PAGE, tokens)
+        assert qad.sync_status() == (0 if tokens == 6 else 8)
+        assert got.taken.tolist() == taken and got.lens.tolist() == taken and got.free_count.tolist() == [left]
+        assert [x[0] for x in table.tolist()] == [3 if taken[0] else -1, -1, 2 if taken[2] else -1]
+        assert got.slots.tolist() == ([48, 49, 50] if taken[0] else [-1] * min(3, tokens)) + ([32, 33, 34] if taken[2] else [-1] * max(0, tokens - 3))
