@@ -632,12 +632,12 @@ enum { SAGE_TOKENS_PACKED = 0, SAGE_TOKENS_FRONT = 1, SAGE_TOKENS_END = 2 };
  * sequences before it need are free together; page j that it takes is
  * free_pages[free_count - 1 - (pages that those before it need) - j].  Where one is not
  * served its table and length stay, and sage_sync_status() reports
- * SAGE_ERR_NO_PAGES.  A negative length, a count that is negative or above `tokens`
- * (it takes no rows), more positions than the table has room for or than 2^30, packed
- * tokens behind the last row (from the first sequence that has some there on none is
- * served that gets tokens), a free_count out of range or a page that is not one is
- * reported as SAGE_ERR_BAD_PAGE; such a sequence (token, page) is not served (has
- * slot -1), and nothing out of bounds is touched.
+ * SAGE_ERR_NO_PAGES, unless another error is pending.  A negative length, a count
+ * that is negative or above `tokens` (it takes no rows), more positions than the table
+ * has room for or than 2^30, packed tokens behind the last row (from the first sequence
+ * that has some there on none is served that gets tokens), a free_count out of range or
+ * a page that is not one is reported as SAGE_ERR_BAD_PAGE; such a sequence (token, page)
+ * is not served (has slot -1), and nothing out of bounds is touched.
  * One or two launches.  B <= 2^20.  Errors: INVALID_ARG, UNSUPPORTED (page_size,
  * layout), MISALIGNED, CUDA.
  */

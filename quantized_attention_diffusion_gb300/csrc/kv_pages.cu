@@ -119,7 +119,8 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const PagesArgs a, in
     block_sums(upto, rows, part);
     const bool has_rows = a.layout != kPagesPacked || count == 0 || rows_before + rows <= a.tokens;
     const bool served = fits && has_rows && (need == 0 || pages_before + upto <= free);
-    if (b < a.B && fits && has_rows && !served) atomicExch(a.err, SAGE_DEVERR_NO_PAGES);
+    // Ordinary, and told by `taken`: in the place of no error that is pending.
+    if (b < a.B && fits && has_rows && !served) atomicCAS(a.err, SAGE_DEVERR_NONE, SAGE_DEVERR_NO_PAGES);
     s_upto[tid] = upto;
     s_rows[tid] = rows;
     s_start[tid] = len;

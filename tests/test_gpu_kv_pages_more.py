@@ -89,3 +89,34 @@ def test_a_batch_whose_rows_are_just_enough_or_one_too_few():
         assert got.taken.tolist() == taken and got.lens.tolist() == taken and got.free_count.tolist() == [left]
         assert [x[0] for x in table.tolist()] == [3 if taken[0] else -1, -1, 2 if taken[2] else -1]
         assert got.slots.tolist() == ([48, 49, 50] if taken[0] else [-1] * min(3, tokens)) + ([32, 33, 34] if taken[2] else [-1] * max(0, tokens - 3))
+
+
+def short_reserve():
+    """One page of the two that are wanted."""
+    import quantized_attention_diffusion_gb300 as qad
+    table = torch.full((2, 1), -1, dtype=torch.int32, device="cuda")
+    got = qad.kv_pages_reserve(ints([0, 1]), ints([1]), ints([0, 0]), ints([1, 1]), table, PAGE, 2)
+    assert got.taken.tolist() == [1, 0]
+
+
+def test_too_few_pages_do_not_hide_an_error_that_is_pending():
+    import quantized_attention_diffusion_gb300 as qad
+    cache = qad.kv_cache_alloc(2, 1, PAGE)
+    x = torch.ones((1, 1, 1, 128), dtype=torch.bfloat16, device="cuda")
+    short_reserve()
+    assert qad.sync_status() == 9 and qad.sync_status() == 0
+    qad.kv_cache_append(None, x, x, cache, ints([2 * PAGE]))             # a slot behind the cache
+    short_reserve()
+    assert qad.sync_status() == 8 and qad.sync_status() == 0
+    short_reserve()
+    qad.kv_cache_append(None, x, x, cache, ints([2 * PAGE]))             # the graver one is kept, whichever is first
+    assert qad.sync_status() == 8 and qad.sync_status() == 0
+
+
+@pytest.mark.parametrize("free", [5, -1, 2 ** 31 - 1, -2 ** 31])
+def test_a_free_count_out_of_range_is_a_bad_page(free):
+    import quantized_attention_diffusion_gb300 as qad
+    table = torch.full((3, 1), -1, dtype=torch.int32, device="cuda")
+    got = qad.kv_pages_reserve(ints([0, 1, 2, 3]), ints([free]), ints([0] * 3), ints([1] * 3), table, PAGE, 3)
+    assert qad.sync_status() == 8
+    assert got.taken.tolist() == ([1] * 3 if free > 0 else [0] * 3) and got.free_count.tolist() == [1 if free > 0 else 0]
