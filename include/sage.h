@@ -654,7 +654,8 @@ sage_status sage_kv_pages_reserve(const int32_t* free_pages, const int32_t* free
  * free_pages, free_count, lens and block_table (released entries become -1) are
  * written in place.  A page in several tables is given back once for each: keep
  * shared pages out.  Errors as sage_kv_pages_reserve; a table entry that is no page,
- * or more pages than the list has room for, is reported as SAGE_ERR_BAD_PAGE.
+ * or more pages than the list has room for, is reported as SAGE_ERR_BAD_PAGE and stays
+ * off the list.
  */
 sage_status sage_kv_pages_release(int32_t* free_pages, int32_t* free_count, int num_pages, int page_size, int32_t* lens,
                                   const int32_t* keep, int B, int32_t* block_table, int table_width, int64_t table_stride,

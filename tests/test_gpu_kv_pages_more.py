@@ -120,3 +120,72 @@ def test_a_free_count_out_of_range_is_a_bad_page(free):
     got = qad.kv_pages_reserve(ints([0, 1, 2, 3]), ints([free]), ints([0] * 3), ints([1] * 3), table, PAGE, 3)
     assert qad.sync_status() == 8
     assert got.taken.tolist() == ([1] * 3 if free > 0 else [0] * 3) and got.free_count.tolist() == [1 if free > 0 else 0]
+
+
+@pytest.mark.parametrize("B,longest,free,bad", [(3, 60, 0, 1), (9, 500, 4, 3), (40, 3000, 17, 40), (1400, 90, 100, 50), (2100, 40, 0, 1), (64, 900, 5, 10 ** 9)])
+def test_entries_that_are_no_pages_stay_out_of_the_free_list(B, longest, free, bad):
+    import quantized_attention_diffusion_gb300 as qad
+    r = random.Random(B)
+    lens = [r.randint(1, longest) for _ in range(B)]
+    keep = [r.choice([0, 0, r.randint(0, n), n, n + 5, -2]) for n in lens]
+    total = sum(pages_of(n) for n in lens)
+    pages = list(range(total + free))
+    r.shuffle(pages)
+    table, at = [], free
+    for n in lens:
+        table.append(pages[at:at + pages_of(n)] + [-1] * (pages_of(longest) - pages_of(n)))
+        at += pages_of(n)
+    held = [(b, j) for b, n in enumerate(lens) for j in range(pages_of(n))]
+    for b, j in (held if bad >= len(held) else r.sample(held, bad)):
+        table[b][j] = r.choice([-1, len(pages), 2 ** 31 - 1, -2 ** 31])
+    stack = pages[:free] + [-9] * total
+
+    back, want = [], [list(x) for x in table]
+    for b, (n, c) in enumerate(zip(lens, keep)):
+        if c < n:
+            for j in range(pages_of(max(0, c)), pages_of(n)):
+                back.append(table[b][j])
+                want[b][j] = -1
+    valid = [p for p in back if 0 <= p < len(pages)]
+    t = torch.tensor(table, dtype=torch.int32, device="cuda")
+    s, f, n = ints(stack), ints([free]), ints(lens)
+    qad.kv_pages_release(s, f, n, ints(keep), t, PAGE)
+    assert qad.sync_status() == (0 if len(valid) == len(back) else 8)
+    assert f.tolist() == [free + len(valid)]
+    assert s.tolist()[:free + len(valid)] == pages[:free] + valid[::-1]
+    assert s.tolist()[free + len(back):] == stack[free + len(back):]
+    assert t.tolist() == want and n.tolist() == [min(a, max(0, b)) for a, b in zip(lens, keep)]
+
+    # and what is reserved next are pages
+    room = torch.full((1, max(1, free + len(valid))), -1, dtype=torch.int32, device="cuda")
+    count = PAGE * (free + len(valid))
+    if count:
+        got = qad.kv_pages_reserve(s, f, ints([0]), ints([count]), room, PAGE, count)
+        assert qad.sync_status() == 0 and got.taken.tolist() == [count] and got.free_count.tolist() == [0]
+        assert sorted(room[0].tolist()) == sorted(pages[:free] + valid)
+
+
+@pytest.mark.parametrize("table,free,left", [
+    ([[1, 9, -1]], 3, [0, 2, 3, 1]),                        # room for one, and one is a page
+    ([[9, 1, 7]], 3, [0, 2, 3, 1]),
+    ([[-1, -1, -1]], 4, [0, 2, 3, 5]),                      # a full list and a row that has no pages
+])
+def test_a_list_without_room_for_what_is_no_page(table, free, left):
+    import quantized_attention_diffusion_gb300 as qad
+    guard = ints([0, 2, 3, 5 if free == 4 else 77, 88])
+    pool = guard[:4]
+    t, f, n = torch.tensor(table, dtype=torch.int32, device="cuda"), ints([free]), ints([48])
+    qad.kv_pages_release(pool, f, n, ints([0]), t, PAGE)
+    assert qad.sync_status() == 8
+    assert pool.tolist() == left and f.tolist() == [4] and guard[4] == 88 and n.tolist() == [0] and (t == -1).all()
+
+
+def test_more_pages_than_the_list_has_room_for():
+    """A page given back twice: the list is full and holds pages alone."""
+    import quantized_attention_diffusion_gb300 as qad
+    guard = ints([0, 1, 2, 77, 88, 99])
+    t, f, n = ints([3, 2, 1, 0]).view(2, 2), ints([3]), ints([32, 32])
+    qad.kv_pages_release(guard[:5], f, n, ints([0, 0]), t, PAGE)
+    assert qad.sync_status() == 8
+    assert f.tolist() == [5] and guard.tolist()[:3] == [0, 1, 2] and guard[5] == 99
+    assert set(guard.tolist()[3:5]) <= {0, 1, 2, 3} and (t == -1).all() and not n.any()
