@@ -1089,7 +1089,8 @@ sage_status sage_rope_frequencies(int dim, double base, int scaling, double fact
     double f = std::pow(base, -2.0 * i / dim);
     if (scaling == SAGE_ROPE_LINEAR) f /= factor;
     if (scaling == SAGE_ROPE_YARN) {
-      const double ramp = std::min(1.0, std::max(0.0, (i - lo) / std::max(1e-3, hi - lo)));
+      // hi <= 0: pair 0, which turns most, turns `low` times or less.
+      const double ramp = hi <= 0.0 ? 1.0 : std::min(1.0, std::max(0.0, (i - lo) / std::max(1e-3, hi - lo)));
       f = f / factor * ramp + f * (1.0 - ramp);
     }
     if (scaling == SAGE_ROPE_BANDS) {
