@@ -76,6 +76,7 @@ constexpr float kFar = 32768.0f;                        // 2^15: most of 32 weig
 constexpr float kAbove = 6.0f;                          // a reference that moves goes so far below the largest weight:
                                                         // 32 of that are a sixteenth of kFar
 constexpr float kFarSum = 0x1p70f, kTiny = 0x1p-55f;    // most of 32 p's sum, and kFar / kFarSum
+constexpr uint32_t kFoldV = 4;                          // V's scales of 32 keys that one of them stands for: within 2^4
 constexpr float kNear = 4096.0f;                        // most of |R| in weigh_even
 constexpr float kSmall = 0x1p-70f;                      // least of L times V's scale there
 constexpr float kLarge = 0x1p60f;                       // most of a row's factor and of K's scale there: their product is finite
@@ -521,15 +522,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
       for (; loaded; ++it) {
         const int s = it & 1, round = it >> 1;
         // In 4 bits a warp's 32 keys get the largest of their scales, and the values the
-        // rest, where that is a power of two down to 2^-14 for all of them.  Rows of zeros in
-        // V alone have no scale that could stand for theirs in the references.  K's may not be
-        // so large that it could not be multiplied by a row's factor first.
+        // rest, where that is a power of two for all of them, of K down to 2^-14, of V to
+        // 2^-kFoldV: a weight that counts in a reference with more than its key's own scale leaves
+        // as many bits fewer to the others (rows of zeros in V would count with any).  K's may
+        // not be so large that it could not be multiplied by a row's factor first.
         uint32_t ratio = 0x3C003C00u;
         if constexpr (kBits == 4) {
           const uint32_t bits = __float_as_uint(scale);
-          const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, bits), least = __reduce_min_sync(0xFFFFFFFFu, bits == 0u ? 0x7F000000u : bits);
+          const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, bits), least = __reduce_min_sync(0xFFFFFFFFu, bits == 0u && !is_v ? 0x7F000000u : bits);
           const uint32_t top = most == 0u ? 0x3F800000u : most;          // no scale but 0: any
-          const bool even = most < 0x7F800000u && (most == 0u ? !is_v : most - least <= 14u << 23) &&
+          const bool even = most < 0x7F800000u && (most == 0u ? !is_v : most - least <= (is_v ? kFoldV : 14u) << 23) &&
                             !__any_sync(0xFFFFFFFFu, (bits & 0x7FFFFFu) != 0u);
           if (even) {
             ratio = bits == 0u ? 0u : ((15u << 10) - ((top - bits) >> 13)) * 0x10001u;

@@ -4,8 +4,9 @@ import math
 import pytest
 import torch
 
-from tests.cache_common import D, ints
+from tests.cache_common import D, assert_within, ints, join, reference
 from tests.gpu_common import ensure_library
+from tests.kv4_common import Cache4
 
 pytestmark = pytest.mark.gpu
 
@@ -154,3 +155,40 @@ def test_values_far_below_others_keep_their_probability(path, near, far):
     # bf16, the weights' fp16, and sums as above
     assert float((out.double().cpu() / want.repeat_interleave(G, dim=0) - 1).abs().max()) <= 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -12
     assert float((lse.double().cpu() - math.log(L)).abs().max()) <= 2.0 ** -10
+
+
+def unlike(n, g):        # within 2^13 of one another
+    return torch.exp2(torch.randint(-6, 8, (n, 1, 1), generator=g).float())
+
+
+def some_zero(n, g):
+    return torch.where(torch.rand((n, 1, 1), generator=g) < 0.1, torch.zeros(()), torch.ones(()))
+
+
+def zero_or_unlike(n, g):
+    return some_zero(n, g) * unlike(n, g)
+
+
+@pytest.mark.parametrize("scale", [0.3, 1.0, 5.0])
+@pytest.mark.parametrize("v_scale", [unlike, some_zero, zero_or_unlike])
+@pytest.mark.parametrize("lens,Sq,G,prefix", [([700, 129], 17, 2, 0), ([1415, 343, 1, 2000], 60, 5, 128), ([130, 130], 60, 3, 0), ([7, 40], 129, 8, 0),
+                                             ([300, 0, 64], 4, 2, 2500), ([5000], 33, 1, 0), ([700, 129], 2, 2, 0)])
+def test_heavy_keys_of_small_values(lens, Sq, G, prefix, v_scale, scale):
+    """Where the keys that have the scores have small values, or zeros, the others' are what the
+    output is made of: weights count with their own scale of V in a row's reference."""
+    import quantized_attention_diffusion_gb300 as qad
+    B, H, page = len(lens), 2, 64
+    cache = Cache4(lens, H, page, seed=Sq + prefix, v_scale=v_scale, extra=(prefix,) if prefix else ())
+    q = torch.randn((B, Sq, H * G, D), generator=torch.Generator().manual_seed(Sq)).to(torch.bfloat16)
+    table = cache.table.cuda()
+    kw = dict(softmax_scale=scale, causal=True, return_lse=True)
+    if prefix:
+        out, lse = qad.attn_fwd_cache_prefix(q.cuda(), cache.gpu(), table[B, :-(-prefix // page)].contiguous(), prefix, table[:B].contiguous(), ints(lens), **kw)
+    else:
+        out, lse = qad.attn_fwd_cache(q.cuda(), cache.gpu(), table, ints(lens), **kw)
+    for b in range(B):
+        rows = join(cache.dense(B), cache.dense(b)) if prefix else cache.dense(b)
+        ref, z, tol, ltol = reference(q[b], rows, True, scale)
+        # below 2^-126 bf16's steps are 2^-133 whatever the value: half of one
+        assert_within(out[b], ref, tol + 2.0 ** -134, f"out of sequence {b}")
+        assert_within(lse[b], z, ltol, f"lse of sequence {b}")
