@@ -280,18 +280,18 @@ __device__ __forceinline__ bool weigh(uint32_t tS, const float* kx, const float*
     for (int e = 0; e < 2; ++e) {
       const int at = 4 * i + 2 * e;
       const float2 k2 = e == 0 ? make_float2(k4.x, k4.y) : make_float2(k4.z, k4.w);
-      float2 v2 = e == 0 ? make_float2(v4.x, v4.y) : make_float2(v4.z, v4.w);
+      const float2 v2 = e == 0 ? make_float2(v4.x, v4.y) : make_float2(v4.z, v4.w);
       const float2 y = fmul2v(make_float2(__uint_as_float(a[at]), __uint_as_float(a[at + 1])), k2);
       float2 x = ffma2_bc(y.x, y.y, z.rk, -z.R);           // rk is a power of two: y * rk is exact
       if constexpr (kSlow) {
         if (at >= left) x.x = -INFINITY;
         if (at + 1 >= left) x.y = -INFINITY;
-        v2 = fmul2v(v2, make_float2(z.f, z.f));
       }
       const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
       sum = fadd2v(sum, p);
       float2 q = fmul2v(p, v2);
       if constexpr (kSlow) {                               // a scale that is not finite stays behind the limit
+        q = fmul2v(q, make_float2(z.f, z.f));              // last: f may be 2^86, and a scale times it infinite
         if (at >= left) q.x = 0.0f;
         if (at + 1 >= left) q.y = 0.0f;
         sumw = fadd2v(sumw, q);
