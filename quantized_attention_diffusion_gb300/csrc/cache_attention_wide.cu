@@ -481,6 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
       };
       Codes<kBits> w[8];
       float scale = 0.0f, even_k = 0.0f;
+      const uint32_t fold_within = (is_v ? kFoldV : 14u) << 23;
       auto load = [&]() {
         loaded = more;
         info = info_next;
@@ -529,12 +530,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
         uint32_t ratio = 0x3C003C00u;
         if constexpr (kBits == 4) {
           const uint32_t bits = __float_as_uint(scale);
-          const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, bits), least = __reduce_min_sync(0xFFFFFFFFu, bits == 0u && !is_v ? 0x7F000000u : bits);
-          const uint32_t top = most == 0u ? 0x3F800000u : most;          // no scale but 0: any
-          const bool even = most < 0x7F800000u && (most == 0u ? !is_v : most - least <= (is_v ? kFoldV : 14u) << 23) &&
-                            !__any_sync(0xFFFFFFFFu, (bits & 0x7FFFFFu) != 0u);
+          const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, bits), least = __reduce_min_sync(0xFFFFFFFFu, bits);
+          const bool even = top < 0x7F800000u && least != 0u && top - least <= fold_within && !__any_sync(0xFFFFFFFFu, (bits & 0x7FFFFFu) != 0u);
           if (even) {
-            ratio = bits == 0u ? 0u : ((15u << 10) - ((top - bits) >> 13)) * 0x10001u;
+            ratio = ((15u << 10) - ((top - bits) >> 13)) * 0x10001u;
             scale = __uint_as_float(top);
           }
           if (is_v && lane == 0) s_even[1][it % kScaleSlots][warp & 3] = even ? scale : -1.0f;
@@ -693,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_wide_kernel(const __gr
             const bool all_seen = key0 + kSub <= lo && top < INFINITY;
             bool usual = z.f == 1.0f;
             if constexpr (kBits == 4)
-              usual = usual && ev.least_k() > 0.0f && fabsf(z.R) <= kNear && z.rk <= kLarge && (z.l.x + z.l.y) * ev.least_v() >= kSmall;
+              usual = usual & (ev.least_k() > 0.0f) & (fabsf(z.R) <= kNear) & (z.rk <= kLarge) & ((z.l.x + z.l.y) * ev.least_v() >= kSmall);
             if (likely(all_seen && __all_sync(0xFFFFFFFFu, usual))) {
               if constexpr (kBits == 4) {
                 c = weigh_even(tS, ev, z);
