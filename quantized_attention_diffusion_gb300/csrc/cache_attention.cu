@@ -31,11 +31,12 @@
 // products of Q and K are exact but for values 2^-28 below the row's largest.
 //
 // Of a cache in 4 bits kc and vc are code times block scale, E2M1 x E4M3, six significant
-// bits between 2^-10 and 2688: exact in fp16 too, at one product for two values.  152 bytes a key
-// leave the issue slots as the bound (60% of them taken, 350 instructions for 16 keys of
-// a warp, of which conversion and scaling are 130): one token of 65536 keys x 24 heads
-// 53.7 us, 4.5 TB/s, 48 ragged sequences 99.7 us, 0.67 of the copy rate.  Without the
-// arithmetic the same copies take 42 us.
+// bits between 2^-10 and 2688: exact in fp16 too, at one product for two values.  With 152 bytes a
+// key the instructions are the bound, 350 for 16 keys of a warp, of which conversion and
+// scaling are 130: while warps attend 0.93 of the issue slots are taken (0.60 over the whole
+// launch: a tile is 2250 clocks of that and 480 of waiting for the next).  One token of 65536
+// keys x 24 heads 53.7 us, 4.5 TB/s, 48 ragged sequences 99.4 us, 0.68 of the copy rate.
+// Without the arithmetic the same copies take 42 us.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -1245,8 +1246,11 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // 8 or 16 query rows a tile where they are all, else the wide kernel's 256: the keys
 // are read and converted once for all rows of a tile.  32 sequences of 16384 keys, 8
-// key/value heads, us: 16 rows 223, as two tiles of eight 325, in the wide kernel 424;
-// 24 rows in the wide kernel 424, as three tiles of eight 482.
+// key/value heads, us, 8 bits / 4 bits: 16 rows 224 / 202, as two tiles of eight 328 / 245,
+// in the wide kernel 381 / 395; 24 rows in the wide kernel 382 / 396, as three tiles of
+// eight 484 / 362, as two of 16 428 / 384; 32 rows 383 / 396, as two of 16 429 / 385; 64 rows
+// 383 / 397, as four of 16 840 / 747.  (17 to 32 rows in 4 bits would be up to 9% sooner done
+// in small tiles; one rule serves both caches.)
 int rows_per_tile(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : kWideRows; }
 int max_ctas(int R) { return kSms * (R == kWideRows ? 1 : ctas_per_sm(R / 8)); }
 int keys_per_tile(int R, int bits) { return R == kWideRows ? kWideTok : tok_of(bits); }

@@ -8,7 +8,8 @@
 // 2^-19 of the largest keep all their bits), but at most 60 from the
 // largest x; where V's scales are farther, a row's weights take a factor f = 2^-D more
 // (1 otherwise) and its accumulator stands relative to R + D.  R and D are whole
-// numbers.  V's codes are exact in fp16.
+// numbers.  V's codes are exact in fp16.  (A p below 2^-126 is 0: no weight that counts has
+// one while V's scales are below 2^100 and within 2^150 of one another.)
 //
 // A CTA owns 256 query rows of one unit and walks its key tiles of 128.  Its two
 // halves are two row tiles of 128, or, where a unit has at most 128 rows, the even
@@ -35,7 +36,7 @@
 // What bounds it is the issue of the softmax's and the conversion's instructions (61% of
 // the slots in 4 bits, the tensor cores active for 38% of the time beside it): a warp's 64
 // scores take 1650 of a buffer's 1950 clocks.  2 x 1000 tokens x 16 heads over up to 9000
-// keys: 173 us in 8 bits, 147 us in 4, 0.39 and 0.46 of the measured bf16 rate (per 8000
+// keys: 173 us in 8 bits, 146 us in 4, 0.39 and 0.46 of the measured bf16 rate (per 8000
 // keys more, 108 us in 4 bits, 0.64 of it; the rest is the start, the parts and their
 // merge); 24 x 5 tokens x 16 heads behind a prefix of 32760, all in all: 70 and 69 us.
 // Until its jumps were few (what is rare told to the compiler, the usual path in a line)

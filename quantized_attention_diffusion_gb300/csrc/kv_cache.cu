@@ -23,9 +23,10 @@
 // back in 62 us, 0.93 of it.  Small calls cost a launch and three loads in a row (start or
 // length, page, row): 5.6 us for 8 tokens, 4.4 us for 3 x 333 read.
 //
-// In 4 bits (kv_rows.cuh has the formulas) a row is 76 bytes.  Writing it is bound by the
-// issue slots, reading it back by HBM: 4 x up to 16384 tokens of 8 heads 38 us (0.73 of
-// the copy rate) and 49 us (0.94).
+// In 4 bits (kv_rows.cuh has the formulas) a row is 76 bytes.  Reading it back is bound by
+// HBM, writing by the latency of its loads: a warp asks for one step's rows, waits and
+// computes with none in flight (the first of its stalls; 0.64 of the issue slots taken, DRAM at
+// 47%).  4 x up to 16384 tokens of 8 heads: 38 us (0.73 of the copy rate) and 49 us (0.94).
 #include <cuda_runtime.h>
 
 #include "kv_rows.cuh"
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_cache_read_kernel(const CacheR
 
 // The same into 4 bits.  Eight tokens a warp, four lanes and 32 channels each: what a
 // row needs once is shared by twice as many as above (4 x up to 16384 tokens of 8 heads:
-// 38 us; by eight lanes a row 45, the issue slots the bound).
+// 38 us; by eight lanes a row 45).
 constexpr int kRows4 = 8;
 __global__ void __launch_bounds__(kWarps * 32) kv4_cache_write_kernel(const CacheWriteArgs a, uint32_t steps,
                                                                       int steps_per_seq) {
