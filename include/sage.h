@@ -569,7 +569,8 @@ uint64_t sage_rope_frequency(double radians);
  *   q_weight, k_weight in : bf16 [D], or NULL for ones
  *   q_out, k_out out: bf16, dense; may be q and k where those are dense, and
  *                   otherwise overlap no input.  fp32 arithmetic, rounded once
- *                   (a row whose squares pass fp32's range becomes zeros)
+ *                   (a row whose squares pass fp32's range becomes zeros; squares
+ *                   below it are zeros, which with eps 0 leaves infinities)
  * One launch.  B * S * (Hq + Hk) <= 2^31 - 1.  Errors: INVALID_ARG, UNSUPPORTED,
  * MISALIGNED, CUDA.
  */
